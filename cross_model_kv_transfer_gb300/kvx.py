@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -41,6 +42,8 @@ KVX_FLAG_TIMEOUT = 16
 KVX_FLAG_BAD_SEQLENS = 32
 KVX_FLAG_BAD_SRC_BLOCK = 64
 KVX_FLAG_NOT_SPD = 128
+KVX_FLAG_BAD_LENGTH = 256
+KVX_FLAG_NOT_FINITE = 512
 
 KVX_F32 = 0
 KVX_BF16 = 1
@@ -53,12 +56,21 @@ KVX_PLAN_TEST_STALL = 1
 KVX_PLAN_TC_SINGLE_CTA = 2
 KVX_MAPPER_PER_HEAD = 0
 KVX_MAPPER_WIDE = 1
+KVX_ROPE_HALF = 0
+KVX_ROPE_INTERLEAVED = 1
+KVX_ROPE_UNSCALED = 0
+KVX_ROPE_LINEAR = 1
+KVX_ROPE_BANDS = 2
+KVX_ROPE_YARN = 3
 
 EXPORTED = ("kvx_plan_create", "kvx_transfer", "kvx_plan_destroy",
             "kvx_status_string", "kvx_plan_kernel", "kvx_plan_launches",
             "kvx_plan_cta_group", "kvx_transfer_static", "kvx_kv_diagnostics",
             "kvx_ridge_workspace_bytes", "kvx_ridge_fit",
-            "kvx_layer_scores_workspace_bytes", "kvx_layer_scores")
+            "kvx_layer_scores_workspace_bytes", "kvx_layer_scores",
+            "kvx_rope_init", "kvx_rope_apply", "kvx_cache8_write",
+            "kvx_attend8_workspace_bytes", "kvx_attend8",
+            "kvx_evict8_workspace_bytes", "kvx_evict8")
 
 
 class PlanDesc(ctypes.Structure):
@@ -145,6 +157,92 @@ class FeatureArgs(ctypes.Structure):
     ]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+        ("low_band", ctypes.c_double), ("high_band", ctypes.c_double),
+        ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+        ("amplitude", ctypes.c_double), ("original_context", ctypes.c_int32),
+    ]
+
+
+class RopeState(ctypes.Structure):
+    """``kvx_rope``: what ``kvx_rope_init`` fills."""
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+        ("turns", ctypes.c_uint64 * 128),
+    ]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("q_out_token_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+        ("k_out_token_stride", ctypes.c_int64), ("k_out_head_stride", ctypes.c_int64),
+        ("ntok", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("transpose", ctypes.c_int32),
+        ("positions", ctypes.c_void_p), ("first_position", ctypes.c_int64),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class Cache8Desc(ctypes.Structure):
+    """``kvx_cache8``."""
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("num_blocks", ctypes.c_int64), ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("max_blocks_per_req", ctypes.c_int32), ("block_table", ctypes.c_void_p),
+    ]
+
+
+class Cache8WriteArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", Cache8Desc), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("num_requests", ctypes.c_int32), ("ntok", ctypes.c_int64),
+        ("cu_seqlens", ctypes.c_void_p), ("start", ctypes.c_void_p),
+        ("src_rows", ctypes.c_void_p), ("num_src_rows", ctypes.c_int64),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class Attend8Args(ctypes.Structure):
+    _fields_ = [
+        ("cache", Cache8Desc), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("ntok", ctypes.c_int64),
+        ("num_requests", ctypes.c_int32), ("max_new", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+        ("max_len", ctypes.c_int32), ("scale", ctypes.c_float), ("lse", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p), ("weights_stride", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class Evict8Args(ctypes.Structure):
+    _fields_ = [
+        ("cache", Cache8Desc), ("dst_table", ctypes.c_void_p),
+        ("max_dst_blocks", ctypes.c_int32), ("num_requests", ctypes.c_int32),
+        ("lens", ctypes.c_void_p), ("max_len", ctypes.c_int32), ("keep", ctypes.c_int32),
+        ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32),
+        ("weights", ctypes.c_void_p), ("weights_stride", ctypes.c_int64),
+        ("kept", ctypes.c_void_p), ("kept_weights", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -197,6 +295,19 @@ def load():
             lib.kvx_ridge_features.argtypes = [ctypes.c_void_p, ctypes.POINTER(FeatureArgs),
                                                ctypes.c_void_p]
             lib.kvx_ridge_features.restype = ctypes.c_int
+            # the decoding calls take their argument block as a ctypes
+            # structure (byref) or as packed bytes
+            for name, argtypes in (
+                    ("kvx_rope_init", [ctypes.POINTER(RopeDesc), ctypes.POINTER(RopeState)]),
+                    ("kvx_rope_apply", [ctypes.c_void_p] * 3),
+                    ("kvx_cache8_write", [ctypes.c_void_p] * 2),
+                    ("kvx_attend8", [ctypes.c_void_p] * 2),
+                    ("kvx_evict8", [ctypes.c_void_p] * 2)):
+                getattr(lib, name).argtypes = argtypes
+                getattr(lib, name).restype = ctypes.c_int
+            for name in ("kvx_attend8_workspace_bytes", "kvx_evict8_workspace_bytes"):
+                getattr(lib, name).argtypes = [ctypes.c_void_p]
+                getattr(lib, name).restype = ctypes.c_size_t
             _lib = lib
     return _lib
 
@@ -260,6 +371,36 @@ def kvx_layer_scores(plan, args: ScoreArgs, stream) -> int:
 
 def kvx_ridge_features(plan, args: FeatureArgs, stream) -> int:
     return load().kvx_ridge_features(plan, ctypes.byref(args), stream)
+
+
+def kvx_rope_init(desc: RopeDesc):
+    """Returns (status, RopeState)."""
+    rope = RopeState()
+    return load().kvx_rope_init(ctypes.byref(desc), ctypes.byref(rope)), rope
+
+
+def kvx_rope_apply(rope: RopeState, args: RopeArgs, stream) -> int:
+    return load().kvx_rope_apply(ctypes.byref(rope), ctypes.byref(args), stream)
+
+
+def kvx_cache8_write(args: Cache8WriteArgs, stream) -> int:
+    return load().kvx_cache8_write(ctypes.byref(args), stream)
+
+
+def kvx_attend8_workspace_bytes(args: Attend8Args) -> int:
+    return int(load().kvx_attend8_workspace_bytes(ctypes.byref(args)))
+
+
+def kvx_attend8(args: Attend8Args, stream) -> int:
+    return load().kvx_attend8(ctypes.byref(args), stream)
+
+
+def kvx_evict8_workspace_bytes(args: Evict8Args) -> int:
+    return int(load().kvx_evict8_workspace_bytes(ctypes.byref(args)))
+
+
+def kvx_evict8(args: Evict8Args, stream) -> int:
+    return load().kvx_evict8(ctypes.byref(args), stream)
 
 
 def ridge_fit(x, y, lam: float = 0.01, w=None, b=None, workspace=None, status=None,
@@ -610,3 +751,344 @@ class Plan:
         st = kvx_kv_diagnostics(self.handle, args, ctypes.c_void_p(stream.cuda_stream))
         if st != KVX_OK:
             raise KvxError(st, "kvx_kv_diagnostics")
+
+
+# --- decoding on a transferred cache -----------------------------------------
+
+def _packer(cls):
+    """``struct`` packer of a ctypes structure's fields (nested ones in line,
+    native alignment): one pack is several times cheaper than as many
+    attribute stores, which is what a single-token call spends its time on."""
+    letters = {ctypes.c_void_p: "P", ctypes.c_int32: "i", ctypes.c_int64: "q",
+               ctypes.c_float: "f", ctypes.c_size_t: "N"}
+
+    def fmt(c):
+        return "".join(fmt(t) if issubclass(t, ctypes.Structure) else letters[t]
+                       for _, t in c._fields_)
+
+    s = struct.Struct("@" + fmt(cls))
+    assert s.size <= ctypes.sizeof(cls) < s.size + 8
+    return s.pack
+
+
+_pack_rope = _packer(RopeArgs)
+_pack_write = _packer(Cache8WriteArgs)
+_pack_attend = _packer(Attend8Args)
+_pack_evict = _packer(Evict8Args)
+
+
+def _int_table(t, name, device, ndim=1):
+    """Data pointer of a contiguous int32 CUDA tensor (0 for None)."""
+    import torch
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.device != device or t.dim() != ndim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {ndim}-D int32 tensor on {device}")
+    return t.data_ptr()
+
+
+def _status_ptr(t, device):
+    return 0 if t is None else _int_table(t, "status", device)
+
+
+def _on_device(device):
+    import torch
+    if device.type != "cuda" or torch.cuda.current_device() != device.index:
+        raise ValueError(f"tensors are on {device}, which is not the current CUDA device")
+
+
+def _raw_stream(stream, device):
+    import torch
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _heads(t, name, dtype, device, heads, dim):
+    """Check a [tokens][heads][dim] tensor with unit stride inside a head."""
+    if t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[1] != heads or \
+            t.shape[2] != dim or t.stride(2) != 1:
+        raise ValueError(f"{name}: expected [tokens][{heads}][{dim}] {dtype} on {device} with "
+                         f"unit stride inside a head")
+    return t
+
+
+class Rope:
+    """A rotation of head vectors by position (``kvx_rope``).
+
+    ``layout`` "half" pairs (i, i + rot_dim/2), "interleaved" (2i, 2i + 1);
+    ``scaling`` None, "linear" (``factor``), "bands" (``factor``, ``low_band``,
+    ``high_band``, ``original_context``) or "yarn" (``factor``, ``beta_fast``,
+    ``beta_slow``, ``original_context``); ``amplitude`` 0 is the scaling's own.
+    """
+
+    def __init__(self, head_dim, theta, *, rot_dim=None, layout="half", scaling=None, factor=1.0,
+                 low_band=0.0, high_band=0.0, beta_fast=32.0, beta_slow=1.0,
+                 original_context=0, amplitude=0.0):
+        layouts = {"half": KVX_ROPE_HALF, "interleaved": KVX_ROPE_INTERLEAVED}
+        scalings = {None: KVX_ROPE_UNSCALED, "linear": KVX_ROPE_LINEAR, "bands": KVX_ROPE_BANDS,
+                    "yarn": KVX_ROPE_YARN}
+        if layout not in layouts or scaling not in scalings:
+            raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
+        desc = RopeDesc(int(head_dim), int(head_dim if rot_dim is None else rot_dim),
+                        layouts[layout], scalings[scaling], float(theta), float(factor),
+                        float(low_band), float(high_band), float(beta_fast), float(beta_slow),
+                        float(amplitude), int(original_context))
+        st, self.state = kvx_rope_init(desc)
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_rope_init")
+        self.head_dim = int(head_dim)
+        self._ptr = ctypes.addressof(self.state)
+
+    def apply(self, q=None, k=None, positions=None, *, transpose=False, first_position=0,
+              q_out=None, k_out=None, status=None, stream=None):
+        """Rotate q [tokens][q_heads][d] and k [tokens][k_heads][d] (either may
+        be None; fp32 or bf16, any token and head strides) at ``positions``
+        (int32, or first_position, first_position + 1, ...); returns (q_out,
+        k_out), allocated unless given (in place with ``q_out=q``).
+        ``transpose`` applies the transposed rotation: the gradient."""
+        import torch
+        x = q if q is not None else k
+        if x is None:
+            raise ValueError("q or k is needed")
+        dev, dt, d = x.device, x.dtype, self.head_dim
+        code = _dtype_code(dt)
+        _on_device(dev)
+        n = x.shape[0]
+        ptrs, strides, heads = [], [], []
+        outs = []
+        for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+            if t is None:
+                outs.append(None)
+                ptrs.append((0, 0))
+                strides.append((0, 0, 0, 0))
+                heads.append(0)
+                continue
+            h = t.shape[1] if t.dim() == 3 else -1
+            _heads(t, name, dt, dev, h, d)
+            if o is None:
+                o = _on_stream(torch.empty, stream, (n, h, d), dtype=dt, device=dev)
+            elif _heads(o, name + "_out", dt, dev, h, d).shape[0] != n:
+                raise ValueError(f"{name}_out has another number of tokens")
+            if t.shape[0] != n:
+                raise ValueError("q and k must hold the same tokens")
+            outs.append(o)
+            ptrs.append((t.data_ptr(), o.data_ptr()))
+            ts, os_ = t.stride(), o.stride()
+            strides.append((ts[0], ts[1], os_[0], os_[1]))
+            heads.append(h)
+        pos = _int_table(positions, "positions", dev)
+        if positions is not None and positions.shape[0] != n:
+            raise ValueError("positions must hold one entry for each token")
+        (qs, ks) = strides
+        a = _pack_rope(ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1], qs[0], qs[1], ks[0], ks[1],
+                       qs[2], qs[3], ks[2], ks[3], n, heads[0], heads[1], code, int(transpose),
+                       pos, first_position, _status_ptr(status, dev))
+        st = load().kvx_rope_apply(self._ptr, a, _raw_stream(stream, dev))
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_rope_apply")
+        return outs[0], outs[1]
+
+
+class Cache8:
+    """An 8-bit paged cache of one layer (``kvx_cache8``): e4m3 codes
+    [num_blocks][heads][block_size][head_dim] (uint8 or float8_e4m3fn) and one
+    fp32 scale for each (block, head), for keys and for values.  The tensors
+    stay the caller's; ``Cache8.empty`` allocates them."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale):
+        import torch
+        dev = k_codes.device
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+            if t.dim() != 4 or t.dtype not in (torch.uint8, torch.float8_e4m3fn) or \
+                    t.shape != k_codes.shape or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous [num_blocks][heads][block_size]"
+                                 f"[head_dim] uint8 or float8_e4m3fn tensor on {dev}")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype != torch.float32 or t.shape != k_codes.shape[:2] or t.device != dev or \
+                    not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous fp32 [num_blocks][heads] tensor "
+                                 f"on {dev}")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.device = dev
+        self.num_blocks, self.heads, self.block_size, self.head_dim = k_codes.shape
+        self._head = (k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
+                      v_scale.data_ptr(), self.num_blocks, self.heads, self.head_dim,
+                      self.block_size)
+
+    @classmethod
+    def empty(cls, num_blocks, heads, head_dim, block_size, device="cuda"):
+        import torch
+        codes = torch.zeros((2, num_blocks, heads, block_size, head_dim), dtype=torch.uint8,
+                            device=device)
+        scale = torch.ones((2, num_blocks, heads), dtype=torch.float32, device=device)
+        return cls(codes[0], codes[1], scale[0], scale[1])
+
+    def _table(self, block_table):
+        return self._head + (block_table.shape[1] if block_table.dim() == 2 else 0,
+                             _int_table(block_table, "block_table", self.device, 2))
+
+    def write(self, k, v, block_table, start=None, *, cu_seqlens=None, src_rows=None, status=None,
+              stream=None):
+        """Quantise new (rotated) keys and values [tokens][heads][d] of R
+        requests into their blocks: request r's tokens go to slots start[r],
+        start[r] + 1, ... (0 without ``start``).  Without ``cu_seqlens`` [R + 1]
+        there is one token for each request.  With ``src_rows`` token g is row
+        src_rows[g] of k and v, so a paged bf16 / fp32 cache can be read."""
+        dev = self.device
+        _on_device(dev)
+        _heads(k, "k", k.dtype, dev, self.heads, self.head_dim)
+        _heads(v, "v", k.dtype, dev, self.heads, self.head_dim)
+        if k.shape[0] != v.shape[0]:
+            raise ValueError("k and v must hold the same rows")
+        R = block_table.shape[0]
+        if cu_seqlens is not None and cu_seqlens.shape[0] != R + 1:
+            raise ValueError("cu_seqlens must have one entry more than block_table has rows")
+        if start is not None and start.shape[0] != R:
+            raise ValueError("start must hold one entry for each request")
+        n = k.shape[0] if src_rows is None else src_rows.shape[0]
+        ks, vs = k.stride(), v.stride()
+        a = _pack_write(*self._table(block_table), k.data_ptr(), v.data_ptr(), ks[0], ks[1],
+                        vs[0], vs[1], _dtype_code(k.dtype), R, n,
+                        _int_table(cu_seqlens, "cu_seqlens", dev),
+                        _int_table(start, "start", dev), _int_table(src_rows, "src_rows", dev),
+                        k.shape[0], _status_ptr(status, dev))
+        st = load().kvx_cache8_write(a, _raw_stream(stream, dev))
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_cache8_write")
+
+    def attend_workspace(self, *, ntok, num_requests, q_heads, max_len, max_new=1, dtype=None,
+                         weights=False):
+        """A workspace (uint8, zero-filled) for ``attend`` calls of at most
+        these sizes that are ordered on one stream."""
+        import torch
+        a = Attend8Args()
+        a.cache = Cache8Desc(*self._head, 1, self.k_codes.data_ptr())
+        a.dtype = _dtype_code(torch.bfloat16 if dtype is None else dtype)
+        a.q_heads, a.ntok, a.num_requests = q_heads, ntok, num_requests
+        a.max_new, a.max_len, a.scale = max_new, max_len, 1.0
+        a.lens = a.cu_seqlens = self.k_codes.data_ptr()   # sizes only: never read
+        if weights:
+            a.weights, a.weights_stride = self.k_scale.data_ptr(), max_len
+        need = kvx_attend8_workspace_bytes(a)
+        if need == 0:
+            raise KvxError(KVX_ERR_INVALID_ARG, "kvx_attend8_workspace_bytes")
+        return torch.zeros(need, dtype=torch.uint8, device=self.device)
+
+    def attend(self, q, block_table, lens, max_len, *, cu_seqlens=None, max_new=1, scale=None,
+               out=None, lse=None, weights=None, workspace=None, status=None, stream=None):
+        """Attention of the new queries q [tokens][q_heads][d] over the slots
+        of their requests (``lens`` [R], at most ``max_len``): query i of n sees
+        slots up to lens - n + i.  Returns (out, lse [tokens][q_heads]).
+        ``weights`` [R][heads][>= max_len] fp32 accumulates the attention weight
+        of each slot.  Scratch is allocated here unless ``workspace`` (from
+        ``attend_workspace``) is given."""
+        import torch
+        dev = self.device
+        _on_device(dev)
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens][q_heads][d]")
+        n, hq, d = q.shape
+        _heads(q, "q", q.dtype, dev, hq, self.head_dim)
+        R = block_table.shape[0]
+        if lens.shape[0] != R or (cu_seqlens is not None and cu_seqlens.shape[0] != R + 1):
+            raise ValueError("lens, cu_seqlens and block_table must hold the same requests")
+        if out is None:
+            out = _on_stream(torch.empty, stream, (n, hq, d), dtype=q.dtype, device=dev)
+        elif _heads(out, "out", q.dtype, dev, hq, d).shape[0] != n:
+            raise ValueError("out has another number of tokens")
+        if lse is None:
+            lse = _on_stream(torch.empty, stream, (n, hq), dtype=torch.float32, device=dev)
+        elif lse.dtype != torch.float32 or tuple(lse.shape) != (n, hq) or lse.device != dev or \
+                not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous fp32 [{n}][{hq}] tensor on {dev}")
+        wptr = wstride = 0
+        if weights is not None:
+            if weights.dtype != torch.float32 or weights.device != dev or weights.dim() != 3 or \
+                    tuple(weights.shape[:2]) != (R, self.heads) or not weights.is_contiguous():
+                raise ValueError(f"weights must be a contiguous fp32 [{R}][{self.heads}][slots] "
+                                 f"tensor on {dev}")
+            wptr, wstride = weights.data_ptr(), weights.shape[2]
+        if workspace is None:
+            workspace = _on_stream(self.attend_workspace, stream, ntok=n, num_requests=R,
+                                  q_heads=hq, max_len=max_len, max_new=max_new, dtype=q.dtype,
+                                  weights=weights is not None)
+        qs, os_ = q.stride(), out.stride()
+        a = _pack_attend(*self._table(block_table), q.data_ptr(), out.data_ptr(), qs[0], qs[1],
+                         os_[0], os_[1], _dtype_code(q.dtype), hq, n, R, max_new,
+                         _int_table(cu_seqlens, "cu_seqlens", dev),
+                         _int_table(lens, "lens", dev), max_len,
+                         d ** -0.5 if scale is None else scale, lse.data_ptr(), wptr, wstride,
+                         workspace.data_ptr(), workspace.numel(), _status_ptr(status, dev))
+        st = load().kvx_attend8(a, _raw_stream(stream, dev))
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_attend8")
+        return out, lse
+
+    def evict_workspace(self, *, num_requests, max_len, keep):
+        """A workspace (uint8) for ``evict`` calls of at most these sizes that
+        are ordered on one stream."""
+        import torch
+        a = Evict8Args()
+        any_ptr = self.k_codes.data_ptr()                 # sizes only: never read
+        a.cache = Cache8Desc(*self._head, 1, any_ptr)
+        a.dst_table = a.lens = a.weights = a.kept = a.new_lens = any_ptr
+        a.max_dst_blocks, a.weights_stride = 2 ** 31 - 1, max_len
+        a.num_requests, a.max_len, a.keep = num_requests, max_len, keep
+        need = kvx_evict8_workspace_bytes(a)
+        if need == 0:
+            raise KvxError(KVX_ERR_INVALID_ARG, "kvx_evict8_workspace_bytes")
+        return torch.zeros(need, dtype=torch.uint8, device=self.device)
+
+    def evict(self, weights, block_table, lens, dst_table, *, max_len, keep, sinks=0, recent=0,
+              kept=None, kept_weights=None, new_lens=None, workspace=None, status=None,
+              stream=None):
+        """Keep ``keep`` slots of each request and head: the first ``sinks``,
+        the last ``recent`` and those of the largest ``weights``
+        [R][heads][>= max_len]; move them into the blocks of ``dst_table`` (same
+        pool, none of them read by this call).  Returns kept slots
+        [R][heads][keep] (-1 beyond), their weights and the new lengths [R]."""
+        import torch
+        dev = self.device
+        _on_device(dev)
+        R = block_table.shape[0]
+        if weights.dtype != torch.float32 or weights.device != dev or weights.dim() != 3 or \
+                tuple(weights.shape[:2]) != (R, self.heads) or not weights.is_contiguous():
+            raise ValueError(f"weights must be a contiguous fp32 [{R}][{self.heads}][slots] tensor "
+                             f"on {dev}")
+        if lens.shape[0] != R or dst_table.dim() != 2 or dst_table.shape[0] != R:
+            raise ValueError("lens, block_table and dst_table must hold the same requests")
+        shape = (R, self.heads, keep)
+        if kept is None:
+            kept = _on_stream(torch.empty, stream, shape, dtype=torch.int32, device=dev)
+        if kept_weights is None:
+            kept_weights = _on_stream(torch.empty, stream, shape, dtype=torch.float32,
+                                      device=dev)
+        if new_lens is None:
+            new_lens = _on_stream(torch.empty, stream, R, dtype=torch.int32, device=dev)
+        if kept_weights.dtype != torch.float32 or kept_weights.device != dev or \
+                tuple(kept_weights.shape) != shape or tuple(kept.shape) != shape or \
+                new_lens.shape[0] != R or not kept_weights.is_contiguous():
+            raise ValueError("kept, kept_weights: contiguous [R][heads][keep]; new_lens: [R]")
+        if workspace is None:
+            workspace = _on_stream(self.evict_workspace, stream, num_requests=R, max_len=max_len,
+                                  keep=keep)
+        a = _pack_evict(*self._table(block_table), _int_table(dst_table, "dst_table", dev, 2),
+                        dst_table.shape[1], R, _int_table(lens, "lens", dev), max_len, keep,
+                        sinks, recent, weights.data_ptr(), weights.shape[2],
+                        _int_table(kept, "kept", dev, 3), kept_weights.data_ptr(),
+                        _int_table(new_lens, "new_lens", dev), workspace.data_ptr(),
+                        workspace.numel(), _status_ptr(status, dev))
+        st = load().kvx_evict8(a, _raw_stream(stream, dev))
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_evict8")
+        return kept, kept_weights, new_lens
+
+
+def _on_stream(make, stream, *args, **kw):
+    """``make(...)`` with ``stream`` current: a tensor allocated for a call on
+    another stream must come from that stream's memory, or it could be handed
+    out again before the call is done."""
+    import torch
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)

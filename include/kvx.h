@@ -89,6 +89,12 @@ typedef enum {
                                         id outside [0, src_num_blocks)       */
 #define KVX_FLAG_NOT_SPD       128u  /* kvx_ridge_fit: XcT Xc + lam I has a
                                         non-positive pivot (W, b left NaN)   */
+#define KVX_FLAG_BAD_LENGTH    256u  /* 8-bit cache calls: a request's length or
+                                        start is negative or beyond the call's
+                                        bound (max_len, the table's width)   */
+#define KVX_FLAG_NOT_FINITE    512u  /* kvx_cache8_write: an infinity (stored as
+                                        the block's largest code) or a NaN
+                                        (stored as 0)                        */
 
 typedef enum { KVX_F32 = 0, KVX_BF16 = 1 } kvx_dtype;
 typedef enum { KVX_CONTIGUOUS = 0, KVX_PAGED = 1 } kvx_layout;
@@ -522,6 +528,233 @@ kvx_status kvx_ridge_features(const kvx_plan *plan, const kvx_feature_args *args
  * Other errors as for kvx_transfer; `stream` as for kvx_transfer. */
 kvx_status kvx_transfer_static(const kvx_plan_desc *desc, const kvx_transfer_args *args,
                                void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Decoding on a transferred cache.  Once its cache is installed, the target
+ * model continues from it token by token ("Helm Intelligent Routing", section
+ * "Why carrying the cache across is the hard part": the target decodes from
+ * the carried state instead of re-reading the prompt).  The calls below are
+ * the operators of that continuation: rotary positions of the new tokens'
+ * queries and keys, an 8-bit paged form of the cache, attention over it, and
+ * eviction of the tokens that attention does not use.
+ *
+ * All of them only validate on the host and enqueue kernels on `stream`; they
+ * neither allocate nor synchronise.  As for kvx_transfer, what only the device
+ * can see (positions, lengths, block ids) never traps: it is bounds-checked,
+ * skipped and flagged in the optional status word.
+ * ------------------------------------------------------------------------- */
+
+/* Which dimensions of the rotated part form pair i: HALF (i, i + rot_dim/2),
+ * INTERLEAVED (2i, 2i + 1). */
+typedef enum { KVX_ROPE_HALF = 0, KVX_ROPE_INTERLEAVED = 1 } kvx_rope_layout;
+
+/* How the frequencies w_i = theta^(-2i/rot_dim) are scaled for contexts longer
+ * than the one the model was trained on.  Turns n_i = original_context * w_i /
+ * (2 pi) are pair i's turns over that context.
+ *   UNSCALED  w_i.
+ *   LINEAR    w_i / factor.
+ *   BANDS     w_i (s + (1 - s) / factor), s = clamp((n_i - low_band) /
+ *             (high_band - low_band), 0, 1): pairs that turn often are kept,
+ *             those that turn seldom stretched (Llama 3.1's rule).
+ *   YARN      w_i (s + (1 - s) / factor), s = 1 - clamp((i - lo) / (hi - lo),
+ *             0, 1), lo = floor(c(beta_fast)), hi = ceil(c(beta_slow)), c(b) =
+ *             rot_dim ln(original_context / (2 pi b)) / (2 ln theta), lo at
+ *             least 0, hi at most rot_dim - 1 and at least lo + 0.001;
+ *             amplitude 0.1 ln(factor) + 1 (the YaRN paper, section 3). */
+typedef enum {
+  KVX_ROPE_UNSCALED = 0,
+  KVX_ROPE_LINEAR = 1,
+  KVX_ROPE_BANDS = 2,
+  KVX_ROPE_YARN = 3
+} kvx_rope_scaling;
+
+typedef struct {
+  int32_t head_dim;         /* d, even, 2..256                                */
+  int32_t rot_dim;          /* rotated dimensions, even, 2..d; the rest of the
+                               head is copied                                 */
+  int32_t layout;           /* kvx_rope_layout                                */
+  int32_t scaling;          /* kvx_rope_scaling                               */
+  double theta;             /* RoPE base, finite, > 1                         */
+  double factor;            /* >= 1 (LINEAR, BANDS, YARN)                     */
+  double low_band, high_band;   /* BANDS: 0 <= low_band < high_band           */
+  double beta_fast, beta_slow;  /* YARN: beta_fast > beta_slow > 0            */
+  double amplitude;         /* factor on the rotated values; 0 = the scaling's
+                               own (1, or YaRN's)                             */
+  int32_t original_context; /* BANDS, YARN: >= 1                              */
+} kvx_rope_desc;
+
+/* A rotation, filled by kvx_rope_init: plain values that the caller keeps and
+ * may copy (no memory of its own, nothing to free). */
+typedef struct {
+  int32_t head_dim, rot_dim, layout;
+  float amplitude;
+  uint64_t turns[128];      /* pair i's turns a position, as a 64-bit fraction */
+} kvx_rope;
+
+/* Host only.  KVX_ERR_INVALID_ARG for a NULL pointer or a value outside the
+ * ranges above. */
+kvx_status kvx_rope_init(const kvx_rope_desc *desc, kvx_rope *rope);
+
+/* DEVICE pointers.  Rows are head vectors with unit stride inside; strides are
+ * in elements, so q and k may be views of one fused projection. */
+typedef struct {
+  const void *q;            /* [ntok][q_heads][d], or NULL                    */
+  const void *k;            /* [ntok][k_heads][d], or NULL                    */
+  void *q_out, *k_out;      /* may equal q / k with the same strides (in place);
+                               other overlaps are not supported               */
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+  int64_t ntok;             /* >= 0                                           */
+  int32_t q_heads, k_heads; /* 1..65535 where the pointer is not NULL         */
+  int32_t dtype;            /* kvx_dtype of all four                          */
+  int32_t transpose;        /* 0: y = a R(p) x; 1: y = a R(p)^T x, the gradient
+                               with respect to x                              */
+  const int32_t *positions; /* [ntok], or NULL: first_position + g            */
+  int64_t first_position;
+  uint32_t *status;         /* optional device word, KVX_FLAG_* OR-ed in      */
+} kvx_rope_args;
+
+/* Rotary positions of queries and keys in one launch: y = a R(p) x on the first
+ * rot_dim dimensions of every head, the others copied.  The angle p w_i is
+ * formed exactly modulo one turn in 64-bit fixed point, so its error does not
+ * grow with the position.  A token whose position is outside [0, 2^31) is left
+ * unwritten (KVX_FLAG_BAD_POSITION).  KVX_ERR_INVALID_ARG for a NULL rope,
+ * args or output, sizes outside the limits, or rows that are not aligned to an
+ * element. */
+kvx_status kvx_rope_apply(const kvx_rope *rope, const kvx_rope_args *args, void *stream);
+
+/* An 8-bit paged cache of one layer.  Slot s of request r lies in block
+ * block_table[r][s / block_size] at s % block_size.  A stored value is
+ * code * scale with an e4m3 code (1-4-3 bits, largest 448) and one fp32 scale
+ * for each (block, head), separate for keys and values.  kvx_cache8_write and
+ * kvx_evict8 store powers of two as scales: the smallest 2^e >= 2^-126 with
+ * amax <= 448 * 2^e.  e4m3 keeps its relative precision over its normal range,
+ * so nothing is lost against an arbitrary scale but up to one bit of range, and
+ * a block whose scale grows later re-scales its older codes exactly (but for
+ * those that become subnormal).  kvx_attend8 takes any positive finite scale. */
+typedef struct {
+  void *k_codes, *v_codes;  /* [num_blocks][heads][block_size][head_dim], 16-byte
+                               aligned                                        */
+  float *k_scale, *v_scale; /* [num_blocks][heads]                            */
+  int64_t num_blocks;       /* >= 1                                           */
+  int32_t heads;            /* KV heads, 1..65535                             */
+  int32_t head_dim;         /* a multiple of 16, 16..256                      */
+  int32_t block_size;       /* tokens a block, 1..1024                        */
+  int32_t max_blocks_per_req;   /* width of the block table, >= 1             */
+  const int32_t *block_table;   /* [R][max_blocks_per_req]                    */
+} kvx_cache8;
+
+typedef struct {
+  kvx_cache8 cache;
+  const void *k, *v;        /* [ntok][heads][d] new keys (rotated) and values;
+                               unit stride inside a head                      */
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  int32_t dtype;            /* kvx_dtype of k and v                           */
+  int32_t num_requests;     /* R >= 1                                         */
+  int64_t ntok;             /* new tokens of all requests, >= 0               */
+  const int32_t *cu_seqlens;    /* [R+1] request table, or NULL: one token for
+                                   each request (ntok == R)                   */
+  const int32_t *start;     /* [R] slots each request already holds: its tokens
+                               go to start[r], start[r] + 1, ...; NULL: 0     */
+  const int32_t *src_rows;  /* [ntok] row of k and v that holds token g, or
+                               NULL: g                                        */
+  int64_t num_src_rows;     /* rows of k and v (with src_rows)                */
+  uint32_t *status;
+} kvx_cache8_write_args;
+
+/* Quantise new keys and values into the cache.  A block that starts with the
+ * call's tokens takes the scale they need; one whose first slots already hold
+ * tokens keeps the larger of its own and the needed scale, and its older codes
+ * are re-scaled (rounded to nearest even where they become subnormal).  Slots
+ * that the call does not write keep their codes.  Two requests of one call must
+ * not write to the same block.  An infinity becomes the largest code, a NaN 0
+ * (KVX_FLAG_NOT_FINITE; neither counts for the scale).  Tokens whose slot lies
+ * beyond the table (KVX_FLAG_BAD_LENGTH), whose block id is outside
+ * [0, num_blocks) (KVX_FLAG_BAD_BLOCK) or whose source row is outside
+ * [0, num_src_rows) (KVX_FLAG_BAD_SRC_BLOCK, stored as zeros) are skipped; a malformed
+ * request table writes nothing (KVX_FLAG_BAD_SEQLENS).  One launch. */
+kvx_status kvx_cache8_write(const kvx_cache8_write_args *args, void *stream);
+
+typedef struct {
+  kvx_cache8 cache;
+  const void *q;            /* [ntok][q_heads][d] rotated queries             */
+  void *out;                /* [ntok][q_heads][d]                             */
+  int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+  int32_t dtype;            /* kvx_dtype of q and out                         */
+  int32_t q_heads;          /* a multiple of cache.heads; query head i reads KV
+                               head i / (q_heads / cache.heads)               */
+  int64_t ntok;             /* queries of all requests, >= 0                  */
+  int32_t num_requests;     /* R >= 1                                         */
+  int32_t max_new;          /* bound on one request's queries, >= 1           */
+  const int32_t *cu_seqlens;    /* [R+1], or NULL: one query for each request */
+  const int32_t *lens;      /* [R] slots each request holds, its new tokens
+                               included                                       */
+  int32_t max_len;          /* bound on lens                                  */
+  float scale;              /* on q.k before the softmax, finite              */
+  float *lse;               /* [ntok][q_heads] log-sum-exp, or NULL           */
+  float *weights;           /* [R][heads][weights_stride], or NULL            */
+  int64_t weights_stride;   /* >= max_len                                     */
+  void *workspace;          /* kvx_attend8_workspace_bytes(), 256-byte aligned,
+                               zero-filled before its first use; each call
+                               leaves it ready for the next one               */
+  size_t workspace_bytes;
+  uint32_t *status;
+} kvx_attend8_args;
+
+/* Scratch of a kvx_attend8 call of these sizes; 0 for sizes that it refuses.
+ * A workspace serves calls that are ordered on one stream. */
+size_t kvx_attend8_workspace_bytes(const kvx_attend8_args *args);
+
+/* Attention of new tokens over the 8-bit cache.  Query i of a request with n
+ * new tokens sees slots j <= lens[r] - n + i (its own last):
+ *   out_i = sum_j p_ij v_j,  p_ij = exp(scale q_i.k_j - lse_i),
+ *   lse_i = log sum_j exp(scale q_i.k_j).
+ * A query that sees nothing (an empty request, or more new tokens than slots)
+ * gives zeros and lse = -inf.  With weights, weights[r][h][j] += the sum of p_ij
+ * over the request's queries and the query heads of KV head h: the accumulated
+ * attention weight by which kvx_evict8 chooses.  Slots at or past lens[r] are
+ * never used and may hold anything; codes of held slots must not be NaN.
+ * Softmax statistics and sums are fp32.  A length outside [0, max_len] counts as
+ * 0 (KVX_FLAG_BAD_LENGTH); slots of a block id outside [0, num_blocks) are
+ * masked (KVX_FLAG_BAD_BLOCK); a malformed request table, or a request with
+ * more than max_new queries, writes nothing (KVX_FLAG_BAD_SEQLENS). */
+kvx_status kvx_attend8(const kvx_attend8_args *args, void *stream);
+
+typedef struct {
+  kvx_cache8 cache;         /* its table names the blocks read                */
+  const int32_t *dst_table; /* [R][max_dst_blocks] blocks of the same pool that
+                               take the kept tokens; none of them may be read
+                               by this call                                   */
+  int32_t max_dst_blocks;   /* >= ceil(min(keep, max_len) / block_size)       */
+  int32_t num_requests;
+  const int32_t *lens;      /* [R] slots each request holds                   */
+  int32_t max_len;          /* bound on lens                                  */
+  int32_t keep;             /* slots kept of each request and head, >= 1      */
+  int32_t sinks, recent;    /* the first and last slots, always kept; sinks +
+                               recent <= keep                                 */
+  const float *weights;     /* [R][heads][weights_stride] accumulated weights */
+  int64_t weights_stride;   /* >= max_len                                     */
+  int32_t *kept;            /* [R][heads][keep] kept slots, ascending, then -1 */
+  float *kept_weights;      /* [R][heads][keep] their weights, then 0; or NULL */
+  int32_t *new_lens;        /* [R] min(lens, keep)                            */
+  void *workspace;          /* kvx_evict8_workspace_bytes(), 256-byte aligned */
+  size_t workspace_bytes;
+  uint32_t *status;
+} kvx_evict8_args;
+
+size_t kvx_evict8_workspace_bytes(const kvx_evict8_args *args);
+
+/* Eviction by accumulated attention weight.  For each request and KV head keep
+ * min(lens[r], keep) slots: the first `sinks`, the last `recent`, and of the
+ * others those of the largest weight (equal weights: the lower slot; a NaN
+ * counts as less than every number).  The kept tokens go to slots 0, 1, ... of
+ * the blocks of dst_table in their old order, each block with the scale its
+ * tokens need.  Heads keep different tokens, so slots no longer name positions
+ * (keys are stored rotated, which attention needs and no more).  A length
+ * outside [0, max_len] counts as 0 (KVX_FLAG_BAD_LENGTH); tokens of a source
+ * block id outside the pool are stored as zeros, those of a destination block
+ * id outside it dropped (KVX_FLAG_BAD_BLOCK). */
+kvx_status kvx_evict8(const kvx_evict8_args *args, void *stream);
 
 #ifdef __cplusplus
 }
