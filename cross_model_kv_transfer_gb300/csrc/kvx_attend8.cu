@@ -11,11 +11,11 @@
 
 #include <cmath>
 
+#include "kvx_async.cuh"
 #include "kvx_cache8.cuh"
 
 namespace {
 
-constexpr int kMaxD = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttendParams {
@@ -58,83 +58,653 @@ __device__ __forceinline__ bool requests_ok(const AttendParams &p) {
   }
   return good;
 }
-// q . k_j of one slot.
-__device__ __forceinline__ float dot_row(const uint8_t *row, const float *q, int d) {
-  float s = 0.f;
-  for (int i = 0; i < d; i += 16) {
-    const uint4 t = __ldg(reinterpret_cast<const uint4 *>(row + i));
-    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 a = floats_of(w[e]), b = floats_of(w[e] >> 16);
-      s += q[i + 4 * e] * a.x + q[i + 4 * e + 1] * a.y + q[i + 4 * e + 2] * b.x + q[i + 4 * e + 3] * b.y;
-    }
+// Two dimensions of a finished row; its log-sum-exp with the first.
+__device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int hq, int d, float2 o, float m,
+                                          float l) {
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const int64_t to = g * p.ot + hq * p.oh + d;
+  if (p.bf16) {
+    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + to;
+    out[0] = __float2bfloat16_rn(o.x * inv);
+    out[1] = __float2bfloat16_rn(o.y * inv);
+  } else {
+    float *out = reinterpret_cast<float *>(p.out) + to;
+    out[0] = o.x * inv;
+    out[1] = o.y * inv;
   }
-  return s;
+  if (d == 0) p.lse[g * p.Hq + hq] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// One warp for each query and head: 32 slots at a time, a lane each, then the
-// lanes share the value dimensions.
-__global__ void __launch_bounds__(128) attend_kernel(const __grid_constant__ AttendParams p) {
-  __shared__ float qs[4][kMaxD];
-  if (!requests_ok(p)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) raise(p.status, KVX_FLAG_BAD_SEQLENS);
+// --- few queries: the slots split over the whole GPU -----------------------------
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// A maximum to subtract: 0 before any score (exp2(-inf - 0) is 0; a NaN score stays NaN).
+__device__ __forceinline__ float finite_or_0(float m) { return m > -INFINITY ? m : 0.f; }
+// D += A B of f16 operands, fp32 accumulation: 16 x 8, 16 deep.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values, transposed between the lanes.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t b) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&b));
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// The flattened work: for each request, each KV head, each group of columns
+// (a column is a query of one head), the steps over its slots.  CTA c of n
+// takes the steps [c T / n, (c + 1) T / n) of all T, so every CTA reads the same
+// number of bytes whatever the lengths are, and a request's slots are split
+// between as many CTAs as that takes.
+struct Walk {
+  int r, len, fresh, segs, seg, steps, step;   // fresh: new tokens; segs: heads x column groups
+  int64_t beg;
+};
+
+template <int DP_, int NT_, int PARTS_, int MT_, int WARPS_, int STAGES_>
+struct SplitCfg {
+  static constexpr int DP = DP_;         // head_dim, padded
+  static constexpr int NT = NT_;         // column tiles of 8
+  static constexpr int PARTS = PARTS_;   // f16 parts of an operand: 1 for bf16, 2 for fp32 queries
+  static constexpr int MT = MT_;         // 16-slot tiles a warp takes at a time
+  static constexpr int WARPS = WARPS_, STAGES = STAGES_;
+  static constexpr int KW = 16 * MT, KT = KW * WARPS, COLS = 8 * NT, CH = DP / 16;
+  static constexpr int ROWF = DP + 4;    // floats of a reduced row (padded against bank conflicts)
+  static constexpr size_t kTile = (size_t)KW * DP;              // bytes of one K or V tile
+  static constexpr size_t kStage = 2 * kTile + 2 * KW * 4 + 16; // + scales + valid bits
+  static constexpr size_t kRing = kStage * STAGES * WARPS;
+  static constexpr size_t kReduce = (size_t)WARPS * (8 * ROWF + 2 * COLS) * 4;   // 8 columns at a time
+  static constexpr size_t kQ = (size_t)PARTS * COLS * DP * 2;   // query fragments (NT * PARTS > 2)
+  static constexpr bool kQInSmem = NT * PARTS > 2;
+  static constexpr size_t kSmem = kRing + kReduce + (kQInSmem ? kQ : 0) + COLS * 4 + 64;
+  static constexpr int kSlot = COLS * (DP + 2);                 // floats of a partial result
+};
+
+struct SplitParams {
+  AttendParams a;
+  int groups;            // column groups of max_new queries
+  int *arrived;          // [R][H][groups] CTAs that have left a partial result
+  float *partial;        // [2 * grid][kSlot]
+  float *scores;         // [R][H][groups][max_len][COLS], base 2, or NULL
+  int vec_q;
+};
+
+template <class C>
+__device__ __forceinline__ void enter_request(const SplitParams &p, Walk &w) {
+  w.len = len_of(p.a, w.r);
+  w.beg = p.a.req.begin(w.r);
+  w.fresh = (int)(p.a.req.begin(w.r + 1) - w.beg);
+  w.steps = w.len > 0 ? (w.len + C::KT - 1) / C::KT : 1;
+  w.segs = p.a.H * ((w.fresh * p.a.G + C::COLS - 1) / C::COLS);
+}
+template <class C>
+__device__ __forceinline__ void advance(const SplitParams &p, Walk &w) {
+  if (++w.step < w.steps) return;
+  w.step = 0;
+  if (++w.seg < w.segs) return;
+  w.seg = 0;
+  do {
+    if (++w.r >= p.a.req.R) return;
+    enter_request<C>(p, w);
+  } while (w.segs == 0);
+}
+// Total steps, and (second form) the walk at step `at`.  A warp scans 32
+// requests at a time.
+template <class C>
+__device__ __forceinline__ int64_t steps_of(const SplitParams &p, int r) {
+  if (r >= p.a.req.R) return 0;
+  Walk w;
+  w.r = r;
+  enter_request<C>(p, w);
+  return (int64_t)w.steps * w.segs;
+}
+template <class C>
+__device__ int64_t total_steps(const SplitParams &p) {
+  int64_t sum = 0;
+  for (int r = threadIdx.x % 32; r < p.a.req.R; r += 32) sum += steps_of<C>(p, r);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  return sum;
+}
+template <class C>
+__device__ Walk walk_at(const SplitParams &p, int64_t at) {
+  const int lane = threadIdx.x % 32;
+  Walk w = {};
+  int64_t before = 0;
+  for (int r0 = 0; r0 < p.a.req.R; r0 += 32) {
+    const int64_t mine = steps_of<C>(p, r0 + lane);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned here = __ballot_sync(~0u, at < before + upto);
+    if (here) {
+      const int who = __ffs(here) - 1;
+      w.r = r0 + who;
+      enter_request<C>(p, w);
+      const int64_t in = at - before - __shfl_sync(~0u, upto - mine, who);
+      w.seg = (int)(in / w.steps);
+      w.step = (int)(in % w.steps);
+      return w;
+    }
+    before += __shfl_sync(~0u, upto, 31);
+  }
+  return w;
+}
+
+// Where 16-byte piece c of slot row j lies in a tile: pieces move by the row,
+// so that both ways of reading (one piece of eight rows, four pieces of two
+// rows) meet every bank once.
+template <int DP>
+__device__ __forceinline__ uint32_t piece_at(int j, int c) {
+  if constexpr (DP == 64) return (uint32_t)(j * 64 + ((c ^ (j >> 1 & 3)) << 4));
+  const int f = (j & 1) << 2 | (j & 6) >> 1;
+  return (uint32_t)(j * DP + ((c ^ f) << 4));
+}
+
+// One warp: 16 MT slots at a time against COLS columns, its own ring of
+// cp.async stages, its own running maximum and sum.  Scores are formed
+// transposed, S^T = K Q^T with slots as the 16 rows, so the codes (converted to
+// f16, exactly) are the large operand of both products and the few columns the
+// small one; O^T = V^T P^T takes V by transposing 16-bit loads that carry two
+// dimensions each.
+//
+// Ranges.  A query row is multiplied by the power of two that brings its
+// largest element to [2^14, 2^15): f16 then holds a bf16 row exactly down to
+// 2^-38 of that element (an fp32 row in two parts).  Probabilities carry their
+// block's value scale, as a share of the largest one seen, times 2^14: f16's 11
+// bits hold down to 2^-28 of the largest product, which costs an output less
+// than its own rounding to bf16 (fp32 outputs take two parts here too).
+template <class C>
+__global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_constant__ SplitParams p) {
+  constexpr int DP = C::DP, NT = C::NT, PARTS = C::PARTS, MT = C::MT, KW = C::KW, CH = C::CH;
+  constexpr int QD = DP / 64;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const AttendParams &a = p.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  unsigned char *ring = smem + warp * C::STAGES * C::kStage;
+  float *red = reinterpret_cast<float *>(smem + C::kRing);
+  float *red_m = red + C::WARPS * 8 * C::ROWF, *red_l = red_m + C::WARPS * C::COLS;
+  uint2 *qs = reinterpret_cast<uint2 *>(smem + C::kRing + C::kReduce);
+  float *col_scale = reinterpret_cast<float *>(smem + C::kRing + C::kReduce + (C::kQInSmem ? C::kQ : 0));
+  int *flag = reinterpret_cast<int *>(col_scale + C::COLS);
+  if (!requests_ok(a)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
     return;
   }
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t row = (int64_t)blockIdx.x * 4 + warp;
-  if (row >= p.req.ntok * p.Hq) return;
-  const int64_t g = row / p.Hq;
-  const int hq = (int)(row % p.Hq), h = hq / p.G, r = p.req.of(g);
-  const int len = len_of(p, r);
-  if (len != __ldg(p.lens + r) && lane == 0) raise(p.status, KVX_FLAG_BAD_LENGTH);
-  const int64_t n = p.req.begin(r + 1) - p.req.begin(r);
-  const int64_t seen = len - n + (g - p.req.begin(r)) + 1;   // slots [0, seen)
-  for (int i = lane; i < p.d; i += 32) qs[warp][i] = q_at(p, g, hq, i);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[kMaxD / 32] = {};
-  for (int64_t j0 = 0; j0 < seen; j0 += 32) {
-    const int64_t j = j0 + lane, page = j < seen ? page_of(p, r, j / p.bs) : -1;
-    const int64_t at = page < 0 ? 0 : (page * p.H + h) * p.bs + j % p.bs;
-    float x = -INFINITY, sv = 0.f;
-    if (page >= 0) {
-      x = dot_row(p.k + at * p.d, qs[warp], p.d) * (p.ks[page * p.H + h] * p.c);
-      sv = p.vs[page * p.H + h];
-    } else if (j < seen) {
-      raise(p.status, KVX_FLAG_BAD_BLOCK);
+  if (blockIdx.x == 0)
+    for (int r = threadIdx.x; r < a.req.R; r += blockDim.x)
+      if (len_of(a, r) != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
+  const int64_t T = total_steps<C>(p), N = T < gridDim.x ? T : gridDim.x;   // CTAs at work
+  if (blockIdx.x >= N) return;
+  const int64_t first = blockIdx.x * T / N, last = (blockIdx.x + 1) * T / N;
+  Walk w = walk_at<C>(p, first), pw = w;
+  int64_t ahead = first;
+
+  // Copy the warp's next tile into a stage: lane l looks up slot l, then 16-byte
+  // pieces go out row by row.
+  const auto fetch = [&](int stage) {
+    unsigned char *st = ring + stage * C::kStage;
+    if (ahead < last) {
+      const int h = pw.seg / (pw.segs / a.H);
+      const int64_t j = (int64_t)pw.step * C::KT + warp * KW + lane % KW;
+      int64_t page = -1;
+      if (j < pw.len) {
+        page = page_of(a, pw.r, j / a.bs);
+        if (page < 0) raise(a.status, KVX_FLAG_BAD_BLOCK);
+      }
+      const int64_t block = page < 0 ? 0 : page * a.H + h;
+      const int64_t row = block * a.bs + (page < 0 ? 0 : j % a.bs);
+      const unsigned valid = __ballot_sync(~0u, page >= 0);
+      const uint32_t sc = (uint32_t)__cvta_generic_to_shared(st + 2 * C::kTile);
+      if (lane < KW) {
+        cp_async4(sc + lane * 4, a.ks + block, page >= 0 ? 4 : 0);
+        cp_async4(sc + (KW + lane) * 4, a.vs + block, page >= 0 ? 4 : 0);
+      }
+      if (lane == 0) *reinterpret_cast<unsigned *>(st + 2 * C::kTile + 2 * KW * 4) = valid;
+      const int real = a.d / 16;
+#pragma unroll
+      for (int i = 0; i < KW * CH / 32; ++i) {
+        const int at = i * 32 + lane, j = at / CH, c = at % CH;
+        const int64_t from = __shfl_sync(~0u, row, j);
+        const bool there = c < real && (valid >> j & 1);
+        const int64_t off = there ? from * a.d + c * 16 : 0;
+        const uint32_t bytes = there ? 16 : 0;
+        cp_async16(st + piece_at<DP>(j, c), a.k + off, bytes);
+        cp_async16(st + C::kTile + piece_at<DP>(j, c), a.v + off, bytes);
+      }
+      advance<C>(p, pw);
+      ++ahead;
     }
-    float top = x;
+    cp_async_commit();
+  };
 #pragma unroll
-    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
-    if (top == -INFINITY) continue;
-    const float now = fmaxf(m, top), down = exp2f(m - now);
-    const float e = exp2f(x - now);
-    float sum = e;
+  for (int s = 0; s < C::STAGES - 1; ++s) fetch(s);
+
+  uint32_t qf[C::kQInSmem ? 1 : NT][PARTS][QD * 4][2];
+  float cs[NT][2];           // factors of columns 2t, 2t + 1
+  int limit[NT][2];          // last slot that they see
+  float m[NT][2], l[NT][2], o[NT][CH][4], vref = 0.f;
+  int stage = 0;
+  bool enter = true;
+  int64_t seg_first = first;   // the CTA's first step of the segment
+  for (int64_t now = first; now < last; ++now) {
+    const int groups = w.segs / a.H, h = w.seg / groups, col0 = w.seg % groups * C::COLS;
+    const int cols = w.fresh * a.G;
+    if (enter) {
+      enter = false;
+      seg_first = now;
+      vref = 0.f;
 #pragma unroll
-    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
-    l = l * down + sum;
-    m = now;
-    for (int i = 0; i < kMaxD / 32; ++i) o[i] *= down;
-    for (int k = 0; k < 32; ++k) {
-      const int64_t a = __shfl_sync(~0u, at, k);
-      const float w = __shfl_sync(~0u, e * sv, k);
-      if (w == 0.f) continue;
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int i = 0; i < kMaxD / 32; ++i)
-        if (32 * i + lane < p.d) o[i] += w * floats_of(__ldg(p.v + a * p.d + 32 * i + lane)).x;
+        for (int e = 0; e < 2; ++e) {
+          m[n][e] = -INFINITY;
+          l[n][e] = 0.f;
+          const int col = col0 + 8 * n + 2 * t + e;
+          limit[n][e] = col < cols ? w.len - w.fresh + col / a.G : -1;
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][c][e] = 0.f;
+      }
+      // query fragments: the thread's column is g, its dimensions 64 q + 16 t ..
+      if (C::kQInSmem) __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (C::kQInSmem && n % C::WARPS != warp % (NT < C::WARPS ? NT : C::WARPS)) continue;
+        if (C::kQInSmem && warp >= NT) continue;
+        const int col = col0 + 8 * n + g;
+        float x[QD][16];
+        float top = 0.f;
+        const int64_t tok = w.beg + col / a.G;
+        const int hq = h * a.G + col % a.G;
+#pragma unroll
+        for (int q = 0; q < QD; ++q) {
+          const int d0 = 64 * q + 16 * t;
+          const bool in = col < cols && d0 < a.d;
+          const int64_t at = tok * a.qt + hq * a.qh + d0;
+          if (PARTS == 1) {
+            const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + at;
+            if (p.vec_q) {
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                const uint4 y = in ? __ldg(reinterpret_cast<const uint4 *>(src) + v) : make_uint4(0, 0, 0, 0);
+                const uint32_t b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  x[q][8 * v + 2 * e] = __uint_as_float(b[e] << 16);
+                  x[q][8 * v + 2 * e + 1] = __uint_as_float(b[e] & 0xffff0000u);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[q][e] = in ? __bfloat162float(src[e]) : 0.f;
+            }
+          } else {
+            const float *src = reinterpret_cast<const float *>(a.q) + at;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[q][e] = in ? __ldg(src + e) : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[q][e]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        int e2 = (int)(__float_as_uint(top) >> 23) - 127;
+        e2 = e2 < -100 ? -100 : e2;
+        const float up = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
+        const float factor = a.c * __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
+#pragma unroll
+        for (int q = 0; q < QD; ++q)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = x[q][4 * s + e] * up;
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+              const uint32_t b0 = half2_bits(y[0], y[1]), b1 = half2_bits(y[2], y[3]);
+              if (C::kQInSmem) {
+                qs[((part * NT + n) * QD * 4 + q * 4 + s) * 32 + lane] = make_uint2(b0, b1);
+              } else {
+                qf[C::kQInSmem ? 0 : n][part][q * 4 + s][0] = b0;
+                qf[C::kQInSmem ? 0 : n][part][q * 4 + s][1] = b1;
+              }
+              const float2 f0 = half2_floats(b0), f1 = half2_floats(b1);
+              y[0] -= f0.x; y[1] -= f0.y; y[2] -= f1.x; y[3] -= f1.y;
+            }
+          }
+        if (C::kQInSmem) {
+          if (t == 0) col_scale[8 * n + g] = factor;
+        } else {
+          cs[n][0] = __shfl_sync(~0u, factor, 8 * t);        // lane 4 g' holds column g'
+          cs[n][1] = __shfl_sync(~0u, factor, 8 * t + 4);
+        }
+      }
+      if (C::kQInSmem) {
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          cs[n][0] = col_scale[8 * n + 2 * t];
+          cs[n][1] = col_scale[8 * n + 2 * t + 1];
+        }
+      }
+    }
+
+    cp_async_wait<C::STAGES - 2>();
+    __syncwarp();
+    fetch(stage == 0 ? C::STAGES - 1 : stage - 1);   // the tile of the step before is spent
+    {
+      const unsigned char *st = ring + stage * C::kStage;
+      const uint32_t vaddr = (uint32_t)__cvta_generic_to_shared(st + C::kTile);
+      const float *ks = reinterpret_cast<const float *>(st + 2 * C::kTile), *vs = ks + KW;
+      const unsigned valid = *reinterpret_cast<const unsigned *>(st + 2 * C::kTile + 2 * KW * 4);
+      const int64_t j0 = (int64_t)w.step * C::KT + warp * KW;
+      if (valid || (p.scores && j0 < w.len)) {
+        // S^T = K Q^T
+        float s[MT][NT][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+#pragma unroll
+        for (int q = 0; q < QD; ++q) {
+          uint4 k0[MT], k1[MT];
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            k0[i] = *reinterpret_cast<const uint4 *>(st + piece_at<DP>(16 * i + g, 4 * q + t));
+            k1[i] = *reinterpret_cast<const uint4 *>(st + piece_at<DP>(16 * i + g + 8, 4 * q + t));
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t b[NT][PARTS][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part) {
+                if (C::kQInSmem) {
+                  const uint2 y = qs[((part * NT + n) * QD * 4 + q * 4 + u) * 32 + lane];
+                  b[n][part][0] = y.x;
+                  b[n][part][1] = y.y;
+                } else {
+                  b[n][part][0] = qf[C::kQInSmem ? 0 : n][part][q * 4 + u][0];
+                  b[n][part][1] = qf[C::kQInSmem ? 0 : n][part][q * 4 + u][1];
+                }
+              }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              const uint32_t x0 = u == 0 ? k0[i].x : u == 1 ? k0[i].y : u == 2 ? k0[i].z : k0[i].w;
+              const uint32_t x1 = u == 0 ? k1[i].x : u == 1 ? k1[i].y : u == 2 ? k1[i].z : k1[i].w;
+              const uint32_t f[4] = {f16x2_of(x0), f16x2_of(x1), f16x2_of(x0 >> 16), f16x2_of(x1 >> 16)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) mma16816(s[i][n], f, b[n][part][0], b[n][part][1]);
+            }
+          }
+        }
+        // scale, mask, the tile's maxima
+        float vmax = 0.f, vsc[MT][2];
+        float top[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int j = 16 * i + 8 * half + g;
+            const float kscale = ks[j];
+            const bool here = valid >> j & 1;
+            vsc[i][half] = vs[j];
+            vmax = fmaxf(vmax, vsc[i][half]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float &x = s[i][n][2 * half + e];
+                x = here && j0 + j <= limit[n][e] ? x * (kscale * cs[n][e]) : -INFINITY;
+                top[n][e] = fmaxf(top[n][e], x);
+              }
+          }
+        if (p.scores) {
+          const int64_t seg = ((int64_t)w.r * a.H + h) * p.groups + w.seg % groups;
+          float *to = p.scores + seg * a.max_len * C::COLS;
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int64_t j = j0 + 16 * i + 8 * half + g;
+              if (j >= w.len) continue;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                *reinterpret_cast<float2 *>(to + j * C::COLS + 8 * n + 2 * t) =
+                    make_float2(s[i][n][2 * half], s[i][n][2 * half + 1]);
+            }
+        }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, off));
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(~0u, top[n][e], off));
+        }
+        bool grew = vmax > vref;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) grew = grew || top[n][e] > m[n][e];
+        if (__any_sync(~0u, grew)) {   // seldom after the first tiles
+          const float vnew = fmaxf(vref, vmax), vdown = vnew > 0.f ? vref / vnew : 0.f;
+          vref = vnew;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float mm = fmaxf(m[n][e], top[n][e]);
+              const float down = ex2(m[n][e] - finite_or_0(mm));
+              m[n][e] = mm;
+              l[n][e] *= down;
+#pragma unroll
+              for (int c = 0; c < CH; ++c) {
+                o[n][c][e] *= down * vdown;
+                o[n][c][2 + e] *= down * vdown;
+              }
+            }
+        }
+        // P^T: probabilities times their value scale, transposed between the lanes
+        uint32_t pb[MT][NT][PARTS][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float f = vref > 0.f ? vsc[i][half] / vref * 16384.f : 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const float p0 = ex2(s[i][n][2 * half] - finite_or_0(m[n][0]));
+              const float p1 = ex2(s[i][n][2 * half + 1] - finite_or_0(m[n][1]));
+              l[n][0] += p0;
+              l[n][1] += p1;
+              float y0 = p0 * f, y1 = p1 * f;
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part) {
+                const uint32_t b = half2_bits(y0, y1);
+                pb[i][n][part][half] = transpose8x8(b);
+                const float2 back = half2_floats(b);
+                y0 -= back.x;
+                y1 -= back.y;
+              }
+            }
+          }
+        // O^T += V^T P^T: rows g and g + 8 of a 16-dimension piece are its
+        // dimensions 2g and 2g + 1
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int c = 0; c < CH; c += 2) {
+            uint32_t v[4];
+            ldmatrix_x4_trans(v, vaddr + piece_at<DP>(16 * i + lane % 16, c + lane / 16));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t y0 = __byte_perm(v[2 * k], 0, 0x3120), y1 = __byte_perm(v[2 * k + 1], 0, 0x3120);
+              const uint32_t f[4] = {f16x2_of(y0), f16x2_of(y0 >> 16), f16x2_of(y1), f16x2_of(y1 >> 16)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part)
+                  mma16816(o[n][c + k], f, pb[i][n][part][0], pb[i][n][part][1]);
+            }
+          }
+      }
+    }
+    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+
+    const bool seg_done = w.step + 1 == w.steps;
+    if (seg_done || now + 1 == last) {
+      // join the warps, eight columns at a time
+      const bool whole = seg_done && w.step + 1 <= now - seg_first + 1;
+      // where it goes: the result, or a partial one (first or last of the CTA)
+      float *slot = p.partial + ((int64_t)blockIdx.x * 2 + (seg_first == first ? 0 : 1)) * C::kSlot;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(~0u, l[n][e], off);
+          float *row = red + (warp * 8 + 2 * t + e) * C::ROWF;
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            *reinterpret_cast<float2 *>(row + 16 * c + 2 * g) =
+                make_float2(o[n][c][e] * (1.f / 16384.f) * vref, o[n][c][2 + e] * (1.f / 16384.f) * vref);
+          if (g == 0) {
+            red_m[warp * C::COLS + 8 * n + 2 * t + e] = m[n][e];
+            red_l[warp * C::COLS + 8 * n + 2 * t + e] = l[n][e];
+          }
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < 8 * (DP / 2); x += 32 * C::WARPS) {
+          const int in = x / (DP / 2), col = 8 * n + in, d = x % (DP / 2) * 2, at = col0 + col;
+          float mm = -INFINITY, ll = 0.f;
+          float2 oo = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int v = 0; v < C::WARPS; ++v) mm = fmaxf(mm, red_m[v * C::COLS + col]);
+#pragma unroll
+          for (int v = 0; v < C::WARPS; ++v) {
+            const float f = ex2(red_m[v * C::COLS + col] - finite_or_0(mm));
+            const float2 y = *reinterpret_cast<const float2 *>(red + (v * 8 + in) * C::ROWF + d);
+            ll += f * red_l[v * C::COLS + col];
+            oo.x += f * y.x;
+            oo.y += f * y.y;
+          }
+          if (whole) {
+            if (at < cols && d < a.d) store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, ll);
+          } else {
+            *reinterpret_cast<float2 *>(slot + col * DP + d) = oo;
+            if (d == 0) {
+              slot[C::COLS * DP + col] = mm;
+              slot[C::COLS * (DP + 1) + col] = ll;
+            }
+          }
+        }
+        __syncthreads();
+      }
+      if (!whole) {
+        // the last CTA of the segment to get here joins all of its parts
+        const int64_t begin = now - w.step, end = begin + w.steps;   // the segment's steps
+        const int64_t c0 = ((begin + 1) * N - 1) / T, c1 = (end * N - 1) / T;
+        int *arrived = p.arrived + ((int64_t)w.r * a.H + h) * p.groups + w.seg % groups;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) *flag = atomicAdd(arrived, 1) == (int)(c1 - c0);
+        __syncthreads();
+        if (*flag) {
+          __threadfence();
+          if (threadIdx.x == 0) *arrived = 0;   // ready for the next call
+          for (int x = threadIdx.x; x < C::COLS * (DP / 2); x += 32 * C::WARPS) {
+            const int col = x / (DP / 2), d = x % (DP / 2) * 2, at = col0 + col;
+            if (at >= cols || d >= a.d) continue;
+            float mm = -INFINITY, ll = 0.f;
+            float2 oo = make_float2(0.f, 0.f);
+            for (int64_t c = c0; c <= c1; ++c) {
+              // CTA c's part is its first segment unless the segment begins inside it
+              const bool second = c == c0 && c * T / N != begin;
+              const float *part = p.partial + (c * 2 + second) * C::kSlot;
+              const float pm = __ldcg(part + C::COLS * DP + col), pl = __ldcg(part + C::COLS * (DP + 1) + col);
+              const float2 y = __ldcg(reinterpret_cast<const float2 *>(part + col * DP + d));
+              const float top = fmaxf(mm, pm), f0 = ex2(mm - finite_or_0(top)), f1 = ex2(pm - finite_or_0(top));
+              ll = ll * f0 + pl * f1;
+              oo.x = oo.x * f0 + y.x * f1;
+              oo.y = oo.y * f0 + y.y * f1;
+              mm = top;
+            }
+            store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, ll);
+          }
+        }
+      }
+      enter = true;
+    }
+    advance<C>(p, w);
+  }
+}
+
+// weights[r][h][j] += sum over the columns of exp2(score - lse): the scores that
+// the split kernel left, read once.
+__global__ void __launch_bounds__(256) weights_of_scores_kernel(const __grid_constant__ SplitParams p,
+                                                                int cols_of_group) {
+  const AttendParams &a = p.a;
+  extern __shared__ float lse2[];
+  const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
+  const int64_t beg = a.req.begin(r);
+  const int cols = (int)(a.req.begin(r + 1) - beg) * a.G;
+  if (!requests_ok(a)) return;
+  for (int c = threadIdx.x; c < cols; c += 256)
+    lse2[c] = a.lse[(beg + c / a.G) * a.Hq + h * a.G + c % a.G] * kLog2e;
+  __syncthreads();
+  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (j >= len) return;
+  float sum = 0.f;
+  for (int c0 = 0; c0 < cols; c0 += cols_of_group) {
+    const int64_t seg = ((int64_t)r * a.H + h) * p.groups + c0 / cols_of_group;
+    const float *x = p.scores + (seg * a.max_len + j) * cols_of_group;
+    for (int c = 0; c < cols_of_group && c0 + c < cols; c += 4) {
+      const float4 y = *reinterpret_cast<const float4 *>(x + c);
+      const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c0 + c + e < cols && z[e] > -INFINITY) sum += ex2(z[e] - lse2[c0 + c + e]);
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxD / 32; ++i) {
-    if (32 * i + lane >= p.d) continue;
-    const int64_t to = g * p.ot + hq * p.oh + 32 * i + lane;
-    if (p.bf16)
-      reinterpret_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(o[i] * inv);
-    else
-      reinterpret_cast<float *>(p.out)[to] = o[i] * inv;
-  }
-  if (lane == 0) p.lse[g * p.Hq + hq] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
 }
 
 // weights[r][h][j] += sum of p_ij: a thread for each slot, the scores again.
@@ -175,11 +745,61 @@ kvx_status check(const kvx_attend8_args *a) {
   return KVX_OK;
 }
 
+// Sizes of a call's workspace and grid.
+struct Shape {
+  int cols, groups, grid;      // columns of a group, groups, CTAs
+  size_t arrived, partial, lse, scores, bytes;   // offsets
+  bool spool;                  // the scores are kept for the weights
+};
+constexpr int kGrid = 152;     // one CTA an SM
+
+Shape shape_of(const kvx_attend8_args *a) {
+  Shape s;
+  const int64_t G = a->q_heads / a->cache.heads, most = G * a->max_new;
+  s.cols = most <= 8 ? 8 : most <= 16 || a->cache.head_dim > 128 ? 16 : 32;   // registers hold 4096 sums
+  s.groups = (int)((most + s.cols - 1) / s.cols);
+  s.grid = kGrid;
+  const int dp = a->cache.head_dim <= 64 ? 64 : a->cache.head_dim <= 128 ? 128 : 256;
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  s.spool = a->weights && most <= 64;
+  s.arrived = 0;
+  s.partial = up((size_t)a->num_requests * a->cache.heads * s.groups * 4);
+  s.lse = s.partial + up((size_t)2 * s.grid * s.cols * (dp + 2) * 4);
+  s.scores = s.lse + up((size_t)a->ntok * a->q_heads * 4);
+  s.bytes = s.scores + (s.spool ? up((size_t)a->num_requests * a->cache.heads * s.groups * a->max_len * s.cols * 4)
+                                : 0);
+  return s;
+}
+
+template <int DP, int NT, int PARTS>
+kvx_status launch_split(const SplitParams &p, int grid, cudaStream_t s) {
+  // 16 slots a warp and 8 warps; stages for about 128 KB in flight
+  using C = SplitCfg<DP, NT, PARTS, 1, 8, DP == 64 ? 8 : DP == 128 ? 5 : 2>;
+  static_assert(C::kSmem <= 227 * 1024, "shared memory");
+  const cudaError_t e =
+      cudaFuncSetAttribute(split_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e != cudaSuccess) return KVX_ERR_CUDA;
+  split_kernel<C><<<grid, 32 * C::WARPS, C::kSmem, s>>>(p);
+  return launched();
+}
+template <int DP, int PARTS>
+kvx_status launch_cols(const SplitParams &p, int cols, int grid, cudaStream_t s) {
+  if (cols == 8) return launch_split<DP, 1, PARTS>(p, grid, s);
+  if (cols == 16) return launch_split<DP, 2, PARTS>(p, grid, s);
+  if constexpr (DP <= 128) return launch_split<DP, 4, PARTS>(p, grid, s);
+  return KVX_ERR_UNSUPPORTED;
+}
+template <int PARTS>
+kvx_status launch_dim(const SplitParams &p, int cols, int grid, cudaStream_t s) {
+  return p.a.d <= 64    ? launch_cols<64, PARTS>(p, cols, grid, s)
+         : p.a.d <= 128 ? launch_cols<128, PARTS>(p, cols, grid, s)
+                        : launch_cols<256, PARTS>(p, cols, grid, s);
+}
+
 }  // namespace
 
 extern "C" size_t kvx_attend8_workspace_bytes(const kvx_attend8_args *a) {
-  if (check(a) != KVX_OK) return 0;
-  return 256 + (size_t)a->ntok * a->q_heads * 4;
+  return check(a) == KVX_OK ? shape_of(a).bytes : 0;
 }
 
 extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
@@ -203,7 +823,9 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.oh = a->out_head_stride;
   p.table = c.block_table;
   p.lens = a->lens;
-  p.lse = a->lse ? a->lse : (float *)((char *)a->workspace + 256);
+  const Shape sh = shape_of(a);
+  char *ws = (char *)a->workspace;
+  p.lse = a->lse ? a->lse : (float *)(ws + sh.lse);
   p.weights = a->weights;
   p.status = a->status;
   p.req = {a->cu_seqlens, a->num_requests, a->ntok};
@@ -220,10 +842,19 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.bf16 = size == 2;
   p.c = a->scale * kLog2e;
   cudaStream_t s = (cudaStream_t)stream;
-  const int64_t rows = a->ntok * a->q_heads;
-  attend_kernel<<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p);
-  if (const kvx_status st = launched()) return st;
-  if (!a->weights || a->max_len == 0) return KVX_OK;
-  weights_kernel<<<dim3((a->max_len + 127) / 128, c.heads, a->num_requests), 128, 0, s>>>(p);
+  SplitParams sp;
+  sp.a = p;
+  sp.groups = sh.groups;
+  sp.arrived = (int *)(ws + sh.arrived);
+  sp.partial = (float *)(ws + sh.partial);
+  sp.scores = sh.spool ? (float *)(ws + sh.scores) : nullptr;
+  sp.vec_q = aligned_to(a->q, 16) && ((p.qt | p.qh) * size) % 16 == 0;
+  const kvx_status st = size == 2 ? launch_dim<1>(sp, sh.cols, sh.grid, s) : launch_dim<2>(sp, sh.cols, sh.grid, s);
+  if (st != KVX_OK || !a->weights || a->max_len == 0) return st;
+  if (sh.spool)
+    weights_of_scores_kernel<<<dim3((a->max_len + 255) / 256, c.heads, a->num_requests), 256,
+                               p.G * p.max_new * 4, s>>>(sp, sh.cols);
+  else
+    weights_kernel<<<dim3((a->max_len + 127) / 128, c.heads, a->num_requests), 128, 0, s>>>(p);
   return launched();
 }
