@@ -28,8 +28,9 @@ struct AttendParams {
   float *lse, *weights;
   uint32_t *status;
   Requests req;
-  int64_t num_blocks, wstride;
-  int H, Hq, G, d, bs, max_blocks, max_len, max_new, bf16;
+  int64_t wstride;
+  int num_blocks, H, Hq, G, d, bs, max_blocks, max_len, max_new, bf16;
+  uint32_t bs_mul, bs_shift;   // j / bs = j * bs_mul >> bs_shift for j < 2^31
   float c;   // scale * log2(e): scores are kept in base 2
 };
 
@@ -38,10 +39,14 @@ __device__ __forceinline__ int len_of(const AttendParams &p, int r) {
   const int n = __ldg(p.lens + r);
   return n < 0 || n > p.max_len ? 0 : n;
 }
-// The pool's block of slot j, or -1.
-__device__ __forceinline__ int64_t page_of(const AttendParams &p, int r, int64_t block) {
-  const int64_t page = block < p.max_blocks ? (int64_t)__ldg(p.table + (int64_t)r * p.max_blocks + block) : -1;
-  return page >= 0 && page < p.num_blocks ? page : -1;
+// The request's block that holds slot j: j / bs by a multiplication.
+__device__ __forceinline__ uint32_t block_of(const AttendParams &p, int j) {
+  return (uint32_t)((uint64_t)(uint32_t)j * p.bs_mul >> p.bs_shift);
+}
+// The pool's block of a request's block, or -1.
+__device__ __forceinline__ int page_of(const AttendParams &p, int r, uint32_t block) {
+  const int page = block < (uint32_t)p.max_blocks ? __ldg(p.table + (int64_t)r * p.max_blocks + block) : -1;
+  return page < p.num_blocks ? page : -1;
 }
 __device__ __forceinline__ float q_at(const AttendParams &p, int64_t g, int h, int i) {
   const int64_t at = g * p.qt + h * p.qh + i;
@@ -111,22 +116,19 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 __device__ __forceinline__ float2 half2_floats(uint32_t b) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&b));
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 // The flattened work: for each request, each KV head, each group of columns
 // (a column is a query of one head), the steps over its slots.  CTA c of n
 // takes the steps [c T / n, (c + 1) T / n) of all T, so every CTA reads the same
 // number of bytes whatever the lengths are, and a request's slots are split
 // between as many CTAs as that takes.
 struct Walk {
-  int r, len, fresh, segs, seg, steps, step;   // fresh: new tokens; segs: heads x column groups
+  int r, len, fresh, groups, h, group, steps, step;   // fresh: new tokens; groups: of columns
   int64_t beg;
 };
 
 template <int DP_, int NT_, int PARTS_, int MT_, int WARPS_, int STAGES_>
 struct SplitCfg {
+  static constexpr int RC = WARPS_ > 8 ? 2 : 4;   // columns joined at a time
   static constexpr int DP = DP_;         // head_dim, padded
   static constexpr int NT = NT_;         // column tiles of 8
   static constexpr int PARTS = PARTS_;   // f16 parts of an operand: 1 for bf16, 2 for fp32 queries
@@ -137,7 +139,7 @@ struct SplitCfg {
   static constexpr size_t kTile = (size_t)KW * DP;              // bytes of one K or V tile
   static constexpr size_t kStage = 2 * kTile + 2 * KW * 4 + 16; // + scales + valid bits
   static constexpr size_t kRing = kStage * STAGES * WARPS;
-  static constexpr size_t kReduce = (size_t)WARPS * (8 * ROWF + 2 * COLS) * 4;   // 8 columns at a time
+  static constexpr size_t kReduce = (size_t)WARPS * (RC * ROWF + 2 * COLS) * 4;
   static constexpr size_t kQ = (size_t)PARTS * COLS * DP * 2;   // query fragments (NT * PARTS > 2)
   static constexpr bool kQInSmem = NT * PARTS > 2;
   static constexpr size_t kSmem = kRing + kReduce + (kQInSmem ? kQ : 0) + COLS * 4 + 64;
@@ -159,18 +161,20 @@ __device__ __forceinline__ void enter_request(const SplitParams &p, Walk &w) {
   w.beg = p.a.req.begin(w.r);
   w.fresh = (int)(p.a.req.begin(w.r + 1) - w.beg);
   w.steps = w.len > 0 ? (w.len + C::KT - 1) / C::KT : 1;
-  w.segs = p.a.H * ((w.fresh * p.a.G + C::COLS - 1) / C::COLS);
+  w.groups = (w.fresh * p.a.G + C::COLS - 1) / C::COLS;
 }
 template <class C>
 __device__ __forceinline__ void advance(const SplitParams &p, Walk &w) {
   if (++w.step < w.steps) return;
   w.step = 0;
-  if (++w.seg < w.segs) return;
-  w.seg = 0;
+  if (++w.group < w.groups) return;
+  w.group = 0;
+  if (++w.h < p.a.H) return;
+  w.h = 0;
   do {
     if (++w.r >= p.a.req.R) return;
     enter_request<C>(p, w);
-  } while (w.segs == 0);
+  } while (w.groups == 0);
 }
 // Total steps, and (second form) the walk at step `at`.  A warp scans 32
 // requests at a time.
@@ -180,7 +184,7 @@ __device__ __forceinline__ int64_t steps_of(const SplitParams &p, int r) {
   Walk w;
   w.r = r;
   enter_request<C>(p, w);
-  return (int64_t)w.steps * w.segs;
+  return (int64_t)w.steps * w.groups * p.a.H;
 }
 template <class C>
 __device__ int64_t total_steps(const SplitParams &p) {
@@ -209,8 +213,10 @@ __device__ Walk walk_at(const SplitParams &p, int64_t at) {
       w.r = r0 + who;
       enter_request<C>(p, w);
       const int64_t in = at - before - __shfl_sync(~0u, upto - mine, who);
-      w.seg = (int)(in / w.steps);
+      const int seg = (int)(in / w.steps);
       w.step = (int)(in % w.steps);
+      w.h = seg / w.groups;
+      w.group = seg % w.groups;
       return w;
     }
     before += __shfl_sync(~0u, upto, 31);
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   unsigned char *ring = smem + warp * C::STAGES * C::kStage;
   float *red = reinterpret_cast<float *>(smem + C::kRing);
-  float *red_m = red + C::WARPS * 8 * C::ROWF, *red_l = red_m + C::WARPS * C::COLS;
+  float *red_m = red + C::WARPS * C::RC * C::ROWF, *red_l = red_m + C::WARPS * C::COLS;
   uint2 *qs = reinterpret_cast<uint2 *>(smem + C::kRing + C::kReduce);
   float *col_scale = reinterpret_cast<float *>(smem + C::kRing + C::kReduce + (C::kQInSmem ? C::kQ : 0));
   int *flag = reinterpret_cast<int *>(col_scale + C::COLS);
@@ -269,35 +275,56 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 
   // Copy the warp's next tile into a stage: lane l looks up slot l, then 16-byte
   // pieces go out row by row.
+  unsigned char *scales = nullptr;
+  float kscale_next = 0.f, vscale_next = 0.f;
+  const auto put_scales = [&]() {
+    if (scales && lane < KW) {
+      reinterpret_cast<float *>(scales)[lane] = kscale_next;
+      reinterpret_cast<float *>(scales)[KW + lane] = vscale_next;
+    }
+    scales = nullptr;
+  };
   const auto fetch = [&](int stage) {
+    put_scales();
     unsigned char *st = ring + stage * C::kStage;
     if (ahead < last) {
-      const int h = pw.seg / (pw.segs / a.H);
-      const int64_t j = (int64_t)pw.step * C::KT + warp * KW + lane % KW;
-      int64_t page = -1;
+      const int j = pw.step * C::KT + warp * KW + lane % KW;   // below len + KT <= 2^31
+      int page = -1;
+      uint32_t off = 0;
       if (j < pw.len) {
-        page = page_of(a, pw.r, j / a.bs);
+        const uint32_t block = block_of(a, j);
+        off = j - block * a.bs;
+        page = page_of(a, pw.r, block);
         if (page < 0) raise(a.status, KVX_FLAG_BAD_BLOCK);
       }
-      const int64_t block = page < 0 ? 0 : page * a.H + h;
-      const int64_t row = block * a.bs + (page < 0 ? 0 : j % a.bs);
       const unsigned valid = __ballot_sync(~0u, page >= 0);
-      const uint32_t sc = (uint32_t)__cvta_generic_to_shared(st + 2 * C::kTile);
-      if (lane < KW) {
-        cp_async4(sc + lane * 4, a.ks + block, page >= 0 ? 4 : 0);
-        cp_async4(sc + (KW + lane) * 4, a.vs + block, page >= 0 ? 4 : 0);
-      }
+      const uint32_t block = page < 0 ? 0u : (uint32_t)page * a.H + pw.h;
+      const uint32_t row = page < 0 ? 0u : block * a.bs + off;
+      // scales by plain loads that land a step later (4-byte asynchronous copies
+      // are not merged: a sector and more for each lane)
+      scales = st + 2 * C::kTile;
+      kscale_next = page >= 0 ? __ldg(a.ks + block) : 0.f;
+      vscale_next = page >= 0 ? __ldg(a.vs + block) : 0.f;
       if (lane == 0) *reinterpret_cast<unsigned *>(st + 2 * C::kTile + 2 * KW * 4) = valid;
-      const int real = a.d / 16;
+      const int c = lane % CH;
+      if (valid == ~0u && C::DP == a.d) {
 #pragma unroll
-      for (int i = 0; i < KW * CH / 32; ++i) {
-        const int at = i * 32 + lane, j = at / CH, c = at % CH;
-        const int64_t from = __shfl_sync(~0u, row, j);
-        const bool there = c < real && (valid >> j & 1);
-        const int64_t off = there ? from * a.d + c * 16 : 0;
-        const uint32_t bytes = there ? 16 : 0;
-        cp_async16(st + piece_at<DP>(j, c), a.k + off, bytes);
-        cp_async16(st + C::kTile + piece_at<DP>(j, c), a.v + off, bytes);
+        for (int i = 0; i < KW * CH / 32; ++i) {
+          const int j = i * (32 / CH) + lane / CH;
+          const uint64_t at = (uint64_t)__shfl_sync(~0u, row, j) * C::DP + c * 16;
+          cp_async16(st + piece_at<DP>(j, c), a.k + at, 16);
+          cp_async16(st + C::kTile + piece_at<DP>(j, c), a.v + at, 16);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < KW * CH / 32; ++i) {
+          const int j = i * (32 / CH) + lane / CH;
+          const uint32_t from = __shfl_sync(~0u, row, j);
+          const bool there = c * 16 < a.d && (valid >> j & 1);
+          const uint64_t at = there ? (uint64_t)from * a.d + c * 16 : 0;
+          cp_async16(st + piece_at<DP>(j, c), a.k + at, there ? 16 : 0);
+          cp_async16(st + C::kTile + piece_at<DP>(j, c), a.v + at, there ? 16 : 0);
+        }
       }
       advance<C>(p, pw);
       ++ahead;
@@ -310,22 +337,27 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
   uint32_t qf[C::kQInSmem ? 1 : NT][PARTS][QD * 4][2];
   float cs[NT][2];           // factors of columns 2t, 2t + 1
   int limit[NT][2];          // last slot that they see
-  float m[NT][2], l[NT][2], o[NT][CH][4], vref = 0.f;
+  // running maxima: as scores without their column's factor, and with it
+  float mx[NT][2], m[NT][2], l[NT][2], o[NT][CH][4];
+  float vref = 0.f, vinv = 0.f;   // largest value scale, and 2^14 over it
+  int limits = 0;                 // the lowest of the limits
   int stage = 0;
   bool enter = true;
   int64_t seg_first = first;   // the CTA's first step of the segment
   for (int64_t now = first; now < last; ++now) {
-    const int groups = w.segs / a.H, h = w.seg / groups, col0 = w.seg % groups * C::COLS;
-    const int cols = w.fresh * a.G;
+    const int h = w.h, col0 = w.group * C::COLS, cols = w.fresh * a.G;
     if (enter) {
       enter = false;
       seg_first = now;
-      vref = 0.f;
+      // below 2^-112 a scale is treated as that: 2^14 over it stays finite
+      vref = 0x1p-112f;
+      vinv = 0x1p126f;
+      limits = w.len - w.fresh + col0 / a.G;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          m[n][e] = -INFINITY;
+          mx[n][e] = m[n][e] = -INFINITY;
           l[n][e] = 0.f;
           const int col = col0 + 8 * n + 2 * t + e;
           limit[n][e] = col < cols ? w.len - w.fresh + col / a.G : -1;
@@ -380,8 +412,9 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
         int e2 = (int)(__float_as_uint(top) >> 23) - 127;
         e2 = e2 < -100 ? -100 : e2;
-        const float up = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
-        const float factor = a.c * __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
+        // the factor stays positive, so that maxima may be taken without it
+        const float up = copysignf(__uint_as_float((uint32_t)(14 - e2 + 127) << 23), a.c);
+        const float factor = fabsf(a.c) * __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
 #pragma unroll
         for (int q = 0; q < QD; ++q)
 #pragma unroll
@@ -420,6 +453,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
     }
 
     cp_async_wait<C::STAGES - 2>();
+    put_scales();
     __syncwarp();
     fetch(stage == 0 ? C::STAGES - 1 : stage - 1);   // the tile of the step before is spent
     {
@@ -427,7 +461,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
       const uint32_t vaddr = (uint32_t)__cvta_generic_to_shared(st + C::kTile);
       const float *ks = reinterpret_cast<const float *>(st + 2 * C::kTile), *vs = ks + KW;
       const unsigned valid = *reinterpret_cast<const unsigned *>(st + 2 * C::kTile + 2 * KW * 4);
-      const int64_t j0 = (int64_t)w.step * C::KT + warp * KW;
+      const int j0 = w.step * C::KT + warp * KW;
       if (valid || (p.scores && j0 < w.len)) {
         // S^T = K Q^T
         float s[MT][NT][4];
@@ -473,67 +507,71 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
             }
           }
         }
-        // scale, mask, the tile's maxima
-        float vmax = 0.f, vsc[MT][2];
-        float top[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
+        // key scales; the mask, where the tile needs one
+        float vsc[MT][2], most = 0.f;
+        bool grew = false;
+        const bool masked = valid != (KW == 32 ? ~0u : (1u << KW % 32) - 1) || j0 + KW - 1 > limits || cols - col0 < C::COLS;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int j = 16 * i + 8 * half + g;
             const float kscale = ks[j];
-            const bool here = valid >> j & 1;
             vsc[i][half] = vs[j];
-            vmax = fmaxf(vmax, vsc[i][half]);
+            most = fmaxf(most, vsc[i][half]);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 float &x = s[i][n][2 * half + e];
-                x = here && j0 + j <= limit[n][e] ? x * (kscale * cs[n][e]) : -INFINITY;
-                top[n][e] = fmaxf(top[n][e], x);
+                x *= kscale;
+                if (masked && !((valid >> j & 1) && j0 + j <= limit[n][e])) x = -INFINITY;
+                grew = grew || x > mx[n][e];
               }
           }
         if (p.scores) {
-          const int64_t seg = ((int64_t)w.r * a.H + h) * p.groups + w.seg % groups;
+          const int64_t seg = ((int64_t)w.r * a.H + h) * p.groups + w.group;
           float *to = p.scores + seg * a.max_len * C::COLS;
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const int64_t j = j0 + 16 * i + 8 * half + g;
+              const int j = j0 + 16 * i + 8 * half + g;
               if (j >= w.len) continue;
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<float2 *>(to + j * C::COLS + 8 * n + 2 * t) =
-                    make_float2(s[i][n][2 * half], s[i][n][2 * half + 1]);
+                *reinterpret_cast<float2 *>(to + (int64_t)j * C::COLS + 8 * n + 2 * t) =
+                    make_float2(s[i][n][2 * half] * cs[n][0], s[i][n][2 * half + 1] * cs[n][1]);
             }
         }
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          vmax = fmaxf(vmax, __shfl_xor_sync(~0u, vmax, off));
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(~0u, top[n][e], off));
-        }
-        bool grew = vmax > vref;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) grew = grew || top[n][e] > m[n][e];
-        if (__any_sync(~0u, grew)) {   // seldom after the first tiles
-          const float vnew = fmaxf(vref, vmax), vdown = vnew > 0.f ? vref / vnew : 0.f;
-          vref = vnew;
+        if (__any_sync(~0u, grew || most > vref)) {   // seldom after the first tiles
+          float top[NT][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float mm = fmaxf(m[n][e], top[n][e]);
-              const float down = ex2(m[n][e] - finite_or_0(mm));
-              m[n][e] = mm;
+              top[n][e] = mx[n][e];
+#pragma unroll
+              for (int i = 0; i < MT; ++i) top[n][e] = fmaxf(top[n][e], fmaxf(s[i][n][e], s[i][n][2 + e]));
+            }
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            most = fmaxf(most, __shfl_xor_sync(~0u, most, off));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(~0u, top[n][e], off));
+          }
+          const float vnew = fmaxf(vref, most), vdown = vref / vnew;
+          vref = vnew;
+          vinv = 16384.f / vnew;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              mx[n][e] = top[n][e];
+              const float mm = finite_or_0(top[n][e] * cs[n][e]), down = ex2(m[n][e] - mm);
+              m[n][e] = top[n][e] > -INFINITY ? mm : -INFINITY;
               l[n][e] *= down;
 #pragma unroll
               for (int c = 0; c < CH; ++c) {
@@ -548,11 +586,11 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const float f = vref > 0.f ? vsc[i][half] / vref * 16384.f : 0.f;
+            const float f = vsc[i][half] * vinv;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const float p0 = ex2(s[i][n][2 * half] - finite_or_0(m[n][0]));
-              const float p1 = ex2(s[i][n][2 * half + 1] - finite_or_0(m[n][1]));
+              const float p0 = ex2(fmaf(s[i][n][2 * half], cs[n][0], -finite_or_0(m[n][0])));
+              const float p1 = ex2(fmaf(s[i][n][2 * half + 1], cs[n][1], -finite_or_0(m[n][1])));
               l[n][0] += p0;
               l[n][1] += p1;
               float y0 = p0 * f, y1 = p1 * f;
@@ -591,29 +629,37 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 
     const bool seg_done = w.step + 1 == w.steps;
     if (seg_done || now + 1 == last) {
-      // join the warps, eight columns at a time
+      // join the warps, RC columns at a time
       const bool whole = seg_done && w.step + 1 <= now - seg_first + 1;
       // where it goes: the result, or a partial one (first or last of the CTA)
       float *slot = p.partial + ((int64_t)blockIdx.x * 2 + (seg_first == first ? 0 : 1)) * C::kSlot;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(~0u, l[n][e], off);
-          float *row = red + (warp * 8 + 2 * t + e) * C::ROWF;
-#pragma unroll
-          for (int c = 0; c < CH; ++c)
-            *reinterpret_cast<float2 *>(row + 16 * c + 2 * g) =
-                make_float2(o[n][c][e] * (1.f / 16384.f) * vref, o[n][c][2 + e] * (1.f / 16384.f) * vref);
           if (g == 0) {
             red_m[warp * C::COLS + 8 * n + 2 * t + e] = m[n][e];
             red_l[warp * C::COLS + 8 * n + 2 * t + e] = l[n][e];
           }
         }
+#pragma unroll
+      for (int round = 0; round < C::COLS / C::RC; ++round) {
+        const int n = round * C::RC / 8;
+        if (t / (C::RC / 2) == round % (8 / C::RC)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float *row = red + (warp * C::RC + 2 * (t % (C::RC / 2)) + e) * C::ROWF;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+              *reinterpret_cast<float2 *>(row + 16 * c + 2 * g) = make_float2(
+                  o[n][c][e] * (1.f / 16384.f) * vref, o[n][c][2 + e] * (1.f / 16384.f) * vref);
+          }
+        }
         __syncthreads();
-        for (int x = threadIdx.x; x < 8 * (DP / 2); x += 32 * C::WARPS) {
-          const int in = x / (DP / 2), col = 8 * n + in, d = x % (DP / 2) * 2, at = col0 + col;
+        for (int x = threadIdx.x; x < C::RC * (DP / 2); x += 32 * C::WARPS) {
+          const int in = x / (DP / 2), col = C::RC * round + in, d = x % (DP / 2) * 2, at = col0 + col;
           float mm = -INFINITY, ll = 0.f;
           float2 oo = make_float2(0.f, 0.f);
 #pragma unroll
@@ -621,7 +667,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 #pragma unroll
           for (int v = 0; v < C::WARPS; ++v) {
             const float f = ex2(red_m[v * C::COLS + col] - finite_or_0(mm));
-            const float2 y = *reinterpret_cast<const float2 *>(red + (v * 8 + in) * C::ROWF + d);
+            const float2 y = *reinterpret_cast<const float2 *>(red + (v * C::RC + in) * C::ROWF + d);
             ll += f * red_l[v * C::COLS + col];
             oo.x += f * y.x;
             oo.y += f * y.y;
@@ -642,7 +688,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
         // the last CTA of the segment to get here joins all of its parts
         const int64_t begin = now - w.step, end = begin + w.steps;   // the segment's steps
         const int64_t c0 = ((begin + 1) * N - 1) / T, c1 = (end * N - 1) / T;
-        int *arrived = p.arrived + ((int64_t)w.r * a.H + h) * p.groups + w.seg % groups;
+        int *arrived = p.arrived + ((int64_t)w.r * a.H + h) * p.groups + w.group;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) *flag = atomicAdd(arrived, 1) == (int)(c1 - c0);
@@ -653,19 +699,24 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
           for (int x = threadIdx.x; x < C::COLS * (DP / 2); x += 32 * C::WARPS) {
             const int col = x / (DP / 2), d = x % (DP / 2) * 2, at = col0 + col;
             if (at >= cols || d >= a.d) continue;
+            // CTA c's part is its first segment unless the segment begins inside it
+            const float *p0 = p.partial + (c0 * 2 + (c0 * T / N != begin)) * C::kSlot;
+            const float *p1 = p.partial + c0 * 2 * C::kSlot;
+            const int parts = (int)(c1 - c0) + 1;
             float mm = -INFINITY, ll = 0.f;
             float2 oo = make_float2(0.f, 0.f);
-            for (int64_t c = c0; c <= c1; ++c) {
-              // CTA c's part is its first segment unless the segment begins inside it
-              const bool second = c == c0 && c * T / N != begin;
-              const float *part = p.partial + (c * 2 + second) * C::kSlot;
-              const float pm = __ldcg(part + C::COLS * DP + col), pl = __ldcg(part + C::COLS * (DP + 1) + col);
+#pragma unroll 8
+            for (int c = 0; c < parts; ++c)
+              mm = fmaxf(mm, __ldcg((c ? p1 + (int64_t)c * 2 * C::kSlot : p0) + C::COLS * DP + col));
+            mm = finite_or_0(mm);
+#pragma unroll 8
+            for (int c = 0; c < parts; ++c) {
+              const float *part = c ? p1 + (int64_t)c * 2 * C::kSlot : p0;
+              const float f = ex2(__ldcg(part + C::COLS * DP + col) - mm);
               const float2 y = __ldcg(reinterpret_cast<const float2 *>(part + col * DP + d));
-              const float top = fmaxf(mm, pm), f0 = ex2(mm - finite_or_0(top)), f1 = ex2(pm - finite_or_0(top));
-              ll = ll * f0 + pl * f1;
-              oo.x = oo.x * f0 + y.x * f1;
-              oo.y = oo.y * f0 + y.y * f1;
-              mm = top;
+              ll += __ldcg(part + C::COLS * (DP + 1) + col) * f;
+              oo.x += y.x * f;
+              oo.y += y.y * f;
             }
             store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, ll);
           }
@@ -713,11 +764,11 @@ __global__ void __launch_bounds__(128) weights_kernel(const __grid_constant__ At
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(p, r);
   const int64_t j = (int64_t)blockIdx.x * 128 + threadIdx.x;
   if (j >= len) return;
-  const int64_t page = page_of(p, r, j / p.bs);
+  const int page = page_of(p, r, block_of(p, (int)j));
   if (page < 0) return;
   const int64_t beg = p.req.begin(r), n = p.req.begin(r + 1) - beg;
-  const uint8_t *row = p.k + ((page * p.H + h) * p.bs + j % p.bs) * p.d;
-  const float ks = p.ks[page * p.H + h] * p.c;
+  const uint8_t *row = p.k + (((int64_t)page * p.H + h) * p.bs + j % p.bs) * p.d;
+  const float ks = p.ks[(int64_t)page * p.H + h] * p.c;
   float sum = 0.f;
   for (int64_t i = j - (len - n) > 0 ? j - (len - n) : 0; i < n; ++i)
     for (int u = 0; u < p.G; ++u) {
@@ -773,8 +824,12 @@ Shape shape_of(const kvx_attend8_args *a) {
 
 template <int DP, int NT, int PARTS>
 kvx_status launch_split(const SplitParams &p, int grid, cudaStream_t s) {
-  // 16 slots a warp and 8 warps; stages for about 128 KB in flight
-  using C = SplitCfg<DP, NT, PARTS, 1, 8, DP == 64 ? 8 : DP == 128 ? 5 : 2>;
+#ifndef MTX
+#define MTX (DP <= 128 && NT * PARTS <= 2 ? 2 : 1)
+#define STX (DP == 64 ? 8 / MTX : DP == 128 ? (MTX == 2 ? 3 : 5) : 2)
+#define WX 8
+#endif
+  using C = SplitCfg<DP, NT, PARTS, MTX, WX, STX>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(split_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
@@ -829,7 +884,13 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.weights = a->weights;
   p.status = a->status;
   p.req = {a->cu_seqlens, a->num_requests, a->ntok};
-  p.num_blocks = c.num_blocks;
+  p.num_blocks = (int)c.num_blocks;
+  // with k = ceil(log2 bs), 2^(31 + k) / bs rounded up is off by less than 2^k / bs
+  // a unit, so the quotient is exact below 2^31
+  int k = 0;
+  while (1 << k < c.block_size) ++k;
+  p.bs_shift = 31 + k;
+  p.bs_mul = (uint32_t)(((uint64_t)1 << (31 + k)) / c.block_size + 1);
   p.wstride = a->weights_stride;
   p.H = c.heads;
   p.Hq = a->q_heads;

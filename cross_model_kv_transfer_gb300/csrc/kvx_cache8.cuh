@@ -79,6 +79,8 @@ inline kvx_status check_cache8(const kvx_cache8 &c) {
       c.head_dim < 16 || c.head_dim > 256 || c.head_dim % 16 || c.block_size < 1 ||
       c.block_size > 1024 || c.max_blocks_per_req < 1)
     return KVX_ERR_INVALID_ARG;
+  // rows are counted in 32 bits
+  if ((uint64_t)c.num_blocks * c.heads > UINT32_MAX / (uint64_t)c.block_size) return KVX_ERR_UNSUPPORTED;
   if (!aligned_to(c.k_codes, 16) || !aligned_to(c.v_codes, 16) || !aligned_to(c.k_scale, 4) ||
       !aligned_to(c.v_scale, 4) || !aligned_to(c.block_table, 4))
     return KVX_ERR_INVALID_ARG;

@@ -636,7 +636,7 @@ typedef struct {
   void *k_codes, *v_codes;  /* [num_blocks][heads][block_size][head_dim], 16-byte
                                aligned                                        */
   float *k_scale, *v_scale; /* [num_blocks][heads]                            */
-  int64_t num_blocks;       /* >= 1                                           */
+  int64_t num_blocks;       /* >= 1; num_blocks * heads * block_size below 2^32 */
   int32_t heads;            /* KV heads, 1..65535                             */
   int32_t head_dim;         /* a multiple of 16, 16..256                      */
   int32_t block_size;       /* tokens a block, 1..1024                        */
