@@ -12,83 +12,12 @@
 #include <cmath>
 
 #include "kvx_async.cuh"
-#include "kvx_cache8.cuh"
+#include "kvx_attend8.cuh"
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-struct AttendParams {
-  const uint8_t *k, *v;
-  const float *ks, *vs;
-  const void *q;
-  void *out;
-  int64_t qt, qh, ot, oh;
-  const int32_t *table, *lens;
-  float *lse, *weights;
-  uint32_t *status;
-  Requests req;
-  int64_t wstride;
-  int num_blocks, H, Hq, G, d, bs, max_blocks, max_len, max_new, bf16;
-  uint32_t bs_mul, bs_shift;   // j / bs = j * bs_mul >> bs_shift for j < 2^31
-  float c;   // scale * log2(e): scores are kept in base 2
-};
-
-// The request's length (0 where it is out of bounds).
-__device__ __forceinline__ int len_of(const AttendParams &p, int r) {
-  const int n = __ldg(p.lens + r);
-  return n < 0 || n > p.max_len ? 0 : n;
-}
-// The request's block that holds slot j: j / bs by a multiplication.
-__device__ __forceinline__ uint32_t block_of(const AttendParams &p, int j) {
-  return (uint32_t)((uint64_t)(uint32_t)j * p.bs_mul >> p.bs_shift);
-}
-// The pool's block of a request's block, or -1.
-__device__ __forceinline__ int page_of(const AttendParams &p, int r, uint32_t block) {
-  const int page = block < (uint32_t)p.max_blocks ? __ldg(p.table + (int64_t)r * p.max_blocks + block) : -1;
-  return page < p.num_blocks ? page : -1;
-}
-__device__ __forceinline__ float q_at(const AttendParams &p, int64_t g, int h, int i) {
-  const int64_t at = g * p.qt + h * p.qh + i;
-  return p.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.q)[at])
-                : reinterpret_cast<const float *>(p.q)[at];
-}
-__device__ __forceinline__ bool requests_ok(const AttendParams &p) {
-  bool good = p.req.ok();
-  if (p.req.cu) {
-    bool few = true;
-    for (int r = threadIdx.x; good && r < p.req.R; r += blockDim.x)
-      few = few && p.req.cu[r + 1] - p.req.cu[r] <= p.max_new;
-    good = __syncthreads_and(good && few);
-  }
-  return good;
-}
-// Two dimensions of a finished row; its log-sum-exp with the first.
-__device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int hq, int d, float2 o, float m,
-                                          float l) {
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  const int64_t to = g * p.ot + hq * p.oh + d;
-  if (p.bf16) {
-    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + to;
-    out[0] = __float2bfloat16_rn(o.x * inv);
-    out[1] = __float2bfloat16_rn(o.y * inv);
-  } else {
-    float *out = reinterpret_cast<float *>(p.out) + to;
-    out[0] = o.x * inv;
-    out[1] = o.y * inv;
-  }
-  if (d == 0) p.lse[g * p.Hq + hq] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
-
 // --- few queries: the slots split over the whole GPU -----------------------------
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// A maximum to subtract: 0 before any score (exp2(-inf - 0) is 0; a NaN score stays NaN).
-__device__ __forceinline__ float finite_or_0(float m) { return m > -INFINITY ? m : 0.f; }
 // D += A B of f16 operands, fp32 accumulation: 16 x 8, 16 deep.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -413,8 +342,8 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
         int e2 = (int)(__float_as_uint(top) >> 23) - 127;
         e2 = e2 < -100 ? -100 : e2;
         // the factor stays positive, so that maxima may be taken without it
-        const float up = copysignf(__uint_as_float((uint32_t)(14 - e2 + 127) << 23), a.c);
-        const float factor = fabsf(a.c) * __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
+        const float up = a.c != 0.f ? copysignf(__uint_as_float((uint32_t)(14 - e2 + 127) << 23), a.c) : 0.f;
+        const float factor = fmaxf(fabsf(a.c) * __uint_as_float((uint32_t)(e2 - 14 + 127) << 23), 0x1p-126f);
 #pragma unroll
         for (int q = 0; q < QD; ++q)
 #pragma unroll
@@ -789,7 +718,7 @@ kvx_status check(const kvx_attend8_args *a) {
   if (const kvx_status st = check_cache8(c)) return st;
   if ((a->dtype != KVX_F32 && a->dtype != KVX_BF16) || a->num_requests < 1 || a->ntok < 0 ||
       a->ntok > INT32_MAX || (!a->cu_seqlens && a->ntok != a->num_requests) || a->max_new < 1 ||
-      a->max_len < 0 || !a->lens || !std::isfinite(a->scale) || a->q_heads < 1 ||
+      a->max_len < 0 || a->max_len > INT32_MAX - 1024 || !a->lens || !std::isfinite(a->scale) || a->q_heads < 1 ||
       a->q_heads > 65535 || a->q_heads % c.heads)
     return KVX_ERR_INVALID_ARG;
   if (a->weights && a->weights_stride < a->max_len) return KVX_ERR_INVALID_ARG;
@@ -854,7 +783,8 @@ kvx_status launch_dim(const SplitParams &p, int cols, int grid, cudaStream_t s) 
 }  // namespace
 
 extern "C" size_t kvx_attend8_workspace_bytes(const kvx_attend8_args *a) {
-  return check(a) == KVX_OK ? shape_of(a).bytes : 0;
+  if (check(a) != KVX_OK) return 0;
+  return kvx_attend8_tc_supports(a) ? kvx_attend8_tc_workspace_bytes(a) : shape_of(a).bytes;
 }
 
 extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
@@ -878,9 +808,7 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.oh = a->out_head_stride;
   p.table = c.block_table;
   p.lens = a->lens;
-  const Shape sh = shape_of(a);
-  char *ws = (char *)a->workspace;
-  p.lse = a->lse ? a->lse : (float *)(ws + sh.lse);
+  p.lse = a->lse;
   p.weights = a->weights;
   p.status = a->status;
   p.req = {a->cu_seqlens, a->num_requests, a->ntok};
@@ -903,6 +831,17 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.bf16 = size == 2;
   p.c = a->scale * kLog2e;
   cudaStream_t s = (cudaStream_t)stream;
+  char *ws = (char *)a->workspace;
+  if (kvx_attend8_tc_supports(a)) {
+    const kvx_status st = kvx_attend8_tc_launch(a, p, ws, s);
+    const bool wide = (int64_t)p.G * p.max_new > 128;
+    if (st != KVX_OK || !a->weights || a->max_len == 0 || !wide) return st;
+    if (!p.lse) return KVX_ERR_INVALID_ARG;
+    weights_kernel<<<dim3((a->max_len + 127) / 128, c.heads, a->num_requests), 128, 0, s>>>(p);
+    return launched();
+  }
+  const Shape sh = shape_of(a);
+  if (!p.lse) p.lse = (float *)(ws + sh.lse);
   SplitParams sp;
   sp.a = p;
   sp.groups = sh.groups;

@@ -1,0 +1,1018 @@
+// kvx_attend8_tc.cu -- attention over the 8-bit cache on tcgen05 tensor cores:
+// bf16 queries, head_dim 128, blocks of whole 8-slot groups.
+//
+// Rows are the (query, head of the group) pairs of one request and KV head, 128
+// to a tile; slots come 128 to a tile by TMA from the paged codes.
+//   S = Q K^T   kind::f8f6f4: the codes as they lie in the cache; a query row,
+//               scaled by a power of two to a largest element in (224, 448], is
+//               the sum of two e4m3 parts (4 + 4 bits: a bf16 element exactly,
+//               down to 1/1792 of the row's largest, below that to 2^-19 of it),
+//   O += P V    kind::f16: P in f16 from tensor memory (it overwrites S), V
+//               converted to f16 in shared memory with its block's scale.
+// Softmax statistics are fp32, a row to a thread: no exchange between threads.
+// The maximum that is subtracted follows the running one lazily: P holds up to
+// 2^8 times what it would with the true one before the sums are scaled down.
+//
+// Roles: warps 0-3 and 4-7 two softmax groups, warps 8-11 convert V, warp 12
+// loads (block lookups, scales, TMA), warp 13 issues the MMAs.  WIDE: the groups
+// take the two 128-row halves of 256 rows, over the same slot tiles.  Narrow
+// (at most 128 rows): they take the even and the odd slot tiles of the same
+// rows, so that one tile's softmax overlaps the other's products.
+//
+// Work: every CTA takes an equal share of all steps (walk below); parts of an item that
+// more than one CTA worked on are joined by the last of them.
+//
+// Every wait is bounded: after 2 s without progress the CTA sets
+// KVX_FLAG_TIMEOUT, all roles leave, copies and MMAs in flight are drained and
+// tensor memory is freed.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvx_attend8.cuh"
+#include "kvx_ptx.cuh"
+
+namespace {
+
+constexpr int kD = 128;             // head_dim
+constexpr int kTile = 128;          // slots and rows of a tile
+constexpr int kTileBytes = kTile * kD;
+constexpr int kKStages = 3, kVStages = 2, kWStages = 2, kRefs = 4;
+constexpr int kLoadWarp = 12, kMmaWarp = 13, kThreads = 14 * 32;
+constexpr uint64_t kWaitNs = 2000000000ull;
+// P carries 2^7 so that f16 keeps probabilities down to 2^-31 of the
+// subtracted maximum's; with the lazy 2^8 that is at most 2^15
+constexpr float kBias = 7.f, kSlack = 8.f;
+
+struct TcShared {
+  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t w_full[kWStages], w_empty[kWStages];
+  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t ref_full[kRefs];
+  uint64_t join, verdict, drain;
+  uint32_t tmem_base;
+  volatile int abort;
+  volatile int last;
+  float ref[kRefs];
+  uint32_t k_mask[kKStages], v_mask[kVStages];   // bit l: slots 4l .. 4l + 3 lie in a block of the pool
+  __align__(16) float ks[kKStages][kTile];   // read and written four at a time
+  __align__(16) float vs[kVStages][kTile];
+};
+constexpr size_t kSmemQ = 4 * (size_t)kTileBytes;     // two tiles of two parts
+constexpr size_t kSmemBytes = 1024 + kSmemQ + (kKStages + kVStages) * (size_t)kTileBytes +
+                              kWStages * 2 * (size_t)kTileBytes + sizeof(TcShared);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+struct TcParams {
+  AttendParams a;
+  int groups;          // row groups of max_new queries
+  int *arrived;        // [R][H][groups]
+  float *partial;      // [2 * grid][WIDE ? 1 : 2][part_size]: sums [rows][kD], maxima, totals
+  float *scores;       // narrow: [R][H][rows][score_ld], base 2, or NULL
+  int score_ld, slot_rows, part_size;   // rows kept of a part (narrow: G * max_new), its floats
+  int box;             // slots of one TMA box
+  int vec_q, vec_out;
+};
+
+struct Waiter {
+  TcShared *sh;
+  uint32_t *status;
+  __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
+    const uint32_t a = smem_addr(bar);
+    if (mbar_try_wait(a, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    while (true) {
+      if (mbar_try_wait(a, parity)) return true;
+      if (sh->abort) return false;
+      if (globaltimer() - t0 > kWaitNs) {
+        sh->abort = 1;
+        raise(status, KVX_FLAG_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) const {
+    return __all_sync(~0u, wait(bar, parity)) != 0;
+  }
+};
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(smem_addr(bar), parity) && globaltimer() - t0 < kWaitNs) {
+  }
+}
+
+// --- the flattened work ---------------------------------------------------------
+// For each request, KV head and group of rows: steps of one (WIDE) or two slot
+// tiles up to the last slot that its rows see.
+struct TcWalk {
+  int r, len, fresh, groups, h, group, steps, step;
+  int64_t beg;
+};
+template <bool WIDE>
+struct Geo {
+  static constexpr int ROWS = WIDE ? 2 * kTile : kTile;
+  static constexpr int SLOTS = WIDE ? kTile : 2 * kTile;   // of a step
+  static constexpr int PARTS = WIDE ? 1 : 2;               // results that a CTA keeps for an item
+};
+template <bool WIDE>
+__device__ __forceinline__ int steps_of(const AttendParams &a, int len, int fresh, int group) {
+  const int64_t end = ((int64_t)(group + 1) * Geo<WIDE>::ROWS + a.G - 1) / a.G;   // its tokens end here
+  const int64_t seen = len - fresh + (end < fresh ? end : fresh);
+  return seen <= 0 ? 1 : (int)((seen + Geo<WIDE>::SLOTS - 1) / Geo<WIDE>::SLOTS);
+}
+template <bool WIDE>
+__device__ __forceinline__ int groups_of(const AttendParams &a, int fresh) {
+  return (int)(((int64_t)fresh * a.G + Geo<WIDE>::ROWS - 1) / Geo<WIDE>::ROWS);
+}
+template <bool WIDE>
+__device__ __forceinline__ void enter_request(const AttendParams &a, TcWalk &w) {
+  w.len = len_of(a, w.r);
+  w.beg = a.req.begin(w.r);
+  w.fresh = (int)(a.req.begin(w.r + 1) - w.beg);
+  w.groups = groups_of<WIDE>(a, w.fresh);
+}
+template <bool WIDE>
+__device__ __forceinline__ void advance(const AttendParams &a, TcWalk &w) {
+  if (++w.step < w.steps) return;
+  w.step = 0;
+  if (++w.group >= w.groups) {
+    w.group = 0;
+    if (++w.h >= a.H) {
+      w.h = 0;
+      do {
+        if (++w.r >= a.req.R) return;
+        enter_request<WIDE>(a, w);
+      } while (w.groups == 0);
+    }
+  }
+  w.steps = steps_of<WIDE>(a, w.len, w.fresh, w.group);
+}
+// Steps of one head of a request (every lane gets the sum).
+template <bool WIDE>
+__device__ __forceinline__ int64_t head_steps(const AttendParams &a, int len, int fresh) {
+  const int groups = groups_of<WIDE>(a, fresh);
+  int64_t sum = 0;
+  for (int g = threadIdx.x % 32; g < groups; g += 32) sum += steps_of<WIDE>(a, len, fresh, g);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  return sum;
+}
+// Total steps (at < 0), or the walk at step `at`, by one warp.
+template <bool WIDE>
+__device__ int64_t walk_at(const AttendParams &a, int64_t at, TcWalk &w) {
+  const int lane = threadIdx.x % 32;
+  int64_t before = 0;
+  for (int r0 = 0; r0 < a.req.R; r0 += 32) {
+    int len = 0, fresh = 0;
+    if (r0 + lane < a.req.R) {
+      len = len_of(a, r0 + lane);
+      fresh = (int)(a.req.begin(r0 + lane + 1) - a.req.begin(r0 + lane));
+    }
+    int64_t mine = 0;     // steps of one head of request r0 + lane
+    if (a.G * a.max_new <= Geo<WIDE>::ROWS) {
+      mine = fresh > 0 ? steps_of<WIDE>(a, len, fresh, 0) : 0;
+    } else {
+      for (int i = 0; i < 32 && r0 + i < a.req.R; ++i) {
+        const int64_t s = head_steps<WIDE>(a, __shfl_sync(~0u, len, i), __shfl_sync(~0u, fresh, i));
+        if (lane == i) mine = s;
+      }
+    }
+    int64_t upto = mine * a.H;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned here = __ballot_sync(~0u, at >= 0 && at < before + upto);
+    if (here) {
+      const int who = __ffs(here) - 1;
+      w.r = r0 + who;
+      enter_request<WIDE>(a, w);
+      const int64_t per = __shfl_sync(~0u, mine, who), in = at - before - (__shfl_sync(~0u, upto, who) - per * a.H);
+      w.h = (int)(in / per);
+      int64_t rem = in % per;
+      for (int g0 = 0;; g0 += 32) {
+        const int64_t s = g0 + lane < w.groups ? steps_of<WIDE>(a, w.len, w.fresh, g0 + lane) : 0;
+        int64_t to = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(~0u, to, o);
+          if (lane >= o) to += y;
+        }
+        const unsigned hit = __ballot_sync(~0u, rem < to);
+        if (hit || g0 + 32 >= w.groups) {
+          const int k = hit ? __ffs(hit) - 1 : 0;
+          w.group = g0 + k;
+          w.steps = (int)__shfl_sync(~0u, s, k);
+          w.step = (int)(rem - (__shfl_sync(~0u, to, k) - w.steps));
+          return 0;
+        }
+        rem -= __shfl_sync(~0u, to, 31);
+      }
+    }
+    before += __shfl_sync(~0u, upto, 31);
+  }
+  return before;
+}
+
+// --- tcgen05 ---------------------------------------------------------------------
+// Instruction descriptors: D fp32, M = N = 128; e4m3 x e4m3 both K-major, and f16 x
+// f16 with B as it lies in memory, [K][N] (MN-major).
+constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | (16u << 17) | (8u << 24);
+
+// S = (Q1 + Q2) K^T: two parts of four 32-deep steps.
+__device__ __forceinline__ void mma_qk(uint32_t d, uint64_t q, uint64_t k) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t a = q + (i / 4) * (kTileBytes >> 4) + (i % 4) * 2, b = k + (i % 4) * 2;
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(kIdescQK), "r"(i)
+        : "memory");
+  }
+}
+// O (+)= P V: eight 16-deep steps; P 8 columns on, V 16 slots (2 KB) on.
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, bool add) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(p + 8 * i), "l"(v + (uint64_t)i * (2048 >> 4)), "r"(kIdescPV), "r"((uint32_t)(add || i > 0))
+        : "memory");
+  }
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_addr(bar))
+               : "memory");
+}
+// [K][N] operand of 16-bit values, 128-byte swizzle: 64-column groups 16 KB
+// apart (leading offset), 8-row groups 1 KB apart (stride offset).
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(kTileBytes >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]),
+        "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+        "=r"(v[30]), "=r"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+      "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+      "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The factor on a row's scores: positive, so that a masked score stays -inf, and
+// NaN for a row with an infinity (NaN elements are NaN in the parts).
+__device__ __forceinline__ float row_factor(const AttendParams &a, float top, float unit) {
+  return top < INFINITY ? fmaxf(fabsf(a.c) * unit, 0x1p-126f) : __uint_as_float(0x7fc00000u);
+}
+// A query row as two e4m3 parts in the swizzled K-major tile; returns the factor
+// on its scores (its sign is in the parts).
+__device__ __forceinline__ float put_query(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
+                                           unsigned char *tile, int row) {
+  const auto piece = [&](int c, float (&v)[16]) {
+    if (!live) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
+    } else if (vec) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 t = __ldg(reinterpret_cast<const uint4 *>(src + 16 * c) + i);
+        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+          v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = __bfloat162float(src[16 * c + e]);
+    }
+  };
+  float top = 0.f, v[16];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    piece(c, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(v[e]));
+  }
+  const float unit = pow2_scale(top);   // top <= 448 unit
+  const float up = a.c != 0.f ? copysignf(1.f / unit, a.c) : 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    piece(c, v);
+    uint32_t p1[4], p2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float y0 = v[4 * j] * up, y1 = v[4 * j + 1] * up, y2 = v[4 * j + 2] * up, y3 = v[4 * j + 3] * up;
+      p1[j] = e4m3x2(y0, y1) | e4m3x2(y2, y3) << 16;
+      const float2 f0 = floats_of(p1[j]), f1 = floats_of(p1[j] >> 16);
+      p2[j] = e4m3x2(y0 - f0.x, y1 - f0.y) | e4m3x2(y2 - f1.x, y3 - f1.y) << 16;
+    }
+    unsigned char *to = tile + row * kD + ((c ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4 *>(to) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+    *reinterpret_cast<uint4 *>(to + kTileBytes) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+  }
+  return row_factor(a, top, unit);
+}
+
+// --- the kernel ------------------------------------------------------------------
+template <bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v) {
+  using G_ = Geo<WIDE>;
+  extern __shared__ unsigned char raw[];
+  unsigned char *qbuf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *kbuf = qbuf + kSmemQ, *vbuf = kbuf + kKStages * kTileBytes, *wbuf = vbuf + kVStages * kTileBytes;
+  TcShared *sh = reinterpret_cast<TcShared *>(wbuf + kWStages * 2 * kTileBytes);
+  const AttendParams &a = p.a;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(smem_addr(&sh->k_full[i]), 32);
+      mbar_init(smem_addr(&sh->k_empty[i]), 1 + (WIDE ? 8 : 4));
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(smem_addr(&sh->v_full[i]), 32);
+      mbar_init(smem_addr(&sh->v_empty[i]), 4);
+    }
+    for (int i = 0; i < kWStages; ++i) {
+      mbar_init(smem_addr(&sh->w_full[i]), 4);
+      mbar_init(smem_addr(&sh->w_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh->q_full[i]), 4);
+      mbar_init(smem_addr(&sh->s_full[i]), 1);
+      mbar_init(smem_addr(&sh->p_full[i]), 4);
+      mbar_init(smem_addr(&sh->pv_done[i]), 1);
+    }
+    for (int i = 0; i < kRefs; ++i) mbar_init(smem_addr(&sh->ref_full[i]), 1);
+    mbar_init(smem_addr(&sh->join), 8);
+    mbar_init(smem_addr(&sh->verdict), 1);
+    mbar_init(smem_addr(&sh->drain), 1);
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(&sh->tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  const bool good = requests_ok(a);
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  const Waiter W{sh, a.status};
+
+  TcWalk w = {};
+  int64_t T = 0, N = 0, first = 0, last = 0;
+  if (good) {
+    T = walk_at<WIDE>(a, -1, w);
+    N = T < gridDim.x ? T : gridDim.x;   // CTAs at work
+    if (blockIdx.x < N) {
+      first = blockIdx.x * T / N;
+      last = (blockIdx.x + 1) * T / N;
+      walk_at<WIDE>(a, first, w);
+    }
+    if (blockIdx.x == 0 && warp == kLoadWarp)
+      for (int r = lane; r < a.req.R; r += 32)
+        if (len_of(a, r) != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
+  } else if (blockIdx.x == 0 && tid == 0) {
+    raise(a.status, KVX_FLAG_BAD_SEQLENS);
+  }
+  const int64_t count = last - first;
+
+  if (count == 0) {
+    // nothing for this CTA
+  } else if (warp < 8) {
+    // ----------------------------------------------------------------------
+    // softmax: a row to a thread
+    // ----------------------------------------------------------------------
+    const int i = warp / 4;                       // group
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t s_col = tmem + lanes + i * kTile, o_col = tmem + lanes + 2 * kTile + i * kTile;
+    const int row = (WIDE ? i * kTile : 0) + warp % 4 * 32 + lane;   // in the item
+    float m = -INFINITY, l = 0.f, cs = 0.f;
+    int limit = -1, floor_limit = -1, rows = 0;
+    bool live = false, warp_live = false, fresh_o = true;
+    uint32_t tile = 0, item = 0, joins = 0;       // tiles of this group, items, joins so far
+    int64_t seg_first = first;
+    bool enter = true;
+    for (int64_t now = first; now < last; ++now) {
+      if (enter) {
+        enter = false;
+        seg_first = now;
+        rows = (int)min((int64_t)G_::ROWS, (int64_t)w.fresh * a.G - (int64_t)w.group * G_::ROWS);
+        live = row < rows;
+        warp_live = row - lane < rows;
+        const int64_t at = (int64_t)w.group * G_::ROWS + row;         // row of the request and head
+        const int64_t tok = at / a.G;
+        limit = live ? (int)(w.len - w.fresh + tok) : -1;
+        // the lowest limit of the warp's rows (dead ones do not matter)
+        floor_limit = (int)(w.len - w.fresh + (at - lane) / a.G);
+        m = -INFINITY;
+        l = 0.f;
+        fresh_o = true;
+        if (WIDE || i == 0) {
+          const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
+                                     (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
+          cs = put_query(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), row % kTile);
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[i]));
+        } else {
+          // the other group writes the rows; their factors are formed again
+          const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
+                                     (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
+          float top = 0.f;
+          if (live)
+            for (int e = 0; e < kD; ++e) top = fmaxf(top, fabsf(__bfloat162float(src[e])));
+          cs = row_factor(a, top, pow2_scale(top));
+        }
+      }
+      // this group's tile of the step
+      const uint32_t n = WIDE ? (uint32_t)(now - first) : (uint32_t)(2 * (now - first) + i);   // of the CTA
+      const int ks = n % kKStages;
+      const int j0 = w.step * G_::SLOTS + (WIDE ? 0 : i * kTile);
+      if (!W.warp_wait(&sh->k_full[ks], n / kKStages & 1)) goto done;
+      if (!W.warp_wait(&sh->s_full[i], tile & 1)) goto done;
+      tc_fence_after();
+      if (warp_live) {
+        const uint32_t mask = sh->k_mask[ks];
+        const bool masked = mask != ~0u || j0 + kTile - 1 > floor_limit;
+        const float4 *scale = reinterpret_cast<const float4 *>(sh->ks[ks]);
+        const uint64_t cs2 = pair(cs, cs);
+        uint32_t out[64];
+        float top, sum;
+        // probabilities with the maximum `ref` subtracted; the tile's maximum and sum
+        const auto pass = [&](float ref, float *spool) {
+          const uint64_t nm2 = pair(kBias - ref, kBias - ref);
+          uint64_t sum2 = pair(0.f, 0.f);
+          top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32];
+            tc_ld32(s_col + 32 * c, s);
+            tc_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 f = scale[8 * c + q];
+              float x[4];
+              unpair(mul2(pair(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), pair(f.x, f.y)), x[0], x[1]);
+              unpair(mul2(pair(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), pair(f.z, f.w)), x[2],
+                     x[3]);
+              if (masked) {
+                const bool in = mask >> (8 * c + q) & 1;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (!in || j0 + 32 * c + 4 * q + e > limit) x[e] = -INFINITY;
+              }
+              top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+              const uint64_t y0 = fma2(pair(x[0], x[1]), cs2, nm2), y1 = fma2(pair(x[2], x[3]), cs2, nm2);
+              float e0, e1, e2, e3;
+              unpair(y0, e0, e1);
+              unpair(y1, e2, e3);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              e2 = ex2(e2);
+              e3 = ex2(e3);
+              sum2 = add2(sum2, add2(pair(e0, e1), pair(e2, e3)));
+              out[16 * c + 2 * q] = f16x2(e0, e1);
+              out[16 * c + 2 * q + 1] = f16x2(e2, e3);
+              if (spool)
+                *reinterpret_cast<float4 *>(spool + 32 * c + 4 * q) =
+                    make_float4(x[0] * cs, x[1] * cs, x[2] * cs, x[3] * cs);
+            }
+          }
+          float s0, s1;
+          unpair(sum2, s0, s1);
+          sum = s0 + s1;
+        };
+        float *spool = !WIDE && p.scores && live && j0 < p.score_ld
+                           ? p.scores + (((int64_t)w.r * a.H + w.h) * p.slot_rows + row) * p.score_ld + j0
+                           : nullptr;
+        pass(finite_or_0(m), spool);
+        const float peak = top * cs;      // -inf where nothing is seen
+        const bool over = peak > m + kSlack || (m == -INFINITY && peak > -INFINITY);
+        if (__any_sync(~0u, over)) {
+          const float mm = fmaxf(m, peak), down = ex2(m - finite_or_0(mm));
+          if (!fresh_o) {
+            if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) goto done;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tc_ld32(o_col + 32 * c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
+              tc_st32(o_col + 32 * c, o);
+            }
+          }
+          m = mm;
+          l *= down;
+          pass(finite_or_0(m), nullptr);
+        }
+        l += sum;
+        tc_st32(s_col, out);
+        tc_st32(s_col + 32, out + 32);
+        tc_wait_st();
+      }
+      fresh_o = false;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_addr(&sh->p_full[i]));
+        mbar_arrive(smem_addr(&sh->k_empty[ks]));
+      }
+      ++tile;
+
+      const bool seg_done = w.step + 1 == w.steps;
+      if (seg_done || now + 1 == last) {
+        // the result of the item, or this CTA's part of it
+        enter = true;
+        if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) goto done;
+        if (!W.warp_wait(&sh->ref_full[item % kRefs], item / kRefs & 1)) goto done;
+        tc_fence_after();
+        const float back = sh->ref[item % kRefs] * (1.f / 128.f);   // V carries 128 / ref
+        ++item;
+        const bool whole = seg_done && w.step + 1 <= now - seg_first + 1;
+        const int64_t at = (int64_t)w.group * G_::ROWS + row;
+        const int64_t tok = w.beg + at / a.G;
+        const int hq = w.h * a.G + (int)(at % a.G);
+        const int64_t part_size = p.part_size;
+        float *slot = p.partial + (((int64_t)blockIdx.x * 2 + (seg_first == first ? 0 : 1)) * G_::PARTS + (WIDE ? 0 : i)) *
+                                      part_size;
+        const bool direct = WIDE && whole;
+        if (warp_live) {
+          const float inv = direct ? (l != 0.f ? back / l : 0.f) : back;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tc_ld32(o_col + 32 * c, o);
+            tc_wait_ld();
+            if (live && !direct) {
+              float4 *to = reinterpret_cast<float4 *>(slot + row * kD + 32 * c);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                to[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                    __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+            } else if (live) {
+              __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.out) + tok * a.ot + hq * a.oh + 32 * c;
+              uint32_t b[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                b[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+              if (p.vec_out) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  reinterpret_cast<uint4 *>(to)[e] = make_uint4(b[4 * e], b[4 * e + 1], b[4 * e + 2], b[4 * e + 3]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  to[2 * e] = __ushort_as_bfloat16((unsigned short)(b[e] & 0xffff));
+                  to[2 * e + 1] = __ushort_as_bfloat16((unsigned short)(b[e] >> 16));
+                }
+              }
+            }
+            __syncwarp();   // together to the next load
+          }
+          if (live) {
+            const float mt = m - kBias;           // what the sums are relative to
+            if (direct) {
+              a.lse[tok * a.Hq + hq] = l != 0.f ? (mt + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+              slot[p.slot_rows * kD + row] = mt;
+              slot[p.slot_rows * (kD + 1) + row] = l;
+            }
+          }
+        }
+        if (!direct) {
+          // join: the CTA's groups first, then, of several CTAs, the last to come
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh->join));
+          if (!W.warp_wait(&sh->join, joins & 1)) goto done;
+          const int64_t begin = now - w.step, end = begin + w.steps;   // the item's steps
+          const int64_t c0 = ((begin + 1) * N - 1) / T, c1 = (end * N - 1) / T;
+          bool mine = whole;
+          if (!whole) {
+            if (tid == 0) {
+              int *arrived = p.arrived + ((int64_t)w.r * a.H + w.h) * p.groups + w.group;
+              __threadfence();
+              const bool all = atomicAdd(arrived, 1) == (int)(c1 - c0);
+              if (all) *arrived = 0;   // ready for the next call
+              __threadfence();
+              sh->last = all;
+              mbar_arrive(smem_addr(&sh->verdict));
+            }
+          } else if (tid == 0) {
+            sh->last = 1;
+            mbar_arrive(smem_addr(&sh->verdict));
+          }
+          if (!W.warp_wait(&sh->verdict, joins & 1)) goto done;
+          mine = sh->last;
+          ++joins;
+          if (mine) {
+            __threadfence();
+            // CTA c's part is its first item unless the item begins inside it
+            const int64_t s0 = (c0 * 2 + (c0 * T / N != begin)) * G_::PARTS, s1 = c0 * 2 * G_::PARTS;
+            const int parts = (int)(c1 - c0 + 1) * G_::PARTS;
+            const auto part_at = [&](int c) {
+              const int cta = c / G_::PARTS, sub = c % G_::PARTS;
+              return p.partial + ((cta ? s1 + (int64_t)cta * 2 * G_::PARTS : s0) + sub) * part_size;
+            };
+            for (int x = tid; x < rows * (kD / 4); x += 256) {
+              const int rr = x / (kD / 4), d = x % (kD / 4) * 4;
+              float mm = -INFINITY, ll = 0.f;
+              float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+              for (int c = 0; c < parts; ++c) mm = fmaxf(mm, __ldcg(part_at(c) + p.slot_rows * kD + rr));
+              mm = finite_or_0(mm);
+#pragma unroll 8
+              for (int c = 0; c < parts; ++c) {
+                const float *part = part_at(c);
+                const float f = ex2(__ldcg(part + p.slot_rows * kD + rr) - mm);
+                const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + rr * kD + d));
+                ll += __ldcg(part + p.slot_rows * (kD + 1) + rr) * f;
+                oo.x += y.x * f;
+                oo.y += y.y * f;
+                oo.z += y.z * f;
+                oo.w += y.w * f;
+              }
+              const int64_t ar = (int64_t)w.group * G_::ROWS + rr;
+              const int64_t tk = w.beg + ar / a.G;
+              const int hh = w.h * a.G + (int)(ar % a.G);
+              store_out(a, tk, hh, d, make_float2(oo.x, oo.y), mm, ll);
+              store_out(a, tk, hh, d + 2, make_float2(oo.z, oo.w), mm, ll);
+            }
+          }
+        }
+      }
+      advance<WIDE>(a, w);
+    }
+  done:;
+  } else if (warp < kLoadWarp) {
+    // ----------------------------------------------------------------------
+    // V to f16, times 128 scale / (the largest scale of this CTA's part)
+    // ----------------------------------------------------------------------
+    const int t = tid - 8 * 32;
+    uint32_t n = 0, item = 0;
+    bool enter = true;
+    float unit = 0.f;
+    for (int64_t now = first; now < last; ++now) {
+      if (enter) {
+        enter = false;
+        const int64_t s0 = (int64_t)w.step * G_::SLOTS;
+        const int64_t steps = min((int64_t)(w.steps - w.step), last - now);
+        const int64_t s1 = min((int64_t)w.len, s0 + steps * G_::SLOTS);
+        float top = 0x1p-112f;    // scales below count as that: their values vanish beside any other
+        if (s1 > s0) {
+          const int b1 = (int)block_of(a, (int)(s1 - 1));
+          for (int b = (int)block_of(a, (int)s0) + lane; b <= b1; b += 32) {
+            const int page = page_of(a, w.r, b);
+            if (page >= 0) top = fmaxf(top, __ldg(a.vs + (int64_t)page * a.H + w.h));
+          }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        unit = 128.f / top;
+        if (t == 0) {
+          sh->ref[item % kRefs] = top;
+          mbar_arrive(smem_addr(&sh->ref_full[item % kRefs]));
+        }
+        ++item;
+      }
+      for (int k = 0; k < (WIDE ? 1 : 2); ++k, ++n) {
+        const int vs = n % kVStages, ws = n % kWStages;
+        const int j0 = w.step * G_::SLOTS + k * kTile;
+        if (!W.warp_wait(&sh->v_full[vs], n / kVStages & 1)) goto cv_done;
+        if (!W.warp_wait(&sh->w_empty[ws], (n / kWStages & 1) ^ 1)) goto cv_done;
+        const unsigned char *src = vbuf + vs * kTileBytes;
+        unsigned char *dst = wbuf + ws * 2 * kTileBytes;
+        const uint32_t mask = sh->v_mask[vs];
+        const int c = t % 8;                      // 16 dimensions
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int j = u * 16 + t / 8;
+          const bool in = (mask >> (j / 4) & 1) && j0 + j < w.len;
+          const float f = sh->vs[vs][j] * unit;
+          const uint32_t f2 = f16x2(f, f);
+          const uint4 y = *reinterpret_cast<const uint4 *>(src + j * kD + ((c ^ (j & 7)) << 4));
+          const uint32_t b[4] = {y.x, y.y, y.z, y.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h[2 * e] = in ? mul_f16x2(f16x2_of(b[e]), f2) : 0u;
+            h[2 * e + 1] = in ? mul_f16x2(f16x2_of(b[e] >> 16), f2) : 0u;
+          }
+          unsigned char *to = dst + (c / 4) * kTileBytes + j * kD;
+          const int p0 = (c % 4 * 2) ^ (j & 7), p1 = p0 ^ 1;
+          // the two halves of the dimensions store in opposite order: no bank twice
+          const bool flip = c >= 4;
+          *reinterpret_cast<uint4 *>(to + ((flip ? p1 : p0) << 4)) =
+              flip ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4 *>(to + ((flip ? p0 : p1) << 4)) =
+              flip ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&sh->w_full[ws]));
+          mbar_arrive(smem_addr(&sh->v_empty[vs]));
+        }
+      }
+      if (w.step + 1 == w.steps) enter = true;
+      advance<WIDE>(a, w);
+    }
+  cv_done:;
+  } else if (warp == kLoadWarp) {
+    // ----------------------------------------------------------------------
+    // block lookups, scales and TMA: lane l looks up slots 4l .. 4l + 3
+    // ----------------------------------------------------------------------
+    uint32_t n = 0;
+    for (int64_t now = first; now < last; ++now) {
+      for (int k = 0; k < (WIDE ? 1 : 2); ++k, ++n) {
+        const int ks = n % kKStages, vs = n % kVStages;
+        const int j = w.step * G_::SLOTS + k * kTile + 4 * lane;
+        int page = -1;
+        uint32_t off = 0;
+        if (j < w.len) {
+          const uint32_t block = block_of(a, j);
+          off = j - block * a.bs;
+          page = page_of(a, w.r, block);
+          if (page < 0) raise(a.status, KVX_FLAG_BAD_BLOCK);
+        }
+        const uint32_t sb = page < 0 ? 0u : (uint32_t)page * a.H + w.h;
+        const int row = (int)(sb * a.bs + off);
+        const float kscale = page >= 0 ? __ldg(a.ks + sb) : 0.f, vscale = page >= 0 ? __ldg(a.vs + sb) : 0.f;
+        const unsigned mask = __ballot_sync(~0u, page >= 0);
+        const int per = p.box / 4, boxes = kTile / p.box;     // lanes a box, boxes
+        const int from = __shfl_sync(~0u, row, lane < boxes ? lane * per : 0);
+        const bool there = lane < boxes && (mask >> (lane * per) & 1);
+        const uint32_t bytes = __popc(__ballot_sync(~0u, there)) * (uint32_t)p.box * kD;
+        if (!W.warp_wait(&sh->k_empty[ks], (n / kKStages & 1) ^ 1)) goto ld_done;
+        *reinterpret_cast<float4 *>(&sh->ks[ks][4 * lane]) = make_float4(kscale, kscale, kscale, kscale);
+        if (lane == 0) {
+          sh->k_mask[ks] = mask;
+          mbar_expect_tx(smem_addr(&sh->k_full[ks]), bytes);
+        }
+        __syncwarp();
+        if (there)
+          tma_load_2d(smem_addr(kbuf + ks * kTileBytes + lane * p.box * kD), &map_k, 0, from,
+                      smem_addr(&sh->k_full[ks]));
+        if (lane != 0) mbar_arrive(smem_addr(&sh->k_full[ks]));
+        if (!W.warp_wait(&sh->v_empty[vs], (n / kVStages & 1) ^ 1)) goto ld_done;
+        *reinterpret_cast<float4 *>(&sh->vs[vs][4 * lane]) = make_float4(vscale, vscale, vscale, vscale);
+        if (lane == 0) {
+          sh->v_mask[vs] = mask;
+          mbar_expect_tx(smem_addr(&sh->v_full[vs]), bytes);
+        }
+        __syncwarp();
+        if (there)
+          tma_load_2d(smem_addr(vbuf + vs * kTileBytes + lane * p.box * kD), &map_v, 0, from,
+                      smem_addr(&sh->v_full[vs]));
+        if (lane != 0) mbar_arrive(smem_addr(&sh->v_full[vs]));
+      }
+      advance<WIDE>(a, w);
+    }
+  ld_done:
+    // drain: the tiles that were asked for have landed (n counts whole tiles; after
+    // an abort the last keys may be one ahead of the values)
+    __syncwarp();
+    if (lane == 0) {
+      for (uint32_t x = n > kKStages ? n - kKStages : 0; x < n; ++x) drain_wait(&sh->k_full[x % kKStages], x / kKStages & 1);
+      for (uint32_t x = n > kVStages ? n - kVStages : 0; x < n; ++x) drain_wait(&sh->v_full[x % kVStages], x / kVStages & 1);
+      if (sh->abort) drain_wait(&sh->k_full[n % kKStages], n / kKStages & 1);
+    }
+  } else {
+    // ----------------------------------------------------------------------
+    // the MMAs, from one thread
+    // ----------------------------------------------------------------------
+    if (lane == 0) {
+      const uint64_t q0 = sw128_desc(smem_addr(qbuf)), k0 = sw128_desc(smem_addr(kbuf)), v0 = mn_desc(smem_addr(wbuf));
+      TcWalk ahead = w;                // of the scores; w is the products with V's
+      uint32_t items = 0;              // items whose scores were begun
+      bool enter = true, issued = false, add = false;
+      // scores of step s of this CTA, group i
+      const auto scores = [&](int64_t s, int i) {
+        const uint32_t n = WIDE ? (uint32_t)s : (uint32_t)(2 * s + i);
+        if (i == 0 && enter) ++items;
+        if (WIDE || i == 0) {
+          if (enter && !W.wait(&sh->q_full[i], (items - 1) & 1)) return false;
+        }
+        if (!W.wait(&sh->k_full[n % kKStages], n / kKStages & 1)) return false;
+        tc_fence_after();
+        mma_qk(tmem + i * kTile, q0 + (WIDE ? (uint64_t)i * (2 * kTileBytes >> 4) : 0),
+               k0 + (uint64_t)(n % kKStages) * (kTileBytes >> 4));
+        issued = true;
+        commit(&sh->s_full[i]);
+        if (!WIDE || i == 1) commit(&sh->k_empty[n % kKStages]);
+        if (i == 1) {
+          enter = ahead.step + 1 == ahead.steps;
+          advance<WIDE>(a, ahead);
+        }
+        return true;
+      };
+      bool ok = scores(0, 0) && scores(0, 1);
+      for (int64_t s = 0; ok && s < count; ++s) {
+        for (int i = 0; ok && i < 2; ++i) {
+          const uint32_t n = WIDE ? (uint32_t)s : (uint32_t)(2 * s + i);
+          ok = W.wait(&sh->p_full[i], s & 1) && W.wait(&sh->w_full[n % kWStages], n / kWStages & 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_pv(tmem + 2 * kTile + i * kTile, tmem + i * kTile, v0 + (uint64_t)(n % kWStages) * (2 * kTileBytes >> 4), add);
+          commit(&sh->pv_done[i]);
+          if (!WIDE || i == 1) commit(&sh->w_empty[n % kWStages]);
+          if (s + 1 < count) ok = scores(s + 1, i);
+        }
+        add = w.step + 1 != w.steps;
+        advance<WIDE>(a, w);
+      }
+      if (issued) {
+        commit(&sh->drain);
+        drain_wait(&sh->drain, 0);
+      }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// weights[r][h][j] += sum over the rows of exp2(score - lse): narrow calls leave
+// their scores, [rows][score_ld].
+__global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_constant__ TcParams p) {
+  const AttendParams &a = p.a;
+  extern __shared__ float lse2[];
+  if (!requests_ok(a)) return;
+  const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
+  const int64_t beg = a.req.begin(r);
+  const int rows = (int)(a.req.begin(r + 1) - beg) * a.G;
+  for (int c = threadIdx.x; c < rows; c += 256)
+    lse2[c] = a.lse[(beg + c / a.G) * a.Hq + h * a.G + c % a.G] * kLog2e;
+  __syncthreads();
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  if (j >= len || rows == 0) return;
+  const float *x = p.scores + ((int64_t)r * a.H + h) * p.slot_rows * p.score_ld + j;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int c = 0; c < rows; ++c) {
+    const float z = x[(int64_t)c * p.score_ld];
+    sum += z > -INFINITY ? ex2(z - lse2[c]) : 0.f;
+  }
+  a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
+}
+
+// --- host ------------------------------------------------------------------------
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+struct TcShape {
+  int rows, groups, slot_rows, part_size, grid, score_ld, box;
+  bool wide, spool;
+  size_t arrived, partial, lse, scores, bytes;
+};
+TcShape tc_shape(const kvx_attend8_args *a) {
+  TcShape s;
+  const int64_t G = a->q_heads / a->cache.heads, most = G * a->max_new;
+  s.wide = most > kTile;
+  s.rows = s.wide ? 2 * kTile : kTile;
+  s.groups = (int)((most + s.rows - 1) / s.rows);
+  s.slot_rows = s.wide ? s.rows : (int)most;
+  s.part_size = (s.slot_rows * (kD + 2) + 3) / 4 * 4;
+  s.grid = 152;                        // one CTA an SM
+  s.score_ld = (a->max_len + 255) / 256 * 256;
+  s.box = a->cache.block_size & -a->cache.block_size;
+  if (s.box > kTile) s.box = kTile;
+  s.spool = a->weights && !s.wide;
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t items = (size_t)a->num_requests * a->cache.heads;
+  s.arrived = 0;
+  s.partial = up(items * s.groups * 4);
+  s.lse = s.partial + up((size_t)2 * s.grid * (s.wide ? 1 : 2) * s.part_size * 4);
+  s.scores = s.lse + up((size_t)a->ntok * a->q_heads * 4);
+  s.bytes = s.scores + (s.spool ? up(items * s.slot_rows * s.score_ld * 4) : 0);
+  return s;
+}
+
+bool encode(CUtensorMap *map, const kvx_cache8 &c, const void *base, int box) {
+  static const EncodeFn fn = reinterpret_cast<EncodeFn>(kvx_tc_encoder());
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)c.num_blocks * c.heads * c.block_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)kD};
+  const cuuint32_t boxes[2] = {(cuuint32_t)kD, (cuuint32_t)box}, one[2] = {1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, boxes, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool WIDE>
+kvx_status launch(const TcParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int grid, cudaStream_t s) {
+  if (cudaFuncSetAttribute(attend_tc_kernel<WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+      cudaSuccess)
+    return KVX_ERR_CUDA;
+  attend_tc_kernel<WIDE><<<grid, kThreads, kSmemBytes, s>>>(p, mk, mv);
+  return launched();
+}
+
+}  // namespace
+
+bool kvx_attend8_tc_supports(const kvx_attend8_args *a) {
+  const kvx_cache8 &c = a->cache;
+  return a->dtype == KVX_BF16 && c.head_dim == kD && c.block_size % 8 == 0 &&
+         (uint64_t)c.num_blocks * c.heads * c.block_size <= INT32_MAX;
+}
+
+size_t kvx_attend8_tc_workspace_bytes(const kvx_attend8_args *a) { return tc_shape(a).bytes; }
+
+kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::AttendParams &a, char *ws, cudaStream_t s) {
+  const TcShape sh = tc_shape(args);
+  CUtensorMap mk, mv;
+  if (!encode(&mk, args->cache, a.k, sh.box) || !encode(&mv, args->cache, a.v, sh.box)) return KVX_ERR_CUDA;
+  TcParams p;
+  p.a = a;
+  if (!p.a.lse) p.a.lse = (float *)(ws + sh.lse);
+  p.groups = sh.groups;
+  p.arrived = (int *)(ws + sh.arrived);
+  p.partial = (float *)(ws + sh.partial);
+  p.scores = sh.spool ? (float *)(ws + sh.scores) : nullptr;
+  p.score_ld = sh.score_ld;
+  p.slot_rows = sh.slot_rows;
+  p.part_size = sh.part_size;
+  p.box = sh.box;
+  p.vec_q = aligned_to(a.q, 16) && (a.qt | a.qh) % 8 == 0;
+  p.vec_out = aligned_to(a.out, 16) && (a.ot | a.oh) % 8 == 0;
+  const kvx_status st = sh.wide ? launch<true>(p, mk, mv, sh.grid, s) : launch<false>(p, mk, mv, sh.grid, s);
+  if (st != KVX_OK || !a.weights || a.max_len == 0) return st;
+  if (!sh.spool) return KVX_OK;
+  weights_of_rows_kernel<<<dim3((a.max_len + 255) / 256, a.H, a.req.R), 256, sh.slot_rows * 4, s>>>(p);
+  return launched();
+}

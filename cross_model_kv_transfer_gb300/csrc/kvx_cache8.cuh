@@ -10,33 +10,7 @@
 
 #include "kvx_internal.h"
 
-namespace {
-
-// Two fp32 to two e4m3 codes, nearest even, clamped to +-448 (low byte = lo).
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Two e4m3 codes (the low half of `codes`) to f16x2, exact.
-__device__ __forceinline__ uint32_t f16x2_of(uint32_t codes) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
-  return r;
-}
-__device__ __forceinline__ float2 floats_of(uint32_t codes) {
-  const uint32_t h = f16x2_of(codes);
-  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
-
-// The smallest power of two, at least 2^-126, with amax <= 448 * scale
-// (448 = 1.75 * 2^8; amax finite and not negative).  From amax's bits: its
-// exponent less 8, one more where its significand is above 1.75.
-__device__ __forceinline__ float pow2_scale(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);
-  return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
-}
+namespace kvx8 {
 
 // Requests of a packed batch: cu[0 .. R] (or one token each without it).
 struct Requests {
@@ -64,6 +38,38 @@ struct Requests {
     return good;
   }
 };
+
+}  // namespace kvx8
+
+namespace {
+
+using kvx8::Requests;
+
+// Two fp32 to two e4m3 codes, nearest even, clamped to +-448 (low byte = lo).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 codes (the low half of `codes`) to f16x2, exact.
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+  return r;
+}
+__device__ __forceinline__ float2 floats_of(uint32_t codes) {
+  const uint32_t h = f16x2_of(codes);
+  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// The smallest power of two, at least 2^-126, with amax <= 448 * scale
+// (448 = 1.75 * 2^8; amax finite and not negative).  From amax's bits: its
+// exponent less 8, one more where its significand is above 1.75.
+__device__ __forceinline__ float pow2_scale(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);
+  return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
+}
 
 __device__ __forceinline__ void raise(uint32_t *status, uint32_t bits) {
   if (status) atomicOr(status, bits);
