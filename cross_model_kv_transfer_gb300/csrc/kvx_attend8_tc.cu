@@ -878,6 +878,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool ok = scores(0, 0) && scores(0, 1);
       for (int64_t s = 0; ok && s < count; ++s) {
+        // a group's next scores follow its products at once, but where an item
+        // ends both groups finish it first: they join before they bring new queries
+        const bool more = s + 1 < count, item_ends = enter;
         for (int i = 0; ok && i < 2; ++i) {
           const uint32_t n = WIDE ? (uint32_t)s : (uint32_t)(2 * s + i);
           ok = W.wait(&sh->p_full[i], s & 1) && W.wait(&sh->w_full[n % kWStages], n / kWStages & 1);
@@ -886,8 +889,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_pv(tmem + 2 * kTile + i * kTile, tmem + i * kTile, v0 + (uint64_t)(n % kWStages) * (2 * kTileBytes >> 4), add);
           commit(&sh->pv_done[i]);
           if (!WIDE || i == 1) commit(&sh->w_empty[n % kWStages]);
-          if (s + 1 < count) ok = scores(s + 1, i);
+          if (more && !item_ends) ok = scores(s + 1, i);
         }
+        if (ok && more && item_ends) ok = scores(s + 1, 0) && scores(s + 1, 1);
         add = w.step + 1 != w.steps;
         advance<WIDE>(a, w);
       }

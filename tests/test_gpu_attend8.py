@@ -106,6 +106,22 @@ def test_matches_fp64(H, G, d, bs, lens, new, dtype):
     assert int(status.item()) == 0
 
 
+@pytest.mark.parametrize("H,G,R,longest,new", [(8, 2, 45, 700, 1), (4, 8, 60, 300, 3), (8, 1, 40, 400, 130),
+                                               (2, 8, 20, 600, 70)])
+def test_more_work_than_the_gpu_holds_at_once(H, G, R, longest, new):
+    """Several items follow one another on an SM, whole and in parts."""
+    lens = [max(new, (longest * (r + 1)) // R) for r in range(R)]
+    news = [new if r % 3 else max(1, new // 2) for r in range(R)]
+    c = make(H, G, 128, 16, lens, news, torch.bfloat16, 37)
+    w = torch.zeros((R, H, max(lens)), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = c["cache"].attend(c["q"].cuda(), dev(c["table"]), dev(lens), max(lens),
+                                 cu_seqlens=dev(c["cu"]), max_new=new, weights=w, status=status)
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], 128 ** -0.5)
+    assert int(status.item()) == 0
+    compare(out, lse, w, want, True, max(lens), new * G)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_the_one_token_form_needs_no_request_table(dtype):
     lens = [40, 1, 133]
