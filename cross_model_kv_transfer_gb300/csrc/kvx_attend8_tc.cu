@@ -30,6 +30,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kvx_attend8.cuh"
 #include "kvx_ptx.cuh"
 
@@ -38,8 +40,12 @@ namespace {
 constexpr int kD = 128;             // head_dim
 constexpr int kTile = 128;          // slots and rows of a tile
 constexpr int kTileBytes = kTile * kD;
-constexpr int kKStages = 3, kVStages = 2, kWStages = 2, kRefs = 4;
-constexpr int kLoadWarp = 12, kMmaWarp = 13, kThreads = 14 * 32;
+constexpr int kKStages = 3, kVStages = 2, kWStages = 2;
+constexpr int kLoadWarp = 12, kMmaWarp = 13, kThreads = 16 * 32;
+// registers a thread: 8 softmax warps, 4 that convert, 4 others; together the
+// launch's 512 x 128
+constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kOtherRegs = 64;
+static_assert(256 * kSoftmaxRegs + 128 * (kConvertRegs + kOtherRegs) == kThreads * 128, "register split");
 constexpr uint64_t kWaitNs = 2000000000ull;
 // P carries 2^7 so that f16 keeps probabilities down to 2^-31 of the
 // subtracted maximum's; with the lazy 2^8 that is at most 2^15
@@ -50,12 +56,13 @@ struct TcShared {
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t w_full[kWStages], w_empty[kWStages];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
-  uint64_t ref_full[kRefs];
   uint64_t join, verdict, drain;
   uint32_t tmem_base;
   volatile int abort;
   volatile int last;
-  float ref[kRefs];
+  // the tile's largest value scale, as a power of two: its exponent for the
+  // softmax, 2^7 over it for the conversion
+  float k_ref[kKStages], v_unit[kVStages];
   uint32_t k_mask[kKStages], v_mask[kVStages];   // bit l: slots 4l .. 4l + 3 lie in a block of the pool
   __align__(16) float ks[kKStages][kTile];   // read and written four at a time
   __align__(16) float vs[kVStages][kTile];
@@ -82,11 +89,14 @@ struct Waiter {
   __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
     const uint32_t a = smem_addr(bar);
     if (mbar_try_wait(a, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (true) {
+    uint64_t t0 = 0;
+    for (uint32_t spin = 1;; ++spin) {
       if (mbar_try_wait(a, parity)) return true;
+      if (spin % 64) continue;          // the clock is slow to read
       if (sh->abort) return false;
-      if (globaltimer() - t0 > kWaitNs) {
+      const uint64_t t = globaltimer();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitNs) {
         sh->abort = 1;
         raise(status, KVX_FLAG_TIMEOUT);
         return false;
@@ -279,6 +289,25 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *v) {
       "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
+// Wait for loads, of which v is one: what follows may not use v before.
+__device__ __forceinline__ void tc_wait_ld32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -307,6 +336,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -323,46 +357,98 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float row_factor(const AttendParams &a, float top, float unit) {
   return top < INFINITY ? fmaxf(fabsf(a.c) * unit, 0x1p-126f) : __uint_as_float(0x7fc00000u);
 }
+// Scores of 32 columns times their key scales (four columns share one vector of
+// scales and one bit of `mask`; column e counts where e <= seen).
+template <bool MASK>
+__device__ __forceinline__ void scaled(const uint32_t *s, float4 f, uint32_t mask, int q, int seen, float (&x)[4]) {
+  unpair(mul2(pair(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), pair(f.x, f.y)), x[0], x[1]);
+  unpair(mul2(pair(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), pair(f.z, f.w)), x[2], x[3]);
+  if constexpr (MASK) {
+    const int last = mask >> q & 1 ? seen - 4 * q : -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = e <= last ? x[e] : -INFINITY;
+  }
+}
+template <bool MASK>
+__device__ __forceinline__ float peak_of(const uint32_t (&s)[32], const float4 *scale, uint32_t mask, int seen, float top) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float x[4];
+    scaled<MASK>(s, scale[q], mask, q, seen, x);
+    top = max3(max3(top, x[0], x[1]), x[2], x[3]);
+  }
+  return top;
+}
+template <bool MASK>
+__device__ __forceinline__ uint64_t probabilities(uint32_t to, const uint32_t (&s)[32], const float4 *scale, uint32_t mask,
+                                                  int seen, uint64_t cs2, uint64_t nm2, uint64_t sum2) {
+  uint32_t out[16];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float x[4];
+    scaled<MASK>(s, scale[q], mask, q, seen, x);
+    unpair(fma2(pair(x[0], x[1]), cs2, nm2), x[0], x[1]);
+    unpair(fma2(pair(x[2], x[3]), cs2, nm2), x[2], x[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+    sum2 = add2(sum2, add2(pair(x[0], x[1]), pair(x[2], x[3])));
+    out[2 * q] = f16x2(x[0], x[1]);
+    out[2 * q + 1] = f16x2(x[2], x[3]);
+  }
+  tc_st16(to, out);
+  return sum2;
+}
+// f over the tile's columns, 32 at a time, the next ones on their way.  The first
+// 32 are in `a` already (asked for); AGAIN: they are asked for again at the end.
+template <bool AGAIN, class F, class T>
+__device__ __forceinline__ T walk_columns(uint32_t col, uint32_t (&a)[32], uint32_t (&b)[32], F f, T acc) {
+#pragma unroll 1
+  for (int c = 0; c < 4; c += 2) {
+    tc_wait_ld32(a);
+    tc_ld32(col + 32 * (c + 1), b);
+    acc = f(0, c, a, acc);
+    tc_wait_ld32(b);
+    if (c == 0 || AGAIN) tc_ld32(col + (c == 0 ? 64 : 0), a);
+    acc = f(0, c + 1, b, acc);
+  }
+  return acc;
+}
 // A query row as two e4m3 parts in the swizzled K-major tile; returns the factor
 // on its scores (its sign is in the parts).
 __device__ __forceinline__ float put_query(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
                                            unsigned char *tile, int row) {
-  const auto piece = [&](int c, float (&v)[16]) {
-    if (!live) {
+  uint32_t x[kD / 2];
+  if (!live) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = 0.f;
-    } else if (vec) {
+    for (int e = 0; e < kD / 2; ++e) x[e] = 0;
+  } else if (vec) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 t = __ldg(reinterpret_cast<const uint4 *>(src + 16 * c) + i);
-        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-          v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = __bfloat162float(src[16 * c + e]);
+    for (int e = 0; e < kD / 8; ++e) {
+      const uint4 t = __ldg(reinterpret_cast<const uint4 *>(src) + e);
+      x[4 * e] = t.x;
+      x[4 * e + 1] = t.y;
+      x[4 * e + 2] = t.z;
+      x[4 * e + 3] = t.w;
     }
-  };
-  float top = 0.f, v[16];
+  } else {
+    const unsigned short *h = reinterpret_cast<const unsigned short *>(src);
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    piece(c, v);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(v[e]));
+    for (int e = 0; e < kD / 2; ++e) x[e] = (uint32_t)h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
   }
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < kD / 2; ++e)
+    top = max3(top, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
   const float unit = pow2_scale(top);   // top <= 448 unit
   const float up = a.c != 0.f ? copysignf(1.f / unit, a.c) : 0.f;
-#pragma unroll 1
+#pragma unroll
   for (int c = 0; c < 8; ++c) {
-    piece(c, v);
     uint32_t p1[4], p2[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float y0 = v[4 * j] * up, y1 = v[4 * j + 1] * up, y2 = v[4 * j + 2] * up, y3 = v[4 * j + 3] * up;
+      const uint32_t u0 = x[8 * c + 2 * j], u1 = x[8 * c + 2 * j + 1];
+      const float y0 = __uint_as_float(u0 << 16) * up, y1 = __uint_as_float(u0 & 0xffff0000u) * up;
+      const float y2 = __uint_as_float(u1 << 16) * up, y3 = __uint_as_float(u1 & 0xffff0000u) * up;
       p1[j] = e4m3x2(y0, y1) | e4m3x2(y2, y3) << 16;
       const float2 f0 = floats_of(p1[j]), f1 = floats_of(p1[j] >> 16);
       p2[j] = e4m3x2(y0 - f0.x, y1 - f0.y) | e4m3x2(y2 - f1.x, y3 - f1.y) << 16;
@@ -406,7 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&sh->p_full[i]), 4);
       mbar_init(smem_addr(&sh->pv_done[i]), 1);
     }
-    for (int i = 0; i < kRefs; ++i) mbar_init(smem_addr(&sh->ref_full[i]), 1);
     mbar_init(smem_addr(&sh->join), 8);
     mbar_init(smem_addr(&sh->verdict), 1);
     mbar_init(smem_addr(&sh->drain), 1);
@@ -444,9 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int64_t count = last - first;
 
-  if (count == 0) {
-    // nothing for this CTA
-  } else if (warp < 8) {
+  if (warp < 8) {
+    more_registers<kSoftmaxRegs>();
     // ----------------------------------------------------------------------
     // softmax: a row to a thread
     // ----------------------------------------------------------------------
@@ -457,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.f, cs = 0.f;
     int limit = -1, floor_limit = -1, rows = 0;
     bool live = false, warp_live = false, fresh_o = true;
-    uint32_t tile = 0, item = 0, joins = 0;       // tiles of this group, items, joins so far
+    uint32_t tile = 0, joins = 0;                 // tiles of this group, joins so far
     int64_t seg_first = first;
     bool enter = true;
     for (int64_t now = first; now < last; ++now) {
@@ -488,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
           float top = 0.f;
           if (live)
+#pragma unroll 16
             for (int e = 0; e < kD; ++e) top = fmaxf(top, fabsf(__bfloat162float(src[e])));
           cs = row_factor(a, top, pow2_scale(top));
         }
@@ -503,69 +588,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t mask = sh->k_mask[ks];
         const bool masked = mask != ~0u || j0 + kTile - 1 > floor_limit;
         const float4 *scale = reinterpret_cast<const float4 *>(sh->ks[ks]);
-        const uint64_t cs2 = pair(cs, cs);
-        uint32_t out[64];
-        float top, sum;
-        // probabilities with the maximum `ref` subtracted; the tile's maximum and sum
-        const auto pass = [&](float ref, float *spool) {
-          const uint64_t nm2 = pair(kBias - ref, kBias - ref);
-          uint64_t sum2 = pair(0.f, 0.f);
-          top = -INFINITY;
-#pragma unroll
+        if (!WIDE && p.scores) {     // the scores themselves, for the weights
+          float *to = live && j0 < p.score_ld
+                          ? p.scores + (((int64_t)w.r * a.H + w.h) * p.slot_rows + row) * p.score_ld + j0
+                          : nullptr;
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t s[32];
             tc_ld32(s_col + 32 * c, s);
             tc_wait_ld();
+            if (to)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 f = scale[8 * c + q];
-              float x[4];
-              unpair(mul2(pair(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), pair(f.x, f.y)), x[0], x[1]);
-              unpair(mul2(pair(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), pair(f.z, f.w)), x[2],
-                     x[3]);
-              if (masked) {
-                const bool in = mask >> (8 * c + q) & 1;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (!in || j0 + 32 * c + 4 * q + e > limit) x[e] = -INFINITY;
+              for (int q = 0; q < 8; ++q) {
+                const float4 f = scale[8 * c + q];
+                const int seen = mask >> (8 * c + q) & 1 ? limit - (j0 + 32 * c + 4 * q) : -1;
+                float4 x;
+                x.x = 0 <= seen ? __uint_as_float(s[4 * q]) * f.x * cs : -INFINITY;
+                x.y = 1 <= seen ? __uint_as_float(s[4 * q + 1]) * f.y * cs : -INFINITY;
+                x.z = 2 <= seen ? __uint_as_float(s[4 * q + 2]) * f.z * cs : -INFINITY;
+                x.w = 3 <= seen ? __uint_as_float(s[4 * q + 3]) * f.w * cs : -INFINITY;
+                *reinterpret_cast<float4 *>(to + 32 * c + 4 * q) = x;
               }
-              top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-              const uint64_t y0 = fma2(pair(x[0], x[1]), cs2, nm2), y1 = fma2(pair(x[2], x[3]), cs2, nm2);
-              float e0, e1, e2, e3;
-              unpair(y0, e0, e1);
-              unpair(y1, e2, e3);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              e2 = ex2(e2);
-              e3 = ex2(e3);
-              sum2 = add2(sum2, add2(pair(e0, e1), pair(e2, e3)));
-              out[16 * c + 2 * q] = f16x2(e0, e1);
-              out[16 * c + 2 * q + 1] = f16x2(e2, e3);
-              if (spool)
-                *reinterpret_cast<float4 *>(spool + 32 * c + 4 * q) =
-                    make_float4(x[0] * cs, x[1] * cs, x[2] * cs, x[3] * cs);
-            }
+            __syncwarp();
           }
-          float s0, s1;
-          unpair(sum2, s0, s1);
-          sum = s0 + s1;
-        };
-        float *spool = !WIDE && p.scores && live && j0 < p.score_ld
-                           ? p.scores + (((int64_t)w.r * a.H + w.h) * p.slot_rows + row) * p.score_ld + j0
-                           : nullptr;
-        pass(finite_or_0(m), spool);
-        const float peak = top * cs;      // -inf where nothing is seen
+        }
+        const float ref = sh->k_ref[ks];
+        uint32_t sa[32], sb[32];
+        tc_ld32(s_col, sa);
+        // the maximum of the tile's scores
+        float top = -INFINITY;
+        if (masked)
+          top = walk_columns<true>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], float top) {
+            return peak_of<true>(s, scale + 8 * c, mask >> (8 * c), limit - (j0 + 32 * c), top);
+          }, top);
+        else
+          top = walk_columns<true>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], float top) {
+            return peak_of<false>(s, scale + 8 * c, 0u, 0, top);
+          }, top);
+        const float peak = top * cs + ref;      // -inf where nothing is seen
         const bool over = peak > m + kSlack || (m == -INFINITY && peak > -INFINITY);
         if (__any_sync(~0u, over)) {
+          // seldom: raise the rows' maxima, scale down what they have
           const float mm = fmaxf(m, peak), down = ex2(m - finite_or_0(mm));
           if (!fresh_o) {
+            tc_wait_ld32(sa);
             if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) goto done;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t o[32];
               tc_ld32(o_col + 32 * c, o);
-              tc_wait_ld();
+              tc_wait_ld32(o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
               tc_st32(o_col + 32 * c, o);
@@ -573,11 +646,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           m = mm;
           l *= down;
-          pass(finite_or_0(m), nullptr);
         }
-        l += sum;
-        tc_st32(s_col, out);
-        tc_st32(s_col + 32, out + 32);
+        // probabilities, packed over the scores that are spent
+        const uint64_t cs2 = pair(cs, cs);
+        const float add = kBias + ref - finite_or_0(m);
+        const uint64_t nm2 = pair(add, add);
+        uint64_t sum2 = pair(0.f, 0.f);
+        if (masked)
+          sum2 = walk_columns<false>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], uint64_t sum2) {
+            return probabilities<true>(s_col + 16 * c, s, scale + 8 * c, mask >> (8 * c), limit - (j0 + 32 * c), cs2, nm2, sum2);
+          }, sum2);
+        else
+          sum2 = walk_columns<false>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], uint64_t sum2) {
+            return probabilities<false>(s_col + 16 * c, s, scale + 8 * c, 0u, 0, cs2, nm2, sum2);
+          }, sum2);
+        float s0, s1;
+        unpair(sum2, s0, s1);
+        l += (s0 + s1) * ex2(-ref);    // without the value scale
         tc_wait_st();
       }
       fresh_o = false;
@@ -594,10 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the result of the item, or this CTA's part of it
         enter = true;
         if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) goto done;
-        if (!W.warp_wait(&sh->ref_full[item % kRefs], item / kRefs & 1)) goto done;
         tc_fence_after();
-        const float back = sh->ref[item % kRefs] * (1.f / 128.f);   // V carries 128 / ref
-        ++item;
+        const float back = 1.f / 128.f;   // V carries 2^7
         const bool whole = seg_done && w.step + 1 <= now - seg_first + 1;
         const int64_t at = (int64_t)w.group * G_::ROWS + row;
         const int64_t tok = w.beg + at / a.G;
@@ -684,29 +767,53 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int cta = c / G_::PARTS, sub = c % G_::PARTS;
               return p.partial + ((cta ? s1 + (int64_t)cta * 2 * G_::PARTS : s0) + sub) * part_size;
             };
-            for (int x = tid; x < rows * (kD / 4); x += 256) {
-              const int rr = x / (kD / 4), d = x % (kD / 4) * 4;
-              float mm = -INFINITY, ll = 0.f;
-              float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-              for (int c = 0; c < parts; ++c) mm = fmaxf(mm, __ldcg(part_at(c) + p.slot_rows * kD + rr));
-              mm = finite_or_0(mm);
-#pragma unroll 8
+            // a warp a row, four rows at once
+            constexpr int B = 4;
+            const int d = lane * 4;
+            for (int r0 = warp; r0 < rows; r0 += 8 * B) {
+              float mm[B], ll[B];
+              float4 oo[B];
+#pragma unroll
+              for (int k = 0; k < B; ++k) {
+                mm[k] = -INFINITY;
+                ll[k] = 0.f;
+                oo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+#pragma unroll 4
+              for (int c = 0; c < parts; ++c) {
+                const float *part = part_at(c) + p.slot_rows * kD;
+#pragma unroll
+                for (int k = 0; k < B; ++k)
+                  if (r0 + 8 * k < rows) mm[k] = fmaxf(mm[k], __ldcg(part + r0 + 8 * k));
+              }
+#pragma unroll
+              for (int k = 0; k < B; ++k) mm[k] = finite_or_0(mm[k]);
+#pragma unroll 4
               for (int c = 0; c < parts; ++c) {
                 const float *part = part_at(c);
-                const float f = ex2(__ldcg(part + p.slot_rows * kD + rr) - mm);
-                const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + rr * kD + d));
-                ll += __ldcg(part + p.slot_rows * (kD + 1) + rr) * f;
-                oo.x += y.x * f;
-                oo.y += y.y * f;
-                oo.z += y.z * f;
-                oo.w += y.w * f;
+#pragma unroll
+                for (int k = 0; k < B; ++k) {
+                  const int rr = r0 + 8 * k;
+                  if (rr >= rows) continue;
+                  const float f = ex2(__ldcg(part + p.slot_rows * kD + rr) - mm[k]);
+                  const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + rr * kD + d));
+                  ll[k] += __ldcg(part + p.slot_rows * (kD + 1) + rr) * f;
+                  oo[k].x += y.x * f;
+                  oo[k].y += y.y * f;
+                  oo[k].z += y.z * f;
+                  oo[k].w += y.w * f;
+                }
               }
-              const int64_t ar = (int64_t)w.group * G_::ROWS + rr;
-              const int64_t tk = w.beg + ar / a.G;
-              const int hh = w.h * a.G + (int)(ar % a.G);
-              store_out(a, tk, hh, d, make_float2(oo.x, oo.y), mm, ll);
-              store_out(a, tk, hh, d + 2, make_float2(oo.z, oo.w), mm, ll);
+#pragma unroll
+              for (int k = 0; k < B; ++k) {
+                const int rr = r0 + 8 * k;
+                if (rr >= rows) continue;
+                const int64_t ar = (int64_t)w.group * G_::ROWS + rr;
+                const int64_t tk = w.beg + ar / a.G;
+                const int hh = w.h * a.G + (int)(ar % a.G);
+                store_out(a, tk, hh, d, make_float2(oo[k].x, oo[k].y), mm[k], ll[k]);
+                store_out(a, tk, hh, d + 2, make_float2(oo[k].z, oo[k].w), mm[k], ll[k]);
+              }
             }
           }
         }
@@ -715,36 +822,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   done:;
   } else if (warp < kLoadWarp) {
+    fewer_registers<kConvertRegs>();
     // ----------------------------------------------------------------------
-    // V to f16, times 128 scale / (the largest scale of this CTA's part)
+    // V to f16, times 2^7 scale / (the tile's largest scale)
     // ----------------------------------------------------------------------
     const int t = tid - 8 * 32;
-    uint32_t n = 0, item = 0;
-    bool enter = true;
-    float unit = 0.f;
+    uint32_t n = 0;
     for (int64_t now = first; now < last; ++now) {
-      if (enter) {
-        enter = false;
-        const int64_t s0 = (int64_t)w.step * G_::SLOTS;
-        const int64_t steps = min((int64_t)(w.steps - w.step), last - now);
-        const int64_t s1 = min((int64_t)w.len, s0 + steps * G_::SLOTS);
-        float top = 0x1p-112f;    // scales below count as that: their values vanish beside any other
-        if (s1 > s0) {
-          const int b1 = (int)block_of(a, (int)(s1 - 1));
-          for (int b = (int)block_of(a, (int)s0) + lane; b <= b1; b += 32) {
-            const int page = page_of(a, w.r, b);
-            if (page >= 0) top = fmaxf(top, __ldg(a.vs + (int64_t)page * a.H + w.h));
-          }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        unit = 128.f / top;
-        if (t == 0) {
-          sh->ref[item % kRefs] = top;
-          mbar_arrive(smem_addr(&sh->ref_full[item % kRefs]));
-        }
-        ++item;
-      }
       for (int k = 0; k < (WIDE ? 1 : 2); ++k, ++n) {
         const int vs = n % kVStages, ws = n % kWStages;
         const int j0 = w.step * G_::SLOTS + k * kTile;
@@ -753,29 +837,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned char *src = vbuf + vs * kTileBytes;
         unsigned char *dst = wbuf + ws * 2 * kTileBytes;
         const uint32_t mask = sh->v_mask[vs];
-        const int c = t % 8;                      // 16 dimensions
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int j = u * 16 + t / 8;
-          const bool in = (mask >> (j / 4) & 1) && j0 + j < w.len;
+        const float unit = sh->v_unit[vs];
+        // 16 lanes a row, 8 dimensions each: loads and stores meet no bank twice
+        const int c = t % 16;
+        unsigned char *to = dst + (c / 8) * kTileBytes;
+        const bool all = mask == ~0u && j0 + kTile <= w.len;
+#pragma unroll 4
+        for (int u = 0; u < 16; ++u) {
+          const int j = u * 8 + t / 16;
           const float f = sh->vs[vs][j] * unit;
           const uint32_t f2 = f16x2(f, f);
-          const uint4 y = *reinterpret_cast<const uint4 *>(src + j * kD + ((c ^ (j & 7)) << 4));
-          const uint32_t b[4] = {y.x, y.y, y.z, y.w};
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h[2 * e] = in ? mul_f16x2(f16x2_of(b[e]), f2) : 0u;
-            h[2 * e + 1] = in ? mul_f16x2(f16x2_of(b[e] >> 16), f2) : 0u;
-          }
-          unsigned char *to = dst + (c / 4) * kTileBytes + j * kD;
-          const int p0 = (c % 4 * 2) ^ (j & 7), p1 = p0 ^ 1;
-          // the two halves of the dimensions store in opposite order: no bank twice
-          const bool flip = c >= 4;
-          *reinterpret_cast<uint4 *>(to + ((flip ? p1 : p0) << 4)) =
-              flip ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4 *>(to + ((flip ? p0 : p1) << 4)) =
-              flip ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
+          const uint2 y = *reinterpret_cast<const uint2 *>(src + j * kD + ((c / 2 ^ (j & 7)) << 4) + (c % 2) * 8);
+          uint4 h;
+          h.x = mul_f16x2(f16x2_of(y.x), f2);
+          h.y = mul_f16x2(f16x2_of(y.x >> 16), f2);
+          h.z = mul_f16x2(f16x2_of(y.y), f2);
+          h.w = mul_f16x2(f16x2_of(y.y >> 16), f2);
+          if (!all && !((mask >> (j / 4) & 1) && j0 + j < w.len)) h = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(to + j * kD + ((c % 8 ^ (j & 7)) << 4)) = h;
         }
         fence_async_proxy();
         __syncwarp();
@@ -784,11 +863,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_addr(&sh->v_empty[vs]));
         }
       }
-      if (w.step + 1 == w.steps) enter = true;
       advance<WIDE>(a, w);
     }
   cv_done:;
   } else if (warp == kLoadWarp) {
+    fewer_registers<kOtherRegs>();
     // ----------------------------------------------------------------------
     // block lookups, scales and TMA: lane l looks up slots 4l .. 4l + 3
     // ----------------------------------------------------------------------
@@ -809,6 +888,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = (int)(sb * a.bs + off);
         const float kscale = page >= 0 ? __ldg(a.ks + sb) : 0.f, vscale = page >= 0 ? __ldg(a.vs + sb) : 0.f;
         const unsigned mask = __ballot_sync(~0u, page >= 0);
+        // the tile's largest value scale, rounded up to a power of two 2^e; scales
+        // below 2^-96 count as that, their values vanish beside any other
+        const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(vscale));
+        const int e = max((int)(most >> 23) + ((most & 0x7fffff) != 0), 127 - 96);
         const int per = p.box / 4, boxes = kTile / p.box;     // lanes a box, boxes
         const int from = __shfl_sync(~0u, row, lane < boxes ? lane * per : 0);
         const bool there = lane < boxes && (mask >> (lane * per) & 1);
@@ -817,6 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4 *>(&sh->ks[ks][4 * lane]) = make_float4(kscale, kscale, kscale, kscale);
         if (lane == 0) {
           sh->k_mask[ks] = mask;
+          sh->k_ref[ks] = (float)(e - 127);
           mbar_expect_tx(smem_addr(&sh->k_full[ks]), bytes);
         }
         __syncwarp();
@@ -828,6 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4 *>(&sh->vs[vs][4 * lane]) = make_float4(vscale, vscale, vscale, vscale);
         if (lane == 0) {
           sh->v_mask[vs] = mask;
+          sh->v_unit[vs] = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
           mbar_expect_tx(smem_addr(&sh->v_full[vs]), bytes);
         }
         __syncwarp();
@@ -847,7 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t x = n > kVStages ? n - kVStages : 0; x < n; ++x) drain_wait(&sh->v_full[x % kVStages], x / kVStages & 1);
       if (sh->abort) drain_wait(&sh->k_full[n % kKStages], n / kKStages & 1);
     }
-  } else {
+  } else if (warp == kMmaWarp) {
+    fewer_registers<kOtherRegs>();
     // ----------------------------------------------------------------------
     // the MMAs, from one thread
     // ----------------------------------------------------------------------
@@ -876,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       };
-      bool ok = scores(0, 0) && scores(0, 1);
+      bool ok = count > 0 && scores(0, 0) && scores(0, 1);
       for (int64_t s = 0; ok && s < count; ++s) {
         // a group's next scores follow its products at once, but where an item
         // ends both groups finish it first: they join before they bring new queries
@@ -901,6 +987,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else {
+    fewer_registers<kOtherRegs>();   // the split counts whole warpgroups
   }
 
   tc_fence_before();
