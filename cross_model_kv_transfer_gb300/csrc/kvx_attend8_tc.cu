@@ -64,8 +64,9 @@ struct TcShared {
   // softmax, 2^7 over it for the conversion
   float k_ref[kKStages], v_unit[kVStages];
   uint32_t k_mask[kKStages], v_mask[kVStages];   // bit l: slots 4l .. 4l + 3 lie in a block of the pool
-  __align__(16) float ks[kKStages][kTile];   // read and written four at a time
-  __align__(16) float vs[kVStages][kTile];
+  // scales, one for four slots (which lie in one block)
+  __align__(16) float ks[kKStages][kTile / 4];
+  __align__(16) float vs[kVStages][kTile / 4];
 };
 constexpr size_t kSmemQ = 4 * (size_t)kTileBytes;     // two tiles of two parts
 constexpr size_t kSmemBytes = 1024 + kSmemQ + (kKStages + kVStages) * (size_t)kTileBytes +
@@ -357,46 +358,53 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float row_factor(const AttendParams &a, float top, float unit) {
   return top < INFINITY ? fmaxf(fabsf(a.c) * unit, 0x1p-126f) : __uint_as_float(0x7fc00000u);
 }
-// Scores of 32 columns times their key scales (four columns share one vector of
-// scales and one bit of `mask`; column e counts where e <= seen).
+// Scores of 32 columns times their key scales, in place.  Four columns share a
+// scale and a bit of `mask`; column e counts where e <= seen.
 template <bool MASK>
-__device__ __forceinline__ void scaled(const uint32_t *s, float4 f, uint32_t mask, int q, int seen, float (&x)[4]) {
-  unpair(mul2(pair(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), pair(f.x, f.y)), x[0], x[1]);
-  unpair(mul2(pair(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), pair(f.z, f.w)), x[2], x[3]);
-  if constexpr (MASK) {
-    const int last = mask >> q & 1 ? seen - 4 * q : -1;
+__device__ __forceinline__ void scale_columns(uint32_t (&s)[32], const float4 *scale, uint32_t mask, int seen) {
+  const float4 f0 = scale[0], f1 = scale[1];
+  const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = e <= last ? x[e] : -INFINITY;
+  for (int e = 0; e < 32; e += 2) {
+    float x0, x1;
+    unpair(mul2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pair(f[e / 4], f[e / 4])), x0, x1);
+    if constexpr (MASK) {
+      const int last = mask >> (e / 4) & 1 ? seen : -1;
+      x0 = e <= last ? x0 : -INFINITY;
+      x1 = e + 1 <= last ? x1 : -INFINITY;
+    }
+    s[e] = __float_as_uint(x0);
+    s[e + 1] = __float_as_uint(x1);
   }
 }
 template <bool MASK>
-__device__ __forceinline__ float peak_of(const uint32_t (&s)[32], const float4 *scale, uint32_t mask, int seen, float top) {
+__device__ __forceinline__ float peak_of(uint32_t (&s)[32], const float4 *scale, uint32_t mask, int seen, float top) {
+  scale_columns<MASK>(s, scale, mask, seen);
+  float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};   // four chains
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    float x[4];
-    scaled<MASK>(s, scale[q], mask, q, seen, x);
-    top = max3(max3(top, x[0], x[1]), x[2], x[3]);
+  for (int e = 0; e < 32; e += 2) {
+    float &u = t[e / 2 % 4];
+    u = max3(u, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
   }
-  return top;
+  return max3(max3(t[0], t[1], t[2]), t[3], t[3]);
 }
 template <bool MASK>
-__device__ __forceinline__ uint64_t probabilities(uint32_t to, const uint32_t (&s)[32], const float4 *scale, uint32_t mask,
+__device__ __forceinline__ uint64_t probabilities(uint32_t to, uint32_t (&s)[32], const float4 *scale, uint32_t mask,
                                                   int seen, uint64_t cs2, uint64_t nm2, uint64_t sum2) {
+  scale_columns<MASK>(s, scale, mask, seen);
+  uint64_t part[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
   uint32_t out[16];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    float x[4];
-    scaled<MASK>(s, scale[q], mask, q, seen, x);
-    unpair(fma2(pair(x[0], x[1]), cs2, nm2), x[0], x[1]);
-    unpair(fma2(pair(x[2], x[3]), cs2, nm2), x[2], x[3]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
-    sum2 = add2(sum2, add2(pair(x[0], x[1]), pair(x[2], x[3])));
-    out[2 * q] = f16x2(x[0], x[1]);
-    out[2 * q + 1] = f16x2(x[2], x[3]);
+  for (int e = 0; e < 32; e += 2) {
+    float x0, x1;
+    unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cs2, nm2), x0, x1);
+    x0 = ex2(x0);
+    x1 = ex2(x1);
+    part[e / 2 % 2] = add2(part[e / 2 % 2], pair(x0, x1));
+    out[e / 2] = f16x2(x0, x1);
   }
   tc_st16(to, out);
-  return sum2;
+  return add2(sum2, add2(part[0], part[1]));
 }
 // f over the tile's columns, 32 at a time, the next ones on their way.  The first
 // 32 are in `a` already (asked for); AGAIN: they are asked for again at the end.
@@ -415,7 +423,7 @@ __device__ __forceinline__ T walk_columns(uint32_t col, uint32_t (&a)[32], uint3
 }
 // A query row as two e4m3 parts in the swizzled K-major tile; returns the factor
 // on its scores (its sign is in the parts).
-__device__ __forceinline__ float put_query(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
+__device__ __noinline__ float put_query(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
                                            unsigned char *tile, int row) {
   uint32_t x[kD / 2];
   if (!live) {
@@ -458,6 +466,173 @@ __device__ __forceinline__ float put_query(const AttendParams &a, bool vec, cons
     *reinterpret_cast<uint4 *>(to + kTileBytes) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
   }
   return row_factor(a, top, unit);
+}
+
+// What a softmax group knows of its item when the item, or the CTA's part of it, ends.
+struct Item {
+  TcWalk w;
+  int64_t T, N, now, seg_first, first;
+  int rows, row;
+  bool live, warp_live;
+  float m, l;
+  uint32_t o_col, tile, joins;   // tiles and joins of this group so far
+};
+// Write the result of the item, or leave this CTA's part of it and let the last to
+// come join the parts.  Seldom, and apart from the loop so that it costs that no
+// registers.
+template <bool WIDE>
+__device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const Item it, int i) {
+  using G_ = Geo<WIDE>;
+  const AttendParams &a = p.a;
+  const Waiter W{sh, a.status};
+  const TcWalk &w = it.w;
+  const uint32_t tile = it.tile, joins = it.joins;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int64_t T = it.T, N = it.N, now = it.now, seg_first = it.seg_first, first = it.first;
+  const int rows = it.rows, row = it.row;
+  const bool live = it.live, warp_live = it.warp_live, seg_done = w.step + 1 == w.steps;
+  const float m = it.m, l = it.l;
+  const uint32_t o_col = it.o_col;
+  // the result of the item, or this CTA's part of it
+  if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) return false;
+  tc_fence_after();
+  const float back = 1.f / 128.f;   // V carries 2^7
+  const bool whole = seg_done && w.step + 1 <= now - seg_first + 1;
+  const int64_t at = (int64_t)w.group * G_::ROWS + row;
+  const int64_t tok = w.beg + at / a.G;
+  const int hq = w.h * a.G + (int)(at % a.G);
+  const int64_t part_size = p.part_size;
+  float *slot = p.partial + (((int64_t)blockIdx.x * 2 + (seg_first == first ? 0 : 1)) * G_::PARTS + (WIDE ? 0 : i)) *
+                                part_size;
+  const bool direct = WIDE && whole;
+  if (warp_live) {
+    const float inv = direct ? (l != 0.f ? back / l : 0.f) : back;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      tc_ld32(o_col + 32 * c, o);
+      tc_wait_ld();
+      if (live && !direct) {
+        float4 *to = reinterpret_cast<float4 *>(slot + row * kD + 32 * c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          to[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                              __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+      } else if (live) {
+        __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.out) + tok * a.ot + hq * a.oh + 32 * c;
+        uint32_t b[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          b[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+        if (p.vec_out) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            reinterpret_cast<uint4 *>(to)[e] = make_uint4(b[4 * e], b[4 * e + 1], b[4 * e + 2], b[4 * e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            to[2 * e] = __ushort_as_bfloat16((unsigned short)(b[e] & 0xffff));
+            to[2 * e + 1] = __ushort_as_bfloat16((unsigned short)(b[e] >> 16));
+          }
+        }
+      }
+      __syncwarp();   // together to the next load
+    }
+    if (live) {
+      const float mt = m - kBias;           // what the sums are relative to
+      if (direct) {
+        a.lse[tok * a.Hq + hq] = l != 0.f ? (mt + log2f(l)) * kLn2 : -INFINITY;
+      } else {
+        slot[p.slot_rows * kD + row] = mt;
+        slot[p.slot_rows * (kD + 1) + row] = l;
+      }
+    }
+  }
+  if (!direct) {
+    // join: the CTA's groups first, then, of several CTAs, the last to come
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sh->join));
+    if (!W.warp_wait(&sh->join, joins & 1)) return false;
+    const int64_t begin = now - w.step, end = begin + w.steps;   // the item's steps
+    const int64_t c0 = ((begin + 1) * N - 1) / T, c1 = (end * N - 1) / T;
+    bool mine = whole;
+    if (!whole) {
+      if (tid == 0) {
+        int *arrived = p.arrived + ((int64_t)w.r * a.H + w.h) * p.groups + w.group;
+        __threadfence();
+        const bool all = atomicAdd(arrived, 1) == (int)(c1 - c0);
+        if (all) *arrived = 0;   // ready for the next call
+        __threadfence();
+        sh->last = all;
+        mbar_arrive(smem_addr(&sh->verdict));
+      }
+    } else if (tid == 0) {
+      sh->last = 1;
+      mbar_arrive(smem_addr(&sh->verdict));
+    }
+    if (!W.warp_wait(&sh->verdict, joins & 1)) return false;
+    mine = sh->last;
+    if (mine) {
+      __threadfence();
+      // CTA c's part is its first item unless the item begins inside it
+      const int64_t s0 = (c0 * 2 + (c0 * T / N != begin)) * G_::PARTS, s1 = c0 * 2 * G_::PARTS;
+      const int parts = (int)(c1 - c0 + 1) * G_::PARTS;
+      const auto part_at = [&](int c) {
+        const int cta = c / G_::PARTS, sub = c % G_::PARTS;
+        return p.partial + ((cta ? s1 + (int64_t)cta * 2 * G_::PARTS : s0) + sub) * part_size;
+      };
+      // a warp a row, four rows at once
+      constexpr int B = 4;
+      const int d = lane * 4;
+      for (int r0 = warp; r0 < rows; r0 += 8 * B) {
+        float mm[B], ll[B];
+        float4 oo[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+          mm[k] = -INFINITY;
+          ll[k] = 0.f;
+          oo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 4
+        for (int c = 0; c < parts; ++c) {
+          const float *part = part_at(c) + p.slot_rows * kD;
+#pragma unroll
+          for (int k = 0; k < B; ++k)
+            if (r0 + 8 * k < rows) mm[k] = fmaxf(mm[k], __ldcg(part + r0 + 8 * k));
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) mm[k] = finite_or_0(mm[k]);
+#pragma unroll 4
+        for (int c = 0; c < parts; ++c) {
+          const float *part = part_at(c);
+#pragma unroll
+          for (int k = 0; k < B; ++k) {
+            const int rr = r0 + 8 * k;
+            if (rr >= rows) continue;
+            const float f = ex2(__ldcg(part + p.slot_rows * kD + rr) - mm[k]);
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + rr * kD + d));
+            ll[k] += __ldcg(part + p.slot_rows * (kD + 1) + rr) * f;
+            oo[k].x += y.x * f;
+            oo[k].y += y.y * f;
+            oo[k].z += y.z * f;
+            oo[k].w += y.w * f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+          const int rr = r0 + 8 * k;
+          if (rr >= rows) continue;
+          const int64_t ar = (int64_t)w.group * G_::ROWS + rr;
+          const int64_t tk = w.beg + ar / a.G;
+          const int hh = w.h * a.G + (int)(ar % a.G);
+          store_out(a, tk, hh, d, make_float2(oo[k].x, oo[k].y), mm[k], ll[k]);
+          store_out(a, tk, hh, d + 2, make_float2(oo[k].z, oo[k].w), mm[k], ll[k]);
+        }
+      }
+    }
+  }
+  return true;
 }
 
 // --- the kernel ------------------------------------------------------------------
@@ -597,18 +772,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t s[32];
             tc_ld32(s_col + 32 * c, s);
             tc_wait_ld();
+            scale_columns<true>(s, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c));
             if (to)
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const float4 f = scale[8 * c + q];
-                const int seen = mask >> (8 * c + q) & 1 ? limit - (j0 + 32 * c + 4 * q) : -1;
-                float4 x;
-                x.x = 0 <= seen ? __uint_as_float(s[4 * q]) * f.x * cs : -INFINITY;
-                x.y = 1 <= seen ? __uint_as_float(s[4 * q + 1]) * f.y * cs : -INFINITY;
-                x.z = 2 <= seen ? __uint_as_float(s[4 * q + 2]) * f.z * cs : -INFINITY;
-                x.w = 3 <= seen ? __uint_as_float(s[4 * q + 3]) * f.w * cs : -INFINITY;
-                *reinterpret_cast<float4 *>(to + 32 * c + 4 * q) = x;
-              }
+              for (int q = 0; q < 32; q += 4)
+                *reinterpret_cast<float4 *>(to + 32 * c + q) =
+                    make_float4(__uint_as_float(s[q]) * cs, __uint_as_float(s[q + 1]) * cs,
+                                __uint_as_float(s[q + 2]) * cs, __uint_as_float(s[q + 3]) * cs);
             __syncwarp();
           }
         }
@@ -619,11 +789,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float top = -INFINITY;
         if (masked)
           top = walk_columns<true>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], float top) {
-            return peak_of<true>(s, scale + 8 * c, mask >> (8 * c), limit - (j0 + 32 * c), top);
+            return peak_of<true>(s, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), top);
           }, top);
         else
           top = walk_columns<true>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], float top) {
-            return peak_of<false>(s, scale + 8 * c, 0u, 0, top);
+            return peak_of<false>(s, scale + 2 * c, 0u, 0, top);
           }, top);
         const float peak = top * cs + ref;      // -inf where nothing is seen
         const bool over = peak > m + kSlack || (m == -INFINITY && peak > -INFINITY);
@@ -654,11 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum2 = pair(0.f, 0.f);
         if (masked)
           sum2 = walk_columns<false>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], uint64_t sum2) {
-            return probabilities<true>(s_col + 16 * c, s, scale + 8 * c, mask >> (8 * c), limit - (j0 + 32 * c), cs2, nm2, sum2);
+            return probabilities<true>(s_col + 16 * c, s, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), cs2, nm2, sum2);
           }, sum2);
         else
           sum2 = walk_columns<false>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], uint64_t sum2) {
-            return probabilities<false>(s_col + 16 * c, s, scale + 8 * c, 0u, 0, cs2, nm2, sum2);
+            return probabilities<false>(s_col + 16 * c, s, scale + 2 * c, 0u, 0, cs2, nm2, sum2);
           }, sum2);
         float s0, s1;
         unpair(sum2, s0, s1);
@@ -676,147 +846,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       const bool seg_done = w.step + 1 == w.steps;
       if (seg_done || now + 1 == last) {
-        // the result of the item, or this CTA's part of it
         enter = true;
-        if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) goto done;
-        tc_fence_after();
-        const float back = 1.f / 128.f;   // V carries 2^7
-        const bool whole = seg_done && w.step + 1 <= now - seg_first + 1;
-        const int64_t at = (int64_t)w.group * G_::ROWS + row;
-        const int64_t tok = w.beg + at / a.G;
-        const int hq = w.h * a.G + (int)(at % a.G);
-        const int64_t part_size = p.part_size;
-        float *slot = p.partial + (((int64_t)blockIdx.x * 2 + (seg_first == first ? 0 : 1)) * G_::PARTS + (WIDE ? 0 : i)) *
-                                      part_size;
-        const bool direct = WIDE && whole;
-        if (warp_live) {
-          const float inv = direct ? (l != 0.f ? back / l : 0.f) : back;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tc_ld32(o_col + 32 * c, o);
-            tc_wait_ld();
-            if (live && !direct) {
-              float4 *to = reinterpret_cast<float4 *>(slot + row * kD + 32 * c);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                to[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                    __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
-            } else if (live) {
-              __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.out) + tok * a.ot + hq * a.oh + 32 * c;
-              uint32_t b[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                b[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-              if (p.vec_out) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  reinterpret_cast<uint4 *>(to)[e] = make_uint4(b[4 * e], b[4 * e + 1], b[4 * e + 2], b[4 * e + 3]);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  to[2 * e] = __ushort_as_bfloat16((unsigned short)(b[e] & 0xffff));
-                  to[2 * e + 1] = __ushort_as_bfloat16((unsigned short)(b[e] >> 16));
-                }
-              }
-            }
-            __syncwarp();   // together to the next load
-          }
-          if (live) {
-            const float mt = m - kBias;           // what the sums are relative to
-            if (direct) {
-              a.lse[tok * a.Hq + hq] = l != 0.f ? (mt + log2f(l)) * kLn2 : -INFINITY;
-            } else {
-              slot[p.slot_rows * kD + row] = mt;
-              slot[p.slot_rows * (kD + 1) + row] = l;
-            }
-          }
-        }
-        if (!direct) {
-          // join: the CTA's groups first, then, of several CTAs, the last to come
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh->join));
-          if (!W.warp_wait(&sh->join, joins & 1)) goto done;
-          const int64_t begin = now - w.step, end = begin + w.steps;   // the item's steps
-          const int64_t c0 = ((begin + 1) * N - 1) / T, c1 = (end * N - 1) / T;
-          bool mine = whole;
-          if (!whole) {
-            if (tid == 0) {
-              int *arrived = p.arrived + ((int64_t)w.r * a.H + w.h) * p.groups + w.group;
-              __threadfence();
-              const bool all = atomicAdd(arrived, 1) == (int)(c1 - c0);
-              if (all) *arrived = 0;   // ready for the next call
-              __threadfence();
-              sh->last = all;
-              mbar_arrive(smem_addr(&sh->verdict));
-            }
-          } else if (tid == 0) {
-            sh->last = 1;
-            mbar_arrive(smem_addr(&sh->verdict));
-          }
-          if (!W.warp_wait(&sh->verdict, joins & 1)) goto done;
-          mine = sh->last;
-          ++joins;
-          if (mine) {
-            __threadfence();
-            // CTA c's part is its first item unless the item begins inside it
-            const int64_t s0 = (c0 * 2 + (c0 * T / N != begin)) * G_::PARTS, s1 = c0 * 2 * G_::PARTS;
-            const int parts = (int)(c1 - c0 + 1) * G_::PARTS;
-            const auto part_at = [&](int c) {
-              const int cta = c / G_::PARTS, sub = c % G_::PARTS;
-              return p.partial + ((cta ? s1 + (int64_t)cta * 2 * G_::PARTS : s0) + sub) * part_size;
-            };
-            // a warp a row, four rows at once
-            constexpr int B = 4;
-            const int d = lane * 4;
-            for (int r0 = warp; r0 < rows; r0 += 8 * B) {
-              float mm[B], ll[B];
-              float4 oo[B];
-#pragma unroll
-              for (int k = 0; k < B; ++k) {
-                mm[k] = -INFINITY;
-                ll[k] = 0.f;
-                oo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-              }
-#pragma unroll 4
-              for (int c = 0; c < parts; ++c) {
-                const float *part = part_at(c) + p.slot_rows * kD;
-#pragma unroll
-                for (int k = 0; k < B; ++k)
-                  if (r0 + 8 * k < rows) mm[k] = fmaxf(mm[k], __ldcg(part + r0 + 8 * k));
-              }
-#pragma unroll
-              for (int k = 0; k < B; ++k) mm[k] = finite_or_0(mm[k]);
-#pragma unroll 4
-              for (int c = 0; c < parts; ++c) {
-                const float *part = part_at(c);
-#pragma unroll
-                for (int k = 0; k < B; ++k) {
-                  const int rr = r0 + 8 * k;
-                  if (rr >= rows) continue;
-                  const float f = ex2(__ldcg(part + p.slot_rows * kD + rr) - mm[k]);
-                  const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + rr * kD + d));
-                  ll[k] += __ldcg(part + p.slot_rows * (kD + 1) + rr) * f;
-                  oo[k].x += y.x * f;
-                  oo[k].y += y.y * f;
-                  oo[k].z += y.z * f;
-                  oo[k].w += y.w * f;
-                }
-              }
-#pragma unroll
-              for (int k = 0; k < B; ++k) {
-                const int rr = r0 + 8 * k;
-                if (rr >= rows) continue;
-                const int64_t ar = (int64_t)w.group * G_::ROWS + rr;
-                const int64_t tk = w.beg + ar / a.G;
-                const int hh = w.h * a.G + (int)(ar % a.G);
-                store_out(a, tk, hh, d, make_float2(oo[k].x, oo[k].y), mm[k], ll[k]);
-                store_out(a, tk, hh, d + 2, make_float2(oo[k].z, oo[k].w), mm[k], ll[k]);
-              }
-            }
-          }
-        }
+        const Item it{w, T, N, now, seg_first, first, rows, row, live, warp_live, m, l, o_col, tile, joins};
+        if (!finish_item<WIDE>(p, sh, it, i)) goto done;
+        joins += !WIDE || !seg_done || now - seg_first + 1 < w.steps;
       }
       advance<WIDE>(a, w);
     }
@@ -845,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
         for (int u = 0; u < 16; ++u) {
           const int j = u * 8 + t / 16;
-          const float f = sh->vs[vs][j] * unit;
+          const float f = sh->vs[vs][j / 4] * unit;
           const uint32_t f2 = f16x2(f, f);
           const uint2 y = *reinterpret_cast<const uint2 *>(src + j * kD + ((c / 2 ^ (j & 7)) << 4) + (c % 2) * 8);
           uint4 h;
@@ -897,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool there = lane < boxes && (mask >> (lane * per) & 1);
         const uint32_t bytes = __popc(__ballot_sync(~0u, there)) * (uint32_t)p.box * kD;
         if (!W.warp_wait(&sh->k_empty[ks], (n / kKStages & 1) ^ 1)) goto ld_done;
-        *reinterpret_cast<float4 *>(&sh->ks[ks][4 * lane]) = make_float4(kscale, kscale, kscale, kscale);
+        sh->ks[ks][lane] = kscale;
         if (lane == 0) {
           sh->k_mask[ks] = mask;
           sh->k_ref[ks] = (float)(e - 127);
@@ -909,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       smem_addr(&sh->k_full[ks]));
         if (lane != 0) mbar_arrive(smem_addr(&sh->k_full[ks]));
         if (!W.warp_wait(&sh->v_empty[vs], (n / kVStages & 1) ^ 1)) goto ld_done;
-        *reinterpret_cast<float4 *>(&sh->vs[vs][4 * lane]) = make_float4(vscale, vscale, vscale, vscale);
+        sh->vs[vs][lane] = vscale;
         if (lane == 0) {
           sh->v_mask[vs] = mask;
           sh->v_unit[vs] = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
