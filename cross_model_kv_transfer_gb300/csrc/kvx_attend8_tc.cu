@@ -144,9 +144,9 @@ __device__ __forceinline__ void enter_request(const AttendParams &a, TcWalk &w) 
   w.fresh = (int)(a.req.begin(w.r + 1) - w.beg);
   w.groups = groups_of<WIDE>(a, w.fresh);
 }
+// To the first step of the next item.
 template <bool WIDE>
-__device__ __forceinline__ void advance(const AttendParams &a, TcWalk &w) {
-  if (++w.step < w.steps) return;
+__device__ __forceinline__ void next_item(const AttendParams &a, TcWalk &w) {
   w.step = 0;
   if (++w.group >= w.groups) {
     w.group = 0;
@@ -322,11 +322,6 @@ __device__ __forceinline__ uint64_t pair(float lo, float hi) {
 __device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -358,53 +353,61 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float row_factor(const AttendParams &a, float top, float unit) {
   return top < INFINITY ? fmaxf(fabsf(a.c) * unit, 0x1p-126f) : __uint_as_float(0x7fc00000u);
 }
-// Scores of 32 columns times their key scales, in place.  Four columns share a
-// scale and a bit of `mask`; column e counts where e <= seen.
+// 32 columns of scores.  Four columns share a key scale f > 0 and a bit of `mask`;
+// with MASK column e counts where e <= seen (the others become -inf, and scales
+// that are missing 1).
 template <bool MASK>
-__device__ __forceinline__ void scale_columns(uint32_t (&s)[32], const float4 *scale, uint32_t mask, int seen) {
+__device__ __forceinline__ void columns(uint32_t (&s)[32], float (&f)[8], const float4 *scale, uint32_t mask, int seen) {
   const float4 f0 = scale[0], f1 = scale[1];
-  const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+  const float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    float x0, x1;
-    unpair(mul2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pair(f[e / 4], f[e / 4])), x0, x1);
+  for (int q = 0; q < 8; ++q) {
+    f[q] = v[q];
     if constexpr (MASK) {
-      const int last = mask >> (e / 4) & 1 ? seen : -1;
-      x0 = e <= last ? x0 : -INFINITY;
-      x1 = e + 1 <= last ? x1 : -INFINITY;
+      const bool in = mask >> q & 1;
+      f[q] = in ? v[q] : 1.f;
+      const int last = in ? seen - 4 * q : -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[4 * q + e] = e <= last ? s[4 * q + e] : 0xff800000u;
     }
-    s[e] = __float_as_uint(x0);
-    s[e + 1] = __float_as_uint(x1);
   }
 }
+// The largest of the scaled scores and `top`.
 template <bool MASK>
 __device__ __forceinline__ float peak_of(uint32_t (&s)[32], const float4 *scale, uint32_t mask, int seen, float top) {
-  scale_columns<MASK>(s, scale, mask, seen);
-  float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};   // four chains
+  float f[8], u[8];
+  columns<MASK>(s, f, scale, mask, seen);
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    float &u = t[e / 2 % 4];
-    u = max3(u, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+  for (int q = 0; q < 8; ++q) {
+    const float *x = reinterpret_cast<const float *>(s) + 4 * q;
+    u[q] = fmaxf(max3(x[0], x[1], x[2]), x[3]) * f[q];
   }
-  return max3(max3(t[0], t[1], t[2]), t[3], t[3]);
+  return max3(max3(top, max3(u[0], u[1], u[2]), max3(u[3], u[4], u[5])), u[6], u[7]);
 }
+// exp2(score f cs + add) in f16 to tensor memory, and their sum.
 template <bool MASK>
 __device__ __forceinline__ uint64_t probabilities(uint32_t to, uint32_t (&s)[32], const float4 *scale, uint32_t mask,
-                                                  int seen, uint64_t cs2, uint64_t nm2, uint64_t sum2) {
-  scale_columns<MASK>(s, scale, mask, seen);
-  uint64_t part[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+                                                  int seen, float cs, uint64_t add, uint64_t sum) {
+  float f[8];
+  columns<MASK>(s, f, scale, mask, seen);
   uint32_t out[16];
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    float x0, x1;
-    unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cs2, nm2), x0, x1);
-    x0 = ex2(x0);
-    x1 = ex2(x1);
-    part[e / 2 % 2] = add2(part[e / 2 % 2], pair(x0, x1));
-    out[e / 2] = f16x2(x0, x1);
+  for (int q = 0; q < 8; ++q) {
+    // not 0, which would make NaN of -inf
+    const float g = MASK ? fmaxf(f[q] * cs, 0x1p-126f) : f[q] * cs;
+    const uint64_t g2 = pair(g, g);
+    const float *x = reinterpret_cast<const float *>(s) + 4 * q;
+    float y[4];
+    unpair(fma2(pair(x[0], x[1]), g2, add), y[0], y[1]);
+    unpair(fma2(pair(x[2], x[3]), g2, add), y[2], y[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = ex2(y[e]);
+    sum = add2(sum, add2(pair(y[0], y[1]), pair(y[2], y[3])));
+    out[2 * q] = f16x2(y[0], y[1]);
+    out[2 * q + 1] = f16x2(y[2], y[3]);
   }
   tc_st16(to, out);
-  return add2(sum2, add2(part[0], part[1]));
+  return sum;
 }
 // f over the tile's columns, 32 at a time, the next ones on their way.  The first
 // 32 are in `a` already (asked for); AGAIN: they are asked for again at the end.
@@ -414,18 +417,15 @@ __device__ __forceinline__ T walk_columns(uint32_t col, uint32_t (&a)[32], uint3
   for (int c = 0; c < 4; c += 2) {
     tc_wait_ld32(a);
     tc_ld32(col + 32 * (c + 1), b);
-    acc = f(0, c, a, acc);
+    acc = f(c, a, acc);
     tc_wait_ld32(b);
     if (c == 0 || AGAIN) tc_ld32(col + (c == 0 ? 64 : 0), a);
-    acc = f(0, c + 1, b, acc);
+    acc = f(c + 1, b, acc);
   }
   return acc;
 }
-// A query row as two e4m3 parts in the swizzled K-major tile; returns the factor
-// on its scores (its sign is in the parts).
-__device__ __noinline__ float put_query(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
-                                           unsigned char *tile, int row) {
-  uint32_t x[kD / 2];
+// A row's 128 elements, packed as they lie (zeros for a dead row).
+__device__ __forceinline__ void load_query(const __nv_bfloat16 *src, bool vec, bool live, uint32_t (&x)[kD / 2]) {
   if (!live) {
 #pragma unroll
     for (int e = 0; e < kD / 2; ++e) x[e] = 0;
@@ -443,10 +443,27 @@ __device__ __noinline__ float put_query(const AttendParams &a, bool vec, const _
 #pragma unroll
     for (int e = 0; e < kD / 2; ++e) x[e] = (uint32_t)h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
   }
+}
+__device__ __forceinline__ float largest(const uint32_t (&x)[kD / 2]) {
   float top = 0.f;
 #pragma unroll
   for (int e = 0; e < kD / 2; ++e)
     top = max3(top, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
+  return top;
+}
+__device__ __noinline__ float query_factor(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live) {
+  uint32_t x[kD / 2];
+  load_query(src, vec, live, x);
+  const float top = largest(x);
+  return row_factor(a, top, pow2_scale(top));
+}
+// A query row as two e4m3 parts in the swizzled K-major tile; returns the factor
+// on its scores (its sign is in the parts).
+__device__ __noinline__ float put_query(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
+                                           unsigned char *tile, int row) {
+  uint32_t x[kD / 2];
+  load_query(src, vec, live, x);
+  const float top = largest(x);
   const float unit = pow2_scale(top);   // top <= 448 unit
   const float up = a.c != 0.f ? copysignf(1.f / unit, a.c) : 0.f;
 #pragma unroll
@@ -468,11 +485,44 @@ __device__ __noinline__ float put_query(const AttendParams &a, bool vec, const _
   return row_factor(a, top, unit);
 }
 
+// O times a row's factor, in place.
+__device__ __noinline__ void scale_down(uint32_t col, float down) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t o[32];
+    tc_ld32(col + 32 * c, o);
+    tc_wait_ld32(o);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
+    tc_st32(col + 32 * c, o);
+  }
+}
+// The tile's scores, base 2, to a row of 128 (NULL: only take part).
+__device__ __noinline__ void keep_scores(uint32_t col, float *to, const float4 *scale, uint32_t mask, int seen, float cs) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t s[32];
+    float f[8];
+    tc_ld32(col + 32 * c, s);
+    tc_wait_ld32(s);
+    columns<true>(s, f, scale + 2 * c, mask >> (8 * c), seen - 32 * c);
+    const float *x = reinterpret_cast<const float *>(s);
+    if (to)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float g = fmaxf(f[q] * cs, 0x1p-126f);
+        *reinterpret_cast<float4 *>(to + 32 * c + 4 * q) =
+            make_float4(x[4 * q] * g, x[4 * q + 1] * g, x[4 * q + 2] * g, x[4 * q + 3] * g);
+      }
+    __syncwarp();
+  }
+}
+
 // What a softmax group knows of its item when the item, or the CTA's part of it, ends.
 struct Item {
   TcWalk w;
-  int64_t T, N, now, seg_first, first;
-  int rows, row;
+  int64_t T, N, now, first;   // now: the CTA's first step of the item
+  int count, rows, row;
   bool live, warp_live;
   float m, l;
   uint32_t o_col, tile, joins;   // tiles and joins of this group so far
@@ -488,21 +538,20 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   const TcWalk &w = it.w;
   const uint32_t tile = it.tile, joins = it.joins;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t T = it.T, N = it.N, now = it.now, seg_first = it.seg_first, first = it.first;
+  const int64_t T = it.T, N = it.N, first = it.first;
   const int rows = it.rows, row = it.row;
-  const bool live = it.live, warp_live = it.warp_live, seg_done = w.step + 1 == w.steps;
+  const bool live = it.live, warp_live = it.warp_live, whole = it.count == w.steps;
   const float m = it.m, l = it.l;
   const uint32_t o_col = it.o_col;
   // the result of the item, or this CTA's part of it
   if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) return false;
   tc_fence_after();
   const float back = 1.f / 128.f;   // V carries 2^7
-  const bool whole = seg_done && w.step + 1 <= now - seg_first + 1;
   const int64_t at = (int64_t)w.group * G_::ROWS + row;
   const int64_t tok = w.beg + at / a.G;
   const int hq = w.h * a.G + (int)(at % a.G);
   const int64_t part_size = p.part_size;
-  float *slot = p.partial + (((int64_t)blockIdx.x * 2 + (seg_first == first ? 0 : 1)) * G_::PARTS + (WIDE ? 0 : i)) *
+  float *slot = p.partial + (((int64_t)blockIdx.x * 2 + (it.now == first ? 0 : 1)) * G_::PARTS + (WIDE ? 0 : i)) *
                                 part_size;
   const bool direct = WIDE && whole;
   if (warp_live) {
@@ -554,7 +603,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&sh->join));
     if (!W.warp_wait(&sh->join, joins & 1)) return false;
-    const int64_t begin = now - w.step, end = begin + w.steps;   // the item's steps
+    const int64_t begin = it.now - w.step, end = begin + w.steps;   // the item's steps
     const int64_t c0 = ((begin + 1) * N - 1) / T, c1 = (end * N - 1) / T;
     bool mine = whole;
     if (!whole) {
@@ -702,7 +751,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (blockIdx.x == 0 && tid == 0) {
     raise(a.status, KVX_FLAG_BAD_SEQLENS);
   }
-  const int64_t count = last - first;
 
   if (warp < 8) {
     more_registers<kSoftmaxRegs>();
@@ -713,145 +761,106 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t s_col = tmem + lanes + i * kTile, o_col = tmem + lanes + 2 * kTile + i * kTile;
     const int row = (WIDE ? i * kTile : 0) + warp % 4 * 32 + lane;   // in the item
-    float m = -INFINITY, l = 0.f, cs = 0.f;
-    int limit = -1, floor_limit = -1, rows = 0;
-    bool live = false, warp_live = false, fresh_o = true;
-    uint32_t tile = 0, joins = 0;                 // tiles of this group, joins so far
-    int64_t seg_first = first;
-    bool enter = true;
-    for (int64_t now = first; now < last; ++now) {
-      if (enter) {
-        enter = false;
-        seg_first = now;
-        rows = (int)min((int64_t)G_::ROWS, (int64_t)w.fresh * a.G - (int64_t)w.group * G_::ROWS);
-        live = row < rows;
-        warp_live = row - lane < rows;
-        const int64_t at = (int64_t)w.group * G_::ROWS + row;         // row of the request and head
-        const int64_t tok = at / a.G;
-        limit = live ? (int)(w.len - w.fresh + tok) : -1;
-        // the lowest limit of the warp's rows (dead ones do not matter)
-        floor_limit = (int)(w.len - w.fresh + (at - lane) / a.G);
-        m = -INFINITY;
-        l = 0.f;
-        fresh_o = true;
-        if (WIDE || i == 0) {
-          const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
-                                     (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
-          cs = put_query(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), row % kTile);
-          fence_async_proxy();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[i]));
-        } else {
-          // the other group writes the rows; their factors are formed again
-          const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
-                                     (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
-          float top = 0.f;
-          if (live)
-#pragma unroll 16
-            for (int e = 0; e < kD; ++e) top = fmaxf(top, fabsf(__bfloat162float(src[e])));
-          cs = row_factor(a, top, pow2_scale(top));
-        }
+    uint32_t tile = 0, joins = 0;                 // tiles of this group and joins so far
+    int ks = WIDE ? 0 : i;                        // the tile's K stage, and its phase
+    uint32_t k_phase = 0;
+    for (int64_t now = first; now < last;) {
+      const int count = (int)min((int64_t)(w.steps - w.step), last - now);
+      const int rows = (int)min((int64_t)G_::ROWS, (int64_t)w.fresh * a.G - (int64_t)w.group * G_::ROWS);
+      const bool live = row < rows, warp_live = row - lane < rows;
+      const int64_t at = (int64_t)w.group * G_::ROWS + row;         // row of the request and head
+      const int64_t tok = at / a.G;
+      const int limit = live ? (int)(w.len - w.fresh + tok) : -1;   // last slot seen
+      const int floor_limit = (int)(w.len - w.fresh + (at - lane) / a.G);   // the lowest of the warp's live rows
+      const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
+                                 (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
+      float m = -INFINITY, l = 0.f, cs;
+      if (WIDE || i == 0) {
+        cs = put_query(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), row % kTile);
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[i]));
+      } else {
+        // the other group writes the rows; their factors are formed again
+        cs = query_factor(a, p.vec_q, src, live);
       }
-      // this group's tile of the step
-      const uint32_t n = WIDE ? (uint32_t)(now - first) : (uint32_t)(2 * (now - first) + i);   // of the CTA
-      const int ks = n % kKStages;
-      const int j0 = w.step * G_::SLOTS + (WIDE ? 0 : i * kTile);
-      if (!W.warp_wait(&sh->k_full[ks], n / kKStages & 1)) goto done;
-      if (!W.warp_wait(&sh->s_full[i], tile & 1)) goto done;
-      tc_fence_after();
-      if (warp_live) {
-        const uint32_t mask = sh->k_mask[ks];
-        const bool masked = mask != ~0u || j0 + kTile - 1 > floor_limit;
-        const float4 *scale = reinterpret_cast<const float4 *>(sh->ks[ks]);
-        if (!WIDE && p.scores) {     // the scores themselves, for the weights
-          float *to = live && j0 < p.score_ld
-                          ? p.scores + (((int64_t)w.r * a.H + w.h) * p.slot_rows + row) * p.score_ld + j0
-                          : nullptr;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t s[32];
-            tc_ld32(s_col + 32 * c, s);
-            tc_wait_ld();
-            scale_columns<true>(s, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c));
-            if (to)
-#pragma unroll
-              for (int q = 0; q < 32; q += 4)
-                *reinterpret_cast<float4 *>(to + 32 * c + q) =
-                    make_float4(__uint_as_float(s[q]) * cs, __uint_as_float(s[q + 1]) * cs,
-                                __uint_as_float(s[q + 2]) * cs, __uint_as_float(s[q + 3]) * cs);
-            __syncwarp();
-          }
-        }
-        const float ref = sh->k_ref[ks];
-        uint32_t sa[32], sb[32];
-        tc_ld32(s_col, sa);
-        // the maximum of the tile's scores
-        float top = -INFINITY;
-        if (masked)
-          top = walk_columns<true>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], float top) {
-            return peak_of<true>(s, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), top);
-          }, top);
-        else
-          top = walk_columns<true>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], float top) {
-            return peak_of<false>(s, scale + 2 * c, 0u, 0, top);
-          }, top);
-        const float peak = top * cs + ref;      // -inf where nothing is seen
-        const bool over = peak > m + kSlack || (m == -INFINITY && peak > -INFINITY);
-        if (__any_sync(~0u, over)) {
-          // seldom: raise the rows' maxima, scale down what they have
-          const float mm = fmaxf(m, peak), down = ex2(m - finite_or_0(mm));
-          if (!fresh_o) {
+      float *spool = !WIDE && p.scores && live
+                         ? p.scores + (((int64_t)w.r * a.H + w.h) * p.slot_rows + row) * p.score_ld
+                         : nullptr;
+      int j0 = w.step * G_::SLOTS + (WIDE ? 0 : i * kTile);
+      for (int s = 0; s < count; ++s) {
+        if (!W.warp_wait(&sh->k_full[ks], k_phase)) goto done;
+        if (!W.warp_wait(&sh->s_full[i], tile & 1)) goto done;
+        tc_fence_after();
+        if (warp_live) {
+          const uint32_t mask = sh->k_mask[ks];
+          const bool masked = mask != ~0u || j0 + kTile - 1 > floor_limit;
+          const float4 *scale = reinterpret_cast<const float4 *>(sh->ks[ks]);
+          const float ref = sh->k_ref[ks];
+          if (!WIDE && p.scores)     // the scores themselves, for the weights
+            keep_scores(s_col, spool && j0 < p.score_ld ? spool + j0 : nullptr, scale, mask, limit - j0, cs);
+          uint32_t sa[32], sb[32];
+          tc_ld32(s_col, sa);
+          float top = -INFINITY;
+          if (masked)
+            top = walk_columns<true>(s_col, sa, sb, [&](int c, uint32_t (&x)[32], float top) {
+              return peak_of<true>(x, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), top);
+            }, top);
+          else
+            top = walk_columns<true>(s_col, sa, sb, [&](int c, uint32_t (&x)[32], float top) {
+              return peak_of<false>(x, scale + 2 * c, 0u, 0, top);
+            }, top);
+          const float peak = top * cs + ref;      // -inf where nothing is seen
+          const bool over = peak > m + kSlack || (m == -INFINITY && peak > -INFINITY);
+          if (__any_sync(~0u, over)) {
+            // seldom: raise the rows' maxima, scale down what they have
+            const float mm = fmaxf(m, peak), down = ex2(m - finite_or_0(mm));
             tc_wait_ld32(sa);
-            if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) goto done;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tc_ld32(o_col + 32 * c, o);
-              tc_wait_ld32(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
-              tc_st32(o_col + 32 * c, o);
+            if (s > 0) {
+              if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) goto done;
+              tc_fence_after();
+              scale_down(o_col, down);
             }
+            m = mm;
+            l *= down;
           }
-          m = mm;
-          l *= down;
+          // probabilities, packed over the scores that are spent
+          const float add = kBias + ref - finite_or_0(m);
+          const uint64_t add2_ = pair(add, add);
+          uint64_t sum = pair(0.f, 0.f);
+          if (masked)
+            sum = walk_columns<false>(s_col, sa, sb, [&](int c, uint32_t (&x)[32], uint64_t sum) {
+              return probabilities<true>(s_col + 16 * c, x, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), cs, add2_, sum);
+            }, sum);
+          else
+            sum = walk_columns<false>(s_col, sa, sb, [&](int c, uint32_t (&x)[32], uint64_t sum) {
+              return probabilities<false>(s_col + 16 * c, x, scale + 2 * c, 0u, 0, cs, add2_, sum);
+            }, sum);
+          float s0, s1;
+          unpair(sum, s0, s1);
+          l += (s0 + s1) * ex2(-ref);    // without the value scale
+          tc_wait_st();
         }
-        // probabilities, packed over the scores that are spent
-        const uint64_t cs2 = pair(cs, cs);
-        const float add = kBias + ref - finite_or_0(m);
-        const uint64_t nm2 = pair(add, add);
-        uint64_t sum2 = pair(0.f, 0.f);
-        if (masked)
-          sum2 = walk_columns<false>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], uint64_t sum2) {
-            return probabilities<true>(s_col + 16 * c, s, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), cs2, nm2, sum2);
-          }, sum2);
-        else
-          sum2 = walk_columns<false>(s_col, sa, sb, [&](auto, int c, uint32_t (&s)[32], uint64_t sum2) {
-            return probabilities<false>(s_col + 16 * c, s, scale + 2 * c, 0u, 0, cs2, nm2, sum2);
-          }, sum2);
-        float s0, s1;
-        unpair(sum2, s0, s1);
-        l += (s0 + s1) * ex2(-ref);    // without the value scale
-        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&sh->p_full[i]));
+          mbar_arrive(smem_addr(&sh->k_empty[ks]));
+        }
+        ++tile;
+        j0 += G_::SLOTS;
+        ks += WIDE ? 1 : 2;
+        if (ks >= kKStages) {
+          ks -= kKStages;
+          k_phase ^= 1;
+        }
       }
-      fresh_o = false;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_addr(&sh->p_full[i]));
-        mbar_arrive(smem_addr(&sh->k_empty[ks]));
-      }
-      ++tile;
-
-      const bool seg_done = w.step + 1 == w.steps;
-      if (seg_done || now + 1 == last) {
-        enter = true;
-        const Item it{w, T, N, now, seg_first, first, rows, row, live, warp_live, m, l, o_col, tile, joins};
-        if (!finish_item<WIDE>(p, sh, it, i)) goto done;
-        joins += !WIDE || !seg_done || now - seg_first + 1 < w.steps;
-      }
-      advance<WIDE>(a, w);
+      // the result of the item, or this CTA's part of it
+      const Item it{w, T, N, now, first, count, rows, row, live, warp_live, m, cs != cs ? cs : l, o_col, tile, joins};
+      if (!finish_item<WIDE>(p, sh, it, i)) goto done;
+      joins += !WIDE || count < w.steps;
+      now += count;
+      next_item<WIDE>(a, w);
     }
   done:;
   } else if (warp < kLoadWarp) {
@@ -861,10 +870,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------------------
     const int t = tid - 8 * 32;
     uint32_t n = 0;
-    for (int64_t now = first; now < last; ++now) {
-      for (int k = 0; k < (WIDE ? 1 : 2); ++k, ++n) {
+    for (int64_t now = first; now < last;) {
+      const int count = (int)min((int64_t)(w.steps - w.step), last - now);
+      int j0 = w.step * G_::SLOTS;
+      for (int k = 0; k < count * (WIDE ? 1 : 2); ++k, ++n, j0 += kTile) {
         const int vs = n % kVStages, ws = n % kWStages;
-        const int j0 = w.step * G_::SLOTS + k * kTile;
         if (!W.warp_wait(&sh->v_full[vs], n / kVStages & 1)) goto cv_done;
         if (!W.warp_wait(&sh->w_empty[ws], (n / kWStages & 1) ^ 1)) goto cv_done;
         const unsigned char *src = vbuf + vs * kTileBytes;
@@ -896,7 +906,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_addr(&sh->v_empty[vs]));
         }
       }
-      advance<WIDE>(a, w);
+      now += count;
+      next_item<WIDE>(a, w);
     }
   cv_done:;
   } else if (warp == kLoadWarp) {
@@ -905,10 +916,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // block lookups, scales and TMA: lane l looks up slots 4l .. 4l + 3
     // ----------------------------------------------------------------------
     uint32_t n = 0;
-    for (int64_t now = first; now < last; ++now) {
-      for (int k = 0; k < (WIDE ? 1 : 2); ++k, ++n) {
+    for (int64_t now = first; now < last;) {
+      const int count = (int)min((int64_t)(w.steps - w.step), last - now);
+      int j = w.step * G_::SLOTS + 4 * lane;
+      for (int k = 0; k < count * (WIDE ? 1 : 2); ++k, ++n, j += kTile) {
         const int ks = n % kKStages, vs = n % kVStages;
-        const int j = w.step * G_::SLOTS + k * kTile + 4 * lane;
         int page = -1;
         uint32_t off = 0;
         if (j < w.len) {
@@ -954,7 +966,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       smem_addr(&sh->v_full[vs]));
         if (lane != 0) mbar_arrive(smem_addr(&sh->v_full[vs]));
       }
-      advance<WIDE>(a, w);
+      now += count;
+      next_item<WIDE>(a, w);
     }
   ld_done:
     // drain: the tiles that were asked for have landed (n counts whole tiles; after
@@ -972,16 +985,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------------------
     if (lane == 0) {
       const uint64_t q0 = sw128_desc(smem_addr(qbuf)), k0 = sw128_desc(smem_addr(kbuf)), v0 = mn_desc(smem_addr(wbuf));
-      TcWalk ahead = w;                // of the scores; w is the products with V's
-      uint32_t items = 0;              // items whose scores were begun
-      bool enter = true, issued = false, add = false;
-      // scores of step s of this CTA, group i
-      const auto scores = [&](int64_t s, int i) {
-        const uint32_t n = WIDE ? (uint32_t)s : (uint32_t)(2 * s + i);
-        if (i == 0 && enter) ++items;
-        if (WIDE || i == 0) {
-          if (enter && !W.wait(&sh->q_full[i], (items - 1) & 1)) return false;
-        }
+      bool ok = true, issued = false;
+      uint32_t items = 0, n = 0, step = 0;   // items, tiles whose scores were begun; steps of the products
+      // a group's scores of the next tile
+      const auto scores = [&](int i) {
         if (!W.wait(&sh->k_full[n % kKStages], n / kKStages & 1)) return false;
         tc_fence_after();
         mma_qk(tmem + i * kTile, q0 + (WIDE ? (uint64_t)i * (2 * kTileBytes >> 4) : 0),
@@ -989,30 +996,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         issued = true;
         commit(&sh->s_full[i]);
         if (!WIDE || i == 1) commit(&sh->k_empty[n % kKStages]);
-        if (i == 1) {
-          enter = ahead.step + 1 == ahead.steps;
-          advance<WIDE>(a, ahead);
-        }
+        if (!WIDE || i == 1) ++n;
         return true;
       };
-      bool ok = count > 0 && scores(0, 0) && scores(0, 1);
-      for (int64_t s = 0; ok && s < count; ++s) {
-        // a group's next scores follow its products at once, but where an item
-        // ends both groups finish it first: they join before they bring new queries
-        const bool more = s + 1 < count, item_ends = enter;
+      for (int64_t now = first; ok && now < last;) {
+        const int count = (int)min((int64_t)(w.steps - w.step), last - now);
+        // The scores of an item begin after all products of the one before: both
+        // groups finish that first, they join before they bring new queries.
         for (int i = 0; ok && i < 2; ++i) {
-          const uint32_t n = WIDE ? (uint32_t)s : (uint32_t)(2 * s + i);
-          ok = W.wait(&sh->p_full[i], s & 1) && W.wait(&sh->w_full[n % kWStages], n / kWStages & 1);
-          if (!ok) break;
-          tc_fence_after();
-          mma_pv(tmem + 2 * kTile + i * kTile, tmem + i * kTile, v0 + (uint64_t)(n % kWStages) * (2 * kTileBytes >> 4), add);
-          commit(&sh->pv_done[i]);
-          if (!WIDE || i == 1) commit(&sh->w_empty[n % kWStages]);
-          if (more && !item_ends) ok = scores(s + 1, i);
+          if (WIDE || i == 0) ok = W.wait(&sh->q_full[i], items & 1);
+          ok = ok && scores(i);
         }
-        if (ok && more && item_ends) ok = scores(s + 1, 0) && scores(s + 1, 1);
-        add = w.step + 1 != w.steps;
-        advance<WIDE>(a, w);
+        ++items;
+        for (int s = 0; ok && s < count; ++s, ++step) {
+          for (int i = 0; ok && i < 2; ++i) {
+            const uint32_t v = WIDE ? step : 2 * step + i;
+            ok = W.wait(&sh->p_full[i], step & 1) && W.wait(&sh->w_full[v % kWStages], v / kWStages & 1);
+            if (!ok) break;
+            tc_fence_after();
+            mma_pv(tmem + 2 * kTile + i * kTile, tmem + i * kTile, v0 + (uint64_t)(v % kWStages) * (2 * kTileBytes >> 4),
+                   s > 0);
+            commit(&sh->pv_done[i]);
+            if (!WIDE || i == 1) commit(&sh->w_empty[v % kWStages]);
+            if (s + 1 < count) ok = scores(i);   // a group's next scores follow its products at once
+          }
+        }
+        now += count;
+        next_item<WIDE>(a, w);
       }
       if (issued) {
         commit(&sh->drain);
