@@ -14,7 +14,7 @@
 // 2^8 times what it would with the true one before the sums are scaled down.
 //
 // Roles: warps 0-3 and 4-7 two softmax groups, warps 8-11 convert V, warp 12
-// loads (block lookups, scales, TMA), warp 13 issues the MMAs.  WIDE: the groups
+// loads (block lookups, scales, TMA), warps 13 and 14 issue the groups' MMAs.  WIDE: the groups
 // take the two 128-row halves of 256 rows, over the same slot tiles.  Narrow
 // (at most 128 rows): they take the even and the odd slot tiles of the same
 // rows, so that one tile's softmax overlaps the other's products.
@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kD = 128;             // head_dim
 constexpr int kTile = 128;          // slots and rows of a tile
+constexpr int kHalf = kTile / 2;   // slots whose scores and products are formed at a time
 constexpr int kTileBytes = kTile * kD;
 constexpr int kKStages = 3, kVStages = 2, kWStages = 2;
 constexpr int kLoadWarp = 12, kMmaWarp = 13, kThreads = 16 * 32;
@@ -55,8 +56,10 @@ struct TcShared {
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t w_full[kWStages], w_empty[kWStages];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
-  uint64_t join, verdict, drain;
+  // [group][half of the tile]; a wait on one names a phase whose predecessor is
+  // known to be over, so its parity is enough
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2];
+  uint64_t join, verdict, drain[2];
   uint32_t tmem_base;
   volatile int abort;
   volatile int last;
@@ -229,39 +232,49 @@ __device__ int64_t walk_at(const AttendParams &a, int64_t at, TcWalk &w) {
 }
 
 // --- tcgen05 ---------------------------------------------------------------------
-// Instruction descriptors: D fp32, M = N = 128; e4m3 x e4m3 both K-major, and f16 x
-// f16 with B as it lies in memory, [K][N] (MN-major).
-constexpr uint32_t kIdescQK = (1u << 4) | (16u << 17) | (8u << 24);
+// Instruction descriptors: D fp32, M = 128; e4m3 x e4m3 both K-major, N = 64, and f16
+// x f16 with B as it lies in memory, [K][N] (MN-major), N = 128.
+constexpr uint32_t kIdescQK = (1u << 4) | (8u << 17) | (8u << 24);
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | (16u << 17) | (8u << 24);
 
-// S = (Q1 + Q2) K^T: two parts of four 32-deep steps.
+// The whole warp calls these, with the same arguments (which stay in uniform
+// registers); one elected lane issues.
+// S = (Q1 + Q2) K^T for 64 slots: two parts of four 32-deep steps.
 __device__ __forceinline__ void mma_qk(uint32_t d, uint64_t q, uint64_t k) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint64_t a = q + (i / 4) * (kTileBytes >> 4) + (i % 4) * 2, b = k + (i % 4) * 2;
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(kIdescQK), "r"(i)
-        : "memory");
-  }
+  asm volatile(
+      "{\n.reg .pred e, f, t;\n.reg .b32 r;\n.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3;\n"
+      "elect.sync r|e, 0xffffffff;\n"
+      "setp.ne.u32 f, 0, 0;\nsetp.eq.u32 t, 0, 0;\n"
+      "add.u64 a1, %1, 2; add.u64 a2, %1, 4; add.u64 a3, %1, 6; add.u64 a4, %1, %4;\n"
+      "add.u64 a5, a4, 2; add.u64 a6, a4, 4; add.u64 a7, a4, 6;\n"
+      "add.u64 b1, %2, 2; add.u64 b2, %2, 4; add.u64 b3, %2, 6;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a4, %2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a5, b1, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a6, b2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a7, b3, %3, t;\n}\n" ::"r"(d),
+      "l"(q), "l"(k), "r"(kIdescQK), "l"((uint64_t)(kTileBytes >> 4))
+      : "memory");
 }
-// O (+)= P V: eight 16-deep steps; P 8 columns on, V 16 slots (2 KB) on.
+// O (+)= P V for 64 slots: four 16-deep steps; P 8 columns on, V 16 slots (2 KB) on.
 __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, bool add) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(p + 8 * i), "l"(v + (uint64_t)i * (2048 >> 4)), "r"(kIdescPV), "r"((uint32_t)(add || i > 0))
-        : "memory");
-  }
+  asm volatile(
+      "{\n.reg .pred e, f, t;\n.reg .b32 r, a1, a2, a3;\n.reg .b64 b1, b2, b3;\n"
+      "elect.sync r|e, 0xffffffff;\n"
+      "setp.ne.u32 f, %4, 0;\nsetp.eq.u32 t, 0, 0;\n"
+      "add.u32 a1, %1, 8; add.u32 a2, %1, 16; add.u32 a3, %1, 24;\n"
+      "add.u64 b1, %2, 128; add.u64 b2, %2, 256; add.u64 b3, %2, 384;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d),
+      "r"(p), "l"(v), "r"(kIdescPV), "r"((uint32_t)add)
+      : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_addr(bar))
-               : "memory");
-}
+__device__ __forceinline__ void commit(uint64_t *bar) { tc_commit_elect<1>(smem_addr(bar)); }
 // [K][N] operand of 16-bit values, 128-byte swizzle: 64-column groups 16 KB
 // apart (leading offset), 8-row groups 1 KB apart (stride offset).
 __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
@@ -409,20 +422,16 @@ __device__ __forceinline__ uint64_t probabilities(uint32_t to, uint32_t (&s)[32]
   tc_st16(to, out);
   return sum;
 }
-// f over the tile's columns, 32 at a time, the next ones on their way.  The first
-// 32 are in `a` already (asked for); AGAIN: they are asked for again at the end.
+// f over 64 columns, 32 at a time, the next ones on their way.  The first 32 are
+// in `a` already (asked for); AGAIN: they are asked for again at the end.
 template <bool AGAIN, class F, class T>
 __device__ __forceinline__ T walk_columns(uint32_t col, uint32_t (&a)[32], uint32_t (&b)[32], F f, T acc) {
-#pragma unroll 1
-  for (int c = 0; c < 4; c += 2) {
-    tc_wait_ld32(a);
-    tc_ld32(col + 32 * (c + 1), b);
-    acc = f(c, a, acc);
-    tc_wait_ld32(b);
-    if (c == 0 || AGAIN) tc_ld32(col + (c == 0 ? 64 : 0), a);
-    acc = f(c + 1, b, acc);
-  }
-  return acc;
+  tc_wait_ld32(a);
+  tc_ld32(col + 32, b);
+  acc = f(0, a, acc);
+  tc_wait_ld32(b);
+  if (AGAIN) tc_ld32(col, a);
+  return f(1, b, acc);
 }
 // A row's 128 elements, packed as they lie (zeros for a dead row).
 __device__ __forceinline__ void load_query(const __nv_bfloat16 *src, bool vec, bool live, uint32_t (&x)[kD / 2]) {
@@ -497,10 +506,10 @@ __device__ __noinline__ void scale_down(uint32_t col, float down) {
     tc_st32(col + 32 * c, o);
   }
 }
-// The tile's scores, base 2, to a row of 128 (NULL: only take part).
+// 64 scores, base 2, to a row (NULL: only take part).
 __device__ __noinline__ void keep_scores(uint32_t col, float *to, const float4 *scale, uint32_t mask, int seen, float cs) {
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 2; ++c) {
     uint32_t s[32];
     float f[8];
     tc_ld32(col + 32 * c, s);
@@ -525,7 +534,7 @@ struct Item {
   int count, rows, row;
   bool live, warp_live;
   float m, l;
-  uint32_t o_col, tile, joins;   // tiles and joins of this group so far
+  uint32_t o_col, half, joins;   // half tiles and joins of this group so far
 };
 // Write the result of the item, or leave this CTA's part of it and let the last to
 // come join the parts.  Seldom, and apart from the loop so that it costs that no
@@ -536,7 +545,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   const AttendParams &a = p.a;
   const Waiter W{sh, a.status};
   const TcWalk &w = it.w;
-  const uint32_t tile = it.tile, joins = it.joins;
+  const uint32_t half = it.half, joins = it.joins;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t T = it.T, N = it.N, first = it.first;
   const int rows = it.rows, row = it.row;
@@ -544,7 +553,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   const float m = it.m, l = it.l;
   const uint32_t o_col = it.o_col;
   // the result of the item, or this CTA's part of it
-  if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) return false;
+  if (!W.warp_wait(&sh->pv_done[i][(half - 1) & 1], (half - 1) >> 1 & 1)) return false;
   tc_fence_after();
   const float back = 1.f / 128.f;   // V carries 2^7
   const int64_t at = (int64_t)w.group * G_::ROWS + row;
@@ -700,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(smem_addr(&sh->k_full[i]), 32);
-      mbar_init(smem_addr(&sh->k_empty[i]), 1 + (WIDE ? 8 : 4));
+      mbar_init(smem_addr(&sh->k_empty[i]), WIDE ? 2 + 8 : 1 + 4);
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(smem_addr(&sh->v_full[i]), 32);
@@ -708,17 +717,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kWStages; ++i) {
       mbar_init(smem_addr(&sh->w_full[i]), 4);
-      mbar_init(smem_addr(&sh->w_empty[i]), 1);
+      mbar_init(smem_addr(&sh->w_empty[i]), WIDE ? 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh->q_full[i]), 4);
-      mbar_init(smem_addr(&sh->s_full[i]), 1);
-      mbar_init(smem_addr(&sh->p_full[i]), 4);
-      mbar_init(smem_addr(&sh->pv_done[i]), 1);
+      mbar_init(smem_addr(&sh->drain[i]), 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(smem_addr(&sh->s_full[i][h]), 1);
+        mbar_init(smem_addr(&sh->p_full[i][h]), 4);
+        mbar_init(smem_addr(&sh->pv_done[i][h]), 1);
+      }
     }
     mbar_init(smem_addr(&sh->join), 8);
     mbar_init(smem_addr(&sh->verdict), 1);
-    mbar_init(smem_addr(&sh->drain), 1);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -761,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t s_col = tmem + lanes + i * kTile, o_col = tmem + lanes + 2 * kTile + i * kTile;
     const int row = (WIDE ? i * kTile : 0) + warp % 4 * 32 + lane;   // in the item
-    uint32_t tile = 0, joins = 0;                 // tiles of this group and joins so far
+    uint32_t half = 0, joins = 0;                 // half tiles of this group and joins so far
     int ks = WIDE ? 0 : i;                        // the tile's K stage, and its phase
     uint32_t k_phase = 0;
     for (int64_t now = first; now < last;) {
@@ -788,26 +799,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                          ? p.scores + (((int64_t)w.r * a.H + w.h) * p.slot_rows + row) * p.score_ld
                          : nullptr;
       int j0 = w.step * G_::SLOTS + (WIDE ? 0 : i * kTile);
-      for (int s = 0; s < count; ++s) {
-        if (!W.warp_wait(&sh->k_full[ks], k_phase)) goto done;
-        if (!W.warp_wait(&sh->s_full[i], tile & 1)) goto done;
+      for (int s = 0; s < 2 * count; ++s, ++half) {
+        const int hf = s & 1;                     // half of the tile
+        const uint32_t col = s_col + hf * kHalf;
+        if (hf == 0 && !W.warp_wait(&sh->k_full[ks], k_phase)) goto done;
+        if (!W.warp_wait(&sh->s_full[i][hf], half >> 1 & 1)) goto done;
         tc_fence_after();
         if (warp_live) {
-          const uint32_t mask = sh->k_mask[ks];
-          const bool masked = mask != ~0u || j0 + kTile - 1 > floor_limit;
-          const float4 *scale = reinterpret_cast<const float4 *>(sh->ks[ks]);
+          const uint32_t mask = sh->k_mask[ks] >> (16 * hf) & 0xffffu;
+          const bool masked = mask != 0xffffu || j0 + kHalf - 1 > floor_limit;
+          const float4 *scale = reinterpret_cast<const float4 *>(sh->ks[ks]) + 4 * hf;
           const float ref = sh->k_ref[ks];
           if (!WIDE && p.scores)     // the scores themselves, for the weights
-            keep_scores(s_col, spool && j0 < p.score_ld ? spool + j0 : nullptr, scale, mask, limit - j0, cs);
+            keep_scores(col, spool && j0 < p.score_ld ? spool + j0 : nullptr, scale, mask, limit - j0, cs);
           uint32_t sa[32], sb[32];
-          tc_ld32(s_col, sa);
+          tc_ld32(col, sa);
           float top = -INFINITY;
           if (masked)
-            top = walk_columns<true>(s_col, sa, sb, [&](int c, uint32_t (&x)[32], float top) {
+            top = walk_columns<true>(col, sa, sb, [&](int c, uint32_t (&x)[32], float top) {
               return peak_of<true>(x, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), top);
             }, top);
           else
-            top = walk_columns<true>(s_col, sa, sb, [&](int c, uint32_t (&x)[32], float top) {
+            top = walk_columns<true>(col, sa, sb, [&](int c, uint32_t (&x)[32], float top) {
               return peak_of<false>(x, scale + 2 * c, 0u, 0, top);
             }, top);
           const float peak = top * cs + ref;      // -inf where nothing is seen
@@ -817,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float mm = fmaxf(m, peak), down = ex2(m - finite_or_0(mm));
             tc_wait_ld32(sa);
             if (s > 0) {
-              if (!W.warp_wait(&sh->pv_done[i], (tile - 1) & 1)) goto done;
+              if (!W.warp_wait(&sh->pv_done[i][(half - 1) & 1], (half - 1) >> 1 & 1)) goto done;
               tc_fence_after();
               scale_down(o_col, down);
             }
@@ -829,12 +842,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t add2_ = pair(add, add);
           uint64_t sum = pair(0.f, 0.f);
           if (masked)
-            sum = walk_columns<false>(s_col, sa, sb, [&](int c, uint32_t (&x)[32], uint64_t sum) {
-              return probabilities<true>(s_col + 16 * c, x, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), cs, add2_, sum);
+            sum = walk_columns<false>(col, sa, sb, [&](int c, uint32_t (&x)[32], uint64_t sum) {
+              return probabilities<true>(col + 16 * c, x, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), cs, add2_, sum);
             }, sum);
           else
-            sum = walk_columns<false>(s_col, sa, sb, [&](int c, uint32_t (&x)[32], uint64_t sum) {
-              return probabilities<false>(s_col + 16 * c, x, scale + 2 * c, 0u, 0, cs, add2_, sum);
+            sum = walk_columns<false>(col, sa, sb, [&](int c, uint32_t (&x)[32], uint64_t sum) {
+              return probabilities<false>(col + 16 * c, x, scale + 2 * c, 0u, 0, cs, add2_, sum);
             }, sum);
           float s0, s1;
           unpair(sum, s0, s1);
@@ -843,20 +856,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_addr(&sh->p_full[i]));
-          mbar_arrive(smem_addr(&sh->k_empty[ks]));
-        }
-        ++tile;
-        j0 += G_::SLOTS;
-        ks += WIDE ? 1 : 2;
-        if (ks >= kKStages) {
-          ks -= kKStages;
-          k_phase ^= 1;
+        if (lane == 0) mbar_arrive(smem_addr(&sh->p_full[i][hf]));
+        j0 += kHalf;
+        if (hf) {
+          if (lane == 0) mbar_arrive(smem_addr(&sh->k_empty[ks]));
+          j0 += G_::SLOTS - kTile;
+          ks += WIDE ? 1 : 2;
+          if (ks >= kKStages) {
+            ks -= kKStages;
+            k_phase ^= 1;
+          }
         }
       }
       // the result of the item, or this CTA's part of it
-      const Item it{w, T, N, now, first, count, rows, row, live, warp_live, m, cs != cs ? cs : l, o_col, tile, joins};
+      const Item it{w, T, N, now, first, count, rows, row, live, warp_live, m, cs != cs ? cs : l, o_col, half, joins};
       if (!finish_item<WIDE>(p, sh, it, i)) goto done;
       joins += !WIDE || count < w.steps;
       now += count;
@@ -978,56 +991,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t x = n > kVStages ? n - kVStages : 0; x < n; ++x) drain_wait(&sh->v_full[x % kVStages], x / kVStages & 1);
       if (sh->abort) drain_wait(&sh->k_full[n % kKStages], n / kKStages & 1);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp < kMmaWarp + 2) {
     fewer_registers<kOtherRegs>();
     // ----------------------------------------------------------------------
-    // the MMAs, from one thread
+    // the MMAs: a warp for each group, so that one's waits hide behind the
+    // other's products
     // ----------------------------------------------------------------------
-    if (lane == 0) {
-      const uint64_t q0 = sw128_desc(smem_addr(qbuf)), k0 = sw128_desc(smem_addr(kbuf)), v0 = mn_desc(smem_addr(wbuf));
-      bool ok = true, issued = false;
-      uint32_t items = 0, n = 0, step = 0;   // items, tiles whose scores were begun; steps of the products
-      // a group's scores of the next tile
-      const auto scores = [&](int i) {
-        if (!W.wait(&sh->k_full[n % kKStages], n / kKStages & 1)) return false;
+    const int i = warp - kMmaWarp;
+    const uint64_t q0 = sw128_desc(smem_addr(qbuf)) + (WIDE ? (uint64_t)i * (2 * kTileBytes >> 4) : 0);
+    const uint64_t k0 = sw128_desc(smem_addr(kbuf)), v0 = mn_desc(smem_addr(wbuf));
+    const uint32_t s_col = tmem + i * kTile, o_col = tmem + 2 * kTile + i * kTile;
+    uint32_t items = 0, u = 0;       // items, and the group's half tiles whose products were begun
+    bool ok = true, issued = false;
+    const auto tile_of = [&](uint32_t half) { return WIDE ? half >> 1 : (half >> 1) * 2 + i; };   // of the CTA
+    const auto scores = [&](uint32_t half) {
+      const uint32_t stage = tile_of(half) % kKStages, hf = half & 1;
+      if (!W.warp_wait(&sh->k_full[stage], tile_of(half) / kKStages & 1)) return false;
+      tc_fence_after();
+      mma_qk(s_col + hf * kHalf, q0, k0 + (uint64_t)(stage * kTileBytes + hf * kHalf * kD >> 4));
+      issued = true;
+      commit(&sh->s_full[i][hf]);
+      if (hf) commit(&sh->k_empty[stage]);
+      return true;
+    };
+    for (int64_t now = first; ok && now < last;) {
+      const int count = (int)min((int64_t)(w.steps - w.step), last - now);
+      ok = W.warp_wait(&sh->q_full[WIDE ? i : 0], items & 1) && scores(u) && scores(u + 1);
+      ++items;
+      for (int s = 0; ok && s < 2 * count; ++s, ++u) {
+        const uint32_t stage = tile_of(u) % kWStages, hf = u & 1;
+        ok = W.warp_wait(&sh->w_full[stage], tile_of(u) / kWStages & 1) && W.warp_wait(&sh->p_full[i][hf], u >> 1 & 1);
+        if (!ok) break;
         tc_fence_after();
-        mma_qk(tmem + i * kTile, q0 + (WIDE ? (uint64_t)i * (2 * kTileBytes >> 4) : 0),
-               k0 + (uint64_t)(n % kKStages) * (kTileBytes >> 4));
-        issued = true;
-        commit(&sh->s_full[i]);
-        if (!WIDE || i == 1) commit(&sh->k_empty[n % kKStages]);
-        if (!WIDE || i == 1) ++n;
-        return true;
-      };
-      for (int64_t now = first; ok && now < last;) {
-        const int count = (int)min((int64_t)(w.steps - w.step), last - now);
-        // The scores of an item begin after all products of the one before: both
-        // groups finish that first, they join before they bring new queries.
-        for (int i = 0; ok && i < 2; ++i) {
-          if (WIDE || i == 0) ok = W.wait(&sh->q_full[i], items & 1);
-          ok = ok && scores(i);
-        }
-        ++items;
-        for (int s = 0; ok && s < count; ++s, ++step) {
-          for (int i = 0; ok && i < 2; ++i) {
-            const uint32_t v = WIDE ? step : 2 * step + i;
-            ok = W.wait(&sh->p_full[i], step & 1) && W.wait(&sh->w_full[v % kWStages], v / kWStages & 1);
-            if (!ok) break;
-            tc_fence_after();
-            mma_pv(tmem + 2 * kTile + i * kTile, tmem + i * kTile, v0 + (uint64_t)(v % kWStages) * (2 * kTileBytes >> 4),
-                   s > 0);
-            commit(&sh->pv_done[i]);
-            if (!WIDE || i == 1) commit(&sh->w_empty[v % kWStages]);
-            if (s + 1 < count) ok = scores(i);   // a group's next scores follow its products at once
-          }
-        }
-        now += count;
-        next_item<WIDE>(a, w);
+        mma_pv(o_col, s_col + hf * kHalf, v0 + (uint64_t)(stage * 2 * kTileBytes + hf * kHalf * kD >> 4), s > 0);
+        commit(&sh->pv_done[i][hf]);
+        if (hf) commit(&sh->w_empty[stage]);
+        // two halves on, over the probabilities just spent: MMAs run in order
+        if (s + 2 < 2 * count) ok = scores(u + 2);
       }
-      if (issued) {
-        commit(&sh->drain);
-        drain_wait(&sh->drain, 0);
-      }
+      now += count;
+      next_item<WIDE>(a, w);
+    }
+    if (issued) {
+      commit(&sh->drain[i]);
+      if (lane == 0) drain_wait(&sh->drain[i], 0);
     }
     __syncwarp();
   } else {
