@@ -386,52 +386,70 @@ __device__ __forceinline__ void columns(uint32_t (&s)[32], float (&f)[8], const 
   }
 }
 // The largest of the scaled scores and `top`.
-template <bool MASK>
-__device__ __forceinline__ float peak_of(uint32_t (&s)[32], const float4 *scale, uint32_t mask, int seen, float top) {
-  float f[8], u[8];
-  columns<MASK>(s, f, scale, mask, seen);
+__device__ __forceinline__ float peak_of(const uint32_t (&s)[32], const float (&f)[8], float top) {
+  const float *x = reinterpret_cast<const float *>(s);
+  float u[8];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float *x = reinterpret_cast<const float *>(s) + 4 * q;
-    u[q] = fmaxf(max3(x[0], x[1], x[2]), x[3]) * f[q];
-  }
+  for (int q = 0; q < 8; ++q) u[q] = fmaxf(max3(x[4 * q], x[4 * q + 1], x[4 * q + 2]), x[4 * q + 3]) * f[q];
   return max3(max3(top, max3(u[0], u[1], u[2]), max3(u[3], u[4], u[5])), u[6], u[7]);
 }
-// exp2(score f cs + add) in f16 to tensor memory, and their sum.
+// exp2(score f cs + add) in f16, two to a register, and their sum.
 template <bool MASK>
-__device__ __forceinline__ uint64_t probabilities(uint32_t to, uint32_t (&s)[32], const float4 *scale, uint32_t mask,
-                                                  int seen, float cs, uint64_t add, uint64_t sum) {
-  float f[8];
-  columns<MASK>(s, f, scale, mask, seen);
-  uint32_t out[16];
+__device__ __forceinline__ uint64_t probabilities(uint32_t *out, const uint32_t (&s)[32], const float (&f)[8], float cs,
+                                                  uint64_t add, uint64_t sum) {
+  const float *x = reinterpret_cast<const float *>(s);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     // not 0, which would make NaN of -inf
     const float g = MASK ? fmaxf(f[q] * cs, 0x1p-126f) : f[q] * cs;
     const uint64_t g2 = pair(g, g);
-    const float *x = reinterpret_cast<const float *>(s) + 4 * q;
     float y[4];
-    unpair(fma2(pair(x[0], x[1]), g2, add), y[0], y[1]);
-    unpair(fma2(pair(x[2], x[3]), g2, add), y[2], y[3]);
+    unpair(fma2(pair(x[4 * q], x[4 * q + 1]), g2, add), y[0], y[1]);
+    unpair(fma2(pair(x[4 * q + 2], x[4 * q + 3]), g2, add), y[2], y[3]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = ex2(y[e]);
     sum = add2(sum, add2(pair(y[0], y[1]), pair(y[2], y[3])));
     out[2 * q] = f16x2(y[0], y[1]);
     out[2 * q + 1] = f16x2(y[2], y[3]);
   }
-  tc_st16(to, out);
   return sum;
 }
-// f over 64 columns, 32 at a time, the next ones on their way.  The first 32 are
-// in `a` already (asked for); AGAIN: they are asked for again at the end.
-template <bool AGAIN, class F, class T>
-__device__ __forceinline__ T walk_columns(uint32_t col, uint32_t (&a)[32], uint32_t (&b)[32], F f, T acc) {
-  tc_wait_ld32(a);
+// A half tile of a row: probabilities over the scores they come from, the row's
+// running maximum (lazily) and sum.  `raise(down)` is called by whole warps when
+// a maximum has to rise: it scales down what the rows have so far.
+template <bool MASK, class F>
+__device__ __forceinline__ bool softmax_half(uint32_t col, const float4 *scale, uint32_t mask, int seen, float cs, float ref,
+                                             float &m, float &l, F raise) {
+  uint32_t a[32], b[32], out[32];
+  float fa[8], fb[8];
+  tc_ld32(col, a);
   tc_ld32(col + 32, b);
-  acc = f(0, a, acc);
+  tc_wait_ld32(a);
   tc_wait_ld32(b);
-  if (AGAIN) tc_ld32(col, a);
-  return f(1, b, acc);
+  columns<MASK>(a, fa, scale, mask, seen);
+  columns<MASK>(b, fb, scale + 2, mask >> 8, seen - 32);
+  float top = -INFINITY, s0, s1;
+#pragma unroll 1
+  while (true) {
+    const float add = kBias + ref - finite_or_0(m);
+    const uint64_t a2 = pair(add, add);
+    uint64_t sum = probabilities<MASK>(out, a, fa, cs, a2, pair(0.f, 0.f));
+    sum = probabilities<MASK>(out + 16, b, fb, cs, a2, sum);
+    top = peak_of(b, fb, peak_of(a, fa, top));
+    const float peak = top * cs + ref;      // -inf where nothing is seen
+    const bool over = peak > m + kSlack || (m == -INFINITY && peak > -INFINITY);
+    unpair(sum, s0, s1);
+    if (!__any_sync(~0u, over)) break;
+    // seldom: the probabilities again, with the rows' maxima raised
+    const float mm = fmaxf(m, peak), down = ex2(m - finite_or_0(mm));
+    if (!raise(down)) return false;
+    m = mm;
+    l *= down;
+  }
+  l += (s0 + s1) * ex2(-ref);    // without the value scale
+  tc_st32(col, out);
+  tc_wait_st();
+  return true;
 }
 // A row's 128 elements, packed as they lie (zeros for a dead row).
 __device__ __forceinline__ void load_query(const __nv_bfloat16 *src, bool vec, bool live, uint32_t (&x)[kD / 2]) {
@@ -812,47 +830,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float ref = sh->k_ref[ks];
           if (!WIDE && p.scores)     // the scores themselves, for the weights
             keep_scores(col, spool && j0 < p.score_ld ? spool + j0 : nullptr, scale, mask, limit - j0, cs);
-          uint32_t sa[32], sb[32];
-          tc_ld32(col, sa);
-          float top = -INFINITY;
-          if (masked)
-            top = walk_columns<true>(col, sa, sb, [&](int c, uint32_t (&x)[32], float top) {
-              return peak_of<true>(x, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), top);
-            }, top);
-          else
-            top = walk_columns<true>(col, sa, sb, [&](int c, uint32_t (&x)[32], float top) {
-              return peak_of<false>(x, scale + 2 * c, 0u, 0, top);
-            }, top);
-          const float peak = top * cs + ref;      // -inf where nothing is seen
-          const bool over = peak > m + kSlack || (m == -INFINITY && peak > -INFINITY);
-          if (__any_sync(~0u, over)) {
-            // seldom: raise the rows' maxima, scale down what they have
-            const float mm = fmaxf(m, peak), down = ex2(m - finite_or_0(mm));
-            tc_wait_ld32(sa);
-            if (s > 0) {
-              if (!W.warp_wait(&sh->pv_done[i][(half - 1) & 1], (half - 1) >> 1 & 1)) goto done;
-              tc_fence_after();
-              scale_down(o_col, down);
-            }
-            m = mm;
-            l *= down;
-          }
-          // probabilities, packed over the scores that are spent
-          const float add = kBias + ref - finite_or_0(m);
-          const uint64_t add2_ = pair(add, add);
-          uint64_t sum = pair(0.f, 0.f);
-          if (masked)
-            sum = walk_columns<false>(col, sa, sb, [&](int c, uint32_t (&x)[32], uint64_t sum) {
-              return probabilities<true>(col + 16 * c, x, scale + 2 * c, mask >> (8 * c), limit - (j0 + 32 * c), cs, add2_, sum);
-            }, sum);
-          else
-            sum = walk_columns<false>(col, sa, sb, [&](int c, uint32_t (&x)[32], uint64_t sum) {
-              return probabilities<false>(col + 16 * c, x, scale + 2 * c, 0u, 0, cs, add2_, sum);
-            }, sum);
-          float s0, s1;
-          unpair(sum, s0, s1);
-          l += (s0 + s1) * ex2(-ref);    // without the value scale
-          tc_wait_st();
+          const auto raise = [&](float down) {
+            if (s == 0) return true;
+            if (!W.warp_wait(&sh->pv_done[i][(half - 1) & 1], (half - 1) >> 1 & 1)) return false;
+            tc_fence_after();
+            scale_down(o_col, down);
+            return true;
+          };
+          if (!(masked ? softmax_half<true>(col, scale, mask, limit - j0, cs, ref, m, l, raise)
+                       : softmax_half<false>(col, scale, 0u, 0, cs, ref, m, l, raise)))
+            goto done;
         }
         tc_fence_before();
         __syncwarp();
