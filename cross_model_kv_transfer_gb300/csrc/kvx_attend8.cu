@@ -722,6 +722,7 @@ kvx_status check(const kvx_attend8_args *a) {
       a->q_heads > 65535 || a->q_heads % c.heads)
     return KVX_ERR_INVALID_ARG;
   if (a->weights && a->weights_stride < a->max_len) return KVX_ERR_INVALID_ARG;
+  if (a->weights && a->num_requests > 65535) return KVX_ERR_UNSUPPORTED;
   return KVX_OK;
 }
 
@@ -741,13 +742,14 @@ Shape shape_of(const kvx_attend8_args *a) {
   s.grid = kGrid;
   const int dp = a->cache.head_dim <= 64 ? 64 : a->cache.head_dim <= 128 ? 128 : 256;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  s.spool = a->weights && most <= 64;
+  // the scores of all columns, while they fit 4 GB (and a CTA's log-sum-exps 48 KB)
+  const size_t score_bytes = (size_t)a->num_requests * a->cache.heads * s.groups * a->max_len * s.cols * 4;
+  s.spool = a->weights && most <= 12288 && score_bytes <= (size_t)4 << 30;
   s.arrived = 0;
   s.partial = up((size_t)a->num_requests * a->cache.heads * s.groups * 4);
   s.lse = s.partial + up((size_t)2 * s.grid * s.cols * (dp + 2) * 4);
   s.scores = s.lse + up((size_t)a->ntok * a->q_heads * 4);
-  s.bytes = s.scores + (s.spool ? up((size_t)a->num_requests * a->cache.heads * s.groups * a->max_len * s.cols * 4)
-                                : 0);
+  s.bytes = s.scores + (s.spool ? up(score_bytes) : 0);
   return s;
 }
 
@@ -832,14 +834,7 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.c = a->scale * kLog2e;
   cudaStream_t s = (cudaStream_t)stream;
   char *ws = (char *)a->workspace;
-  if (kvx_attend8_tc_supports(a)) {
-    const kvx_status st = kvx_attend8_tc_launch(a, p, ws, s);
-    const bool wide = (int64_t)p.G * p.max_new > 128;
-    if (st != KVX_OK || !a->weights || a->max_len == 0 || !wide) return st;
-    if (!p.lse) return KVX_ERR_INVALID_ARG;
-    weights_kernel<<<dim3((a->max_len + 127) / 128, c.heads, a->num_requests), 128, 0, s>>>(p);
-    return launched();
-  }
+  if (kvx_attend8_tc_supports(a)) return kvx_attend8_tc_launch(a, p, ws, s);
   const Shape sh = shape_of(a);
   if (!p.lse) p.lse = (float *)(ws + sh.lse);
   SplitParams sp;

@@ -59,7 +59,7 @@ struct TcShared {
   // [group][half of the tile]; a wait on one names a phase whose predecessor is
   // known to be over, so its parity is enough
   uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2];
-  uint64_t join, verdict, drain[2];
+  uint64_t join, verdict, spent, drain[2];
   uint32_t tmem_base;
   volatile int abort;
   volatile int last;
@@ -87,8 +87,9 @@ struct TcParams {
   int vec_q, vec_out;
 };
 
-struct Waiter {
-  TcShared *sh;
+template <class S>
+struct WaiterT {
+  S *sh;
   uint32_t *status;
   __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
     const uint32_t a = smem_addr(bar);
@@ -111,6 +112,7 @@ struct Waiter {
     return __all_sync(~0u, wait(bar, parity)) != 0;
   }
 };
+using Waiter = WaiterT<TcShared>;
 __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
   while (!mbar_try_wait(smem_addr(bar), parity) && globaltimer() - t0 < kWaitNs) {
@@ -120,15 +122,19 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
 // --- the flattened work ---------------------------------------------------------
 // For each request, KV head and group of rows: steps of one (WIDE) or two slot
 // tiles up to the last slot that its rows see.
+// An item costs its steps and a fixed part (queries, a filling and draining
+// pipeline, the result), so the shares are of costs: an item takes SETUP + steps
+// places, `base` on, and its step s is at place base + SETUP + s.
 struct TcWalk {
-  int r, len, fresh, groups, h, group, steps, step;
-  int64_t beg;
+  int r, len, fresh, groups, h, group, steps, step;   // step: the CTA's first of the item
+  int64_t beg, base;
 };
 template <bool WIDE>
 struct Geo {
   static constexpr int ROWS = WIDE ? 2 * kTile : kTile;
   static constexpr int SLOTS = WIDE ? kTile : 2 * kTile;   // of a step
   static constexpr int PARTS = WIDE ? 1 : 2;               // results that a CTA keeps for an item
+  static constexpr int SETUP = WIDE ? 5 : 2;
 };
 template <bool WIDE>
 __device__ __forceinline__ int steps_of(const AttendParams &a, int len, int fresh, int group) {
@@ -150,6 +156,7 @@ __device__ __forceinline__ void enter_request(const AttendParams &a, TcWalk &w) 
 // To the first step of the next item.
 template <bool WIDE>
 __device__ __forceinline__ void next_item(const AttendParams &a, TcWalk &w) {
+  w.base += Geo<WIDE>::SETUP + w.steps;
   w.step = 0;
   if (++w.group >= w.groups) {
     w.group = 0;
@@ -163,17 +170,22 @@ __device__ __forceinline__ void next_item(const AttendParams &a, TcWalk &w) {
   }
   w.steps = steps_of<WIDE>(a, w.len, w.fresh, w.group);
 }
-// Steps of one head of a request (every lane gets the sum).
+// The CTA's steps of the item, from w.step on (the share ends at place `last`).
 template <bool WIDE>
-__device__ __forceinline__ int64_t head_steps(const AttendParams &a, int len, int fresh) {
+__device__ __forceinline__ int steps_here(const TcWalk &w, int64_t last) {
+  return (int)min((int64_t)w.steps, last - w.base - Geo<WIDE>::SETUP) - w.step;
+}
+// Places of one head of a request (every lane gets the sum).
+template <bool WIDE>
+__device__ __forceinline__ int64_t head_places(const AttendParams &a, int len, int fresh) {
   const int groups = groups_of<WIDE>(a, fresh);
   int64_t sum = 0;
-  for (int g = threadIdx.x % 32; g < groups; g += 32) sum += steps_of<WIDE>(a, len, fresh, g);
+  for (int g = threadIdx.x % 32; g < groups; g += 32) sum += Geo<WIDE>::SETUP + steps_of<WIDE>(a, len, fresh, g);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   return sum;
 }
-// Total steps (at < 0), or the walk at step `at`, by one warp.
+// Total places (at < 0), or the walk at place `at`, by one warp.
 template <bool WIDE>
 __device__ int64_t walk_at(const AttendParams &a, int64_t at, TcWalk &w) {
   const int lane = threadIdx.x % 32;
@@ -184,12 +196,12 @@ __device__ int64_t walk_at(const AttendParams &a, int64_t at, TcWalk &w) {
       len = len_of(a, r0 + lane);
       fresh = (int)(a.req.begin(r0 + lane + 1) - a.req.begin(r0 + lane));
     }
-    int64_t mine = 0;     // steps of one head of request r0 + lane
+    int64_t mine = 0;     // places of one head of request r0 + lane
     if (a.G * a.max_new <= Geo<WIDE>::ROWS) {
-      mine = fresh > 0 ? steps_of<WIDE>(a, len, fresh, 0) : 0;
+      mine = fresh > 0 ? Geo<WIDE>::SETUP + steps_of<WIDE>(a, len, fresh, 0) : 0;
     } else {
       for (int i = 0; i < 32 && r0 + i < a.req.R; ++i) {
-        const int64_t s = head_steps<WIDE>(a, __shfl_sync(~0u, len, i), __shfl_sync(~0u, fresh, i));
+        const int64_t s = head_places<WIDE>(a, __shfl_sync(~0u, len, i), __shfl_sync(~0u, fresh, i));
         if (lane == i) mine = s;
       }
     }
@@ -208,7 +220,7 @@ __device__ int64_t walk_at(const AttendParams &a, int64_t at, TcWalk &w) {
       w.h = (int)(in / per);
       int64_t rem = in % per;
       for (int g0 = 0;; g0 += 32) {
-        const int64_t s = g0 + lane < w.groups ? steps_of<WIDE>(a, w.len, w.fresh, g0 + lane) : 0;
+        const int64_t s = g0 + lane < w.groups ? Geo<WIDE>::SETUP + steps_of<WIDE>(a, w.len, w.fresh, g0 + lane) : 0;
         int64_t to = s;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -219,8 +231,10 @@ __device__ int64_t walk_at(const AttendParams &a, int64_t at, TcWalk &w) {
         if (hit || g0 + 32 >= w.groups) {
           const int k = hit ? __ffs(hit) - 1 : 0;
           w.group = g0 + k;
-          w.steps = (int)__shfl_sync(~0u, s, k);
-          w.step = (int)(rem - (__shfl_sync(~0u, to, k) - w.steps));
+          const int places = (int)__shfl_sync(~0u, s, k), in_item = (int)(rem - (__shfl_sync(~0u, to, k) - places));
+          w.steps = places - Geo<WIDE>::SETUP;
+          w.step = max(0, in_item - Geo<WIDE>::SETUP);
+          w.base = at - in_item;
           return 0;
         }
         rem -= __shfl_sync(~0u, to, 31);
@@ -235,6 +249,7 @@ __device__ int64_t walk_at(const AttendParams &a, int64_t at, TcWalk &w) {
 // Instruction descriptors: D fp32, M = 128; e4m3 x e4m3 both K-major, N = 64, and f16
 // x f16 with B as it lies in memory, [K][N] (MN-major), N = 128.
 constexpr uint32_t kIdescQK = (1u << 4) | (8u << 17) | (8u << 24);
+constexpr uint32_t kIdescKQ = (1u << 4) | (16u << 17) | (8u << 24);   // N = 128
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | (16u << 17) | (8u << 24);
 
 // The whole warp calls these, with the same arguments (which stay in uniform
@@ -257,6 +272,26 @@ __device__ __forceinline__ void mma_qk(uint32_t d, uint64_t q, uint64_t k) {
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a6, b2, %3, t;\n"
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a7, b3, %3, t;\n}\n" ::"r"(d),
       "l"(q), "l"(k), "r"(kIdescQK), "l"((uint64_t)(kTileBytes >> 4))
+      : "memory");
+}
+// S^T = K (Q1 + Q2)^T for 128 slots and rows.
+__device__ __forceinline__ void mma_kq(uint32_t d, uint64_t k, uint64_t q) {
+  asm volatile(
+      "{\n.reg .pred e, f, t;\n.reg .b32 r;\n.reg .b64 a1, a2, a3, b1, b2, b3, b4, b5, b6, b7;\n"
+      "elect.sync r|e, 0xffffffff;\n"
+      "setp.ne.u32 f, 0, 0;\nsetp.eq.u32 t, 0, 0;\n"
+      "add.u64 a1, %1, 2; add.u64 a2, %1, 4; add.u64 a3, %1, 6;\n"
+      "add.u64 b1, %2, 2; add.u64 b2, %2, 4; add.u64 b3, %2, 6; add.u64 b4, %2, %4;\n"
+      "add.u64 b5, b4, 2; add.u64 b6, b4, 4; add.u64 b7, b4, 6;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, b4, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b5, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b6, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b7, %3, t;\n}\n" ::"r"(d),
+      "l"(k), "l"(q), "r"(kIdescKQ), "l"((uint64_t)(kTileBytes >> 4))
       : "memory");
 }
 // O (+)= P V for 64 slots: four 16-deep steps; P 8 columns on, V 16 slots (2 KB) on.
@@ -334,6 +369,11 @@ __device__ __forceinline__ uint64_t pair(float lo, float hi) {
 }
 __device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
@@ -548,7 +588,7 @@ __device__ __noinline__ void keep_scores(uint32_t col, float *to, const float4 *
 // What a softmax group knows of its item when the item, or the CTA's part of it, ends.
 struct Item {
   TcWalk w;
-  int64_t T, N, now, first;   // now: the CTA's first step of the item
+  int64_t T, N;
   int count, rows, row;
   bool live, warp_live;
   float m, l;
@@ -565,7 +605,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   const TcWalk &w = it.w;
   const uint32_t half = it.half, joins = it.joins;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t T = it.T, N = it.N, first = it.first;
+  const int64_t T = it.T, N = it.N;
   const int rows = it.rows, row = it.row;
   const bool live = it.live, warp_live = it.warp_live, whole = it.count == w.steps;
   const float m = it.m, l = it.l;
@@ -573,12 +613,14 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   // the result of the item, or this CTA's part of it
   if (!W.warp_wait(&sh->pv_done[i][(half - 1) & 1], (half - 1) >> 1 & 1)) return false;
   tc_fence_after();
+  // narrow: the parts of the item before have been read by all
+  if (!WIDE && joins > 0 && !W.warp_wait(&sh->spent, (joins - 1) & 1)) return false;
   const float back = 1.f / 128.f;   // V carries 2^7
   const int64_t at = (int64_t)w.group * G_::ROWS + row;
   const int64_t tok = w.beg + at / a.G;
   const int hq = w.h * a.G + (int)(at % a.G);
   const int64_t part_size = p.part_size;
-  float *slot = p.partial + (((int64_t)blockIdx.x * 2 + (it.now == first ? 0 : 1)) * G_::PARTS + (WIDE ? 0 : i)) *
+  float *slot = p.partial + (((int64_t)blockIdx.x * 2 + (w.step == 0)) * G_::PARTS + (WIDE ? 0 : i)) *
                                 part_size;
   const bool direct = WIDE && whole;
   if (warp_live) {
@@ -630,8 +672,8 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&sh->join));
     if (!W.warp_wait(&sh->join, joins & 1)) return false;
-    const int64_t begin = it.now - w.step, end = begin + w.steps;   // the item's steps
-    const int64_t c0 = ((begin + 1) * N - 1) / T, c1 = (end * N - 1) / T;
+    // the CTAs of its first and its last step
+    const int64_t begin = w.base + G_::SETUP, c0 = ((begin + 1) * N - 1) / T, c1 = ((begin + w.steps) * N - 1) / T;
     bool mine = whole;
     if (!whole) {
       if (tid == 0) {
@@ -651,8 +693,8 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
     mine = sh->last;
     if (mine) {
       __threadfence();
-      // CTA c's part is its first item unless the item begins inside it
-      const int64_t s0 = (c0 * 2 + (c0 * T / N != begin)) * G_::PARTS, s1 = c0 * 2 * G_::PARTS;
+      // a CTA keeps two parts: of an item that others began, and of one that it began
+      const int64_t s0 = (c0 * 2 + 1) * G_::PARTS, s1 = c0 * 2 * G_::PARTS;
       const int parts = (int)(c1 - c0 + 1) * G_::PARTS;
       const auto part_at = [&](int c) {
         const int cta = c / G_::PARTS, sub = c % G_::PARTS;
@@ -707,6 +749,8 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
         }
       }
     }
+    __syncwarp();
+    if (!WIDE && lane == 0) mbar_arrive(smem_addr(&sh->spent));
   }
   return true;
 }
@@ -748,6 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_addr(&sh->join), 8);
     mbar_init(smem_addr(&sh->verdict), 1);
+    mbar_init(smem_addr(&sh->spent), 8);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -765,14 +810,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Waiter W{sh, a.status};
 
   TcWalk w = {};
-  int64_t T = 0, N = 0, first = 0, last = 0;
+  int64_t T = 0, N = 0, last = -1;
   if (good) {
     T = walk_at<WIDE>(a, -1, w);
     N = T < gridDim.x ? T : gridDim.x;   // CTAs at work
     if (blockIdx.x < N) {
-      first = blockIdx.x * T / N;
       last = (blockIdx.x + 1) * T / N;
-      walk_at<WIDE>(a, first, w);
+      walk_at<WIDE>(a, blockIdx.x * T / N, w);
     }
     if (blockIdx.x == 0 && warp == kLoadWarp)
       for (int r = lane; r < a.req.R; r += 32)
@@ -793,8 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t half = 0, joins = 0;                 // half tiles of this group and joins so far
     int ks = WIDE ? 0 : i;                        // the tile's K stage, and its phase
     uint32_t k_phase = 0;
-    for (int64_t now = first; now < last;) {
-      const int count = (int)min((int64_t)(w.steps - w.step), last - now);
+    for (; w.base + G_::SETUP < last; next_item<WIDE>(a, w)) {
+      const int count = steps_here<WIDE>(w, last);
       const int rows = (int)min((int64_t)G_::ROWS, (int64_t)w.fresh * a.G - (int64_t)w.group * G_::ROWS);
       const bool live = row < rows, warp_live = row - lane < rows;
       const int64_t at = (int64_t)w.group * G_::ROWS + row;         // row of the request and head
@@ -856,11 +900,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // the result of the item, or this CTA's part of it
-      const Item it{w, T, N, now, first, count, rows, row, live, warp_live, m, cs != cs ? cs : l, o_col, half, joins};
+      const Item it{w, T, N, count, rows, row, live, warp_live, m, cs != cs ? cs : l, o_col, half, joins};
       if (!finish_item<WIDE>(p, sh, it, i)) goto done;
       joins += !WIDE || count < w.steps;
-      now += count;
-      next_item<WIDE>(a, w);
     }
   done:;
   } else if (warp < kLoadWarp) {
@@ -870,8 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------------------
     const int t = tid - 8 * 32;
     uint32_t n = 0;
-    for (int64_t now = first; now < last;) {
-      const int count = (int)min((int64_t)(w.steps - w.step), last - now);
+    for (; w.base + G_::SETUP < last; next_item<WIDE>(a, w)) {
+      const int count = steps_here<WIDE>(w, last);
       int j0 = w.step * G_::SLOTS;
       for (int k = 0; k < count * (WIDE ? 1 : 2); ++k, ++n, j0 += kTile) {
         const int vs = n % kVStages, ws = n % kWStages;
@@ -906,8 +948,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_addr(&sh->v_empty[vs]));
         }
       }
-      now += count;
-      next_item<WIDE>(a, w);
     }
   cv_done:;
   } else if (warp == kLoadWarp) {
@@ -916,8 +956,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // block lookups, scales and TMA: lane l looks up slots 4l .. 4l + 3
     // ----------------------------------------------------------------------
     uint32_t n = 0;
-    for (int64_t now = first; now < last;) {
-      const int count = (int)min((int64_t)(w.steps - w.step), last - now);
+    for (; w.base + G_::SETUP < last; next_item<WIDE>(a, w)) {
+      const int count = steps_here<WIDE>(w, last);
       int j = w.step * G_::SLOTS + 4 * lane;
       for (int k = 0; k < count * (WIDE ? 1 : 2); ++k, ++n, j += kTile) {
         const int ks = n % kKStages, vs = n % kVStages;
@@ -966,8 +1006,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                       smem_addr(&sh->v_full[vs]));
         if (lane != 0) mbar_arrive(smem_addr(&sh->v_full[vs]));
       }
-      now += count;
-      next_item<WIDE>(a, w);
     }
   ld_done:
     // drain: the tiles that were asked for have landed (n counts whole tiles; after
@@ -1001,8 +1039,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (hf) commit(&sh->k_empty[stage]);
       return true;
     };
-    for (int64_t now = first; ok && now < last;) {
-      const int count = (int)min((int64_t)(w.steps - w.step), last - now);
+    for (; ok && w.base + G_::SETUP < last; next_item<WIDE>(a, w)) {
+      const int count = steps_here<WIDE>(w, last);
       ok = W.warp_wait(&sh->q_full[WIDE ? i : 0], items & 1) && scores(u) && scores(u + 1);
       ++items;
       for (int s = 0; ok && s < 2 * count; ++s, ++u) {
@@ -1016,8 +1054,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // two halves on, over the probabilities just spent: MMAs run in order
         if (s + 2 < 2 * count) ok = scores(u + 2);
       }
-      now += count;
-      next_item<WIDE>(a, w);
     }
     if (issued) {
       commit(&sh->drain[i]);
@@ -1057,6 +1093,200 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
     sum += z > -INFINITY ? ex2(z - lse2[c]) : 0.f;
   }
   a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
+}
+
+// --- accumulated weights of wide calls -------------------------------------------
+// weights[r][h][j] += sum over the rows that see slot j of exp2(score - lse).
+// The scores are formed again, transposed (S^T = K Q^T, slots in the lanes), so
+// that a slot's sum stays in one thread: no atomics, one order of summation.  A CTA
+// takes `per` slot tiles of one request and head, its rows 256 at a time; two groups
+// of four warps take turns with the tiles.
+constexpr int kWtStages = 4, kWtThreads = 10 * 32;
+struct WtShared {
+  uint64_t k_full[kWtStages], k_empty[kWtStages], q_full, spent, s_full[2], s_empty[2], drain;
+  uint32_t tmem_base;
+  volatile int abort;
+  uint32_t mask[kWtStages];
+  float ks[kWtStages][kTile / 4];
+  __align__(16) float4 rows[kTile];   // of row pairs: two factors, two log-sum-exps (base 2, negative)
+};
+constexpr size_t kWtSmem = 1024 + kSmemQ + kWtStages * (size_t)kTileBytes + sizeof(WtShared);
+
+__global__ void __launch_bounds__(kWtThreads, 1)
+    weights_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_k, int per) {
+  extern __shared__ unsigned char raw[];
+  unsigned char *qbuf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *kbuf = qbuf + kSmemQ;
+  WtShared *sh = reinterpret_cast<WtShared *>(kbuf + kWtStages * kTileBytes);
+  const AttendParams &a = p.a;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
+  const int t0 = blockIdx.x * per, t1 = min(t0 + per, (len + kTile - 1) / kTile);   // tiles
+  if (tid == 0) {
+    for (int i = 0; i < kWtStages; ++i) {
+      mbar_init(smem_addr(&sh->k_full[i]), 32);
+      mbar_init(smem_addr(&sh->k_empty[i]), 1 + 4);
+    }
+    mbar_init(smem_addr(&sh->q_full), 8);
+    mbar_init(smem_addr(&sh->spent), 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh->s_full[i]), 1);
+      mbar_init(smem_addr(&sh->s_empty[i]), 4);
+    }
+    mbar_init(smem_addr(&sh->drain), 1);
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(&sh->tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  const bool good = requests_ok(a);
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  const WaiterT<WtShared> W{sh, a.status};
+  const int64_t beg = a.req.begin(r);
+  const int fresh = good ? (int)(a.req.begin(r + 1) - beg) : 0, rows = fresh * a.G;
+  // rows that see the CTA's first slot: from the first query whose limit reaches it
+  const int row0 = max(0, t0 * kTile - (len - fresh)) * a.G / (2 * kTile) * (2 * kTile);
+  const int chunks = t0 < t1 && row0 < rows ? (rows - row0 + 2 * kTile - 1) / (2 * kTile) : 0, tiles = t1 - t0;
+
+  if (warp < 8) {
+    const int i = warp / 4;
+    const uint32_t s_col = tmem + ((uint32_t)(warp % 4 * 32) << 16) + i * 2 * kTile;
+    for (int c = 0; c < chunks; ++c) {
+      // queries: a row a thread, once all warps are through with the rows before
+      if (c > 0 && !W.warp_wait(&sh->spent, (c - 1) & 1)) goto done;
+      const int row = row0 + c * 2 * kTile + tid;
+      const bool live = row < rows;
+      const int64_t tok = beg + row / a.G;
+      const int hq = h * a.G + row % a.G;
+      const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + tok * a.qt + (int64_t)hq * a.qh;
+      const float cs = put_query(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, tid % kTile);
+      float *pair_of = reinterpret_cast<float *>(&sh->rows[tid / 2]) + tid % 2;
+      // a dead row gives exp2(-inf)
+      pair_of[0] = live ? cs : 0.f;
+      pair_of[2] = live ? -a.lse[tok * a.Hq + hq] * kLog2e : -INFINITY;
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh->q_full));
+      if (!W.warp_wait(&sh->q_full, c & 1)) goto done;   // the other rows' constants
+      for (int t = 0; t < tiles; ++t) {
+        const int n = c * tiles + t;
+        if ((n & 1) != i) continue;
+        const int ks = n % kWtStages, j = (t0 + t) * kTile + warp % 4 * 32 + lane;
+        if (!W.warp_wait(&sh->k_full[ks], n / kWtStages & 1)) goto done;
+        if (!W.warp_wait(&sh->s_full[i], n >> 1 & 1)) goto done;
+        tc_fence_after();
+        const int in = warp % 4 * 32 + lane;
+        const float f = sh->ks[ks][in / 4];
+        const bool there = j < len && (sh->mask[ks] >> (in / 4) & 1);
+        // columns below `from` do not see the slot
+        const int from = (int)min((int64_t)INT32_MAX, max((int64_t)j - (len - fresh), (int64_t)0) * a.G) - (row0 + c * 2 * kTile);
+        const bool masked = __any_sync(~0u, from > 0);
+        const uint64_t f2 = pair(f, f);
+        uint64_t sum = pair(0.f, 0.f);
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+          uint32_t s[32];
+          tc_ld32(s_col + 32 * q, s);
+          tc_wait_ld32(s);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float4 k = sh->rows[16 * q + e / 2];
+            float x0, x1;
+            unpair(fma2(mul2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f2), pair(k.x, k.y), pair(k.z, k.w)),
+                   x0, x1);
+            if (masked) {
+              x0 = 32 * q + e >= from ? x0 : -INFINITY;
+              x1 = 32 * q + e + 1 >= from ? x1 : -INFINITY;
+            }
+            sum = add2(sum, pair(ex2(x0), ex2(x1)));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&sh->s_empty[i]));
+          mbar_arrive(smem_addr(&sh->k_empty[ks]));
+        }
+        float u0, u1;
+        unpair(sum, u0, u1);
+        if (there) a.weights[((int64_t)r * a.H + h) * a.wstride + j] += u0 + u1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh->spent));
+    }
+  done:;
+  } else if (warp == 8) {
+    int n = 0;
+    for (int c = 0; c < chunks; ++c)
+      for (int t = 0; t < tiles; ++t, ++n) {
+        const int ks = n % kWtStages, j = (t0 + t) * kTile + 4 * lane;
+        int page = -1;
+        uint32_t off = 0;
+        if (j < len) {
+          const uint32_t block = block_of(a, j);
+          off = j - block * a.bs;
+          page = page_of(a, r, block);
+        }
+        const uint32_t sb = page < 0 ? 0u : (uint32_t)page * a.H + h;
+        const int row = (int)(sb * a.bs + off);
+        const float kscale = page >= 0 ? __ldg(a.ks + sb) : 0.f;
+        const unsigned mask = __ballot_sync(~0u, page >= 0);
+        const int step = p.box / 4, boxes = kTile / p.box;
+        const int from = __shfl_sync(~0u, row, lane < boxes ? lane * step : 0);
+        const bool there = lane < boxes && (mask >> (lane * step) & 1);
+        const uint32_t bytes = __popc(__ballot_sync(~0u, there)) * (uint32_t)p.box * kD;
+        if (!W.warp_wait(&sh->k_empty[ks], (n / kWtStages & 1) ^ 1)) goto ld_done;
+        sh->ks[ks][lane] = kscale;
+        if (lane == 0) {
+          sh->mask[ks] = mask;
+          mbar_expect_tx(smem_addr(&sh->k_full[ks]), bytes);
+        }
+        __syncwarp();
+        if (there)
+          tma_load_2d(smem_addr(kbuf + ks * kTileBytes + lane * p.box * kD), &map_k, 0, from, smem_addr(&sh->k_full[ks]));
+        if (lane != 0) mbar_arrive(smem_addr(&sh->k_full[ks]));
+      }
+  ld_done:
+    __syncwarp();
+    if (lane == 0)
+      for (int x = n > kWtStages ? n - kWtStages : 0; x < n; ++x) drain_wait(&sh->k_full[x % kWtStages], x / kWtStages & 1);
+  } else {
+    const uint64_t q0 = sw128_desc(smem_addr(qbuf)), k0 = sw128_desc(smem_addr(kbuf));
+    bool ok = true, issued = false;
+    int n = 0;
+    for (int c = 0; ok && c < chunks; ++c) {
+      ok = W.warp_wait(&sh->q_full, c & 1);
+      for (int t = 0; ok && t < tiles; ++t, ++n) {
+        const int ks = n % kWtStages, i = n & 1;
+        ok = W.warp_wait(&sh->k_full[ks], n / kWtStages & 1) && W.warp_wait(&sh->s_empty[i], (n >> 1 & 1) ^ 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t k = k0 + (uint64_t)(ks * kTileBytes >> 4);
+        mma_kq(tmem + i * 2 * kTile, k, q0);
+        mma_kq(tmem + i * 2 * kTile + kTile, k, q0 + (2 * kTileBytes >> 4));
+        issued = true;
+        commit(&sh->s_full[i]);
+        commit(&sh->k_empty[ks]);
+      }
+    }
+    if (issued) {
+      commit(&sh->drain);
+      if (lane == 0) drain_wait(&sh->drain, 0);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // --- host ------------------------------------------------------------------------
@@ -1141,7 +1371,16 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   p.vec_out = aligned_to(a.out, 16) && (a.ot | a.oh) % 8 == 0;
   const kvx_status st = sh.wide ? launch<true>(p, mk, mv, sh.grid, s) : launch<false>(p, mk, mv, sh.grid, s);
   if (st != KVX_OK || !a.weights || a.max_len == 0) return st;
-  if (!sh.spool) return KVX_OK;
+  if (sh.wide) {
+    // as few slot tiles a CTA as lets all run at once, 16 at most
+    const int tiles = (args->max_len + kTile - 1) / kTile, items = a.H * a.req.R;
+    int per = 1;
+    while (per < 16 && (int64_t)items * ((tiles + per - 1) / per) > 152) ++per;
+    if (cudaFuncSetAttribute(weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWtSmem) != cudaSuccess)
+      return KVX_ERR_CUDA;
+    weights_tc_kernel<<<dim3((tiles + per - 1) / per, a.H, a.req.R), kWtThreads, kWtSmem, s>>>(p, mk, per);
+    return launched();
+  }
   weights_of_rows_kernel<<<dim3((a.max_len + 255) / 256, a.H, a.req.R), 256, sh.slot_rows * 4, s>>>(p);
   return launched();
 }
