@@ -52,6 +52,16 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // subtracted maximum's; with the lazy 2^8 that is at most 2^15
 constexpr float kBias = 7.f, kSlack = 8.f;
 
+struct TcWalk {
+  int r, len, fresh, groups, h, group, steps, step;   // step: the CTA's first of the item
+  int64_t beg, base;
+};
+struct Share {
+  TcWalk w;                // its first item
+  int64_t T, N, last;      // all places, CTAs at work, the place at which it ends
+  bool good;               // the request table is
+};
+
 struct TcShared {
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
@@ -63,6 +73,7 @@ struct TcShared {
   uint32_t tmem_base;
   volatile int abort;
   volatile int last;
+  Share share;
   // the tile's largest value scale, as a power of two: its exponent for the
   // softmax, 2^7 over it for the conversion
   float k_ref[kKStages], v_unit[kVStages];
@@ -120,43 +131,33 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
 }
 
 // --- the flattened work ---------------------------------------------------------
-// For each request, KV head and group of rows: steps of one (WIDE) or two slot
-// tiles up to the last slot that its rows see.
-// An item costs its steps and a fixed part (queries, a filling and draining
-// pipeline, the result), so the shares are of costs: an item takes SETUP + steps
-// places, `base` on, and its step s is at place base + SETUP + s.
-struct TcWalk {
-  int r, len, fresh, groups, h, group, steps, step;   // step: the CTA's first of the item
-  int64_t beg, base;
+// For each request, KV head and group of rows an item: steps of one or two slot
+// tiles up to the last slot that its rows see.  An item costs its steps and a fixed
+// part (queries, a filling and draining pipeline, the result), so the CTAs' shares
+// are of costs: an item takes SETUP + steps places from `base` on, and its step s
+// is at place base + SETUP + s.
+struct Wide {
+  static constexpr int ROWS = 2 * kTile, SLOTS = kTile;   // of an item, of a step
+  static constexpr int PARTS = 1;                         // results that a CTA keeps for an item
+  static constexpr int SETUP = 5;
 };
-template <bool WIDE>
-struct Geo {
-  static constexpr int ROWS = WIDE ? 2 * kTile : kTile;
-  static constexpr int SLOTS = WIDE ? kTile : 2 * kTile;   // of a step
-  static constexpr int PARTS = WIDE ? 1 : 2;               // results that a CTA keeps for an item
-  static constexpr int SETUP = WIDE ? 5 : 2;
+struct Narrow {
+  static constexpr int ROWS = kTile, SLOTS = 2 * kTile, PARTS = 2, SETUP = 2;
 };
-template <bool WIDE>
+template <class G>
 __device__ __forceinline__ int steps_of(const AttendParams &a, int len, int fresh, int group) {
-  const int64_t end = ((int64_t)(group + 1) * Geo<WIDE>::ROWS + a.G - 1) / a.G;   // its tokens end here
+  const int64_t end = ((int64_t)(group + 1) * G::ROWS + a.G - 1) / a.G;   // its tokens end here
   const int64_t seen = len - fresh + (end < fresh ? end : fresh);
-  return seen <= 0 ? 1 : (int)((seen + Geo<WIDE>::SLOTS - 1) / Geo<WIDE>::SLOTS);
+  return seen <= 0 ? 1 : (int)((seen + G::SLOTS - 1) / G::SLOTS);
 }
-template <bool WIDE>
+template <class G>
 __device__ __forceinline__ int groups_of(const AttendParams &a, int fresh) {
-  return (int)(((int64_t)fresh * a.G + Geo<WIDE>::ROWS - 1) / Geo<WIDE>::ROWS);
-}
-template <bool WIDE>
-__device__ __forceinline__ void enter_request(const AttendParams &a, TcWalk &w) {
-  w.len = len_of(a, w.r);
-  w.beg = a.req.begin(w.r);
-  w.fresh = (int)(a.req.begin(w.r + 1) - w.beg);
-  w.groups = groups_of<WIDE>(a, w.fresh);
+  return (int)(((int64_t)fresh * a.G + G::ROWS - 1) / G::ROWS);
 }
 // To the first step of the next item.
-template <bool WIDE>
+template <class G>
 __device__ __forceinline__ void next_item(const AttendParams &a, TcWalk &w) {
-  w.base += Geo<WIDE>::SETUP + w.steps;
+  w.base += G::SETUP + w.steps;
   w.step = 0;
   if (++w.group >= w.groups) {
     w.group = 0;
@@ -164,85 +165,120 @@ __device__ __forceinline__ void next_item(const AttendParams &a, TcWalk &w) {
       w.h = 0;
       do {
         if (++w.r >= a.req.R) return;
-        enter_request<WIDE>(a, w);
+        w.len = len_of(a, w.r);
+        w.beg = a.req.begin(w.r);
+        w.fresh = (int)(a.req.begin(w.r + 1) - w.beg);
+        w.groups = groups_of<G>(a, w.fresh);
       } while (w.groups == 0);
     }
   }
-  w.steps = steps_of<WIDE>(a, w.len, w.fresh, w.group);
+  w.steps = steps_of<G>(a, w.len, w.fresh, w.group);
 }
 // The CTA's steps of the item, from w.step on (the share ends at place `last`).
-template <bool WIDE>
+template <class G>
 __device__ __forceinline__ int steps_here(const TcWalk &w, int64_t last) {
-  return (int)min((int64_t)w.steps, last - w.base - Geo<WIDE>::SETUP) - w.step;
+  return (int)min((int64_t)w.steps, last - w.base - G::SETUP) - w.step;
 }
-// Places of one head of a request (every lane gets the sum).
-template <bool WIDE>
-__device__ __forceinline__ int64_t head_places(const AttendParams &a, int len, int fresh) {
-  const int groups = groups_of<WIDE>(a, fresh);
-  int64_t sum = 0;
-  for (int g = threadIdx.x % 32; g < groups; g += 32) sum += Geo<WIDE>::SETUP + steps_of<WIDE>(a, len, fresh, g);
+__device__ __forceinline__ int64_t scan_up(int64_t v) {   // inclusive, over the lanes
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  return sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, v, o);
+    if ((int)(threadIdx.x % 32) >= o) v += y;
+  }
+  return v;
 }
-// Total places (at < 0), or the walk at place `at`, by one warp.
-template <bool WIDE>
-__device__ int64_t walk_at(const AttendParams &a, int64_t at, TcWalk &w) {
+// 32 requests from r0 on, one a lane: the lane's request, the places of one of its
+// heads, the places up to and with it; whether the table is good there.
+struct Requests32 {
+  int len, fresh;
+  int64_t beg, head, upto;
+  bool good;
+};
+template <class G>
+__device__ __forceinline__ Requests32 look(const AttendParams &a, int r0) {
+  const int r = r0 + threadIdx.x % 32;
+  Requests32 q = {};
+  bool good = true;
+  if (r < a.req.R) {
+    q.len = len_of(a, r);
+    q.beg = a.req.begin(r);
+    const int64_t end = a.req.begin(r + 1);
+    q.fresh = (int)(end - q.beg);
+    good = end >= q.beg && end - q.beg <= a.max_new && (r > 0 || q.beg == 0) && (r + 1 < a.req.R || end == a.req.ntok);
+    if (!good) q.fresh = 0;
+    if (blockIdx.x == 0 && q.len != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
+  }
+  if (a.G * a.max_new <= G::ROWS) {
+    q.head = q.fresh > 0 ? G::SETUP + steps_of<G>(a, q.len, q.fresh, 0) : 0;
+  } else {
+    for (int i = 0; i < 32 && r0 + i < a.req.R; ++i) {
+      const int len = __shfl_sync(~0u, q.len, i), fresh = __shfl_sync(~0u, q.fresh, i), groups = groups_of<G>(a, fresh);
+      int64_t sum = 0;
+      for (int g = threadIdx.x % 32; g < groups; g += 32) sum += G::SETUP + steps_of<G>(a, len, fresh, g);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      if ((int)(threadIdx.x % 32) == i) q.head = sum;
+    }
+  }
+  q.upto = scan_up(q.head * a.H);
+  q.good = __all_sync(~0u, good);
+  return q;
+}
+// One warp: the CTA's share.
+template <class G>
+__device__ void find_share(const AttendParams &a, Share &s) {
   const int lane = threadIdx.x % 32;
+  s.good = true;
+  s.T = 0;
+  s.N = 0;
+  s.last = -1;
+  s.w = {};
+  Requests32 q;
+  for (int r0 = 0; r0 < a.req.R; r0 += 32) {
+    q = look<G>(a, r0);
+    s.good = s.good && q.good;
+    s.T += __shfl_sync(~0u, q.upto, 31);
+  }
+  if (!s.good) return;
+  s.N = s.T < gridDim.x ? s.T : gridDim.x;
+  if (blockIdx.x >= s.N) return;
+  const int64_t at = blockIdx.x * s.T / s.N;
+  s.last = (blockIdx.x + 1) * s.T / s.N;
   int64_t before = 0;
   for (int r0 = 0; r0 < a.req.R; r0 += 32) {
-    int len = 0, fresh = 0;
-    if (r0 + lane < a.req.R) {
-      len = len_of(a, r0 + lane);
-      fresh = (int)(a.req.begin(r0 + lane + 1) - a.req.begin(r0 + lane));
+    if (a.req.R > 32) q = look<G>(a, r0);      // otherwise it is at hand
+    const unsigned here = __ballot_sync(~0u, at < before + q.upto);
+    if (!here) {
+      before += __shfl_sync(~0u, q.upto, 31);
+      continue;
     }
-    int64_t mine = 0;     // places of one head of request r0 + lane
-    if (a.G * a.max_new <= Geo<WIDE>::ROWS) {
-      mine = fresh > 0 ? Geo<WIDE>::SETUP + steps_of<WIDE>(a, len, fresh, 0) : 0;
-    } else {
-      for (int i = 0; i < 32 && r0 + i < a.req.R; ++i) {
-        const int64_t s = head_places<WIDE>(a, __shfl_sync(~0u, len, i), __shfl_sync(~0u, fresh, i));
-        if (lane == i) mine = s;
+    const int who = __ffs(here) - 1;
+    TcWalk &w = s.w;
+    w.r = r0 + who;
+    w.len = __shfl_sync(~0u, q.len, who);
+    w.fresh = __shfl_sync(~0u, q.fresh, who);
+    w.beg = __shfl_sync(~0u, q.beg, who);
+    w.groups = groups_of<G>(a, w.fresh);
+    const int64_t per = __shfl_sync(~0u, q.head, who), in = at - before - (__shfl_sync(~0u, q.upto, who) - per * a.H);
+    w.h = (int)(in / per);
+    int64_t rem = in % per;
+    for (int g0 = 0;; g0 += 32) {
+      const int64_t places = g0 + lane < w.groups ? G::SETUP + steps_of<G>(a, w.len, w.fresh, g0 + lane) : 0;
+      const int64_t to = scan_up(places);
+      const unsigned hit = __ballot_sync(~0u, rem < to);
+      if (hit || g0 + 32 >= w.groups) {
+        const int k = hit ? __ffs(hit) - 1 : 0;
+        const int here_places = (int)__shfl_sync(~0u, places, k);
+        const int in_item = (int)(rem - (__shfl_sync(~0u, to, k) - here_places));
+        w.group = g0 + k;
+        w.steps = here_places - G::SETUP;
+        w.step = max(0, in_item - G::SETUP);
+        w.base = at - in_item;
+        return;
       }
+      rem -= __shfl_sync(~0u, to, 31);
     }
-    int64_t upto = mine * a.H;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(~0u, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const unsigned here = __ballot_sync(~0u, at >= 0 && at < before + upto);
-    if (here) {
-      const int who = __ffs(here) - 1;
-      w.r = r0 + who;
-      enter_request<WIDE>(a, w);
-      const int64_t per = __shfl_sync(~0u, mine, who), in = at - before - (__shfl_sync(~0u, upto, who) - per * a.H);
-      w.h = (int)(in / per);
-      int64_t rem = in % per;
-      for (int g0 = 0;; g0 += 32) {
-        const int64_t s = g0 + lane < w.groups ? Geo<WIDE>::SETUP + steps_of<WIDE>(a, w.len, w.fresh, g0 + lane) : 0;
-        int64_t to = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(~0u, to, o);
-          if (lane >= o) to += y;
-        }
-        const unsigned hit = __ballot_sync(~0u, rem < to);
-        if (hit || g0 + 32 >= w.groups) {
-          const int k = hit ? __ffs(hit) - 1 : 0;
-          w.group = g0 + k;
-          const int places = (int)__shfl_sync(~0u, s, k), in_item = (int)(rem - (__shfl_sync(~0u, to, k) - places));
-          w.steps = places - Geo<WIDE>::SETUP;
-          w.step = max(0, in_item - Geo<WIDE>::SETUP);
-          w.base = at - in_item;
-          return 0;
-        }
-        rem -= __shfl_sync(~0u, to, 31);
-      }
-    }
-    before += __shfl_sync(~0u, upto, 31);
   }
-  return before;
 }
 
 // --- tcgen05 ---------------------------------------------------------------------
@@ -524,34 +560,65 @@ __device__ __noinline__ float query_factor(const AttendParams &a, bool vec, cons
   const float top = largest(x);
   return row_factor(a, top, pow2_scale(top));
 }
-// A query row as two e4m3 parts in the swizzled K-major tile; returns the factor
-// on its scores (its sign is in the parts).
-__device__ __noinline__ float put_query(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
-                                           unsigned char *tile, int row) {
-  uint32_t x[kD / 2];
-  load_query(src, vec, live, x);
-  const float top = largest(x);
-  const float unit = pow2_scale(top);   // top <= 448 unit
-  const float up = a.c != 0.f ? copysignf(1.f / unit, a.c) : 0.f;
+// 32 query rows of a warp as two e4m3 parts in the swizzled K-major tile (from row
+// `first` of the tile on; `src` is the lane's own row).  Half a warp loads a row at
+// a time.  Returns the lane's factor on its row's scores (its sign is in the
+// parts).
+__device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
+                                          unsigned char *tile, int first) {
+  const int lane = threadIdx.x % 32, c = lane % 16;      // 8 dimensions
+  uint4 x[16];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    uint32_t p1[4], p2[4];
+  for (int i = 0; i < 16; ++i) {
+    const int row = 2 * i + lane / 16;
+    const uint64_t p = __shfl_sync(~0u, (uint64_t)src, row);
+    const bool there = __shfl_sync(~0u, (int)live, row);
+    const __nv_bfloat16 *from = reinterpret_cast<const __nv_bfloat16 *>(p) + 8 * c;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (there && vec) {
+      x[i] = __ldg(reinterpret_cast<const uint4 *>(from));
+    } else if (there) {
+      const unsigned short *h = reinterpret_cast<const unsigned short *>(from);
+      uint32_t v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t u0 = x[8 * c + 2 * j], u1 = x[8 * c + 2 * j + 1];
-      const float y0 = __uint_as_float(u0 << 16) * up, y1 = __uint_as_float(u0 & 0xffff0000u) * up;
-      const float y2 = __uint_as_float(u1 << 16) * up, y3 = __uint_as_float(u1 & 0xffff0000u) * up;
-      p1[j] = e4m3x2(y0, y1) | e4m3x2(y2, y3) << 16;
-      const float2 f0 = floats_of(p1[j]), f1 = floats_of(p1[j] >> 16);
-      p2[j] = e4m3x2(y0 - f0.x, y1 - f0.y) | e4m3x2(y2 - f1.x, y3 - f1.y) << 16;
+      for (int e = 0; e < 4; ++e) v[e] = (uint32_t)h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
+      x[i] = make_uint4(v[0], v[1], v[2], v[3]);
     }
-    unsigned char *to = tile + row * kD + ((c ^ (row & 7)) << 4);
-    *reinterpret_cast<uint4 *>(to) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-    *reinterpret_cast<uint4 *>(to + kTileBytes) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
   }
-  return row_factor(a, top, unit);
+  float mine = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    float y[8], top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[2 * e] = __uint_as_float(v[e] << 16);
+      y[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+      top = max3(top, fabsf(y[2 * e]), fabsf(y[2 * e + 1]));
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    const float unit = pow2_scale(top);   // top <= 448 unit
+    const float up = a.c != 0.f ? copysignf(1.f / unit, a.c) : 0.f;
+    const float other = __shfl_xor_sync(~0u, top, 16);
+    if (lane / 2 == i) mine = lane % 2 == lane / 16 ? top : other;
+    uint32_t p1[2], p2[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float *z = y + 4 * e;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[k] *= up;
+      p1[e] = e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16;
+      const float2 f0 = floats_of(p1[e]), f1 = floats_of(p1[e] >> 16);
+      p2[e] = e4m3x2(z[0] - f0.x, z[1] - f0.y) | e4m3x2(z[2] - f1.x, z[3] - f1.y) << 16;
+    }
+    const int row = first + 2 * i + lane / 16;
+    unsigned char *to = tile + row * kD + ((c / 2 ^ (row & 7)) << 4) + (c & 1) * 8;
+    *reinterpret_cast<uint2 *>(to) = make_uint2(p1[0], p1[1]);
+    *reinterpret_cast<uint2 *>(to + kTileBytes) = make_uint2(p2[0], p2[1]);
+  }
+  return row_factor(a, mine, pow2_scale(mine));
 }
-
 // O times a row's factor, in place.
 __device__ __noinline__ void scale_down(uint32_t col, float down) {
 #pragma unroll 1
@@ -599,7 +666,7 @@ struct Item {
 // registers.
 template <bool WIDE>
 __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const Item it, int i) {
-  using G_ = Geo<WIDE>;
+  using G_ = std::conditional_t<WIDE, Wide, Narrow>;
   const AttendParams &a = p.a;
   const Waiter W{sh, a.status};
   const TcWalk &w = it.w;
@@ -700,53 +767,45 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
         const int cta = c / G_::PARTS, sub = c % G_::PARTS;
         return p.partial + ((cta ? s1 + (int64_t)cta * 2 * G_::PARTS : s0) + sub) * part_size;
       };
-      // a warp a row, four rows at once
-      constexpr int B = 4;
+      // a warp a row: the parts' maxima and totals by the lanes, 32 parts at a
+      // time, then the sums of one part after another, several on their way
       const int d = lane * 4;
-      for (int r0 = warp; r0 < rows; r0 += 8 * B) {
-        float mm[B], ll[B];
-        float4 oo[B];
+      for (int rr = warp; rr < rows; rr += 8) {
+        float mm = -INFINITY, ll = 0.f;
+        float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < parts; c0 += 32) {
+          const float *own = part_at(min(c0 + lane, parts - 1)) + p.slot_rows * kD + rr;
+          float pm = __ldcg(own), pl = __ldcg(own + p.slot_rows);
+          if (c0 + lane >= parts) {
+            pm = -INFINITY;
+            pl = 0.f;
+          }
+          float top = fmaxf(mm, pm);
 #pragma unroll
-        for (int k = 0; k < B; ++k) {
-          mm[k] = -INFINITY;
-          ll[k] = 0.f;
-          oo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll 4
-        for (int c = 0; c < parts; ++c) {
-          const float *part = part_at(c) + p.slot_rows * kD;
+          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+          const float down = ex2(mm - finite_or_0(top)), f = ex2(pm - finite_or_0(top));
+          mm = top;
+          pl *= f;
 #pragma unroll
-          for (int k = 0; k < B; ++k)
-            if (r0 + 8 * k < rows) mm[k] = fmaxf(mm[k], __ldcg(part + r0 + 8 * k));
-        }
-#pragma unroll
-        for (int k = 0; k < B; ++k) mm[k] = finite_or_0(mm[k]);
-#pragma unroll 4
-        for (int c = 0; c < parts; ++c) {
-          const float *part = part_at(c);
-#pragma unroll
-          for (int k = 0; k < B; ++k) {
-            const int rr = r0 + 8 * k;
-            if (rr >= rows) continue;
-            const float f = ex2(__ldcg(part + p.slot_rows * kD + rr) - mm[k]);
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + rr * kD + d));
-            ll[k] += __ldcg(part + p.slot_rows * (kD + 1) + rr) * f;
-            oo[k].x += y.x * f;
-            oo[k].y += y.y * f;
-            oo[k].z += y.z * f;
-            oo[k].w += y.w * f;
+          for (int o = 16; o; o >>= 1) pl += __shfl_xor_sync(~0u, pl, o);
+          ll = ll * down + pl;
+          oo = make_float4(oo.x * down, oo.y * down, oo.z * down, oo.w * down);
+          const int here = min(32, parts - c0);
+#pragma unroll 8
+          for (int c = 0; c < here; ++c) {
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part_at(c0 + c) + rr * kD + d));
+            const float fc = __shfl_sync(~0u, f, c);
+            oo.x += y.x * fc;
+            oo.y += y.y * fc;
+            oo.z += y.z * fc;
+            oo.w += y.w * fc;
           }
         }
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-          const int rr = r0 + 8 * k;
-          if (rr >= rows) continue;
-          const int64_t ar = (int64_t)w.group * G_::ROWS + rr;
-          const int64_t tk = w.beg + ar / a.G;
-          const int hh = w.h * a.G + (int)(ar % a.G);
-          store_out(a, tk, hh, d, make_float2(oo[k].x, oo[k].y), mm[k], ll[k]);
-          store_out(a, tk, hh, d + 2, make_float2(oo[k].z, oo[k].w), mm[k], ll[k]);
-        }
+        const int64_t ar = (int64_t)w.group * G_::ROWS + rr;
+        const int64_t tk = w.beg + ar / a.G;
+        const int hh = w.h * a.G + (int)(ar % a.G);
+        store_out(a, tk, hh, d, make_float2(oo.x, oo.y), mm, ll);
+        store_out(a, tk, hh, d + 2, make_float2(oo.z, oo.w), mm, ll);
       }
     }
     __syncwarp();
@@ -760,7 +819,7 @@ template <bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v) {
-  using G_ = Geo<WIDE>;
+  using G_ = std::conditional_t<WIDE, Wide, Narrow>;
   extern __shared__ unsigned char raw[];
   unsigned char *qbuf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   unsigned char *kbuf = qbuf + kSmemQ, *vbuf = kbuf + kKStages * kTileBytes, *wbuf = vbuf + kVStages * kTileBytes;
@@ -802,28 +861,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (warp == kLoadWarp) {
+    Share share;
+    find_share<G_>(a, share);
+    if (lane == 0) {
+      sh->share = share;
+      if (!share.good && blockIdx.x == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
+    }
+  }
   tc_fence_before();
   __syncthreads();
-  const bool good = requests_ok(a);
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   const Waiter W{sh, a.status};
-
-  TcWalk w = {};
-  int64_t T = 0, N = 0, last = -1;
-  if (good) {
-    T = walk_at<WIDE>(a, -1, w);
-    N = T < gridDim.x ? T : gridDim.x;   // CTAs at work
-    if (blockIdx.x < N) {
-      last = (blockIdx.x + 1) * T / N;
-      walk_at<WIDE>(a, blockIdx.x * T / N, w);
-    }
-    if (blockIdx.x == 0 && warp == kLoadWarp)
-      for (int r = lane; r < a.req.R; r += 32)
-        if (len_of(a, r) != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
-  } else if (blockIdx.x == 0 && tid == 0) {
-    raise(a.status, KVX_FLAG_BAD_SEQLENS);
-  }
+  TcWalk w = sh->share.w;
+  const int64_t T = sh->share.T, N = sh->share.N, last = sh->share.last;
 
   if (warp < 8) {
     more_registers<kSoftmaxRegs>();
@@ -837,8 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t half = 0, joins = 0;                 // half tiles of this group and joins so far
     int ks = WIDE ? 0 : i;                        // the tile's K stage, and its phase
     uint32_t k_phase = 0;
-    for (; w.base + G_::SETUP < last; next_item<WIDE>(a, w)) {
-      const int count = steps_here<WIDE>(w, last);
+    for (; w.base + G_::SETUP < last; next_item<G_>(a, w)) {
+      const int count = steps_here<G_>(w, last);
       const int rows = (int)min((int64_t)G_::ROWS, (int64_t)w.fresh * a.G - (int64_t)w.group * G_::ROWS);
       const bool live = row < rows, warp_live = row - lane < rows;
       const int64_t at = (int64_t)w.group * G_::ROWS + row;         // row of the request and head
@@ -849,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
       float m = -INFINITY, l = 0.f, cs;
       if (WIDE || i == 0) {
-        cs = put_query(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), row % kTile);
+        cs = put_queries(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32);
         fence_async_proxy();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[i]));
@@ -912,8 +964,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------------------
     const int t = tid - 8 * 32;
     uint32_t n = 0;
-    for (; w.base + G_::SETUP < last; next_item<WIDE>(a, w)) {
-      const int count = steps_here<WIDE>(w, last);
+    for (; w.base + G_::SETUP < last; next_item<G_>(a, w)) {
+      const int count = steps_here<G_>(w, last);
       int j0 = w.step * G_::SLOTS;
       for (int k = 0; k < count * (WIDE ? 1 : 2); ++k, ++n, j0 += kTile) {
         const int vs = n % kVStages, ws = n % kWStages;
@@ -956,8 +1008,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // block lookups, scales and TMA: lane l looks up slots 4l .. 4l + 3
     // ----------------------------------------------------------------------
     uint32_t n = 0;
-    for (; w.base + G_::SETUP < last; next_item<WIDE>(a, w)) {
-      const int count = steps_here<WIDE>(w, last);
+    for (; w.base + G_::SETUP < last; next_item<G_>(a, w)) {
+      const int count = steps_here<G_>(w, last);
       int j = w.step * G_::SLOTS + 4 * lane;
       for (int k = 0; k < count * (WIDE ? 1 : 2); ++k, ++n, j += kTile) {
         const int ks = n % kKStages, vs = n % kVStages;
@@ -1039,8 +1091,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (hf) commit(&sh->k_empty[stage]);
       return true;
     };
-    for (; ok && w.base + G_::SETUP < last; next_item<WIDE>(a, w)) {
-      const int count = steps_here<WIDE>(w, last);
+    for (; ok && w.base + G_::SETUP < last; next_item<G_>(a, w)) {
+      const int count = steps_here<G_>(w, last);
       ok = W.warp_wait(&sh->q_full[WIDE ? i : 0], items & 1) && scores(u) && scores(u + 1);
       ++items;
       for (int s = 0; ok && s < 2 * count; ++s, ++u) {
@@ -1166,7 +1218,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int64_t tok = beg + row / a.G;
       const int hq = h * a.G + row % a.G;
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + tok * a.qt + (int64_t)hq * a.qh;
-      const float cs = put_query(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, tid % kTile);
+      const float cs = put_queries(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32);
       float *pair_of = reinterpret_cast<float *>(&sh->rows[tid / 2]) + tid % 2;
       // a dead row gives exp2(-inf)
       pair_of[0] = live ? cs : 0.f;
