@@ -19,8 +19,8 @@
 // (at most 128 rows): they take the even and the odd slot tiles of the same
 // rows, so that one tile's softmax overlaps the other's products.
 //
-// Work: every CTA takes an equal share of all steps (walk below); parts of an item that
-// more than one CTA worked on are joined by the last of them.
+// Work: every CTA takes an equal share of all steps and item costs (below); what
+// several CTAs did of an item is joined by a second kernel.
 //
 // Every wait is bounded: after 2 s without progress the CTA sets
 // KVX_FLAG_TIMEOUT, all roles leave, copies and MMAs in flight are drained and
@@ -69,10 +69,9 @@ struct TcShared {
   // [group][half of the tile]; a wait on one names a phase whose predecessor is
   // known to be over, so its parity is enough
   uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2];
-  uint64_t join, verdict, spent, drain[2];
+  uint64_t join, spent, drain[2];
   uint32_t tmem_base;
   volatile int abort;
-  volatile int last;
   Share share;
   // the tile's largest value scale, as a power of two: its exponent for the
   // softmax, 2^7 over it for the conversion
@@ -89,8 +88,7 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 struct TcParams {
   AttendParams a;
-  int groups;          // row groups of max_new queries
-  int *arrived;        // [R][H][groups]
+  int grid;            // CTAs that share the work
   float *partial;      // [2 * grid][WIDE ? 1 : 2][part_size]: sums [rows][kD], maxima, totals
   float *scores;       // narrow: [R][H][rows][score_ld], base 2, or NULL
   int score_ld, slot_rows, part_size;   // rows kept of a part (narrow: G * max_new), its floats
@@ -195,7 +193,7 @@ struct Requests32 {
   bool good;
 };
 template <class G>
-__device__ __forceinline__ Requests32 look(const AttendParams &a, int r0) {
+__device__ __forceinline__ Requests32 look(const AttendParams &a, int r0, bool tell) {
   const int r = r0 + threadIdx.x % 32;
   Requests32 q = {};
   bool good = true;
@@ -206,7 +204,7 @@ __device__ __forceinline__ Requests32 look(const AttendParams &a, int r0) {
     q.fresh = (int)(end - q.beg);
     good = end >= q.beg && end - q.beg <= a.max_new && (r > 0 || q.beg == 0) && (r + 1 < a.req.R || end == a.req.ntok);
     if (!good) q.fresh = 0;
-    if (blockIdx.x == 0 && q.len != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
+    if (tell && q.len != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
   }
   if (a.G * a.max_new <= G::ROWS) {
     q.head = q.fresh > 0 ? G::SETUP + steps_of<G>(a, q.len, q.fresh, 0) : 0;
@@ -224,9 +222,9 @@ __device__ __forceinline__ Requests32 look(const AttendParams &a, int r0) {
   q.good = __all_sync(~0u, good);
   return q;
 }
-// One warp: the CTA's share.
+// One warp: the share of CTA `cta` of `ctas`.
 template <class G>
-__device__ void find_share(const AttendParams &a, Share &s) {
+__device__ void find_share(const AttendParams &a, int cta, int ctas, bool tell, Share &s) {
   const int lane = threadIdx.x % 32;
   s.good = true;
   s.T = 0;
@@ -235,18 +233,18 @@ __device__ void find_share(const AttendParams &a, Share &s) {
   s.w = {};
   Requests32 q;
   for (int r0 = 0; r0 < a.req.R; r0 += 32) {
-    q = look<G>(a, r0);
+    q = look<G>(a, r0, tell);
     s.good = s.good && q.good;
     s.T += __shfl_sync(~0u, q.upto, 31);
   }
   if (!s.good) return;
-  s.N = s.T < gridDim.x ? s.T : gridDim.x;
-  if (blockIdx.x >= s.N) return;
-  const int64_t at = blockIdx.x * s.T / s.N;
-  s.last = (blockIdx.x + 1) * s.T / s.N;
+  s.N = s.T < ctas ? s.T : ctas;
+  if (cta >= s.N) return;
+  const int64_t at = cta * s.T / s.N;
+  s.last = (cta + 1) * s.T / s.N;
   int64_t before = 0;
   for (int r0 = 0; r0 < a.req.R; r0 += 32) {
-    if (a.req.R > 32) q = look<G>(a, r0);      // otherwise it is at hand
+    if (a.req.R > 32) q = look<G>(a, r0, false);      // otherwise it is at hand
     const unsigned here = __ballot_sync(~0u, at < before + q.upto);
     if (!here) {
       before += __shfl_sync(~0u, q.upto, 31);
@@ -393,6 +391,9 @@ template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
+// The kernel is launched while the one before on its stream still runs: what that
+// one writes may be read after this.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -652,10 +653,107 @@ __device__ __noinline__ void keep_scores(uint32_t col, float *to, const float4 *
   }
 }
 
+// Join the parts of an item that CTAs c0 .. c0 + ctas - 1 left: rows first, first +
+// stride, ... of the warp.  A CTA keeps parts of an item that others began, and of
+// one that it began.  The parts' maxima and totals by the lanes, 32 parts at a time,
+// then their sums, of four rows at once so that enough is on its way.
+template <class G>
+__device__ __noinline__ void join_rows(const TcParams &p, const TcWalk &w, int c0, int ctas, int first, int stride, int rows) {
+  constexpr int B = 4;
+  const AttendParams &a = p.a;
+  const int lane = threadIdx.x % 32, parts = ctas * G::PARTS;
+  const auto part_at = [&](int c) {
+    const int64_t cta = c0 + c / G::PARTS;
+    return p.partial + ((cta * 2 + (c < G::PARTS)) * G::PARTS + c % G::PARTS) * (int64_t)p.part_size;
+  };
+  for (int r0 = first; r0 < rows; r0 += stride * B) {
+    float mm[B], ll[B], f[B];
+    float4 oo[B];
+    int rr[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      rr[k] = min(r0 + k * stride, rows - 1);   // a row beyond is formed twice
+      mm[k] = -INFINITY;
+      ll[k] = 0.f;
+      oo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int at = 0; at < parts; at += 32) {
+      const float *own = part_at(min(at + lane, parts - 1)) + p.slot_rows * kD;
+      float pm[B], pl[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        pm[k] = __ldcg(own + rr[k]);
+        pl[k] = __ldcg(own + p.slot_rows + rr[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        if (at + lane >= parts) {
+          pm[k] = -INFINITY;
+          pl[k] = 0.f;
+        }
+        float top = fmaxf(mm[k], pm[k]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        const float down = ex2(mm[k] - finite_or_0(top));
+        f[k] = ex2(pm[k] - finite_or_0(top));
+        mm[k] = top;
+        float sum = pl[k] * f[k];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        ll[k] = ll[k] * down + sum;
+        oo[k] = make_float4(oo[k].x * down, oo[k].y * down, oo[k].z * down, oo[k].w * down);
+      }
+      const int here = min(32, parts - at);
+#pragma unroll 2
+      for (int c = 0; c < here; ++c) {
+        const float *part = part_at(at + c) + lane * 4;
+        float4 y[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) y[k] = __ldcg(reinterpret_cast<const float4 *>(part + rr[k] * kD));
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+          const float g = __shfl_sync(~0u, f[k], c);
+          oo[k].x += y[k].x * g;
+          oo[k].y += y[k].y * g;
+          oo[k].z += y[k].z * g;
+          oo[k].w += y[k].w * g;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const int64_t row = (int64_t)w.group * G::ROWS + rr[k], tok = w.beg + row / a.G;
+      const int hq = w.h * a.G + (int)(row % a.G);
+      store_out(a, tok, hq, lane * 4, make_float2(oo[k].x, oo[k].y), mm[k], ll[k]);
+      store_out(a, tok, hq, lane * 4 + 2, make_float2(oo[k].z, oo[k].w), mm[k], ll[k]);
+    }
+  }
+}
+// The items that several CTAs worked on: block x looks after the boundary between
+// CTAs x and x + 1, where that is the first inside its item; block y after a slice
+// of the rows.
+template <class G>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcParams p) {
+  __shared__ Share share;
+  if (threadIdx.x < 32) {
+    Share s;
+    find_share<G>(p.a, blockIdx.x + 1, p.grid, false, s);
+    if (threadIdx.x == 0) share = s;
+  }
+  wait_for_kernel_before();
+  __syncthreads();
+  const TcWalk w = share.w;
+  if (!share.good || share.last < 0 || w.step == 0) return;   // nothing here, or an item begins here
+  const int64_t T = share.T, N = share.N, begin = w.base + G::SETUP;
+  const int c0 = (int)(((begin + 1) * N - 1) / T), c1 = (int)(((begin + w.steps) * N - 1) / T);   // of its first and last step
+  if (c0 != (int)blockIdx.x) return;
+  const int rows = (int)min((int64_t)G::ROWS, (int64_t)w.fresh * p.a.G - (int64_t)w.group * G::ROWS);
+  join_rows<G>(p, w, c0, c1 - c0 + 1, blockIdx.y * 8 + threadIdx.x / 32, gridDim.y * 8, rows);
+}
+
 // What a softmax group knows of its item when the item, or the CTA's part of it, ends.
 struct Item {
   TcWalk w;
-  int64_t T, N;
   int count, rows, row;
   bool live, warp_live;
   float m, l;
@@ -672,7 +770,6 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   const TcWalk &w = it.w;
   const uint32_t half = it.half, joins = it.joins;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t T = it.T, N = it.N;
   const int rows = it.rows, row = it.row;
   const bool live = it.live, warp_live = it.warp_live, whole = it.count == w.steps;
   const float m = it.m, l = it.l;
@@ -680,7 +777,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   // the result of the item, or this CTA's part of it
   if (!W.warp_wait(&sh->pv_done[i][(half - 1) & 1], (half - 1) >> 1 & 1)) return false;
   tc_fence_after();
-  // narrow: the parts of the item before have been read by all
+  // narrow: the parts of the item joined before have been read by all
   if (!WIDE && joins > 0 && !W.warp_wait(&sh->spent, (joins - 1) & 1)) return false;
   const float back = 1.f / 128.f;   // V carries 2^7
   const int64_t at = (int64_t)w.group * G_::ROWS + row;
@@ -734,82 +831,16 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
     }
   }
   if (!direct) {
-    // join: the CTA's groups first, then, of several CTAs, the last to come
-    __threadfence();
+    // narrow: an item that this CTA did alone is joined from its two groups here,
+    // what several CTAs worked on by the next kernel
+    if (WIDE || !whole) return true;
+    __threadfence_block();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&sh->join));
     if (!W.warp_wait(&sh->join, joins & 1)) return false;
-    // the CTAs of its first and its last step
-    const int64_t begin = w.base + G_::SETUP, c0 = ((begin + 1) * N - 1) / T, c1 = ((begin + w.steps) * N - 1) / T;
-    bool mine = whole;
-    if (!whole) {
-      if (tid == 0) {
-        int *arrived = p.arrived + ((int64_t)w.r * a.H + w.h) * p.groups + w.group;
-        __threadfence();
-        const bool all = atomicAdd(arrived, 1) == (int)(c1 - c0);
-        if (all) *arrived = 0;   // ready for the next call
-        __threadfence();
-        sh->last = all;
-        mbar_arrive(smem_addr(&sh->verdict));
-      }
-    } else if (tid == 0) {
-      sh->last = 1;
-      mbar_arrive(smem_addr(&sh->verdict));
-    }
-    if (!W.warp_wait(&sh->verdict, joins & 1)) return false;
-    mine = sh->last;
-    if (mine) {
-      __threadfence();
-      // a CTA keeps two parts: of an item that others began, and of one that it began
-      const int64_t s0 = (c0 * 2 + 1) * G_::PARTS, s1 = c0 * 2 * G_::PARTS;
-      const int parts = (int)(c1 - c0 + 1) * G_::PARTS;
-      const auto part_at = [&](int c) {
-        const int cta = c / G_::PARTS, sub = c % G_::PARTS;
-        return p.partial + ((cta ? s1 + (int64_t)cta * 2 * G_::PARTS : s0) + sub) * part_size;
-      };
-      // a warp a row: the parts' maxima and totals by the lanes, 32 parts at a
-      // time, then the sums of one part after another, several on their way
-      const int d = lane * 4;
-      for (int rr = warp; rr < rows; rr += 8) {
-        float mm = -INFINITY, ll = 0.f;
-        float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c0 = 0; c0 < parts; c0 += 32) {
-          const float *own = part_at(min(c0 + lane, parts - 1)) + p.slot_rows * kD + rr;
-          float pm = __ldcg(own), pl = __ldcg(own + p.slot_rows);
-          if (c0 + lane >= parts) {
-            pm = -INFINITY;
-            pl = 0.f;
-          }
-          float top = fmaxf(mm, pm);
-#pragma unroll
-          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-          const float down = ex2(mm - finite_or_0(top)), f = ex2(pm - finite_or_0(top));
-          mm = top;
-          pl *= f;
-#pragma unroll
-          for (int o = 16; o; o >>= 1) pl += __shfl_xor_sync(~0u, pl, o);
-          ll = ll * down + pl;
-          oo = make_float4(oo.x * down, oo.y * down, oo.z * down, oo.w * down);
-          const int here = min(32, parts - c0);
-#pragma unroll 8
-          for (int c = 0; c < here; ++c) {
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(part_at(c0 + c) + rr * kD + d));
-            const float fc = __shfl_sync(~0u, f, c);
-            oo.x += y.x * fc;
-            oo.y += y.y * fc;
-            oo.z += y.z * fc;
-            oo.w += y.w * fc;
-          }
-        }
-        const int64_t ar = (int64_t)w.group * G_::ROWS + rr;
-        const int64_t tk = w.beg + ar / a.G;
-        const int hh = w.h * a.G + (int)(ar % a.G);
-        store_out(a, tk, hh, d, make_float2(oo.x, oo.y), mm, ll);
-        store_out(a, tk, hh, d + 2, make_float2(oo.z, oo.w), mm, ll);
-      }
-    }
+    join_rows<G_>(p, w, blockIdx.x, 1, warp, 8, rows);
     __syncwarp();
-    if (!WIDE && lane == 0) mbar_arrive(smem_addr(&sh->spent));
+    if (lane == 0) mbar_arrive(smem_addr(&sh->spent));
   }
   return true;
 }
@@ -850,7 +881,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     mbar_init(smem_addr(&sh->join), 8);
-    mbar_init(smem_addr(&sh->verdict), 1);
     mbar_init(smem_addr(&sh->spent), 8);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -863,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kLoadWarp) {
     Share share;
-    find_share<G_>(a, share);
+    find_share<G_>(a, blockIdx.x, gridDim.x, blockIdx.x == 0, share);
     if (lane == 0) {
       sh->share = share;
       if (!share.good && blockIdx.x == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
@@ -875,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh->tmem_base;
   const Waiter W{sh, a.status};
   TcWalk w = sh->share.w;
-  const int64_t T = sh->share.T, N = sh->share.N, last = sh->share.last;
+  const int64_t last = sh->share.last;
 
   if (warp < 8) {
     more_registers<kSoftmaxRegs>();
@@ -952,9 +982,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // the result of the item, or this CTA's part of it
-      const Item it{w, T, N, count, rows, row, live, warp_live, m, cs != cs ? cs : l, o_col, half, joins};
+      const Item it{w, count, rows, row, live, warp_live, m, cs != cs ? cs : l, o_col, half, joins};
       if (!finish_item<WIDE>(p, sh, it, i)) goto done;
-      joins += !WIDE || count < w.steps;
+      joins += !WIDE && count == w.steps;
     }
   done:;
   } else if (warp < kLoadWarp) {
@@ -1347,17 +1377,15 @@ typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, voi
                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 struct TcShape {
-  int rows, groups, slot_rows, part_size, grid, score_ld, box;
+  int slot_rows, part_size, grid, score_ld, box;
   bool wide, spool;
-  size_t arrived, partial, lse, scores, bytes;
+  size_t partial, lse, scores, bytes;
 };
 TcShape tc_shape(const kvx_attend8_args *a) {
   TcShape s;
   const int64_t G = a->q_heads / a->cache.heads, most = G * a->max_new;
   s.wide = most > kTile;
-  s.rows = s.wide ? 2 * kTile : kTile;
-  s.groups = (int)((most + s.rows - 1) / s.rows);
-  s.slot_rows = s.wide ? s.rows : (int)most;
+  s.slot_rows = s.wide ? Wide::ROWS : (int)most;
   s.part_size = (s.slot_rows * (kD + 2) + 3) / 4 * 4;
   s.grid = 152;                        // one CTA an SM
   s.score_ld = (a->max_len + 255) / 256 * 256;
@@ -1366,8 +1394,7 @@ TcShape tc_shape(const kvx_attend8_args *a) {
   s.spool = a->weights && !s.wide;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t items = (size_t)a->num_requests * a->cache.heads;
-  s.arrived = 0;
-  s.partial = up(items * s.groups * 4);
+  s.partial = 0;
   s.lse = s.partial + up((size_t)2 * s.grid * (s.wide ? 1 : 2) * s.part_size * 4);
   s.scores = s.lse + up((size_t)a->ntok * a->q_heads * 4);
   s.bytes = s.scores + (s.spool ? up(items * s.slot_rows * s.score_ld * 4) : 0);
@@ -1385,13 +1412,31 @@ bool encode(CUtensorMap *map, const kvx_cache8 &c, const void *base, int box) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launch beside the end of the kernel before (which the kernel waits for itself).
+template <class... P, class... A>
+kvx_status launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? KVX_OK : KVX_ERR_CUDA;
+}
+
 template <bool WIDE>
-kvx_status launch(const TcParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int grid, cudaStream_t s) {
+kvx_status launch(const TcParams &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
+  using G = std::conditional_t<WIDE, Wide, Narrow>;
   if (cudaFuncSetAttribute(attend_tc_kernel<WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
       cudaSuccess)
     return KVX_ERR_CUDA;
-  attend_tc_kernel<WIDE><<<grid, kThreads, kSmemBytes, s>>>(p, mk, mv);
-  return launched();
+  attend_tc_kernel<WIDE><<<p.grid, kThreads, kSmemBytes, s>>>(p, mk, mv);
+  if (const kvx_status st = launched()) return st;
+  return launch_after(join_kernel<G>, dim3(p.grid - 1, (p.slot_rows + 31) / 32), 256, 0, s, p);
 }
 
 }  // namespace
@@ -1411,8 +1456,7 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   TcParams p;
   p.a = a;
   if (!p.a.lse) p.a.lse = (float *)(ws + sh.lse);
-  p.groups = sh.groups;
-  p.arrived = (int *)(ws + sh.arrived);
+  p.grid = sh.grid;
   p.partial = (float *)(ws + sh.partial);
   p.scores = sh.spool ? (float *)(ws + sh.scores) : nullptr;
   p.score_ld = sh.score_ld;
@@ -1421,7 +1465,7 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   p.box = sh.box;
   p.vec_q = aligned_to(a.q, 16) && (a.qt | a.qh) % 8 == 0;
   p.vec_out = aligned_to(a.out, 16) && (a.ot | a.oh) % 8 == 0;
-  const kvx_status st = sh.wide ? launch<true>(p, mk, mv, sh.grid, s) : launch<false>(p, mk, mv, sh.grid, s);
+  const kvx_status st = sh.wide ? launch<true>(p, mk, mv, s) : launch<false>(p, mk, mv, s);
   if (st != KVX_OK || !a.weights || a.max_len == 0) return st;
   if (sh.wide) {
     // as few slot tiles a CTA as lets all run at once, 16 at most
