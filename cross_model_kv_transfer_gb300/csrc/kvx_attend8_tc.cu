@@ -90,7 +90,7 @@ struct TcParams {
   AttendParams a;
   int grid;            // CTAs that share the work
   float *partial;      // [2 * grid][WIDE ? 1 : 2][part_size]: sums [rows][kD], maxima, totals
-  float *scores;       // narrow: [R][H][rows][score_ld], base 2, or NULL
+  float *scores;       // base 2, or NULL; narrow: [R][H][rows][score_ld], columns: [R][H][score_ld][slot_rows]
   int score_ld, slot_rows, part_size;   // rows kept of a part (narrow: G * max_new), its floats
   int box;             // slots of one TMA box
   int vec_q, vec_out;
@@ -138,6 +138,11 @@ struct Wide {
   static constexpr int ROWS = 2 * kTile, SLOTS = kTile;   // of an item, of a step
   static constexpr int PARTS = 1;                         // results that a CTA keeps for an item
   static constexpr int SETUP = 5;
+};
+// Few columns (kernel further down): rows are the columns of S^T.
+template <int NC>
+struct Columns {
+  static constexpr int ROWS = NC, SLOTS = 2 * kTile, PARTS = 2, SETUP = 2;
 };
 struct Narrow {
   static constexpr int ROWS = kTile, SLOTS = 2 * kTile, PARTS = 2, SETUP = 2;
@@ -561,12 +566,12 @@ __device__ __noinline__ float query_factor(const AttendParams &a, bool vec, cons
   const float top = largest(x);
   return row_factor(a, top, pow2_scale(top));
 }
-// 32 query rows of a warp as two e4m3 parts in the swizzled K-major tile (from row
-// `first` of the tile on; `src` is the lane's own row).  Half a warp loads a row at
+// 32 query rows of a warp as two e4m3 parts, `part` bytes apart, in the swizzled
+// K-major tile (from row `first` of the tile on; `src` is the lane's own row).  Half a warp loads a row at
 // a time.  Returns the lane's factor on its row's scores (its sign is in the
 // parts).
 __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
-                                          unsigned char *tile, int first) {
+                                          unsigned char *tile, int first, int part) {
   const int lane = threadIdx.x % 32, c = lane % 16;      // 8 dimensions
   uint4 x[16];
 #pragma unroll
@@ -616,7 +621,7 @@ __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const
     const int row = first + 2 * i + lane / 16;
     unsigned char *to = tile + row * kD + ((c / 2 ^ (row & 7)) << 4) + (c & 1) * 8;
     *reinterpret_cast<uint2 *>(to) = make_uint2(p1[0], p1[1]);
-    *reinterpret_cast<uint2 *>(to + kTileBytes) = make_uint2(p2[0], p2[1]);
+    *reinterpret_cast<uint2 *>(to + part) = make_uint2(p2[0], p2[1]);
   }
   return row_factor(a, mine, pow2_scale(mine));
 }
@@ -656,10 +661,9 @@ __device__ __noinline__ void keep_scores(uint32_t col, float *to, const float4 *
 // Join the parts of an item that CTAs c0 .. c0 + ctas - 1 left: rows first, first +
 // stride, ... of the warp.  A CTA keeps parts of an item that others began, and of
 // one that it began.  The parts' maxima and totals by the lanes, 32 parts at a time,
-// then their sums, of four rows at once so that enough is on its way.
-template <class G>
+// then their sums, of B rows at once.
+template <class G, int B>
 __device__ __noinline__ void join_rows(const TcParams &p, const TcWalk &w, int c0, int ctas, int first, int stride, int rows) {
-  constexpr int B = 4;
   const AttendParams &a = p.a;
   const int lane = threadIdx.x % 32, parts = ctas * G::PARTS;
   const auto part_at = [&](int c) {
@@ -704,7 +708,7 @@ __device__ __noinline__ void join_rows(const TcParams &p, const TcWalk &w, int c
         oo[k] = make_float4(oo[k].x * down, oo[k].y * down, oo[k].z * down, oo[k].w * down);
       }
       const int here = min(32, parts - at);
-#pragma unroll 2
+#pragma unroll (8 / B)
       for (int c = 0; c < here; ++c) {
         const float *part = part_at(at + c) + lane * 4;
         float4 y[B];
@@ -748,7 +752,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcPar
   const int c0 = (int)(((begin + 1) * N - 1) / T), c1 = (int)(((begin + w.steps) * N - 1) / T);   // of its first and last step
   if (c0 != (int)blockIdx.x) return;
   const int rows = (int)min((int64_t)G::ROWS, (int64_t)w.fresh * p.a.G - (int64_t)w.group * G::ROWS);
-  join_rows<G>(p, w, c0, c1 - c0 + 1, blockIdx.y * 8 + threadIdx.x / 32, gridDim.y * 8, rows);
+  join_rows<G, G::ROWS >= 128 ? 4 : 1>(p, w, c0, c1 - c0 + 1, blockIdx.y * 8 + threadIdx.x / 32, gridDim.y * 8, rows);
 }
 
 // What a softmax group knows of its item when the item, or the CTA's part of it, ends.
@@ -838,7 +842,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&sh->join));
     if (!W.warp_wait(&sh->join, joins & 1)) return false;
-    join_rows<G_>(p, w, blockIdx.x, 1, warp, 8, rows);
+    join_rows<G_, 1>(p, w, blockIdx.x, 1, warp, 8, rows);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&sh->spent));
   }
@@ -931,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
       float m = -INFINITY, l = 0.f, cs;
       if (WIDE || i == 0) {
-        cs = put_queries(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32);
+        cs = put_queries(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes);
         fence_async_proxy();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[i]));
@@ -1177,6 +1181,519 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
   a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
 }
 
+// --- few columns --------------------------------------------------------------------
+// At most 16 (query, head of the group) pairs: one token of a group of heads, or a
+// few.  128 rows of which 8 count would cost the shared memory more than HBM can
+// bring, so here the slots are the rows and the pairs the columns, and neither K nor
+// V is converted: both products take the codes as they lie in the cache.
+//   S^T = K (Q1 + Q2)^T   the queries in two e4m3 parts, a slot to a lane,
+//   O^T += V^T P^T        P in three e5m2 parts (3 + 3 + 3 bits: an f16 value to
+//                         2^-10 of it), formed from the top bytes of an f16 and of
+//                         what it leaves; V transposed by the descriptor.
+// A slot's probabilities carry its block's value scale (as a power in the
+// exponent), so that O needs none; sums without it are kept beside.  Four warps
+// share a maximum for each column: they vote on a tile, and only where one of them
+// exceeds it by 2^4 do they agree on a new one and scale O down.
+// Two groups of four warps take the even and the odd slot tiles.
+constexpr int kCkStages = 5, kCvStages = 5, kColThreads = 11 * 32;
+constexpr int kColLoad = 8, kColMma = 9;
+constexpr float kColBias = 11.f, kColSlack = 4.f;   // P at most 2^15, nothing lost above 2^-28 of the maximum
+constexpr int kColQBytes = 32 * kD, kColPBytes = kTile * 16;   // a part of the queries, of a tile's probabilities
+struct ColShared {
+  uint64_t k_full[kCkStages], k_empty[kCkStages], v_full[kCvStages], v_empty[kCvStages];
+  uint64_t q_full, item_done, s_full[2][2], p_full[2][2], pv_done[2][2], vote[2], agree[2], join, spent, drain[2];
+  uint32_t tmem_base;
+  volatile int abort;
+  Share share;
+  volatile uint32_t over[2][2];
+  uint32_t mask[kCkStages];
+  float ks[kCkStages][kTile / 4], vs[kCkStages][kTile / 4];
+  float cs[2][16];             // of the item (in turn) and column
+  float warp_max[2][4][16], warp_sum[2][4][16];
+};
+constexpr size_t kColSmem = 1024 + (kCkStages + kCvStages) * (size_t)kTileBytes + 2 * kColQBytes + 2 * 2 * 3 * kColPBytes +
+                            sizeof(ColShared);
+static_assert(kColSmem <= 227 * 1024, "shared memory");
+// D fp32, M = 128, N = 16; e4m3 both K-major, and e4m3 x e5m2 both as they lie in
+// memory (MN-major).
+constexpr uint32_t kIdescColS = (1u << 4) | (2u << 17) | (8u << 24);
+constexpr uint32_t kIdescColO = (1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) | (2u << 17) | (8u << 24);
+
+// 32 slots deep each: four steps for each of two query parts, for each of three
+// parts of P.
+__device__ __forceinline__ void mma_col_s(uint32_t d, uint64_t k, uint64_t q) {
+  asm volatile(
+      "{\n.reg .pred e, f, t;\n.reg .b32 r;\n.reg .b64 a1, a2, a3, b1, b2, b3, b4, b5, b6, b7;\n"
+      "elect.sync r|e, 0xffffffff;\n"
+      "setp.ne.u32 f, 0, 0;\nsetp.eq.u32 t, 0, 0;\n"
+      "add.u64 a1, %1, 2; add.u64 a2, %1, 4; add.u64 a3, %1, 6;\n"
+      "add.u64 b1, %2, 2; add.u64 b2, %2, 4; add.u64 b3, %2, 6; add.u64 b4, %2, %4;\n"
+      "add.u64 b5, b4, 2; add.u64 b6, b4, 4; add.u64 b7, b4, 6;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, b4, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b5, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b6, %3, t;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b7, %3, t;\n}\n" ::"r"(d),
+      "l"(k), "l"(q), "r"(kIdescColS), "l"((uint64_t)(kColQBytes >> 4))
+      : "memory");
+}
+__device__ __forceinline__ void mma_col_o(uint32_t d, uint64_t v, uint64_t p, bool add) {
+#pragma unroll
+  for (int part = 0; part < 3; ++part)
+    asm volatile(
+        "{\n.reg .pred e, f, t;\n.reg .b32 r;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        "elect.sync r|e, 0xffffffff;\n"
+        "setp.ne.u32 f, %4, 0;\nsetp.eq.u32 t, 0, 0;\n"
+        "add.u64 a1, %1, 256; add.u64 a2, %1, 512; add.u64 a3, %1, 768;\n"
+        "add.u64 b1, %2, 32; add.u64 b2, %2, 64; add.u64 b3, %2, 96;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n}\n" ::"r"(d),
+        "l"(v), "l"(p + (uint64_t)part * (kColPBytes >> 4)), "r"(kIdescColO), "r"((uint32_t)(add || part > 0))
+        : "memory");
+}
+// V as operand [slots][128 dimensions], 128-byte swizzle: one 128-dimension group,
+// 8-slot groups 1 KB apart.
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(1024 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+// P as operand [slots][16 columns], no swizzle: 8-slot groups 128 bytes apart.
+__device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(kColPBytes >> 4) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\ntcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld8_wait(uint32_t addr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\ntcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(addr)
+      : "memory");
+}
+template <int NC>
+__device__ __forceinline__ void ld_columns(uint32_t addr, uint32_t (&v)[NC]) {
+  if constexpr (NC == 8) tc_ld8_wait(addr, v);
+  else tc_ld16(addr, v);
+}
+template <int NC>
+__device__ __forceinline__ void st_columns(uint32_t addr, const uint32_t (&v)[NC]) {
+  if constexpr (NC == 8) tc_st8(addr, v);
+  else tc_st16(addr, v);
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int NC>
+__global__ void __launch_bounds__(kColThreads, 1)
+    columns_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v) {
+  using G_ = Columns<NC>;
+  extern __shared__ unsigned char raw[];
+  unsigned char *kbuf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *vbuf = kbuf + kCkStages * kTileBytes, *qbuf = vbuf + kCvStages * kTileBytes, *pbuf = qbuf + 2 * kColQBytes;
+  ColShared *sh = reinterpret_cast<ColShared *>(pbuf + 2 * 2 * 3 * kColPBytes);
+  const AttendParams &a = p.a;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  if (tid == 0) {
+    for (int i = 0; i < kCkStages; ++i) {
+      mbar_init(smem_addr(&sh->k_full[i]), 32);
+      mbar_init(smem_addr(&sh->k_empty[i]), 1 + 4);
+    }
+    for (int i = 0; i < kCvStages; ++i) {
+      mbar_init(smem_addr(&sh->v_full[i]), 32);
+      mbar_init(smem_addr(&sh->v_empty[i]), 1);
+    }
+    mbar_init(smem_addr(&sh->q_full), 1);
+    mbar_init(smem_addr(&sh->item_done), 8);
+    for (int i = 0; i < 2; ++i) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_addr(&sh->s_full[i][b]), 1);
+        mbar_init(smem_addr(&sh->p_full[i][b]), 4);
+        mbar_init(smem_addr(&sh->pv_done[i][b]), 1);
+        sh->over[i][b] = 0;
+      }
+      mbar_init(smem_addr(&sh->vote[i]), 4);
+      mbar_init(smem_addr(&sh->agree[i]), 4);
+      mbar_init(smem_addr(&sh->drain[i]), 1);
+    }
+    mbar_init(smem_addr(&sh->join), 8);
+    mbar_init(smem_addr(&sh->spent), 8);
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kColMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(
+                     smem_addr(&sh->tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == kColLoad) {
+    Share share;
+    find_share<G_>(a, blockIdx.x, gridDim.x, blockIdx.x == 0, share);
+    if (lane == 0) {
+      sh->share = share;
+      if (!share.good && blockIdx.x == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  const WaiterT<ColShared> W{sh, a.status};
+  TcWalk w = sh->share.w;
+  const int64_t last = sh->share.last;
+  // scores of group i, buffer b; sums of group i
+  const auto s_at = [&](int i, int b) { return tmem + (i * 2 + b) * 16; };
+  const auto o_at = [&](int i) { return tmem + 64 + i * 16; };
+
+  if (warp < 8) {
+    const int i = warp / 4, in = warp % 4 * 32 + lane;      // group; slot of the tile, dimension of the sums
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    uint32_t t = 0, items = 0, joins = 0, agreed = 0;       // tiles of the group, items, joins, agreements so far
+    int ks = i;
+    uint32_t k_phase = 0;
+    for (; w.base + G_::SETUP < last; next_item<G_>(a, w), ++items) {
+      const int count = steps_here<G_>(w, last);
+      const int64_t row0 = (int64_t)w.group * NC;
+      const int rows = (int)min((int64_t)NC, (int64_t)w.fresh * a.G - row0);
+      if (warp == 0) {
+        // both groups have formed the last scores of the item before
+        if (items > 0 && !W.warp_wait(&sh->item_done, (items - 1) & 1)) goto done;
+        const int64_t tok = (row0 + lane) / a.G;
+        const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
+                                   (int64_t)(w.h * a.G + (int)((row0 + lane) % a.G)) * a.qh;
+        const float f = put_queries(a, p.vec_q, src, lane < rows, qbuf, 0, kColQBytes);
+        if (lane < 16) sh->cs[items & 1][lane] = f;
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh->q_full));
+      }
+      float cs[NC], m[NC], l[NC];
+      if (!W.warp_wait(&sh->q_full, items & 1)) goto done;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        cs[c] = sh->cs[items & 1][c];
+        m[c] = -INFINITY;
+        l[c] = 0.f;
+      }
+      const int low = (int)(w.len - w.fresh + row0 / a.G);   // last slot that the first column sees
+      float *spool = p.scores ? p.scores + ((int64_t)w.r * a.H + w.h) * p.score_ld * (int64_t)NC : nullptr;
+      int j = w.step * G_::SLOTS + i * kTile + in;
+      for (int s = 0; s < count; ++s, ++t) {
+        const int b = t & 1;
+        if (!W.warp_wait(&sh->k_full[ks], k_phase)) goto done;
+        if (!W.warp_wait(&sh->s_full[i][b], t >> 1 & 1)) goto done;
+        tc_fence_after();
+        const float f = sh->ks[ks][in / 4], v = sh->vs[ks][in / 4];
+        const bool there = sh->mask[ks] >> (in / 4) & 1;
+        // value scales below 2^-96 count as that (their values vanish beside any other)
+        const float lv = there ? fmaxf(lg2(v), -96.f) : 0.f;
+        uint32_t x[NC];
+        ld_columns<NC>(s_at(i, b) + lanes, x);
+        float y[NC];           // scores, base 2
+        const bool masked = __any_sync(~0u, !there || j > low);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          y[c] = __uint_as_float(x[c]) * f * cs[c];
+          if (masked && (!there || j > (int)(w.len - w.fresh + (row0 + c) / a.G) || c >= rows)) y[c] = -INFINITY;
+        }
+        if (spool && j < p.score_ld) {
+#pragma unroll
+          for (int c = 0; c < NC; c += 4)
+            *reinterpret_cast<float4 *>(spool + (int64_t)j * NC + c) = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
+        }
+        bool over = false;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          y[c] += lv;
+          over = over || y[c] > m[c] + kColSlack;
+        }
+        if (__any_sync(~0u, over) && lane == 0) sh->over[i][b] = t + 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh->vote[i]));
+        if (!W.warp_wait(&sh->vote[i], t & 1)) goto done;
+        if (sh->over[i][b] == t + 1) {
+          // seldom: a new maximum for all columns, and O scaled down to it
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            float top = y[c];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+            if (lane == 0) sh->warp_max[i][warp % 4][c] = top;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh->agree[i]));
+          if (!W.warp_wait(&sh->agree[i], agreed++ & 1)) goto done;
+          float down[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            float top = m[c];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, sh->warp_max[i][k][c]);
+            down[c] = ex2(m[c] - finite_or_0(top));
+            m[c] = top;
+            l[c] *= down[c];
+          }
+          if (s > 0) {
+            if (!W.warp_wait(&sh->pv_done[i][(t - 1) & 1], (t - 1) >> 1 & 1)) goto done;
+            tc_fence_after();
+            uint32_t o[NC];
+            ld_columns<NC>(o_at(i) + lanes, o);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * down[c]);
+            st_columns<NC>(o_at(i) + lanes, o);
+            tc_wait_st();
+          }
+        }
+        // probabilities times the value scale, and sums without it
+        const float without = ex2(-lv);
+        uint32_t h[NC / 2];
+#pragma unroll
+        for (int c = 0; c < NC; c += 2) {
+          const float e0 = ex2(y[c] + (kColBias - finite_or_0(m[c]))), e1 = ex2(y[c + 1] + (kColBias - finite_or_0(m[c + 1])));
+          l[c] = fmaf(e0, without, l[c]);
+          l[c + 1] = fmaf(e1, without, l[c + 1]);
+          h[c / 2] = f16x2(e0, e1);
+        }
+        if (__any_sync(~0u, !there || j >= w.len)) {
+          // slots of no block of the pool or beyond the length: zero values, so that
+          // their zero probabilities meet no NaN
+          const uint32_t tile = 2 * t + i, vstage = tile % kCvStages;
+          if (!W.warp_wait(&sh->v_full[vstage], tile / kCvStages & 1)) goto done;
+          if (!there || j >= w.len) {
+            uint4 *row = reinterpret_cast<uint4 *>(vbuf + vstage * kTileBytes + in * kD);
+#pragma unroll
+            for (int k = 0; k < kD / 16; ++k) row[k] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        // the buffer's last products are done
+        if (t >= 2 && !W.warp_wait(&sh->pv_done[i][b], (t - 2) >> 1 & 1)) goto done;
+        unsigned char *to = pbuf + (i * 2 + b) * 3 * kColPBytes + in * 16;
+        uint32_t part[3][4] = {};
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) {
+          const uint32_t a0 = h[c / 2], a1 = h[c / 2 + 1];
+          const uint32_t r0 = sub_f16x2(a0, a0 & 0xff00ff00u), r1 = sub_f16x2(a1, a1 & 0xff00ff00u);
+          const uint32_t q0 = sub_f16x2(r0, r0 & 0xff00ff00u), q1 = sub_f16x2(r1, r1 & 0xff00ff00u);
+          part[0][c / 4] = __byte_perm(a0, a1, 0x7531);
+          part[1][c / 4] = __byte_perm(r0, r1, 0x7531);
+          part[2][c / 4] = e5m2x2(q0) | e5m2x2(q1) << 16;
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4 *>(to + k * kColPBytes) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
+        fence_async_proxy();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&sh->p_full[i][b]));
+          mbar_arrive(smem_addr(&sh->k_empty[ks]));
+        }
+        j += G_::SLOTS;
+        ks += 2;
+        if (ks >= kCkStages) {
+          ks -= kCkStages;
+          k_phase ^= 1;
+        }
+      }
+      if (lane == 0) mbar_arrive(smem_addr(&sh->item_done));
+      // this group's part of the item
+      if (!W.warp_wait(&sh->pv_done[i][(t - 1) & 1], (t - 1) >> 1 & 1)) goto done;
+      if (joins > 0 && !W.warp_wait(&sh->spent, (joins - 1) & 1)) goto done;
+      tc_fence_after();
+      uint32_t o[NC];
+      ld_columns<NC>(o_at(i) + lanes, o);
+      float *slot = p.partial + (((int64_t)blockIdx.x * 2 + (w.step == 0)) * 2 + i) * (int64_t)p.part_size;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (c < rows) slot[c * kD + in] = __uint_as_float(o[c]);
+        float sum = l[c];
+#pragma unroll
+        for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
+        if (lane == 0) sh->warp_sum[i][warp % 4][c] = sum;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh->agree[i]));
+      if (!W.warp_wait(&sh->agree[i], agreed++ & 1)) goto done;
+      if (warp % 4 == 0 && lane < rows) {
+        float mine = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) mine = lane == c ? m[c] : mine;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum += sh->warp_sum[i][k][lane];
+        slot[p.slot_rows * kD + lane] = mine - kColBias;
+        slot[p.slot_rows * (kD + 1) + lane] = sum;
+      }
+      if (count == w.steps) {
+        // an item of this CTA alone: its two parts
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh->join));
+        if (!W.warp_wait(&sh->join, joins & 1)) goto done;
+        join_rows<G_, 1>(p, w, blockIdx.x, 1, warp, 8, rows);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh->spent));
+        ++joins;
+      }
+    }
+  done:;
+  } else if (warp == kColLoad) {
+    // A tile's blocks are looked up two tiles ahead, their scales one: nothing
+    // waits for them.
+    struct Tile {
+      int page, row;
+      bool asked;
+    };
+    int k = 0, end = 0, j = 0;      // tile of the item, tiles of the item in this CTA, the lane's first slot
+    bool more = w.base + G_::SETUP < last;
+    const auto enter = [&]() {
+      k = 0;
+      end = 2 * steps_here<G_>(w, last);
+      j = w.step * G_::SLOTS + 4 * lane;
+    };
+    if (more) enter();
+    const auto next = [&](Tile &x, int &h) {
+      x.asked = more;
+      x.page = -1;
+      x.row = 0;
+      h = w.h;
+      if (!more) return;
+      if (j < w.len) {
+        const uint32_t block = block_of(a, j);
+        x.row = j - block * a.bs;                  // in the block, until the page is known
+        x.page = page_of(a, w.r, block);
+        if (x.page < 0) raise(a.status, KVX_FLAG_BAD_BLOCK);
+      }
+      j += kTile;
+      if (++k == end) {
+        next_item<G_>(a, w);
+        more = w.base + G_::SETUP < last;
+        if (more) enter();
+      }
+    };
+    Tile t0, t1;
+    int h0, h1;
+    float ks0 = 0.f, vs0 = 0.f;
+    const auto scales = [&](const Tile &x, int h, float &f, float &g) {
+      f = g = 0.f;
+      if (x.page < 0) return;
+      const uint32_t sb = (uint32_t)x.page * a.H + h;
+      f = __ldg(a.ks + sb);
+      g = __ldg(a.vs + sb);
+    };
+    next(t0, h0);
+    scales(t0, h0, ks0, vs0);
+    next(t1, h1);
+    uint32_t n = 0;
+    for (; t0.asked; ++n) {
+      const int ks = n % kCkStages, vs = n % kCvStages;
+      const int row = t0.page < 0 ? 0 : (int)(((uint32_t)t0.page * a.H + h0) * a.bs + t0.row);
+      const unsigned mask = __ballot_sync(~0u, t0.page >= 0);
+      const float kscale = ks0, vscale = vs0;
+      // what the next tiles need, on its way
+      t0 = t1;
+      h0 = h1;
+      scales(t0, h0, ks0, vs0);
+      next(t1, h1);
+      const int per = p.box / 4, boxes = kTile / p.box;     // lanes a box, boxes
+      const int from = __shfl_sync(~0u, row, lane < boxes ? lane * per : 0);
+      const bool there = lane < boxes && (mask >> (lane * per) & 1);
+      const uint32_t bytes = __popc(__ballot_sync(~0u, there)) * (uint32_t)p.box * kD;
+      if (!W.warp_wait(&sh->k_empty[ks], (n / kCkStages & 1) ^ 1)) goto ld_done;
+      sh->ks[ks][lane] = kscale;
+      sh->vs[ks][lane] = vscale;
+      if (lane == 0) {
+        sh->mask[ks] = mask;
+        mbar_expect_tx(smem_addr(&sh->k_full[ks]), bytes);
+      }
+      __syncwarp();
+      if (there)
+        tma_load_2d(smem_addr(kbuf + ks * kTileBytes + lane * p.box * kD), &map_k, 0, from, smem_addr(&sh->k_full[ks]));
+      if (lane != 0) mbar_arrive(smem_addr(&sh->k_full[ks]));
+      if (!W.warp_wait(&sh->v_empty[vs], (n / kCvStages & 1) ^ 1)) goto ld_done;
+      if (lane == 0) mbar_expect_tx(smem_addr(&sh->v_full[vs]), bytes);
+      __syncwarp();
+      if (there)
+        tma_load_2d(smem_addr(vbuf + vs * kTileBytes + lane * p.box * kD), &map_v, 0, from, smem_addr(&sh->v_full[vs]));
+      if (lane != 0) mbar_arrive(smem_addr(&sh->v_full[vs]));
+    }
+  ld_done:
+    __syncwarp();
+    if (lane == 0) {
+      for (uint32_t x = n > kCkStages ? n - kCkStages : 0; x < n; ++x) drain_wait(&sh->k_full[x % kCkStages], x / kCkStages & 1);
+      for (uint32_t x = n > kCvStages ? n - kCvStages : 0; x < n; ++x) drain_wait(&sh->v_full[x % kCvStages], x / kCvStages & 1);
+      if (sh->abort) drain_wait(&sh->k_full[n % kCkStages], n / kCkStages & 1);
+    }
+  } else {
+    const int i = warp - kColMma;
+    const uint64_t q0 = sw128_desc(smem_addr(qbuf)), k0 = sw128_desc(smem_addr(kbuf)), v0 = v_desc(smem_addr(vbuf));
+    const uint64_t p0 = p_desc(smem_addr(pbuf + i * 2 * 3 * kColPBytes));
+    uint32_t items = 0, t = 0;
+    bool ok = true, issued = false;
+    const auto scores = [&](uint32_t t) {
+      const uint32_t tile = 2 * t + i, stage = tile % kCkStages;
+      if (!W.warp_wait(&sh->k_full[stage], tile / kCkStages & 1)) return false;
+      tc_fence_after();
+      mma_col_s(s_at(i, t & 1), k0 + (uint64_t)(stage * kTileBytes >> 4), q0);
+      issued = true;
+      commit(&sh->s_full[i][t & 1]);
+      commit(&sh->k_empty[stage]);
+      return true;
+    };
+    for (; ok && w.base + G_::SETUP < last; next_item<G_>(a, w)) {
+      const int count = steps_here<G_>(w, last);
+      ok = W.warp_wait(&sh->q_full, items & 1) && scores(t) && (count == 1 || scores(t + 1));
+      ++items;
+      for (int s = 0; ok && s < count; ++s, ++t) {
+        const uint32_t tile = 2 * t + i, stage = tile % kCvStages;
+        ok = W.warp_wait(&sh->v_full[stage], tile / kCvStages & 1) && W.warp_wait(&sh->p_full[i][t & 1], t >> 1 & 1);
+        if (!ok) break;
+        tc_fence_after();
+        mma_col_o(o_at(i), v0 + (uint64_t)(stage * kTileBytes >> 4), p0 + (uint64_t)((t & 1) * 3 * kColPBytes >> 4), s > 0);
+        commit(&sh->pv_done[i][t & 1]);
+        commit(&sh->v_empty[stage]);
+        if (s + 2 < count) ok = scores(t + 2);   // its buffer's scores were read before P came
+      }
+    }
+    if (issued) {
+      commit(&sh->drain[i]);
+      if (lane == 0) drain_wait(&sh->drain[i], 0);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kColMma)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
+}
+
 // --- accumulated weights of wide calls -------------------------------------------
 // weights[r][h][j] += sum over the rows that see slot j of exp2(score - lse).
 // The scores are formed again, transposed (S^T = K Q^T, slots in the lanes), so
@@ -1248,7 +1765,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int64_t tok = beg + row / a.G;
       const int hq = h * a.G + row % a.G;
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + tok * a.qt + (int64_t)hq * a.qh;
-      const float cs = put_queries(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32);
+      const float cs = put_queries(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32, kTileBytes);
       float *pair_of = reinterpret_cast<float *>(&sh->rows[tid / 2]) + tid % 2;
       // a dead row gives exp2(-inf)
       pair_of[0] = live ? cs : 0.f;
@@ -1371,6 +1888,32 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
+// The same from the scores of few columns, [score_ld][slot_rows].
+__global__ void __launch_bounds__(256) weights_of_columns_kernel(const __grid_constant__ TcParams p) {
+  const AttendParams &a = p.a;
+  __shared__ float lse2[16];
+  const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r), j = blockIdx.x * 256 + threadIdx.x;
+  const int64_t beg = a.req.begin(r);
+  const bool good = requests_ok(a);
+  const int rows = good ? (int)(a.req.begin(r + 1) - beg) * a.G : 0;
+  wait_for_kernel_before();
+  if (threadIdx.x < rows)
+    lse2[threadIdx.x] = a.lse[(beg + threadIdx.x / a.G) * a.Hq + h * a.G + threadIdx.x % a.G] * kLog2e;
+  __syncthreads();
+  if (j >= len || rows == 0) return;
+  const float *x = p.scores + (((int64_t)r * a.H + h) * p.score_ld + j) * p.slot_rows;
+  float sum = 0.f;
+#pragma unroll 2
+  for (int c = 0; c < p.slot_rows; c += 4) {
+    const float4 y = __ldcs(reinterpret_cast<const float4 *>(x + c));
+    const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < rows && z[e] > -INFINITY) sum += ex2(z[e] - lse2[c + e]);
+  }
+  a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
+}
+
 // --- host ------------------------------------------------------------------------
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -1378,14 +1921,15 @@ typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, voi
 
 struct TcShape {
   int slot_rows, part_size, grid, score_ld, box;
-  bool wide, spool;
+  bool wide, columns, spool;
   size_t partial, lse, scores, bytes;
 };
 TcShape tc_shape(const kvx_attend8_args *a) {
   TcShape s;
   const int64_t G = a->q_heads / a->cache.heads, most = G * a->max_new;
   s.wide = most > kTile;
-  s.slot_rows = s.wide ? Wide::ROWS : (int)most;
+  s.columns = most <= 16;
+  s.slot_rows = s.wide ? Wide::ROWS : s.columns ? (most <= 8 ? 8 : 16) : (int)most;
   s.part_size = (s.slot_rows * (kD + 2) + 3) / 4 * 4;
   s.grid = 152;                        // one CTA an SM
   s.score_ld = (a->max_len + 255) / 256 * 256;
@@ -1428,13 +1972,12 @@ kvx_status launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? KVX_OK : KVX_ERR_CUDA;
 }
 
-template <bool WIDE>
-kvx_status launch(const TcParams &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
-  using G = std::conditional_t<WIDE, Wide, Narrow>;
-  if (cudaFuncSetAttribute(attend_tc_kernel<WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
-      cudaSuccess)
+template <class G, class K>
+kvx_status launch(K kernel, int threads, size_t smem, const TcParams &p, const CUtensorMap &mk, const CUtensorMap &mv,
+                  cudaStream_t s) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return KVX_ERR_CUDA;
-  attend_tc_kernel<WIDE><<<p.grid, kThreads, kSmemBytes, s>>>(p, mk, mv);
+  kernel<<<p.grid, threads, smem, s>>>(p, mk, mv);
   if (const kvx_status st = launched()) return st;
   return launch_after(join_kernel<G>, dim3(p.grid - 1, (p.slot_rows + 31) / 32), 256, 0, s, p);
 }
@@ -1465,7 +2008,11 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   p.box = sh.box;
   p.vec_q = aligned_to(a.q, 16) && (a.qt | a.qh) % 8 == 0;
   p.vec_out = aligned_to(a.out, 16) && (a.ot | a.oh) % 8 == 0;
-  const kvx_status st = sh.wide ? launch<true>(p, mk, mv, s) : launch<false>(p, mk, mv, s);
+  const kvx_status st =
+      sh.wide      ? launch<Wide>(attend_tc_kernel<true>, kThreads, kSmemBytes, p, mk, mv, s)
+      : !sh.columns ? launch<Narrow>(attend_tc_kernel<false>, kThreads, kSmemBytes, p, mk, mv, s)
+      : sh.slot_rows == 8 ? launch<Columns<8>>(columns_kernel<8>, kColThreads, kColSmem, p, mk, mv, s)
+                          : launch<Columns<16>>(columns_kernel<16>, kColThreads, kColSmem, p, mk, mv, s);
   if (st != KVX_OK || !a.weights || a.max_len == 0) return st;
   if (sh.wide) {
     // as few slot tiles a CTA as lets all run at once, 16 at most
@@ -1477,6 +2024,8 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
     weights_tc_kernel<<<dim3((tiles + per - 1) / per, a.H, a.req.R), kWtThreads, kWtSmem, s>>>(p, mk, per);
     return launched();
   }
-  weights_of_rows_kernel<<<dim3((a.max_len + 255) / 256, a.H, a.req.R), 256, sh.slot_rows * 4, s>>>(p);
+  const dim3 grid((a.max_len + 255) / 256, a.H, a.req.R);
+  if (sh.columns) return launch_after(weights_of_columns_kernel, grid, 256, 0, s, p);
+  weights_of_rows_kernel<<<grid, 256, sh.slot_rows * 4, s>>>(p);
   return launched();
 }
