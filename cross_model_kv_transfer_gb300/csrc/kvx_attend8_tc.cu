@@ -41,7 +41,11 @@ constexpr int kD = 128;             // head_dim
 constexpr int kTile = 128;          // slots and rows of a tile
 constexpr int kHalf = kTile / 2;   // slots whose scores and products are formed at a time
 constexpr int kTileBytes = kTile * kD;
-constexpr int kKStages = 3, kVStages = 2, kWStages = 2;
+// narrow: a stage must serve one group only, whose waits on it then know that the
+// phase before is over
+constexpr int kMaxKStages = 4, kVStages = 2, kWStages = 2;
+template <bool WIDE>
+constexpr int kStagesOf = WIDE ? 3 : 4;
 constexpr int kLoadWarp = 12, kMmaWarp = 13, kThreads = 16 * 32;
 // registers a thread: 8 softmax warps, 4 that convert, 4 others; together the
 // launch's 512 x 128
@@ -63,7 +67,7 @@ struct Share {
 };
 
 struct TcShared {
-  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t k_full[kMaxKStages], k_empty[kMaxKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t w_full[kWStages], w_empty[kWStages];
   // [group][half of the tile]; a wait on one names a phase whose predecessor is
@@ -75,21 +79,30 @@ struct TcShared {
   Share share;
   // the tile's largest value scale, as a power of two: its exponent for the
   // softmax, 2^7 over it for the conversion
-  float k_ref[kKStages], v_unit[kVStages];
-  uint32_t k_mask[kKStages], v_mask[kVStages];   // bit l: slots 4l .. 4l + 3 lie in a block of the pool
+  float k_ref[kMaxKStages], v_unit[kVStages];
+  uint32_t k_mask[kMaxKStages], v_mask[kVStages];   // bit l: slots 4l .. 4l + 3 lie in a block of the pool
   // scales, one for four slots (which lie in one block)
-  __align__(16) float ks[kKStages][kTile / 4];
+  __align__(16) float ks[kMaxKStages][kTile / 4];
   __align__(16) float vs[kVStages][kTile / 4];
 };
-constexpr size_t kSmemQ = 4 * (size_t)kTileBytes;     // two tiles of two parts
-constexpr size_t kSmemBytes = 1024 + kSmemQ + (kKStages + kVStages) * (size_t)kTileBytes +
-                              kWStages * 2 * (size_t)kTileBytes + sizeof(TcShared);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+constexpr size_t kSmemQ = 4 * (size_t)kTileBytes;     // two tiles of two parts; narrow one
+template <bool WIDE>
+constexpr size_t smem_bytes() {
+  return 1024 + (WIDE ? kSmemQ : kSmemQ / 2) + (kStagesOf<WIDE> + kVStages) * (size_t)kTileBytes +
+         kWStages * 2 * (size_t)kTileBytes + sizeof(TcShared);
+}
+static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1024, "shared memory");
 
+// Where CTA x begins inside an item that CTA x - 1 began: what to join.
+struct Split {
+  int r, h, group, c0, ctas, rows;   // ctas 0: nothing
+  int64_t beg;
+};
 struct TcParams {
   AttendParams a;
   int grid;            // CTAs that share the work
-  float *partial;      // [2 * grid][WIDE ? 1 : 2][part_size]: sums [rows][kD], maxima, totals
+  Split *splits;       // [grid]
+  float *partial;      // [2 * grid][PARTS][part_size]: sums [rows][kD], maxima, totals
   float *scores;       // base 2, or NULL; narrow: [R][H][rows][score_ld], columns: [R][H][score_ld][slot_rows]
   int score_ld, slot_rows, part_size;   // rows kept of a part (narrow: G * max_new), its floats
   int box;             // slots of one TMA box
@@ -533,98 +546,92 @@ __device__ __forceinline__ bool softmax_half(uint32_t col, const float4 *scale, 
   tc_wait_st();
   return true;
 }
-// A row's 128 elements, packed as they lie (zeros for a dead row).
-__device__ __forceinline__ void load_query(const __nv_bfloat16 *src, bool vec, bool live, uint32_t (&x)[kD / 2]) {
-  if (!live) {
-#pragma unroll
-    for (int e = 0; e < kD / 2; ++e) x[e] = 0;
-  } else if (vec) {
-#pragma unroll
+// The factor of a lane's row, from its largest element.
+__device__ __noinline__ float query_factor(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live) {
+  float top = 0.f;
+  if (live && vec) {
+#pragma unroll 4
     for (int e = 0; e < kD / 8; ++e) {
       const uint4 t = __ldg(reinterpret_cast<const uint4 *>(src) + e);
-      x[4 * e] = t.x;
-      x[4 * e + 1] = t.y;
-      x[4 * e + 2] = t.z;
-      x[4 * e + 3] = t.w;
+      const uint32_t v[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        top = max3(top, fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xffff0000u)));
     }
-  } else {
-    const unsigned short *h = reinterpret_cast<const unsigned short *>(src);
-#pragma unroll
-    for (int e = 0; e < kD / 2; ++e) x[e] = (uint32_t)h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
+  } else if (live) {
+#pragma unroll 4
+    for (int e = 0; e < kD; ++e) top = fmaxf(top, fabsf(__bfloat162float(src[e])));
   }
-}
-__device__ __forceinline__ float largest(const uint32_t (&x)[kD / 2]) {
-  float top = 0.f;
-#pragma unroll
-  for (int e = 0; e < kD / 2; ++e)
-    top = max3(top, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
-  return top;
-}
-__device__ __noinline__ float query_factor(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live) {
-  uint32_t x[kD / 2];
-  load_query(src, vec, live, x);
-  const float top = largest(x);
   return row_factor(a, top, pow2_scale(top));
 }
-// 32 query rows of a warp as two e4m3 parts, `part` bytes apart, in the swizzled
-// K-major tile (from row `first` of the tile on; `src` is the lane's own row).  Half a warp loads a row at
-// a time.  Returns the lane's factor on its row's scores (its sign is in the
-// parts).
+// Up to 32 query rows of a warp (`count` of them, rounded up to 8) as two e4m3
+// parts, `part` bytes apart, in the swizzled K-major tile, from row `first` of the
+// tile on; `src` is the lane's own row.  Half a warp loads a row, eight rows at a
+// time: short code, which a CTA runs cold.  Returns the lane's factor on its row's
+// scores (its sign is in the parts).
 __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
-                                          unsigned char *tile, int first, int part) {
+                                          unsigned char *tile, int first, int part, int count) {
   const int lane = threadIdx.x % 32, c = lane % 16;      // 8 dimensions
-  uint4 x[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int row = 2 * i + lane / 16;
-    const uint64_t p = __shfl_sync(~0u, (uint64_t)src, row);
-    const bool there = __shfl_sync(~0u, (int)live, row);
-    const __nv_bfloat16 *from = reinterpret_cast<const __nv_bfloat16 *>(p) + 8 * c;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (there && vec) {
-      x[i] = __ldg(reinterpret_cast<const uint4 *>(from));
-    } else if (there) {
-      const unsigned short *h = reinterpret_cast<const unsigned short *>(from);
-      uint32_t v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (uint32_t)h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
-      x[i] = make_uint4(v[0], v[1], v[2], v[3]);
-    }
-  }
   float mine = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; 2 * i0 < count; i0 += 4) {
+    uint4 x[4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    float y[8], top = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y[2 * e] = __uint_as_float(v[e] << 16);
-      y[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
-      top = max3(top, fabsf(y[2 * e]), fabsf(y[2 * e + 1]));
+    for (int i = 0; i < 4; ++i) {
+      const int row = 2 * (i0 + i) + lane / 16;
+      const uint64_t p = __shfl_sync(~0u, (uint64_t)src, row);
+      const bool there = __shfl_sync(~0u, (int)live, row);
+      const uint4 *from = reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + 8 * c);
+      x[i] = there && vec ? __ldg(from) : make_uint4(0, 0, 0, 0);
+      if (!vec && there) {
+        const unsigned short *h = reinterpret_cast<const unsigned short *>(from);
+        uint32_t v[4] = {};
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t u = (uint32_t)h[e] << (16 * (e & 1));
+          v[0] |= e / 2 == 0 ? u : 0u;
+          v[1] |= e / 2 == 1 ? u : 0u;
+          v[2] |= e / 2 == 2 ? u : 0u;
+          v[3] |= e / 2 == 3 ? u : 0u;
+        }
+        x[i] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
     }
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    const float unit = pow2_scale(top);   // top <= 448 unit
-    const float up = a.c != 0.f ? copysignf(1.f / unit, a.c) : 0.f;
-    const float other = __shfl_xor_sync(~0u, top, 16);
-    if (lane / 2 == i) mine = lane % 2 == lane / 16 ? top : other;
-    uint32_t p1[2], p2[2];
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      float y[8], top = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float *z = y + 4 * e;
+      for (int e = 0; e < 4; ++e) {
+        y[2 * e] = __uint_as_float(v[e] << 16);
+        y[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+        top = max3(top, fabsf(y[2 * e]), fabsf(y[2 * e + 1]));
+      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) z[k] *= up;
-      p1[e] = e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16;
-      const float2 f0 = floats_of(p1[e]), f1 = floats_of(p1[e] >> 16);
-      p2[e] = e4m3x2(z[0] - f0.x, z[1] - f0.y) | e4m3x2(z[2] - f1.x, z[3] - f1.y) << 16;
+      for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      const float unit = pow2_scale(top);   // top <= 448 unit
+      const float up = a.c != 0.f ? copysignf(1.f / unit, a.c) : 0.f;
+      const float other = __shfl_xor_sync(~0u, top, 16);
+      if (lane / 2 == i0 + i) mine = lane % 2 == lane / 16 ? top : other;
+      uint32_t p1[2], p2[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float *z = y + 4 * e;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] *= up;
+        p1[e] = e4m3x2(z[0], z[1]) | e4m3x2(z[2], z[3]) << 16;
+        const float2 f0 = floats_of(p1[e]), f1 = floats_of(p1[e] >> 16);
+        p2[e] = e4m3x2(z[0] - f0.x, z[1] - f0.y) | e4m3x2(z[2] - f1.x, z[3] - f1.y) << 16;
+      }
+      const int row = first + 2 * (i0 + i) + lane / 16;
+      unsigned char *to = tile + row * kD + ((c / 2 ^ (row & 7)) << 4) + (c & 1) * 8;
+      *reinterpret_cast<uint2 *>(to) = make_uint2(p1[0], p1[1]);
+      *reinterpret_cast<uint2 *>(to + part) = make_uint2(p2[0], p2[1]);
     }
-    const int row = first + 2 * i + lane / 16;
-    unsigned char *to = tile + row * kD + ((c / 2 ^ (row & 7)) << 4) + (c & 1) * 8;
-    *reinterpret_cast<uint2 *>(to) = make_uint2(p1[0], p1[1]);
-    *reinterpret_cast<uint2 *>(to + part) = make_uint2(p2[0], p2[1]);
   }
   return row_factor(a, mine, pow2_scale(mine));
 }
+
 // O times a row's factor, in place.
 __device__ __noinline__ void scale_down(uint32_t col, float down) {
 #pragma unroll 1
@@ -733,26 +740,85 @@ __device__ __noinline__ void join_rows(const TcParams &p, const TcWalk &w, int c
     }
   }
 }
-// The items that several CTAs worked on: block x looks after the boundary between
-// CTAs x and x + 1, where that is the first inside its item; block y after a slice
-// of the rows.
+// One lane of each CTA leaves this for the kernel that joins.
+template <class G>
+__device__ __forceinline__ void note_split(const TcParams &p, const Share &s) {
+  Split x = {};
+  const TcWalk &w = s.w;
+  if (s.good && s.last >= 0 && w.step > 0) {
+    const int64_t begin = w.base + G::SETUP;
+    const int c0 = (int)(((begin + 1) * s.N - 1) / s.T), c1 = (int)(((begin + w.steps) * s.N - 1) / s.T);   // first, last step
+    if (c0 + 1 == (int)blockIdx.x) {
+      x.r = w.r;
+      x.h = w.h;
+      x.group = w.group;
+      x.c0 = c0;
+      x.ctas = c1 - c0 + 1;
+      x.rows = (int)min((int64_t)G::ROWS, (int64_t)w.fresh * p.a.G - (int64_t)w.group * G::ROWS);
+      x.beg = w.beg;
+    }
+  }
+  p.splits[blockIdx.x] = x;
+}
+// The items that several CTAs worked on: block x looks after the one that CTA x + 1
+// noted, block y after a slice of its rows.
 template <class G>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcParams p) {
-  __shared__ Share share;
-  if (threadIdx.x < 32) {
-    Share s;
-    find_share<G>(p.a, blockIdx.x + 1, p.grid, false, s);
-    if (threadIdx.x == 0) share = s;
-  }
   wait_for_kernel_before();
+  const Split x = p.splits[blockIdx.x + 1];
+  if (x.ctas == 0) return;
+  TcWalk w;
+  w.h = x.h;
+  w.group = x.group;
+  w.beg = x.beg;
+  join_rows<G, 4>(p, w, x.c0, x.ctas, blockIdx.y * 8 + threadIdx.x / 32, gridDim.y * 8, x.rows);
+}
+// The same with a block for a row, whose warps share the parts: few rows, many parts.
+template <class G>
+__global__ void __launch_bounds__(256) join_row_kernel(const __grid_constant__ TcParams p) {
+  __shared__ float top[8], sum[8];
+  __shared__ float4 part_sum[8][32];
+  wait_for_kernel_before();
+  const Split x = p.splits[blockIdx.x + 1];
+  const int row = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32, parts = x.ctas * G::PARTS;
+  if (row >= x.rows || parts == 0) return;
+  float mm = -INFINITY, ll = 0.f;
+  float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 5
+  for (int c = warp; c < parts; c += 8) {
+    const int64_t cta = x.c0 + c / G::PARTS;
+    const float *part = p.partial + ((cta * 2 + (c < G::PARTS)) * G::PARTS + c % G::PARTS) * (int64_t)p.part_size;
+    const float pm = __ldcg(part + p.slot_rows * kD + row), pl = __ldcg(part + p.slot_rows * (kD + 1) + row);
+    const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + row * kD) + lane);
+    const float now = fmaxf(mm, pm), f0 = ex2(mm - finite_or_0(now)), f1 = ex2(pm - finite_or_0(now));
+    mm = now;
+    ll = ll * f0 + pl * f1;
+    oo = make_float4(oo.x * f0 + y.x * f1, oo.y * f0 + y.y * f1, oo.z * f0 + y.z * f1, oo.w * f0 + y.w * f1);
+  }
+  part_sum[warp][lane] = oo;
+  if (lane == 0) {
+    top[warp] = mm;
+    sum[warp] = ll;
+  }
   __syncthreads();
-  const TcWalk w = share.w;
-  if (!share.good || share.last < 0 || w.step == 0) return;   // nothing here, or an item begins here
-  const int64_t T = share.T, N = share.N, begin = w.base + G::SETUP;
-  const int c0 = (int)(((begin + 1) * N - 1) / T), c1 = (int)(((begin + w.steps) * N - 1) / T);   // of its first and last step
-  if (c0 != (int)blockIdx.x) return;
-  const int rows = (int)min((int64_t)G::ROWS, (int64_t)w.fresh * p.a.G - (int64_t)w.group * G::ROWS);
-  join_rows<G, G::ROWS >= 128 ? 4 : 1>(p, w, c0, c1 - c0 + 1, blockIdx.y * 8 + threadIdx.x / 32, gridDim.y * 8, rows);
+  if (warp > 0) return;
+  mm = -INFINITY;
+  ll = 0.f;
+  oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mm = fmaxf(mm, top[k]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float f = ex2(top[k] - finite_or_0(mm));
+    const float4 y = part_sum[k][lane];
+    ll += sum[k] * f;
+    oo = make_float4(oo.x + y.x * f, oo.y + y.y * f, oo.z + y.z * f, oo.w + y.w * f);
+  }
+  const AttendParams &a = p.a;
+  const int64_t at = (int64_t)x.group * G::ROWS + row, tok = x.beg + at / a.G;
+  const int hq = x.h * a.G + (int)(at % a.G);
+  store_out(a, tok, hq, lane * 4, make_float2(oo.x, oo.y), mm, ll);
+  store_out(a, tok, hq, lane * 4 + 2, make_float2(oo.z, oo.w), mm, ll);
 }
 
 // What a softmax group knows of its item when the item, or the CTA's part of it, ends.
@@ -855,9 +921,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v) {
   using G_ = std::conditional_t<WIDE, Wide, Narrow>;
+  constexpr int kKStages = kStagesOf<WIDE>;
   extern __shared__ unsigned char raw[];
   unsigned char *qbuf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  unsigned char *kbuf = qbuf + kSmemQ, *vbuf = kbuf + kKStages * kTileBytes, *wbuf = vbuf + kVStages * kTileBytes;
+  unsigned char *kbuf = qbuf + (WIDE ? kSmemQ : kSmemQ / 2), *vbuf = kbuf + kKStages * kTileBytes, *wbuf = vbuf + kVStages * kTileBytes;
   TcShared *sh = reinterpret_cast<TcShared *>(wbuf + kWStages * 2 * kTileBytes);
   const AttendParams &a = p.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -900,6 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     find_share<G_>(a, blockIdx.x, gridDim.x, blockIdx.x == 0, share);
     if (lane == 0) {
       sh->share = share;
+      note_split<G_>(p, share);
       if (!share.good && blockIdx.x == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
     }
   }
@@ -935,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
       float m = -INFINITY, l = 0.f, cs;
       if (WIDE || i == 0) {
-        cs = put_queries(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes);
+        cs = put_queries(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes, 32);
         fence_async_proxy();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[i]));
@@ -1195,23 +1263,27 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
 // share a maximum for each column: they vote on a tile, and only where one of them
 // exceeds it by 2^4 do they agree on a new one and scale O down.
 // Two groups of four warps take the even and the odd slot tiles.
-constexpr int kCkStages = 5, kCvStages = 5, kColThreads = 11 * 32;
-constexpr int kColLoad = 8, kColMma = 9;
+// even numbers of stages: a stage serves one group, whose waits on it then know
+// that the phase before is over
+constexpr int kCkStages = 4, kCvStages = 6, kScales = 16, kColThreads = 12 * 32;
+constexpr int kColLoad = 8, kColMma = 10;   // keys and values; a group each
 constexpr float kColBias = 11.f, kColSlack = 4.f;   // P at most 2^15, nothing lost above 2^-28 of the maximum
 constexpr int kColQBytes = 32 * kD, kColPBytes = kTile * 16;   // a part of the queries, of a tile's probabilities
 struct ColShared {
   uint64_t k_full[kCkStages], k_empty[kCkStages], v_full[kCvStages], v_empty[kCvStages];
-  uint64_t q_full, item_done, s_full[2][2], p_full[2][2], pv_done[2][2], vote[2], agree[2], join, spent, drain[2];
+  // scales[n % kScales] of tile n: the loader is never that far ahead of the softmax
+  uint64_t scales[kScales], q_full[2], item_done[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], vote[2], agree[2], join, spent, drain[2];
   uint32_t tmem_base;
   volatile int abort;
   Share share;
   volatile uint32_t over[2][2];
-  uint32_t mask[kCkStages];
-  float ks[kCkStages][kTile / 4], vs[kCkStages][kTile / 4];
+  uint32_t mask[kScales];
+  float ks[kScales][kTile / 4], vs[kScales][kTile / 4];
   float cs[2][16];             // of the item (in turn) and column
   float warp_max[2][4][16], warp_sum[2][4][16];
 };
-constexpr size_t kColSmem = 1024 + (kCkStages + kCvStages) * (size_t)kTileBytes + 2 * kColQBytes + 2 * 2 * 3 * kColPBytes +
+constexpr size_t kColSmem = 1024 + (kCkStages + kCvStages) * (size_t)kTileBytes + 4 * kColQBytes + 2 * 2 * 3 * kColPBytes +
                             sizeof(ColShared);
 static_assert(kColSmem <= 227 * 1024, "shared memory");
 // D fp32, M = 128, N = 16; e4m3 both K-major, and e4m3 x e5m2 both as they lie in
@@ -1315,21 +1387,20 @@ __global__ void __launch_bounds__(kColThreads, 1)
   using G_ = Columns<NC>;
   extern __shared__ unsigned char raw[];
   unsigned char *kbuf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  unsigned char *vbuf = kbuf + kCkStages * kTileBytes, *qbuf = vbuf + kCvStages * kTileBytes, *pbuf = qbuf + 2 * kColQBytes;
+  unsigned char *vbuf = kbuf + kCkStages * kTileBytes, *qbuf = vbuf + kCvStages * kTileBytes, *pbuf = qbuf + 4 * kColQBytes;
   ColShared *sh = reinterpret_cast<ColShared *>(pbuf + 2 * 2 * 3 * kColPBytes);
   const AttendParams &a = p.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
     for (int i = 0; i < kCkStages; ++i) {
       mbar_init(smem_addr(&sh->k_full[i]), 32);
-      mbar_init(smem_addr(&sh->k_empty[i]), 1 + 4);
+      mbar_init(smem_addr(&sh->k_empty[i]), 1);
     }
+    for (int i = 0; i < kScales; ++i) mbar_init(smem_addr(&sh->scales[i]), 32);
     for (int i = 0; i < kCvStages; ++i) {
       mbar_init(smem_addr(&sh->v_full[i]), 32);
       mbar_init(smem_addr(&sh->v_empty[i]), 1);
     }
-    mbar_init(smem_addr(&sh->q_full), 1);
-    mbar_init(smem_addr(&sh->item_done), 8);
     for (int i = 0; i < 2; ++i) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_addr(&sh->s_full[i][b]), 1);
@@ -1337,6 +1408,8 @@ __global__ void __launch_bounds__(kColThreads, 1)
         mbar_init(smem_addr(&sh->pv_done[i][b]), 1);
         sh->over[i][b] = 0;
       }
+      mbar_init(smem_addr(&sh->q_full[i]), 1);
+      mbar_init(smem_addr(&sh->item_done[i]), 8);
       mbar_init(smem_addr(&sh->vote[i]), 4);
       mbar_init(smem_addr(&sh->agree[i]), 4);
       mbar_init(smem_addr(&sh->drain[i]), 1);
@@ -1357,6 +1430,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
     find_share<G_>(a, blockIdx.x, gridDim.x, blockIdx.x == 0, share);
     if (lane == 0) {
       sh->share = share;
+      note_split<G_>(p, share);
       if (!share.good && blockIdx.x == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
     }
   }
@@ -1375,26 +1449,35 @@ __global__ void __launch_bounds__(kColThreads, 1)
     const int i = warp / 4, in = warp % 4 * 32 + lane;      // group; slot of the tile, dimension of the sums
     const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     uint32_t t = 0, items = 0, joins = 0, agreed = 0;       // tiles of the group, items, joins, agreements so far
-    int ks = i;
-    uint32_t k_phase = 0;
+    // the queries: warp 0 brings an item's while the one before is worked on
+    const auto bring = [&](const TcWalk &w, uint32_t item) {
+      const int64_t row0 = (int64_t)w.group * NC, tok = (row0 + lane) / a.G;
+      const int rows = (int)min((int64_t)NC, (int64_t)w.fresh * a.G - row0);
+      const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
+                                 (int64_t)(w.h * a.G + (int)((row0 + lane) % a.G)) * a.qh;
+      const float f = put_queries(a, p.vec_q, src, lane < rows, qbuf + (item & 1) * 2 * kColQBytes, 0, kColQBytes, 16);
+      if (lane < 16) sh->cs[item & 1][lane] = f;
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[item & 1]));
+    };
+    if (warp == 0 && w.base + G_::SETUP < last) bring(w, 0);
     for (; w.base + G_::SETUP < last; next_item<G_>(a, w), ++items) {
       const int count = steps_here<G_>(w, last);
       const int64_t row0 = (int64_t)w.group * NC;
       const int rows = (int)min((int64_t)NC, (int64_t)w.fresh * a.G - row0);
       if (warp == 0) {
-        // both groups have formed the last scores of the item before
-        if (items > 0 && !W.warp_wait(&sh->item_done, (items - 1) & 1)) goto done;
-        const int64_t tok = (row0 + lane) / a.G;
-        const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
-                                   (int64_t)(w.h * a.G + (int)((row0 + lane) % a.G)) * a.qh;
-        const float f = put_queries(a, p.vec_q, src, lane < rows, qbuf, 0, kColQBytes);
-        if (lane < 16) sh->cs[items & 1][lane] = f;
-        fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh->q_full));
+        // the next item's queries, once both groups have formed the last scores of
+        // the item before this one
+        TcWalk ahead = w;
+        next_item<G_>(a, ahead);
+        if (ahead.base + G_::SETUP < last) {
+          if (items > 0 && !W.warp_wait(&sh->item_done[(items + 1) & 1], (items - 1) >> 1 & 1)) goto done;
+          bring(ahead, items + 1);
+        }
       }
       float cs[NC], m[NC], l[NC];
-      if (!W.warp_wait(&sh->q_full, items & 1)) goto done;
+      if (!W.warp_wait(&sh->q_full[items & 1], items >> 1 & 1)) goto done;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         cs[c] = sh->cs[items & 1][c];
@@ -1406,7 +1489,9 @@ __global__ void __launch_bounds__(kColThreads, 1)
       int j = w.step * G_::SLOTS + i * kTile + in;
       for (int s = 0; s < count; ++s, ++t) {
         const int b = t & 1;
-        if (!W.warp_wait(&sh->k_full[ks], k_phase)) goto done;
+        const uint32_t tile = 2 * t + i;
+        const int ks = tile % kScales;
+        if (!W.warp_wait(&sh->scales[ks], tile / kScales & 1)) goto done;
         if (!W.warp_wait(&sh->s_full[i][b], t >> 1 & 1)) goto done;
         tc_fence_after();
         const float f = sh->ks[ks][in / 4], v = sh->vs[ks][in / 4];
@@ -1483,7 +1568,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
         if (__any_sync(~0u, !there || j >= w.len)) {
           // slots of no block of the pool or beyond the length: zero values, so that
           // their zero probabilities meet no NaN
-          const uint32_t tile = 2 * t + i, vstage = tile % kCvStages;
+          const uint32_t vstage = tile % kCvStages;
           if (!W.warp_wait(&sh->v_full[vstage], tile / kCvStages & 1)) goto done;
           if (!there || j >= w.len) {
             uint4 *row = reinterpret_cast<uint4 *>(vbuf + vstage * kTileBytes + in * kD);
@@ -1512,16 +1597,10 @@ __global__ void __launch_bounds__(kColThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_addr(&sh->p_full[i][b]));
-          mbar_arrive(smem_addr(&sh->k_empty[ks]));
         }
         j += G_::SLOTS;
-        ks += 2;
-        if (ks >= kCkStages) {
-          ks -= kCkStages;
-          k_phase ^= 1;
-        }
       }
-      if (lane == 0) mbar_arrive(smem_addr(&sh->item_done));
+      if (lane == 0) mbar_arrive(smem_addr(&sh->item_done[items & 1]));
       // this group's part of the item
       if (!W.warp_wait(&sh->pv_done[i][(t - 1) & 1], (t - 1) >> 1 & 1)) goto done;
       if (joins > 0 && !W.warp_wait(&sh->spent, (joins - 1) & 1)) goto done;
@@ -1563,11 +1642,12 @@ __global__ void __launch_bounds__(kColThreads, 1)
       }
     }
   done:;
-  } else if (warp == kColLoad) {
-    // A tile's blocks are looked up two tiles ahead, their scales one: nothing
-    // waits for them.
+  } else if (warp < kColMma) {
+    // A warp loads the keys and all scales, another the values.  A tile's blocks are
+    // looked up two tiles ahead, their scales one: nothing waits for them.
+    const bool keys = warp == kColLoad;
     struct Tile {
-      int page, row;
+      int page, off;
       bool asked;
     };
     int k = 0, end = 0, j = 0;      // tile of the item, tiles of the item in this CTA, the lane's first slot
@@ -1581,14 +1661,14 @@ __global__ void __launch_bounds__(kColThreads, 1)
     const auto next = [&](Tile &x, int &h) {
       x.asked = more;
       x.page = -1;
-      x.row = 0;
+      x.off = 0;
       h = w.h;
       if (!more) return;
       if (j < w.len) {
         const uint32_t block = block_of(a, j);
-        x.row = j - block * a.bs;                  // in the block, until the page is known
+        x.off = j - block * a.bs;
         x.page = page_of(a, w.r, block);
-        if (x.page < 0) raise(a.status, KVX_FLAG_BAD_BLOCK);
+        if (x.page < 0 && keys) raise(a.status, KVX_FLAG_BAD_BLOCK);
       }
       j += kTile;
       if (++k == end) {
@@ -1599,60 +1679,59 @@ __global__ void __launch_bounds__(kColThreads, 1)
     };
     Tile t0, t1;
     int h0, h1;
-    float ks0 = 0.f, vs0 = 0.f;
+    float f0 = 0.f, g0 = 0.f;
     const auto scales = [&](const Tile &x, int h, float &f, float &g) {
       f = g = 0.f;
-      if (x.page < 0) return;
+      if (x.page < 0 || !keys) return;
       const uint32_t sb = (uint32_t)x.page * a.H + h;
       f = __ldg(a.ks + sb);
       g = __ldg(a.vs + sb);
     };
     next(t0, h0);
-    scales(t0, h0, ks0, vs0);
+    scales(t0, h0, f0, g0);
     next(t1, h1);
-    uint32_t n = 0;
-    for (; t0.asked; ++n) {
-      const int ks = n % kCkStages, vs = n % kCvStages;
-      const int row = t0.page < 0 ? 0 : (int)(((uint32_t)t0.page * a.H + h0) * a.bs + t0.row);
+    const int stages = keys ? kCkStages : kCvStages, per = p.box / 4, boxes = kTile / p.box;   // lanes a box, boxes
+    uint64_t *full = keys ? sh->k_full : sh->v_full, *empty = keys ? sh->k_empty : sh->v_empty;
+    unsigned char *buf = keys ? kbuf : vbuf;
+    const CUtensorMap *map = keys ? &map_k : &map_v;
+    uint32_t n = 0, phase = 0;
+    for (int st = 0; t0.asked; ++n) {
+      const int row = t0.page < 0 ? 0 : (int)(((uint32_t)t0.page * a.H + h0) * a.bs + t0.off);
       const unsigned mask = __ballot_sync(~0u, t0.page >= 0);
-      const float kscale = ks0, vscale = vs0;
+      const float kscale = f0, vscale = g0;
       // what the next tiles need, on its way
       t0 = t1;
       h0 = h1;
-      scales(t0, h0, ks0, vs0);
+      scales(t0, h0, f0, g0);
       next(t1, h1);
-      const int per = p.box / 4, boxes = kTile / p.box;     // lanes a box, boxes
       const int from = __shfl_sync(~0u, row, lane < boxes ? lane * per : 0);
       const bool there = lane < boxes && (mask >> (lane * per) & 1);
       const uint32_t bytes = __popc(__ballot_sync(~0u, there)) * (uint32_t)p.box * kD;
-      if (!W.warp_wait(&sh->k_empty[ks], (n / kCkStages & 1) ^ 1)) goto ld_done;
-      sh->ks[ks][lane] = kscale;
-      sh->vs[ks][lane] = vscale;
-      if (lane == 0) {
-        sh->mask[ks] = mask;
-        mbar_expect_tx(smem_addr(&sh->k_full[ks]), bytes);
+      if (!W.warp_wait(&empty[st], phase ^ 1)) break;
+      if (keys) {
+        const int sc = n % kScales;
+        sh->ks[sc][lane] = kscale;
+        sh->vs[sc][lane] = vscale;
+        if (lane == 0) sh->mask[sc] = mask;
+        __syncwarp();
+        mbar_arrive(smem_addr(&sh->scales[sc]));
       }
+      if (lane == 0) mbar_expect_tx(smem_addr(&full[st]), bytes);
       __syncwarp();
-      if (there)
-        tma_load_2d(smem_addr(kbuf + ks * kTileBytes + lane * p.box * kD), &map_k, 0, from, smem_addr(&sh->k_full[ks]));
-      if (lane != 0) mbar_arrive(smem_addr(&sh->k_full[ks]));
-      if (!W.warp_wait(&sh->v_empty[vs], (n / kCvStages & 1) ^ 1)) goto ld_done;
-      if (lane == 0) mbar_expect_tx(smem_addr(&sh->v_full[vs]), bytes);
-      __syncwarp();
-      if (there)
-        tma_load_2d(smem_addr(vbuf + vs * kTileBytes + lane * p.box * kD), &map_v, 0, from, smem_addr(&sh->v_full[vs]));
-      if (lane != 0) mbar_arrive(smem_addr(&sh->v_full[vs]));
+      if (there) tma_load_2d(smem_addr(buf + st * kTileBytes + lane * p.box * kD), map, 0, from, smem_addr(&full[st]));
+      if (lane != 0) mbar_arrive(smem_addr(&full[st]));
+      if (++st == stages) {
+        st = 0;
+        phase ^= 1;
+      }
     }
-  ld_done:
     __syncwarp();
-    if (lane == 0) {
-      for (uint32_t x = n > kCkStages ? n - kCkStages : 0; x < n; ++x) drain_wait(&sh->k_full[x % kCkStages], x / kCkStages & 1);
-      for (uint32_t x = n > kCvStages ? n - kCvStages : 0; x < n; ++x) drain_wait(&sh->v_full[x % kCvStages], x / kCvStages & 1);
-      if (sh->abort) drain_wait(&sh->k_full[n % kCkStages], n / kCkStages & 1);
-    }
+    if (lane == 0)
+      for (uint32_t x = n > (uint32_t)stages ? n - stages : 0; x < n; ++x) drain_wait(&full[x % stages], x / stages & 1);
   } else {
     const int i = warp - kColMma;
-    const uint64_t q0 = sw128_desc(smem_addr(qbuf)), k0 = sw128_desc(smem_addr(kbuf)), v0 = v_desc(smem_addr(vbuf));
+    const uint64_t k0 = sw128_desc(smem_addr(kbuf)), v0 = v_desc(smem_addr(vbuf));
+    uint64_t q0 = 0;                 // the item's queries
     const uint64_t p0 = p_desc(smem_addr(pbuf + i * 2 * 3 * kColPBytes));
     uint32_t items = 0, t = 0;
     bool ok = true, issued = false;
@@ -1668,7 +1747,8 @@ __global__ void __launch_bounds__(kColThreads, 1)
     };
     for (; ok && w.base + G_::SETUP < last; next_item<G_>(a, w)) {
       const int count = steps_here<G_>(w, last);
-      ok = W.warp_wait(&sh->q_full, items & 1) && scores(t) && (count == 1 || scores(t + 1));
+      q0 = sw128_desc(smem_addr(qbuf + (items & 1) * 2 * kColQBytes));
+      ok = W.warp_wait(&sh->q_full[items & 1], items >> 1 & 1) && scores(t) && (count == 1 || scores(t + 1));
       ++items;
       for (int s = 0; ok && s < count; ++s, ++t) {
         const uint32_t tile = 2 * t + i, stage = tile % kCvStages;
@@ -1765,7 +1845,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int64_t tok = beg + row / a.G;
       const int hq = h * a.G + row % a.G;
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + tok * a.qt + (int64_t)hq * a.qh;
-      const float cs = put_queries(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32, kTileBytes);
+      const float cs = put_queries(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32, kTileBytes, 32);
       float *pair_of = reinterpret_cast<float *>(&sh->rows[tid / 2]) + tid % 2;
       // a dead row gives exp2(-inf)
       pair_of[0] = live ? cs : 0.f;
@@ -1922,7 +2002,7 @@ typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, voi
 struct TcShape {
   int slot_rows, part_size, grid, score_ld, box;
   bool wide, columns, spool;
-  size_t partial, lse, scores, bytes;
+  size_t splits, partial, lse, scores, bytes;
 };
 TcShape tc_shape(const kvx_attend8_args *a) {
   TcShape s;
@@ -1938,7 +2018,8 @@ TcShape tc_shape(const kvx_attend8_args *a) {
   s.spool = a->weights && !s.wide;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t items = (size_t)a->num_requests * a->cache.heads;
-  s.partial = 0;
+  s.splits = 0;
+  s.partial = up(s.grid * sizeof(Split));
   s.lse = s.partial + up((size_t)2 * s.grid * (s.wide ? 1 : 2) * s.part_size * 4);
   s.scores = s.lse + up((size_t)a->ntok * a->q_heads * 4);
   s.bytes = s.scores + (s.spool ? up(items * s.slot_rows * s.score_ld * 4) : 0);
@@ -1979,6 +2060,7 @@ kvx_status launch(K kernel, int threads, size_t smem, const TcParams &p, const C
     return KVX_ERR_CUDA;
   kernel<<<p.grid, threads, smem, s>>>(p, mk, mv);
   if (const kvx_status st = launched()) return st;
+  if constexpr (G::ROWS <= 16) return launch_after(join_row_kernel<G>, dim3(p.grid - 1, p.slot_rows), 256, 0, s, p);
   return launch_after(join_kernel<G>, dim3(p.grid - 1, (p.slot_rows + 31) / 32), 256, 0, s, p);
 }
 
@@ -2000,6 +2082,7 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   p.a = a;
   if (!p.a.lse) p.a.lse = (float *)(ws + sh.lse);
   p.grid = sh.grid;
+  p.splits = (Split *)(ws + sh.splits);
   p.partial = (float *)(ws + sh.partial);
   p.scores = sh.spool ? (float *)(ws + sh.scores) : nullptr;
   p.score_ld = sh.score_ld;
@@ -2009,8 +2092,8 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   p.vec_q = aligned_to(a.q, 16) && (a.qt | a.qh) % 8 == 0;
   p.vec_out = aligned_to(a.out, 16) && (a.ot | a.oh) % 8 == 0;
   const kvx_status st =
-      sh.wide      ? launch<Wide>(attend_tc_kernel<true>, kThreads, kSmemBytes, p, mk, mv, s)
-      : !sh.columns ? launch<Narrow>(attend_tc_kernel<false>, kThreads, kSmemBytes, p, mk, mv, s)
+      sh.wide      ? launch<Wide>(attend_tc_kernel<true>, kThreads, smem_bytes<true>(), p, mk, mv, s)
+      : !sh.columns ? launch<Narrow>(attend_tc_kernel<false>, kThreads, smem_bytes<false>(), p, mk, mv, s)
       : sh.slot_rows == 8 ? launch<Columns<8>>(columns_kernel<8>, kColThreads, kColSmem, p, mk, mv, s)
                           : launch<Columns<16>>(columns_kernel<16>, kColThreads, kColSmem, p, mk, mv, s);
   if (st != KVX_OK || !a.weights || a.max_len == 0) return st;
