@@ -777,12 +777,32 @@ _pack_attend = _packer(Attend8Args)
 _pack_evict = _packer(Evict8Args)
 
 
+class _Fast:
+    """What a single-token call looks up every time, looked up once: torch, the
+    library's entry points, and torch's own (device, raw stream) queries."""
+    torch = None
+
+    @classmethod
+    def ready(cls):
+        import torch
+        lib = load()
+        cls.f32, cls.bf16, cls.i32 = torch.float32, torch.bfloat16, torch.int32
+        cls.codes = {torch.float32: KVX_F32, torch.bfloat16: KVX_BF16}
+        cls.rope, cls.write = lib.kvx_rope_apply, lib.kvx_cache8_write
+        cls.attend, cls.evict = lib.kvx_attend8, lib.kvx_evict8
+        cls.empty = torch.empty
+        cls.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        cls.raw = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda i: torch.cuda.current_stream(i).cuda_stream)
+        cls.torch = torch
+
+
 def _int_table(t, name, device, ndim=1):
     """Data pointer of a contiguous int32 CUDA tensor (0 for None)."""
-    import torch
     if t is None:
         return 0
-    if t.dtype != torch.int32 or t.device != device or t.dim() != ndim or not t.is_contiguous():
+    if t.dtype is not _Fast.i32 or t.device != device or t.dim() != ndim or \
+            not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {ndim}-D int32 tensor on {device}")
     return t.data_ptr()
 
@@ -792,23 +812,32 @@ def _status_ptr(t, device):
 
 
 def _on_device(device):
-    import torch
-    if device.type != "cuda" or torch.cuda.current_device() != device.index:
+    if device.type != "cuda":
+        raise ValueError(f"tensors are on {device}, which is not a CUDA device")
+    if _Fast.torch is None:
+        _Fast.ready()
+    if _Fast.device() != device.index:
         raise ValueError(f"tensors are on {device}, which is not the current CUDA device")
 
 
 def _raw_stream(stream, device):
-    import torch
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return _Fast.raw(device.index) if stream is None else stream.cuda_stream
 
 
 def _heads(t, name, dtype, device, heads, dim):
-    """Check a [tokens][heads][dim] tensor with unit stride inside a head."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[1] != heads or \
-            t.shape[2] != dim or t.stride(2) != 1:
+    """Check a [tokens][heads][dim] tensor with unit stride inside a head;
+    returns its strides and token count."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or t.dtype is not dtype or t.device != device or shape[1] != heads or \
+            shape[2] != dim or stride[2] != 1:
         raise ValueError(f"{name}: expected [tokens][{heads}][{dim}] {dtype} on {device} with "
                          f"unit stride inside a head")
-    return t
+    return stride, shape[0]
+
+
+def _code_of(dtype):
+    code = _Fast.codes.get(dtype)
+    return _dtype_code(dtype) if code is None else code
 
 
 class Rope:
@@ -845,47 +874,49 @@ class Rope:
         (int32, or first_position, first_position + 1, ...); returns (q_out,
         k_out), allocated unless given (in place with ``q_out=q``).
         ``transpose`` applies the transposed rotation: the gradient."""
-        import torch
         x = q if q is not None else k
         if x is None:
             raise ValueError("q or k is needed")
         dev, dt, d = x.device, x.dtype, self.head_dim
-        code = _dtype_code(dt)
         _on_device(dev)
+        code = _code_of(dt)
         n = x.shape[0]
-        ptrs, strides, heads = [], [], []
-        outs = []
-        for name, t, o in (("q", q, q_out), ("k", k, k_out)):
-            if t is None:
-                outs.append(None)
-                ptrs.append((0, 0))
-                strides.append((0, 0, 0, 0))
-                heads.append(0)
-                continue
-            h = t.shape[1] if t.dim() == 3 else -1
-            _heads(t, name, dt, dev, h, d)
-            if o is None:
-                o = _on_stream(torch.empty, stream, (n, h, d), dtype=dt, device=dev)
-            elif _heads(o, name + "_out", dt, dev, h, d).shape[0] != n:
-                raise ValueError(f"{name}_out has another number of tokens")
-            if t.shape[0] != n:
+        qp = kp = qo = ko = hq = hk = 0
+        qs = ks = qos = kos = (0, 0, 0)
+        if q is not None:
+            hq = q.shape[1]
+            qs, n = _heads(q, "q", dt, dev, hq, d)
+            if q_out is None:
+                q_out = _new(stream, (n, hq, d), dt, dev)
+                qos = (hq * d, d, 1)
+            else:
+                qos, m = _heads(q_out, "q_out", dt, dev, hq, d)
+                if m != n:
+                    raise ValueError("q_out has another number of tokens")
+            qp, qo = q.data_ptr(), q_out.data_ptr()
+        if k is not None:
+            hk = k.shape[1]
+            ks, m = _heads(k, "k", dt, dev, hk, d)
+            if m != n:
                 raise ValueError("q and k must hold the same tokens")
-            outs.append(o)
-            ptrs.append((t.data_ptr(), o.data_ptr()))
-            ts, os_ = t.stride(), o.stride()
-            strides.append((ts[0], ts[1], os_[0], os_[1]))
-            heads.append(h)
+            if k_out is None:
+                k_out = _new(stream, (n, hk, d), dt, dev)
+                kos = (hk * d, d, 1)
+            else:
+                kos, m = _heads(k_out, "k_out", dt, dev, hk, d)
+                if m != n:
+                    raise ValueError("k_out has another number of tokens")
+            kp, ko = k.data_ptr(), k_out.data_ptr()
         pos = _int_table(positions, "positions", dev)
-        if positions is not None and positions.shape[0] != n:
+        if pos and positions.shape[0] != n:
             raise ValueError("positions must hold one entry for each token")
-        (qs, ks) = strides
-        a = _pack_rope(ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1], qs[0], qs[1], ks[0], ks[1],
-                       qs[2], qs[3], ks[2], ks[3], n, heads[0], heads[1], code, int(transpose),
-                       pos, first_position, _status_ptr(status, dev))
-        st = load().kvx_rope_apply(self._ptr, a, _raw_stream(stream, dev))
+        a = _pack_rope(qp, kp, qo, ko, qs[0], qs[1], ks[0], ks[1], qos[0], qos[1], kos[0], kos[1],
+                       n, hq, hk, code, 1 if transpose else 0, pos, first_position,
+                       _status_ptr(status, dev))
+        st = _Fast.rope(self._ptr, a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_rope_apply")
-        return outs[0], outs[1]
+        return (None if q is None else q_out), (None if k is None else k_out)
 
 
 class Cache8:
@@ -923,8 +954,8 @@ class Cache8:
         return cls(codes[0], codes[1], scale[0], scale[1])
 
     def _table(self, block_table):
-        return self._head + (block_table.shape[1] if block_table.dim() == 2 else 0,
-                             _int_table(block_table, "block_table", self.device, 2))
+        ptr = _int_table(block_table, "block_table", self.device, 2)
+        return self._head + (block_table.shape[1], ptr)
 
     def write(self, k, v, block_table, start=None, *, cu_seqlens=None, src_rows=None, status=None,
               stream=None):
@@ -935,23 +966,23 @@ class Cache8:
         src_rows[g] of k and v, so a paged bf16 / fp32 cache can be read."""
         dev = self.device
         _on_device(dev)
-        _heads(k, "k", k.dtype, dev, self.heads, self.head_dim)
-        _heads(v, "v", k.dtype, dev, self.heads, self.head_dim)
-        if k.shape[0] != v.shape[0]:
+        dt = k.dtype
+        ks, rows = _heads(k, "k", dt, dev, self.heads, self.head_dim)
+        vs, m = _heads(v, "v", dt, dev, self.heads, self.head_dim)
+        if m != rows:
             raise ValueError("k and v must hold the same rows")
+        table = self._table(block_table)
         R = block_table.shape[0]
         if cu_seqlens is not None and cu_seqlens.shape[0] != R + 1:
             raise ValueError("cu_seqlens must have one entry more than block_table has rows")
         if start is not None and start.shape[0] != R:
             raise ValueError("start must hold one entry for each request")
-        n = k.shape[0] if src_rows is None else src_rows.shape[0]
-        ks, vs = k.stride(), v.stride()
-        a = _pack_write(*self._table(block_table), k.data_ptr(), v.data_ptr(), ks[0], ks[1],
-                        vs[0], vs[1], _dtype_code(k.dtype), R, n,
+        a = _pack_write(*table, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
+                        _code_of(dt), R, rows if src_rows is None else src_rows.shape[0],
                         _int_table(cu_seqlens, "cu_seqlens", dev),
                         _int_table(start, "start", dev), _int_table(src_rows, "src_rows", dev),
-                        k.shape[0], _status_ptr(status, dev))
-        st = load().kvx_cache8_write(a, _raw_stream(stream, dev))
+                        rows, _status_ptr(status, dev))
+        st = _Fast.write(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_cache8_write")
 
@@ -981,47 +1012,54 @@ class Cache8:
         ``weights`` [R][heads][>= max_len] fp32 accumulates the attention weight
         of each slot.  Scratch is allocated here unless ``workspace`` (from
         ``attend_workspace``) is given."""
-        import torch
-        dev = self.device
+        dev, dt = self.device, q.dtype
         _on_device(dev)
         if q.dim() != 3:
             raise ValueError("q must be [tokens][q_heads][d]")
-        n, hq, d = q.shape
-        _heads(q, "q", q.dtype, dev, hq, self.head_dim)
+        hq, d = q.shape[1], self.head_dim
+        qs, n = _heads(q, "q", dt, dev, hq, d)
+        table = self._table(block_table)
         R = block_table.shape[0]
         if lens.shape[0] != R or (cu_seqlens is not None and cu_seqlens.shape[0] != R + 1):
             raise ValueError("lens, cu_seqlens and block_table must hold the same requests")
+        code = _code_of(dt)
         if out is None:
-            out = _on_stream(torch.empty, stream, (n, hq, d), dtype=q.dtype, device=dev)
-        elif _heads(out, "out", q.dtype, dev, hq, d).shape[0] != n:
-            raise ValueError("out has another number of tokens")
+            out = _new(stream, (n, hq, d), dt, dev)
+            os_ = (hq * d, d, 1)
+        else:
+            os_, m = _heads(out, "out", dt, dev, hq, d)
+            if m != n:
+                raise ValueError("out has another number of tokens")
         if lse is None:
-            lse = _on_stream(torch.empty, stream, (n, hq), dtype=torch.float32, device=dev)
-        elif lse.dtype != torch.float32 or tuple(lse.shape) != (n, hq) or lse.device != dev or \
+            lse = _new(stream, (n, hq), _Fast.f32, dev)
+        elif lse.dtype is not _Fast.f32 or tuple(lse.shape) != (n, hq) or lse.device != dev or \
                 not lse.is_contiguous():
             raise ValueError(f"lse must be a contiguous fp32 [{n}][{hq}] tensor on {dev}")
         wptr = wstride = 0
         if weights is not None:
-            if weights.dtype != torch.float32 or weights.device != dev or weights.dim() != 3 or \
-                    tuple(weights.shape[:2]) != (R, self.heads) or not weights.is_contiguous():
-                raise ValueError(f"weights must be a contiguous fp32 [{R}][{self.heads}][slots] "
-                                 f"tensor on {dev}")
-            wptr, wstride = weights.data_ptr(), weights.shape[2]
+            wptr, wstride = self._weights(weights, R)
         if workspace is None:
             workspace = _on_stream(self.attend_workspace, stream, ntok=n, num_requests=R,
-                                  q_heads=hq, max_len=max_len, max_new=max_new, dtype=q.dtype,
-                                  weights=weights is not None)
-        qs, os_ = q.stride(), out.stride()
-        a = _pack_attend(*self._table(block_table), q.data_ptr(), out.data_ptr(), qs[0], qs[1],
-                         os_[0], os_[1], _dtype_code(q.dtype), hq, n, R, max_new,
-                         _int_table(cu_seqlens, "cu_seqlens", dev),
+                                   q_heads=hq, max_len=max_len, max_new=max_new, dtype=dt,
+                                   weights=weights is not None)
+        a = _pack_attend(*table, q.data_ptr(), out.data_ptr(), qs[0], qs[1], os_[0], os_[1], code,
+                         hq, n, R, max_new, _int_table(cu_seqlens, "cu_seqlens", dev),
                          _int_table(lens, "lens", dev), max_len,
                          d ** -0.5 if scale is None else scale, lse.data_ptr(), wptr, wstride,
                          workspace.data_ptr(), workspace.numel(), _status_ptr(status, dev))
-        st = load().kvx_attend8(a, _raw_stream(stream, dev))
+        st = _Fast.attend(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_attend8")
         return out, lse
+
+    def _weights(self, w, R):
+        """Pointer and row length of accumulated weights [R][heads][slots]."""
+        shape = w.shape
+        if w.dtype is not _Fast.f32 or w.device != self.device or len(shape) != 3 or \
+                shape[0] != R or shape[1] != self.heads or not w.is_contiguous():
+            raise ValueError(f"weights must be a contiguous fp32 [{R}][{self.heads}][slots] tensor "
+                             f"on {self.device}")
+        return w.data_ptr(), shape[2]
 
     def evict_workspace(self, *, num_requests, max_len, keep):
         """A workspace (uint8) for ``evict`` calls of at most these sizes that
@@ -1046,41 +1084,46 @@ class Cache8:
         [R][heads][>= max_len]; move them into the blocks of ``dst_table`` (same
         pool, none of them read by this call).  Returns kept slots
         [R][heads][keep] (-1 beyond), their weights and the new lengths [R]."""
-        import torch
         dev = self.device
         _on_device(dev)
+        table = self._table(block_table)
         R = block_table.shape[0]
-        if weights.dtype != torch.float32 or weights.device != dev or weights.dim() != 3 or \
-                tuple(weights.shape[:2]) != (R, self.heads) or not weights.is_contiguous():
-            raise ValueError(f"weights must be a contiguous fp32 [{R}][{self.heads}][slots] tensor "
-                             f"on {dev}")
+        wptr, wstride = self._weights(weights, R)
         if lens.shape[0] != R or dst_table.dim() != 2 or dst_table.shape[0] != R:
             raise ValueError("lens, block_table and dst_table must hold the same requests")
         shape = (R, self.heads, keep)
         if kept is None:
-            kept = _on_stream(torch.empty, stream, shape, dtype=torch.int32, device=dev)
+            kept = _new(stream, shape, _Fast.i32, dev)
+        elif tuple(kept.shape) != shape:
+            raise ValueError("kept must be [R][heads][keep]")
         if kept_weights is None:
-            kept_weights = _on_stream(torch.empty, stream, shape, dtype=torch.float32,
-                                      device=dev)
+            kept_weights = _new(stream, shape, _Fast.f32, dev)
+        elif kept_weights.dtype is not _Fast.f32 or kept_weights.device != dev or \
+                tuple(kept_weights.shape) != shape or not kept_weights.is_contiguous():
+            raise ValueError(f"kept_weights must be a contiguous fp32 [R][heads][keep] tensor on {dev}")
         if new_lens is None:
-            new_lens = _on_stream(torch.empty, stream, R, dtype=torch.int32, device=dev)
-        if kept_weights.dtype != torch.float32 or kept_weights.device != dev or \
-                tuple(kept_weights.shape) != shape or tuple(kept.shape) != shape or \
-                new_lens.shape[0] != R or not kept_weights.is_contiguous():
-            raise ValueError("kept, kept_weights: contiguous [R][heads][keep]; new_lens: [R]")
+            new_lens = _new(stream, (R,), _Fast.i32, dev)
+        elif new_lens.shape[0] != R:
+            raise ValueError("new_lens must be [R]")
         if workspace is None:
             workspace = _on_stream(self.evict_workspace, stream, num_requests=R, max_len=max_len,
-                                  keep=keep)
-        a = _pack_evict(*self._table(block_table), _int_table(dst_table, "dst_table", dev, 2),
-                        dst_table.shape[1], R, _int_table(lens, "lens", dev), max_len, keep,
-                        sinks, recent, weights.data_ptr(), weights.shape[2],
+                                   keep=keep)
+        a = _pack_evict(*table, _int_table(dst_table, "dst_table", dev, 2), dst_table.shape[1], R,
+                        _int_table(lens, "lens", dev), max_len, keep, sinks, recent, wptr, wstride,
                         _int_table(kept, "kept", dev, 3), kept_weights.data_ptr(),
                         _int_table(new_lens, "new_lens", dev), workspace.data_ptr(),
                         workspace.numel(), _status_ptr(status, dev))
-        st = load().kvx_evict8(a, _raw_stream(stream, dev))
+        st = _Fast.evict(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_evict8")
         return kept, kept_weights, new_lens
+
+
+def _new(stream, shape, dtype, device):
+    """An uninitialised tensor for a call on ``stream``."""
+    if stream is None:
+        return _Fast.empty(shape, dtype=dtype, device=device)
+    return _on_stream(_Fast.empty, stream, shape, dtype=dtype, device=device)
 
 
 def _on_stream(make, stream, *args, **kw):
