@@ -3,9 +3,14 @@
 // For each block and head, separately for keys and values: the scale is the
 // smallest power of two that brings the largest new magnitude to 448 or less
 // (or the block's own where it already holds tokens and that is larger), and
-// code = e4m3(x / scale).  Bound by HBM: the new rows are read once (a warp
-// re-reads its few rows from L1 after their maximum is known) and one byte an
-// element is written.
+// code = e4m3(x / scale).  Bound by HBM: the new rows are read once and one byte an
+// element is written.  139 thousand bf16 tokens of 8 heads x 128 dimensions into
+// blocks of 16 take 141 us, 6.06 TB/s, where a copy reaches 6.74.  A run of up to 64
+// elements a lane (those 16 x 128) stays in registers between the maximum and the
+// codes, all of its loads on their way at once; a longer one is read again, from L1
+// or L2 (the same call then takes 238 us).  The maximum is taken on the bits, bf16
+// two at a time, and finite numbers are told from others once a run: with
+// both done element by element the call was bound by its instructions (229 us).
 //
 // A warp quantises one run: the tokens of one request that share a block, for
 // one head's keys or values.  Runs are found from the tokens: a unit of
@@ -33,38 +38,86 @@ struct WriteParams {
   int H, d, bs, max_blocks, per_unit, bf16;
 };
 
-// 16 consecutive elements; infinities and NaN leave `amax` alone and raise `odd`.
+// 16 consecutive elements as they lie.
 template <typename T>
-__device__ __forceinline__ void load16(const T *p, bool vec, float (&v)[16]) {
-  if constexpr (sizeof(T) == 2) {
+struct Sixteen {
+  uint4 x[sizeof(T)];
+  __device__ __forceinline__ void load(const T *p, bool vec) {
     if (vec) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 t = reinterpret_cast<const uint4 *>(p)[i];
-        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-          v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-      }
+      for (int i = 0; i < (int)sizeof(T); ++i) x[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
     } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = __bfloat162float(p[i]);
-    }
-  } else {
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 t = reinterpret_cast<const float4 *>(p)[i];
-        v[4 * i] = t.x; v[4 * i + 1] = t.y; v[4 * i + 2] = t.z; v[4 * i + 3] = t.w;
-      }
-    } else {
+      T v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = p[i];
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T); ++i) {
+        constexpr int n = 16 / sizeof(T);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (sizeof(T) == 2)
+            w[k] = (uint32_t)__bfloat16_as_ushort(v[n * i + 2 * k]) | (uint32_t)__bfloat16_as_ushort(v[n * i + 2 * k + 1]) << 16;
+          else
+            w[k] = __float_as_uint(v[n * i + k]);
+        }
+        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) x[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void floats(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 2) {
+          v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+          v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        } else {
+          v[4 * i + k] = __uint_as_float(w[k]);
+        }
+      }
+    }
+  }
+  // The larger of the magnitudes' bits and `most` (bf16: two at a time, in the two
+  // halves): above those of every finite number where there is an infinity or a NaN.
+  __device__ __forceinline__ uint32_t largest(uint32_t most) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 2) most = __vmaxu2(most, w[k] & 0x7fff7fffu);
+        else most = max(most, w[k] & 0x7fffffffu);
+      }
+    }
+    return most;
+  }
+  // The largest finite magnitude and `amax` (where there is an infinity or a NaN).
+  __device__ __forceinline__ float largest_finite(float amax) const {
+    float v[16];
+    floats(v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = fabsf(v[e]) < INFINITY ? fmaxf(amax, fabsf(v[e])) : amax;
+    return amax;
+  }
+  template <bool ODD>
+  __device__ __forceinline__ uint4 codes(float f) const {
+    float v[16];
+    floats(v);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = ODD && v[e] != v[e] ? 0.f : v[e] * f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = e4m3x2(v[4 * j], v[4 * j + 1]) | e4m3x2(v[4 * j + 2], v[4 * j + 3]) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
 
 template <typename T>
 __device__ void write_run(const WriteParams &p, int m, int h, int64_t page, int s0, int64_t g0, int n,
@@ -81,22 +134,49 @@ __device__ void write_run(const WriteParams &p, int m, int h, int64_t page, int 
     }
     return x + row * p.ts[m];
   };
-  float amax = 0.f;
-  bool odd = false, lost = false;
-  for (int i = mine; i < n; i += rows) {
-    const T *src = source(i);
-    lost = lost || !src;
-    if (!src) continue;
-    float v[16];
-    load16(src, vec, v);
+  uint32_t most = 0;
+  bool lost = false;
+  constexpr int HELD = 4;
+  Sixteen<T> held[HELD];
+  const bool holds = n <= HELD * rows;     // of the whole warp
+  if (holds) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float a = fabsf(v[e]);
-      if (a < INFINITY) amax = fmaxf(amax, a); else odd = true;
+    for (int k = 0; k < HELD; ++k) {
+      const int i = mine + k * rows;
+      const T *src = i < n ? source(i) : nullptr;
+      lost = lost || (i < n && !src);
+      if (src) held[k].load(src, vec); else held[k].zero();
+    }
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) most = held[k].largest(most);
+  } else {
+#pragma unroll 2
+    for (int i = mine; i < n; i += rows) {
+      const T *src = source(i);
+      lost = lost || !src;
+      if (!src) continue;
+      Sixteen<T> x;
+      x.load(src, vec);
+      most = x.largest(most);
     }
   }
+  if constexpr (sizeof(T) == 2) most = max(most & 0xffffu, most >> 16) << 16;
+  most = __reduce_max_sync(~0u, most);
+  float amax = __uint_as_float(most);
+  const bool odd = most >= 0x7f800000u;
+  if (odd) {     // seldom: leave the infinities and NaN out
+    amax = 0.f;
+    for (int i = mine; i < n; i += rows) {
+      const T *src = source(i);
+      if (!src) continue;
+      Sixteen<T> x;
+      x.load(src, vec);
+      amax = x.largest_finite(amax);
+    }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    if (lane == 0) raise(p.status, KVX_FLAG_NOT_FINITE);
+  }
   float *scale = p.scale[m] + page * p.H + h;
   float now = pow2_scale(amax);
   if (s0) {   // the block's first tokens stay: one scale for both
@@ -121,42 +201,64 @@ __device__ void write_run(const WriteParams &p, int m, int h, int64_t page, int 
   }
   if (lane == 0) *scale = now;
   const float f = 1.f / now;
-  for (int i = mine; i < n; i += rows) {
-    const T *src = source(i);
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (src) {
-      float v[16];
-      load16(src, vec, v);
+  const auto store = [&](int i, const Sixteen<T> &x) {
+    __stcs(reinterpret_cast<uint4 *>(to + (int64_t)(s0 + i) * p.d), odd ? x.template codes<true>(f) : x.template codes<false>(f));
+  };
+  if (holds) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        v[e] = v[e] != v[e] ? 0.f : v[e] * f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = e4m3x2(v[4 * j], v[4 * j + 1]) | e4m3x2(v[4 * j + 2], v[4 * j + 3]) << 16;
+    for (int k = 0; k < HELD; ++k)
+      if (mine + k * rows < n) store(mine + k * rows, held[k]);
+  } else {
+#pragma unroll 2
+    for (int i = mine; i < n; i += rows) {
+      const T *src = source(i);
+      Sixteen<T> x;
+      if (src) x.load(src, vec); else x.zero();
+      store(i, x);
     }
-    *reinterpret_cast<uint4 *>(to + (int64_t)(s0 + i) * p.d) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  if (odd) raise(p.status, KVX_FLAG_NOT_FINITE);
   if (lost) raise(p.status, KVX_FLAG_BAD_SRC_BLOCK);
 }
 
-// Grid: x = units of tokens, y = groups of kWriteWarps (head, K|V) pairs.
+// The request of token g, by the whole warp: how many requests begin at or before it.
+__device__ __forceinline__ int request_of(const Requests &q, int64_t g) {
+  if (!q.cu) return (int)g;
+  int n = 0;
+  for (int r0 = 0; r0 < q.R; r0 += 32) {
+    const int r = r0 + threadIdx.x % 32;
+    const unsigned here = __ballot_sync(~0u, r < q.R && (int64_t)__ldg(q.cu + r) <= g);
+    n += __popc(here);
+    if (here != ~0u) break;
+  }
+  return n - 1;
+}
+// Requests::ok by each warp for itself.
+__device__ __forceinline__ bool table_ok(const Requests &q) {
+  bool good = true;
+  if (q.cu)
+    for (int r = threadIdx.x % 32; r < q.R; r += 32) {
+      const int32_t beg = __ldg(q.cu + r), end = __ldg(q.cu + r + 1);
+      good = good && end >= beg && (r > 0 || beg == 0) && (r + 1 < q.R || end == q.ntok);
+    }
+  return __all_sync(~0u, good);
+}
+
+// Grid: x = units of tokens, y = groups of (head, K|V) pairs.  A warp takes several
+// pairs of a run in turn: finding the run costs more than one pair of it (up to four
+// pairs 141 us, two 147; CTAs of eight warps 154).
 template <typename T>
 __global__ void __launch_bounds__(32 * kWriteWarps) write_kernel(const __grid_constant__ WriteParams p,
                                                                  bool vec) {
-  const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
-  if (!p.req.ok()) {
-    if (first_cta && threadIdx.x == 0) raise(p.status, KVX_FLAG_BAD_SEQLENS);
+  const int hm0 = blockIdx.y * kWriteWarps + threadIdx.x / 32;
+  const bool speaks = hm0 == 0 && threadIdx.x % 32 == 0;
+  if (!table_ok(p.req)) {
+    if (speaks && blockIdx.x == 0) raise(p.status, KVX_FLAG_BAD_SEQLENS);
     return;
   }
-  const int hm = blockIdx.y * kWriteWarps + threadIdx.x / 32;
-  if (hm >= 2 * p.H) return;
-  const int m = hm / p.H, h = hm % p.H;
-  const bool speaks = hm == 0 && threadIdx.x % 32 == 0;
   int64_t g = (int64_t)blockIdx.x * p.per_unit;
   const int64_t end = g + p.per_unit < p.req.ntok ? g + p.per_unit : p.req.ntok;
   while (g < end) {
-    const int r = p.req.of(g);
+    const int r = request_of(p.req, g);
     const int64_t beg = p.req.begin(r), stop = p.req.begin(r + 1);
     const int64_t start = p.start ? (int64_t)p.start[r] : 0;
     if (start < 0) {
@@ -169,10 +271,12 @@ __global__ void __launch_bounds__(32 * kWriteWarps) write_kernel(const __grid_co
     const int64_t left = stop - g, n = p.bs - s0 < left ? p.bs - s0 : left;
     if (g == beg || s0 == 0) {
       const int64_t page = block < p.max_blocks ? (int64_t)p.table[(int64_t)r * p.max_blocks + block] : -1;
-      if (page >= 0 && page < p.num_blocks)
-        write_run<T>(p, m, h, page, s0, g, (int)n, vec);
-      else if (speaks)
+      if (page >= 0 && page < p.num_blocks) {
+        for (int hm = hm0; hm < 2 * p.H; hm += gridDim.y * kWriteWarps)
+          write_run<T>(p, hm / p.H, hm % p.H, page, s0, g, (int)n, vec);
+      } else if (speaks) {
         raise(p.status, block < p.max_blocks ? KVX_FLAG_BAD_BLOCK : KVX_FLAG_BAD_LENGTH);
+      }
     }
     g += n;
   }
@@ -219,8 +323,10 @@ extern "C" kvx_status kvx_cache8_write(const kvx_cache8_write_args *a, void *str
   p.per_unit = (int)(mean < 1 ? 1 : mean > c.block_size ? c.block_size : mean);
   const bool vec = aligned_to(a->k, 16) && aligned_to(a->v, 16) &&
                    ((p.ts[0] | p.ts[1] | p.hs[0] | p.hs[1]) * size) % 16 == 0;
-  const dim3 grid((unsigned)((a->ntok + p.per_unit - 1) / p.per_unit),
-                  (unsigned)((2 * c.heads + kWriteWarps - 1) / kWriteWarps));
+  // pairs in turn in a warp: up to four once that leaves 16 warps an SM
+  const int64_t units = (a->ntok + p.per_unit - 1) / p.per_unit, want = units * 2 * c.heads / (152 * 16);
+  const int turns = kWriteWarps * (int)(want < 1 ? 1 : want > 4 ? 4 : want);
+  const dim3 grid((unsigned)units, (unsigned)((2 * c.heads + turns - 1) / turns));
   cudaStream_t s = (cudaStream_t)stream;
   if (size == 2)
     write_kernel<__nv_bfloat16><<<grid, 32 * kWriteWarps, 0, s>>>(p, vec);
