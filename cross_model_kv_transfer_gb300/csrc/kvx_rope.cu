@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
   const int a0 = p.interleaved ? 2 * u * V : u * V;
   const int a1 = p.interleaved ? a0 + V : a0 + half;
-#pragma unroll 2
+#pragma unroll 4
   for (int j = 0; j < p.head_steps; ++j, h += p.head_lanes) {
     const T *src;
     T *dst;
@@ -298,9 +298,11 @@ extern "C" kvx_status kvx_rope_apply(const kvx_rope *rope, const kvx_rope_args *
     return cudaGetLastError() == cudaSuccess ? KVX_OK : KVX_ERR_CUDA;
   }
   const int pieces = rot / 2 / V + (d - rot) / V, slots = kRopeThreads / pieces;
-  // up to eight heads in turn in a thread once that leaves threads for two
-  // waves; the heads side by side in a CTA are a power of two, to fill it
-  const int64_t want = a->ntok * total * pieces / (152 * 2048 * 2);
+  // up to eight heads in turn in a thread, fewer where that would not leave 1024
+  // threads an SM (2047 fp32 tokens of 16 + 8 heads x 128, 64 turned: 19.6 us; with
+  // 512 an SM 20.3, with 2048 22.8, with 4096 26.1); the heads side by side in a
+  // CTA are a power of two, to fill it
+  const int64_t want = a->ntok * total * pieces / (152 * 1024);
   const int turns = (int)(want < 1 ? 1 : want > 8 ? 8 : want);
   p.head_lanes = 1;
   while (2 * p.head_lanes <= slots && 2 * p.head_lanes * turns <= total) p.head_lanes *= 2;
