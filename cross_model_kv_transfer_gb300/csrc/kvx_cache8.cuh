@@ -77,6 +77,10 @@ __device__ __forceinline__ void raise(uint32_t *status, uint32_t bits) {
 
 inline bool aligned_to(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// The kernel is launched while the one before on its stream still runs: what that
+// one writes may be read after this.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Host checks of a cache.
 inline kvx_status check_cache8(const kvx_cache8 &c) {
   if (!c.k_codes || !c.v_codes || !c.k_scale || !c.v_scale || !c.block_table)
@@ -91,6 +95,22 @@ inline kvx_status check_cache8(const kvx_cache8 &c) {
       !aligned_to(c.v_scale, 4) || !aligned_to(c.block_table, 4))
     return KVX_ERR_INVALID_ARG;
   return KVX_OK;
+}
+
+// Launch beside the end of the kernel before (which the kernel waits for itself).
+template <class... P, class... A>
+kvx_status launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? KVX_OK : KVX_ERR_CUDA;
 }
 
 inline kvx_status launched() { return cudaGetLastError() == cudaSuccess ? KVX_OK : KVX_ERR_CUDA; }
