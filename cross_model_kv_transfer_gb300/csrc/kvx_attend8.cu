@@ -672,8 +672,9 @@ __global__ void __launch_bounds__(256) weights_of_scores_kernel(const __grid_con
   __syncthreads();
   const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (j >= len) return;
-  float sum = 0.f;
+  float sum = 0.f;     // of the groups' sums: fewer roundings than of all in a row
   for (int c0 = 0; c0 < cols; c0 += cols_of_group) {
+    float part = 0.f;
     const int64_t seg = ((int64_t)r * a.H + h) * p.groups + c0 / cols_of_group;
     const float *x = p.scores + (seg * a.max_len + j) * cols_of_group;
     for (int c = 0; c < cols_of_group && c0 + c < cols; c += 4) {
@@ -681,8 +682,9 @@ __global__ void __launch_bounds__(256) weights_of_scores_kernel(const __grid_con
       const float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (c0 + c + e < cols && z[e] > -INFINITY) sum += ex2(z[e] - lse2[c0 + c + e]);
+        if (c0 + c + e < cols && z[e] > -INFINITY) part += ex2(z[e] - lse2[c0 + c + e]);
     }
+    sum += part;
   }
   a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
 }
@@ -699,7 +701,9 @@ __global__ void __launch_bounds__(128) weights_kernel(const __grid_constant__ At
   const uint8_t *row = p.k + (((int64_t)page * p.H + h) * p.bs + j % p.bs) * p.d;
   const float ks = p.ks[(int64_t)page * p.H + h] * p.c;
   float sum = 0.f;
-  for (int64_t i = j - (len - n) > 0 ? j - (len - n) : 0; i < n; ++i)
+  const int64_t i0 = j - (len - n) > 0 ? j - (len - n) : 0;
+  float part = 0.f;    // of 32 queries: fewer roundings than of all in a row
+  for (int64_t i = i0; i < n; ++i) {
     for (int u = 0; u < p.G; ++u) {
       const int hq = h * p.G + u;
       float s = 0.f;
@@ -707,8 +711,13 @@ __global__ void __launch_bounds__(128) weights_kernel(const __grid_constant__ At
         const float2 a = floats_of(*reinterpret_cast<const uint16_t *>(row + e));
         s += q_at(p, beg + i, hq, e) * a.x + q_at(p, beg + i, hq, e + 1) * a.y;
       }
-      sum += exp2f(s * ks - p.lse[(beg + i) * p.Hq + hq] * kLog2e);
+      part += exp2f(s * ks - p.lse[(beg + i) * p.Hq + hq] * kLog2e);
     }
+    if ((i - i0) % 32 == 31 || i + 1 == n) {
+      sum += part;
+      part = 0.f;
+    }
+  }
   p.weights[((int64_t)r * p.H + h) * p.wstride + j] += sum;
 }
 
@@ -755,12 +764,11 @@ Shape shape_of(const kvx_attend8_args *a) {
 
 template <int DP, int NT, int PARTS>
 kvx_status launch_split(const SplitParams &p, int grid, cudaStream_t s) {
-#ifndef MTX
-#define MTX (DP <= 128 && NT * PARTS <= 2 ? 2 : 1)
-#define STX (DP == 64 ? 8 / MTX : DP == 128 ? (MTX == 2 ? 3 : 5) : 2)
-#define WX 8
-#endif
-  using C = SplitCfg<DP, NT, PARTS, MTX, WX, STX>;
+  // tiles of 16 slots a warp works on at once, while the sums leave registers for two;
+  // stages: 8 slots tiles deep, or what shared memory holds
+  constexpr int MT = DP <= 128 && NT * PARTS <= 2 ? 2 : 1;
+  constexpr int STAGES = DP == 64 ? 8 / MT : DP == 128 ? (MT == 2 ? 3 : 5) : 2;
+  using C = SplitCfg<DP, NT, PARTS, MT, 8, STAGES>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(split_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);

@@ -1,5 +1,6 @@
 // kvx_attend8_tc.cu -- attention over the 8-bit cache on tcgen05 tensor cores:
-// bf16 queries, head_dim 128, blocks of whole 8-slot groups.
+// bf16 queries, head_dim up to 128 (fewer dimensions lie in tiles of 128 whose
+// others are zero), blocks of whole 8-slot groups.
 //
 // Rows are the (query, head of the group) pairs of one request and KV head, 128
 // to a tile; slots come 128 to a tile by TMA from the paged codes.
@@ -37,7 +38,7 @@
 
 namespace {
 
-constexpr int kD = 128;             // head_dim
+constexpr int kD = 128;             // dimensions of a tile
 constexpr int kTile = 128;          // slots and rows of a tile
 constexpr int kHalf = kTile / 2;   // slots whose scores and products are formed at a time
 constexpr int kTileBytes = kTile * kD;
@@ -548,7 +549,7 @@ __device__ __noinline__ float query_factor(const AttendParams &a, bool vec, cons
   float top = 0.f;
   if (live && vec) {
 #pragma unroll 4
-    for (int e = 0; e < kD / 8; ++e) {
+    for (int e = 0; e < a.d / 8; ++e) {
       const uint4 t = __ldg(reinterpret_cast<const uint4 *>(src) + e);
       const uint32_t v[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
@@ -557,7 +558,7 @@ __device__ __noinline__ float query_factor(const AttendParams &a, bool vec, cons
     }
   } else if (live) {
 #pragma unroll 4
-    for (int e = 0; e < kD; ++e) top = fmaxf(top, fabsf(__bfloat162float(src[e])));
+    for (int e = 0; e < a.d; ++e) top = fmaxf(top, fabsf(__bfloat162float(src[e])));
   }
   return row_factor(a, top, pow2_scale(top));
 }
@@ -577,7 +578,7 @@ __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const
     for (int i = 0; i < 4; ++i) {
       const int row = 2 * (i0 + i) + lane / 16;
       const uint64_t p = __shfl_sync(~0u, (uint64_t)src, row);
-      const bool there = __shfl_sync(~0u, (int)live, row);
+      const bool there = __shfl_sync(~0u, (int)live, row) && 8 * c < a.d;
       const uint4 *from = reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + 8 * c);
       x[i] = there && vec ? __ldg(from) : make_uint4(0, 0, 0, 0);
       if (!vec && there) {
@@ -732,6 +733,7 @@ __device__ __noinline__ void join_rows(const TcParams &p, const TcWalk &w, int c
     for (int k = 0; k < B; ++k) {
       const int64_t row = (int64_t)w.group * G::ROWS + rr[k], tok = w.beg + row / a.G;
       const int hq = w.h * a.G + (int)(row % a.G);
+      if (lane * 4 >= a.d) continue;
       store_out(a, tok, hq, lane * 4, make_float2(oo[k].x, oo[k].y), mm[k], ll[k]);
       store_out(a, tok, hq, lane * 4 + 2, make_float2(oo[k].z, oo[k].w), mm[k], ll[k]);
     }
@@ -814,6 +816,7 @@ __global__ void __launch_bounds__(256) join_row_kernel(const __grid_constant__ T
   const AttendParams &a = p.a;
   const int64_t at = (int64_t)x.group * G::ROWS + row, tok = x.beg + at / a.G;
   const int hq = x.h * a.G + (int)(at % a.G);
+  if (lane * 4 >= a.d) return;
   store_out(a, tok, hq, lane * 4, make_float2(oo.x, oo.y), mm, ll);
   store_out(a, tok, hq, lane * 4 + 2, make_float2(oo.z, oo.w), mm, ll);
 }
@@ -876,10 +879,12 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
         if (p.vec_out) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            reinterpret_cast<uint4 *>(to)[e] = make_uint4(b[4 * e], b[4 * e + 1], b[4 * e + 2], b[4 * e + 3]);
+            if (32 * c + 8 * e < a.d)
+              reinterpret_cast<uint4 *>(to)[e] = make_uint4(b[4 * e], b[4 * e + 1], b[4 * e + 2], b[4 * e + 3]);
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
+            if (32 * c + 2 * e >= a.d) break;
             to[2 * e] = __ushort_as_bfloat16((unsigned short)(b[e] & 0xffff));
             to[2 * e + 1] = __ushort_as_bfloat16((unsigned short)(b[e] >> 16));
           }
@@ -2026,8 +2031,9 @@ TcShape tc_shape(const kvx_attend8_args *a) {
 bool encode(CUtensorMap *map, const kvx_cache8 &c, const void *base, int box) {
   static const EncodeFn fn = reinterpret_cast<EncodeFn>(kvx_tc_encoder());
   if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)c.num_blocks * c.heads * c.block_size};
-  const cuuint64_t strides[1] = {(cuuint64_t)kD};
+  // fewer dimensions are filled with zeros
+  const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.num_blocks * c.heads * c.block_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
   const cuuint32_t boxes[2] = {(cuuint32_t)kD, (cuuint32_t)box}, one[2] = {1u, 1u};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, boxes, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -2049,7 +2055,7 @@ kvx_status launch(K kernel, int threads, size_t smem, const TcParams &p, const C
 
 bool kvx_attend8_tc_supports(const kvx_attend8_args *a) {
   const kvx_cache8 &c = a->cache;
-  return a->dtype == KVX_BF16 && c.head_dim == kD && c.block_size % 8 == 0 &&
+  return a->dtype == KVX_BF16 && c.head_dim <= kD && c.block_size % 8 == 0 &&
          (uint64_t)c.num_blocks * c.heads * c.block_size <= INT32_MAX;
 }
 
