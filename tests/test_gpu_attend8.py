@@ -290,3 +290,25 @@ def test_no_queries_and_no_slots():
     w = torch.ones((1, 1, 8), device="cuda")
     out, lse = c["cache"].attend(c["q"].cuda(), dev(c["table"]), dev([0]), 0, weights=w)
     assert (out == 0).all() and torch.isneginf(lse).all() and (w == 1).all()
+
+
+@pytest.mark.parametrize("G,new", [(4, 1), (4, 12), (4, 70), (16, 1), (3, 61)])
+@pytest.mark.parametrize("d", [128, 112, 48])
+def test_unaligned_rows_of_every_form(d, G, new):
+    """bf16 queries and outputs that no 16-byte access can reach, few rows to many,
+    with the weights."""
+    lens = [new + 77, new + 200]
+    c = make(2, G, d, 16, lens, [new, new], torch.bfloat16, 41)
+    n, hq = 2 * new, 2 * G
+    wide = torch.full((n, hq + 1, d + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:, 1:d + 1] = c["q"].cuda()
+    into = torch.full((n, hq, d + 5), 3.0, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((2, 2, max(lens)), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = c["cache"].attend(wide[:, 1:, 1:d + 1], dev(c["table"]), dev(lens), max(lens),
+                                 cu_seqlens=dev(c["cu"]), max_new=new, out=into[:, :, 3:d + 3],
+                                 weights=w, status=status)
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], d ** -0.5)
+    assert int(status.item()) == 0
+    compare(out, lse, w, want, True, max(lens), new * G)
+    assert (into[:, :, :3] == 3).all() and (into[:, :, d + 3:] == 3).all()
