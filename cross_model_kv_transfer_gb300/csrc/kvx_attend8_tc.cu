@@ -33,6 +33,7 @@
 
 #include <type_traits>
 
+
 #include "kvx_attend8.cuh"
 #include "kvx_ptx.cuh"
 
@@ -478,19 +479,12 @@ __device__ __forceinline__ void columns(uint32_t (&s)[32], float (&f)[8], const 
     }
   }
 }
-// The largest of the scaled scores and `top`.
-__device__ __forceinline__ float peak_of(const uint32_t (&s)[32], const float (&f)[8], float top) {
-  const float *x = reinterpret_cast<const float *>(s);
-  float u[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) u[q] = fmaxf(max3(x[4 * q], x[4 * q + 1], x[4 * q + 2]), x[4 * q + 3]) * f[q];
-  return max3(max3(top, max3(u[0], u[1], u[2]), max3(u[3], u[4], u[5])), u[6], u[7]);
-}
-// exp2(score f cs + add) in f16, two to a register, and their sum.
+// exp2(y), y = score f cs + add, in f16, two to a register, their sum and the largest y.
 template <bool MASK>
 __device__ __forceinline__ uint64_t probabilities(uint32_t *out, const uint32_t (&s)[32], const float (&f)[8], float cs,
-                                                  uint64_t add, uint64_t sum) {
+                                                  uint64_t add, uint64_t sum, float &top) {
   const float *x = reinterpret_cast<const float *>(s);
+  float t0 = top, t1 = top;
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     // not 0, which would make NaN of -inf
@@ -499,12 +493,15 @@ __device__ __forceinline__ uint64_t probabilities(uint32_t *out, const uint32_t 
     float y[4];
     unpair(fma2(pair(x[4 * q], x[4 * q + 1]), g2, add), y[0], y[1]);
     unpair(fma2(pair(x[4 * q + 2], x[4 * q + 3]), g2, add), y[2], y[3]);
+    t0 = max3(t0, y[0], y[1]);
+    t1 = max3(t1, y[2], y[3]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = ex2(y[e]);
     sum = add2(sum, add2(pair(y[0], y[1]), pair(y[2], y[3])));
     out[2 * q] = f16x2(y[0], y[1]);
     out[2 * q + 1] = f16x2(y[2], y[3]);
   }
+  top = fmaxf(t0, t1);
   return sum;
 }
 // A half tile of a row: probabilities over the scores they come from, the row's
@@ -521,20 +518,20 @@ __device__ __forceinline__ bool softmax_half(uint32_t col, const float4 *scale, 
   tc_wait_ld32(b);
   columns<MASK>(a, fa, scale, mask, seen);
   columns<MASK>(b, fb, scale + 2, mask >> 8, seen - 32);
-  float top = -INFINITY, s0, s1;
+  float s0, s1;
 #pragma unroll 1
   while (true) {
     const float add = kBias + ref - finite_or_0(m);
     const uint64_t a2 = pair(add, add);
-    uint64_t sum = probabilities<MASK>(out, a, fa, cs, a2, pair(0.f, 0.f));
-    sum = probabilities<MASK>(out + 16, b, fb, cs, a2, sum);
-    top = peak_of(b, fb, peak_of(a, fa, top));
-    const float peak = top * cs + ref;      // -inf where nothing is seen
-    const bool over = peak > m + kSlack || (m == -INFINITY && peak > -INFINITY);
+    float top = -INFINITY;
+    uint64_t sum = probabilities<MASK>(out, a, fa, cs, a2, pair(0.f, 0.f), top);
+    sum = probabilities<MASK>(out + 16, b, fb, cs, a2, sum, top);
+    // -inf where nothing is seen
+    const bool over = top > kBias + kSlack || (m == -INFINITY && top > -INFINITY);
     unpair(sum, s0, s1);
     if (!__any_sync(~0u, over)) break;
     // seldom: the probabilities again, with the rows' maxima raised
-    const float mm = fmaxf(m, peak), down = ex2(m - finite_or_0(mm));
+    const float mm = fmaxf(m, top - kBias + finite_or_0(m)), down = ex2(m - finite_or_0(mm));
     if (!raise(down)) return false;
     m = mm;
     l *= down;
@@ -565,17 +562,19 @@ __device__ __noinline__ float query_factor(const AttendParams &a, bool vec, cons
 // Up to 32 query rows of a warp (`count` of them, rounded up to 8) as two e4m3
 // parts, `part` bytes apart, in the swizzled K-major tile, from row `first` of the
 // tile on; `src` is the lane's own row.  Half a warp loads a row, eight rows at a
-// time: short code, which a CTA runs cold.  Returns the lane's factor on its row's
+// time where a CTA does one or two items and runs this code cold, sixteen where it
+// does many (wide calls).  Returns the lane's factor on its row's
 // scores (its sign is in the parts).
+template <int N>
 __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
                                           unsigned char *tile, int first, int part, int count) {
   const int lane = threadIdx.x % 32, c = lane % 16;      // 8 dimensions
   float mine = 0.f;
 #pragma unroll 1
-  for (int i0 = 0; 2 * i0 < count; i0 += 4) {
-    uint4 x[4];
+  for (int i0 = 0; 2 * i0 < count; i0 += N) {
+    uint4 x[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int row = 2 * (i0 + i) + lane / 16;
       const uint64_t p = __shfl_sync(~0u, (uint64_t)src, row);
       const bool there = __shfl_sync(~0u, (int)live, row) && 8 * c < a.d;
@@ -596,7 +595,7 @@ __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       float y[8], top = 0.f;
 #pragma unroll
@@ -859,38 +858,70 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   const bool direct = WIDE && whole;
   if (warp_live) {
     const float inv = direct ? (l != 0.f ? back / l : 0.f) : back;
+    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + tok * a.ot + hq * a.oh;
+    if (WIDE && (!direct || p.vec_out)) {
+      // Through shared memory, so that rows go out whole: a lane's row is written
+      // there 16 bytes at a time, and half a warp stores a row's 256.  It lies where
+      // the warp's own query rows were, whose products are over.
+      extern __shared__ unsigned char raw[];
+      unsigned char *own = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023)) +
+                           i * 2 * kTileBytes + warp % 4 * 32 * kD;
+      const auto cell = [&](int r, int at) {    // 16 bytes `at` of row r
+        return reinterpret_cast<uint4 *>(own + (at / 8) * kTileBytes + r * 128 + ((at % 8 ^ (r & 7)) << 4));
+      };
+      uint64_t to = direct ? (uint64_t)out : (uint64_t)(slot + row * kD);
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[32];
-      tc_ld32(o_col + 32 * c, o);
-      tc_wait_ld();
-      if (live && !direct) {
-        float4 *to = reinterpret_cast<float4 *>(slot + row * kD + 32 * c);
+      for (int half_row = 0; half_row < (direct ? 1 : 2); ++half_row) {
+#pragma unroll 1
+        for (int c = 0; c < (direct ? 4 : 2); ++c) {
+          uint32_t o[32];
+          tc_ld32(o_col + 64 * half_row + 32 * c, o);
+          tc_wait_ld32(o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          to[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                              __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
-      } else if (live) {
-        __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.out) + tok * a.ot + hq * a.oh + 32 * c;
-        uint32_t b[16];
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+          if (direct) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          b[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-        if (p.vec_out) {
+            for (int e = 0; e < 4; ++e) {
+              uint32_t b[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (32 * c + 8 * e < a.d)
-              reinterpret_cast<uint4 *>(to)[e] = make_uint4(b[4 * e], b[4 * e + 1], b[4 * e + 2], b[4 * e + 3]);
-        } else {
+              for (int k = 0; k < 4; ++k) b[k] = pack_bf16(__uint_as_float(o[8 * e + 2 * k]), __uint_as_float(o[8 * e + 2 * k + 1]));
+              *cell(lane, 4 * c + e) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+          } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (32 * c + 2 * e >= a.d) break;
-            to[2 * e] = __ushort_as_bfloat16((unsigned short)(b[e] & 0xffff));
-            to[2 * e + 1] = __ushort_as_bfloat16((unsigned short)(b[e] >> 16));
+            for (int e = 0; e < 8; ++e) *cell(lane, 8 * c + e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += 2) {
+          const int r = r0 + lane / 16;
+          const uint64_t base = __shfl_sync(~0u, to, r);
+          if (row - lane + r < rows && (!direct || 8 * (lane % 16) < a.d))
+            reinterpret_cast<uint4 *>(base)[lane % 16] = *cell(r, lane % 16);
+        }
+        to += 256;
+        __syncwarp();
       }
-      __syncwarp();   // together to the next load
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tc_ld32(o_col + 32 * c, o);
+        tc_wait_ld32(o);
+        if (live && !direct) {
+          float4 *to = reinterpret_cast<float4 *>(slot + row * kD + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            to[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+        } else if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * c + e < a.d) out[32 * c + e] = __float2bfloat16_rn(__uint_as_float(o[e]) * inv);
+        }
+        __syncwarp();   // together to the next load
+      }
     }
     if (live) {
       const float mt = m - kBias;           // what the sums are relative to
@@ -1005,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
       float m = -INFINITY, l = 0.f, cs;
       if (WIDE || i == 0) {
-        cs = put_queries(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes, 32);
+        cs = put_queries<WIDE ? 8 : 4>(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes, 32);
         fence_async_proxy();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[i]));
@@ -1236,6 +1267,7 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
   const int64_t beg = a.req.begin(r);
   const int rows = (int)(a.req.begin(r + 1) - beg) * a.G;
+  wait_for_kernel_before();
   for (int c = threadIdx.x; c < rows; c += 256)
     lse2[c] = a.lse[(beg + c / a.G) * a.Hq + h * a.G + c % a.G] * kLog2e;
   __syncthreads();
@@ -1457,7 +1489,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
       const int rows = (int)min((int64_t)NC, (int64_t)w.fresh * a.G - row0);
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
                                  (int64_t)(w.h * a.G + (int)((row0 + lane) % a.G)) * a.qh;
-      const float f = put_queries(a, p.vec_q, src, lane < rows, qbuf + (item & 1) * 2 * kColQBytes, 0, kColQBytes, 16);
+      const float f = put_queries<4>(a, p.vec_q, src, lane < rows, qbuf + (item & 1) * 2 * kColQBytes, 0, kColQBytes, 16);
       if (lane < 16) sh->cs[item & 1][lane] = f;
       fence_async_proxy();
       __syncwarp();
@@ -1847,8 +1879,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int64_t tok = beg + row / a.G;
       const int hq = h * a.G + row % a.G;
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + tok * a.qt + (int64_t)hq * a.qh;
-      const float cs = put_queries(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32, kTileBytes, 32);
+      const float cs = put_queries<4>(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32, kTileBytes, 32);
       float *pair_of = reinterpret_cast<float *>(&sh->rows[tid / 2]) + tid % 2;
+      if (c == 0) wait_for_kernel_before();   // the log-sum-exps
       // a dead row gives exp2(-inf)
       pair_of[0] = live ? cs : 0.f;
       pair_of[2] = live ? -a.lse[tok * a.Hq + hq] * kLog2e : -INFINITY;
@@ -2091,11 +2124,9 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
     while (per < 16 && (int64_t)items * ((tiles + per - 1) / per) > 152) ++per;
     if (cudaFuncSetAttribute(weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWtSmem) != cudaSuccess)
       return KVX_ERR_CUDA;
-    weights_tc_kernel<<<dim3((tiles + per - 1) / per, a.H, a.req.R), kWtThreads, kWtSmem, s>>>(p, mk, per);
-    return launched();
+    return launch_after(weights_tc_kernel, dim3((tiles + per - 1) / per, a.H, a.req.R), kWtThreads, kWtSmem, s, p, mk, per);
   }
   const dim3 grid((a.max_len + 255) / 256, a.H, a.req.R);
   if (sh.columns) return launch_after(weights_of_columns_kernel, grid, 256, 0, s, p);
-  weights_of_rows_kernel<<<grid, 256, sh.slot_rows * 4, s>>>(p);
-  return launched();
+  return launch_after(weights_of_rows_kernel, grid, 256, sh.slot_rows * 4, s, p);
 }
