@@ -17,7 +17,7 @@
 // Roles: warps 0-3 and 4-7 two softmax groups, warps 8-11 convert V, warp 12
 // loads (block lookups, scales, TMA), warps 13 and 14 issue the groups' MMAs.  WIDE: the groups
 // take the two 128-row halves of 256 rows, over the same slot tiles.  Narrow
-// (at most 128 rows): they take the even and the odd slot tiles of the same
+// (at most 64 rows): they take the even and the odd slot tiles of the same
 // rows, so that one tile's softmax overlaps the other's products.
 //
 // Work: every CTA takes an equal share of all steps and item costs (below); what
@@ -1808,7 +1808,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
 }
 
-// --- accumulated weights of wide calls -------------------------------------------
+// --- accumulated weights where the scores were not kept ----------------------------
 // weights[r][h][j] += sum over the rows that see slot j of exp2(score - lse).
 // The scores are formed again, transposed (S^T = K Q^T, slots in the lanes), so
 // that a slot's sum stays in one thread: no atomics, one order of summation.  A CTA
@@ -2042,22 +2042,28 @@ struct TcShape {
 TcShape tc_shape(const kvx_attend8_args *a) {
   TcShape s;
   const int64_t G = a->q_heads / a->cache.heads, most = G * a->max_new;
-  s.wide = most > kTile;
+  // One step of the cases below: 16 requests of 1024 to 16,384 slots, 8 KV heads,
+  // without and with weights.  16 rows: columns 109 and 135 us, narrow 143 and 195.
+  // 24 rows: narrow 149 and 214, wide 177 and 323; 64 rows: 186 and 315 against 186
+  // and 334; 128 rows: 254 and 507 against 182 and 333.
   s.columns = most <= 16;
+  s.wide = most > 64;
   s.slot_rows = s.wide ? Wide::ROWS : s.columns ? (most <= 8 ? 8 : 16) : (int)most;
   s.part_size = (s.slot_rows * (kD + 2) + 3) / 4 * 4;
   s.grid = 152;                        // one CTA an SM
   s.score_ld = (a->max_len + 255) / 256 * 256;
   s.box = a->cache.block_size & -a->cache.block_size;
   if (s.box > kTile) s.box = kTile;
-  s.spool = a->weights && !s.wide;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t items = (size_t)a->num_requests * a->cache.heads;
   s.splits = 0;
   s.partial = up(s.grid * sizeof(Split));
   s.lse = s.partial + up((size_t)2 * s.grid * (s.wide ? 1 : 2) * s.part_size * 4);
   s.scores = s.lse + up((size_t)a->ntok * a->q_heads * 4);
-  s.bytes = s.scores + (s.spool ? up(items * s.slot_rows * s.score_ld * 4) : 0);
+  // for the weights, scores are kept while they take 4 GB at most, else formed again
+  const size_t score_bytes = items * s.slot_rows * s.score_ld * 4;
+  s.spool = a->weights && !s.wide && score_bytes <= (size_t)4 << 30;
+  s.bytes = s.scores + (s.spool ? up(score_bytes) : 0);
   return s;
 }
 
@@ -2117,7 +2123,7 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
       : sh.slot_rows == 8 ? launch<Columns<8>>(columns_kernel<8>, kColThreads, kColSmem, p, mk, mv, s)
                           : launch<Columns<16>>(columns_kernel<16>, kColThreads, kColSmem, p, mk, mv, s);
   if (st != KVX_OK || !a.weights || a.max_len == 0) return st;
-  if (sh.wide) {
+  if (!sh.spool) {
     // as few slot tiles a CTA as lets all run at once, 16 at most
     const int tiles = (args->max_len + kTile - 1) / kTile, items = a.H * a.req.R;
     int per = 1;

@@ -312,3 +312,18 @@ def test_unaligned_rows_of_every_form(d, G, new):
     assert int(status.item()) == 0
     compare(out, lse, w, want, True, max(lens), new * G)
     assert (into[:, :, :3] == 3).all() and (into[:, :, d + 3:] == 3).all()
+
+
+@pytest.mark.parametrize("G,new", [(8, 1), (5, 4)])
+def test_weights_where_the_bound_on_lengths_is_too_large_to_keep_scores(G, new):
+    """Kept scores would take more than 4 GB: they are formed again instead."""
+    lens, bound = [new + 300, new + 77], 1 << 26
+    c = make(2, G, 128, 16, lens, [new, new], torch.bfloat16, 43)
+    w = torch.zeros((2, 2, bound), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = c["cache"].attend(c["q"].cuda(), dev(c["table"]), dev(lens), bound, cu_seqlens=dev(c["cu"]),
+                                 max_new=new, weights=w, status=status)
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], 128 ** -0.5)
+    assert int(status.item()) == 0
+    compare(out, lse, w[:, :, :max(lens)].contiguous(), want, True, max(lens), new * G)
+    assert not w[:, :, max(lens):].any()
