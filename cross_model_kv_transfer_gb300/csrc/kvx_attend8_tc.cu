@@ -20,6 +20,15 @@
 // (at most 64 rows): they take the even and the odd slot tiles of the same
 // rows, so that one tile's softmax overlaps the other's products.
 //
+// What it reaches.  Wide, one request of 8192 tokens, 64 heads: 1217 us, 0.90
+// PFLOP/s of the two products counted once, 0.46 of what bf16 matrix products reach;
+// counters have the tensor pipe active 0.37 of the time and the schedulers issuing
+// 0.48 of it: bound by the two groups' chain of score product, softmax and value
+// product.  (Score products in half tiles of 64 columns run at 0.6 of their rate at
+// 128, but whole tiles leave a group nothing to do while they are formed: 1397 us.)  61 tokens of 32
+// heads against 8192 slots, two requests: 45 us, 15 to join what 152 CTAs left, 26
+// for the weights; about a third of that fills and drains pipelines.
+//
 // Work: every CTA takes an equal share of all steps and item costs (below); what
 // several CTAs did of an item is joined by a second kernel.
 //
@@ -148,7 +157,9 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
 // tiles up to the last slot that its rows see.  An item costs its steps and a fixed
 // part (queries, a filling and draining pipeline, the result), so the CTAs' shares
 // are of costs: an item takes SETUP + steps places from `base` on, and its step s
-// is at place base + SETUP + s.
+// is at place base + SETUP + s.  Measured: wide, 8192 tokens, SETUP 3, 4, 5, 6: 1394,
+// 1293, 1217, 1213 us; narrow, 0, 1, 2, 3: 238, 211, 200, 201 us for a step of 16
+// requests.
 struct Wide {
   static constexpr int ROWS = 2 * kTile, SLOTS = kTile;   // of an item, of a step
   static constexpr int PARTS = 1;                         // results that a CTA keeps for an item
@@ -1297,6 +1308,10 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
 // share a maximum for each column: they vote on a tile, and only where one of them
 // exceeds it by 2^4 do they agree on a new one and scale O down.
 // Two groups of four warps take the even and the odd slot tiles.
+// Bound by HBM and what surrounds it: one query of 64 heads over 131,071 slots of 8
+// heads 56 us, 4.8 TB/s (a copy 6.7); 16 requests of 1024 to 16,384 slots 72 us.  The
+// narrow form above takes 119 and 208 there, matrix instructions on registers (16 x 8
+// x 16) 80 and 119.
 // even numbers of stages: a stage serves one group, whose waits on it then know
 // that the phase before is over
 constexpr int kCkStages = 4, kCvStages = 6, kScales = 16, kColThreads = 12 * 32;
@@ -2003,30 +2018,47 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// The same from the scores of few columns, [score_ld][slot_rows].
+// The same from the scores of few columns, [score_ld][slot_rows].  Bound by the
+// chain of its loads: a thread has four slots' on their way at once (16 requests of up
+// to 16,384 slots, 8 heads, with the attention before it: 93 us; two slots 95, one 97).
+constexpr int kSlotsOfThread = 4;
 __global__ void __launch_bounds__(256) weights_of_columns_kernel(const __grid_constant__ TcParams p) {
   const AttendParams &a = p.a;
   __shared__ float lse2[16];
-  const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r), j = blockIdx.x * 256 + threadIdx.x;
-  const int64_t beg = a.req.begin(r);
+  const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
+  const int64_t beg = a.req.begin(r), j0 = (int64_t)blockIdx.x * (256 * kSlotsOfThread) + threadIdx.x;
   const bool good = requests_ok(a);
   const int rows = good ? (int)(a.req.begin(r + 1) - beg) * a.G : 0;
+  float *to = a.weights + ((int64_t)r * a.H + h) * a.wstride + j0;
+  float before[kSlotsOfThread], sum[kSlotsOfThread] = {};
+#pragma unroll
+  for (int k = 0; k < kSlotsOfThread; ++k) before[k] = j0 + 256 * k < len ? to[256 * k] : 0.f;
   wait_for_kernel_before();
+  if ((int64_t)blockIdx.x * (256 * kSlotsOfThread) >= len || rows == 0) return;
   if (threadIdx.x < rows)
     lse2[threadIdx.x] = a.lse[(beg + threadIdx.x / a.G) * a.Hq + h * a.G + threadIdx.x % a.G] * kLog2e;
+  const float *x = p.scores + (((int64_t)r * a.H + h) * p.score_ld + j0) * p.slot_rows;
   __syncthreads();
-  if (j >= len || rows == 0) return;
-  const float *x = p.scores + (((int64_t)r * a.H + h) * p.score_ld + j) * p.slot_rows;
-  float sum = 0.f;
-#pragma unroll 2
-  for (int c = 0; c < p.slot_rows; c += 4) {
-    const float4 y = __ldcs(reinterpret_cast<const float4 *>(x + c));
-    const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll 1
+  for (int c = 0; c < rows; c += 8) {
+    float4 y[kSlotsOfThread][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < rows && z[e] > -INFINITY) sum += ex2(z[e] - lse2[c + e]);
+    for (int k = 0; k < kSlotsOfThread; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (j0 + 256 * k < len) y[k][e] = __ldcs(reinterpret_cast<const float4 *>(x + 256 * k * p.slot_rows + c) + e);
+#pragma unroll
+    for (int k = 0; k < kSlotsOfThread; ++k) {
+      if (j0 + 256 * k >= len) continue;
+      const float z[8] = {y[k][0].x, y[k][0].y, y[k][0].z, y[k][0].w, y[k][1].x, y[k][1].y, y[k][1].z, y[k][1].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < rows && z[e] > -INFINITY) sum[k] += ex2(z[e] - lse2[c + e]);
+    }
   }
-  a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
+#pragma unroll
+  for (int k = 0; k < kSlotsOfThread; ++k)
+    if (j0 + 256 * k < len) to[256 * k] = before[k] + sum[k];
 }
 
 // --- host ------------------------------------------------------------------------
@@ -2132,7 +2164,7 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
       return KVX_ERR_CUDA;
     return launch_after(weights_tc_kernel, dim3((tiles + per - 1) / per, a.H, a.req.R), kWtThreads, kWtSmem, s, p, mk, per);
   }
-  const dim3 grid((a.max_len + 255) / 256, a.H, a.req.R);
-  if (sh.columns) return launch_after(weights_of_columns_kernel, grid, 256, 0, s, p);
-  return launch_after(weights_of_rows_kernel, grid, 256, sh.slot_rows * 4, s, p);
+  const auto grid = [&](int slots) { return dim3((a.max_len + slots - 1) / slots, a.H, a.req.R); };
+  if (sh.columns) return launch_after(weights_of_columns_kernel, grid(256 * kSlotsOfThread), 256, 0, s, p);
+  return launch_after(weights_of_rows_kernel, grid(256), 256, sh.slot_rows * 4, s, p);
 }

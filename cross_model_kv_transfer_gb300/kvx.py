@@ -14,7 +14,11 @@ Low level (same names as the C ABI): ``kvx_plan_create``, ``kvx_transfer``,
 Convenience: ``Plan`` (owns a plan handle), ``Plan.transfer(...)`` which
 takes torch CUDA tensors, checks their shapes, dtypes and devices, and calls
 ``kvx_transfer`` on the current torch stream, and ``Plan.kv_diagnostics(...)``
-(fidelity statistics of a mapped cache against the target's own).
+(fidelity statistics of a mapped cache against the target's own).  Decoding on a
+transferred cache: ``Rope`` (rotary positions of new queries and keys) and
+``Cache8``, one layer's 8-bit paged cache with its ``write``, ``attend`` and
+``evict``; low level ``kvx_rope_init``, ``kvx_rope_apply``, ``kvx_cache8_write``,
+``kvx_attend8`` and ``kvx_evict8`` with their ``*_workspace_bytes``.
 """
 from __future__ import annotations
 

@@ -717,7 +717,11 @@ size_t kvx_attend8_workspace_bytes(const kvx_attend8_args *args);
  * Softmax statistics and sums are fp32.  A length outside [0, max_len] counts as
  * 0 (KVX_FLAG_BAD_LENGTH); slots of a block id outside [0, num_blocks) are
  * masked (KVX_FLAG_BAD_BLOCK); a malformed request table, or a request with
- * more than max_new queries, writes nothing (KVX_FLAG_BAD_SEQLENS). */
+ * more than max_new queries, writes nothing (KVX_FLAG_BAD_SEQLENS).  One to three
+ * launches.  bf16 queries with head_dim up to 128 and blocks of whole 8-slot groups
+ * run on the tcgen05 tensor cores: there an element of a query counts to 2^-19 of
+ * its row's largest.  max_len is at most 2^31 - 1025.  A kernel's wait that gives up
+ * sets KVX_FLAG_TIMEOUT. */
 kvx_status kvx_attend8(const kvx_attend8_args *args, void *stream);
 
 typedef struct {
@@ -742,6 +746,9 @@ typedef struct {
   uint32_t *status;
 } kvx_evict8_args;
 
+/* A fixed, small size: selection and move work in registers and shared memory,
+ * and the workspace is there so that a later need for one changes no caller.  0
+ * for sizes that kvx_evict8 refuses. */
 size_t kvx_evict8_workspace_bytes(const kvx_evict8_args *args);
 
 /* Eviction by accumulated attention weight.  For each request and KV head keep
@@ -753,7 +760,8 @@ size_t kvx_evict8_workspace_bytes(const kvx_evict8_args *args);
  * (keys are stored rotated, which attention needs and no more).  A length
  * outside [0, max_len] counts as 0 (KVX_FLAG_BAD_LENGTH); tokens of a source
  * block id outside the pool are stored as zeros, those of a destination block
- * id outside it dropped (KVX_FLAG_BAD_BLOCK). */
+ * id outside it dropped (KVX_FLAG_BAD_BLOCK).  One or two launches.  max_len is
+ * at most 2^31 - 1025. */
 kvx_status kvx_evict8(const kvx_evict8_args *args, void *stream);
 
 #ifdef __cplusplus
