@@ -8,8 +8,8 @@
 // cluster of CTAs works on one request and head, each on its slots, with their
 // histograms added up through distributed shared memory: a chain of short steps,
 // bound by their latency (16 requests of up to 16,384 slots, 8 heads: 21 us, of
-// which the weights' bytes would be 0.7).  One CTA for each made that 28, and
-// 131,072 slots of one request 236 us in all where eight take 72.
+// which the weights' bytes would be 0.7).  With one CTA for each the call takes 76 us
+// instead of 72, and one request of 131,072 slots, 32,768 kept, 228 instead of 63.
 //
 // Move.  A block's tokens are read as code * scale, and the block gets the
 // smallest power of two as scale that its tokens allow.  Bound by HBM: every
@@ -454,9 +454,10 @@ extern "C" kvx_status kvx_evict8(const kvx_evict8_args *a, void *stream) {
   p.recent = a->recent;
   const int64_t most = a->keep < a->max_len ? a->keep : a->max_len;
   const int64_t blocks = (most + c.block_size - 1) / c.block_size, rows = (int64_t)c.heads * a->num_requests;
-  // One launch where no warp would move more than a block: 17.5 us for 512 of 2048
-  // slots and 8 heads where two launches take 21; with 4096 slots kept of 16,384
-  // one takes 35 us and two 32, for four requests 45 and 38.
+  // One launch where no warp would move more than a block: 18.4 us for 512 of 2048
+  // slots and 8 heads where two launches take 19.1, and a launch less of the host's
+  // time; with 4096 slots kept of 16,384 one takes 30.7 us and two 27.5, for four
+  // requests 56 and 36.
   const bool few = rows <= 152 / kMaxCtas && blocks <= kMaxCtas * kWarps;
   // CTAs of a request and head: one for 4096 slots, while all fit the GPU at once;
   // where the selection moves the slots too, one for as many blocks as it has warps
