@@ -773,6 +773,7 @@ __device__ __forceinline__ void note_split(const TcParams &p, const Share &s) {
 // noted, block y after a slice of its rows.
 template <class G>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcParams p) {
+  let_next_kernel_start();
   wait_for_kernel_before();
   const Split x = p.splits[blockIdx.x + 1];
   if (x.ctas == 0) return;
@@ -787,6 +788,7 @@ template <class G>
 __global__ void __launch_bounds__(256) join_row_kernel(const __grid_constant__ TcParams p) {
   __shared__ float top[8], sum[8];
   __shared__ float4 part_sum[8][32];
+  let_next_kernel_start();
   wait_for_kernel_before();
   const Split x = p.splits[blockIdx.x + 1];
   const int row = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32, parts = x.ctas * G::PARTS;
@@ -1274,11 +1276,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_constant__ TcParams p) {
   const AttendParams &a = p.a;
   extern __shared__ float lse2[];
-  if (!requests_ok(a)) return;
+  const bool good = requests_ok(a);
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
   const int64_t beg = a.req.begin(r);
   const int rows = (int)(a.req.begin(r + 1) - beg) * a.G;
   wait_for_kernel_before();
+  if (!good) return;
   for (int c = threadIdx.x; c < rows; c += 256)
     lse2[c] = a.lse[(beg + c / a.G) * a.Hq + h * a.G + c % a.G] * kLog2e;
   __syncthreads();
@@ -1882,6 +1885,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   // rows that see the CTA's first slot: from the first query whose limit reaches it
   const int row0 = max(0, t0 * kTile - (len - fresh)) * a.G / (2 * kTile) * (2 * kTile);
   const int chunks = t0 < t1 && row0 < rows ? (rows - row0 + 2 * kTile - 1) / (2 * kTile) : 0, tiles = t1 - t0;
+  if (chunks == 0) wait_for_kernel_before();   // every CTA does, so that this kernel ends after that one
 
   if (warp < 8) {
     const int i = warp / 4;

@@ -18,15 +18,6 @@ struct Requests {
   int R;
   int64_t ntok;
   __device__ int64_t begin(int r) const { return cu ? (int64_t)cu[r] : r; }
-  __device__ int of(int64_t g) const {
-    if (!cu) return (int)g;
-    int lo = 0, hi = R - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)cu[mid] <= g) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-  }
   // Starts at 0, never decreases, ends at ntok; every thread of the CTA calls it.
   __device__ bool ok() const {
     bool good = true;
@@ -80,6 +71,8 @@ inline bool aligned_to(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)
 // The kernel is launched while the one before on its stream still runs: what that
 // one writes may be read after this.
 __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel may start once all CTAs have come here; it calls the above.
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Host checks of a cache.
 inline kvx_status check_cache8(const kvx_cache8 &c) {
