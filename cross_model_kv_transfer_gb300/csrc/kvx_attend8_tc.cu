@@ -1830,15 +1830,18 @@ __global__ void __launch_bounds__(kColThreads, 1)
 // weights[r][h][j] += sum over the rows that see slot j of exp2(score - lse).
 // The scores are formed again, transposed (S^T = K Q^T, slots in the lanes), so
 // that a slot's sum stays in one thread: no atomics, one order of summation.  A CTA
-// takes `per` slot tiles of one request and head, its rows 256 at a time; two groups
-// of four warps take turns with the tiles.
-constexpr int kWtStages = 4, kWtThreads = 10 * 32;
+// takes up to `per` slot tiles of one request and head, spread over its length because
+// fewer rows see the late ones, and the rows 256 at a time; two groups of four warps
+// take turns with the tiles.  Bound by the exponentials' chain and, where a CTA has
+// few tiles, by laying out the rows: 26 us for 244 rows and two requests of 8192.
+constexpr int kWtStages = 4, kWtThreads = 10 * 32, kWtTiles = 16;   // tiles: of a CTA at most
 struct WtShared {
   uint64_t k_full[kWtStages], k_empty[kWtStages], q_full, spent, s_full[2], s_empty[2], drain;
   uint32_t tmem_base;
   volatile int abort;
   uint32_t mask[kWtStages];
   float ks[kWtStages][kTile / 4];
+  float sum[kWtTiles][kTile];
   __align__(16) float4 rows[kTile];   // of row pairs: two factors, two log-sum-exps (base 2, negative)
 };
 constexpr size_t kWtSmem = 1024 + kSmemQ + kWtStages * (size_t)kTileBytes + sizeof(WtShared);
@@ -1852,7 +1855,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   const AttendParams &a = p.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
-  const int t0 = blockIdx.x * per, t1 = min(t0 + per, (len + kTile - 1) / kTile);   // tiles
+  // the CTA's tiles, at most `per`: t0, t0 + step, ...
+  const int all = (len + kTile - 1) / kTile, step = (all + per - 1) / per, t0 = blockIdx.x;
+  const int tiles = t0 < step ? (all - t0 - 1) / step + 1 : 0;
+  const auto tile_at = [&](int t) { return t0 + t * step; };
+  for (int x = tid; x < kWtTiles * kTile; x += kWtThreads) (&sh->sum[0][0])[x] = 0.f;
   if (tid == 0) {
     for (int i = 0; i < kWtStages; ++i) {
       mbar_init(smem_addr(&sh->k_full[i]), 32);
@@ -1884,13 +1891,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   const int fresh = good ? (int)(a.req.begin(r + 1) - beg) : 0, rows = fresh * a.G;
   // rows that see the CTA's first slot: from the first query whose limit reaches it
   const int row0 = max(0, t0 * kTile - (len - fresh)) * a.G / (2 * kTile) * (2 * kTile);
-  const int chunks = t0 < t1 && row0 < rows ? (rows - row0 + 2 * kTile - 1) / (2 * kTile) : 0, tiles = t1 - t0;
+  const int chunks = tiles > 0 && row0 < rows ? (rows - row0 + 2 * kTile - 1) / (2 * kTile) : 0;
+  // how many of the tiles the chunk's last row sees: all of them in the last chunk
+  const auto seen = [&](int c) {
+    const int limit = len - fresh + (min(row0 + (c + 1) * 2 * kTile, rows) - 1) / a.G, t = limit / kTile - t0;
+    return limit < 0 || t < 0 ? 0 : min(tiles, t / step + 1);
+  };
   if (chunks == 0) wait_for_kernel_before();   // every CTA does, so that this kernel ends after that one
 
   if (warp < 8) {
     const int i = warp / 4;
     const uint32_t s_col = tmem + ((uint32_t)(warp % 4 * 32) << 16) + i * 2 * kTile;
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0, n = 0; c < chunks; ++c) {
       // queries: a row a thread, once all warps are through with the rows before
       if (c > 0 && !W.warp_wait(&sh->spent, (c - 1) & 1)) goto done;
       const int row = row0 + c * 2 * kTile + tid;
@@ -1908,10 +1920,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh->q_full));
       if (!W.warp_wait(&sh->q_full, c & 1)) goto done;   // the other rows' constants
-      for (int t = 0; t < tiles; ++t) {
-        const int n = c * tiles + t;
+      const int count = seen(c);
+      for (int t = 0; t < count; ++t, ++n) {
         if ((n & 1) != i) continue;
-        const int ks = n % kWtStages, j = (t0 + t) * kTile + warp % 4 * 32 + lane;
+        const int ks = n % kWtStages, j = tile_at(t) * kTile + warp % 4 * 32 + lane;
         if (!W.warp_wait(&sh->k_full[ks], n / kWtStages & 1)) goto done;
         if (!W.warp_wait(&sh->s_full[i], n >> 1 & 1)) goto done;
         tc_fence_after();
@@ -1949,7 +1961,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         float u0, u1;
         unpair(sum, u0, u1);
-        if (there) a.weights[((int64_t)r * a.H + h) * a.wstride + j] += u0 + u1;
+        // a slot's sum passes from group to group with the chunks
+        float *total = &sh->sum[t][in];
+        if (c + 1 < chunks) *total += u0 + u1;
+        else if (there) a.weights[((int64_t)r * a.H + h) * a.wstride + j] += *total + (u0 + u1);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh->spent));
@@ -1957,9 +1972,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   done:;
   } else if (warp == 8) {
     int n = 0;
-    for (int c = 0; c < chunks; ++c)
-      for (int t = 0; t < tiles; ++t, ++n) {
-        const int ks = n % kWtStages, j = (t0 + t) * kTile + 4 * lane;
+    for (int c = 0; c < chunks; ++c) {
+      const int count = seen(c);
+      for (int t = 0; t < count; ++t, ++n) {
+        const int ks = n % kWtStages, j = tile_at(t) * kTile + 4 * lane;
         int page = -1;
         uint32_t off = 0;
         if (j < len) {
@@ -1986,6 +2002,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           tma_load_2d(smem_addr(kbuf + ks * kTileBytes + lane * p.box * kD), &map_k, 0, from, smem_addr(&sh->k_full[ks]));
         if (lane != 0) mbar_arrive(smem_addr(&sh->k_full[ks]));
       }
+    }
   ld_done:
     __syncwarp();
     if (lane == 0)
@@ -1996,7 +2013,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     int n = 0;
     for (int c = 0; ok && c < chunks; ++c) {
       ok = W.warp_wait(&sh->q_full, c & 1);
-      for (int t = 0; ok && t < tiles; ++t, ++n) {
+      const int count = seen(c);
+      for (int t = 0; ok && t < count; ++t, ++n) {
         const int ks = n % kWtStages, i = n & 1;
         ok = W.warp_wait(&sh->k_full[ks], n / kWtStages & 1) && W.warp_wait(&sh->s_empty[i], (n >> 1 & 1) ^ 1);
         if (!ok) break;
@@ -2160,10 +2178,10 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
                           : launch<Columns<16>>(columns_kernel<16>, kColThreads, kColSmem, p, mk, mv, s);
   if (st != KVX_OK || !a.weights || a.max_len == 0) return st;
   if (!sh.spool) {
-    // as few slot tiles a CTA as lets all run at once, 16 at most
+    // as few slot tiles a CTA as lets all run at once, within what it has room for
     const int tiles = (args->max_len + kTile - 1) / kTile, items = a.H * a.req.R;
     int per = 1;
-    while (per < 16 && (int64_t)items * ((tiles + per - 1) / per) > 152) ++per;
+    while (per < kWtTiles && (int64_t)items * ((tiles + per - 1) / per) > 152) ++per;
     if (cudaFuncSetAttribute(weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWtSmem) != cudaSuccess)
       return KVX_ERR_CUDA;
     return launch_after(weights_tc_kernel, dim3((tiles + per - 1) / per, a.H, a.req.R), kWtThreads, kWtSmem, s, p, mk, per);
