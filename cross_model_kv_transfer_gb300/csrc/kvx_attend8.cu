@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
             oo.y += f * y.y;
           }
           if (whole) {
-            if (at < cols && d < a.d) store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, ll);
+            if (at < cols && d < a.d) store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, 0.f, ll);
           } else {
             *reinterpret_cast<float2 *>(slot + col * DP + d) = oo;
             if (d == 0) {
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
               oo.x += y.x * f;
               oo.y += y.y * f;
             }
-            store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, ll);
+            store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, 0.f, ll);
           }
         }
       }

@@ -63,9 +63,10 @@ __device__ __forceinline__ bool requests_ok(const AttendParams &p) {
   }
   return good;
 }
-// Two dimensions of a finished row; its log-sum-exp with the first.
+// Two dimensions of a finished row, whose sums o and l are relative to exp2(m + shift);
+// its log-sum-exp with the first.
 __device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int hq, int d, float2 o, float m,
-                                          float l) {
+                                          float shift, float l) {
   const float inv = l != 0.f ? 1.f / l : 0.f;
   const int64_t to = g * p.ot + hq * p.oh + d;
   if (p.bf16) {
@@ -77,7 +78,7 @@ __device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int 
     out[0] = o.x * inv;
     out[1] = o.y * inv;
   }
-  if (d == 0) p.lse[g * p.Hq + hq] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (d == 0) p.lse[g * p.Hq + hq] = l != 0.f ? (m + (shift + log2f(l))) * kLn2 : -INFINITY;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -113,7 +113,7 @@ struct TcParams {
   AttendParams a;
   int grid;            // CTAs that share the work
   Split *splits;       // [grid]
-  float *partial;      // [2 * grid][PARTS][part_size]: sums [rows][kD], maxima, totals
+  float *partial;      // [2 * grid][PARTS][part_size]: sums [rows][kD], maxima, their shifts, totals
   float *scores;       // base 2, or NULL; narrow: [R][H][rows][score_ld], columns: [R][H][score_ld][slot_rows]
   int score_ld, slot_rows, part_size;   // rows kept of a part (narrow: G * max_new), its floats
   int box;             // slots of one TMA box
@@ -515,12 +515,60 @@ __device__ __forceinline__ uint64_t probabilities(uint32_t *out, const uint32_t 
   top = fmaxf(t0, t1);
   return sum;
 }
+// Beyond this (base 2) the maximum's own half ulp counts in an exponent.
+constexpr float kFar = 65536.f;
+// 32 of a row's scores from tensor memory, each rounded once to fp32.
+__device__ __forceinline__ void rounded_scores(uint32_t (&s)[32], uint32_t col, const float4 *scale, uint32_t mask, int seen, float cs) {
+  float f[8];
+  tc_ld32(col, s);
+  tc_wait_ld32(s);
+  columns<true>(s, f, scale, mask, seen);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__fmul_rn(__uint_as_float(s[e]), fmaxf(f[e / 4] * cs, 0x1p-126f)));
+}
+// The largest of the 64 scores of a half tile.
+__device__ __noinline__ float largest_score(uint32_t col, const float4 *scale, uint32_t mask, int seen, float cs) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t s[32];
+    rounded_scores(s, col + 32 * c, scale + 2 * c, mask >> (8 * c), seen - 32 * c, cs);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(s[e]));
+  }
+  return top;
+}
+// The probabilities exp2((score - m) + add) of a half tile over the scores they come
+// from; returns their sum.
+__device__ __noinline__ float far_probabilities(uint32_t col, const float4 *scale, uint32_t mask, int seen, float cs, float m,
+                                                float add) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t s[32], out[16];
+    rounded_scores(s, col + 32 * c, scale + 2 * c, mask >> (8 * c), seen - 32 * c, cs);
+    float part = 0.f;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float y0 = ex2((__uint_as_float(s[e]) - m) + add), y1 = ex2((__uint_as_float(s[e + 1]) - m) + add);
+      part += y0 + y1;
+      out[e / 2] = f16x2(y0, y1);
+    }
+    tc_st16(col + 16 * c, out);     // where scores were read already
+    sum += part;
+  }
+  tc_wait_st();
+  return sum;
+}
 // A half tile of a row: probabilities over the scores they come from, the row's
-// running maximum (lazily) and sum.  `raise(down)` is called by whole warps when
-// a maximum has to rise: it scales down what the rows have so far.
+// running maximum (lazily) and sum.  What is subtracted from a score plus its tile's
+// value scale is m + shift: a score as it was rounded, and the value scale's exponent
+// of its tile.  They are kept apart because their sum would be rounded: from 2^25 on by
+// more than f16 has room for.  `raise(down)` is called by whole warps when a maximum
+// has to rise: it scales down what the rows have so far.
 template <bool MASK, class F>
 __device__ __forceinline__ bool softmax_half(uint32_t col, const float4 *scale, uint32_t mask, int seen, float cs, float ref,
-                                             float &m, float &l, F raise) {
+                                             float &m, float &shift, float &l, F raise) {
   uint32_t a[32], b[32], out[32];
   float fa[8], fb[8];
   tc_ld32(col, a);
@@ -529,27 +577,36 @@ __device__ __forceinline__ bool softmax_half(uint32_t col, const float4 *scale, 
   tc_wait_ld32(b);
   columns<MASK>(a, fa, scale, mask, seen);
   columns<MASK>(b, fb, scale + 2, mask >> 8, seen - 32);
+  const float add = kBias + (ref - shift) - finite_or_0(m);
+  const uint64_t a2 = pair(add, add);
+  float top = -INFINITY;
+  uint64_t sum = probabilities<MASK>(out, a, fa, cs, a2, pair(0.f, 0.f), top);
+  sum = probabilities<MASK>(out + 16, b, fb, cs, a2, sum, top);
+  // -inf where nothing is seen
+  const bool over = top > kBias + kSlack || (m == -INFINITY && top > -INFINITY) || fabsf(add) > kFar;
   float s0, s1;
-#pragma unroll 1
-  while (true) {
-    const float add = kBias + ref - finite_or_0(m);
-    const uint64_t a2 = pair(add, add);
-    float top = -INFINITY;
-    uint64_t sum = probabilities<MASK>(out, a, fa, cs, a2, pair(0.f, 0.f), top);
-    sum = probabilities<MASK>(out + 16, b, fb, cs, a2, sum, top);
-    // -inf where nothing is seen
-    const bool over = top > kBias + kSlack || (m == -INFINITY && top > -INFINITY);
-    unpair(sum, s0, s1);
-    if (!__any_sync(~0u, over)) break;
-    // seldom: the probabilities again, with the rows' maxima raised
-    const float mm = fmaxf(m, top - kBias + finite_or_0(m)), down = ex2(m - finite_or_0(mm));
-    if (!raise(down)) return false;
-    m = mm;
-    l *= down;
+  unpair(sum, s0, s1);
+  if (!__any_sync(~0u, over)) {
+    l += (s0 + s1) * ex2(-ref);    // without the value scale
+    tc_st32(col, out);
+    tc_wait_st();
+    return true;
   }
-  l += (s0 + s1) * ex2(-ref);    // without the value scale
-  tc_st32(col, out);
-  tc_wait_st();
+  // seldom: the probabilities again, from scores rounded before the maximum, which is one
+  // of them, is subtracted.  That is exact for all scores near it, so none is above kBias
+  // now however large they are.
+  const uint32_t in = MASK ? mask : 0xffffu;
+  const int last = MASK ? seen : kTile;
+  const float most = largest_score(col, scale, in, last, cs);
+  const float by = (most - finite_or_0(m)) + (ref - shift);
+  const bool rises = m == -INFINITY ? most > -INFINITY : by > 0.f;
+  const float down = m == -INFINITY ? 0.f : rises ? ex2(-by) : 1.f;
+  if (!raise(down)) return false;
+  if (rises) {
+    m = most;
+    shift = ref;
+  }
+  l = l * down + far_probabilities(col, scale, in, last, cs, finite_or_0(m), kBias + (ref - shift)) * ex2(-ref);
   return true;
 }
 // The factor of a lane's row, from its largest element.
@@ -673,6 +730,8 @@ __device__ __noinline__ void keep_scores(uint32_t col, float *to, const float4 *
   }
 }
 
+// A part's sums are relative to exp2(m + shift) of its row: is a + sa above b + sb?
+__device__ __forceinline__ bool above(float a, float sa, float b, float sb) { return (a - b) + (sa - sb) > 0.f; }
 // Join the parts of an item that CTAs c0 .. c0 + ctas - 1 left: rows first, first +
 // stride, ... of the warp.  A CTA keeps parts of an item that others began, and of
 // one that it began.  The parts' maxima and totals by the lanes, 32 parts at a time,
@@ -686,36 +745,48 @@ __device__ __noinline__ void join_rows(const TcParams &p, const TcWalk &w, int c
     return p.partial + ((cta * 2 + (c < G::PARTS)) * G::PARTS + c % G::PARTS) * (int64_t)p.part_size;
   };
   for (int r0 = first; r0 < rows; r0 += stride * B) {
-    float mm[B], ll[B], f[B];
+    float mm[B], sh[B], ll[B], f[B];
     float4 oo[B];
     int rr[B];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
       rr[k] = min(r0 + k * stride, rows - 1);   // a row beyond is formed twice
       mm[k] = -INFINITY;
+      sh[k] = 0.f;
       ll[k] = 0.f;
       oo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int at = 0; at < parts; at += 32) {
       const float *own = part_at(min(at + lane, parts - 1)) + p.slot_rows * kD;
-      float pm[B], pl[B];
+      float pm[B], ps[B], pl[B];
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         pm[k] = __ldcg(own + rr[k]);
-        pl[k] = __ldcg(own + p.slot_rows + rr[k]);
+        ps[k] = __ldcg(own + p.slot_rows + rr[k]);
+        pl[k] = __ldcg(own + 2 * p.slot_rows + rr[k]);
       }
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         if (at + lane >= parts) {
           pm[k] = -INFINITY;
+          ps[k] = 0.f;
           pl[k] = 0.f;
         }
-        float top = fmaxf(mm[k], pm[k]);
+        const bool own_above = above(pm[k], ps[k], mm[k], sh[k]);
+        float top = own_above ? pm[k] : mm[k], shift = own_above ? ps[k] : sh[k];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        const float down = ex2(mm[k] - finite_or_0(top));
-        f[k] = ex2(pm[k] - finite_or_0(top));
+        for (int o = 16; o; o >>= 1) {
+          const float y = __shfl_xor_sync(~0u, top, o), z = __shfl_xor_sync(~0u, shift, o);
+          const bool other = above(y, z, top, shift);
+          top = other ? y : top;
+          shift = other ? z : shift;
+        }
+        top = __shfl_sync(~0u, top, 0);       // equal sums of unequal terms
+        shift = __shfl_sync(~0u, shift, 0);
+        const float down = ex2((mm[k] - finite_or_0(top)) + (sh[k] - shift));
+        f[k] = ex2((pm[k] - finite_or_0(top)) + (ps[k] - shift));
         mm[k] = top;
+        sh[k] = shift;
         float sum = pl[k] * f[k];
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -744,8 +815,8 @@ __device__ __noinline__ void join_rows(const TcParams &p, const TcWalk &w, int c
       const int64_t row = (int64_t)w.group * G::ROWS + rr[k], tok = w.beg + row / a.G;
       const int hq = w.h * a.G + (int)(row % a.G);
       if (lane * 4 >= a.d) continue;
-      store_out(a, tok, hq, lane * 4, make_float2(oo[k].x, oo[k].y), mm[k], ll[k]);
-      store_out(a, tok, hq, lane * 4 + 2, make_float2(oo[k].z, oo[k].w), mm[k], ll[k]);
+      store_out(a, tok, hq, lane * 4, make_float2(oo[k].x, oo[k].y), mm[k], sh[k], ll[k]);
+      store_out(a, tok, hq, lane * 4 + 2, make_float2(oo[k].z, oo[k].w), mm[k], sh[k], ll[k]);
     }
   }
 }
@@ -786,41 +857,51 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcPar
 // The same with a block for a row, whose warps share the parts: few rows, many parts.
 template <class G>
 __global__ void __launch_bounds__(256) join_row_kernel(const __grid_constant__ TcParams p) {
-  __shared__ float top[8], sum[8];
+  __shared__ float top[8], shift[8], sum[8];
   __shared__ float4 part_sum[8][32];
   let_next_kernel_start();
   wait_for_kernel_before();
   const Split x = p.splits[blockIdx.x + 1];
   const int row = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32, parts = x.ctas * G::PARTS;
   if (row >= x.rows || parts == 0) return;
-  float mm = -INFINITY, ll = 0.f;
+  float mm = -INFINITY, sh = 0.f, ll = 0.f;
   float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 5
   for (int c = warp; c < parts; c += 8) {
     const int64_t cta = x.c0 + c / G::PARTS;
     const float *part = p.partial + ((cta * 2 + (c < G::PARTS)) * G::PARTS + c % G::PARTS) * (int64_t)p.part_size;
-    const float pm = __ldcg(part + p.slot_rows * kD + row), pl = __ldcg(part + p.slot_rows * (kD + 1) + row);
+    const float pm = __ldcg(part + p.slot_rows * kD + row), ps = __ldcg(part + p.slot_rows * (kD + 1) + row),
+                pl = __ldcg(part + p.slot_rows * (kD + 2) + row);
     const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + row * kD) + lane);
-    const float now = fmaxf(mm, pm), f0 = ex2(mm - finite_or_0(now)), f1 = ex2(pm - finite_or_0(now));
-    mm = now;
+    const bool own = above(pm, ps, mm, sh);
+    const float now = finite_or_0(own ? pm : mm), by = own ? ps : sh;
+    const float f0 = ex2((mm - now) + (sh - by)), f1 = ex2((pm - now) + (ps - by));
+    mm = own ? pm : mm;
+    sh = by;
     ll = ll * f0 + pl * f1;
     oo = make_float4(oo.x * f0 + y.x * f1, oo.y * f0 + y.y * f1, oo.z * f0 + y.z * f1, oo.w * f0 + y.w * f1);
   }
   part_sum[warp][lane] = oo;
   if (lane == 0) {
     top[warp] = mm;
+    shift[warp] = sh;
     sum[warp] = ll;
   }
   __syncthreads();
   if (warp > 0) return;
   mm = -INFINITY;
+  sh = 0.f;
   ll = 0.f;
   oo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) mm = fmaxf(mm, top[k]);
+  for (int k = 0; k < 8; ++k) {
+    const bool own = above(top[k], shift[k], mm, sh);
+    mm = own ? top[k] : mm;
+    sh = own ? shift[k] : sh;
+  }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float f = ex2(top[k] - finite_or_0(mm));
+    const float f = ex2((top[k] - finite_or_0(mm)) + (shift[k] - sh));
     const float4 y = part_sum[k][lane];
     ll += sum[k] * f;
     oo = make_float4(oo.x + y.x * f, oo.y + y.y * f, oo.z + y.z * f, oo.w + y.w * f);
@@ -829,8 +910,8 @@ __global__ void __launch_bounds__(256) join_row_kernel(const __grid_constant__ T
   const int64_t at = (int64_t)x.group * G::ROWS + row, tok = x.beg + at / a.G;
   const int hq = x.h * a.G + (int)(at % a.G);
   if (lane * 4 >= a.d) return;
-  store_out(a, tok, hq, lane * 4, make_float2(oo.x, oo.y), mm, ll);
-  store_out(a, tok, hq, lane * 4 + 2, make_float2(oo.z, oo.w), mm, ll);
+  store_out(a, tok, hq, lane * 4, make_float2(oo.x, oo.y), mm, sh, ll);
+  store_out(a, tok, hq, lane * 4 + 2, make_float2(oo.z, oo.w), mm, sh, ll);
 }
 
 // What a softmax group knows of its item when the item, or the CTA's part of it, ends.
@@ -838,11 +919,11 @@ struct Item {
   TcWalk w;
   int count, rows, row;
   bool live, warp_live;
-  float m, l;
+  float m, shift, l;
   uint32_t o_col, half, joins;   // half tiles and joins of this group so far
 };
-// Write the result of the item, or leave this CTA's part of it and let the last to
-// come join the parts.  Seldom, and apart from the loop so that it costs that no
+// Write the result of the item, or leave this CTA's part of it for the kernel that
+// joins.  Seldom, and apart from the loop so that it costs that no
 // registers.
 template <bool WIDE>
 __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const Item it, int i) {
@@ -854,7 +935,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int rows = it.rows, row = it.row;
   const bool live = it.live, warp_live = it.warp_live, whole = it.count == w.steps;
-  const float m = it.m, l = it.l;
+  const float m = it.m, shift = it.shift - kBias, l = it.l;   // what the sums are relative to
   const uint32_t o_col = it.o_col;
   // the result of the item, or this CTA's part of it
   if (!W.warp_wait(&sh->pv_done[i][(half - 1) & 1], (half - 1) >> 1 & 1)) return false;
@@ -937,12 +1018,12 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
       }
     }
     if (live) {
-      const float mt = m - kBias;           // what the sums are relative to
       if (direct) {
-        a.lse[tok * a.Hq + hq] = l != 0.f ? (mt + log2f(l)) * kLn2 : -INFINITY;
+        a.lse[tok * a.Hq + hq] = l != 0.f ? (m + (shift + log2f(l))) * kLn2 : -INFINITY;
       } else {
-        slot[p.slot_rows * kD + row] = mt;
-        slot[p.slot_rows * (kD + 1) + row] = l;
+        slot[p.slot_rows * kD + row] = m;
+        slot[p.slot_rows * (kD + 1) + row] = shift;
+        slot[p.slot_rows * (kD + 2) + row] = l;
       }
     }
   }
@@ -1047,7 +1128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int floor_limit = (int)(w.len - w.fresh + (at - lane) / a.G);   // the lowest of the warp's live rows
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
                                  (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
-      float m = -INFINITY, l = 0.f, cs;
+      float m = -INFINITY, shift = 0.f, l = 0.f, cs;
       if (WIDE || i == 0) {
         cs = put_queries<WIDE ? 8 : 4>(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes, 32);
         fence_async_proxy();
@@ -1081,8 +1162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             scale_down(o_col, down);
             return true;
           };
-          if (!(masked ? softmax_half<true>(col, scale, mask, limit - j0, cs, ref, m, l, raise)
-                       : softmax_half<false>(col, scale, 0u, 0, cs, ref, m, l, raise)))
+          if (!(masked ? softmax_half<true>(col, scale, mask, limit - j0, cs, ref, m, shift, l, raise)
+                       : softmax_half<false>(col, scale, 0u, 0, cs, ref, m, shift, l, raise)))
             goto done;
         }
         tc_fence_before();
@@ -1100,7 +1181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // the result of the item, or this CTA's part of it
-      const Item it{w, count, rows, row, live, warp_live, m, cs != cs ? cs : l, o_col, half, joins};
+      const Item it{w, count, rows, row, live, warp_live, m, shift, cs != cs ? cs : l, o_col, half, joins};
       if (!finish_item<WIDE>(p, sh, it, i)) goto done;
       joins += !WIDE && count == w.steps;
     }
@@ -1678,8 +1759,9 @@ __global__ void __launch_bounds__(kColThreads, 1)
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum += sh->warp_sum[i][k][lane];
-        slot[p.slot_rows * kD + lane] = mine - kColBias;
-        slot[p.slot_rows * (kD + 1) + lane] = sum;
+        slot[p.slot_rows * kD + lane] = mine;
+        slot[p.slot_rows * (kD + 1) + lane] = -kColBias;
+        slot[p.slot_rows * (kD + 2) + lane] = sum;
       }
       if (count == w.steps) {
         // an item of this CTA alone: its two parts
@@ -2103,7 +2185,7 @@ TcShape tc_shape(const kvx_attend8_args *a) {
   s.columns = most <= 16;
   s.wide = most > 64;
   s.slot_rows = s.wide ? Wide::ROWS : s.columns ? (most <= 8 ? 8 : 16) : (int)most;
-  s.part_size = (s.slot_rows * (kD + 2) + 3) / 4 * 4;
+  s.part_size = (s.slot_rows * (kD + 3) + 3) / 4 * 4;
   s.grid = 152;                        // one CTA an SM
   s.score_ld = (a->max_len + 255) / 256 * 256;
   s.box = a->cache.block_size & -a->cache.block_size;
