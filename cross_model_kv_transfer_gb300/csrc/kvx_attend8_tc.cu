@@ -40,8 +40,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cfloat>
 #include <type_traits>
-
 
 #include "kvx_attend8.cuh"
 #include "kvx_ptx.cuh"
@@ -1390,7 +1390,9 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
 // A slot's probabilities carry its block's value scale (as a power in the
 // exponent), so that O needs none; sums without it are kept beside.  Four warps
 // share a maximum for each column: they vote on a tile, and only where one of them
-// exceeds it by 2^4 do they agree on a new one and scale O down.
+// exceeds it by 2^4 do they agree on a new one and scale O down.  The maximum is of score
+// plus value scale; once one is beyond kFar, where that sum's rounding would count, an
+// item takes the largest score and the largest value scale apart.
 // Two groups of four warps take the even and the odd slot tiles.
 // Bound by HBM and what surrounds it: one query of 64 heads over 131,071 slots of 8
 // heads 56 us, 4.8 TB/s (a copy 6.7); 16 requests of 1024 to 16,384 slots 72 us.  The
@@ -1415,6 +1417,7 @@ struct ColShared {
   float ks[kScales][kTile / 4], vs[kScales][kTile / 4];
   float cs[2][16];             // of the item (in turn) and column
   float warp_max[2][4][16], warp_sum[2][4][16];
+  float far_max[2][4][17];     // scores by column, then value scales
 };
 constexpr size_t kColSmem = 1024 + (kCkStages + kCvStages) * (size_t)kTileBytes + 4 * kColQBytes + 2 * 2 * 3 * kColPBytes +
                             sizeof(ColShared);
@@ -1609,12 +1612,13 @@ __global__ void __launch_bounds__(kColThreads, 1)
           bring(ahead, items + 1);
         }
       }
-      float cs[NC], m[NC], l[NC];
+      float cs[NC], m[NC], l[NC], shift = 0.f;   // sums are relative to exp2(m + shift - kColBias)
+      bool far = false;
       if (!W.warp_wait(&sh->q_full[items & 1], items >> 1 & 1)) goto done;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         cs[c] = sh->cs[items & 1][c];
-        m[c] = -INFINITY;
+        m[c] = -FLT_MAX;     // nothing seen: any score is over it
         l[c] = 0.f;
       }
       const int low = (int)(w.len - w.fresh + row0 / a.G);   // last slot that the first column sees
@@ -1645,11 +1649,14 @@ __global__ void __launch_bounds__(kColThreads, 1)
           for (int c = 0; c < NC; c += 4)
             *reinterpret_cast<float4 *>(spool + (int64_t)j * NC + c) = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
         }
+        // exponents of the probabilities times the value scale: score less maximum, which
+        // are near each other where it counts, comes first
+        float e[NC];
         bool over = false;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          y[c] += lv;
-          over = over || y[c] > m[c] + kColSlack;
+          e[c] = (y[c] - m[c]) + (lv - shift + kColBias);
+          over = over || e[c] > kColBias + kColSlack;
         }
         if (__any_sync(~0u, over) && lane == 0) sh->over[i][b] = t + 1;
         __syncwarp();
@@ -1659,7 +1666,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
           // seldom: a new maximum for all columns, and O scaled down to it
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            float top = y[c];
+            float top = y[c] + lv;
 #pragma unroll
             for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
             if (lane == 0) sh->warp_max[i][warp % 4][c] = top;
@@ -1667,15 +1674,49 @@ __global__ void __launch_bounds__(kColThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sh->agree[i]));
           if (!W.warp_wait(&sh->agree[i], agreed++ & 1)) goto done;
-          float down[NC];
+          float down[NC], by = 0.f;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            float top = m[c];
+            float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 4; ++k) top = fmaxf(top, sh->warp_max[i][k][c]);
-            down[c] = ex2(m[c] - finite_or_0(top));
+            far = far || (top > -INFINITY && fabsf(top) > kFar);
+            down[c] = fmaxf(m[c], top);      // the new maximum
+          }
+          if (far) {
+            // the same of scores alone, and the largest value scale
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              float top = y[c];
+#pragma unroll
+              for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+              if (lane == 0) sh->far_max[i][warp % 4][c] = top;
+            }
+            float top = lv;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+            if (lane == 0) sh->far_max[i][warp % 4][NC] = top;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh->agree[i]));
+            if (!W.warp_wait(&sh->agree[i], agreed++ & 1)) goto done;
+            by = -shift;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) shift = fmaxf(shift, sh->far_max[i][k][NC]);
+            by += shift;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              down[c] = m[c];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) down[c] = fmaxf(down[c], sh->far_max[i][k][c]);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float top = down[c];
+            down[c] = ex2((m[c] - top) - by);
             m[c] = top;
             l[c] *= down[c];
+            e[c] = (y[c] - top) + (lv - shift + kColBias);
           }
           if (s > 0) {
             if (!W.warp_wait(&sh->pv_done[i][(t - 1) & 1], (t - 1) >> 1 & 1)) goto done;
@@ -1693,7 +1734,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
         uint32_t h[NC / 2];
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {
-          const float e0 = ex2(y[c] + (kColBias - finite_or_0(m[c]))), e1 = ex2(y[c + 1] + (kColBias - finite_or_0(m[c + 1])));
+          const float e0 = ex2(e[c]), e1 = ex2(e[c + 1]);
           l[c] = fmaf(e0, without, l[c]);
           l[c + 1] = fmaf(e1, without, l[c + 1]);
           h[c / 2] = f16x2(e0, e1);
@@ -1753,14 +1794,14 @@ __global__ void __launch_bounds__(kColThreads, 1)
       if (lane == 0) mbar_arrive(smem_addr(&sh->agree[i]));
       if (!W.warp_wait(&sh->agree[i], agreed++ & 1)) goto done;
       if (warp % 4 == 0 && lane < rows) {
-        float mine = -INFINITY;
+        float mine = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) mine = lane == c ? m[c] : mine;
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum += sh->warp_sum[i][k][lane];
         slot[p.slot_rows * kD + lane] = mine;
-        slot[p.slot_rows * (kD + 1) + lane] = -kColBias;
+        slot[p.slot_rows * (kD + 1) + lane] = shift - kColBias;
         slot[p.slot_rows * (kD + 2) + lane] = sum;
       }
       if (count == w.steps) {

@@ -21,7 +21,7 @@ pytestmark = pytest.mark.gpu
 
 SIZES = [2.0 ** 17, 2.0 ** 24, 2.0 ** 27, 1e9, 2.0 ** 36, 1e20, 1e30]
 # few rows of each (request, KV head) to many: H, G, new
-NARROW, WIDE = (2, 4, 12), (2, 4, 70)
+FEW8, FEW16, NARROW, WIDE = (2, 8, 1), (2, 4, 4), (2, 4, 12), (2, 4, 70)
 
 
 def attend(c, lens, new, G, scale, weights=None):
@@ -73,7 +73,7 @@ def planted(H, G, new, d, bs, lens, dtype, size, seed):
 
 
 @pytest.mark.parametrize("size", SIZES)
-@pytest.mark.parametrize("H,G,new", [NARROW, WIDE])
+@pytest.mark.parametrize("H,G,new", [FEW8, FEW16, NARROW, WIDE])
 def test_huge_scores_beside_ordinary_ones(H, G, new, size):
     lens = [700, 150]
     c, big, scale = planted(H, G, new, 128, 16, lens, torch.bfloat16, size, 3)
@@ -107,7 +107,7 @@ def rising(H, G, new, n, dtype, size):
 
 
 @pytest.mark.parametrize("size", SIZES)
-@pytest.mark.parametrize("H,G,new", [NARROW, WIDE])
+@pytest.mark.parametrize("H,G,new", [FEW8, FEW16, NARROW, WIDE])
 def test_scores_that_rise_from_tile_to_tile(H, G, new, size):
     c, scale = rising(H, G, new, 900, torch.bfloat16, size)
     out, lse, want = attend(c, [900], new, G, scale)
@@ -135,7 +135,7 @@ def equal_keys(H, G, new, n, dtype, size):
 
 
 @pytest.mark.parametrize("size", SIZES)
-@pytest.mark.parametrize("H,G,new", [NARROW, WIDE])
+@pytest.mark.parametrize("H,G,new", [FEW8, FEW16, NARROW, WIDE])
 def test_equal_keys_share_the_weight(H, G, new, size):
     c, scale = equal_keys(H, G, new, 3000, torch.bfloat16, size)
     out, lse, want = attend(c, [3000], new, G, scale)
@@ -143,7 +143,7 @@ def test_equal_keys_share_the_weight(H, G, new, size):
     certain(out, lse, want, np.ones((new, H * G), dtype=bool), True)
 
 
-@pytest.mark.parametrize("H,G,new", [NARROW, WIDE])
+@pytest.mark.parametrize("H,G,new", [FEW8, FEW16, NARROW, WIDE])
 def test_rows_of_infinities_and_nan_end_and_stay_alone(H, G, new):
     lens = [300]
     c = make(H, G, 128, 16, lens, [new], torch.bfloat16, 17)
