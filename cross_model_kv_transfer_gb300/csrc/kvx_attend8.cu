@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               mx[n][e] = top[n][e];
-              const float mm = finite_or_0(top[n][e] * cs[n][e]), down = ex2(m[n][e] - mm);
+              const float mm = finite_or_0(__fmul_rn(top[n][e], cs[n][e])), down = ex2(m[n][e] - mm);
               m[n][e] = top[n][e] > -INFINITY ? mm : -INFINITY;
               l[n][e] *= down;
 #pragma unroll
@@ -526,8 +526,10 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
             const float f = vsc[i][half] * vinv;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const float p0 = ex2(fmaf(s[i][n][2 * half], cs[n][0], -finite_or_0(m[n][0])));
-              const float p1 = ex2(fmaf(s[i][n][2 * half + 1], cs[n][1], -finite_or_0(m[n][1])));
+              // a score is rounded before the maximum, which is a rounded score, is
+              // subtracted: none comes out above it, however large both are
+              const float p0 = ex2(__fmul_rn(s[i][n][2 * half], cs[n][0]) - finite_or_0(m[n][0]));
+              const float p1 = ex2(__fmul_rn(s[i][n][2 * half + 1], cs[n][1]) - finite_or_0(m[n][1]));
               l[n][0] += p0;
               l[n][1] += p1;
               float y0 = p0 * f, y1 = p1 * f;

@@ -143,6 +143,22 @@ def test_equal_keys_share_the_weight(H, G, new, size):
     certain(out, lse, want, np.ones((new, H * G), dtype=bool), True)
 
 
+# the form of fp32 queries, large head dims and odd blocks: few columns to many
+SPLIT = [(2, 4, 1, 128, 16, torch.float32), (2, 8, 2, 64, 16, torch.float32), (1, 4, 20, 128, 24, torch.float32),
+         (2, 2, 3, 256, 16, torch.bfloat16), (2, 2, 20, 256, 32, torch.float32), (1, 4, 9, 128, 7, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("H,G,new,d,bs,dtype", SPLIT)
+def test_huge_scores_in_the_split_form(H, G, new, d, bs, dtype, size):
+    lens = [1500, 150]
+    c, big, scale = planted(H, G, new, d, bs, lens, dtype, size, 3)
+    bf16 = dtype == torch.bfloat16
+    out, lse, want = attend(c, lens, new, G, scale)
+    certain(out, lse, want, big, bf16)
+    ordinary(out, lse, want, ~big, bf16, 1500)
+
+
 @pytest.mark.parametrize("H,G,new", [FEW8, FEW16, NARROW, WIDE])
 def test_rows_of_infinities_and_nan_end_and_stay_alone(H, G, new):
     lens = [300]
