@@ -81,6 +81,8 @@ struct SplitCfg {
   static constexpr bool kQInSmem = NT * PARTS > 2;
   static constexpr size_t kSmem = kRing + kReduce + (kQInSmem ? kQ : 0) + COLS * 4 + 64;
   static constexpr int kSlot = COLS * (DP + 2);                 // floats of a partial result
+  static constexpr size_t kAgainTile = kTile;                   // the weights' second pass: keys only
+  static constexpr size_t kAgainSmem = kAgainTile * WARPS + (kQInSmem ? kQ : 0) + COLS * 4;
 };
 
 struct SplitParams {
@@ -171,6 +173,150 @@ __device__ __forceinline__ uint32_t piece_at(int j, int c) {
   return (uint32_t)(j * DP + ((c ^ f) << 4));
 }
 
+// Query fragments of a group of columns: the thread's column is g, its dimensions
+// 64 q + 16 t ..; every thread of the CTA calls it where they lie in shared memory.
+template <class C>
+struct Queries {
+  static constexpr int QD = C::DP / 64;
+  uint32_t f[C::kQInSmem ? 1 : C::NT][C::PARTS][QD * 4][2];
+  float cs[C::NT][2];           // factors of columns 2t, 2t + 1
+  __device__ __forceinline__ void load(const SplitParams &p, int64_t beg, int h, int col0, int cols, uint2 *qs,
+                                       float *col_scale) {
+    constexpr int NT = C::NT, PARTS = C::PARTS;
+    const AttendParams &a = p.a;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    if (C::kQInSmem) __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (C::kQInSmem && n % C::WARPS != warp % (NT < C::WARPS ? NT : C::WARPS)) continue;
+      if (C::kQInSmem && warp >= NT) continue;
+      const int col = col0 + 8 * n + g;
+      float x[QD][16];
+      float top = 0.f;
+      const int64_t tok = beg + col / a.G;
+      const int hq = h * a.G + col % a.G;
+#pragma unroll
+      for (int q = 0; q < QD; ++q) {
+        const int d0 = 64 * q + 16 * t;
+        const bool in = col < cols && d0 < a.d;
+        const int64_t at = tok * a.qt + hq * a.qh + d0;
+        if (PARTS == 1) {
+          const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + at;
+          if (p.vec_q) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const uint4 y = in ? __ldg(reinterpret_cast<const uint4 *>(src) + v) : make_uint4(0, 0, 0, 0);
+              const uint32_t b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                x[q][8 * v + 2 * e] = __uint_as_float(b[e] << 16);
+                x[q][8 * v + 2 * e + 1] = __uint_as_float(b[e] & 0xffff0000u);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[q][e] = in ? __bfloat162float(src[e]) : 0.f;
+          }
+        } else {
+          const float *src = reinterpret_cast<const float *>(a.q) + at;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[q][e] = in ? __ldg(src + e) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[q][e]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      int e2 = (int)(__float_as_uint(top) >> 23) - 127;
+      e2 = e2 < -100 ? -100 : e2;
+      // the factor stays positive, so that maxima may be taken without it
+      const float up = a.c != 0.f ? copysignf(__uint_as_float((uint32_t)(14 - e2 + 127) << 23), a.c) : 0.f;
+      const float factor = fmaxf(fabsf(a.c) * __uint_as_float((uint32_t)(e2 - 14 + 127) << 23), 0x1p-126f);
+#pragma unroll
+      for (int q = 0; q < QD; ++q)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = x[q][4 * s + e] * up;
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            const uint32_t b0 = half2_bits(y[0], y[1]), b1 = half2_bits(y[2], y[3]);
+            if (C::kQInSmem) {
+              qs[((part * NT + n) * QD * 4 + q * 4 + s) * 32 + lane] = make_uint2(b0, b1);
+            } else {
+              f[C::kQInSmem ? 0 : n][part][q * 4 + s][0] = b0;
+              f[C::kQInSmem ? 0 : n][part][q * 4 + s][1] = b1;
+            }
+            const float2 r0 = half2_floats(b0), r1 = half2_floats(b1);
+            y[0] -= r0.x; y[1] -= r0.y; y[2] -= r1.x; y[3] -= r1.y;
+          }
+        }
+      if (C::kQInSmem) {
+        if (t == 0) col_scale[8 * n + g] = factor;
+      } else {
+        cs[n][0] = __shfl_sync(~0u, factor, 8 * t);        // lane 4 g' holds column g'
+        cs[n][1] = __shfl_sync(~0u, factor, 8 * t + 4);
+      }
+    }
+    if (C::kQInSmem) {
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        cs[n][0] = col_scale[8 * n + 2 * t];
+        cs[n][1] = col_scale[8 * n + 2 * t + 1];
+      }
+    }
+  }
+  // S^T = K Q^T of a warp's tile at st
+  __device__ __forceinline__ void scores(const unsigned char *st, const uint2 *qs, float (&s)[C::MT][C::NT][4]) const {
+    constexpr int DP = C::DP, NT = C::NT, PARTS = C::PARTS, MT = C::MT;
+    const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+#pragma unroll
+    for (int q = 0; q < QD; ++q) {
+      uint4 k0[MT], k1[MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        k0[i] = *reinterpret_cast<const uint4 *>(st + piece_at<DP>(16 * i + g, 4 * q + t));
+        k1[i] = *reinterpret_cast<const uint4 *>(st + piece_at<DP>(16 * i + g + 8, 4 * q + t));
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t b[NT][PARTS][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            if (C::kQInSmem) {
+              const uint2 y = qs[((part * NT + n) * QD * 4 + q * 4 + u) * 32 + lane];
+              b[n][part][0] = y.x;
+              b[n][part][1] = y.y;
+            } else {
+              b[n][part][0] = f[C::kQInSmem ? 0 : n][part][q * 4 + u][0];
+              b[n][part][1] = f[C::kQInSmem ? 0 : n][part][q * 4 + u][1];
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const uint32_t x0 = u == 0 ? k0[i].x : u == 1 ? k0[i].y : u == 2 ? k0[i].z : k0[i].w;
+          const uint32_t x1 = u == 0 ? k1[i].x : u == 1 ? k1[i].y : u == 2 ? k1[i].z : k1[i].w;
+          const uint32_t kf[4] = {f16x2_of(x0), f16x2_of(x1), f16x2_of(x0 >> 16), f16x2_of(x1 >> 16)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) mma16816(s[i][n], kf, b[n][part][0], b[n][part][1]);
+        }
+      }
+    }
+  }
+};
+
 // One warp: 16 MT slots at a time against COLS columns, its own ring of
 // cp.async stages, its own running maximum and sum.  Scores are formed
 // transposed, S^T = K Q^T with slots as the 16 rows, so the codes (converted to
@@ -187,7 +333,6 @@ __device__ __forceinline__ uint32_t piece_at(int j, int c) {
 template <class C>
 __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_constant__ SplitParams p) {
   constexpr int DP = C::DP, NT = C::NT, PARTS = C::PARTS, MT = C::MT, KW = C::KW, CH = C::CH;
-  constexpr int QD = DP / 64;
   extern __shared__ __align__(128) unsigned char smem[];
   const AttendParams &a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -271,8 +416,8 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 #pragma unroll
   for (int s = 0; s < C::STAGES - 1; ++s) fetch(s);
 
-  uint32_t qf[C::kQInSmem ? 1 : NT][PARTS][QD * 4][2];
-  float cs[NT][2];           // factors of columns 2t, 2t + 1
+  Queries<C> qf;
+  const auto &cs = qf.cs;
   int limit[NT][2];          // last slot that they see
   // running maxima: as scores without their column's factor, and with it
   float mx[NT][2], m[NT][2], l[NT][2], o[NT][CH][4];
@@ -304,89 +449,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[n][c][e] = 0.f;
       }
-      // query fragments: the thread's column is g, its dimensions 64 q + 16 t ..
-      if (C::kQInSmem) __syncthreads();
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (C::kQInSmem && n % C::WARPS != warp % (NT < C::WARPS ? NT : C::WARPS)) continue;
-        if (C::kQInSmem && warp >= NT) continue;
-        const int col = col0 + 8 * n + g;
-        float x[QD][16];
-        float top = 0.f;
-        const int64_t tok = w.beg + col / a.G;
-        const int hq = h * a.G + col % a.G;
-#pragma unroll
-        for (int q = 0; q < QD; ++q) {
-          const int d0 = 64 * q + 16 * t;
-          const bool in = col < cols && d0 < a.d;
-          const int64_t at = tok * a.qt + hq * a.qh + d0;
-          if (PARTS == 1) {
-            const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + at;
-            if (p.vec_q) {
-#pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                const uint4 y = in ? __ldg(reinterpret_cast<const uint4 *>(src) + v) : make_uint4(0, 0, 0, 0);
-                const uint32_t b[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  x[q][8 * v + 2 * e] = __uint_as_float(b[e] << 16);
-                  x[q][8 * v + 2 * e + 1] = __uint_as_float(b[e] & 0xffff0000u);
-                }
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) x[q][e] = in ? __bfloat162float(src[e]) : 0.f;
-            }
-          } else {
-            const float *src = reinterpret_cast<const float *>(a.q) + at;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[q][e] = in ? __ldg(src + e) : 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[q][e]));
-        }
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        int e2 = (int)(__float_as_uint(top) >> 23) - 127;
-        e2 = e2 < -100 ? -100 : e2;
-        // the factor stays positive, so that maxima may be taken without it
-        const float up = a.c != 0.f ? copysignf(__uint_as_float((uint32_t)(14 - e2 + 127) << 23), a.c) : 0.f;
-        const float factor = fmaxf(fabsf(a.c) * __uint_as_float((uint32_t)(e2 - 14 + 127) << 23), 0x1p-126f);
-#pragma unroll
-        for (int q = 0; q < QD; ++q)
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = x[q][4 * s + e] * up;
-#pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-              const uint32_t b0 = half2_bits(y[0], y[1]), b1 = half2_bits(y[2], y[3]);
-              if (C::kQInSmem) {
-                qs[((part * NT + n) * QD * 4 + q * 4 + s) * 32 + lane] = make_uint2(b0, b1);
-              } else {
-                qf[C::kQInSmem ? 0 : n][part][q * 4 + s][0] = b0;
-                qf[C::kQInSmem ? 0 : n][part][q * 4 + s][1] = b1;
-              }
-              const float2 f0 = half2_floats(b0), f1 = half2_floats(b1);
-              y[0] -= f0.x; y[1] -= f0.y; y[2] -= f1.x; y[3] -= f1.y;
-            }
-          }
-        if (C::kQInSmem) {
-          if (t == 0) col_scale[8 * n + g] = factor;
-        } else {
-          cs[n][0] = __shfl_sync(~0u, factor, 8 * t);        // lane 4 g' holds column g'
-          cs[n][1] = __shfl_sync(~0u, factor, 8 * t + 4);
-        }
-      }
-      if (C::kQInSmem) {
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          cs[n][0] = col_scale[8 * n + 2 * t];
-          cs[n][1] = col_scale[8 * n + 2 * t + 1];
-        }
-      }
+      qf.load(p, w.beg, h, col0, cols, qs, col_scale);
     }
 
     cp_async_wait<C::STAGES - 2>();
@@ -400,50 +463,8 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
       const unsigned valid = *reinterpret_cast<const unsigned *>(st + 2 * C::kTile + 2 * KW * 4);
       const int j0 = w.step * C::KT + warp * KW;
       if (valid || (p.scores && j0 < w.len)) {
-        // S^T = K Q^T
         float s[MT][NT][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
-#pragma unroll
-        for (int q = 0; q < QD; ++q) {
-          uint4 k0[MT], k1[MT];
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            k0[i] = *reinterpret_cast<const uint4 *>(st + piece_at<DP>(16 * i + g, 4 * q + t));
-            k1[i] = *reinterpret_cast<const uint4 *>(st + piece_at<DP>(16 * i + g + 8, 4 * q + t));
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t b[NT][PARTS][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int part = 0; part < PARTS; ++part) {
-                if (C::kQInSmem) {
-                  const uint2 y = qs[((part * NT + n) * QD * 4 + q * 4 + u) * 32 + lane];
-                  b[n][part][0] = y.x;
-                  b[n][part][1] = y.y;
-                } else {
-                  b[n][part][0] = qf[C::kQInSmem ? 0 : n][part][q * 4 + u][0];
-                  b[n][part][1] = qf[C::kQInSmem ? 0 : n][part][q * 4 + u][1];
-                }
-              }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              const uint32_t x0 = u == 0 ? k0[i].x : u == 1 ? k0[i].y : u == 2 ? k0[i].z : k0[i].w;
-              const uint32_t x1 = u == 0 ? k1[i].x : u == 1 ? k1[i].y : u == 2 ? k1[i].z : k1[i].w;
-              const uint32_t f[4] = {f16x2_of(x0), f16x2_of(x1), f16x2_of(x0 >> 16), f16x2_of(x1 >> 16)};
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part) mma16816(s[i][n], f, b[n][part][0], b[n][part][1]);
-            }
-          }
-        }
+        qf.scores(st, qs, s);
         // key scales; the mask, where the tile needs one
         float vsc[MT][2], most = 0.f;
         bool grew = false;
@@ -672,18 +693,21 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 __global__ void __launch_bounds__(256) weights_of_scores_kernel(const __grid_constant__ SplitParams p,
                                                                 int cols_of_group) {
   const AttendParams &a = p.a;
-  extern __shared__ float lse2[];
+  constexpr int kCols = 512;     // at a time: whole groups
+  __shared__ float2 lse[kCols];
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
-  const int64_t beg = a.req.begin(r);
+  if (!requests_ok(a) || (int64_t)blockIdx.x * 256 >= len) return;
+  const int64_t beg = a.req.begin(r), j = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int cols = (int)(a.req.begin(r + 1) - beg) * a.G;
-  if (!requests_ok(a)) return;
-  for (int c = threadIdx.x; c < cols; c += 256)
-    lse2[c] = a.lse[(beg + c / a.G) * a.Hq + h * a.G + c % a.G] * kLog2e;
-  __syncthreads();
-  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (j >= len) return;
   float sum = 0.f;     // of the groups' sums: fewer roundings than of all in a row
   for (int c0 = 0; c0 < cols; c0 += cols_of_group) {
+    if (c0 % kCols == 0) {
+      __syncthreads();
+      for (int c = threadIdx.x; c < kCols && c0 + c < cols; c += 256)
+        lse[c] = a.stats[(beg + (c0 + c) / a.G) * a.Hq + h * a.G + (c0 + c) % a.G];
+      __syncthreads();
+    }
+    if (j >= len) continue;
     float part = 0.f;
     const int64_t seg = ((int64_t)r * a.H + h) * p.groups + c0 / cols_of_group;
     const float *x = p.scores + (seg * a.max_len + j) * cols_of_group;
@@ -692,43 +716,92 @@ __global__ void __launch_bounds__(256) weights_of_scores_kernel(const __grid_con
       const float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (c0 + c + e < cols && z[e] > -INFINITY) part += ex2(z[e] - lse2[c0 + c + e]);
+        if (c0 + c + e < cols && z[e] > -INFINITY) part += probability(z[e], lse[c0 % kCols + c + e]);
     }
     sum += part;
   }
-  a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
+  if (j < len) a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
 }
 
-// weights[r][h][j] += sum of p_ij: a thread for each slot, the scores again.
-__global__ void __launch_bounds__(128) weights_kernel(const __grid_constant__ AttendParams p) {
-  if (!requests_ok(p)) return;
-  const int r = blockIdx.z, h = blockIdx.y, len = len_of(p, r);
-  const int64_t j = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  if (j >= len) return;
-  const int page = page_of(p, r, block_of(p, (int)j));
-  if (page < 0) return;
-  const int64_t beg = p.req.begin(r), n = p.req.begin(r + 1) - beg;
-  const uint8_t *row = p.k + (((int64_t)page * p.H + h) * p.bs + j % p.bs) * p.d;
-  const float ks = p.ks[(int64_t)page * p.H + h] * p.c;
-  float sum = 0.f;
-  const int64_t i0 = j - (len - n) > 0 ? j - (len - n) : 0;
-  float part = 0.f;    // of 32 queries: fewer roundings than of all in a row
-  for (int64_t i = i0; i < n; ++i) {
-    for (int u = 0; u < p.G; ++u) {
-      const int hq = h * p.G + u;
-      float s = 0.f;
-      for (int e = 0; e < p.d; e += 2) {
-        const float2 a = floats_of(*reinterpret_cast<const uint16_t *>(row + e));
-        s += q_at(p, beg + i, hq, e) * a.x + q_at(p, beg + i, hq, e + 1) * a.y;
-      }
-      part += exp2f(s * ks - p.lse[(beg + i) * p.Hq + hq] * kLog2e);
-    }
-    if ((i - i0) % 32 == 31 || i + 1 == n) {
-      sum += part;
-      part = 0.f;
-    }
+// The same where the scores were not kept: formed again from the same operands in the
+// same order, so that they are the same numbers.  A CTA takes as many slots as a step of
+// the split kernel and all columns that see one of them.
+template <class C>
+__global__ void __launch_bounds__(32 * C::WARPS) weights_again_kernel(const __grid_constant__ SplitParams p) {
+  constexpr int DP = C::DP, NT = C::NT, MT = C::MT, KW = C::KW, CH = C::CH;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const AttendParams &a = p.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  unsigned char *st = smem + warp * C::kAgainTile;
+  uint2 *qs = reinterpret_cast<uint2 *>(smem + C::WARPS * C::kAgainTile);
+  float *col_scale = reinterpret_cast<float *>(smem + C::WARPS * C::kAgainTile + (C::kQInSmem ? C::kQ : 0));
+  const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
+  if (!requests_ok(a) || (int64_t)blockIdx.x * C::KT >= len) return;
+  const int first = blockIdx.x * C::KT, j0 = first + warp * KW;
+  const int64_t beg = a.req.begin(r);
+  const int fresh = (int)(a.req.begin(r + 1) - beg), cols = fresh * a.G;
+  // the warp's keys and their scales
+  const int j = j0 + lane % KW;
+  int page = -1;
+  uint32_t row = 0;
+  if (j < len) {
+    const uint32_t block = block_of(a, j);
+    page = page_of(a, r, block);
+    if (page >= 0) row = ((uint32_t)page * a.H + h) * a.bs + (j - block * a.bs);
   }
-  p.weights[((int64_t)r * p.H + h) * p.wstride + j] += sum;
+  const float kscale = page >= 0 ? __ldg(a.ks + (uint32_t)page * a.H + h) : 0.f;
+  const unsigned valid = __ballot_sync(~0u, page >= 0);
+  const int c = lane % CH;
+#pragma unroll
+  for (int i = 0; i < KW * CH / 32; ++i) {
+    const int k = i * (32 / CH) + lane / CH;
+    const uint32_t from = __shfl_sync(~0u, row, k);
+    const bool there = c * 16 < a.d && (valid >> k & 1);
+    cp_async16(st + piece_at<DP>(k, c), a.k + (there ? (uint64_t)from * a.d + c * 16 : 0), there ? 16 : 0);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncwarp();
+  float sum[MT][2] = {};
+  Queries<C> qf;
+  // from the group of the first query that sees the CTA's first slot
+  const int group0 = (int)((int64_t)max(0, first - (len - fresh)) * a.G / C::COLS);
+  for (int col0 = group0 * C::COLS; col0 < cols; col0 += C::COLS) {
+    qf.load(p, beg, h, col0, cols, qs, col_scale);
+    float s[MT][NT][4];
+    qf.scores(st, qs, s);
+    float part[MT][2] = {};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = col0 + 8 * n + 2 * t + e;
+        const int limit = col < cols ? len - fresh + col / a.G : -1;
+        const float2 lse = col < cols ? a.stats[(beg + col / a.G) * a.Hq + h * a.G + col % a.G] : make_float2(0.f, INFINITY);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int k = 16 * i + 8 * half + g;
+            const float scale = __shfl_sync(~0u, kscale, k);
+            const float z = __fmul_rn(__fmul_rn(s[i][n][2 * half + e], scale), qf.cs[n][e]);
+            if ((valid >> k & 1) && j0 + k <= limit && z > -INFINITY) part[i][half] += probability(z, lse);
+          }
+      }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) sum[i][half] += part[i][half];
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) sum[i][half] += __shfl_xor_sync(~0u, sum[i][half], o);
+      const int k = 16 * i + 8 * half + g;
+      if (t == 0 && (valid >> k & 1)) a.weights[((int64_t)r * a.H + h) * a.wstride + j0 + k] += sum[i][half];
+    }
 }
 
 kvx_status check(const kvx_attend8_args *a) {
@@ -748,7 +821,7 @@ kvx_status check(const kvx_attend8_args *a) {
 // Sizes of a call's workspace and grid.
 struct Shape {
   int cols, groups, grid;      // columns of a group, groups, CTAs
-  size_t arrived, partial, lse, scores, bytes;   // offsets
+  size_t arrived, partial, stats, scores, bytes;   // offsets
   bool spool;                  // the scores are kept for the weights
 };
 constexpr int kGrid = 152;     // one CTA an SM
@@ -761,43 +834,49 @@ Shape shape_of(const kvx_attend8_args *a) {
   s.grid = kGrid;
   const int dp = a->cache.head_dim <= 64 ? 64 : a->cache.head_dim <= 128 ? 128 : 256;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  // the scores of all columns, while they fit 4 GB (and a CTA's log-sum-exps 48 KB)
+  // the scores of all columns, while they fit 4 GB
   const size_t score_bytes = (size_t)a->num_requests * a->cache.heads * s.groups * a->max_len * s.cols * 4;
-  s.spool = a->weights && most <= 12288 && score_bytes <= (size_t)4 << 30;
+  s.spool = a->weights && score_bytes <= (size_t)4 << 30;
   s.arrived = 0;
   s.partial = up((size_t)a->num_requests * a->cache.heads * s.groups * 4);
-  s.lse = s.partial + up((size_t)2 * s.grid * s.cols * (dp + 2) * 4);
-  s.scores = s.lse + up((size_t)a->ntok * a->q_heads * 4);
+  s.stats = s.partial + up((size_t)2 * s.grid * s.cols * (dp + 2) * 4);
+  s.scores = s.stats + up((size_t)a->ntok * a->q_heads * sizeof(float2));
   s.bytes = s.scores + (s.spool ? up(score_bytes) : 0);
   return s;
 }
 
-template <int DP, int NT, int PARTS>
-kvx_status launch_split(const SplitParams &p, int grid, cudaStream_t s) {
-  // tiles of 16 slots a warp works on at once, while the sums leave registers for two;
-  // stages: 8 slots tiles deep, or what shared memory holds
-  constexpr int MT = DP <= 128 && NT * PARTS <= 2 ? 2 : 1;
-  constexpr int STAGES = DP == 64 ? 8 / MT : DP == 128 ? (MT == 2 ? 3 : 5) : 2;
-  using C = SplitCfg<DP, NT, PARTS, MT, 8, STAGES>;
+template <class C>
+kvx_status launch_split(const SplitParams &p, int grid, bool again, cudaStream_t s) {
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
-  const cudaError_t e =
-      cudaFuncSetAttribute(split_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-  if (e != cudaSuccess) return KVX_ERR_CUDA;
+  if (cudaFuncSetAttribute(split_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess)
+    return KVX_ERR_CUDA;
   split_kernel<C><<<grid, 32 * C::WARPS, C::kSmem, s>>>(p);
+  if (const kvx_status st = launched()) return st;
+  if (!again) return KVX_OK;
+  if (cudaFuncSetAttribute(weights_again_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kAgainSmem) !=
+      cudaSuccess)
+    return KVX_ERR_CUDA;
+  weights_again_kernel<C><<<dim3((p.a.max_len + C::KT - 1) / C::KT, p.a.H, p.a.req.R), 32 * C::WARPS, C::kAgainSmem, s>>>(p);
   return launched();
 }
+// tiles of 16 slots a warp works on at once, while the sums leave registers for two;
+// stages: 8 slots tiles deep, or what shared memory holds
+template <int DP, int NT, int PARTS>
+using Cfg = SplitCfg<DP, NT, PARTS, (DP <= 128 && NT * PARTS <= 2 ? 2 : 1), 8,
+                     (DP == 64 ? (NT * PARTS <= 2 ? 4 : 8) : DP == 128 ? (NT * PARTS <= 2 ? 3 : 5) : 2)>;
 template <int DP, int PARTS>
-kvx_status launch_cols(const SplitParams &p, int cols, int grid, cudaStream_t s) {
-  if (cols == 8) return launch_split<DP, 1, PARTS>(p, grid, s);
-  if (cols == 16) return launch_split<DP, 2, PARTS>(p, grid, s);
-  if constexpr (DP <= 128) return launch_split<DP, 4, PARTS>(p, grid, s);
+kvx_status launch_cols(const SplitParams &p, int cols, int grid, bool again, cudaStream_t s) {
+  if (cols == 8) return launch_split<Cfg<DP, 1, PARTS>>(p, grid, again, s);
+  if (cols == 16) return launch_split<Cfg<DP, 2, PARTS>>(p, grid, again, s);
+  if constexpr (DP <= 128) return launch_split<Cfg<DP, 4, PARTS>>(p, grid, again, s);
   return KVX_ERR_UNSUPPORTED;
 }
+// The split kernel and, with `again`, the weights from scores that were not kept.
 template <int PARTS>
-kvx_status launch_dim(const SplitParams &p, int cols, int grid, cudaStream_t s) {
-  return p.a.d <= 64    ? launch_cols<64, PARTS>(p, cols, grid, s)
-         : p.a.d <= 128 ? launch_cols<128, PARTS>(p, cols, grid, s)
-                        : launch_cols<256, PARTS>(p, cols, grid, s);
+kvx_status launch_dim(const SplitParams &p, int cols, int grid, bool again, cudaStream_t s) {
+  return p.a.d <= 64    ? launch_cols<64, PARTS>(p, cols, grid, again, s)
+         : p.a.d <= 128 ? launch_cols<128, PARTS>(p, cols, grid, again, s)
+                        : launch_cols<256, PARTS>(p, cols, grid, again, s);
 }
 
 }  // namespace
@@ -830,6 +909,7 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.lens = a->lens;
   p.lse = a->lse;
   p.weights = a->weights;
+  p.stats = nullptr;
   p.status = a->status;
   p.req = {a->cu_seqlens, a->num_requests, a->ntok};
   p.num_blocks = (int)c.num_blocks;
@@ -854,7 +934,8 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   char *ws = (char *)a->workspace;
   if (kvx_attend8_tc_supports(a)) return kvx_attend8_tc_launch(a, p, ws, s);
   const Shape sh = shape_of(a);
-  if (!p.lse) p.lse = (float *)(ws + sh.lse);
+  const bool weighs = a->weights && a->max_len > 0;
+  if (weighs) p.stats = (float2 *)(ws + sh.stats);
   SplitParams sp;
   sp.a = p;
   sp.groups = sh.groups;
@@ -862,12 +943,9 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   sp.partial = (float *)(ws + sh.partial);
   sp.scores = sh.spool ? (float *)(ws + sh.scores) : nullptr;
   sp.vec_q = aligned_to(a->q, 16) && ((p.qt | p.qh) * size) % 16 == 0;
-  const kvx_status st = size == 2 ? launch_dim<1>(sp, sh.cols, sh.grid, s) : launch_dim<2>(sp, sh.cols, sh.grid, s);
-  if (st != KVX_OK || !a->weights || a->max_len == 0) return st;
-  if (sh.spool)
-    weights_of_scores_kernel<<<dim3((a->max_len + 255) / 256, c.heads, a->num_requests), 256,
-                               p.G * p.max_new * 4, s>>>(sp, sh.cols);
-  else
-    weights_kernel<<<dim3((a->max_len + 127) / 128, c.heads, a->num_requests), 128, 0, s>>>(p);
+  const bool again = weighs && !sh.spool;
+  const kvx_status st = size == 2 ? launch_dim<1>(sp, sh.cols, sh.grid, again, s) : launch_dim<2>(sp, sh.cols, sh.grid, again, s);
+  if (st != KVX_OK || !weighs || again) return st;
+  weights_of_scores_kernel<<<dim3((a->max_len + 255) / 256, c.heads, a->num_requests), 256, 0, s>>>(sp, sh.cols);
   return launched();
 }

@@ -17,7 +17,10 @@ struct AttendParams {
   void *out;
   int64_t qt, qh, ot, oh;
   const int32_t *table, *lens;
-  float *lse, *weights;
+  float *lse, *weights;      // lse may be NULL
+  // with weights, [ntok][Hq]: a row's log-sum-exp in base 2 as two terms, a score and the
+  // rest.  Their sum in fp32 would be off by half an ulp of large scores.
+  float2 *stats;
   uint32_t *status;
   kvx8::Requests req;
   int64_t wstride;
@@ -48,11 +51,6 @@ __device__ __forceinline__ int page_of(const AttendParams &p, int r, uint32_t bl
   const int page = block < (uint32_t)p.max_blocks ? __ldg(p.table + (int64_t)r * p.max_blocks + block) : -1;
   return page < p.num_blocks ? page : -1;
 }
-__device__ __forceinline__ float q_at(const AttendParams &p, int64_t g, int h, int i) {
-  const int64_t at = g * p.qt + h * p.qh + i;
-  return p.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.q)[at])
-                : reinterpret_cast<const float *>(p.q)[at];
-}
 __device__ __forceinline__ bool requests_ok(const AttendParams &p) {
   bool good = p.req.ok();
   if (p.req.cu) {
@@ -63,6 +61,20 @@ __device__ __forceinline__ bool requests_ok(const AttendParams &p) {
   }
   return good;
 }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The log-sum-exp of a row whose sum l is relative to exp2(m + shift).
+__device__ __forceinline__ void store_lse(const AttendParams &p, int64_t g, int hq, float m, float shift, float l) {
+  const bool any = l != 0.f;
+  const float rest = shift + log2f(l);
+  if (p.lse) p.lse[g * p.Hq + hq] = any ? (m + rest) * kLn2 : -INFINITY;
+  if (p.stats) p.stats[g * p.Hq + hq] = any ? make_float2(m, rest) : make_float2(0.f, INFINITY);
+}
+// The probability of a score, rounded as the attention kernel rounded it.
+__device__ __forceinline__ float probability(float score, float2 lse) { return ex2((score - lse.x) - lse.y); }
 // Two dimensions of a finished row, whose sums o and l are relative to exp2(m + shift);
 // its log-sum-exp with the first.
 __device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int hq, int d, float2 o, float m,
@@ -78,21 +90,15 @@ __device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int 
     out[0] = o.x * inv;
     out[1] = o.y * inv;
   }
-  if (d == 0) p.lse[g * p.Hq + hq] = l != 0.f ? (m + (shift + log2f(l))) * kLn2 : -INFINITY;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  if (d == 0) store_lse(p, g, hq, m, shift, l);
 }
 // A maximum to subtract: 0 before any score (exp2(-inf - 0) is 0; a NaN score stays NaN).
 __device__ __forceinline__ float finite_or_0(float m) { return m > -INFINITY ? m : 0.f; }
 
 }  // namespace
 
-// kvx_attend8_tc.cu: bf16 queries and head_dim 128 over blocks of whole 8-slot
-// groups.  `workspace` is zero-filled before its first use.
+// kvx_attend8_tc.cu: bf16 queries and head_dim up to 128 over blocks of whole 8-slot
+// groups.
 bool kvx_attend8_tc_supports(const kvx_attend8_args *a);
 size_t kvx_attend8_tc_workspace_bytes(const kvx_attend8_args *a);
 kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *a, const kvx8::AttendParams &p, char *workspace,

@@ -516,7 +516,7 @@ __device__ __forceinline__ uint64_t probabilities(uint32_t *out, const uint32_t 
   return sum;
 }
 // Beyond this (base 2) the maximum's own half ulp counts in an exponent.
-constexpr float kFar = 65536.f;
+constexpr float kFar = 4096.f;
 // 32 of a row's scores from tensor memory, each rounded once to fp32.
 __device__ __forceinline__ void rounded_scores(uint32_t (&s)[32], uint32_t col, const float4 *scale, uint32_t mask, int seen, float cs) {
   float f[8];
@@ -1019,7 +1019,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
     }
     if (live) {
       if (direct) {
-        a.lse[tok * a.Hq + hq] = l != 0.f ? (m + (shift + log2f(l))) * kLn2 : -INFINITY;
+        store_lse(a, tok, hq, m, shift, l);
       } else {
         slot[p.slot_rows * kD + row] = m;
         slot[p.slot_rows * (kD + 1) + row] = shift;
@@ -1356,7 +1356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // their scores, [rows][score_ld].
 __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_constant__ TcParams p) {
   const AttendParams &a = p.a;
-  extern __shared__ float lse2[];
+  extern __shared__ float2 lse2[];
   const bool good = requests_ok(a);
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
   const int64_t beg = a.req.begin(r);
@@ -1364,7 +1364,7 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
   wait_for_kernel_before();
   if (!good) return;
   for (int c = threadIdx.x; c < rows; c += 256)
-    lse2[c] = a.lse[(beg + c / a.G) * a.Hq + h * a.G + c % a.G] * kLog2e;
+    lse2[c] = a.stats[(beg + c / a.G) * a.Hq + h * a.G + c % a.G];
   __syncthreads();
   const int j = blockIdx.x * 256 + threadIdx.x;
   if (j >= len || rows == 0) return;
@@ -1373,7 +1373,7 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
 #pragma unroll 8
   for (int c = 0; c < rows; ++c) {
     const float z = x[(int64_t)c * p.score_ld];
-    sum += z > -INFINITY ? ex2(z - lse2[c]) : 0.f;
+    sum += z > -INFINITY ? probability(z, lse2[c]) : 0.f;
   }
   a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
 }
@@ -1966,8 +1966,33 @@ struct WtShared {
   float ks[kWtStages][kTile / 4];
   float sum[kWtTiles][kTile];
   __align__(16) float4 rows[kTile];   // of row pairs: two factors, two log-sum-exps (base 2, negative)
+  __align__(16) float4 terms[kTile];  // the log-sum-exps' two terms: two scores, two rests (negative)
+  int far[8];                         // a warp's rows with scores beyond kFar
 };
 constexpr size_t kWtSmem = 1024 + kSmemQ + kWtStages * (size_t)kTileBytes + sizeof(WtShared);
+// A slot's sum over 256 columns, of which those below `from` do not see it, where some
+// scores are beyond kFar: they are rounded as the attention kernel did, then the two terms
+// of their row's log-sum-exp are subtracted.
+__device__ __noinline__ float far_weights(uint32_t col, float f, int from, const float4 *rows, const float4 *terms) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    uint32_t s[32];
+    tc_ld32(col + 32 * q, s);
+    tc_wait_ld32(s);
+    float part = 0.f;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float4 k = rows[16 * q + e / 2], t = terms[16 * q + e / 2];
+      const float z0 = __fmul_rn(__uint_as_float(s[e]), fmaxf(f * k.x, 0x1p-126f));
+      const float z1 = __fmul_rn(__uint_as_float(s[e + 1]), fmaxf(f * k.y, 0x1p-126f));
+      part += 32 * q + e >= from ? ex2((z0 + t.x) + t.z) : 0.f;
+      part += 32 * q + e + 1 >= from ? ex2((z1 + t.y) + t.w) : 0.f;
+    }
+    sum += part;
+  }
+  return sum;
+}
 
 __global__ void __launch_bounds__(kWtThreads, 1)
     weights_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_k, int per) {
@@ -2035,14 +2060,21 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + tok * a.qt + (int64_t)hq * a.qh;
       const float cs = put_queries<4>(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32, kTileBytes, 32);
       float *pair_of = reinterpret_cast<float *>(&sh->rows[tid / 2]) + tid % 2;
+      float *terms_of = reinterpret_cast<float *>(&sh->terms[tid / 2]) + tid % 2;
       if (c == 0) wait_for_kernel_before();   // the log-sum-exps
       // a dead row gives exp2(-inf)
+      const float2 lse = live ? a.stats[tok * a.Hq + hq] : make_float2(0.f, INFINITY);
       pair_of[0] = live ? cs : 0.f;
-      pair_of[2] = live ? -a.lse[tok * a.Hq + hq] * kLog2e : -INFINITY;
+      pair_of[2] = -(lse.x + lse.y);
+      terms_of[0] = -lse.x;
+      terms_of[2] = -lse.y;
+      const bool beyond = __any_sync(~0u, fabsf(lse.x) > kFar);
+      if (lane == 0) sh->far[warp] = beyond;
       fence_async_proxy();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh->q_full));
       if (!W.warp_wait(&sh->q_full, c & 1)) goto done;   // the other rows' constants
+      const bool far = __any_sync(~0u, sh->far[lane % 8]);
       const int count = seen(c);
       for (int t = 0; t < count; ++t, ++n) {
         if ((n & 1) != i) continue;
@@ -2058,8 +2090,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const bool masked = __any_sync(~0u, from > 0);
         const uint64_t f2 = pair(f, f);
         uint64_t sum = pair(0.f, 0.f);
+        if (far) sum = pair(far_weights(s_col, f, from, sh->rows, sh->terms), 0.f);
 #pragma unroll 1
-        for (int q = 0; q < 8; ++q) {
+        for (int q = far ? 8 : 0; q < 8; ++q) {
           uint32_t s[32];
           tc_ld32(s_col + 32 * q, s);
           tc_wait_ld32(s);
@@ -2169,7 +2202,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 constexpr int kSlotsOfThread = 4;
 __global__ void __launch_bounds__(256) weights_of_columns_kernel(const __grid_constant__ TcParams p) {
   const AttendParams &a = p.a;
-  __shared__ float lse2[16];
+  __shared__ float2 lse2[16];
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
   const int64_t beg = a.req.begin(r), j0 = (int64_t)blockIdx.x * (256 * kSlotsOfThread) + threadIdx.x;
   const bool good = requests_ok(a);
@@ -2181,7 +2214,7 @@ __global__ void __launch_bounds__(256) weights_of_columns_kernel(const __grid_co
   wait_for_kernel_before();
   if ((int64_t)blockIdx.x * (256 * kSlotsOfThread) >= len || rows == 0) return;
   if (threadIdx.x < rows)
-    lse2[threadIdx.x] = a.lse[(beg + threadIdx.x / a.G) * a.Hq + h * a.G + threadIdx.x % a.G] * kLog2e;
+    lse2[threadIdx.x] = a.stats[(beg + threadIdx.x / a.G) * a.Hq + h * a.G + threadIdx.x % a.G];
   const float *x = p.scores + (((int64_t)r * a.H + h) * p.score_ld + j0) * p.slot_rows;
   __syncthreads();
 #pragma unroll 1
@@ -2198,7 +2231,7 @@ __global__ void __launch_bounds__(256) weights_of_columns_kernel(const __grid_co
       const float z[8] = {y[k][0].x, y[k][0].y, y[k][0].z, y[k][0].w, y[k][1].x, y[k][1].y, y[k][1].z, y[k][1].w};
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (c + e < rows && z[e] > -INFINITY) sum[k] += ex2(z[e] - lse2[c + e]);
+        if (c + e < rows && z[e] > -INFINITY) sum[k] += probability(z[e], lse2[c + e]);
     }
   }
 #pragma unroll
@@ -2214,7 +2247,7 @@ typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, voi
 struct TcShape {
   int slot_rows, part_size, grid, score_ld, box;
   bool wide, columns, spool;
-  size_t splits, partial, lse, scores, bytes;
+  size_t splits, partial, stats, scores, bytes;
 };
 TcShape tc_shape(const kvx_attend8_args *a) {
   TcShape s;
@@ -2235,8 +2268,8 @@ TcShape tc_shape(const kvx_attend8_args *a) {
   const size_t items = (size_t)a->num_requests * a->cache.heads;
   s.splits = 0;
   s.partial = up(s.grid * sizeof(Split));
-  s.lse = s.partial + up((size_t)2 * s.grid * (s.wide ? 1 : 2) * s.part_size * 4);
-  s.scores = s.lse + up((size_t)a->ntok * a->q_heads * 4);
+  s.stats = s.partial + up((size_t)2 * s.grid * (s.wide ? 1 : 2) * s.part_size * 4);
+  s.scores = s.stats + up((size_t)a->ntok * a->q_heads * sizeof(float2));
   // for the weights, scores are kept while they take 4 GB at most, else formed again
   const size_t score_bytes = items * s.slot_rows * s.score_ld * 4;
   s.spool = a->weights && !s.wide && score_bytes <= (size_t)4 << 30;
@@ -2283,7 +2316,7 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   if (!encode(&mk, args->cache, a.k, sh.box) || !encode(&mv, args->cache, a.v, sh.box)) return KVX_ERR_CUDA;
   TcParams p;
   p.a = a;
-  if (!p.a.lse) p.a.lse = (float *)(ws + sh.lse);
+  p.a.stats = a.weights ? (float2 *)(ws + sh.stats) : nullptr;
   p.grid = sh.grid;
   p.splits = (Split *)(ws + sh.splits);
   p.partial = (float *)(ws + sh.partial);
@@ -2311,5 +2344,5 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   }
   const auto grid = [&](int slots) { return dim3((a.max_len + slots - 1) / slots, a.H, a.req.R); };
   if (sh.columns) return launch_after(weights_of_columns_kernel, grid(256 * kSlotsOfThread), 256, 0, s, p);
-  return launch_after(weights_of_rows_kernel, grid(256), 256, sh.slot_rows * 4, s, p);
+  return launch_after(weights_of_rows_kernel, grid(256), 256, sh.slot_rows * sizeof(float2), s, p);
 }

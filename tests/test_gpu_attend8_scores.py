@@ -176,3 +176,84 @@ def test_rows_of_infinities_and_nan_end_and_stay_alone(H, G, new):
     want = ref.attend(good.double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], 128 ** -0.5)
     assert int(status.item()) == 0 and torch.isnan(out[torch.tensor(odd).cuda()]).all()
     ordinary(out, lse, want, ~odd, True, 300)
+
+
+# Weights: kept scores of 8 and 16 columns, of narrow rows and of the split form; scores
+# formed again by the wide form, and by every other one where the bound on the lengths is
+# too large to keep them.
+WEIGHED = [(*FEW8, 128, 16, torch.bfloat16), (*FEW16, 128, 16, torch.bfloat16), (*NARROW, 128, 16, torch.bfloat16),
+           (*WIDE, 128, 16, torch.bfloat16), (2, 4, 3, 64, 16, torch.float32), (1, 4, 20, 128, 24, torch.float32),
+           (2, 2, 20, 256, 16, torch.bfloat16)]
+
+
+def check_weights(w, out, lse, want, c, lens, new, G, sure, n):
+    """Each weight is the sum of its sure rows' probabilities, off by 2^-20 of themselves,
+    and of its ordinary ones', off as in test_gpu_attend8.py."""
+    H = w.shape[1]
+    xe = np.where(sure, 0, 2.0 ** -16 * want[4]).max()
+    tol = (2 * xe + n * 2.0 ** -23 + (new * G + 16) * 2.0 ** -23 + 2.0 ** -20) * want[2] + 1e-30
+    got = w[..., :max(lens)].double().cpu().numpy()
+    assert np.isfinite(got).all() and (np.abs(got - want[2]) <= tol).all(), (np.abs(got - want[2]) / tol).max()
+    assert not w[..., max(lens):].any()
+
+
+@pytest.mark.parametrize("size", [2.0 ** 13, 2.0 ** 17, 1e9, 1e30])
+@pytest.mark.parametrize("bound", [0, 1 << 26])
+@pytest.mark.parametrize("H,G,new,d,bs,dtype", WEIGHED)
+def test_weights_of_huge_scores(H, G, new, d, bs, dtype, bound, size):
+    lens = [1100, 150]
+    c, big, scale = planted(H, G, new, d, bs, lens, dtype, size, 5)
+    bound = bound or max(lens)
+    w = torch.zeros((2, H, bound), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = c["cache"].attend(c["q"].cuda(), dev(c["table"]), dev(lens), bound, cu_seqlens=dev(c["cu"]),
+                                 max_new=new, scale=scale, weights=w, status=status)
+    assert int(status.item()) == 0
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], scale)
+    certain(out, lse, want, big, dtype == torch.bfloat16)
+    check_weights(w, out, lse, want, c, lens, new, G, big, 1100)
+
+
+@pytest.mark.parametrize("bound", [0, 1 << 26])
+@pytest.mark.parametrize("H,G,new,d,bs,dtype", WEIGHED[:4] + [(2, 4, 3, 128, 16, torch.float32)])
+def test_weights_of_equal_keys(H, G, new, d, bs, dtype, bound):
+    c, scale = equal_keys(H, G, new, 1500, dtype, 1e9)
+    bound = bound or 1500
+    w = torch.zeros((1, H, bound), device="cuda")
+    out, lse = c["cache"].attend(c["q"].cuda(), dev(c["table"]), dev([1500]), bound, cu_seqlens=dev(c["cu"]),
+                                 max_new=new, scale=scale, weights=w)
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], [1500], c["cu"], scale)
+    check_weights(w, out, lse, want, c, [1500], new, G, np.ones((new, H * G), dtype=bool), 1500)
+
+
+@pytest.mark.parametrize("lens,new,G,d,bs,dtype", [([400, 33, 0, 257], [70, 33, 2, 1], 4, 64, 16, torch.float32),
+                                                   ([90, 700], [90, 9], 2, 256, 32, torch.bfloat16),
+                                                   ([300], [300], 8, 128, 24, torch.float32)])
+def test_split_weights_without_kept_scores(lens, new, G, d, bs, dtype):
+    c = make(2, G, d, bs, lens, new, dtype, 43)
+    bound = 1 << 26
+    w = torch.full((len(lens), 2, bound), 0.25, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = c["cache"].attend(c["q"].cuda(), dev(c["table"]), dev(lens), bound, cu_seqlens=dev(c["cu"]),
+                                 max_new=max(new), weights=w, status=status)
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], d ** -0.5)
+    assert int(status.item()) == 0
+    n = max(lens)
+    compare(out, lse, None, want, dtype == torch.bfloat16, n, max(new) * G)
+    for r, L in enumerate(lens):
+        assert (w[r, :, L:] == 0.25).all()
+        ws = want[2][r, :, :L]
+        got = w[r, :, :L].double().cpu().numpy() - 0.25
+        tol = (2 * 2.0 ** -16 * want[4].max() + (n + max(new) * G + 16) * 2.0 ** -23) * (ws + 0.25)
+        assert (np.abs(got - ws) <= tol).all()
+
+
+def test_more_columns_than_shared_memory_holds_log_sum_exps_for():
+    """Kept scores of more than 12,288 columns."""
+    H, G, new, n = 1, 16, 900, 900
+    c = make(H, G, 64, 16, [n], [new], torch.float32, 47)
+    w = torch.zeros((1, H, n), device="cuda")
+    out, lse = c["cache"].attend(c["q"].cuda(), dev(c["table"]), dev([n]), n, cu_seqlens=dev(c["cu"]), max_new=new,
+                                 weights=w)
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], [n], c["cu"], 0.125)
+    compare(out, lse, w, want, False, n, new * G)
