@@ -88,7 +88,7 @@ struct SplitCfg {
 struct SplitParams {
   AttendParams a;
   int groups;            // column groups of max_new queries
-  int *arrived;          // [R][H][groups] CTAs that have left a partial result
+  int *arrived;          // [grid] CTAs that have left a partial result of the item split after CTA c
   float *partial;        // [2 * grid][kSlot]
   float *scores;         // [R][H][groups][max_len][COLS], base 2, or NULL
   int vec_q;
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
         // the last CTA of the segment to get here joins all of its parts
         const int64_t begin = now - w.step, end = begin + w.steps;   // the segment's steps
         const int64_t c0 = ((begin + 1) * N - 1) / T, c1 = (end * N - 1) / T;
-        int *arrived = p.arrived + ((int64_t)w.r * a.H + h) * p.groups + w.group;
+        int *arrived = p.arrived + c0;     // of a CTA's items only the last can be split after it
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) *flag = atomicAdd(arrived, 1) == (int)(c1 - c0);
@@ -825,6 +825,7 @@ struct Shape {
   bool spool;                  // the scores are kept for the weights
 };
 constexpr int kGrid = 152;     // one CTA an SM
+static_assert(kGrid * sizeof(int) <= kWorkspaceHead, "the counters");
 
 Shape shape_of(const kvx_attend8_args *a) {
   Shape s;
@@ -838,7 +839,7 @@ Shape shape_of(const kvx_attend8_args *a) {
   const size_t score_bytes = (size_t)a->num_requests * a->cache.heads * s.groups * a->max_len * s.cols * 4;
   s.spool = a->weights && score_bytes <= (size_t)4 << 30;
   s.arrived = 0;
-  s.partial = up((size_t)a->num_requests * a->cache.heads * s.groups * 4);
+  s.partial = kWorkspaceHead;
   s.stats = s.partial + up((size_t)2 * s.grid * s.cols * (dp + 2) * 4);
   s.scores = s.stats + up((size_t)a->ntok * a->q_heads * sizeof(float2));
   s.bytes = s.scores + (s.spool ? up(score_bytes) : 0);

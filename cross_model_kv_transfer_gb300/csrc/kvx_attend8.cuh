@@ -35,6 +35,11 @@ namespace {
 
 using kvx8::AttendParams;
 
+// A workspace begins with the split form's counters, which are zero between calls: where
+// they lie and how many there are depends on no call's sizes, and no form uses these
+// bytes for anything else, so that one workspace serves calls of different sizes and forms.
+constexpr size_t kWorkspaceHead = 1024;
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // The request's length (0 where it is out of bounds).

@@ -2266,8 +2266,8 @@ TcShape tc_shape(const kvx_attend8_args *a) {
   if (s.box > kTile) s.box = kTile;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t items = (size_t)a->num_requests * a->cache.heads;
-  s.splits = 0;
-  s.partial = up(s.grid * sizeof(Split));
+  s.splits = kWorkspaceHead;
+  s.partial = s.splits + up(s.grid * sizeof(Split));
   s.stats = s.partial + up((size_t)2 * s.grid * (s.wide ? 1 : 2) * s.part_size * 4);
   s.scores = s.stats + up((size_t)a->ntok * a->q_heads * sizeof(float2));
   // for the weights, scores are kept while they take 4 GB at most, else formed again

@@ -695,8 +695,9 @@ typedef struct {
   float *weights;           /* [R][heads][weights_stride], or NULL            */
   int64_t weights_stride;   /* >= max_len                                     */
   void *workspace;          /* kvx_attend8_workspace_bytes(), 256-byte aligned,
-                               zero-filled before its first use; each call
-                               leaves it ready for the next one               */
+                               its first 1024 bytes zero-filled before its first
+                               use; each call leaves it ready for the next one,
+                               whatever that one's sizes, types and blocks    */
   size_t workspace_bytes;
   uint32_t *status;
 } kvx_attend8_args;
