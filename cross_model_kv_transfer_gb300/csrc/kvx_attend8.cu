@@ -815,6 +815,8 @@ kvx_status check(const kvx_attend8_args *a) {
     return KVX_ERR_INVALID_ARG;
   if (a->weights && a->weights_stride < a->max_len) return KVX_ERR_INVALID_ARG;
   if (a->weights && a->num_requests > 65535) return KVX_ERR_UNSUPPORTED;
+  // the rows of one request and KV head are counted in 32 bits
+  if ((int64_t)(a->q_heads / c.heads) * most_new(a) > INT32_MAX - 1024) return KVX_ERR_UNSUPPORTED;
   return KVX_OK;
 }
 
@@ -829,7 +831,7 @@ static_assert(kGrid * sizeof(int) <= kWorkspaceHead, "the counters");
 
 Shape shape_of(const kvx_attend8_args *a) {
   Shape s;
-  const int64_t G = a->q_heads / a->cache.heads, most = G * a->max_new;
+  const int64_t G = a->q_heads / a->cache.heads, most = G * most_new(a);
   s.cols = most <= 8 ? 8 : most <= 16 || a->cache.head_dim > 128 ? 16 : 32;   // registers hold 4096 sums
   s.groups = (int)((most + s.cols - 1) / s.cols);
   s.grid = kGrid;
@@ -928,7 +930,7 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.bs = c.block_size;
   p.max_blocks = c.max_blocks_per_req;
   p.max_len = a->max_len;
-  p.max_new = a->max_new;
+  p.max_new = most_new(a);
   p.bf16 = size == 2;
   p.c = a->scale * kLog2e;
   cudaStream_t s = (cudaStream_t)stream;

@@ -97,6 +97,11 @@ __device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int 
   }
   if (d == 0) store_lse(p, g, hq, m, shift, l);
 }
+// The most queries that one request of the call can have: max_new may be any bound.
+inline int most_new(const kvx_attend8_args *a) {
+  return (int)(a->max_new < a->ntok ? a->max_new : a->ntok > 1 ? a->ntok : 1);
+}
+
 // A maximum to subtract: 0 before any score (exp2(-inf - 0) is 0; a NaN score stays NaN).
 __device__ __forceinline__ float finite_or_0(float m) { return m > -INFINITY ? m : 0.f; }
 

@@ -237,7 +237,7 @@ __device__ __forceinline__ Requests32 look(const AttendParams &a, int r0, bool t
     if (!good) q.fresh = 0;
     if (tell && q.len != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
   }
-  if (a.G * a.max_new <= G::ROWS) {
+  if ((int64_t)a.G * a.max_new <= G::ROWS) {
     q.head = q.fresh > 0 ? G::SETUP + steps_of<G>(a, q.len, q.fresh, 0) : 0;
   } else {
     for (int i = 0; i < 32 && r0 + i < a.req.R; ++i) {
@@ -2251,7 +2251,7 @@ struct TcShape {
 };
 TcShape tc_shape(const kvx_attend8_args *a) {
   TcShape s;
-  const int64_t G = a->q_heads / a->cache.heads, most = G * a->max_new;
+  const int64_t G = a->q_heads / a->cache.heads, most = G * most_new(a);
   // One step of the cases below: 16 requests of 1024 to 16,384 slots, 8 KV heads,
   // without and with weights.  16 rows: columns 109 and 135 us, narrow 143 and 195.
   // 24 rows: narrow 149 and 214, wide 177 and 323; 64 rows: 186 and 315 against 186

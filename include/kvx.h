@@ -685,7 +685,8 @@ typedef struct {
                                head i / (q_heads / cache.heads)               */
   int64_t ntok;             /* queries of all requests, >= 0                  */
   int32_t num_requests;     /* R >= 1                                         */
-  int32_t max_new;          /* bound on one request's queries, >= 1           */
+  int32_t max_new;          /* bound on one request's queries, >= 1; any looser
+                               than ntok counts as ntok                       */
   const int32_t *cu_seqlens;    /* [R+1], or NULL: one query for each request */
   const int32_t *lens;      /* [R] slots each request holds, its new tokens
                                included                                       */
@@ -721,8 +722,9 @@ size_t kvx_attend8_workspace_bytes(const kvx_attend8_args *args);
  * more than max_new queries, writes nothing (KVX_FLAG_BAD_SEQLENS).  One to three
  * launches.  bf16 queries with head_dim up to 128 and blocks of whole 8-slot groups
  * run on the tcgen05 tensor cores: there an element of a query counts to 2^-19 of
- * its row's largest.  max_len is at most 2^31 - 1025.  A kernel's wait that gives up
- * sets KVX_FLAG_TIMEOUT. */
+ * its row's largest.  max_len is at most 2^31 - 1025, and min(max_new, ntok) times
+ * q_heads / heads at most 2^31 - 1025 (else KVX_ERR_UNSUPPORTED).  A kernel's wait that
+ * gives up sets KVX_FLAG_TIMEOUT. */
 kvx_status kvx_attend8(const kvx_attend8_args *args, void *stream);
 
 typedef struct {

@@ -49,3 +49,18 @@ def test_one_workspace_for_calls_that_grow_and_shrink(d, bs, dtypes, weights):
     for turn in range(2):
         for R, new, dt, c, lens, want in made:
             call(c, lens, want, R, new, H, G, dt, ws, weights)
+
+
+@pytest.mark.parametrize("G,max_new", [(2, 2 ** 31 - 1), (8, 2 ** 29)])
+@pytest.mark.parametrize("new", [1, 130, 420])
+def test_any_bound_on_a_requests_queries(G, max_new, new):
+    H, lens, news = 2, [500, 60], [new, 1]
+    c = make(H, G, 128, 16, lens, news, torch.bfloat16, 53)
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], 128 ** -0.5)
+    w = torch.zeros((2, H, 500), device="cuda")
+    out = torch.full(c["q"].shape, 1e30, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _, lse = c["cache"].attend(c["q"].cuda(), dev(c["table"]), dev(lens), 500, cu_seqlens=dev(c["cu"]), max_new=max_new,
+                               out=out, weights=w, status=status)
+    assert int(status.item()) == 0
+    compare(out, lse, w, want, True, 500, new * G)
