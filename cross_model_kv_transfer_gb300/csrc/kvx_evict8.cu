@@ -264,7 +264,9 @@ __device__ __forceinline__ float largest(const uint4 &t, float scale) {
   return fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)) * scale;
 }
 __device__ __forceinline__ uint4 rescaled(const uint4 &t, float f) {
-  if (f == 1.f) return t;
+  // An infinite factor is that of zeros beside a large value in their old block and none
+  // in the new one (a code that is none keeps it below 2^18): they stay as they are.
+  if (f == 1.f || f == INFINITY) return t;
   uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
