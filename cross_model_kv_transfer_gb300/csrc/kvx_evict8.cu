@@ -474,8 +474,10 @@ extern "C" kvx_status kvx_evict8(const kvx_evict8_args *a, void *stream) {
   p.key_cap = each < kMaxKeys ? each : kMaxKeys;
   const size_t smem = (size_t)p.key_cap * 4;
   const auto kernel = few ? select_kernel<true> : select_kernel<false>;
+  // the same for every call: the attribute is the kernel's, which calls from other
+  // host threads share, not this launch's
   if (sizeof(Shared) + smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4) != cudaSuccess)
     return KVX_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, c.heads, a->num_requests);
