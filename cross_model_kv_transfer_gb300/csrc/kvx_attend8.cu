@@ -823,7 +823,7 @@ kvx_status check(const kvx_attend8_args *a) {
 // Sizes of a call's workspace and grid.
 struct Shape {
   int cols, groups, grid;      // columns of a group, groups, CTAs
-  size_t arrived, partial, stats, scores, bytes;   // offsets
+  size_t arrived, partial, stats, scores, bytes;   // offsets; what lies before the scores is needed
   bool spool;                  // the scores are kept for the weights
 };
 constexpr int kGrid = 152;     // one CTA an SM
@@ -837,14 +837,14 @@ Shape shape_of(const kvx_attend8_args *a) {
   s.grid = kGrid;
   const int dp = a->cache.head_dim <= 64 ? 64 : a->cache.head_dim <= 128 ? 128 : 256;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  // the scores of all columns, while they fit 4 GB
-  const size_t score_bytes = (size_t)a->num_requests * a->cache.heads * s.groups * a->max_len * s.cols * 4;
-  s.spool = a->weights && score_bytes <= (size_t)4 << 30;
   s.arrived = 0;
   s.partial = kWorkspaceHead;
   s.stats = s.partial + up((size_t)2 * s.grid * s.cols * (dp + 2) * 4);
   s.scores = s.stats + up((size_t)a->ntok * a->q_heads * sizeof(float2));
-  s.bytes = s.scores + (s.spool ? up(score_bytes) : 0);
+  // the scores of all columns, where the workspace has room for them
+  const uint64_t kept = score_bytes(a, (int64_t)s.groups * s.cols, a->max_len);
+  s.spool = a->weights && kept <= kMostScores && a->workspace_bytes >= s.scores + kept;
+  s.bytes = s.scores + (a->weights ? up(kept < kMostScores ? kept : kMostScores) : 0);
   return s;
 }
 
@@ -895,7 +895,8 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   const kvx_cache8 &c = a->cache;
   const int size = a->dtype == KVX_BF16 ? 2 : 4;
   if (!a->q || !a->out || !aligned_to(a->q, size) || !aligned_to(a->out, size)) return KVX_ERR_INVALID_ARG;
-  if (!a->workspace || !aligned_to(a->workspace, 256) || a->workspace_bytes < kvx_attend8_workspace_bytes(a))
+  const size_t least = kvx_attend8_tc_supports(a) ? kvx_attend8_tc_least_bytes(a) : shape_of(a).scores;
+  if (!a->workspace || !aligned_to(a->workspace, 256) || a->workspace_bytes < least)
     return KVX_ERR_INVALID_ARG;
   AttendParams p;
   p.k = (const uint8_t *)c.k_codes;

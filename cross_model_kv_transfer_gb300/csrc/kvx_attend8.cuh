@@ -102,6 +102,15 @@ inline int most_new(const kvx_attend8_args *a) {
   return (int)(a->max_new < a->ntok ? a->max_new : a->ntok > 1 ? a->ntok : 1);
 }
 
+// Bytes of the scores of `rows` columns for every slot, request and KV head that a call
+// keeps for the weights: at most kMostScores, or it forms them again.
+constexpr uint64_t kMostScores = (uint64_t)4 << 30;
+inline uint64_t score_bytes(const kvx_attend8_args *a, int64_t rows, int64_t slots) {
+  const double b = 4.0 * a->num_requests * a->cache.heads * (double)rows * (double)slots;
+  return b > (double)kMostScores ? kMostScores + 1
+                                 : (uint64_t)a->num_requests * a->cache.heads * rows * slots * 4;
+}
+
 // A maximum to subtract: 0 before any score (exp2(-inf - 0) is 0; a NaN score stays NaN).
 __device__ __forceinline__ float finite_or_0(float m) { return m > -INFINITY ? m : 0.f; }
 
@@ -110,6 +119,9 @@ __device__ __forceinline__ float finite_or_0(float m) { return m > -INFINITY ? m
 // kvx_attend8_tc.cu: bf16 queries and head_dim up to 128 over blocks of whole 8-slot
 // groups.
 bool kvx_attend8_tc_supports(const kvx_attend8_args *a);
+// Of a workspace: the bytes that the call needs, and with those in which calls of at most
+// its sizes can keep scores.
+size_t kvx_attend8_tc_least_bytes(const kvx_attend8_args *a);
 size_t kvx_attend8_tc_workspace_bytes(const kvx_attend8_args *a);
 kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *a, const kvx8::AttendParams &p, char *workspace,
                                  cudaStream_t s);

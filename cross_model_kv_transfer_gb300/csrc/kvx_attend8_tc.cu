@@ -2265,15 +2265,16 @@ TcShape tc_shape(const kvx_attend8_args *a) {
   s.box = a->cache.block_size & -a->cache.block_size;
   if (s.box > kTile) s.box = kTile;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t items = (size_t)a->num_requests * a->cache.heads;
   s.splits = kWorkspaceHead;
   s.partial = s.splits + up(s.grid * sizeof(Split));
   s.stats = s.partial + up((size_t)2 * s.grid * (s.wide ? 1 : 2) * s.part_size * 4);
   s.scores = s.stats + up((size_t)a->ntok * a->q_heads * sizeof(float2));
-  // for the weights, scores are kept while they take 4 GB at most, else formed again
-  const size_t score_bytes = items * s.slot_rows * s.score_ld * 4;
-  s.spool = a->weights && !s.wide && score_bytes <= (size_t)4 << 30;
-  s.bytes = s.scores + (s.spool ? up(score_bytes) : 0);
+  // scores for the weights are kept where the workspace has room for them; room is made
+  // for those of smaller calls too (a wide call keeps none, 64 rows of a narrow one most)
+  const uint64_t kept = score_bytes(a, s.slot_rows, s.score_ld);
+  s.spool = a->weights && !s.wide && kept <= kMostScores && a->workspace_bytes >= s.scores + kept;
+  const uint64_t most_kept = s.wide ? score_bytes(a, 64, s.score_ld) : kept;
+  s.bytes = s.scores + (a->weights ? up(most_kept < kMostScores ? most_kept : kMostScores) : 0);
   return s;
 }
 
@@ -2308,6 +2309,7 @@ bool kvx_attend8_tc_supports(const kvx_attend8_args *a) {
          (uint64_t)c.num_blocks * c.heads * c.block_size <= INT32_MAX;
 }
 
+size_t kvx_attend8_tc_least_bytes(const kvx_attend8_args *a) { return tc_shape(a).scores; }
 size_t kvx_attend8_tc_workspace_bytes(const kvx_attend8_args *a) { return tc_shape(a).bytes; }
 
 kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::AttendParams &a, char *ws, cudaStream_t s) {

@@ -992,8 +992,10 @@ class Cache8:
 
     def attend_workspace(self, *, ntok, num_requests, q_heads, max_len, max_new=1, dtype=None,
                          weights=False):
-        """A workspace (uint8, zero-filled) for ``attend`` calls of at most
-        these sizes that are ordered on one stream."""
+        """A workspace (uint8) for ``attend`` calls of at most these sizes and
+        queries of ``dtype`` (bf16) that are ordered on one stream.  With
+        ``weights`` it has room for scores, up to 4 GB by ``max_len``; without,
+        calls with weights run in it too and form their scores a second time."""
         import torch
         a = Attend8Args()
         a.cache = Cache8Desc(*self._head, 1, self.k_codes.data_ptr())

@@ -703,8 +703,12 @@ typedef struct {
   uint32_t *status;
 } kvx_attend8_args;
 
-/* Scratch of a kvx_attend8 call of these sizes; 0 for sizes that it refuses.
- * A workspace serves calls that are ordered on one stream. */
+/* Scratch of kvx_attend8 calls of at most these sizes (requests, queries, max_new,
+ * max_len, q_heads) over caches of these heads, head_dim and blocks; 0 for sizes that
+ * it refuses.  It never falls as one of them rises.  With weights it has room for
+ * scores (up to 4 GB, by max_len), which calls then keep for the weights; a call with
+ * weights also runs in what the same sizes without them ask for, and forms its
+ * scores a second time.  A workspace serves calls that are ordered on one stream. */
 size_t kvx_attend8_workspace_bytes(const kvx_attend8_args *args);
 
 /* Attention of new tokens over the 8-bit cache.  Query i of a request with n

@@ -19,3 +19,35 @@ def test_rows_that_32_bits_cannot_count_are_refused():
     for dtype in (kvx.KVX_BF16, kvx.KVX_F32):
         a = attend_args(wide, q_heads=32768, ntok=2 ** 16, max_new=2 ** 16, dtype=dtype)
         assert a.workspace_bytes == 0 and kvx.kvx_attend8(a, None) == kvx.KVX_ERR_UNSUPPORTED
+
+
+BOUNDS = {"num_requests": [1, 2, 7, 16, 64, 1000, 65535], "ntok": [1, 2, 64, 500, 5000, 2 ** 20],
+          "max_new": [1, 2, 4, 8, 9, 16, 17, 33, 64, 65, 128, 1000, 5000, 2 ** 31 - 1],
+          "max_len": [0, 1, 255, 4096, 16384, 131071, 2 ** 24, 2 ** 27, 2 ** 31 - 1025],
+          "q_heads": [8, 16, 40, 64, 512, 1024]}
+
+
+@pytest.mark.parametrize("weights", [None, P])
+@pytest.mark.parametrize("d,bs,dtype", [(128, 16, kvx.KVX_BF16), (64, 16, kvx.KVX_BF16), (64, 16, kvx.KVX_F32),
+                                        (128, 24, kvx.KVX_F32), (256, 16, kvx.KVX_BF16), (128, 7, kvx.KVX_BF16)])
+def test_workspaces_never_fall_as_a_bound_rises(d, bs, dtype, weights):
+    cache = cache_desc(heads=8, head_dim=d, block_size=bs)
+    at = dict(num_requests=16, ntok=2000, max_new=8, max_len=16384, q_heads=64)
+
+    def size(**sizes):
+        return attend_args(cache, weights=weights, weights_stride=2 ** 31, dtype=dtype, **sizes).workspace_bytes
+
+    for base in (at, dict(at, max_new=1), dict(at, max_new=100), dict(at, max_len=2 ** 20, num_requests=200)):
+        for name, values in BOUNDS.items():
+            got = [size(**dict(base, **{name: v})) for v in values]
+            assert all(x > 0 for x in got) and got == sorted(got), (name, got)
+
+
+def test_a_workspace_of_larger_calls_is_large_enough_for_every_smaller_one():
+    """The window of a prompt, then decoding: the sizes at which a wide call keeps no
+    scores and a narrow one does."""
+    cache = cache_desc(heads=8, head_dim=128)
+    sizes = dict(num_requests=16, max_len=16384, q_heads=64, weights=P, weights_stride=16384)
+    window = attend_args(cache, ntok=16 * 64, max_new=64, **sizes).workspace_bytes
+    for new in (1, 2, 8, 16):
+        assert attend_args(cache, ntok=16 * new, max_new=new, **sizes).workspace_bytes <= window

@@ -64,3 +64,26 @@ def test_any_bound_on_a_requests_queries(G, max_new, new):
                                out=out, weights=w, status=status)
     assert int(status.item()) == 0
     compare(out, lse, w, want, True, 500, new * G)
+
+
+@pytest.mark.parametrize("d,bs,dtype", [(128, 16, torch.bfloat16), (64, 16, torch.float32)])
+@pytest.mark.parametrize("room", ["of the window", "without weights", "of the window without weights"])
+def test_a_window_and_then_single_tokens(d, bs, dtype, room):
+    """A workspace of large bounds serves small calls; one without room for scores serves
+    calls with weights."""
+    H, G, R, bound = 8, 8, 16, 16384
+    ws = None
+    for new in (64, 1, 2, 5, 1):
+        lens = [new + (53 * r + 7) % 400 for r in range(R)]
+        c = make(H, G, d, bs, lens, [new] * R, dtype, 61 + new)
+        want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], d ** -0.5)
+        if ws is None or room == "without weights":
+            ws = c["cache"].attend_workspace(ntok=R * new, num_requests=R, q_heads=H * G, max_len=bound, max_new=new,
+                                             dtype=dtype, weights="without" not in room)
+        w = torch.zeros((R, H, bound), device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = c["cache"].attend(c["q"].cuda(), dev(c["table"]), dev(lens), bound, cu_seqlens=dev(c["cu"]),
+                                     max_new=new, weights=w, workspace=ws, status=status)
+        assert int(status.item()) == 0
+        compare(out, lse, w[..., :max(lens)].contiguous(), want, dtype == torch.bfloat16, max(lens), new * G)
+        assert not w[..., max(lens):].any()
