@@ -811,6 +811,13 @@ def _int_table(t, name, device, ndim=1):
     return t.data_ptr()
 
 
+def _workspace(t, device):
+    """Pointer and bytes of a workspace: any contiguous tensor on the device."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _status_ptr(t, device):
     return 0 if t is None else _int_table(t, "status", device)
 
@@ -1052,7 +1059,7 @@ class Cache8:
                          hq, n, R, max_new, _int_table(cu_seqlens, "cu_seqlens", dev),
                          _int_table(lens, "lens", dev), max_len,
                          d ** -0.5 if scale is None else scale, lse.data_ptr(), wptr, wstride,
-                         workspace.data_ptr(), workspace.numel(), _status_ptr(status, dev))
+                         *_workspace(workspace, dev), _status_ptr(status, dev))
         st = _Fast.attend(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_attend8")
@@ -1117,8 +1124,8 @@ class Cache8:
         a = _pack_evict(*table, _int_table(dst_table, "dst_table", dev, 2), dst_table.shape[1], R,
                         _int_table(lens, "lens", dev), max_len, keep, sinks, recent, wptr, wstride,
                         _int_table(kept, "kept", dev, 3), kept_weights.data_ptr(),
-                        _int_table(new_lens, "new_lens", dev), workspace.data_ptr(),
-                        workspace.numel(), _status_ptr(status, dev))
+                        _int_table(new_lens, "new_lens", dev), *_workspace(workspace, dev),
+                        _status_ptr(status, dev))
         st = _Fast.evict(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_evict8")
