@@ -775,6 +775,7 @@ def _packer(cls):
     return s.pack
 
 
+_WORKSPACE_HEAD = 1024    # bytes of a kvx_attend8 workspace that must be zero at first
 _pack_rope = _packer(RopeArgs)
 _pack_write = _packer(Cache8WriteArgs)
 _pack_attend = _packer(Attend8Args)
@@ -1015,7 +1016,9 @@ class Cache8:
         need = kvx_attend8_workspace_bytes(a)
         if need == 0:
             raise KvxError(KVX_ERR_INVALID_ARG, "kvx_attend8_workspace_bytes")
-        return torch.zeros(need, dtype=torch.uint8, device=self.device)
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        ws[:_WORKSPACE_HEAD].zero_()
+        return ws
 
     def attend(self, q, block_table, lens, max_len, *, cu_seqlens=None, max_new=1, scale=None,
                out=None, lse=None, weights=None, workspace=None, status=None, stream=None):
@@ -1087,7 +1090,7 @@ class Cache8:
         need = kvx_evict8_workspace_bytes(a)
         if need == 0:
             raise KvxError(KVX_ERR_INVALID_ARG, "kvx_evict8_workspace_bytes")
-        return torch.zeros(need, dtype=torch.uint8, device=self.device)
+        return torch.empty(need, dtype=torch.uint8, device=self.device)
 
     def evict(self, weights, block_table, lens, dst_table, *, max_len, keep, sinks=0, recent=0,
               kept=None, kept_weights=None, new_lens=None, workspace=None, status=None,

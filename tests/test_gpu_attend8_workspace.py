@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import decode_reference as ref
+from cross_model_kv_transfer_gb300 import kvx
 from test_gpu_attend8 import compare, dev, make
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +88,32 @@ def test_a_window_and_then_single_tokens(d, bs, dtype, room):
         assert int(status.item()) == 0
         compare(out, lse, w[..., :max(lens)].contiguous(), want, dtype == torch.bfloat16, max(lens), new * G)
         assert not w[..., max(lens):].any()
+
+
+@pytest.mark.parametrize("G,new,d,dtype", [(8, 1, 128, torch.bfloat16), (4, 10, 128, torch.bfloat16),
+                                           (4, 70, 64, torch.bfloat16), (4, 3, 64, torch.float32),
+                                           (2, 20, 256, torch.bfloat16)])
+def test_only_the_first_1024_bytes_have_to_be_zero(G, new, d, dtype):
+    H, lens = 2, [900, 77]
+    c = make(H, G, d, 16, lens, [new, new], dtype, 71)
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], d ** -0.5)
+    ws = c["cache"].attend_workspace(ntok=2 * new, num_requests=2, q_heads=H * G, max_len=900, max_new=new,
+                                     dtype=dtype, weights=True)
+    assert not ws[:1024].any()
+    ws[1024:] = 0xFF
+    for _ in range(2):
+        call(c, lens, want, 2, new, H, G, dtype, ws, True)
+
+
+def test_the_rest_of_a_workspace_is_not_filled():
+    """It may be gigabytes: a call without a workspace would spend its time there."""
+    cache = kvx.Cache8.empty(4, 2, 128, 16)
+    make_ws = lambda: cache.attend_workspace(ntok=1, num_requests=1, q_heads=16, max_len=1 << 22, weights=True)
+    ws = make_ws()
+    at, size = ws.data_ptr(), ws.numel()
+    assert size > 1 << 28
+    ws.fill_(0xFF)
+    del ws
+    ws = make_ws()                        # the allocator gives the same memory again
+    assert (ws.data_ptr(), ws.numel()) == (at, size)
+    assert not ws[:1024].any() and (ws[1024:] == 0xFF).all()
