@@ -1005,15 +1005,24 @@ class Cache8:
         ``weights`` it has room for scores, up to 4 GB by ``max_len``; without,
         calls with weights run in it too and form their scores a second time."""
         import torch
+        return self._attend_scratch(torch.bfloat16 if dtype is None else dtype, ntok, num_requests, q_heads,
+                                    max_len, max_new, weights, None)
+
+    def _attend_scratch(self, dtype, ntok, num_requests, q_heads, max_len, max_new, weights, most_scores):
+        """A workspace, with room for scores unless that takes more than ``most_scores`` bytes."""
+        import torch
         a = Attend8Args()
         a.cache = Cache8Desc(*self._head, 1, self.k_codes.data_ptr())
-        a.dtype = _dtype_code(torch.bfloat16 if dtype is None else dtype)
+        a.dtype = _dtype_code(dtype)
         a.q_heads, a.ntok, a.num_requests = q_heads, ntok, num_requests
         a.max_new, a.max_len, a.scale = max_new, max_len, 1.0
         a.lens = a.cu_seqlens = self.k_codes.data_ptr()   # sizes only: never read
+        need = kvx_attend8_workspace_bytes(a)
         if weights:
             a.weights, a.weights_stride = self.k_scale.data_ptr(), max_len
-        need = kvx_attend8_workspace_bytes(a)
+            roomy = kvx_attend8_workspace_bytes(a)
+            if roomy == 0 or most_scores is None or roomy - need <= most_scores:
+                need = roomy
         if need == 0:
             raise KvxError(KVX_ERR_INVALID_ARG, "kvx_attend8_workspace_bytes")
         ws = torch.empty(need, dtype=torch.uint8, device=self.device)
@@ -1026,7 +1035,7 @@ class Cache8:
         of their requests (``lens`` [R], at most ``max_len``): query i of n sees
         slots up to lens - n + i.  Returns (out, lse [tokens][q_heads]).
         ``weights`` [R][heads][>= max_len] fp32 accumulates the attention weight
-        of each slot.  Scratch is allocated here unless ``workspace`` (from
+        of each slot.  Scratch (for scores at most 1 GB) is allocated here unless ``workspace`` (from
         ``attend_workspace``) is given."""
         dev, dt = self.device, q.dtype
         _on_device(dev)
@@ -1055,9 +1064,8 @@ class Cache8:
         if weights is not None:
             wptr, wstride = self._weights(weights, R)
         if workspace is None:
-            workspace = _on_stream(self.attend_workspace, stream, ntok=n, num_requests=R,
-                                   q_heads=hq, max_len=max_len, max_new=max_new, dtype=dt,
-                                   weights=weights is not None)
+            workspace = _on_stream(self._attend_scratch, stream, dt, n, R, hq, max_len, max_new,
+                                   weights is not None, 1 << 30)
         a = _pack_attend(*table, q.data_ptr(), out.data_ptr(), qs[0], qs[1], os_[0], os_[1], code,
                          hq, n, R, max_new, _int_table(cu_seqlens, "cu_seqlens", dev),
                          _int_table(lens, "lens", dev), max_len,

@@ -117,3 +117,20 @@ def test_the_rest_of_a_workspace_is_not_filled():
     ws = make_ws()                        # the allocator gives the same memory again
     assert (ws.data_ptr(), ws.numel()) == (at, size)
     assert not ws[:1024].any() and (ws[1024:] == 0xFF).all()
+
+
+def test_a_call_without_a_workspace_takes_a_gigabyte_for_scores_at_most():
+    c = make(1, 8, 128, 16, [300], [1], torch.bfloat16, 73)
+    q, table, lens = c["q"].cuda(), dev(c["table"]), dev([300])
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], [300], c["cu"], 128 ** -0.5)
+    taken = []
+    for bound in (1 << 20, 1 << 24, 1 << 26, 1 << 28):      # scores of 32 MB, 512 MB, 2 GB, 8 GB
+        w = torch.zeros((1, 1, bound), device="cuda")
+        torch.cuda.synchronize()
+        held = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        out, lse = c["cache"].attend(q, table, lens, bound, weights=w)
+        taken.append(torch.cuda.max_memory_allocated() - held)
+        compare(out, lse, w[..., :300].contiguous(), want, True, 300, 8)
+        del w
+    assert taken[0] < 1 << 26 and 1 << 29 <= taken[1] < 1 << 30 and max(taken[2:]) < 1 << 26
