@@ -589,7 +589,9 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 
     const bool seg_done = w.step + 1 == w.steps;
     if (seg_done || now + 1 == last) {
-      // join the warps, RC columns at a time
+      // join the warps, RC columns at a time.  Sums over the values are averages from here
+      // on, weighted with their sums of probabilities: below the largest value, which may
+      // be near the largest fp32.
       const bool whole = seg_done && w.step + 1 <= now - seg_first + 1;
       // where it goes: the result, or a partial one (first or last of the CTA)
       float *slot = p.partial + ((int64_t)blockIdx.x * 2 + (seg_first == first ? 0 : 1)) * C::kSlot;
@@ -611,10 +613,11 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float *row = red + (warp * C::RC + 2 * (t % (C::RC / 2)) + e) * C::ROWF;
+            const float inv = l[n][e] != 0.f ? (1.f / 16384.f) / l[n][e] : 0.f;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-              *reinterpret_cast<float2 *>(row + 16 * c + 2 * g) = make_float2(
-                  o[n][c][e] * (1.f / 16384.f) * vref, o[n][c][2 + e] * (1.f / 16384.f) * vref);
+              *reinterpret_cast<float2 *>(row + 16 * c + 2 * g) =
+                  make_float2(o[n][c][e] * inv * vref, o[n][c][2 + e] * inv * vref);
           }
         }
         __syncthreads();
@@ -624,16 +627,21 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
           float2 oo = make_float2(0.f, 0.f);
 #pragma unroll
           for (int v = 0; v < C::WARPS; ++v) mm = fmaxf(mm, red_m[v * C::COLS + col]);
+          float f[C::WARPS];
 #pragma unroll
           for (int v = 0; v < C::WARPS; ++v) {
-            const float f = ex2(red_m[v * C::COLS + col] - finite_or_0(mm));
+            f[v] = ex2(red_m[v * C::COLS + col] - finite_or_0(mm)) * red_l[v * C::COLS + col];
+            ll += f[v];
+          }
+          const float inv = ll != 0.f ? 1.f / ll : 0.f;
+#pragma unroll
+          for (int v = 0; v < C::WARPS; ++v) {
             const float2 y = *reinterpret_cast<const float2 *>(red + (v * C::RC + in) * C::ROWF + d);
-            ll += f * red_l[v * C::COLS + col];
-            oo.x += f * y.x;
-            oo.y += f * y.y;
+            oo.x += f[v] * inv * y.x;
+            oo.y += f[v] * inv * y.y;
           }
           if (whole) {
-            if (at < cols && d < a.d) store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, 0.f, ll);
+            if (at < cols && d < a.d) store_row(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, 0.f, ll);
           } else {
             *reinterpret_cast<float2 *>(slot + col * DP + d) = oo;
             if (d == 0) {
@@ -669,16 +677,21 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
             for (int c = 0; c < parts; ++c)
               mm = fmaxf(mm, __ldcg((c ? p1 + (int64_t)c * 2 * C::kSlot : p0) + C::COLS * DP + col));
             mm = finite_or_0(mm);
+            const auto share = [&](const float *part) {
+              return ex2(__ldcg(part + C::COLS * DP + col) - mm) * __ldcg(part + C::COLS * (DP + 1) + col);
+            };
+#pragma unroll 8
+            for (int c = 0; c < parts; ++c) ll += share(c ? p1 + (int64_t)c * 2 * C::kSlot : p0);
+            const float inv = ll != 0.f ? 1.f / ll : 0.f;
 #pragma unroll 8
             for (int c = 0; c < parts; ++c) {
               const float *part = c ? p1 + (int64_t)c * 2 * C::kSlot : p0;
-              const float f = ex2(__ldcg(part + C::COLS * DP + col) - mm);
+              const float f = share(part) * inv;
               const float2 y = __ldcg(reinterpret_cast<const float2 *>(part + col * DP + d));
-              ll += __ldcg(part + C::COLS * (DP + 1) + col) * f;
               oo.x += y.x * f;
               oo.y += y.y * f;
             }
-            store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, 0.f, ll);
+            store_row(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, 0.f, ll);
           }
         }
       }

@@ -80,22 +80,27 @@ __device__ __forceinline__ void store_lse(const AttendParams &p, int64_t g, int 
 }
 // The probability of a score, rounded as the attention kernel rounded it.
 __device__ __forceinline__ float probability(float score, float2 lse) { return ex2((score - lse.x) - lse.y); }
-// Two dimensions of a finished row, whose sums o and l are relative to exp2(m + shift);
-// its log-sum-exp with the first.
-__device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int hq, int d, float2 o, float m,
+// Two dimensions of a finished row, and with the first its log-sum-exp, of a sum l
+// relative to exp2(m + shift).
+__device__ __forceinline__ void store_row(const AttendParams &p, int64_t g, int hq, int d, float2 o, float m,
                                           float shift, float l) {
-  const float inv = l != 0.f ? 1.f / l : 0.f;
   const int64_t to = g * p.ot + hq * p.oh + d;
   if (p.bf16) {
     __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + to;
-    out[0] = __float2bfloat16_rn(o.x * inv);
-    out[1] = __float2bfloat16_rn(o.y * inv);
+    out[0] = __float2bfloat16_rn(o.x);
+    out[1] = __float2bfloat16_rn(o.y);
   } else {
     float *out = reinterpret_cast<float *>(p.out) + to;
-    out[0] = o.x * inv;
-    out[1] = o.y * inv;
+    out[0] = o.x;
+    out[1] = o.y;
   }
   if (d == 0) store_lse(p, g, hq, m, shift, l);
+}
+// The same of sums o that are relative to exp2(m + shift) too.
+__device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int hq, int d, float2 o, float m,
+                                          float shift, float l) {
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  store_row(p, g, hq, d, make_float2(o.x * inv, o.y * inv), m, shift, l);
 }
 // The most queries that one request of the call can have: max_new may be any bound.
 inline int most_new(const kvx_attend8_args *a) {

@@ -1254,10 +1254,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = (int)(sb * a.bs + off);
         const float kscale = page >= 0 ? __ldg(a.ks + sb) : 0.f, vscale = page >= 0 ? __ldg(a.vs + sb) : 0.f;
         const unsigned mask = __ballot_sync(~0u, page >= 0);
-        // the tile's largest value scale, rounded up to a power of two 2^e; scales
-        // below 2^-96 count as that, their values vanish beside any other
+        // the tile's largest value scale, rounded up to a power of two 2^e.  Not below
+        // 2^-96: such values vanish beside any other.  Not above 2^126: ex2 gives 0 for
+        // 2^-127, and codes whose values are finite leave f16 room for the rest.
         const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(vscale));
-        const int e = max((int)(most >> 23) + ((most & 0x7fffff) != 0), 127 - 96);
+        const int e = min(max((int)(most >> 23) + ((most & 0x7fffff) != 0), 127 - 96), 127 + 126);
         const int per = p.box / 4, boxes = kTile / p.box;     // lanes a box, boxes
         const int from = __shfl_sync(~0u, row, lane < boxes ? lane * per : 0);
         const bool there = lane < boxes && (mask >> (lane * per) & 1);
@@ -1730,7 +1731,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
           }
         }
         // probabilities times the value scale, and sums without it
-        const float without = ex2(-lv);
+        const float root = ex2(-0.5f * lv), without = root * root;   // ex2 gives 0 for 2^-127
         uint32_t h[NC / 2];
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {

@@ -631,7 +631,8 @@ kvx_status kvx_rope_apply(const kvx_rope *rope, const kvx_rope_args *args, void 
  * amax <= 448 * 2^e.  e4m3 keeps its relative precision over its normal range,
  * so nothing is lost against an arbitrary scale but up to one bit of range, and
  * a block whose scale grows later re-scales its older codes exactly (but for
- * those that become subnormal).  kvx_attend8 takes any positive finite scale. */
+ * those that become subnormal).  kvx_attend8 takes any positive finite scale; it may
+ * count value scales below 2^-96 as 2^-96. */
 typedef struct {
   void *k_codes, *v_codes;  /* [num_blocks][heads][block_size][head_dim], 16-byte
                                aligned                                        */

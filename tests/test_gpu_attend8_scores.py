@@ -257,3 +257,18 @@ def test_more_columns_than_shared_memory_holds_log_sum_exps_for():
                                  weights=w)
     want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], [n], c["cu"], 0.125)
     compare(out, lse, w, want, False, n, new * G)
+
+
+@pytest.mark.parametrize("exp", [-90, 100, 126, 127])
+@pytest.mark.parametrize("H,G,new,d,bs,dtype", WEIGHED)
+def test_value_scales_at_the_ends_of_their_range(H, G, new, d, bs, dtype, exp):
+    """Values up to 2^127 (codes up to 1 under the largest scales) and down to 2^-96."""
+    lens = [300, 90]
+    c = make(H, G, d, bs, lens, [new, new], dtype, 19)
+    v = c["cache"].v_codes
+    small = (v & 0x80) | (v & 0x7F).clamp(max=0x38)
+    v.copy_(torch.where((v & 0x7F) == 0x7F, v, small))            # slots that nobody holds keep their NaN
+    c["cache"].v_scale.fill_(2.0 ** exp)
+    c["rv"] = ref.RefCache(v.cpu().numpy(), c["cache"].v_scale.cpu().numpy())
+    out, lse, want = attend(c, lens, new, G, d ** -0.5)
+    compare(out, lse, None, want, dtype == torch.bfloat16, 300, 1)
