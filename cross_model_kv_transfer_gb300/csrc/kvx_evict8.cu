@@ -421,6 +421,11 @@ kvx_status check(const kvx_evict8_args *a) {
   return KVX_OK;
 }
 
+bool overlap(const void *a, int64_t a_words, const void *b, int64_t b_words) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + 4 * (uintptr_t)b_words && y < x + 4 * (uintptr_t)a_words;
+}
+
 }  // namespace
 
 extern "C" size_t kvx_evict8_workspace_bytes(const kvx_evict8_args *a) {
@@ -432,6 +437,12 @@ extern "C" kvx_status kvx_evict8(const kvx_evict8_args *a, void *stream) {
   if (!a->workspace || !aligned_to(a->workspace, 256) || a->workspace_bytes < kvx_evict8_workspace_bytes(a))
     return KVX_ERR_INVALID_ARG;
   const kvx_cache8 &c = a->cache;
+  // results are written while other CTAs still read lengths and weights
+  const int64_t lists = (int64_t)a->num_requests * c.heads;
+  if (overlap(a->lens, a->num_requests, a->new_lens, a->num_requests) ||
+      (a->kept_weights && a->max_len > 0 &&
+       overlap(a->weights, (lists - 1) * a->weights_stride + a->max_len, a->kept_weights, lists * a->keep)))
+    return KVX_ERR_INVALID_ARG;
   EvictParams p;
   p.codes[0] = (uint8_t *)c.k_codes;
   p.codes[1] = (uint8_t *)c.v_codes;

@@ -747,8 +747,9 @@ typedef struct {
   const float *weights;     /* [R][heads][weights_stride] accumulated weights */
   int64_t weights_stride;   /* >= max_len                                     */
   int32_t *kept;            /* [R][heads][keep] kept slots, ascending, then -1 */
-  float *kept_weights;      /* [R][heads][keep] their weights, then 0; or NULL */
-  int32_t *new_lens;        /* [R] min(lens, keep)                            */
+  float *kept_weights;      /* [R][heads][keep] their weights, then 0, which
+                               overlap no weights; or NULL                    */
+  int32_t *new_lens;        /* [R] min(lens, keep); overlaps no lens          */
   void *workspace;          /* kvx_evict8_workspace_bytes(), 256-byte aligned */
   size_t workspace_bytes;
   uint32_t *status;

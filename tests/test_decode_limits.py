@@ -3,7 +3,7 @@ request's queries, sizes of workspaces (no GPU needed: nothing is enqueued)."""
 import pytest
 
 from cross_model_kv_transfer_gb300 import kvx
-from test_decode_abi import P, attend_args, cache_desc
+from test_decode_abi import P, attend_args, cache_desc, evict_args
 
 
 @pytest.mark.parametrize("dtype", [kvx.KVX_BF16, kvx.KVX_F32])
@@ -51,3 +51,14 @@ def test_a_workspace_of_larger_calls_is_large_enough_for_every_smaller_one():
     window = attend_args(cache, ntok=16 * 64, max_new=64, **sizes).workspace_bytes
     for new in (1, 2, 8, 16):
         assert attend_args(cache, ntok=16 * new, max_new=new, **sizes).workspace_bytes <= window
+
+
+def test_evictions_in_place_are_refused():
+    """Other CTAs still read the lengths and weights when the results are written."""
+    Q = P + (1 << 20)
+    ok = dict(lens=P, new_lens=P + 8, weights=Q, kept_weights=Q + 4 * (3 * 64 + 64), weights_stride=64, max_len=64)
+    for over in (dict(new_lens=P), dict(new_lens=P + 4), dict(new_lens=P - 4), dict(kept_weights=Q),
+                 dict(kept_weights=Q + 4 * 64), dict(kept_weights=Q + 4 * (3 * 64 + 63)),
+                 dict(kept_weights=Q - 4 * (4 * 32 - 1))):
+        a = evict_args(**dict(ok, **over))
+        assert a.workspace_bytes > 0 and kvx.kvx_evict8(a, None) == kvx.KVX_ERR_INVALID_ARG, over
