@@ -908,6 +908,7 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   const kvx_cache8 &c = a->cache;
   const int size = a->dtype == KVX_BF16 ? 2 : 4;
   if (!a->q || !a->out || !aligned_to(a->q, size) || !aligned_to(a->out, size)) return KVX_ERR_INVALID_ARG;
+  if (a->weights && a->out == a->q) return KVX_ERR_INVALID_ARG;   // scores may be formed again
   const size_t least = kvx_attend8_tc_supports(a) ? kvx_attend8_tc_least_bytes(a) : shape_of(a).scores;
   if (!a->workspace || !aligned_to(a->workspace, 256) || a->workspace_bytes < least)
     return KVX_ERR_INVALID_ARG;

@@ -679,7 +679,8 @@ kvx_status kvx_cache8_write(const kvx_cache8_write_args *args, void *stream);
 typedef struct {
   kvx_cache8 cache;
   const void *q;            /* [ntok][q_heads][d] rotated queries             */
-  void *out;                /* [ntok][q_heads][d]                             */
+  void *out;                /* [ntok][q_heads][d]; may be q (with its strides)
+                               without weights only                          */
   int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
   int32_t dtype;            /* kvx_dtype of q and out                         */
   int32_t q_heads;          /* a multiple of cache.heads; query head i reads KV

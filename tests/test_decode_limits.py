@@ -62,3 +62,10 @@ def test_evictions_in_place_are_refused():
                  dict(kept_weights=Q - 4 * (4 * 32 - 1))):
         a = evict_args(**dict(ok, **over))
         assert a.workspace_bytes > 0 and kvx.kvx_evict8(a, None) == kvx.KVX_ERR_INVALID_ARG, over
+
+
+def test_attention_in_place_is_refused_with_weights():
+    """Weights may need the queries again when the outputs are written already."""
+    sizes = dict(q=P, out=P, weights=P, weights_stride=64)
+    for dtype in (kvx.KVX_BF16, kvx.KVX_F32):
+        assert kvx.kvx_attend8(attend_args(dtype=dtype, **sizes), None) == kvx.KVX_ERR_INVALID_ARG

@@ -134,3 +134,17 @@ def test_a_call_without_a_workspace_takes_a_gigabyte_for_scores_at_most():
         compare(out, lse, w[..., :300].contiguous(), want, True, 300, 8)
         del w
     assert taken[0] < 1 << 26 and 1 << 29 <= taken[1] < 1 << 30 and max(taken[2:]) < 1 << 26
+
+
+@pytest.mark.parametrize("G,new,d,dtype", [(8, 1, 128, torch.bfloat16), (4, 10, 128, torch.bfloat16),
+                                           (4, 140, 128, torch.bfloat16), (4, 3, 64, torch.float32),
+                                           (2, 40, 256, torch.bfloat16)])
+def test_outputs_over_the_queries(G, new, d, dtype):
+    H, R = 2, 30
+    lens = [new + (61 * r) % 700 for r in range(R)]
+    c = make(H, G, d, 16, lens, [new] * R, dtype, 79)
+    want = ref.attend(c["q"].double().numpy(), c["rk"], c["rv"], c["table"], lens, c["cu"], d ** -0.5)
+    q = c["q"].cuda()
+    out, lse = c["cache"].attend(q, dev(c["table"]), dev(lens), max(lens), cu_seqlens=dev(c["cu"]), max_new=new, out=q)
+    assert out is q
+    compare(out, lse, None, want, dtype == torch.bfloat16, max(lens), new * G)
