@@ -85,6 +85,8 @@ struct SplitCfg {
   static constexpr size_t kAgainSmem = kAgainTile * WARPS + (kQInSmem ? kQ : 0) + COLS * 4;
 };
 
+constexpr float kRoom = 24.f, kUnit = 0x1p-38f;   // 2^-kRoom over the 2^14 that probabilities carry
+
 struct SplitParams {
   AttendParams a;
   int groups;            // column groups of max_new queries
@@ -421,6 +423,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
   int limit[NT][2];          // last slot that they see
   // running maxima: as scores without their column's factor, and with it
   float mx[NT][2], m[NT][2], l[NT][2], o[NT][CH][4];
+  bool far = false;                // one of the warp's maxima is
   float vref = 0.f, vinv = 0.f;   // largest value scale, and 2^14 over it
   int limits = 0;                 // the lowest of the limits
   int stage = 0;
@@ -434,6 +437,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
       // below 2^-112 a scale is treated as that: 2^14 over it stays finite
       vref = 0x1p-112f;
       vinv = 0x1p126f;
+      far = false;
       limits = w.len - w.fresh + col0 / a.G;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -530,6 +534,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
               mx[n][e] = top[n][e];
               const float mm = finite_or_0(__fmul_rn(top[n][e], cs[n][e])), down = ex2(m[n][e] - mm);
               m[n][e] = top[n][e] > -INFINITY ? mm : -INFINITY;
+              far = far || fabsf(mm) > kFar;
               l[n][e] *= down;
 #pragma unroll
               for (int c = 0; c < CH; ++c) {
@@ -537,6 +542,23 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
                 o[n][c][2 + e] *= down * vdown;
               }
             }
+        }
+        // Far scores are rounded before the maximum, which is a rounded score, is
+        // subtracted: none comes out above it, however large both are.
+        if (__any_sync(~0u, far)) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[i][n][e] = __fmul_rn(s[i][n][e], cs[n][e & 1]) - finite_or_0(m[n][e & 1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[i][n][e] = fmaf(s[i][n][e], cs[n][e & 1], -finite_or_0(m[n][e & 1]));
         }
         // P^T: probabilities times their value scale, transposed between the lanes
         uint32_t pb[MT][NT][PARTS][2];
@@ -547,10 +569,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
             const float f = vsc[i][half] * vinv;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              // a score is rounded before the maximum, which is a rounded score, is
-              // subtracted: none comes out above it, however large both are
-              const float p0 = ex2(__fmul_rn(s[i][n][2 * half], cs[n][0]) - finite_or_0(m[n][0]));
-              const float p1 = ex2(__fmul_rn(s[i][n][2 * half + 1], cs[n][1]) - finite_or_0(m[n][1]));
+              const float p0 = ex2(s[i][n][2 * half]), p1 = ex2(s[i][n][2 * half + 1]);
               l[n][0] += p0;
               l[n][1] += p1;
               float y0 = p0 * f, y1 = p1 * f;
@@ -589,9 +608,8 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 
     const bool seg_done = w.step + 1 == w.steps;
     if (seg_done || now + 1 == last) {
-      // join the warps, RC columns at a time.  Sums over the values are averages from here
-      // on, weighted with their sums of probabilities: below the largest value, which may
-      // be near the largest fp32.
+      // join the warps, RC columns at a time.  From here on sums carry the values' scale,
+      // which may be near the largest fp32, and 2^-kRoom: room for 2^kRoom slots
       const bool whole = seg_done && w.step + 1 <= now - seg_first + 1;
       // where it goes: the result, or a partial one (first or last of the CTA)
       float *slot = p.partial + ((int64_t)blockIdx.x * 2 + (seg_first == first ? 0 : 1)) * C::kSlot;
@@ -603,7 +621,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
           for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(~0u, l[n][e], off);
           if (g == 0) {
             red_m[warp * C::COLS + 8 * n + 2 * t + e] = m[n][e];
-            red_l[warp * C::COLS + 8 * n + 2 * t + e] = l[n][e];
+            red_l[warp * C::COLS + 8 * n + 2 * t + e] = l[n][e] * (kUnit * 16384.f);
           }
         }
 #pragma unroll
@@ -613,11 +631,10 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float *row = red + (warp * C::RC + 2 * (t % (C::RC / 2)) + e) * C::ROWF;
-            const float inv = l[n][e] != 0.f ? (1.f / 16384.f) / l[n][e] : 0.f;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
               *reinterpret_cast<float2 *>(row + 16 * c + 2 * g) =
-                  make_float2(o[n][c][e] * inv * vref, o[n][c][2 + e] * inv * vref);
+                  make_float2(o[n][c][e] * kUnit * vref, o[n][c][2 + e] * kUnit * vref);
           }
         }
         __syncthreads();
@@ -627,21 +644,16 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
           float2 oo = make_float2(0.f, 0.f);
 #pragma unroll
           for (int v = 0; v < C::WARPS; ++v) mm = fmaxf(mm, red_m[v * C::COLS + col]);
-          float f[C::WARPS];
 #pragma unroll
           for (int v = 0; v < C::WARPS; ++v) {
-            f[v] = ex2(red_m[v * C::COLS + col] - finite_or_0(mm)) * red_l[v * C::COLS + col];
-            ll += f[v];
-          }
-          const float inv = ll != 0.f ? 1.f / ll : 0.f;
-#pragma unroll
-          for (int v = 0; v < C::WARPS; ++v) {
+            const float f = ex2(red_m[v * C::COLS + col] - finite_or_0(mm));
             const float2 y = *reinterpret_cast<const float2 *>(red + (v * C::RC + in) * C::ROWF + d);
-            oo.x += f[v] * inv * y.x;
-            oo.y += f[v] * inv * y.y;
+            ll += f * red_l[v * C::COLS + col];
+            oo.x += f * y.x;
+            oo.y += f * y.y;
           }
           if (whole) {
-            if (at < cols && d < a.d) store_row(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, 0.f, ll);
+            if (at < cols && d < a.d) store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, kRoom, ll);
           } else {
             *reinterpret_cast<float2 *>(slot + col * DP + d) = oo;
             if (d == 0) {
@@ -677,21 +689,16 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
             for (int c = 0; c < parts; ++c)
               mm = fmaxf(mm, __ldcg((c ? p1 + (int64_t)c * 2 * C::kSlot : p0) + C::COLS * DP + col));
             mm = finite_or_0(mm);
-            const auto share = [&](const float *part) {
-              return ex2(__ldcg(part + C::COLS * DP + col) - mm) * __ldcg(part + C::COLS * (DP + 1) + col);
-            };
-#pragma unroll 8
-            for (int c = 0; c < parts; ++c) ll += share(c ? p1 + (int64_t)c * 2 * C::kSlot : p0);
-            const float inv = ll != 0.f ? 1.f / ll : 0.f;
 #pragma unroll 8
             for (int c = 0; c < parts; ++c) {
               const float *part = c ? p1 + (int64_t)c * 2 * C::kSlot : p0;
-              const float f = share(part) * inv;
+              const float f = ex2(__ldcg(part + C::COLS * DP + col) - mm);
               const float2 y = __ldcg(reinterpret_cast<const float2 *>(part + col * DP + d));
+              ll += __ldcg(part + C::COLS * (DP + 1) + col) * f;
               oo.x += y.x * f;
               oo.y += y.y * f;
             }
-            store_row(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, 0.f, ll);
+            store_out(a, w.beg + at / a.G, h * a.G + at % a.G, d, oo, mm, kRoom, ll);
           }
         }
       }

@@ -40,6 +40,10 @@ using kvx8::AttendParams;
 // bytes for anything else, so that one workspace serves calls of different sizes and forms.
 constexpr size_t kWorkspaceHead = 1024;
 
+// Scores (base 2) beyond this are far: their own half ulp, 2^-12 here, counts in exponents
+// that are their differences to an unrounded number.
+constexpr float kFar = 4096.f;
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // The request's length (0 where it is out of bounds).
@@ -80,28 +84,24 @@ __device__ __forceinline__ void store_lse(const AttendParams &p, int64_t g, int 
 }
 // The probability of a score, rounded as the attention kernel rounded it.
 __device__ __forceinline__ float probability(float score, float2 lse) { return ex2((score - lse.x) - lse.y); }
-// Two dimensions of a finished row, and with the first its log-sum-exp, of a sum l
-// relative to exp2(m + shift).
-__device__ __forceinline__ void store_row(const AttendParams &p, int64_t g, int hq, int d, float2 o, float m,
-                                          float shift, float l) {
-  const int64_t to = g * p.ot + hq * p.oh + d;
-  if (p.bf16) {
-    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + to;
-    out[0] = __float2bfloat16_rn(o.x);
-    out[1] = __float2bfloat16_rn(o.y);
-  } else {
-    float *out = reinterpret_cast<float *>(p.out) + to;
-    out[0] = o.x;
-    out[1] = o.y;
-  }
-  if (d == 0) store_lse(p, g, hq, m, shift, l);
-}
-// The same of sums o that are relative to exp2(m + shift) too.
+// Two dimensions of a finished row, whose sums o and l are relative to exp2(m + shift);
+// its log-sum-exp with the first.
 __device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int hq, int d, float2 o, float m,
                                           float shift, float l) {
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  store_row(p, g, hq, d, make_float2(o.x * inv, o.y * inv), m, shift, l);
+  const int64_t to = g * p.ot + hq * p.oh + d;
+  if (p.bf16) {
+    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + to;
+    out[0] = __float2bfloat16_rn(o.x * inv);
+    out[1] = __float2bfloat16_rn(o.y * inv);
+  } else {
+    float *out = reinterpret_cast<float *>(p.out) + to;
+    out[0] = o.x * inv;
+    out[1] = o.y * inv;
+  }
+  if (d == 0) store_lse(p, g, hq, m, shift, l);
 }
+
 // The most queries that one request of the call can have: max_new may be any bound.
 inline int most_new(const kvx_attend8_args *a) {
   return (int)(a->max_new < a->ntok ? a->max_new : a->ntok > 1 ? a->ntok : 1);

@@ -515,8 +515,7 @@ __device__ __forceinline__ uint64_t probabilities(uint32_t *out, const uint32_t 
   top = fmaxf(t0, t1);
   return sum;
 }
-// Beyond this (base 2) the maximum's own half ulp counts in an exponent.
-constexpr float kFar = 4096.f;
+__device__ __forceinline__ bool is_far(float m) { return m > -INFINITY && fabsf(m) > kFar; }
 // 32 of a row's scores from tensor memory, each rounded once to fp32.
 __device__ __forceinline__ void rounded_scores(uint32_t (&s)[32], uint32_t col, const float4 *scale, uint32_t mask, int seen, float cs) {
   float f[8];
@@ -560,12 +559,34 @@ __device__ __noinline__ float far_probabilities(uint32_t col, const float4 *scal
   tc_wait_st();
   return sum;
 }
+// The probabilities exp2(score + add) of a half tile whose scores are near, the same way.
+__device__ __noinline__ float near_probabilities(uint32_t col, const float4 *scale, uint32_t mask, int seen, float cs,
+                                                 float add) {
+  uint64_t sum = pair(0.f, 0.f);
+  const uint64_t a2 = pair(add, add);
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t s[32], out[16];
+    float f[8], top = 0.f;
+    tc_ld32(col + 32 * c, s);
+    tc_wait_ld32(s);
+    columns<true>(s, f, scale + 2 * c, mask >> (8 * c), seen - 32 * c);
+    sum = probabilities<true>(out, s, f, cs, a2, sum, top);
+    tc_st16(col + 16 * c, out);
+  }
+  tc_wait_st();
+  float s0, s1;
+  unpair(sum, s0, s1);
+  return s0 + s1;
+}
 // A half tile of a row: probabilities over the scores they come from, the row's
 // running maximum (lazily) and sum.  What is subtracted from a score plus its tile's
-// value scale is m + shift: a score as it was rounded, and the value scale's exponent
-// of its tile.  They are kept apart because their sum would be rounded: from 2^25 on by
-// more than f16 has room for.  `raise(down)` is called by whole warps when a maximum
-// has to rise: it scales down what the rows have so far.
+// value scale is m + shift: the largest such sum and 0, or where it is far a score as it was
+// rounded and the value scale's exponent of its tile, because the sum of those would be
+// rounded: from 2^25 on by more than f16 has room for.  `raise(down)` is called by whole
+// warps when a maximum has to rise: it scales down what the rows have so far.  What it
+// takes then is in functions of their own, so that it costs the others no registers (in a
+// loop around the code below a prompt of 8192 tokens takes 1266 us, this way 1134).
 template <bool MASK, class F>
 __device__ __forceinline__ bool softmax_half(uint32_t col, const float4 *scale, uint32_t mask, int seen, float cs, float ref,
                                              float &m, float &shift, float &l, F raise) {
@@ -592,11 +613,19 @@ __device__ __forceinline__ bool softmax_half(uint32_t col, const float4 *scale, 
     tc_wait_st();
     return true;
   }
-  // seldom: the probabilities again, from scores rounded before the maximum, which is one
-  // of them, is subtracted.  That is exact for all scores near it, so none is above kBias
-  // now however large they are.
+  // seldom: the maximum rises, and the probabilities again.  Where it and the scores are
+  // near they come from the same sums, which are within 2^-10 of kBias at most then.
   const uint32_t in = MASK ? mask : 0xffffu;
   const int last = MASK ? seen : kTile;
+  if (!__any_sync(~0u, is_far(m) || is_far(top) || fabsf(add) > kFar)) {
+    const float mm = fmaxf(m, top - kBias + finite_or_0(m)), down = ex2(m - finite_or_0(mm));
+    if (!raise(down)) return false;
+    m = mm;
+    l = l * down + near_probabilities(col, scale, in, last, cs, kBias + (ref - shift) - finite_or_0(m)) * ex2(-ref);
+    return true;
+  }
+  // Far: from scores rounded before the maximum, which is one of them, is subtracted.  That
+  // is exact for all scores near it, so none is above kBias however large they are.
   const float most = largest_score(col, scale, in, last, cs);
   const float by = (most - finite_or_0(m)) + (ref - shift);
   const bool rises = m == -INFINITY ? most > -INFINITY : by > 0.f;
@@ -730,8 +759,48 @@ __device__ __noinline__ void keep_scores(uint32_t col, float *to, const float4 *
   }
 }
 
-// A part's sums are relative to exp2(m + shift) of its row: is a + sa above b + sb?
+// A part's sums are relative to exp2 of its row's m + shift, which is left as one number
+// where m is not far, as two where it is.
+__device__ __forceinline__ void leave_part(float *tops, int rows, int row, float m, float shift, float l) {
+  const bool far = is_far(m);
+  tops[row] = far ? m : m + shift;
+  tops[rows + row] = far ? shift : 0.f;
+  tops[2 * rows + row] = l;
+}
+// Is a + sa above b + sb?
 __device__ __forceinline__ bool above(float a, float sa, float b, float sb) { return (a - b) + (sa - sb) > 0.f; }
+// A warp joins the parts of a row, of which some are far.
+template <class G>
+__device__ __forceinline__ void join_far(const TcParams &p, int c0, int parts, int row, int64_t tok, int hq) {
+  const int lane = threadIdx.x % 32;
+  float mm = -INFINITY, sh = 0.f, ll = 0.f;
+  float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int c = 0; c < parts; ++c) {
+    const int64_t cta = c0 + c / G::PARTS;
+    const float *part = p.partial + ((cta * 2 + (c < G::PARTS)) * G::PARTS + c % G::PARTS) * (int64_t)p.part_size;
+    const float *tops = part + p.slot_rows * kD + row;
+    const float pm = __ldcg(tops), ps = __ldcg(tops + p.slot_rows), pl = __ldcg(tops + 2 * p.slot_rows);
+    const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + row * kD) + lane);
+    const bool own = above(pm, ps, mm, sh);
+    const float now = finite_or_0(own ? pm : mm), by = own ? ps : sh;
+    const float f0 = ex2((mm - now) + (sh - by)), f1 = ex2((pm - now) + (ps - by));
+    mm = own ? pm : mm;
+    sh = by;
+    ll = ll * f0 + pl * f1;
+    oo = make_float4(oo.x * f0 + y.x * f1, oo.y * f0 + y.y * f1, oo.z * f0 + y.z * f1, oo.w * f0 + y.w * f1);
+  }
+  if (lane * 4 >= p.a.d) return;
+  store_out(p.a, tok, hq, lane * 4, make_float2(oo.x, oo.y), mm, sh, ll);
+  store_out(p.a, tok, hq, lane * 4 + 2, make_float2(oo.z, oo.w), mm, sh, ll);
+}
+template <class G>
+__device__ __noinline__ void join_far_rows(const TcParams &p, const TcWalk &w, int c0, int parts, int first, int stride, int rows) {
+  for (int k = first; k < rows; k += stride) {
+    const int64_t row = (int64_t)w.group * G::ROWS + k;
+    join_far<G>(p, c0, parts, k, w.beg + row / p.a.G, w.h * p.a.G + (int)(row % p.a.G));
+  }
+}
 // Join the parts of an item that CTAs c0 .. c0 + ctas - 1 left: rows first, first +
 // stride, ... of the warp.  A CTA keeps parts of an item that others began, and of
 // one that it began.  The parts' maxima and totals by the lanes, 32 parts at a time,
@@ -745,48 +814,38 @@ __device__ __noinline__ void join_rows(const TcParams &p, const TcWalk &w, int c
     return p.partial + ((cta * 2 + (c < G::PARTS)) * G::PARTS + c % G::PARTS) * (int64_t)p.part_size;
   };
   for (int r0 = first; r0 < rows; r0 += stride * B) {
-    float mm[B], sh[B], ll[B], f[B];
+    float mm[B], ll[B], f[B];
     float4 oo[B];
     int rr[B];
+    bool far = false;
 #pragma unroll
     for (int k = 0; k < B; ++k) {
       rr[k] = min(r0 + k * stride, rows - 1);   // a row beyond is formed twice
       mm[k] = -INFINITY;
-      sh[k] = 0.f;
       ll[k] = 0.f;
       oo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int at = 0; at < parts; at += 32) {
       const float *own = part_at(min(at + lane, parts - 1)) + p.slot_rows * kD;
-      float pm[B], ps[B], pl[B];
+      float pm[B], pl[B];
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         pm[k] = __ldcg(own + rr[k]);
-        ps[k] = __ldcg(own + p.slot_rows + rr[k]);
         pl[k] = __ldcg(own + 2 * p.slot_rows + rr[k]);
       }
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         if (at + lane >= parts) {
           pm[k] = -INFINITY;
-          ps[k] = 0.f;
           pl[k] = 0.f;
         }
-        const bool own_above = above(pm[k], ps[k], mm[k], sh[k]);
-        float top = own_above ? pm[k] : mm[k], shift = own_above ? ps[k] : sh[k];
+        far = far || is_far(pm[k]);
+        float top = fmaxf(mm[k], pm[k]);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          const float y = __shfl_xor_sync(~0u, top, o), z = __shfl_xor_sync(~0u, shift, o);
-          const bool other = above(y, z, top, shift);
-          top = other ? y : top;
-          shift = other ? z : shift;
-        }
-        top = __shfl_sync(~0u, top, 0);       // equal sums of unequal terms
-        shift = __shfl_sync(~0u, shift, 0);
-        const float down = ex2((mm[k] - finite_or_0(top)) + (sh[k] - shift));
-        f[k] = ex2((pm[k] - finite_or_0(top)) + (ps[k] - shift));
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        const float down = ex2(mm[k] - finite_or_0(top));
+        f[k] = ex2(pm[k] - finite_or_0(top));
         mm[k] = top;
-        sh[k] = shift;
         float sum = pl[k] * f[k];
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -810,13 +869,17 @@ __device__ __noinline__ void join_rows(const TcParams &p, const TcWalk &w, int c
         }
       }
     }
+    if (__any_sync(~0u, far)) {     // seldom: from the start, by both numbers of the parts
+      join_far_rows<G>(p, w, c0, parts, r0, stride, rows);
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < B; ++k) {
       const int64_t row = (int64_t)w.group * G::ROWS + rr[k], tok = w.beg + row / a.G;
       const int hq = w.h * a.G + (int)(row % a.G);
       if (lane * 4 >= a.d) continue;
-      store_out(a, tok, hq, lane * 4, make_float2(oo[k].x, oo[k].y), mm[k], sh[k], ll[k]);
-      store_out(a, tok, hq, lane * 4 + 2, make_float2(oo[k].z, oo[k].w), mm[k], sh[k], ll[k]);
+      store_out(a, tok, hq, lane * 4, make_float2(oo[k].x, oo[k].y), mm[k], 0.f, ll[k]);
+      store_out(a, tok, hq, lane * 4 + 2, make_float2(oo[k].z, oo[k].w), mm[k], 0.f, ll[k]);
     }
   }
 }
@@ -842,8 +905,9 @@ __device__ __forceinline__ void note_split(const TcParams &p, const Share &s) {
 }
 // The items that several CTAs worked on: block x looks after the one that CTA x + 1
 // noted, block y after a slice of its rows.
+// Three blocks an SM: its loads wait long (after a prompt of 2048 tokens 15 us, two 19).
 template <class G>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcParams p) {
+__global__ void __launch_bounds__(256, 3) join_kernel(const __grid_constant__ TcParams p) {
   let_next_kernel_start();
   wait_for_kernel_before();
   const Split x = p.splits[blockIdx.x + 1];
@@ -857,61 +921,57 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcPar
 // The same with a block for a row, whose warps share the parts: few rows, many parts.
 template <class G>
 __global__ void __launch_bounds__(256) join_row_kernel(const __grid_constant__ TcParams p) {
-  __shared__ float top[8], shift[8], sum[8];
+  __shared__ float top[8], sum[8];
   __shared__ float4 part_sum[8][32];
   let_next_kernel_start();
   wait_for_kernel_before();
   const Split x = p.splits[blockIdx.x + 1];
   const int row = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32, parts = x.ctas * G::PARTS;
   if (row >= x.rows || parts == 0) return;
-  float mm = -INFINITY, sh = 0.f, ll = 0.f;
+  float mm = -INFINITY, ll = 0.f;
   float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool far = false;
 #pragma unroll 5
   for (int c = warp; c < parts; c += 8) {
     const int64_t cta = x.c0 + c / G::PARTS;
     const float *part = p.partial + ((cta * 2 + (c < G::PARTS)) * G::PARTS + c % G::PARTS) * (int64_t)p.part_size;
-    const float pm = __ldcg(part + p.slot_rows * kD + row), ps = __ldcg(part + p.slot_rows * (kD + 1) + row),
-                pl = __ldcg(part + p.slot_rows * (kD + 2) + row);
+    const float pm = __ldcg(part + p.slot_rows * kD + row), pl = __ldcg(part + p.slot_rows * (kD + 2) + row);
     const float4 y = __ldcg(reinterpret_cast<const float4 *>(part + row * kD) + lane);
-    const bool own = above(pm, ps, mm, sh);
-    const float now = finite_or_0(own ? pm : mm), by = own ? ps : sh;
-    const float f0 = ex2((mm - now) + (sh - by)), f1 = ex2((pm - now) + (ps - by));
-    mm = own ? pm : mm;
-    sh = by;
+    const float now = fmaxf(mm, pm), f0 = ex2(mm - finite_or_0(now)), f1 = ex2(pm - finite_or_0(now));
+    far = far || is_far(pm);
+    mm = now;
     ll = ll * f0 + pl * f1;
     oo = make_float4(oo.x * f0 + y.x * f1, oo.y * f0 + y.y * f1, oo.z * f0 + y.z * f1, oo.w * f0 + y.w * f1);
   }
   part_sum[warp][lane] = oo;
   if (lane == 0) {
     top[warp] = mm;
-    shift[warp] = sh;
     sum[warp] = ll;
   }
-  __syncthreads();
+  far = __syncthreads_or(far);
   if (warp > 0) return;
+  const AttendParams &a = p.a;
+  const int64_t at = (int64_t)x.group * G::ROWS + row, tok = x.beg + at / a.G;
+  const int hq = x.h * a.G + (int)(at % a.G);
+  if (far) {
+    join_far<G>(p, x.c0, parts, row, tok, hq);
+    return;
+  }
   mm = -INFINITY;
-  sh = 0.f;
   ll = 0.f;
   oo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const bool own = above(top[k], shift[k], mm, sh);
-    mm = own ? top[k] : mm;
-    sh = own ? shift[k] : sh;
-  }
+  for (int k = 0; k < 8; ++k) mm = fmaxf(mm, top[k]);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float f = ex2((top[k] - finite_or_0(mm)) + (shift[k] - sh));
+    const float f = ex2(top[k] - finite_or_0(mm));
     const float4 y = part_sum[k][lane];
     ll += sum[k] * f;
     oo = make_float4(oo.x + y.x * f, oo.y + y.y * f, oo.z + y.z * f, oo.w + y.w * f);
   }
-  const AttendParams &a = p.a;
-  const int64_t at = (int64_t)x.group * G::ROWS + row, tok = x.beg + at / a.G;
-  const int hq = x.h * a.G + (int)(at % a.G);
   if (lane * 4 >= a.d) return;
-  store_out(a, tok, hq, lane * 4, make_float2(oo.x, oo.y), mm, sh, ll);
-  store_out(a, tok, hq, lane * 4 + 2, make_float2(oo.z, oo.w), mm, sh, ll);
+  store_out(a, tok, hq, lane * 4, make_float2(oo.x, oo.y), mm, 0.f, ll);
+  store_out(a, tok, hq, lane * 4 + 2, make_float2(oo.z, oo.w), mm, 0.f, ll);
 }
 
 // What a softmax group knows of its item when the item, or the CTA's part of it, ends.
@@ -1021,9 +1081,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
       if (direct) {
         store_lse(a, tok, hq, m, shift, l);
       } else {
-        slot[p.slot_rows * kD + row] = m;
-        slot[p.slot_rows * (kD + 1) + row] = shift;
-        slot[p.slot_rows * (kD + 2) + row] = l;
+        leave_part(slot + p.slot_rows * kD, p.slot_rows, row, m, shift, l);
       }
     }
   }
@@ -1358,23 +1416,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_constant__ TcParams p) {
   const AttendParams &a = p.a;
   extern __shared__ float2 lse2[];
+  __shared__ float lse1[64];     // of near rows as one number
   const bool good = requests_ok(a);
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
   const int64_t beg = a.req.begin(r);
   const int rows = (int)(a.req.begin(r + 1) - beg) * a.G;
   wait_for_kernel_before();
   if (!good) return;
-  for (int c = threadIdx.x; c < rows; c += 256)
-    lse2[c] = a.stats[(beg + c / a.G) * a.Hq + h * a.G + c % a.G];
-  __syncthreads();
+  bool far = false;
+  for (int c = threadIdx.x; c < rows; c += 256) {
+    const float2 lse = a.stats[(beg + c / a.G) * a.Hq + h * a.G + c % a.G];
+    lse2[c] = lse;
+    lse1[c] = lse.x + lse.y;
+    far = fabsf(lse.x) > kFar;
+  }
+  far = __syncthreads_or(far);
   const int j = blockIdx.x * 256 + threadIdx.x;
   if (j >= len || rows == 0) return;
   const float *x = p.scores + ((int64_t)r * a.H + h) * p.slot_rows * p.score_ld + j;
   float sum = 0.f;
+  if (!far) {
 #pragma unroll 8
-  for (int c = 0; c < rows; ++c) {
-    const float z = x[(int64_t)c * p.score_ld];
-    sum += z > -INFINITY ? probability(z, lse2[c]) : 0.f;
+    for (int c = 0; c < rows; ++c) {
+      const float z = x[(int64_t)c * p.score_ld];
+      sum += z > -INFINITY ? ex2(z - lse1[c]) : 0.f;
+    }
+  } else {
+    for (int c = 0; c < rows; ++c) {
+      const float z = x[(int64_t)c * p.score_ld];
+      sum += z > -INFINITY ? probability(z, lse2[c]) : 0.f;
+    }
   }
   a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
 }
@@ -1681,10 +1752,10 @@ __global__ void __launch_bounds__(kColThreads, 1)
             float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 4; ++k) top = fmaxf(top, sh->warp_max[i][k][c]);
-            far = far || (top > -INFINITY && fabsf(top) > kFar);
+            far = far || is_far(top);
             down[c] = fmaxf(m[c], top);      // the new maximum
           }
-          if (far) {
+          if (__builtin_expect(far, 0)) {
             // the same of scores alone, and the largest value scale
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -1801,9 +1872,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum += sh->warp_sum[i][k][lane];
-        slot[p.slot_rows * kD + lane] = mine;
-        slot[p.slot_rows * (kD + 1) + lane] = shift - kColBias;
-        slot[p.slot_rows * (kD + 2) + lane] = sum;
+        leave_part(slot + p.slot_rows * kD, p.slot_rows, lane, mine > -FLT_MAX ? mine : -INFINITY, shift - kColBias, sum);
       }
       if (count == w.steps) {
         // an item of this CTA alone: its two parts
@@ -1974,7 +2043,7 @@ constexpr size_t kWtSmem = 1024 + kSmemQ + kWtStages * (size_t)kTileBytes + size
 // A slot's sum over 256 columns, of which those below `from` do not see it, where some
 // scores are beyond kFar: they are rounded as the attention kernel did, then the two terms
 // of their row's log-sum-exp are subtracted.
-__device__ __noinline__ float far_weights(uint32_t col, float f, int from, const float4 *rows, const float4 *terms) {
+__device__ __noinline__ float far_weights(uint32_t col, float f, int from, const WtShared *sh) {
   float sum = 0.f;
 #pragma unroll 1
   for (int q = 0; q < 8; ++q) {
@@ -1984,7 +2053,8 @@ __device__ __noinline__ float far_weights(uint32_t col, float f, int from, const
     float part = 0.f;
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-      const float4 k = rows[16 * q + e / 2], t = terms[16 * q + e / 2];
+      const float4 k = sh->rows[16 * q + e / 2];
+      const float4 t = sh->far[q] ? sh->terms[16 * q + e / 2] : make_float4(k.z, k.w, 0.f, 0.f);   // of warp q
       const float z0 = __fmul_rn(__uint_as_float(s[e]), fmaxf(f * k.x, 0x1p-126f));
       const float z1 = __fmul_rn(__uint_as_float(s[e + 1]), fmaxf(f * k.y, 0x1p-126f));
       part += 32 * q + e >= from ? ex2((z0 + t.x) + t.z) : 0.f;
@@ -2067,62 +2137,68 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const float2 lse = live ? a.stats[tok * a.Hq + hq] : make_float2(0.f, INFINITY);
       pair_of[0] = live ? cs : 0.f;
       pair_of[2] = -(lse.x + lse.y);
-      terms_of[0] = -lse.x;
-      terms_of[2] = -lse.y;
       const bool beyond = __any_sync(~0u, fabsf(lse.x) > kFar);
+      if (beyond) {
+        terms_of[0] = -lse.x;
+        terms_of[2] = -lse.y;
+      }
       if (lane == 0) sh->far[warp] = beyond;
       fence_async_proxy();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh->q_full));
       if (!W.warp_wait(&sh->q_full, c & 1)) goto done;   // the other rows' constants
-      const bool far = __any_sync(~0u, sh->far[lane % 8]);
-      const int count = seen(c);
-      for (int t = 0; t < count; ++t, ++n) {
-        if ((n & 1) != i) continue;
-        const int ks = n % kWtStages, j = tile_at(t) * kTile + warp % 4 * 32 + lane;
-        if (!W.warp_wait(&sh->k_full[ks], n / kWtStages & 1)) goto done;
-        if (!W.warp_wait(&sh->s_full[i], n >> 1 & 1)) goto done;
-        tc_fence_after();
-        const int in = warp % 4 * 32 + lane;
-        const float f = sh->ks[ks][in / 4];
-        const bool there = j < len && (sh->mask[ks] >> (in / 4) & 1);
-        // columns below `from` do not see the slot
-        const int from = (int)min((int64_t)INT32_MAX, max((int64_t)j - (len - fresh), (int64_t)0) * a.G) - (row0 + c * 2 * kTile);
-        const bool masked = __any_sync(~0u, from > 0);
-        const uint64_t f2 = pair(f, f);
-        uint64_t sum = pair(0.f, 0.f);
-        if (far) sum = pair(far_weights(s_col, f, from, sh->rows, sh->terms), 0.f);
+      const auto work = [&](auto far) {
+        const int count = seen(c);
+        for (int t = 0; t < count; ++t, ++n) {
+          if ((n & 1) != i) continue;
+          const int ks = n % kWtStages, j = tile_at(t) * kTile + warp % 4 * 32 + lane;
+          if (!W.warp_wait(&sh->k_full[ks], n / kWtStages & 1)) return false;
+          if (!W.warp_wait(&sh->s_full[i], n >> 1 & 1)) return false;
+          tc_fence_after();
+          const int in = warp % 4 * 32 + lane;
+          const float f = sh->ks[ks][in / 4];
+          const bool there = j < len && (sh->mask[ks] >> (in / 4) & 1);
+          // columns below `from` do not see the slot
+          const int from = (int)min((int64_t)INT32_MAX, max((int64_t)j - (len - fresh), (int64_t)0) * a.G) - (row0 + c * 2 * kTile);
+          const bool masked = __any_sync(~0u, from > 0);
+          const uint64_t f2 = pair(f, f);
+          uint64_t sum = pair(0.f, 0.f);
+          if constexpr (decltype(far)::value) sum = pair(far_weights(s_col, f, from, sh), 0.f);
 #pragma unroll 1
-        for (int q = far ? 8 : 0; q < 8; ++q) {
-          uint32_t s[32];
-          tc_ld32(s_col + 32 * q, s);
-          tc_wait_ld32(s);
+          for (int q = decltype(far)::value ? 8 : 0; q < 8; ++q) {
+            uint32_t s[32];
+            tc_ld32(s_col + 32 * q, s);
+            tc_wait_ld32(s);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float4 k = sh->rows[16 * q + e / 2];
-            float x0, x1;
-            unpair(fma2(mul2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f2), pair(k.x, k.y), pair(k.z, k.w)),
-                   x0, x1);
-            if (masked) {
-              x0 = 32 * q + e >= from ? x0 : -INFINITY;
-              x1 = 32 * q + e + 1 >= from ? x1 : -INFINITY;
+            for (int e = 0; e < 32; e += 2) {
+              const float4 k = sh->rows[16 * q + e / 2];
+              float x0, x1;
+              unpair(fma2(mul2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f2), pair(k.x, k.y), pair(k.z, k.w)),
+                     x0, x1);
+              if (masked) {
+                x0 = 32 * q + e >= from ? x0 : -INFINITY;
+                x1 = 32 * q + e + 1 >= from ? x1 : -INFINITY;
+              }
+              sum = add2(sum, pair(ex2(x0), ex2(x1)));
             }
-            sum = add2(sum, pair(ex2(x0), ex2(x1)));
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&sh->s_empty[i]));
+            mbar_arrive(smem_addr(&sh->k_empty[ks]));
+          }
+          float u0, u1;
+          unpair(sum, u0, u1);
+          // a slot's sum passes from group to group with the chunks
+          float *total = &sh->sum[t][in];
+          if (c + 1 < chunks) *total += u0 + u1;
+          else if (there) a.weights[((int64_t)r * a.H + h) * a.wstride + j] += *total + (u0 + u1);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_addr(&sh->s_empty[i]));
-          mbar_arrive(smem_addr(&sh->k_empty[ks]));
-        }
-        float u0, u1;
-        unpair(sum, u0, u1);
-        // a slot's sum passes from group to group with the chunks
-        float *total = &sh->sum[t][in];
-        if (c + 1 < chunks) *total += u0 + u1;
-        else if (there) a.weights[((int64_t)r * a.H + h) * a.wstride + j] += *total + (u0 + u1);
-      }
+        return true;
+      };
+      const bool far = __any_sync(~0u, sh->far[lane % 8]);
+      if (!(far ? work(std::true_type()) : work(std::false_type()))) goto done;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh->spent));
     }
