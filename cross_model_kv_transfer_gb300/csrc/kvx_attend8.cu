@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
         // key scales; the mask, where the tile needs one
         float vsc[MT][2], most = 0.f;
         bool grew = false;
-        const bool masked = valid != (KW == 32 ? ~0u : (1u << KW % 32) - 1) || j0 + KW - 1 > limits || cols - col0 < C::COLS;
+        // (with 16 slots a warp, lanes 16 .. 31 stand for the same ones)
+        const bool masked = valid != ~0u || j0 + KW - 1 > limits || cols - col0 < C::COLS;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
