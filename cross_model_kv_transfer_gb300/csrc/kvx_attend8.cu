@@ -11,8 +11,10 @@
 // 16 x 8 x 16 matrix instructions: codes are exact in f16, fp32 queries and
 // probabilities go in two f16 parts.  Bound by those instructions, whose rate on this
 // GPU is about 150 TFLOP/s: fp32, 16 requests of 1024 to 16,384 slots with 64 heads
-// over 8 x 128 take 137 us with weights; one short request (4 heads over 2 x 64, 512
-// slots) 13 us, the latency of its chain.
+// over 8 x 128 take 104 us, 133 with weights; one short request (4 heads over 2 x 64, 512
+// slots) 13 us, the latency of its chain.  Prompts take long: every group of columns
+// reads and multiplies all of its request's slots, those that none of it sees as well
+// (8192 fp32 tokens of 64 heads 19.9 ms).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

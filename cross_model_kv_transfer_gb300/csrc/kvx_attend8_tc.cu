@@ -7,7 +7,8 @@
 //   S = Q K^T   kind::f8f6f4: the codes as they lie in the cache; a query row,
 //               scaled by a power of two to a largest element in (224, 448], is
 //               the sum of two e4m3 parts (4 + 4 bits: a bf16 element exactly,
-//               down to 1/1792 of the row's largest, below that to 2^-19 of it),
+//               down to 1/896 of the row's largest, below that to 2^-17.8 of it:
+//               the second part's step is 2^-9),
 //   O += P V    kind::f16: P in f16 from tensor memory (it overwrites S), V
 //               converted to f16 in shared memory with its block's scale.
 // Softmax statistics are fp32, a row to a thread: no exchange between threads.
@@ -20,14 +21,15 @@
 // (at most 64 rows): they take the even and the odd slot tiles of the same
 // rows, so that one tile's softmax overlaps the other's products.
 //
-// What it reaches.  Wide, one request of 8192 tokens, 64 heads: 1217 us, 0.90
-// PFLOP/s of the two products counted once, 0.46 of what bf16 matrix products reach;
-// counters have the tensor pipe active 0.37 of the time and the schedulers issuing
-// 0.48 of it: bound by the two groups' chain of score product, softmax and value
+// What it reaches.  Wide, one request of 8192 tokens, 64 heads: 1070 us, 1.03
+// PFLOP/s of the two products counted once, 0.52 of what bf16 matrix products reach;
+// counters have the tensor pipe active 0.45 of the time and the schedulers issuing
+// 0.55 of it: bound by the two groups' chain of score product, softmax and value
 // product.  (Score products in half tiles of 64 columns run at 0.6 of their rate at
-// 128, but whole tiles leave a group nothing to do while they are formed: 1397 us.)  61 tokens of 32
-// heads against 8192 slots, two requests: 45 us, 15 to join what 152 CTAs left, 26
-// for the weights; about a third of that fills and drains pipelines.
+// 128, but whole tiles leave a group nothing to do while they are formed: 1397 us
+// where half tiles took 1217.)  61 tokens of 32 heads against 8192 slots, two
+// requests: 45 us, 16 to join what 152 CTAs left, 26 for the weights; about a third
+// of that fills and drains pipelines.
 //
 // Work: every CTA takes an equal share of all steps and item costs (below); what
 // several CTAs did of an item is joined by a second kernel.
@@ -157,21 +159,24 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
 // tiles up to the last slot that its rows see.  An item costs its steps and a fixed
 // part (queries, a filling and draining pipeline, the result), so the CTAs' shares
 // are of costs: an item takes SETUP + steps places from `base` on, and its step s
-// is at place base + SETUP + s.  Measured: wide, 8192 tokens, SETUP 3, 4, 5, 6: 1394,
-// 1293, 1217, 1213 us; narrow, 0, 1, 2, 3: 238, 211, 200, 201 us for a step of 16
-// requests.
+// is at place base + SETUP + s.  Measured, us, with SETUP as given: wide 5, 6, 7, 8, 9: a
+// prompt of 8192 tokens 1133, 1082, 1070, 1079, 1089, one of 2048 158, 157, 154, 159, 147,
+// 128 rows each of 16 requests of 1024 to 16,384 slots 168, 163, 161, 161, 163.  The same
+// requests narrow 2, 3, 4, 5, 6: 24 rows 152, 145, 147, 152, 155, 40 rows 168, 157, 152, 153,
+// 156, 64 rows 193, 180, 167, 161, 156; columns 1, 2, 3, 4: 8 rows 84, 74, 73, 72, 16 rows 136,
+// 108, 101, 95.
 struct Wide {
   static constexpr int ROWS = 2 * kTile, SLOTS = kTile;   // of an item, of a step
   static constexpr int PARTS = 1;                         // results that a CTA keeps for an item
-  static constexpr int SETUP = 5;
+  static constexpr int SETUP = 7;
 };
 // Few columns (kernel further down): rows are the columns of S^T.
 template <int NC>
 struct Columns {
-  static constexpr int ROWS = NC, SLOTS = 2 * kTile, PARTS = 2, SETUP = 2;
+  static constexpr int ROWS = NC, SLOTS = 2 * kTile, PARTS = 2, SETUP = 4;
 };
 struct Narrow {
-  static constexpr int ROWS = kTile, SLOTS = 2 * kTile, PARTS = 2, SETUP = 2;
+  static constexpr int ROWS = kTile, SLOTS = 2 * kTile, PARTS = 2, SETUP = 4;
 };
 template <class G>
 __device__ __forceinline__ int steps_of(const AttendParams &a, int len, int fresh, int group) {
@@ -1466,10 +1471,10 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
 // plus value scale; once one is beyond kFar, where that sum's rounding would count, an
 // item takes the largest score and the largest value scale apart.
 // Two groups of four warps take the even and the odd slot tiles.
-// Bound by HBM and what surrounds it: one query of 64 heads over 131,071 slots of 8
-// heads 56 us, 4.8 TB/s (a copy 6.7); 16 requests of 1024 to 16,384 slots 72 us.  The
-// narrow form above takes 119 and 208 there, matrix instructions on registers (16 x 8
-// x 16) 80 and 119.
+// One query of 64 heads over 131,071 slots of 8 heads takes 57 us, 4.7 TB/s (a copy
+// 6.7); 16 requests of 1024 to 16,384 slots 73 us, and with 16 columns, which read the
+// same bytes, 94: the chain of a tile's softmax counts beside them.  The narrow form
+// above takes 146 there, matrix instructions on registers (16 x 8 x 16) 88 with 8.
 // even numbers of stages: a stage serves one group, whose waits on it then know
 // that the phase before is over
 constexpr int kCkStages = 4, kCvStages = 6, kScales = 16, kColThreads = 12 * 32;
@@ -2275,7 +2280,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 
 // The same from the scores of few columns, [score_ld][slot_rows].  Bound by the
 // chain of its loads: a thread has four slots' on their way at once (16 requests of up
-// to 16,384 slots, 8 heads, with the attention before it: 93 us; two slots 95, one 97).
+// to 16,384 slots, 8 heads: 12 us; two slots 2 more, one 4).
 constexpr int kSlotsOfThread = 4;
 __global__ void __launch_bounds__(256) weights_of_columns_kernel(const __grid_constant__ TcParams p) {
   const AttendParams &a = p.a;
@@ -2329,10 +2334,10 @@ struct TcShape {
 TcShape tc_shape(const kvx_attend8_args *a) {
   TcShape s;
   const int64_t G = a->q_heads / a->cache.heads, most = G * most_new(a);
-  // One step of the cases below: 16 requests of 1024 to 16,384 slots, 8 KV heads,
-  // without and with weights.  16 rows: columns 109 and 135 us, narrow 143 and 195.
-  // 24 rows: narrow 149 and 214, wide 177 and 323; 64 rows: 186 and 315 against 186
-  // and 334; 128 rows: 254 and 507 against 182 and 333.
+  // 16 requests of 1024 to 16,384 slots, 8 KV heads, without and with weights.  16 rows:
+  // columns 94 and 119 us, narrow 146 and 189.  24 rows: narrow 147 and 202, wide 151 and
+  // 298; 64 rows: 167 and 274 against 159 and 308; 128 rows: 216 and 432 against 160 and
+  // 309.
   s.columns = most <= 16;
   s.wide = most > 64;
   s.slot_rows = s.wide ? Wide::ROWS : s.columns ? (most <= 8 ? 8 : 16) : (int)most;
