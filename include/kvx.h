@@ -617,7 +617,8 @@ typedef struct {
 /* Rotary positions of queries and keys in one launch: y = a R(p) x on the first
  * rot_dim dimensions of every head, the others copied.  The angle p w_i is
  * formed exactly modulo one turn in 64-bit fixed point, so its error does not
- * grow with the position.  A token whose position is outside [0, 2^31) is left
+ * grow with the position; its cosine and sine are within 9e-8 for fp32 rows and
+ * within 8e-7 for bf16 ones.  A token whose position is outside [0, 2^31) is left
  * unwritten (KVX_FLAG_BAD_POSITION).  KVX_ERR_INVALID_ARG for a NULL rope,
  * args or output, sizes outside the limits, or rows that are not aligned to an
  * element. */
@@ -722,15 +723,20 @@ size_t kvx_attend8_workspace_bytes(const kvx_attend8_args *args);
  * over the request's queries and the query heads of KV head h: the accumulated
  * attention weight by which kvx_evict8 chooses.  Slots at or past lens[r] are
  * never used and may hold anything; codes of held slots must not be NaN.
- * Softmax statistics and sums are fp32.  A length outside [0, max_len] counts as
- * 0 (KVX_FLAG_BAD_LENGTH); slots of a block id outside [0, num_blocks) are
- * masked (KVX_FLAG_BAD_BLOCK); a malformed request table, or a request with
- * more than max_new queries, writes nothing (KVX_FLAG_BAD_SEQLENS).  One to three
- * launches.  bf16 queries with head_dim up to 128 and blocks of whole 8-slot groups
- * run on the tcgen05 tensor cores: there an element of a query counts to 2^-19 of
- * its row's largest.  max_len is at most 2^31 - 1025, and min(max_new, ntok) times
- * q_heads / heads at most 2^31 - 1025 (else KVX_ERR_UNSUPPORTED).  A kernel's wait that
- * gives up sets KVX_FLAG_TIMEOUT. */
+ * Softmax statistics and sums are fp32.  Probabilities are rounded before their
+ * product with the values: to 2^-11 of themselves for bf16 queries (2^-9 where a
+ * request has at most 16 rows of a KV head; values under scales that are no powers
+ * of two to 2^-11 where it has more), to 2^-21 for fp32 ones.  A length outside
+ * [0, max_len] counts as 0 (KVX_FLAG_BAD_LENGTH); slots of a block id outside
+ * [0, num_blocks) are masked (KVX_FLAG_BAD_BLOCK); a malformed request table, or a
+ * request with more than max_new queries, writes nothing (KVX_FLAG_BAD_SEQLENS).
+ * One to three launches.  bf16 queries with head_dim up to 128 and blocks of whole
+ * 8-slot groups run on the tcgen05 tensor cores: there an element of a query counts
+ * to 2^-17 of its row's largest.  Scores may be as large as fp32 holds: they are
+ * known to 2^-16 of themselves, and where that tells slots apart a row gets the
+ * softmax of them.  max_len is at most 2^31 - 1025, and min(max_new, ntok) times
+ * q_heads / heads at most 2^31 - 1025 (else KVX_ERR_UNSUPPORTED).  A kernel's wait
+ * that gives up sets KVX_FLAG_TIMEOUT. */
 kvx_status kvx_attend8(const kvx_attend8_args *args, void *stream);
 
 typedef struct {
