@@ -1033,7 +1033,9 @@ class Cache8:
                out=None, lse=None, weights=None, workspace=None, status=None, stream=None):
         """Attention of the new queries q [tokens][q_heads][d] over the slots
         of their requests (``lens`` [R], at most ``max_len``): query i of n sees
-        slots up to lens - n + i.  Returns (out, lse [tokens][q_heads]).
+        slots up to lens - n + i.  With ``cu_seqlens`` [R + 1] a request has up
+        to ``max_new`` queries (more: nothing is written, and ``status`` tells).
+        Returns (out, lse [tokens][q_heads]); ``out`` may be q without weights.
         ``weights`` [R][heads][>= max_len] fp32 accumulates the attention weight
         of each slot.  Scratch (for scores at most 1 GB) is allocated here unless ``workspace`` (from
         ``attend_workspace``) is given."""
