@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
       vref = 0x1p-112f;
       vinv = 0x1p126f;
       far = false;
-      limits = w.len - w.fresh + col0 / a.G;
+      limits = first_limit(a, w.len, w.fresh) + col0 / a.G * limit_step(a);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) split_kernel(const __grid_const
           mx[n][e] = m[n][e] = -INFINITY;
           l[n][e] = 0.f;
           const int col = col0 + 8 * n + 2 * t + e;
-          limit[n][e] = col < cols ? w.len - w.fresh + col / a.G : -1;
+          limit[n][e] = col < cols ? first_limit(a, w.len, w.fresh) + col / a.G * limit_step(a) : -1;
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -827,6 +827,16 @@ __global__ void __launch_bounds__(32 * C::WARPS) weights_again_kernel(const __gr
     }
 }
 
+// A pass of a call whose requests share prefixes: over the prefixes (`all`) or over the
+// requests' own slots (`before`).
+struct Pass {
+  kvx8::Requests req;
+  kvx8::Groups groups;
+  const float *before;
+  float2 *stats;             // of the prefixes: written, then read with `before`
+  int all;
+};
+
 kvx_status check(const kvx_attend8_args *a) {
   if (!a) return KVX_ERR_INVALID_ARG;
   const kvx_cache8 &c = a->cache;
@@ -905,23 +915,10 @@ kvx_status launch_dim(const SplitParams &p, int cols, int grid, bool again, cuda
                         : launch_cols<256, PARTS>(p, cols, grid, again, s);
 }
 
-}  // namespace
-
-extern "C" size_t kvx_attend8_workspace_bytes(const kvx_attend8_args *a) {
-  if (check(a) != KVX_OK) return 0;
-  return kvx_attend8_tc_supports(a) ? kvx_attend8_tc_workspace_bytes(a) : shape_of(a).bytes;
-}
-
-extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
-  if (const kvx_status st = check(a)) return st;
-  if (a->ntok == 0) return KVX_OK;
+// Enqueue a checked call, or a pass of one.
+kvx_status enqueue(const kvx_attend8_args *a, const Pass &pass, cudaStream_t s) {
   const kvx_cache8 &c = a->cache;
   const int size = a->dtype == KVX_BF16 ? 2 : 4;
-  if (!a->q || !a->out || !aligned_to(a->q, size) || !aligned_to(a->out, size)) return KVX_ERR_INVALID_ARG;
-  if (a->weights && a->out == a->q) return KVX_ERR_INVALID_ARG;   // scores may be formed again
-  const size_t least = kvx_attend8_tc_supports(a) ? kvx_attend8_tc_least_bytes(a) : shape_of(a).scores;
-  if (!a->workspace || !aligned_to(a->workspace, 256) || a->workspace_bytes < least)
-    return KVX_ERR_INVALID_ARG;
   AttendParams p;
   p.k = (const uint8_t *)c.k_codes;
   p.v = (const uint8_t *)c.v_codes;
@@ -937,9 +934,13 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.lens = a->lens;
   p.lse = a->lse;
   p.weights = a->weights;
-  p.stats = nullptr;
+  p.stats = pass.all ? pass.stats : nullptr;
   p.status = a->status;
-  p.req = {a->cu_seqlens, a->num_requests, a->ntok};
+  p.req = pass.req;
+  p.groups = pass.groups;
+  p.before = pass.before;
+  p.before_stats = pass.stats;
+  p.all = pass.all;
   p.num_blocks = (int)c.num_blocks;
   // with k = ceil(log2 bs), 2^(31 + k) / bs rounded up is off by less than 2^k / bs
   // a unit, so the quotient is exact below 2^31
@@ -956,9 +957,8 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   p.max_blocks = c.max_blocks_per_req;
   p.max_len = a->max_len;
   p.max_new = most_new(a);
-  p.bf16 = size == 2;
+  p.bf16 = size == 2 && !pass.all;    // what a prefix gives stays in fp32
   p.c = a->scale * kLog2e;
-  cudaStream_t s = (cudaStream_t)stream;
   char *ws = (char *)a->workspace;
   if (kvx_attend8_tc_supports(a)) return kvx_attend8_tc_launch(a, p, ws, s);
   const Shape sh = shape_of(a);
@@ -976,4 +976,97 @@ extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
   if (st != KVX_OK || !weighs || again) return st;
   weights_of_scores_kernel<<<dim3((a->max_len + 255) / 256, c.heads, a->num_requests), 256, 0, s>>>(sp, sh.cols);
   return launched();
+}
+
+size_t least_bytes(const kvx_attend8_args *a) {
+  return kvx_attend8_tc_supports(a) ? kvx_attend8_tc_least_bytes(a) : shape_of(a).scores;
+}
+
+// The two passes of a call whose requests share prefixes, as calls of their own, and what
+// they leave beside the workspace of the larger one.
+struct Shared {
+  kvx_attend8_args before, own;
+  size_t out, stats, bytes;
+};
+kvx_status shared_of(const kvx_attend8_shared_args *a, Shared &s) {
+  if (!a) return KVX_ERR_INVALID_ARG;
+  if (const kvx_status st = check(&a->own)) return st;
+  if (a->own.weights || !a->prefix_table || !aligned_to(a->prefix_table, 4) || !a->prefix_lens || a->max_prefix_blocks < 1 ||
+      a->num_prefixes < 1 || (!a->groups && a->num_prefixes != 1) || a->max_group < 1)
+    return KVX_ERR_INVALID_ARG;
+  s.own = s.before = a->own;
+  kvx_attend8_args &b = s.before;
+  b.cache.block_table = a->prefix_table;
+  b.cache.max_blocks_per_req = a->max_prefix_blocks;
+  b.lens = a->prefix_lens;
+  b.max_len = a->max_prefix;
+  b.num_requests = a->num_prefixes;
+  b.cu_seqlens = a->prefix_lens;      // any table: the pass has its own requests
+  const int64_t members = a->max_group < a->own.num_requests ? a->max_group : a->own.num_requests;
+  const int64_t most = members * (a->own.cu_seqlens ? most_new(&a->own) : 1);
+  b.max_new = (int32_t)(most < INT32_MAX ? most : INT32_MAX);
+  if (const kvx_status st = check(&b)) return st;
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t one = least_bytes(&b), two = least_bytes(&s.own), rows = (size_t)a->own.ntok * a->own.q_heads;
+  s.out = up(one > two ? one : two);
+  s.stats = s.out + up(rows * a->own.cache.head_dim * sizeof(float));
+  s.bytes = s.stats + up(rows * sizeof(float2));
+  return KVX_OK;
+}
+
+bool usable(const kvx_attend8_args *a, size_t least) {
+  const int size = a->dtype == KVX_BF16 ? 2 : 4;
+  return a->q && a->out && aligned_to(a->q, size) && aligned_to(a->out, size) && a->workspace &&
+         aligned_to(a->workspace, 256) && a->workspace_bytes >= least;
+}
+
+}  // namespace
+
+extern "C" size_t kvx_attend8_workspace_bytes(const kvx_attend8_args *a) {
+  if (check(a) != KVX_OK) return 0;
+  return kvx_attend8_tc_supports(a) ? kvx_attend8_tc_workspace_bytes(a) : shape_of(a).bytes;
+}
+
+extern "C" kvx_status kvx_attend8(const kvx_attend8_args *a, void *stream) {
+  if (const kvx_status st = check(a)) return st;
+  if (a->ntok == 0) return KVX_OK;
+  if (!usable(a, least_bytes(a))) return KVX_ERR_INVALID_ARG;
+  if (a->weights && a->out == a->q) return KVX_ERR_INVALID_ARG;   // scores may be formed again
+  Pass pass = {};
+  pass.req = {a->cu_seqlens, a->num_requests, a->ntok, nullptr, 0, 0};
+  return enqueue(a, pass, (cudaStream_t)stream);
+}
+
+extern "C" size_t kvx_attend8_shared_workspace_bytes(const kvx_attend8_shared_args *a) {
+  Shared s;
+  return shared_of(a, s) == KVX_OK ? s.bytes : 0;
+}
+
+// Two passes: each prefix against the queries of all requests that share it, as one
+// request's, and the requests' own slots, whose results are joined with the first pass's
+// where they are written.  A prefix is read once for its group and not once a request, and
+// its products have a group's rows: what they cost is that of a prompt of as many tokens.
+extern "C" kvx_status kvx_attend8_shared(const kvx_attend8_shared_args *a, void *stream) {
+  Shared s;
+  if (const kvx_status st = shared_of(a, s)) return st;
+  const kvx_attend8_args &own = s.own;
+  if (own.ntok == 0) return KVX_OK;
+  if (!usable(&own, s.bytes)) return KVX_ERR_INVALID_ARG;
+  char *ws = (char *)own.workspace;
+  kvx_attend8_args &before = s.before;
+  before.out = ws + s.out;
+  before.out_token_stride = (int64_t)own.q_heads * own.cache.head_dim;
+  before.out_head_stride = own.cache.head_dim;
+  before.lse = nullptr;
+  Pass pass = {};
+  pass.all = 1;
+  pass.stats = (float2 *)(ws + s.stats);
+  pass.req = {own.cu_seqlens, a->num_prefixes, own.ntok, a->groups, own.num_requests, 0};
+  if (!a->groups) pass.req = {nullptr, 1, own.ntok, nullptr, 0, 1};
+  if (const kvx_status st = enqueue(&before, pass, (cudaStream_t)stream)) return st;
+  pass.all = 0;
+  pass.before = (const float *)(ws + s.out);
+  pass.req = {own.cu_seqlens, own.num_requests, own.ntok, nullptr, 0, 0};
+  pass.groups = {a->groups, a->num_prefixes, before.max_new};
+  return enqueue(&own, pass, (cudaStream_t)stream);
 }

@@ -23,8 +23,17 @@ struct AttendParams {
   float2 *stats;
   uint32_t *status;
   kvx8::Requests req;
+  // Requests that share a prefix.  The pass over the prefixes: `all`, a query sees every
+  // slot, and `req` is the groups.  The pass over the requests' own slots: `before` and
+  // `before_stats` are what the first left, [ntok][Hq][d] and [ntok][Hq], to join with,
+  // and `groups` is checked again, so that a bad table stops both passes.
+  kvx8::Groups groups;
+  const float *before;
+  const float2 *before_stats;
   int64_t wstride;
-  int num_blocks, H, Hq, G, d, bs, max_blocks, max_len, max_new, bf16;
+  int num_blocks, H, Hq, G, d, bs, max_blocks, max_len, max_new;
+  int bf16;                    // the type of out
+  int all;
   uint32_t bs_mul, bs_shift;   // j / bs = j * bs_mul >> bs_shift for j < 2^31
   float c;   // scale * log2(e): scores are kept in base 2
 };
@@ -60,12 +69,18 @@ __device__ __forceinline__ int page_of(const AttendParams &p, int r, uint32_t bl
   const int page = block < (uint32_t)p.max_blocks ? __ldg(p.table + (int64_t)r * p.max_blocks + block) : -1;
   return page < p.num_blocks ? page : -1;
 }
+// The last slot that query i of a request sees is first_limit + i * a query's step.
+__device__ __forceinline__ int first_limit(const AttendParams &p, int len, int fresh) {
+  return p.all ? len - 1 : len - fresh;
+}
+__device__ __forceinline__ int limit_step(const AttendParams &p) { return p.all ? 0 : 1; }
 __device__ __forceinline__ bool requests_ok(const AttendParams &p) {
   bool good = p.req.ok();
-  if (p.req.cu) {
+  if (good && p.groups.of) good = __syncthreads_and(p.groups.ok(p.req, threadIdx.x, blockDim.x));
+  if (p.req.table()) {
     bool few = true;
     for (int r = threadIdx.x; good && r < p.req.R; r += blockDim.x)
-      few = few && p.req.cu[r + 1] - p.req.cu[r] <= p.max_new;
+      few = few && p.req.begin(r + 1) - p.req.begin(r) <= p.max_new;
     good = __syncthreads_and(good && few);
   }
   return good;
@@ -75,8 +90,28 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A row's two parts, one here (sum l relative to exp2(m + shift)) and one from before: the
+// factors on their outputs and the log-sum-exp of both, in base 2 as two terms.
+struct Joined {
+  float own, before;
+  float2 lse;
+};
+__device__ __forceinline__ Joined join_before(const AttendParams &p, int64_t g, int hq, float m, float shift, float l) {
+  const float2 b = __ldcg(p.before_stats + g * p.Hq + hq);
+  if (l == 0.f) return {0.f, b.y < INFINITY ? 1.f : 0.f, b};
+  const float rest = shift + log2f(l);
+  if (b.y == INFINITY) return {1.f, 0.f, make_float2(m, rest)};
+  const float more = (b.x - m) + (b.y - rest), up = ex2(more), down = ex2(-more);   // differences first: exact where they count
+  return {1.f / (1.f + up), 1.f / (1.f + down),
+          more > 0.f ? make_float2(b.x, b.y + log2f(1.f + down)) : make_float2(m, rest + log2f(1.f + up))};
+}
 // The log-sum-exp of a row whose sum l is relative to exp2(m + shift).
 __device__ __forceinline__ void store_lse(const AttendParams &p, int64_t g, int hq, float m, float shift, float l) {
+  if (p.before) {
+    const float2 both = join_before(p, g, hq, m, shift, l).lse;
+    if (p.lse) p.lse[g * p.Hq + hq] = both.y == INFINITY ? -INFINITY : (both.x + both.y) * kLn2;
+    return;
+  }
   const bool any = l != 0.f;
   const float rest = shift + log2f(l);
   if (p.lse) p.lse[g * p.Hq + hq] = any ? (m + rest) * kLn2 : -INFINITY;
@@ -90,14 +125,22 @@ __device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int 
                                           float shift, float l) {
   const float inv = l != 0.f ? 1.f / l : 0.f;
   const int64_t to = g * p.ot + hq * p.oh + d;
+  o.x *= inv;
+  o.y *= inv;
+  if (p.before) {
+    const Joined j = join_before(p, g, hq, m, shift, l);
+    const float2 b = __ldcg(reinterpret_cast<const float2 *>(p.before + (g * p.Hq + hq) * p.d + d));
+    o.x = o.x * j.own + b.x * j.before;
+    o.y = o.y * j.own + b.y * j.before;
+  }
   if (p.bf16) {
     __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + to;
-    out[0] = __float2bfloat16_rn(o.x * inv);
-    out[1] = __float2bfloat16_rn(o.y * inv);
+    out[0] = __float2bfloat16_rn(o.x);
+    out[1] = __float2bfloat16_rn(o.y);
   } else {
     float *out = reinterpret_cast<float *>(p.out) + to;
-    out[0] = o.x * inv;
-    out[1] = o.y * inv;
+    out[0] = o.x;
+    out[1] = o.y;
   }
   if (d == 0) store_lse(p, g, hq, m, shift, l);
 }

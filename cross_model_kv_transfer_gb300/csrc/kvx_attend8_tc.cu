@@ -181,7 +181,7 @@ struct Narrow {
 template <class G>
 __device__ __forceinline__ int steps_of(const AttendParams &a, int len, int fresh, int group) {
   const int64_t end = ((int64_t)(group + 1) * G::ROWS + a.G - 1) / a.G;   // its tokens end here
-  const int64_t seen = len - fresh + (end < fresh ? end : fresh);
+  const int64_t seen = a.all ? len : len - fresh + (end < fresh ? end : fresh);
   return seen <= 0 ? 1 : (int)((seen + G::SLOTS - 1) / G::SLOTS);
 }
 template <class G>
@@ -262,7 +262,7 @@ __device__ __forceinline__ Requests32 look(const AttendParams &a, int r0, bool t
 template <class G>
 __device__ void find_share(const AttendParams &a, int cta, int ctas, bool tell, Share &s) {
   const int lane = threadIdx.x % 32;
-  s.good = true;
+  s.good = !a.groups.of || __all_sync(~0u, a.groups.ok(a.req, lane, 32));
   s.T = 0;
   s.N = 0;
   s.last = -1;
@@ -1017,8 +1017,9 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   const bool direct = WIDE && whole;
   if (warp_live) {
     const float inv = direct ? (l != 0.f ? back / l : 0.f) : back;
+    const bool full = direct && !a.bf16;      // the result in fp32
     __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + tok * a.ot + hq * a.oh;
-    if (WIDE && (!direct || p.vec_out)) {
+    if (WIDE && (!direct || full || (p.vec_out && !a.before))) {
       // Through shared memory, so that rows go out whole: a lane's row is written
       // there 16 bytes at a time, and half a warp stores a row's 256.  It lies where
       // the warp's own query rows were, whose products are over.
@@ -1028,17 +1029,19 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
       const auto cell = [&](int r, int at) {    // 16 bytes `at` of row r
         return reinterpret_cast<uint4 *>(own + (at / 8) * kTileBytes + r * 128 + ((at % 8 ^ (r & 7)) << 4));
       };
-      uint64_t to = direct ? (uint64_t)out : (uint64_t)(slot + row * kD);
+      const bool narrow = direct && !full;    // the result in bf16: a row in one go
+      uint64_t to = full ? (uint64_t)(reinterpret_cast<float *>(a.out) + tok * a.ot + hq * a.oh)
+                    : direct ? (uint64_t)out : (uint64_t)(slot + row * kD);
 #pragma unroll 1
-      for (int half_row = 0; half_row < (direct ? 1 : 2); ++half_row) {
+      for (int half_row = 0; half_row < (narrow ? 1 : 2); ++half_row) {
 #pragma unroll 1
-        for (int c = 0; c < (direct ? 4 : 2); ++c) {
+        for (int c = 0; c < (narrow ? 4 : 2); ++c) {
           uint32_t o[32];
           tc_ld32(o_col + 64 * half_row + 32 * c, o);
           tc_wait_ld32(o);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
-          if (direct) {
+          if (narrow) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t b[4];
@@ -1056,18 +1059,35 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
         for (int r0 = 0; r0 < 32; r0 += 2) {
           const int r = r0 + lane / 16;
           const uint64_t base = __shfl_sync(~0u, to, r);
-          if (row - lane + r < rows && (!direct || 8 * (lane % 16) < a.d))
+          const int dim = narrow ? 8 * (lane % 16) : 64 * half_row + 4 * (lane % 16);
+          if (row - lane + r < rows && (!direct || dim < a.d))
             reinterpret_cast<uint4 *>(base)[lane % 16] = *cell(r, lane % 16);
         }
         to += 256;
         __syncwarp();
       }
     } else {
+      // rows of the thread's own; what came before them is joined here
+      Joined j = {1.f, 0.f, {}};
+      if (live && direct && a.before) j = join_before(a, tok, hq, m, shift, l);
+      const float own = inv * j.own;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         tc_ld32(o_col + 32 * c, o);
         tc_wait_ld32(o);
+        if (live && direct && a.before) {
+          const float *b = a.before + (tok * a.Hq + hq) * a.d + 32 * c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            if (32 * c + e < a.d) {
+              const float4 y = __ldcg(reinterpret_cast<const float4 *>(b + e));
+              o[e] = __float_as_uint(fmaf(y.x, j.before, __uint_as_float(o[e]) * own));
+              o[e + 1] = __float_as_uint(fmaf(y.y, j.before, __uint_as_float(o[e + 1]) * own));
+              o[e + 2] = __float_as_uint(fmaf(y.z, j.before, __uint_as_float(o[e + 2]) * own));
+              o[e + 3] = __float_as_uint(fmaf(y.w, j.before, __uint_as_float(o[e + 3]) * own));
+            }
+        }
         if (live && !direct) {
           float4 *to = reinterpret_cast<float4 *>(slot + row * kD + 32 * c);
 #pragma unroll
@@ -1077,7 +1097,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
         } else if (live) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (32 * c + e < a.d) out[32 * c + e] = __float2bfloat16_rn(__uint_as_float(o[e]) * inv);
+            if (32 * c + e < a.d) out[32 * c + e] = __float2bfloat16_rn(__uint_as_float(o[e]) * (a.before ? 1.f : inv));
         }
         __syncwarp();   // together to the next load
       }
@@ -1187,8 +1207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = row < rows, warp_live = row - lane < rows;
       const int64_t at = (int64_t)w.group * G_::ROWS + row;         // row of the request and head
       const int64_t tok = at / a.G;
-      const int limit = live ? (int)(w.len - w.fresh + tok) : -1;   // last slot seen
-      const int floor_limit = (int)(w.len - w.fresh + (at - lane) / a.G);   // the lowest of the warp's live rows
+      const int first = first_limit(a, w.len, w.fresh), more = limit_step(a);
+      const int limit = live ? (int)(first + tok * more) : -1;   // last slot seen
+      const int floor_limit = (int)(first + (at - lane) / a.G * more);   // the lowest of the warp's live rows
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
                                  (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
       float m = -INFINITY, shift = 0.f, l = 0.f, cs;
@@ -1698,7 +1719,8 @@ __global__ void __launch_bounds__(kColThreads, 1)
         m[c] = -FLT_MAX;     // nothing seen: any score is over it
         l[c] = 0.f;
       }
-      const int low = (int)(w.len - w.fresh + row0 / a.G);   // last slot that the first column sees
+      const int first = first_limit(a, w.len, w.fresh), more = limit_step(a);
+      const int low = (int)(first + row0 / a.G * more);      // last slot that the first column sees
       float *spool = p.scores ? p.scores + ((int64_t)w.r * a.H + w.h) * p.score_ld * (int64_t)NC : nullptr;
       int j = w.step * G_::SLOTS + i * kTile + in;
       for (int s = 0; s < count; ++s, ++t) {
@@ -1719,7 +1741,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           y[c] = __uint_as_float(x[c]) * f * cs[c];
-          if (masked && (!there || j > (int)(w.len - w.fresh + (row0 + c) / a.G) || c >= rows)) y[c] = -INFINITY;
+          if (masked && (!there || j > (int)(first + (row0 + c) / a.G * more) || c >= rows)) y[c] = -INFINITY;
         }
         if (spool && j < p.score_ld) {
 #pragma unroll
@@ -2400,7 +2422,7 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   if (!encode(&mk, args->cache, a.k, sh.box) || !encode(&mv, args->cache, a.v, sh.box)) return KVX_ERR_CUDA;
   TcParams p;
   p.a = a;
-  p.a.stats = a.weights ? (float2 *)(ws + sh.stats) : nullptr;
+  if (a.weights) p.a.stats = (float2 *)(ws + sh.stats);
   p.grid = sh.grid;
   p.splits = (Split *)(ws + sh.splits);
   p.partial = (float *)(ws + sh.partial);

@@ -18,7 +18,12 @@ takes torch CUDA tensors, checks their shapes, dtypes and devices, and calls
 transferred cache: ``Rope`` (rotary positions of new queries and keys) and
 ``Cache8``, one layer's 8-bit paged cache with its ``write``, ``attend`` and
 ``evict``; low level ``kvx_rope_init``, ``kvx_rope_apply``, ``kvx_cache8_write``,
-``kvx_attend8`` and ``kvx_evict8`` with their ``*_workspace_bytes``.
+``kvx_attend8`` and ``kvx_evict8`` with their ``*_workspace_bytes``.  Several
+continuations of one prompt: ``Cache8.attend_shared`` (attention over a prefix
+that requests share and their own slots), ``Pages`` (references to a pool's pages,
+with ``fork``, ``reserve``, ``free`` and ``compact``), ``copy_pages`` and
+``beam_select``; low level ``kvx_attend8_shared``, ``kvx_pages_*``,
+``kvx_cache8_copy`` and ``kvx_beam_select``.
 """
 from __future__ import annotations
 
@@ -48,6 +53,7 @@ KVX_FLAG_BAD_SRC_BLOCK = 64
 KVX_FLAG_NOT_SPD = 128
 KVX_FLAG_BAD_LENGTH = 256
 KVX_FLAG_NOT_FINITE = 512
+KVX_FLAG_NO_PAGES = 1024
 
 KVX_F32 = 0
 KVX_BF16 = 1
@@ -74,7 +80,11 @@ EXPORTED = ("kvx_plan_create", "kvx_transfer", "kvx_plan_destroy",
             "kvx_layer_scores_workspace_bytes", "kvx_layer_scores",
             "kvx_rope_init", "kvx_rope_apply", "kvx_cache8_write",
             "kvx_attend8_workspace_bytes", "kvx_attend8",
-            "kvx_evict8_workspace_bytes", "kvx_evict8")
+            "kvx_evict8_workspace_bytes", "kvx_evict8",
+            "kvx_attend8_shared_workspace_bytes", "kvx_attend8_shared",
+            "kvx_pages_fork", "kvx_pages_free", "kvx_pages_reserve", "kvx_pages_compact",
+            "kvx_pages_workspace_bytes", "kvx_cache8_copy",
+            "kvx_beam_workspace_bytes", "kvx_beam_select")
 
 
 class PlanDesc(ctypes.Structure):
@@ -247,6 +257,71 @@ class Evict8Args(ctypes.Structure):
     ]
 
 
+class Attend8SharedArgs(ctypes.Structure):
+    _fields_ = [
+        ("own", Attend8Args), ("prefix_table", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+        ("groups", ctypes.c_void_p), ("max_prefix_blocks", ctypes.c_int32),
+        ("num_prefixes", ctypes.c_int32), ("max_prefix", ctypes.c_int32),
+        ("max_group", ctypes.c_int32),
+    ]
+
+
+class PagesForkArgs(ctypes.Structure):
+    _fields_ = [
+        ("refs", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32),
+        ("num_rows", ctypes.c_int32), ("width", ctypes.c_int32), ("table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p), ("parents", ctypes.c_void_p), ("num_new", ctypes.c_int32),
+        ("new_table", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class PagesFreeArgs(ctypes.Structure):
+    _fields_ = [
+        ("refs", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("num_rows", ctypes.c_int32),
+        ("width", ctypes.c_int32), ("table", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class PagesReserveArgs(ctypes.Structure):
+    _fields_ = [
+        ("refs", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32),
+        ("num_rows", ctypes.c_int32), ("width", ctypes.c_int32), ("table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p), ("add", ctypes.c_void_p), ("add_all", ctypes.c_int32),
+        ("copies", ctypes.c_void_p), ("caches", ctypes.c_void_p), ("num_caches", ctypes.c_int32),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class PagesCompactArgs(ctypes.Structure):
+    _fields_ = [
+        ("refs", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32),
+        ("tables", ctypes.c_void_p), ("entries", ctypes.c_void_p), ("num_tables", ctypes.c_int32),
+        ("used", ctypes.c_void_p), ("moved", ctypes.c_void_p), ("caches", ctypes.c_void_p),
+        ("num_caches", ctypes.c_int32), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p),
+    ]
+
+
+class Cache8CopyArgs(ctypes.Structure):
+    _fields_ = [
+        ("caches", ctypes.c_void_p), ("num_caches", ctypes.c_int32), ("pairs", ctypes.c_void_p),
+        ("num_pairs", ctypes.c_int32), ("count", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class BeamArgs(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("num_requests", ctypes.c_int32), ("beams", ctypes.c_int32), ("out_beams", ctypes.c_int32),
+        ("vocab", ctypes.c_int32), ("eos", ctypes.c_int32), ("scores", ctypes.c_void_p),
+        ("done", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+        ("new_scores", ctypes.c_void_p), ("new_done", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("status", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -306,12 +381,22 @@ def load():
                     ("kvx_rope_apply", [ctypes.c_void_p] * 3),
                     ("kvx_cache8_write", [ctypes.c_void_p] * 2),
                     ("kvx_attend8", [ctypes.c_void_p] * 2),
-                    ("kvx_evict8", [ctypes.c_void_p] * 2)):
+                    ("kvx_evict8", [ctypes.c_void_p] * 2),
+                    ("kvx_attend8_shared", [ctypes.c_void_p] * 2),
+                    ("kvx_pages_fork", [ctypes.c_void_p] * 2),
+                    ("kvx_pages_free", [ctypes.c_void_p] * 2),
+                    ("kvx_pages_reserve", [ctypes.c_void_p] * 2),
+                    ("kvx_pages_compact", [ctypes.c_void_p] * 2),
+                    ("kvx_cache8_copy", [ctypes.c_void_p] * 2),
+                    ("kvx_beam_select", [ctypes.c_void_p] * 2)):
                 getattr(lib, name).argtypes = argtypes
                 getattr(lib, name).restype = ctypes.c_int
-            for name in ("kvx_attend8_workspace_bytes", "kvx_evict8_workspace_bytes"):
+            for name in ("kvx_attend8_workspace_bytes", "kvx_evict8_workspace_bytes",
+                         "kvx_attend8_shared_workspace_bytes", "kvx_beam_workspace_bytes"):
                 getattr(lib, name).argtypes = [ctypes.c_void_p]
                 getattr(lib, name).restype = ctypes.c_size_t
+            lib.kvx_pages_workspace_bytes.argtypes = [ctypes.c_int64]
+            lib.kvx_pages_workspace_bytes.restype = ctypes.c_size_t
             _lib = lib
     return _lib
 
@@ -405,6 +490,46 @@ def kvx_evict8_workspace_bytes(args: Evict8Args) -> int:
 
 def kvx_evict8(args: Evict8Args, stream) -> int:
     return load().kvx_evict8(ctypes.byref(args), stream)
+
+
+def kvx_attend8_shared_workspace_bytes(args: Attend8SharedArgs) -> int:
+    return int(load().kvx_attend8_shared_workspace_bytes(ctypes.byref(args)))
+
+
+def kvx_attend8_shared(args: Attend8SharedArgs, stream) -> int:
+    return load().kvx_attend8_shared(ctypes.byref(args), stream)
+
+
+def kvx_pages_fork(args: PagesForkArgs, stream) -> int:
+    return load().kvx_pages_fork(ctypes.byref(args), stream)
+
+
+def kvx_pages_free(args: PagesFreeArgs, stream) -> int:
+    return load().kvx_pages_free(ctypes.byref(args), stream)
+
+
+def kvx_pages_reserve(args: PagesReserveArgs, stream) -> int:
+    return load().kvx_pages_reserve(ctypes.byref(args), stream)
+
+
+def kvx_pages_compact(args: PagesCompactArgs, stream) -> int:
+    return load().kvx_pages_compact(ctypes.byref(args), stream)
+
+
+def kvx_pages_workspace_bytes(num_blocks: int) -> int:
+    return int(load().kvx_pages_workspace_bytes(int(num_blocks)))
+
+
+def kvx_cache8_copy(args: Cache8CopyArgs, stream) -> int:
+    return load().kvx_cache8_copy(ctypes.byref(args), stream)
+
+
+def kvx_beam_workspace_bytes(args: BeamArgs) -> int:
+    return int(load().kvx_beam_workspace_bytes(ctypes.byref(args)))
+
+
+def kvx_beam_select(args: BeamArgs, stream) -> int:
+    return load().kvx_beam_select(ctypes.byref(args), stream)
 
 
 def ridge_fit(x, y, lam: float = 0.01, w=None, b=None, workspace=None, status=None,
@@ -780,6 +905,11 @@ _pack_rope = _packer(RopeArgs)
 _pack_write = _packer(Cache8WriteArgs)
 _pack_attend = _packer(Attend8Args)
 _pack_evict = _packer(Evict8Args)
+_pack_shared = _packer(Attend8SharedArgs)
+_pack_cache = _packer(Cache8Desc)
+_pack_fork = _packer(PagesForkArgs)
+_pack_reserve = _packer(PagesReserveArgs)
+_pack_beam = _packer(BeamArgs)
 
 
 class _Fast:
@@ -795,6 +925,8 @@ class _Fast:
         cls.codes = {torch.float32: KVX_F32, torch.bfloat16: KVX_BF16}
         cls.rope, cls.write = lib.kvx_rope_apply, lib.kvx_cache8_write
         cls.attend, cls.evict = lib.kvx_attend8, lib.kvx_evict8
+        cls.shared, cls.fork = lib.kvx_attend8_shared, lib.kvx_pages_fork
+        cls.reserve, cls.beam = lib.kvx_pages_reserve, lib.kvx_beam_select
         cls.empty = torch.empty
         cls.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         cls.raw = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -1050,18 +1182,7 @@ class Cache8:
         if lens.shape[0] != R or (cu_seqlens is not None and cu_seqlens.shape[0] != R + 1):
             raise ValueError("lens, cu_seqlens and block_table must hold the same requests")
         code = _code_of(dt)
-        if out is None:
-            out = _new(stream, (n, hq, d), dt, dev)
-            os_ = (hq * d, d, 1)
-        else:
-            os_, m = _heads(out, "out", dt, dev, hq, d)
-            if m != n:
-                raise ValueError("out has another number of tokens")
-        if lse is None:
-            lse = _new(stream, (n, hq), _Fast.f32, dev)
-        elif lse.dtype is not _Fast.f32 or tuple(lse.shape) != (n, hq) or lse.device != dev or \
-                not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous fp32 [{n}][{hq}] tensor on {dev}")
+        out, os_, lse = self._attend_outputs(out, lse, n, hq, dt, stream)
         wptr = wstride = 0
         if weights is not None:
             wptr, wstride = self._weights(weights, R)
@@ -1076,6 +1197,91 @@ class Cache8:
         st = _Fast.attend(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_attend8")
+        return out, lse
+
+    def _attend_outputs(self, out, lse, n, hq, dt, stream):
+        """The outputs of n queries, checked or allocated, and the strides of the first."""
+        dev, d = self.device, self.head_dim
+        if out is None:
+            out = _new(stream, (n, hq, d), dt, dev)
+            os_ = (hq * d, d, 1)
+        else:
+            os_, m = _heads(out, "out", dt, dev, hq, d)
+            if m != n:
+                raise ValueError("out has another number of tokens")
+        if lse is None:
+            lse = _new(stream, (n, hq), _Fast.f32, dev)
+        elif lse.dtype is not _Fast.f32 or tuple(lse.shape) != (n, hq) or lse.device != dev or \
+                not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous fp32 [{n}][{hq}] tensor on {dev}")
+        return out, os_, lse
+
+    def attend_shared_workspace(self, *, ntok, num_requests, q_heads, max_prefix, max_len,
+                                num_prefixes=1, max_group=None, max_new=1, dtype=None):
+        """A workspace (uint8) for ``attend_shared`` calls of at most these sizes
+        and queries of ``dtype`` (bf16) that are ordered on one stream."""
+        import torch
+        a = Attend8SharedArgs()
+        own, any_ptr = a.own, self.k_codes.data_ptr()     # sizes only: never read
+        own.cache = Cache8Desc(*self._head, 1, any_ptr)
+        own.dtype = _dtype_code(torch.bfloat16 if dtype is None else dtype)
+        own.q_heads, own.ntok, own.num_requests = q_heads, ntok, num_requests
+        own.max_new, own.max_len, own.scale = max_new, max_len, 1.0
+        own.lens = own.cu_seqlens = a.prefix_table = a.prefix_lens = a.groups = any_ptr
+        a.max_prefix_blocks, a.num_prefixes, a.max_prefix = 1, num_prefixes, max_prefix
+        a.max_group = num_requests if max_group is None else max_group
+        need = kvx_attend8_shared_workspace_bytes(a)
+        if need == 0:
+            raise KvxError(KVX_ERR_INVALID_ARG, "kvx_attend8_shared_workspace_bytes")
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        ws[:_WORKSPACE_HEAD].zero_()
+        return ws
+
+    def attend_shared(self, q, prefix_table, prefix_lens, block_table, lens, *, max_prefix, max_len,
+                      groups=None, max_group=None, cu_seqlens=None, max_new=1, scale=None, out=None,
+                      lse=None, workspace=None, status=None, stream=None):
+        """Attention of requests that share prefixes: as ``attend`` of sequences
+        that hold a prefix's slots and then the request's own.  Requests
+        groups[p] .. groups[p + 1] - 1 (``groups`` [P + 1]; without it all) have
+        the slots of row p of ``prefix_table`` (``prefix_lens`` [P], at most
+        ``max_prefix``) before those of ``block_table`` and ``lens``; a prefix has
+        at most ``max_group`` requests (more: nothing is written, and ``status``
+        tells).  The new queries are the last of a request's own slots.  A prefix
+        is read once for its whole group.  Returns (out, lse [tokens][q_heads])
+        over both.  Scratch is allocated here unless ``workspace`` (from
+        ``attend_shared_workspace``) is given."""
+        dev, dt = self.device, q.dtype
+        _on_device(dev)
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens][q_heads][d]")
+        hq, d = q.shape[1], self.head_dim
+        qs, n = _heads(q, "q", dt, dev, hq, d)
+        table = self._table(block_table)
+        R, P = block_table.shape[0], prefix_lens.shape[0]
+        if lens.shape[0] != R or (cu_seqlens is not None and cu_seqlens.shape[0] != R + 1):
+            raise ValueError("lens, cu_seqlens and block_table must hold the same requests")
+        before = _int_table(prefix_table, "prefix_table", dev, 2)
+        if prefix_table.shape[0] != P or (P != 1 if groups is None else groups.shape[0] != P + 1):
+            raise ValueError("prefix_table, prefix_lens and groups must hold the same prefixes")
+        code = _code_of(dt)
+        out, os_, lse = self._attend_outputs(out, lse, n, hq, dt, stream)
+        if max_group is None:
+            max_group = R
+        if workspace is None:
+            workspace = _on_stream(self.attend_shared_workspace, stream, ntok=n, num_requests=R,
+                                   q_heads=hq, max_prefix=max_prefix, max_len=max_len,
+                                   num_prefixes=P, max_group=max_group, max_new=max_new, dtype=dt)
+        a = _pack_shared(*table, q.data_ptr(), out.data_ptr(), qs[0], qs[1], os_[0], os_[1], code,
+                         hq, n, R, max_new, _int_table(cu_seqlens, "cu_seqlens", dev),
+                         _int_table(lens, "lens", dev), max_len,
+                         d ** -0.5 if scale is None else scale, lse.data_ptr(), 0, 0,
+                         *_workspace(workspace, dev), _status_ptr(status, dev), before,
+                         _int_table(prefix_lens, "prefix_lens", dev),
+                         _int_table(groups, "groups", dev), prefix_table.shape[1], P, max_prefix,
+                         max_group)
+        st = _Fast.shared(a, _raw_stream(stream, dev))
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_attend8_shared")
         return out, lse
 
     def _weights(self, w, R):
@@ -1143,6 +1349,254 @@ class Cache8:
         if st != KVX_OK:
             raise KvxError(st, "kvx_evict8")
         return kept, kept_weights, new_lens
+
+
+def _cache_array(caches, num_blocks, device):
+    """The caches as an array of ``kvx_cache8`` (kept by the caller for the call) and its address."""
+    for c in caches:
+        if c.device != device or c.num_blocks != num_blocks:
+            raise ValueError(f"caches must hold {num_blocks} blocks on {device}")
+    if not caches:
+        return None, 0
+    # the block table is not used: any aligned address
+    raw = b"".join(_pack_cache(*c._head, 1, c._head[2]) for c in caches)
+    return raw, ctypes.cast(raw, ctypes.c_void_p).value
+
+
+class Pages:
+    """References to the pages (blocks) of a pool: ``refs`` [num_blocks] int32
+    counts the entries of block tables that hold each, 0 for a free page.  A
+    table's entries of -1 hold none.  The caches of all layers share one set of
+    tables and one ``Pages``.  ``Pages.empty`` starts with all pages free."""
+
+    def __init__(self, refs, block_size):
+        import torch
+        if refs.dtype != torch.int32 or refs.dim() != 1 or not refs.is_contiguous():
+            raise ValueError("refs must be a contiguous 1-D int32 tensor")
+        self.refs, self.block_size, self.device = refs, int(block_size), refs.device
+        self.num_blocks = refs.shape[0]
+
+    @classmethod
+    def empty(cls, num_blocks, block_size, device="cuda"):
+        import torch
+        return cls(torch.zeros(num_blocks, dtype=torch.int32, device=device), block_size)
+
+    def workspace(self):
+        """A workspace (uint8) for ``reserve`` and ``compact`` calls that are
+        ordered on one stream."""
+        import torch
+        need = kvx_pages_workspace_bytes(self.num_blocks)
+        if need == 0:
+            raise KvxError(KVX_ERR_INVALID_ARG, "kvx_pages_workspace_bytes")
+        return torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def _rows(self, table, lens, name="table"):
+        ptr = _int_table(table, name, self.device, 2)
+        if lens is not None and lens.shape[0] != table.shape[0]:
+            raise ValueError(f"lens and {name} must hold the same rows")
+        return table.shape[0], table.shape[1], ptr
+
+    def fork(self, table, lens, parents, *, new_table=None, new_lens=None, status=None, stream=None):
+        """New rows in place of those of ``table`` [R][width]: row n continues
+        row parents[n] (-1: an empty row) and shares the pages that its length
+        covers.  The old rows hold nothing afterwards.  Returns (new_table
+        [N][width], new_lens [N])."""
+        dev = self.device
+        _on_device(dev)
+        R, width, ptr = self._rows(table, lens)
+        parent = _int_table(parents, "parents", dev)
+        N = parents.shape[0]
+        if new_table is None:
+            new_table = _new(stream, (N, width), _Fast.i32, dev)
+        elif tuple(new_table.shape) != (N, width):
+            raise ValueError("new_table must be [N][width]")
+        if new_lens is None:
+            new_lens = _new(stream, (N,), _Fast.i32, dev)
+        elif tuple(new_lens.shape) != (N,):
+            raise ValueError("new_lens must be [N]")
+        a = _pack_fork(self.refs.data_ptr(), self.num_blocks, self.block_size, R, width, ptr,
+                       _int_table(lens, "lens", dev), parent, N,
+                       _int_table(new_table, "new_table", dev, 2),
+                       _int_table(new_lens, "new_lens", dev), _status_ptr(status, dev))
+        st = _Fast.fork(a, _raw_stream(stream, dev))
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_pages_fork")
+        return new_table, new_lens
+
+    def free(self, table, *, status=None, stream=None):
+        """The rows of ``table`` (some rows of one: a slice) release their pages;
+        their entries become -1."""
+        dev = self.device
+        _on_device(dev)
+        R, width, ptr = self._rows(table, None)
+        a = PagesFreeArgs(self.refs.data_ptr(), self.num_blocks, R, width, ptr,
+                          _status_ptr(status, dev))
+        st = kvx_pages_free(a, _raw_stream(stream, dev))
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_pages_free")
+
+    def reserve(self, table, lens, new=1, *, max_new=None, caches=(), copies=None, workspace=None,
+                status=None, stream=None):
+        """Make slots lens .. lens + new - 1 of every row of ``table`` writable:
+        each behind a page of the row's own, taken from the free ones where
+        there is none or others hold it too; a page that holds slots of the
+        row is then copied in all ``caches``.  ``new`` is one number, or
+        one for each row (int32 tensor, at most ``max_new``).  Returns
+        the copied pages [R][2], from and to (-1: none).  With too few free
+        pages nothing changes, and ``status`` tells (KVX_FLAG_NO_PAGES)."""
+        dev = self.device
+        _on_device(dev)
+        R, width, ptr = self._rows(table, lens)
+        add = 0
+        if isinstance(new, int):
+            most = new
+        else:
+            add = _int_table(new, "new", dev)
+            if new.shape[0] != R:
+                raise ValueError("new must hold one entry for each row")
+            most = width * self.block_size if max_new is None else max_new
+        if copies is None:
+            copies = _new(stream, (R, 2), _Fast.i32, dev)
+        elif tuple(copies.shape) != (R, 2):
+            raise ValueError("copies must be [R][2]")
+        if workspace is None:
+            workspace = _on_stream(self.workspace, stream)
+        keep, array = _cache_array(caches, self.num_blocks, dev)
+        a = _pack_reserve(self.refs.data_ptr(), self.num_blocks, self.block_size, R, width, ptr,
+                          _int_table(lens, "lens", dev), add, most,
+                          _int_table(copies, "copies", dev, 2), array, len(caches),
+                          *_workspace(workspace, dev), _status_ptr(status, dev))
+        st = _Fast.reserve(a, _raw_stream(stream, dev))
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_pages_reserve")
+        return copies
+
+    def compact(self, tables, caches=(), *, used=None, moved=None, workspace=None, status=None,
+                stream=None):
+        """Move the held pages to the lowest numbers, in all ``caches``, and
+        rewrite ``tables`` (up to eight int32 tensors, which hold all
+        references).  Returns (used [1], moved [num_blocks]): how many pages are
+        held, and each page's new number (-1: it is free)."""
+        dev = self.device
+        _on_device(dev)
+        if used is None:
+            used = _new(stream, (1,), _Fast.i32, dev)
+        if moved is None:
+            moved = _new(stream, (self.num_blocks,), _Fast.i32, dev)
+        elif tuple(moved.shape) != (self.num_blocks,):
+            raise ValueError("moved must be [num_blocks]")
+        if workspace is None:
+            workspace = _on_stream(self.workspace, stream)
+        keep, array = _cache_array(caches, self.num_blocks, dev)
+        n = len(tables)
+        ptrs = (ctypes.c_void_p * max(1, n))(*[_int_table(t, "tables", dev, t.dim()) for t in tables])
+        entries = (ctypes.c_int64 * max(1, n))(*[t.numel() for t in tables])
+        a = PagesCompactArgs(self.refs.data_ptr(), self.num_blocks, self.block_size,
+                             ctypes.addressof(ptrs), ctypes.addressof(entries), n,
+                             _int_table(used, "used", dev), _int_table(moved, "moved", dev), array,
+                             len(caches), *_workspace(workspace, dev), _status_ptr(status, dev))
+        st = kvx_pages_compact(a, _raw_stream(stream, dev))
+        if st != KVX_OK:
+            raise KvxError(st, "kvx_pages_compact")
+        return used, moved
+
+
+def copy_pages(caches, pairs, count=None, *, status=None, stream=None):
+    """Copy whole pages, codes and scales, in all ``caches`` (``kvx_cache8_copy``):
+    from page pairs[i][0] to page pairs[i][1] (pairs with a negative one are
+    skipped); with ``count`` [1] only the first count[0]."""
+    if not caches:
+        return
+    dev = caches[0].device
+    _on_device(dev)
+    keep, array = _cache_array(caches, caches[0].num_blocks, dev)
+    ptr = _int_table(pairs, "pairs", dev, 2)
+    if pairs.shape[1] != 2:
+        raise ValueError("pairs must be [pairs][2]")
+    a = Cache8CopyArgs(array, len(caches), ptr, pairs.shape[0], _int_table(count, "count", dev),
+                       _status_ptr(status, dev))
+    st = kvx_cache8_copy(a, _raw_stream(stream, dev))
+    if st != KVX_OK:
+        raise KvxError(st, "kvx_cache8_copy")
+
+
+def beam_workspace(*, requests, beams, vocab, out=None, device="cuda"):
+    """A workspace (uint8) for ``beam_select`` calls of at most these sizes that
+    are ordered on one stream."""
+    import torch
+    a = BeamArgs(dtype=KVX_F32, num_requests=requests, beams=beams,
+                 out_beams=beams if out is None else out, vocab=vocab, eos=-1)
+    need = kvx_beam_workspace_bytes(a)
+    if need == 0:
+        raise KvxError(KVX_ERR_INVALID_ARG, "kvx_beam_workspace_bytes")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def beam_select(logits, scores, *, beams=None, eos=None, done=None, tokens=None, parents=None,
+                new_scores=None, new_done=None, workspace=None, status=None, stream=None):
+    """Beam search's selection (``kvx_beam_select``): of the candidates of each
+    request, scores[b][k] + log_softmax(logits[b * K + k])[v], the ``beams`` (K) of
+    the largest score, equal ones by k and v.  ``logits`` [B * K][V] (fp32 or bf16,
+    unit stride inside a row), ``scores`` [B][K] fp32 (-inf: no beam); beams that
+    are ``done`` [B][K] (bool) have one candidate, ``eos`` with the score they
+    have.  Returns (tokens, parents, scores, done) [B][beams]: parents are rows of
+    logits, as ``Pages.fork`` takes them (-1, with a score of -inf: no candidate);
+    done is None without ``eos``."""
+    dev = logits.device
+    _on_device(dev)
+    if logits.dim() != 2 or logits.stride(1) != 1 and logits.shape[1] > 1:
+        raise ValueError("logits must be [beams][vocab] with unit stride inside a row")
+    if scores.dtype is not _Fast.f32 or scores.dim() != 2 or scores.device != dev or \
+            not scores.is_contiguous() or scores.numel() != logits.shape[0]:
+        raise ValueError(f"scores must be a contiguous fp32 [requests][beams] tensor on {dev}, "
+                         f"one for each row of logits")
+    B, K = scores.shape
+    N = K if beams is None else beams
+    torch = _Fast.torch
+    done_ptr = new_done_ptr = 0
+    if done is not None:
+        if eos is None:
+            raise ValueError("done needs eos")
+        done_ptr = _flags(done, "done", (B, K), dev)
+    tokens = _output(tokens, "tokens", (B, N), _Fast.i32, dev, stream)
+    parents = _output(parents, "parents", (B, N), _Fast.i32, dev, stream)
+    new_scores = _output(new_scores, "new_scores", (B, N), _Fast.f32, dev, stream)
+    if eos is not None:
+        if new_done is None:
+            new_done = _new(stream, (B, N), torch.bool, dev)
+        new_done_ptr = _flags(new_done, "new_done", (B, N), dev)
+    elif new_done is not None:
+        raise ValueError("new_done needs eos")
+    if workspace is None:
+        workspace = _on_stream(beam_workspace, stream, requests=B, beams=K, vocab=logits.shape[1],
+                               out=N, device=dev)
+    a = _pack_beam(logits.data_ptr(), logits.stride(0), _code_of(logits.dtype), B, K, N,
+                   logits.shape[1], -1 if eos is None else eos, scores.data_ptr(), done_ptr,
+                   tokens.data_ptr(), parents.data_ptr(), new_scores.data_ptr(), new_done_ptr,
+                   *_workspace(workspace, dev), _status_ptr(status, dev))
+    st = _Fast.beam(a, _raw_stream(stream, dev))
+    if st != KVX_OK:
+        raise KvxError(st, "kvx_beam_select")
+    return tokens, parents, new_scores, new_done
+
+
+def _flags(t, name, shape, device):
+    """Data pointer of a contiguous bool (or uint8) tensor."""
+    torch = _Fast.torch
+    if t.dtype not in (torch.bool, torch.uint8) or tuple(t.shape) != shape or t.device != device or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bool {list(shape)} tensor on {device}")
+    return t.data_ptr()
+
+
+def _output(t, name, shape, dtype, device, stream):
+    """An output, checked or allocated."""
+    if t is None:
+        return _new(stream, shape, dtype, device)
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
+    return t
 
 
 def _new(stream, shape, dtype, device):

@@ -94,7 +94,10 @@ typedef enum {
                                         bound (max_len, the table's width)   */
 #define KVX_FLAG_NOT_FINITE    512u  /* kvx_cache8_write: an infinity (stored as
                                         the block's largest code) or a NaN
-                                        (stored as 0)                        */
+                                        (stored as 0); kvx_beam_select: a
+                                        logit or score that is NaN or +inf   */
+#define KVX_FLAG_NO_PAGES     1024u  /* kvx_pages_reserve: fewer pages are free
+                                        than the call needs: nothing changes */
 
 typedef enum { KVX_F32 = 0, KVX_BF16 = 1 } kvx_dtype;
 typedef enum { KVX_CONTIGUOUS = 0, KVX_PAGED = 1 } kvx_layout;
@@ -779,6 +782,215 @@ size_t kvx_evict8_workspace_bytes(const kvx_evict8_args *args);
  * id outside it dropped (KVX_FLAG_BAD_BLOCK).  One or two launches.  max_len is
  * at most 2^31 - 1025. */
 kvx_status kvx_evict8(const kvx_evict8_args *args, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Several continuations of one transferred prompt: samples, the beams of a
+ * search, users who ask about one document.  Each request then holds a prefix,
+ * which it shares with others, and slots of its own; its pages are counted, so
+ * that rows of a block table may share them; and beam search chooses which rows
+ * go on.  As for the calls above, these only validate on the host and enqueue
+ * kernels; what only the device can see is bounds-checked, skipped and flagged.
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  kvx_attend8_args own;     /* as for kvx_attend8, of the requests' own slots; out and
+                               lse are those of prefix and own slots together;
+                               no weights; kvx_attend8_shared_workspace_bytes() */
+  const int32_t *prefix_table;  /* [P][max_prefix_blocks] blocks of own.cache's pool  */
+  const int32_t *prefix_lens;   /* [P] slots of each prefix                   */
+  const int32_t *groups;    /* [P+1] requests groups[p] .. groups[p+1]-1 have prefix
+                               p, or NULL: P == 1, all of them                */
+  int32_t max_prefix_blocks;    /* width of the prefix table, >= 1            */
+  int32_t num_prefixes;     /* P >= 1                                         */
+  int32_t max_prefix;       /* bound on prefix_lens                           */
+  int32_t max_group;        /* bound on one prefix's requests, >= 1; any looser
+                               than R counts as R                             */
+} kvx_attend8_shared_args;
+
+/* Scratch of kvx_attend8_shared calls of at most these sizes, as
+ * kvx_attend8_workspace_bytes (its first 1024 bytes zero-filled before the first
+ * use); 0 for sizes that it refuses.  Its calls and those of kvx_attend8 may use
+ * one workspace that is large enough for both. */
+size_t kvx_attend8_shared_workspace_bytes(const kvx_attend8_shared_args *args);
+
+/* Attention of requests that share prefixes: query i of a request with n new
+ * tokens sees all prefix_lens[p] slots of its group's prefix and its own slots
+ * j <= lens[r] - n + i,
+ *   out_i = sum_j p_ij v_j,  p_ij = exp(scale q_i.k_j - lse_i)
+ * over both, as kvx_attend8 of one sequence that holds the prefix's slots and then
+ * the request's.  The prefix's last block may be part full, and its blocks
+ * need not be the requests'.  A prefix is read once for its group, not once for
+ * each request, and multiplied with the rows of all of them at once; what that
+ * gives is kept in fp32 until it is joined with the request's own slots.  A length
+ * outside its bound counts as 0 (KVX_FLAG_BAD_LENGTH); slots of a block id outside the pool
+ * are masked (KVX_FLAG_BAD_BLOCK); a malformed request or group table, or a group
+ * with more than max_group * max_new queries, writes neither out nor lse
+ * (KVX_FLAG_BAD_SEQLENS).  Accuracy as of kvx_attend8.  Two to four launches.
+ * KVX_ERR_INVALID_ARG also for weights, and without groups for P != 1. */
+kvx_status kvx_attend8_shared(const kvx_attend8_shared_args *args, void *stream);
+
+/* References to the pages (blocks) of a pool: refs[b] is the number of entries
+ * of block tables that hold page b, 0 for a free one.  A table's rows hold their
+ * entries that are not -1.  The calls below keep refs and the tables that they
+ * are given in step; a program starts with refs and tables of zeros and -1.  All
+ * caches of a model's layers share one set of tables and refs. */
+
+typedef struct {
+  int32_t *refs;            /* [num_blocks]                                   */
+  int64_t num_blocks;       /* 1 .. 2^31 - 1025                               */
+  int32_t block_size;       /* slots a page, 1..1024                          */
+  int32_t num_rows;         /* R, >= 0                                        */
+  int32_t width;            /* of the tables, >= 1; width * block_size at most
+                               2^31 - 1025                                    */
+  const int32_t *table;     /* [R][width]; its rows release what they hold    */
+  const int32_t *lens;      /* [R] slots of each row                          */
+  const int32_t *parents;   /* [N] row of `table` that each new row continues,
+                               or -1: an empty row                            */
+  int32_t num_new;          /* N, >= 0                                        */
+  int32_t *new_table;       /* [N][width]; overlaps no table                  */
+  int32_t *new_lens;        /* [N]; overlaps no lens                          */
+  uint32_t *status;
+} kvx_pages_fork_args;
+
+/* New rows in place of old ones (beam search's reordering, forked samples, rows
+ * kept of a batch): new row n holds its parent's pages of ceil(len / block_size)
+ * entries, shared with the parent's other children, and the parent's length;
+ * its other entries are -1.  Then the old rows hold nothing: pages that no new row
+ * holds are free, those reserved beyond an old row's length among them.  Nothing
+ * is copied: kvx_pages_reserve does that before a shared page is written.  A parent
+ * outside [-1, R) gives an empty row (KVX_FLAG_BAD_ROW), a length outside
+ * [0, width * block_size] counts as 0 (KVX_FLAG_BAD_LENGTH), an entry outside
+ * [-1, num_blocks), or of -1 below a row's length, becomes -1 (KVX_FLAG_BAD_BLOCK).  One launch. */
+kvx_status kvx_pages_fork(const kvx_pages_fork_args *args, void *stream);
+
+typedef struct {
+  int32_t *refs;            /* [num_blocks]                                   */
+  int64_t num_blocks;
+  int32_t num_rows, width;
+  int32_t *table;           /* [R][width], becomes -1                         */
+  uint32_t *status;
+} kvx_pages_free_args;
+
+/* The rows release their pages and hold nothing: their entries become -1.  An
+ * entry outside [-1, num_blocks) releases nothing (KVX_FLAG_BAD_BLOCK).  One
+ * launch. */
+kvx_status kvx_pages_free(const kvx_pages_free_args *args, void *stream);
+
+typedef struct {
+  int32_t *refs;            /* [num_blocks]                                   */
+  int64_t num_blocks;
+  int32_t block_size, num_rows, width;
+  int32_t *table;           /* [R][width]                                     */
+  const int32_t *lens;      /* [R] slots that each row holds                  */
+  const int32_t *add;       /* [R] slots to reserve for each row, or NULL     */
+  int32_t add_all;          /* the same for all rows, >= 0 (with add: a bound on it) */
+  int32_t *copies;          /* [R][2] pages copied, from and to, else -1, -1  */
+  const kvx_cache8 *caches; /* HOST array [num_caches] of the layers' caches, with
+                               num_blocks and block_size as here (their block
+                               tables are not used); or NULL                  */
+  int32_t num_caches;       /* >= 0                                           */
+  void *workspace;          /* kvx_pages_workspace_bytes(num_blocks), 256-byte
+                               aligned; for calls ordered on one stream       */
+  size_t workspace_bytes;
+  uint32_t *status;
+} kvx_pages_reserve_args;
+
+/* Make slots lens[r] .. lens[r] + add - 1 of every row writable: a page of the
+ * row's own behind each.  In the order of rows, and of slots in a row: where a row
+ * has no page it takes a free one, where others hold the page as well it lets go
+ * of it and takes a free one (the last of its holders keeps it), and where
+ * such a page holds slots of the row it is copied for all caches, codes and
+ * scales.  The i-th page taken is the i-th free one, by number, before the call.
+ * If fewer are free than are needed nothing changes (KVX_FLAG_NO_PAGES, copies all
+ * -1): free some and call again.  A row whose length or whose new slots do not fit
+ * its width reserves nothing (KVX_FLAG_BAD_LENGTH); an entry outside
+ * [-1, num_blocks) counts as -1 (KVX_FLAG_BAD_BLOCK).  Asynchronous; one to four
+ * launches, and one for every 32 caches. */
+kvx_status kvx_pages_reserve(const kvx_pages_reserve_args *args, void *stream);
+
+typedef struct {
+  int32_t *refs;            /* [num_blocks]                                   */
+  int64_t num_blocks;
+  int32_t block_size;
+  int32_t *const *tables;   /* HOST array of tables to rewrite (device pointers);
+                               or NULL                                        */
+  const int64_t *entries;   /* HOST array: entries of each                    */
+  int32_t num_tables;       /* 0..8                                           */
+  int32_t *used;            /* [1] pages that are held                        */
+  int32_t *moved;           /* [num_blocks] new number of each page, -1: it is free */
+  const kvx_cache8 *caches; /* as for kvx_pages_reserve                       */
+  int32_t num_caches;
+  void *workspace;          /* kvx_pages_workspace_bytes(num_blocks)          */
+  size_t workspace_bytes;
+  uint32_t *status;
+} kvx_pages_compact_args;
+
+/* Move the held pages to numbers 0 .. used - 1: those at or beyond `used`, in
+ * their order, into the free ones below it, for all caches, and rewrite the tables
+ * by `moved`.  All tables that hold pages of the pool must be among them, or be
+ * rewritten by `moved` afterwards.  An entry outside [-1, num_blocks) stays
+ * (KVX_FLAG_BAD_BLOCK); one of a free page becomes -1.  Two or three launches, and one
+ * for every 32 caches. */
+kvx_status kvx_pages_compact(const kvx_pages_compact_args *args, void *stream);
+
+/* Scratch of the two calls above; 0 for a num_blocks that they refuse. */
+size_t kvx_pages_workspace_bytes(int64_t num_blocks);
+
+typedef struct {
+  const kvx_cache8 *caches; /* HOST array, as for kvx_pages_reserve; all of one
+                               num_blocks                                     */
+  int32_t num_caches;       /* >= 0                                           */
+  const int32_t *pairs;     /* [num_pairs][2] page copied from, to            */
+  int32_t num_pairs;        /* >= 0                                           */
+  const int32_t *count;     /* [1] pairs that count, at most num_pairs, or NULL: all */
+  uint32_t *status;
+} kvx_cache8_copy_args;
+
+/* Copy whole pages, codes and scales, in all caches.  A pair with a negative
+ * page is skipped, one with a page outside the pool too (KVX_FLAG_BAD_BLOCK), a count
+ * outside [0, num_pairs] copies nothing (KVX_FLAG_BAD_LENGTH).  A page that is copied to must be
+ * copied to once, and not be copied from.  One launch for every 32 caches. */
+kvx_status kvx_cache8_copy(const kvx_cache8_copy_args *args, void *stream);
+
+typedef struct {
+  const void *logits;       /* [B * K][V], unit stride inside a row           */
+  int64_t row_stride;       /* elements                                       */
+  int32_t dtype;            /* kvx_dtype                                      */
+  int32_t num_requests;     /* B >= 0                                         */
+  int32_t beams;            /* K of a request, 1..32                          */
+  int32_t out_beams;        /* N that go on, 1..32                            */
+  int32_t vocab;            /* V >= 1                                         */
+  int32_t eos;              /* token that ends a beam, or -1                  */
+  const float *scores;      /* [B][K] log-probability of each beam so far; -inf:
+                               no beam                                        */
+  const uint8_t *done;      /* [B][K] nonzero: the beam has ended; or NULL    */
+  int32_t *tokens;          /* [B][N]                                         */
+  int32_t *parents;         /* [B][N] row b * K + k that each continues       */
+  float *new_scores;        /* [B][N]; overlaps no scores                     */
+  uint8_t *new_done;        /* [B][N], or NULL; overlaps no done              */
+  void *workspace;          /* kvx_beam_workspace_bytes(), 256-byte aligned; for
+                               calls ordered on one stream                    */
+  size_t workspace_bytes;
+  uint32_t *status;
+} kvx_beam_args;
+
+/* Scratch of kvx_beam_select calls of at most these sizes (requests, beams,
+ * out_beams, vocab); 0 for sizes that it refuses. */
+size_t kvx_beam_workspace_bytes(const kvx_beam_args *args);
+
+/* Beam search's selection: of every request's candidates the N of the largest score,
+ *   score(k, v) = scores[k] + logits[k][v] - log sum_u exp(logits[k][u]),
+ * in falling order; equal ones by k, then v.  A beam that has ended has one candidate:
+ * eos, with the score that it has.  new_done: the token is eos.  Logits of -inf
+ * and beams whose score is -inf give no candidates; a request with fewer than N
+ * has tokens and parents of -1 and scores of -inf behind them.  A logit that is
+ * NaN or +inf counts as -inf, a beam whose score is NaN or +inf as none
+ * (KVX_FLAG_NOT_FINITE).  Each beam's logits are read once; scores are ranked as
+ * fp64 sums of the fp32 (or bf16) logits, the scores and log-sum-exps that are
+ * known to about 2^-22, and rounded to fp32 when they are written.  parents are what
+ * kvx_pages_fork takes.  Two launches.  KVX_ERR_INVALID_ARG also for eos outside
+ * [-1, V), and for done without eos. */
+kvx_status kvx_beam_select(const kvx_beam_args *args, void *stream);
 
 #ifdef __cplusplus
 }
