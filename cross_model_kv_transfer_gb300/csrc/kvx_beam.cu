@@ -4,14 +4,19 @@
 // Of a beam's candidates only its N largest logits can be chosen, so one pass over a row
 // finds those and the row's sum of exponentials, and the beams' lists are ranked after.
 //
-// A row is read by a cluster of eight CTAs, each a contiguous share of it, in chunks
-// that the threads hold in registers.  The largest logit of each thread is ranked among
-// the CTA's: the N-th of them bounds the chunk's N-th largest from below, and at most N
-// threads have anything above it.  What lies above goes to a list in shared memory, is
-// ranked there with the N that were found before, and the first N stay.  Keys are 64 bits, the
-// logit in an order-preserving form and behind it the falling position: no two are equal,
-// so nothing depends on the order in which a list was filled.  Sums are fp32 over a
-// thread's elements, relative to its running maximum, fp64 over threads and CTAs.
+// A row is read by a cluster of one to eight CTAs, each a contiguous share of it, in
+// chunks that the threads hold in registers.  Each warp's q-th largest of its lanes' largest
+// logits, q = N / 8 rounded up, is exceeded or equalled by q logits; the least of the
+// eight warps' is below N of the chunk, so only what is not below it, nor below the N-th of
+// what was found before, can be among the N largest.  That goes to a list in
+// shared memory, is ranked there with what was found before, and the first N stay.  Where
+// too many logits are equal to the bound the threads' largest are ranked as 64-bit keys
+// instead: at most N threads have anything not below the N-th of them.  Keys are
+// the logit in an order-preserving form and behind it the falling position: no two are
+// equal, so nothing depends on the order in which a list was filled.
+//
+// Sums of exponentials are relative to a thread's running maximum, fp32 over a warp's
+// elements and fp64 above (about as many additions as there are warps: fp64 is slow here).
 //
 // Bound by HBM where there are many rows, by the latency of a chunk's ranking (a few
 // barriers) where there are few.
@@ -38,7 +43,7 @@ struct BeamParams {
   // what the rows' clusters leave: keys, falling, 0 behind the last; log-sum-exps
   unsigned long long *keys;      // [B * K][N]
   double *lse;                   // [B * K]
-  int K, N, V, eos;
+  int K, N, V, eos, ctas;        // CTAs a row
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -67,42 +72,43 @@ __device__ __forceinline__ bool lives(const BeamParams &p, int row) {
 
 // E logits a thread and chunk, V a load.  Position of element j * V + k: j * 256 V + V t + k.
 template <class T, int V, int E>
-__device__ __forceinline__ void load_chunk(const T *row, int at, int end, float (&x)[E], bool &odd) {
+__device__ __forceinline__ void load_chunk(const T *row, int at, int end, float (&x)[E]) {
 #pragma unroll
   for (int j = 0; j < E / V; ++j) {
     const int v = at + (j * kThreads + threadIdx.x) * V;
-    float y[V];
     if constexpr (V == 1) {
-      y[0] = v < end ? (float)row[v] : -INFINITY;
+      x[j] = v < end ? (float)row[v] : -INFINITY;
     } else {
-      // rows are whole loads: a load is in or out
-      const uint4 w = v < end ? __ldcs(reinterpret_cast<const uint4 *>(row + v)) : make_uint4(0, 0, 0, 0);
+      // rows are whole loads: a load is in or out; out are -inf
+      constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+      const uint4 w = v < end ? __ldcs(reinterpret_cast<const uint4 *>(row + v)) : make_uint4(none, none, none, none);
       const uint32_t b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        y[k] = sizeof(T) == 4 ? __uint_as_float(b[k % 4]) : __uint_as_float(k % 2 ? b[k / 2 % 4] & 0xffff0000u : b[k / 2 % 4] << 16);
-#pragma unroll
-      for (int k = 0; k < V; ++k) y[k] = v + k < end ? y[k] : -INFINITY;
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const bool bad = !(y[k] < INFINITY);
-      odd = odd || bad;
-      x[j * V + k] = bad ? -INFINITY : y[k] + 0.f;     // -0 and 0 are equal
+        x[j * V + k] = __uint_as_float(sizeof(T) == 4 ? b[k % 4] : k % 2 ? b[k / 2 % 4] & 0xffff0000u : b[k / 2 % 4] << 16);
     }
   }
 }
+// The sum of a thread's chunk relative to exp(m).
+template <int E>
+__device__ __forceinline__ float sum_of(const float (&x)[E], float m) {
+  float s[4] = {};
+#pragma unroll
+  for (int e = 0; e < E; ++e) s[e % 4] += ex2((x[e] - m) * kLog2e);
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
 
+constexpr int kList = kMostBeams * 32 + kMostBeams;
 struct RowShared {
   unsigned long long top[kThreads];
-  unsigned long long list[kMostBeams * 32 + kMostBeams];
+  unsigned long long list[kList];
   unsigned long long best[2][kMostBeams];
   unsigned long long bound;
-  double sum[kWarps];
-  float max[kWarps];
-  double total;                 // of the CTA, relative to most
-  float most;
-  int count;
+  uint32_t warp_bound[kWarps];
+  double total;                 // of the CTA, relative to exp(unit)
+  float sum[kWarps], max[kWarps];
+  float unit;
+  int count, now;               // the list's; which of best is the last
 };
 // The first n of `count` keys, ranked, to `best` (0 behind the last); all threads call it.
 __device__ __forceinline__ void rank_list(const unsigned long long *list, int count, unsigned long long *best, int n) {
@@ -116,13 +122,46 @@ __device__ __forceinline__ void rank_list(const unsigned long long *list, int co
   }
 }
 
+// The chunk's list from ranked keys of the threads: where it overflows.  Apart from the
+// loop, from the logits read again, so that it costs that no registers.
 template <class T, int V, int E>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
-    row_kernel(const __grid_constant__ BeamParams p) {
+__device__ __noinline__ void list_by_keys(RowShared &sh, int n, unsigned long long before, const T *row, int at, int end) {
+  const int tid = threadIdx.x;
+  float x[E];
+  load_chunk<T, V, E>(row, at, end, x);
+  const auto key = [&](int e) {
+    return x[e] < INFINITY ? key_of(x[e] + 0.f, at + (e / V * kThreads + tid) * V + e % V) : 0ull;
+  };
+  unsigned long long mine = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) mine = max(mine, key(e));
+  __syncthreads();                  // the count that led here has been read by all
+  sh.top[tid] = mine;
+  if (tid == 0) {
+    sh.count = 0;
+    sh.bound = 1;                   // fewer than N threads have anything: all of it counts
+  }
+  __syncthreads();
+  int above = 0;
+  for (int j = 0; j < kThreads; ++j) above += sh.top[j] > mine;
+  if (mine && above == n - 1) sh.bound = mine;
+  __syncthreads();
+  const unsigned long long bound = sh.bound;
+  if (mine >= bound)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const unsigned long long k = key(e);
+      if (k >= bound && k > before) sh.list[atomicAdd(&sh.count, 1)] = k;
+    }
+  __syncthreads();
+}
+
+template <class T, int V, int E>
+__global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant__ BeamParams p) {
   static_assert(E <= 32, "the list holds 32 elements of each thread above the bound");
   __shared__ RowShared sh;
   wait_for_kernel_before();
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, rank = blockIdx.x % kCluster, row = blockIdx.x / kCluster;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, rank = blockIdx.x % p.ctas, row = blockIdx.x / p.ctas;
   if (!lives(p, row)) {               // the whole cluster
     if (rank == 0 && tid == 0 && !(p.scores[row] < INFINITY)) raise(p.status, KVX_FLAG_NOT_FINITE);
     if (rank == 0 && tid < p.N) p.keys[(int64_t)row * p.N + tid] = 0;
@@ -131,65 +170,79 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   const T *x_of = reinterpret_cast<const T *>(p.logits) + row * p.stride;
   // the CTA's share of the row, in whole loads
   const int64_t loads = (p.V + V - 1) / V;
-  const int begin = (int)(loads * rank / kCluster * V), end = (int)min((int64_t)p.V, loads * (rank + 1) / kCluster * V);
-  float most = -INFINITY, sum = 0.f;
-  bool odd = false;
+  const int begin = (int)(loads * rank / p.ctas * V), end = (int)min((int64_t)p.V, loads * (rank + 1) / p.ctas * V);
+  float unit = -INFINITY, sum = 0.f;  // the thread's sum, relative to exp(unit)
   int now = 0;
+  const int rounds = (p.N + kWarps - 1) / kWarps;
   if (tid < kMostBeams) sh.best[0][tid] = 0;
+  if (tid == 0) sh.count = 0;
   for (int64_t at = begin; at < end; at += kThreads * E) {
     float x[E];
-    load_chunk<T, V, E>(x_of, (int)at, end, x, odd);
+    load_chunk<T, V, E>(x_of, (int)at, end, x);
     float top = x[0];
-    int where = 0;
 #pragma unroll
-    for (int e = 1; e < E; ++e) {
-      where = x[e] > top ? e : where;
-      top = fmaxf(top, x[e]);
-    }
-    if (top > most) {
-      sum *= ex2((most - top) * kLog2e);
-      most = top;
-    }
-    if (most > -INFINITY) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum += ex2((x[e] - most) * kLog2e);
-    }
-    const auto position = [&](int e) { return (int)at + (e / V * kThreads + tid) * V + e % V; };
-    const unsigned long long mine = key_of(top, position(where));
-    sh.top[tid] = mine;
-    if (tid == 0) {
-      sh.count = 0;
-      sh.bound = 1;                   // fewer than N threads have anything: all of it counts
-    }
-    __syncthreads();
-    // the bound: the N-th largest of the threads' keys, or of those found so far
-    int above = 0;
-    if (mine) {
-#pragma unroll 8
-      for (int j = 0; j < kThreads; ++j) above += sh.top[j] > mine;
-      if (above == p.N - 1) sh.bound = mine;
-    }
-    __syncthreads();
-    const unsigned long long before = sh.best[now][p.N - 1], bound = before > sh.bound ? before : sh.bound;
-    if (mine >= bound) {
+    for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
+    // relative to the maximum so far, or 0 before any
+    const auto reference = [&] { return fmaxf(unit, top) > -INFINITY ? fmaxf(unit, top) : 0.f; };
+    float more = sum_of<E>(x, reference());
+    if (!(top < INFINITY) || !(more < INFINITY)) {
+      // a NaN or an infinity: they become -inf
+      raise(p.status, KVX_FLAG_NOT_FINITE);
+      top = -INFINITY;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const unsigned long long key = key_of(x[e], position(e));
-        if (key >= bound) sh.list[atomicAdd(&sh.count, 1)] = key;
+        x[e] = x[e] < INFINITY ? x[e] : -INFINITY;
+        top = fmaxf(top, x[e]);
       }
+      more = sum_of<E>(x, reference());
     }
-    if (tid < p.N && sh.best[now][tid]) sh.list[atomicAdd(&sh.count, 1)] = sh.best[now][tid];
+    sum = sum * ex2((unit - reference()) * kLog2e) + more;
+    unit = fmaxf(unit, top);
+    // the bound
+    uint32_t left = top > -INFINITY ? ordered(top + 0.f) : 0u, least = 0;
+    for (int i = 0; i < rounds; ++i) {
+      least = __reduce_max_sync(~0u, left);
+      left = left == least ? 0u : left;
+    }
+    if (lane == 0) sh.warp_bound[warp] = least;
     __syncthreads();
-    rank_list(sh.list, sh.count, sh.best[now ^ 1], p.N);
-    now ^= 1;
+    const unsigned long long before = sh.best[now][p.N - 1];
+    least = ~0u;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) least = min(least, sh.warp_bound[w]);
+    least = max(least, (uint32_t)(before >> 32));
+    const float bound = least ? logit_of((unsigned long long)least << 32) : -INFINITY;
+    const auto position = [&](int e) { return (int)at + (e / V * kThreads + tid) * V + e % V; };
+    const auto put = [&](unsigned long long key) {
+      const int to = atomicAdd(&sh.count, 1);
+      if (to < kList - kMostBeams) sh.list[to] = key;
+    };
+    if (top >= bound) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (x[e] >= bound) {
+          const unsigned long long key = key_of(x[e] + 0.f, position(e));   // -0 and 0 are equal
+          if (key > before) put(key);
+        }
+    }
     __syncthreads();
+    if (sh.count > kList - kMostBeams) list_by_keys<T, V, E>(sh, p.N, before, x_of, (int)at, end);
+    const int found = sh.count;
+    if (found) {                      // of the whole CTA
+      const unsigned long long old = tid < p.N ? sh.best[now][tid] : 0;
+      if (old) sh.list[found + tid] = old;      // they are at the front of best
+      const int held = __syncthreads_count(old != 0);
+      rank_list(sh.list, found + held, sh.best[now ^ 1], p.N);
+      now ^= 1;
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+    }
   }
-  if (odd) raise(p.status, KVX_FLAG_NOT_FINITE);
   // the CTA's sum
-  float top = most;
+  float top = unit;
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  double part = most > -INFINITY ? (double)sum * exp((double)most - (double)top) : 0.0;
+  float part = unit > -INFINITY ? sum * ex2((unit - top) * kLog2e) : 0.f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
   if (lane == 0) {
@@ -200,10 +253,10 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   if (tid == 0) {
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.max[w]);
     double total = 0.0;
-    for (int w = 0; w < kWarps; ++w)
-      if (sh.max[w] > -INFINITY) total += sh.sum[w] * exp((double)sh.max[w] - (double)top);
+    for (int w = 0; w < kWarps; ++w) total += top > -INFINITY ? (double)(sh.sum[w] * ex2((sh.max[w] - top) * kLog2e)) : 0.0;
     sh.total = total;
-    sh.most = top;
+    sh.unit = top;
+    sh.now = now;
   }
   // the cluster's: the first CTA ranks the lists of all
   const auto cluster_barrier = [] {
@@ -226,30 +279,27 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   };
   cluster_barrier();
   if (rank == 0) {
-    // which of the two lists is the last depends on the chunks of a CTA
-    const auto now_of = [&](int64_t c) {
-      const int64_t from = loads * c / kCluster * V, to = min((int64_t)p.V, loads * (c + 1) / kCluster * V);
-      return (int)((to - from + kThreads * E - 1) / (kThreads * E) & 1);
-    };
-    for (int i = tid; i < kCluster * p.N; i += kThreads) {
-      const int c = i / p.N;
-      sh.list[i] = load64(remote(&sh.best[now_of(c)][i % p.N], c));
+    const int n = p.ctas * p.N;
+    if (tid < n) {
+      const int c = tid / p.N;
+      sh.list[tid] = load64(remote(&sh.best[load32(remote(&sh.now, c))][tid % p.N], c));
     }
-    if (tid == 0) {
+    if (tid == kThreads - 1) {        // not one of the others' warps, mostly
       float tops[kCluster], top = -INFINITY;
+#pragma unroll
       for (int c = 0; c < kCluster; ++c) {
-        tops[c] = __uint_as_float(load32(remote(&sh.most, c)));
+        tops[c] = c < p.ctas ? __uint_as_float(load32(remote(&sh.unit, c))) : -INFINITY;
         top = fmaxf(top, tops[c]);
       }
       double total = 0.0;
+#pragma unroll
       for (int c = 0; c < kCluster; ++c)
-        if (tops[c] > -INFINITY) total += __longlong_as_double(load64(remote(&sh.total, c))) * exp((double)tops[c] - (double)top);
+        if (c < p.ctas && tops[c] > -INFINITY) total += __longlong_as_double(load64(remote(&sh.total, c))) * (double)ex2((tops[c] - top) * kLog2e);
       p.lse[row] = (double)top + log(total);
     }
     __syncthreads();
     // ranked among each other; the 0s of short lists stay behind
     unsigned long long *to = p.keys + (int64_t)row * p.N;
-    const int n = kCluster * p.N;
     const unsigned long long key = tid < n ? sh.list[tid] : 0;
     int above = 0, some = 0;
     for (int j = 0; j < n; ++j) {
@@ -262,39 +312,43 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   cluster_barrier();                  // shared memory of the others is read until here
 }
 
-// Candidate i = k * N + j of a request: the j-th of beam k.  In that order equal scores
-// go to the lower beam and token.
-struct PickShared {
-  double top[kThreads];
-  int place[kThreads];
-  double list[kMostBeams * (kMostBeams * kMostBeams / kThreads)];
-  int list_place[kMostBeams * (kMostBeams * kMostBeams / kThreads)];
-  double bound;
-  int bound_place, count;
-};
-constexpr double kNone = -INFINITY;
+// A score as a number of the same order; 0 is below all of them.
+__device__ __forceinline__ unsigned long long ordered(double x) {
+  const long long b = __double_as_longlong(x + 0.0);
+  return (unsigned long long)b ^ ((unsigned long long)(b >> 63) | 1ull << 63);
+}
+__device__ __forceinline__ double score_of(unsigned long long k) {
+  return __longlong_as_double((long long)(k ^ (k >> 63 ? 1ull << 63 : ~0ull)));
+}
 // a before b?
-__device__ __forceinline__ bool first(double a, int at, double b, int bt) { return a > b || (a == b && at < bt); }
+__device__ __forceinline__ bool first(unsigned long long a, int at, unsigned long long b, int bt) {
+  return a > b || (a == b && at < bt);
+}
+constexpr int kEach = kMostBeams * kMostBeams / kThreads;     // candidates a thread
+struct PickShared {
+  unsigned long long top[kThreads], list[kMostBeams * kEach], bound;
+  int place[kThreads], list_place[kMostBeams * kEach], bound_place, count;
+};
+// Candidate i = k * N + j of a request: the j-th of beam k.  In that order equal scores
+// go to the lower beam and token.  Ranked as a chunk's logits are where they overflow.
 __global__ void __launch_bounds__(kThreads) pick_kernel(const __grid_constant__ BeamParams p) {
-  constexpr int kEach = kMostBeams * kMostBeams / kThreads;
   __shared__ PickShared sh;
   wait_for_kernel_before();
-  const int tid = threadIdx.x, b = blockIdx.x, all = p.K * p.N;
-  double x[kEach], top = kNone;
+  const int tid = threadIdx.x, b = blockIdx.x, all = p.K * p.N, threads = min(all, kThreads);
+  unsigned long long x[kEach], top = 0;
   int place = INT32_MAX;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const int i = e * kThreads + tid;
-    x[e] = kNone;
+    x[e] = 0;
     if (i >= all) continue;
     const int row = b * p.K + i / p.N;
     const float score = p.scores[row];
-    const bool over = p.done && p.done[row];
-    if (over) {
-      if (i % p.N == 0 && score < INFINITY) x[e] = score;
+    if (p.done && p.done[row]) {
+      if (i % p.N == 0 && fabsf(score) < INFINITY) x[e] = ordered((double)score);
     } else {
       const unsigned long long key = __ldcg(p.keys + (int64_t)row * p.N + i % p.N);
-      if (key) x[e] = (double)score + ((double)logit_of(key) - __ldcg(p.lse + row));
+      if (key) x[e] = ordered((double)score + ((double)logit_of(key) - __ldcg(p.lse + row)));
     }
     if (x[e] > top) {
       top = x[e];
@@ -305,14 +359,14 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const __grid_constant__ 
   sh.place[tid] = place;
   if (tid == 0) {
     sh.count = 0;
-    sh.bound = kNone;
+    sh.bound = 0;
     sh.bound_place = INT32_MAX;
   }
   __syncthreads();
-  if (top > kNone) {
+  if (top) {
     int above = 0;
-#pragma unroll 8
-    for (int j = 0; j < kThreads; ++j) above += first(sh.top[j], sh.place[j], top, place);
+#pragma unroll 4
+    for (int j = 0; j < threads; ++j) above += first(sh.top[j], sh.place[j], top, place);
     if (above == p.N - 1) {
       sh.bound = top;
       sh.bound_place = place;
@@ -322,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const __grid_constant__ 
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const int i = e * kThreads + tid;
-    if (x[e] > kNone && !first(sh.bound, sh.bound_place, x[e], i)) {
+    if (x[e] && !first(sh.bound, sh.bound_place, x[e], i)) {
       const int at = atomicAdd(&sh.count, 1);
       sh.list[at] = x[e];
       sh.list_place[at] = i;
@@ -339,13 +393,37 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const __grid_constant__ 
   };
   if (tid < p.N && tid >= n) put(tid, -1, -1, -INFINITY);
   if (tid < n) {
-    const double s = sh.list[tid];
+    const unsigned long long s = sh.list[tid];
     const int i = sh.list_place[tid], row = b * p.K + i / p.N;
     int above = 0;
     for (int j = 0; j < n; ++j) above += first(sh.list[j], sh.list_place[j], s, i);
     if (above < p.N)
-      put(above, p.done && p.done[row] ? p.eos : token_of(__ldcg(p.keys + (int64_t)row * p.N + i % p.N)), row, (float)s);
+      put(above, p.done && p.done[row] ? p.eos : token_of(__ldcg(p.keys + (int64_t)row * p.N + i % p.N)), row,
+          (float)score_of(s));
   }
+}
+
+// CTAs a row: as many as fill the GPU, up to four CTAs an SM, while each has a chunk.
+int ctas_of(int64_t rows, int64_t vocab) {
+  int c = 1;
+  while (c < kCluster && rows * c * 2 <= 152 * 4 && vocab > (int64_t)c * 2048) c *= 2;
+  return c;
+}
+template <class T, int V, int E>
+kvx_status launch_rows(const BeamParams &p, int64_t rows, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * p.ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, row_kernel<T, V, E>, p) == cudaSuccess ? KVX_OK : KVX_ERR_CUDA;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -374,7 +452,7 @@ extern "C" kvx_status kvx_beam_select(const kvx_beam_args *a, void *stream) {
     return KVX_ERR_INVALID_ARG;
   const int rows = a->num_requests * a->beams;
   BeamParams p = {a->logits, a->row_stride, a->scores, a->done,   a->tokens,    a->parents, a->new_scores, a->new_done, a->status,
-                  nullptr,   nullptr,       a->beams,  a->out_beams, a->vocab, a->eos};
+                  nullptr,   nullptr,       a->beams,  a->out_beams, a->vocab, a->eos, 1};
   p.keys = (unsigned long long *)a->workspace;
   p.lse = (double *)((char *)a->workspace + up256((size_t)rows * a->out_beams * 8));
   // loads of 16 bytes where rows begin on such a boundary and the last one stays inside
@@ -382,12 +460,9 @@ extern "C" kvx_status kvx_beam_select(const kvx_beam_args *a, void *stream) {
   const int per = 16 / size;
   const bool vec = aligned_to(a->logits, 16) && a->row_stride % per == 0 && a->vocab % per == 0;
   cudaStream_t s = (cudaStream_t)stream;
-  const dim3 grid((unsigned)rows * kCluster);
-  const kvx_status st =
-      size == 4 ? (vec ? launch_after(row_kernel<float, 4, 32>, grid, kThreads, 0, s, p)
-                       : launch_after(row_kernel<float, 1, 16>, grid, kThreads, 0, s, p))
-                : (vec ? launch_after(row_kernel<__nv_bfloat16, 8, 32>, grid, kThreads, 0, s, p)
-                       : launch_after(row_kernel<__nv_bfloat16, 1, 16>, grid, kThreads, 0, s, p));
+  p.ctas = ctas_of(rows, a->vocab);
+  const kvx_status st = size == 4 ? (vec ? launch_rows<float, 4, 32>(p, rows, s) : launch_rows<float, 1, 16>(p, rows, s))
+                                  : (vec ? launch_rows<__nv_bfloat16, 8, 32>(p, rows, s) : launch_rows<__nv_bfloat16, 1, 16>(p, rows, s));
   if (st != KVX_OK) return st;
   return launch_after(pick_kernel, dim3((unsigned)a->num_requests), kThreads, 0, s, p);
 }

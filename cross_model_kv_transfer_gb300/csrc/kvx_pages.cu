@@ -256,84 +256,120 @@ struct ReserveParams {
   const int32_t *lens, *add;
   uint32_t *status;
   int bs, R, W, add_all;
+  int lanes, chunks, rows;     // of a row: lanes of a warp, times that they take; rows of a warp
 };
-struct Span {
-  int first, count, len;     // entries to be the row's own; its length
+// An entry of a row's new slots, one a lane.
+struct Entry {
+  int32_t *at;               // NULL: none
+  int value, row, len;       // -1 no page, -(page + 2) a page that others hold too
+  bool first, whole;         // of the row's entries; its page holds none of the row's slots
 };
-__device__ __forceinline__ Span span_of(const ReserveParams &p, int r, bool tell) {
-  const int64_t len = p.lens[r], add = p.add ? p.add[r] : p.add_all;
-  if (len < 0 || add < 0 || add > p.add_all || len + add > (int64_t)p.W * p.bs) {
-    if (tell && threadIdx.x % 32 == 0) raise(p.status, KVX_FLAG_BAD_LENGTH);
-    return {0, 0, 0};
+__device__ __forceinline__ Entry entry_of(const ReserveParams &p, int turn, bool tell) {
+  const int lane = threadIdx.x % 32, at_once = 32 / p.lanes;
+  const int r = (int)(threadIdx.x / 32) * p.rows + turn / p.chunks * at_once + lane / p.lanes;
+  const int b = turn % p.chunks * 32 + lane % p.lanes;
+  Entry e = {nullptr, 0, r, 0, b == 0, true};
+  if (r >= p.R) {
+    e.row = -1;
+    return e;
   }
-  const int first = (int)(len / p.bs);
-  return {first, add ? (int)((len + add - 1) / p.bs) - first + 1 : 0, (int)len};
+  const int64_t len = __ldg(p.lens + r), add = p.add ? __ldg(p.add + r) : p.add_all;
+  if (len < 0 || add < 0 || add > p.add_all || len + add > (int64_t)p.W * p.bs) {
+    if (tell && b == 0) raise(p.status, KVX_FLAG_BAD_LENGTH);
+    return e;
+  }
+  const uint32_t first = (uint32_t)len / (uint32_t)p.bs, inside = (uint32_t)len - first * p.bs;
+  if (add == 0 || first + b > (uint32_t)(len + add - 1) / (uint32_t)p.bs) return e;
+  e.whole = b > 0 || inside == 0;
+  e.at = p.table + (int64_t)r * p.W + first + b;
+  e.value = *e.at;
+  return e;
 }
-// A row to a warp, its entries to the lanes; a warp has consecutive rows.  An entry whose
-// page others hold too is marked as -(page + 2) until it is decided whether the row
-// keeps it: all such entries let go of their page, and where none is left behind it the
-// last row of them takes it back.
+// The entries are looked after by the first CTA, rows to its warps in order, and a row's
+// entries to lanes side by side: two for a token, a warp's for a prompt.  Where each
+// warp takes one turn its entries stay in registers between the phases.  All CTAs
+// look through the references.
+//
+// Which of the rows that hold a page keeps it: all that ask let go of it, and where that
+// leaves none the last of them, found by a minimum over -(row + 1), takes it back.
 template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const __grid_constant__ ReserveParams p) {
+  __shared__ int needs_of[kWarps];
   wait_for_kernel_before();
-  const int lane = threadIdx.x % 32, warp = blockIdx.x * kWarps + threadIdx.x / 32;
-  int32_t *free_of = p.work, *needs_of = p.work + kSums, *list = p.work + kListAt;
-  const Range rows = share_of<CTAS>(p.R, 1), pages = share_of<CTAS>(p.num_blocks, 32);
-  // what is free, and which entries are shared
+  const int lane = threadIdx.x % 32, in = threadIdx.x / 32, warp = blockIdx.x * kWarps + in;
+  int32_t *free_of = p.work, *list = p.work + kListAt;
+  const bool leads = blockIdx.x == 0;
+  const int turns = in * p.rows < p.R ? p.rows / (32 / p.lanes) * p.chunks : 0;
+  Entry only = {nullptr, 0, -1, 0, false, true};
+  const auto entries = [&](auto f) {
+    if (turns == 1) {
+      f(only);
+    } else {
+      for (int t = 0; t < turns; ++t) {
+        Entry e = entry_of(p, t, false);
+        f(e);
+      }
+    }
+  };
+  bool shared = false;
+  if (leads) {
+    for (int t = 0; t < turns; ++t) {
+      Entry e = entry_of(p, t, true);
+      if (e.at && (e.value < 0 || e.value >= p.num_blocks)) {
+        if (e.value != -1) raise(p.status, KVX_FLAG_BAD_BLOCK);
+        if (e.value != -1) *e.at = -1;
+        e.value = -1;
+      } else if (e.at && __ldcg(p.refs + e.value) > 1) {
+        e.value = -(e.value + 2);
+        *e.at = e.value;
+        shared = true;
+      }
+      if (turns == 1) only = e;
+    }
+  }
+  // what is free
+  const Range pages = share_of<CTAS>(p.num_blocks, 32);
   int free_here = 0;
   walk(p.refs, pages, [&](int, int c) { free_here += __popc(__ballot_sync(~0u, c == 0)); });
   if (lane == 0) free_of[warp] = free_here;
-  const auto entries = [&](auto f) {
-    for (int r = (int)rows.begin; r < (int)rows.end; ++r) {
-      const Span s = span_of(p, r, false);
-      int32_t *row = p.table + (int64_t)r * p.W + s.first;
-      for (int b0 = 0; b0 < s.count; b0 += 32) f(r, s, b0 + lane < s.count ? row + b0 + lane : nullptr, b0 + lane);
+  barrier<CTAS>();
+  if (leads) {
+    if (__syncthreads_or(shared)) {
+      entries([&](Entry &e) {
+        if (e.at && e.value < -1) atomicSub(p.refs - (e.value + 2), 1);
+      });
+      __syncthreads();
+      entries([&](Entry &e) {
+        int32_t *count = p.refs - (e.value + 2);
+        if (e.at && e.value < -1 && __ldcg(count) <= 0) atomicMin(count, -(e.row + 1));
+      });
+      __syncthreads();
     }
-  };
-  for (int r = (int)rows.begin; r < (int)rows.end; ++r) span_of(p, r, true);
-  entries([&](int, const Span &, int32_t *e, int) {
-    if (!e) return;
-    const int page = *e;
-    if (page < 0 || page >= p.num_blocks) {
-      if (page != -1) {
-        raise(p.status, KVX_FLAG_BAD_BLOCK);
-        *e = -1;
+    int needs = 0;
+    entries([&](Entry &e) {
+      bool need = e.at && e.value < 0;
+      if (need && e.value < -1) {
+        int32_t *count = p.refs - (e.value + 2);
+        if (__ldcg(count) == -(e.row + 1)) {     // others of its rows see this or the 1: not theirs
+          *count = 1;
+          e.value = -(e.value + 2);
+          *e.at = e.value;
+          need = false;
+        }
       }
-    } else if (__ldcg(p.refs + page) > 1) {
-      *e = -(page + 2);
-    }
-  });
+      needs += __popc(__ballot_sync(~0u, need));
+    });
+    if (lane == 0) needs_of[in] = needs;
+    __syncthreads();
+    const int sum = __reduce_add_sync(~0u, needs_of[lane]);
+    if (threadIdx.x == 0) p.work[kCountAt] = sum;
+  }
   barrier<CTAS>();
-  entries([&](int, const Span &, int32_t *e, int) {
-    if (e && *e < -1) atomicSub(p.refs - (*e + 2), 1);
-  });
-  barrier<CTAS>();
-  entries([&](int r, const Span &, int32_t *e, int) {
-    if (!e || *e >= -1) return;
-    int32_t *count = p.refs - (*e + 2);
-    if (__ldcg(count) <= 0) atomicMin(count, -(r + 1));
-  });
-  barrier<CTAS>();
-  int needs = 0;
-  entries([&](int r, const Span &, int32_t *e, int) {
-    bool need = e && *e < 0;
-    if (need && *e < -1) {
-      int32_t *count = p.refs - (*e + 2);
-      if (__ldcg(count) == -(r + 1)) {     // others of its rows see this or the 1 below: not theirs
-        *count = 1;
-        *e = -(*e + 2);
-        need = false;
-      }
-    }
-    needs += __popc(__ballot_sync(~0u, need));
-  });
-  if (lane == 0) needs_of[warp] = needs;
-  barrier<CTAS>();
-  const int2 free_sum = sums_of<CTAS>(free_of, warp), need_sum = sums_of<CTAS>(needs_of, warp);
-  const int wanted = need_sum.y;
+  const int wanted = __ldcg(p.work + kCountAt);
+  const int2 free_sum = sums_of<CTAS>(free_of, warp);
   const bool enough = wanted <= free_sum.y;
   // the free pages that are taken, in order
-  if (enough && free_sum.x < wanted) {
+  if (enough && free_here && free_sum.x < wanted) {
     int at = free_sum.x;
     walk(p.refs, pages, [&](int page, int c) {
       const unsigned mask = __ballot_sync(~0u, c == 0);
@@ -343,34 +379,29 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const __grid_const
     });
   }
   barrier<CTAS>();
-  if (!enough) {
-    if (warp == 0 && lane == 0) raise(p.status, KVX_FLAG_NO_PAGES);
-    entries([&](int, const Span &, int32_t *e, int) {
-      if (!e || *e >= -1) return;
-      atomicAdd(p.refs - (*e + 2), 1);
-      *e = -(*e + 2);
-    });
-  }
-  int at = need_sum.x;
-  for (int r = (int)rows.begin + lane; r < (int)rows.end; r += 32) {
-    p.copies[2 * (int64_t)r] = -1;
-    p.copies[2 * (int64_t)r + 1] = -1;
-  }
-  __syncwarp();
-  if (!enough) return;
-  entries([&](int r, const Span &s, int32_t *e, int b) {
-    const bool need = e && *e < 0;
+  if (!leads) return;
+  if (!enough && threadIdx.x == 0) raise(p.status, KVX_FLAG_NO_PAGES);
+  int at = 0;
+  for (int w = 0; w < in; ++w) at += needs_of[w];
+  entries([&](Entry &e) {
+    const bool need = e.at && e.value < 0;
     const unsigned mask = __ballot_sync(~0u, need);
-    if (need) {
-      const int page = __ldcg(list + at + lanes_below(mask)), old = -(*e + 2);
-      if (old >= 0 && b == 0 && s.len % p.bs) {
-        p.copies[2 * (int64_t)r] = old;
-        p.copies[2 * (int64_t)r + 1] = page;
-      }
-      *e = page;
+    const int old = -(e.value + 2);            // -1: none
+    int page = -1;
+    if (need && enough) {
+      page = __ldcg(list + at + lanes_below(mask));
+      *e.at = page;
       p.refs[page] = 1;
+    } else if (need && old >= 0) {             // as it was
+      atomicAdd(p.refs + old, 1);
+      *e.at = old;
     }
     at += __popc(mask);
+    if (e.first && e.row >= 0) {
+      const bool copied = page >= 0 && old >= 0 && !e.whole;
+      p.copies[2 * (int64_t)e.row] = copied ? old : -1;
+      p.copies[2 * (int64_t)e.row + 1] = copied ? page : -1;
+    }
   });
 }
 
@@ -452,7 +483,7 @@ __global__ void __launch_bounds__(256) rewrite_kernel(const __grid_constant__ Re
 // --- host ------------------------------------------------------------------------
 
 // One CTA for a small pool, a cluster of eight for more.
-constexpr int64_t kSmallPool = 16384;
+constexpr int64_t kSmallPool = 8192;
 // pages, and slots of a row, are counted in 32 bits, a little beyond the last one too
 constexpr int64_t kMostPages = INT32_MAX - 1024, kMostSlots = INT32_MAX - 1024;
 template <class P>
@@ -530,6 +561,13 @@ extern "C" kvx_status kvx_pages_reserve(const kvx_pages_reserve_args *a, void *s
     return KVX_ERR_INVALID_ARG;
   ReserveParams p = {a->refs, a->num_blocks, a->table,      a->copies,   (int32_t *)a->workspace, a->lens,
                      a->add,  a->status,     a->block_size, a->num_rows, a->width,                a->add_all};
+  // entries of a row at most, lanes for them, and rows for the warps
+  const int64_t asked = ((int64_t)a->add_all + a->block_size - 1) / a->block_size + 1, per = asked < a->width ? asked : a->width;
+  p.lanes = 1;
+  while (p.lanes < 32 && p.lanes < per) p.lanes *= 2;
+  p.chunks = (int)((per + 31) / 32);
+  const int at_once = 32 / p.lanes;
+  p.rows = (int)(((int64_t)a->num_rows + kWarps * at_once - 1) / (kWarps * at_once)) * at_once;
   cudaStream_t s = (cudaStream_t)stream;
   if (const kvx_status st = launch_counting(reserve_kernel<1>, reserve_kernel<kBigCtas>, p, s)) return st;
   return copy_pages(a->caches, a->num_caches, a->num_blocks, a->copies, a->num_rows, nullptr, a->status, s);

@@ -909,6 +909,7 @@ _pack_shared = _packer(Attend8SharedArgs)
 _pack_cache = _packer(Cache8Desc)
 _pack_fork = _packer(PagesForkArgs)
 _pack_reserve = _packer(PagesReserveArgs)
+_pack_compact = _packer(PagesCompactArgs)
 _pack_beam = _packer(BeamArgs)
 
 
@@ -927,6 +928,7 @@ class _Fast:
         cls.attend, cls.evict = lib.kvx_attend8, lib.kvx_evict8
         cls.shared, cls.fork = lib.kvx_attend8_shared, lib.kvx_pages_fork
         cls.reserve, cls.beam = lib.kvx_pages_reserve, lib.kvx_beam_select
+        cls.compact = lib.kvx_pages_compact
         cls.empty = torch.empty
         cls.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         cls.raw = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -1088,6 +1090,8 @@ class Cache8:
         self._head = (k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
                       v_scale.data_ptr(), self.num_blocks, self.heads, self.head_dim,
                       self.block_size)
+        # as one of an array of caches, whose block tables are not used: any aligned address
+        self._packed = _pack_cache(*self._head, 1, self._head[2])
 
     @classmethod
     def empty(cls, num_blocks, heads, head_dim, block_size, device="cuda"):
@@ -1353,13 +1357,12 @@ class Cache8:
 
 def _cache_array(caches, num_blocks, device):
     """The caches as an array of ``kvx_cache8`` (kept by the caller for the call) and its address."""
-    for c in caches:
-        if c.device != device or c.num_blocks != num_blocks:
-            raise ValueError(f"caches must hold {num_blocks} blocks on {device}")
     if not caches:
         return None, 0
-    # the block table is not used: any aligned address
-    raw = b"".join(_pack_cache(*c._head, 1, c._head[2]) for c in caches)
+    for c in caches:
+        if c.num_blocks != num_blocks or c.device != device:
+            raise ValueError(f"caches must hold {num_blocks} blocks on {device}")
+    raw = ctypes.c_char_p(b"".join([c._packed for c in caches]))
     return raw, ctypes.cast(raw, ctypes.c_void_p).value
 
 
@@ -1489,13 +1492,13 @@ class Pages:
             workspace = _on_stream(self.workspace, stream)
         keep, array = _cache_array(caches, self.num_blocks, dev)
         n = len(tables)
-        ptrs = (ctypes.c_void_p * max(1, n))(*[_int_table(t, "tables", dev, t.dim()) for t in tables])
-        entries = (ctypes.c_int64 * max(1, n))(*[t.numel() for t in tables])
-        a = PagesCompactArgs(self.refs.data_ptr(), self.num_blocks, self.block_size,
-                             ctypes.addressof(ptrs), ctypes.addressof(entries), n,
-                             _int_table(used, "used", dev), _int_table(moved, "moved", dev), array,
-                             len(caches), *_workspace(workspace, dev), _status_ptr(status, dev))
-        st = kvx_pages_compact(a, _raw_stream(stream, dev))
+        lists = (ctypes.c_int64 * (2 * n + 1))(
+            *[_int_table(t, "tables", dev, t.dim()) for t in tables], *[t.numel() for t in tables])
+        at = ctypes.addressof(lists)
+        a = _pack_compact(self.refs.data_ptr(), self.num_blocks, self.block_size, at, at + 8 * n, n,
+                          _int_table(used, "used", dev), _int_table(moved, "moved", dev), array,
+                          len(caches), *_workspace(workspace, dev), _status_ptr(status, dev))
+        st = _Fast.compact(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_pages_compact")
         return used, moved
