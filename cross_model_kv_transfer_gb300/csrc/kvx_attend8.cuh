@@ -173,3 +173,8 @@ size_t kvx_attend8_tc_least_bytes(const kvx_attend8_args *a);
 size_t kvx_attend8_tc_workspace_bytes(const kvx_attend8_args *a);
 kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *a, const kvx8::AttendParams &p, char *workspace,
                                  cudaStream_t s);
+
+// kvx_attend8_own.cu: the own slots of requests that share prefixes, few rows and not too
+// many slots.
+bool kvx_attend8_own_supports(const kvx_attend8_args *a);
+kvx_status kvx_attend8_own_launch(const kvx_attend8_args *a, const kvx8::AttendParams &p, cudaStream_t s);
