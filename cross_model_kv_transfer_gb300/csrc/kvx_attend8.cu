@@ -620,6 +620,8 @@ struct Pass {
   const float *before;
   float2 *stats;             // of the prefixes: written, then read with `before`
   int all;
+  int parts;                 // in place of `before` and `stats`: what the prefixes leave in parts
+  void *part_bytes;
 };
 
 kvx_status check(const kvx_attend8_args *a) {
@@ -745,7 +747,8 @@ kvx_status enqueue(const kvx_attend8_args *a, const Pass &pass, cudaStream_t s) 
   p.bf16 = size == 2 && !pass.all;    // what a prefix gives stays in fp32
   p.c = a->scale * kLog2e;
   char *ws = (char *)a->workspace;
-  if (pass.before && kvx_attend8_own_supports(a)) return kvx_attend8_own_launch(a, p, s);
+  if (pass.parts || (pass.before && kvx_attend8_own_supports(a)))
+    return kvx_attend8_own_launch(a, p, pass.parts, pass.part_bytes, pass.all, s);
   if (kvx_attend8_tc_supports(a)) return kvx_attend8_tc_launch(a, p, ws, s);
   const Shape sh = shape_of(a);
   const bool weighs = a->weights && a->max_len > 0;
@@ -772,6 +775,7 @@ size_t least_bytes(const kvx_attend8_args *a) {
 // they leave beside the workspace of the larger one.
 struct Shared {
   kvx_attend8_args before, own;
+  int parts;                 // 0: one result for each row of the first pass
   size_t out, stats, bytes;
 };
 kvx_status shared_of(const kvx_attend8_shared_args *a, Shared &s) {
@@ -797,6 +801,10 @@ kvx_status shared_of(const kvx_attend8_shared_args *a, Shared &s) {
   s.out = up(one > two ? one : two);
   s.stats = s.out + up(rows * a->own.cache.head_dim * sizeof(float));
   s.bytes = s.stats + up(rows * sizeof(float2));
+  // parts lie behind the head, and there is room for those of smaller calls
+  const size_t room = kWorkspaceHead + kvx_attend8_parts_bytes(&b);
+  s.bytes = s.bytes > room ? s.bytes : room;
+  s.parts = kvx_attend8_own_supports(&s.own) ? kvx_attend8_parts(&b) : 0;
   return KVX_OK;
 }
 
@@ -846,6 +854,8 @@ extern "C" kvx_status kvx_attend8_shared(const kvx_attend8_shared_args *a, void 
   before.lse = nullptr;
   Pass pass = {};
   pass.all = 1;
+  pass.parts = s.parts;
+  pass.part_bytes = ws + kWorkspaceHead;
   pass.stats = (float2 *)(ws + s.stats);
   pass.req = {own.cu_seqlens, a->num_prefixes, own.ntok, a->groups, own.num_requests, 0};
   if (!a->groups) pass.req = {nullptr, 1, own.ntok, nullptr, 0, 1};

@@ -175,6 +175,9 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *a, const kvx8::AttendPa
                                  cudaStream_t s);
 
 // kvx_attend8_own.cu: the own slots of requests that share prefixes, few rows and not too
-// many slots.
+// many slots; and their prefixes, where they are not much work, in a number of parts.
 bool kvx_attend8_own_supports(const kvx_attend8_args *a);
-kvx_status kvx_attend8_own_launch(const kvx_attend8_args *a, const kvx8::AttendParams &p, cudaStream_t s);
+int kvx_attend8_parts(const kvx_attend8_args *before);
+size_t kvx_attend8_parts_bytes(const kvx_attend8_args *before);
+kvx_status kvx_attend8_own_launch(const kvx_attend8_args *a, const kvx8::AttendParams &p, int parts, void *part_bytes, bool prefixes,
+                                  cudaStream_t s);

@@ -1,8 +1,11 @@
-// kvx_attend8_own.cu -- the second pass of kvx_attend8_shared where a request has few rows
-// and few slots of its own: samples and beams that have been decoded for a while.
+#define OWN_MT 2
+#define OWN_W 4
+#define OWN_COLS 8
+// kvx_attend8_own.cu -- kvx_attend8_shared where a request has few rows and few slots of
+// its own: samples and beams that have been decoded for a while.
 //
 //   out = a out_before + b sum_j exp(x_j - m) v_j / sum_j exp(x_j - m)
-// with a and b from the two parts' log-sum-exps (join_before).
+// with a and b from the two parts' log-sum-exps.
 //
 // There are many such items, a (request, KV head) each, of a few tiles of slots: what the
 // forms for long caches spend on an item (shares of the work, a pipeline filled and
@@ -11,13 +14,34 @@
 // result is joined with the prefix's where it is formed.  A warp takes tiles of 16 MT slots
 // in turn, two on their way; the products and roundings are those of the split form
 // (kvx_attend8.cu).
+//
+// The prefixes themselves go the same way while their products are few: a CTA for each
+// prefix, KV head, group of up to 32 columns and split of the slots leaves its maxima, totals and
+// sums, and the items join all splits' with their own.  Two launches then, and no
+// kernel that joins.
 #include "kvx_attend8_mma.cuh"
 
 namespace {
 
+constexpr int kMostParts = 32;      // splits of a prefix
+constexpr double kMostWork = 4e8;   // multiplications of the scores
+
+// What the splits leave: [part][token][Hq][d] sums, [part][token][Hq] maxima and totals,
+// relative to exp2(maximum + kRoom).
+struct Parts {
+  float *sums;
+  float2 *tops;
+  int64_t rows;
+  int count;
+};
+struct OwnParams {
+  SplitParams s;
+  Parts parts;               // count 0: `before` is one result
+};
+
 template <class C>
 constexpr size_t own_smem() {
-  return C::kRing + (C::kQInSmem ? C::kQ : 0) + (C::COLS * (2 * C::WARPS + 4)) * 4;
+  return C::kRing + (C::kQInSmem ? C::kQ : 0) + (C::COLS * (2 * C::WARPS + 3 + 2 * kMostParts)) * 4;
 }
 
 // What a warp has of its columns.
@@ -47,7 +71,7 @@ struct Sums {
   // A tile of 16 MT slots from j0 on, whose codes and scales lie at st.
   __device__ __forceinline__ void add(const unsigned char *st, int j0, const Queries<C> &qf, const uint2 *qs, const int (&limit)[NT][2],
                                       int limits) {
-    const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int lane = threadIdx.x % 32, g = lane / 4;
     const uint32_t vaddr = (uint32_t)__cvta_generic_to_shared(st + C::kTile);
     const float *ks = reinterpret_cast<const float *>(st + 2 * C::kTile), *vs = ks + C::KW;
     const unsigned valid = *reinterpret_cast<const unsigned *>(st + 2 * C::kTile + 2 * C::KW * 4);
@@ -170,44 +194,81 @@ struct Sums {
   }
 };
 
-template <class C>
-__global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constant__ SplitParams p) {
+// PART: of a prefix's slots, CTAs (prefix and KV head, group of columns, split).  Else: of a
+// request's own, CTAs (request and KV head, group of columns).
+template <class C, bool PART>
+__global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constant__ OwnParams op) {
   constexpr int DP = C::DP, NT = C::NT, KW = C::KW, CH = C::CH, W = C::WARPS, COLS = C::COLS;
   extern __shared__ __align__(128) unsigned char smem[];
+  const SplitParams &p = op.s;
   const AttendParams &a = p.a;
+  const Parts &parts = op.parts;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   unsigned char *ring = smem + warp * 2 * C::kStage;
   uint2 *qs = reinterpret_cast<uint2 *>(smem + C::kRing);
   float *warp_m = reinterpret_cast<float *>(smem + C::kRing + (C::kQInSmem ? C::kQ : 0)), *warp_l = warp_m + W * COLS;
-  float *own_of = warp_l + W * COLS, *before_of = own_of + COLS, *col_scale = before_of + COLS;
+  float *own_of = warp_l + W * COLS, *before_of = own_of + COLS, *col_scale = before_of + COLS, *part_of = col_scale + COLS,
+        *part_total = part_of + kMostParts * COLS;
   const int r = blockIdx.x / a.H, h = blockIdx.x % a.H, col0 = blockIdx.y * COLS;
-  if (!requests_ok(a)) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
-    return;
+  if (PART) {
+    // the items may start beside this: what they read before they wait was there before
+    wait_for_kernel_before();
+    let_next_kernel_start();
+  }
+  // What all else waits for is asked for at once: blocks are looked up before the length is
+  // known, and the whole request table is looked through while the first tiles are on their
+  // way.  Nothing is written before the barrier that tells whether it is good; until then
+  // the CTA's own request has to lie within bounds.
+  const auto look = [&](int tile) { return tile >= 0 ? page_of(a, r, block_of(a, tile * KW + lane % KW)) : -1; };
+  int page0 = -1, page1 = -1, page2 = -1;
+  if (!PART) {
+    page0 = look(warp);
+    page1 = look(warp + W);
+    page2 = look(warp + 2 * W);
   }
   const int len = len_of(a, r);
-  if (h == 0 && col0 == 0 && tid == 0 && len != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
-  const int64_t beg = a.req.begin(r);
-  const int fresh = (int)(a.req.begin(r + 1) - beg), cols = fresh * a.G;
+  const int64_t beg = a.req.begin(r), end = a.req.begin(r + 1);
+  const int all = (len + KW - 1) / KW;
+  // the CTA's tiles
+  const int begin = PART ? (int)((int64_t)all * blockIdx.z / parts.count) : 0;
+  const int tiles = PART ? (int)((int64_t)all * (blockIdx.z + 1) / parts.count) : all;
+  if (PART) {
+    page0 = look(begin + warp);
+    page1 = look(begin + warp + W);
+    page2 = look(begin + warp + 2 * W);
+  }
+  const bool inside = beg >= 0 && end >= beg && end <= a.req.ntok && end - beg <= a.max_new;
+  const int fresh = inside ? (int)(end - beg) : 0, cols = fresh * a.G;
+  const auto table_ok = [&]() {
+    bool good = true;
+    for (int i = tid; i < a.req.R; i += 32 * W) {
+      const int64_t from = a.req.begin(i), to = a.req.begin(i + 1);
+      good = good && to >= from && to - from <= a.max_new && (i > 0 || from == 0) && (i + 1 < a.req.R || to == a.req.ntok);
+    }
+    return good && (!a.groups.of || a.groups.ok(a.req, tid, 32 * W));
+  };
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && !__syncthreads_and(table_ok())) {
+    if (tid == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
+    return;
+  }
+  if (h == 0 && col0 == 0 && blockIdx.z == 0 && tid == 0 && len != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
   if (col0 >= cols) return;
-  const int tiles = (len + KW - 1) / KW;
 
-  // a tile's codes into one of the warp's two stages: lane l looks up slot l
-  const auto fetch = [&](int tile, int stage) {
+  // A tile goes through three steps, so that nothing waits for one before it: its blocks are
+  // looked up (lane l slot l), a turn later its codes and scales are asked for, and the
+  // scales come to shared memory before it is used.
+  float kscale = 0.f, vscale = 0.f;
+  const auto fetch = [&](int tile, int page, int stage) {
     unsigned char *st = ring + stage * C::kStage;
     if (tile < tiles) {
       const int j = tile * KW + lane % KW;
-      int page = -1;
-      uint32_t off = 0;
-      if (j < len) {
-        const uint32_t block = block_of(a, j);
-        off = j - block * a.bs;
-        page = page_of(a, r, block);
-        if (page < 0) raise(a.status, KVX_FLAG_BAD_BLOCK);
-      }
+      if (j >= len) page = -1;
+      else if (page < 0) raise(a.status, KVX_FLAG_BAD_BLOCK);
       const unsigned valid = __ballot_sync(~0u, page >= 0);
       const uint32_t block = page < 0 ? 0u : (uint32_t)page * a.H + h;
-      const uint32_t row = page < 0 ? 0u : block * a.bs + off;
+      const uint32_t row = page < 0 ? 0u : block * a.bs + (j - block_of(a, j) * a.bs);
+      kscale = page >= 0 ? __ldg(a.ks + block) : 0.f;
+      vscale = page >= 0 ? __ldg(a.vs + block) : 0.f;
       const int c = lane % CH;
 #pragma unroll
       for (int i = 0; i < KW * CH / 32; ++i) {
@@ -218,37 +279,47 @@ __global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constan
         cp_async16(st + piece_at<DP>(j, c), a.k + at, there ? 16 : 0);
         cp_async16(st + C::kTile + piece_at<DP>(j, c), a.v + at, there ? 16 : 0);
       }
-      // scales by plain loads, which are waited for with the codes' lookups
-      if (lane < KW) {
-        reinterpret_cast<float *>(st + 2 * C::kTile)[lane] = page >= 0 ? __ldg(a.ks + block) : 0.f;
-        reinterpret_cast<float *>(st + 2 * C::kTile)[KW + lane] = page >= 0 ? __ldg(a.vs + block) : 0.f;
-      }
       if (lane == 0) *reinterpret_cast<unsigned *>(st + 2 * C::kTile + 2 * KW * 4) = valid;
     }
     cp_async_commit();
   };
-  fetch(warp, 0);
-  fetch(warp + W, 1);
-  const int first = first_limit(a, len, fresh), limits = cols - col0 < COLS ? -1 : first + col0 / a.G;
+  const auto put_scales = [&](int stage, float k, float v) {
+    float *to = reinterpret_cast<float *>(ring + stage * C::kStage + 2 * C::kTile);
+    if (lane < KW) {
+      to[lane] = k;
+      to[KW + lane] = v;
+    }
+  };
+  fetch(begin + warp, page0, 0);
+  float k_now = kscale, v_now = vscale;
+  fetch(begin + warp + W, page1, 1);
+  const int first = first_limit(a, len, fresh), more = limit_step(a);
+  const int limits = cols - col0 < COLS ? -1 : first + col0 / a.G * more;
   int limit[NT][2];          // last slot that the thread's columns see
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int col = col0 + 8 * n + 2 * t + e;
-      limit[n][e] = col < cols ? first + col / a.G : -1;
+      limit[n][e] = col < cols ? first + col / a.G * more : -1;
     }
   Queries<C> qf;
   qf.load(p, beg, h, col0, cols, qs, col_scale);
+  const bool good = table_ok();
   Sums<C> x;
   x.clear();
   int stage = 0;
-  for (int tile = warp; tile < tiles; tile += W) {
+  for (int tile = begin + warp; tile < tiles; tile += W) {
+    const int page3 = look(tile + 3 * W);
+    put_scales(stage, k_now, v_now);
+    k_now = kscale;
+    v_now = vscale;
     cp_async_wait<1>();
     __syncwarp();
     x.add(ring + stage * C::kStage, tile * KW, qf, qs, limit, limits);
     __syncwarp();
-    fetch(tile + 2 * W, stage);
+    fetch(tile + 2 * W, page2, stage);
+    page2 = page3;
     stage ^= 1;
   }
   cp_async_wait<0>();
@@ -265,13 +336,51 @@ __global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constan
         warp_l[warp * COLS + 8 * n + 2 * t + e] = x.l[n][e] * (kUnit * 16384.f);
       }
     }
-  wait_for_kernel_before();
-  __syncthreads();             // and the ring is free
+  if (!PART) wait_for_kernel_before();
+  // one result of the prefix: its rows are on their way before they are needed
+  constexpr int kQuads = 8 * (DP / 4) / (32 * W);
+  float4 before_row[NT][kQuads];
+  if (!PART && !parts.count) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k) {
+        const int i = tid + k * 32 * W, d = i % (DP / 4) * 4, col = col0 + 8 * n + i / (DP / 4);
+        before_row[n][k] = col < cols && d < a.d ? __ldcg(reinterpret_cast<const float4 *>(
+                                                       a.before + ((beg + col / a.G) * a.Hq + h * a.G + col % a.G) * a.d + d))
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+  }
+  if (!__syncthreads_and(good)) return;      // and the ring is free
+  float *red = reinterpret_cast<float *>(smem);
+  constexpr int ROWF = DP + 4;
+  const auto put_sums = [&](int n) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float *row = red + (warp * 8 + 2 * t + e) * ROWF;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        *reinterpret_cast<float2 *>(row + 16 * c + 2 * g) = make_float2(x.o[n][c][e] * kUnit * x.vref, x.o[n][c][2 + e] * kUnit * x.vref);
+    }
+  };
+  put_sums(0);
+  if (!PART && parts.count) {
+    for (int i = tid; i < parts.count * COLS; i += 32 * W) {
+      const int q = i / COLS, col = col0 + i % COLS;
+      const float2 y = col < cols ? __ldcg(parts.tops + q * parts.rows + (beg + col / a.G) * a.Hq + h * a.G + col % a.G)
+                                  : make_float2(-INFINITY, 0.f);
+      part_of[i] = y.x;
+      part_total[i] = y.y;
+    }
+    __syncthreads();
+  }
   if (tid < COLS && col0 + tid < cols) {
     const int col = col0 + tid;
     float mm = -INFINITY, l = 0.f;
 #pragma unroll
     for (int v = 0; v < W; ++v) mm = fmaxf(mm, warp_m[v * COLS + tid]);
+    if (!PART)
+      for (int q = 0; q < parts.count; ++q) mm = fmaxf(mm, part_of[q * COLS + tid]);
 #pragma unroll
     for (int v = 0; v < W; ++v) {
       const float f = ex2(warp_m[v * COLS + tid] - finite_or_0(mm));
@@ -280,36 +389,58 @@ __global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constan
     }
     const int64_t tok = beg + col / a.G;
     const int hq = h * a.G + col % a.G;
-    const Joined j = join_before(a, tok, hq, mm, kRoom, l);
-    own_of[tid] = l != 0.f ? j.own / l : 0.f;
-    before_of[tid] = j.before;
-    if (a.lse) a.lse[tok * a.Hq + hq] = j.lse.y == INFINITY ? -INFINITY : (j.lse.x + j.lse.y) * kLn2;
+    if (PART) {
+      own_of[tid] = 1.f;
+      parts.tops[(int64_t)blockIdx.z * parts.rows + tok * a.Hq + hq] = make_float2(mm, l);
+    } else if (parts.count) {
+      for (int q = 0; q < parts.count; ++q) {
+        const float f = ex2(part_of[q * COLS + tid] - finite_or_0(mm));
+        l += f * part_total[q * COLS + tid];
+        part_of[q * COLS + tid] = f;
+      }
+      own_of[tid] = before_of[tid] = l != 0.f ? 1.f / l : 0.f;
+      if (a.lse) a.lse[tok * a.Hq + hq] = l != 0.f ? (mm + (kRoom + log2f(l))) * kLn2 : -INFINITY;
+    } else {
+      const Joined j = join_before(a, tok, hq, mm, kRoom, l);
+      own_of[tid] = l != 0.f ? j.own / l : 0.f;
+      before_of[tid] = j.before;
+      if (a.lse) a.lse[tok * a.Hq + hq] = j.lse.y == INFINITY ? -INFINITY : (j.lse.x + j.lse.y) * kLn2;
+    }
   }
-  float *red = reinterpret_cast<float *>(smem);
-  constexpr int ROWF = DP + 4;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    if (n > 0) __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float *row = red + (warp * 8 + 2 * t + e) * ROWF;
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-        *reinterpret_cast<float2 *>(row + 16 * c + 2 * g) = make_float2(x.o[n][c][e] * kUnit * x.vref, x.o[n][c][2 + e] * kUnit * x.vref);
+    if (n > 0) {
+      __syncthreads();
+      put_sums(n);
     }
     __syncthreads();
-    for (int i = tid; i < 8 * (DP / 4); i += 32 * W) {
-      const int in = i / (DP / 4), d = i % (DP / 4) * 4, c = 8 * n + in, col = col0 + c;
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+      const int i = tid + k * 32 * W, in = i / (DP / 4), d = i % (DP / 4) * 4, c = 8 * n + in, col = col0 + c;
       if (col >= cols || d >= a.d) continue;
       const int64_t tok = beg + col / a.G;
       const int hq = h * a.G + col % a.G;
-      const float4 b = __ldcg(reinterpret_cast<const float4 *>(a.before + (tok * a.Hq + hq) * a.d + d));
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int64_t row = tok * a.Hq + hq;
+      float4 b = before_row[n][k], y = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!PART && parts.count) {
+        b = y;
+#pragma unroll 16
+        for (int q = 0; q < parts.count; ++q) {
+          const float f = part_of[q * COLS + c];
+          const float4 z = __ldcg(reinterpret_cast<const float4 *>(parts.sums + (q * parts.rows + row) * a.d + d));
+          // a split without slots that count left no sums
+          if (f != 0.f) b = make_float4(fmaf(f, z.x, b.x), fmaf(f, z.y, b.y), fmaf(f, z.z, b.z), fmaf(f, z.w, b.w));
+        }
+      }
 #pragma unroll
       for (int v = 0; v < W; ++v) {
         const float f = warp_m[v * COLS + c];
         const float4 z = *reinterpret_cast<const float4 *>(red + (v * 8 + in) * ROWF + d);
         y = make_float4(fmaf(f, z.x, y.x), fmaf(f, z.y, y.y), fmaf(f, z.z, y.z), fmaf(f, z.w, y.w));
+      }
+      if (PART) {
+        *reinterpret_cast<float4 *>(parts.sums + ((int64_t)blockIdx.z * parts.rows + row) * a.d + d) = y;
+        continue;
       }
       const float own = own_of[c], before = before_of[c];
       y = make_float4(y.x * own + b.x * before, y.y * own + b.y * before, y.z * own + b.z * before, y.w * own + b.w * before);
@@ -341,39 +472,76 @@ __global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constan
 }
 
 template <int DP, int NT, int PARTS>
-kvx_status launch_own(const SplitParams &p, int groups, cudaStream_t s) {
-  using C = SplitCfg<DP, NT, PARTS, (DP <= 128 && NT * PARTS <= 2 ? 2 : 1), 4, 2>;
-  static_assert(C::kStage % 16 == 0 && 4 * 8 * (DP + 4) * 4 <= C::kRing, "shared memory");
+kvx_status launch_own(const OwnParams &p, int groups, bool part, cudaStream_t s) {
+  constexpr int W = DP <= 128 ? OWN_W : 4;
+  using C = SplitCfg<DP, NT, PARTS, (DP <= 128 && NT * PARTS <= 2 ? OWN_MT : 1), W, 2>;
+  static_assert(C::kStage % 16 == 0 && W * 8 * (DP + 4) * 4 <= C::kRing, "shared memory");
   constexpr int smem = (int)own_smem<C>();
-  if (cudaFuncSetAttribute(own_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return KVX_ERR_CUDA;
-  return launch_after(own_kernel<C>, dim3((unsigned)(p.a.req.R * p.a.H), (unsigned)groups), 128, smem, s, p);
+  const auto kernel = part ? own_kernel<C, true> : own_kernel<C, false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return KVX_ERR_CUDA;
+  return launch_after(kernel, dim3((unsigned)(p.s.a.req.R * p.s.a.H), (unsigned)groups, part ? (unsigned)p.parts.count : 1u), 32 * W, smem,
+                      s, p);
 }
+// Columns of a CTA: registers hold 4096 sums a warp.
+int columns_of(int64_t most, int d) { return most <= 8 ? 8 : OWN_COLS; }
 template <int PARTS>
-kvx_status launch_dim(const SplitParams &p, int most, cudaStream_t s) {
-  // columns of a CTA: registers hold 4096 sums a warp
-  const int cols = most <= 8 ? 8 : most <= 16 || p.a.d > 128 ? 16 : 32, groups = (most + cols - 1) / cols;
-  if (p.a.d > 128) return cols == 8 ? launch_own<256, 1, PARTS>(p, groups, s) : launch_own<256, 2, PARTS>(p, groups, s);
-  if (p.a.d > 64)
-    return cols == 8    ? launch_own<128, 1, PARTS>(p, groups, s)
-           : cols == 16 ? launch_own<128, 2, PARTS>(p, groups, s)
-                        : launch_own<128, 4, PARTS>(p, groups, s);
-  return cols == 8    ? launch_own<64, 1, PARTS>(p, groups, s)
-         : cols == 16 ? launch_own<64, 2, PARTS>(p, groups, s)
-                      : launch_own<64, 4, PARTS>(p, groups, s);
+kvx_status launch_dim(const OwnParams &p, int most, bool part, cudaStream_t s) {
+  const int d = p.s.a.d, cols = columns_of(most, d), groups = (most + cols - 1) / cols;
+  if (d > 128) return cols == 8 ? launch_own<256, 1, PARTS>(p, groups, part, s) : launch_own<256, 2, PARTS>(p, groups, part, s);
+  if (d > 64)
+    return cols == 8    ? launch_own<128, 1, PARTS>(p, groups, part, s)
+           : cols == 16 ? launch_own<128, 2, PARTS>(p, groups, part, s)
+           : cols == 24 ? launch_own<128, 3, PARTS>(p, groups, part, s)
+                        : launch_own<128, 4, PARTS>(p, groups, part, s);
+  return cols == 8    ? launch_own<64, 1, PARTS>(p, groups, part, s)
+         : cols == 16 ? launch_own<64, 2, PARTS>(p, groups, part, s)
+         : cols == 24 ? launch_own<64, 3, PARTS>(p, groups, part, s)
+                      : launch_own<64, 4, PARTS>(p, groups, part, s);
+}
+int64_t rows_of(const kvx_attend8_args *a) { return (int64_t)(a->q_heads / a->cache.heads) * most_new(a); }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+// Bytes of the parts' sums, maxima and totals: at most kPartRoom, or there is one result.
+constexpr size_t kPartRoom = (size_t)32 << 20;
+size_t bytes_of(int64_t parts, int64_t rows, int64_t d) {
+  const double b = (double)parts * rows * (4 * d + 8) + 512;
+  return b > 2 * (double)kPartRoom ? 2 * kPartRoom : up256((size_t)(parts * rows * d * 4)) + up256((size_t)(parts * rows * 8));
 }
 
 }  // namespace
 
 bool kvx_attend8_own_supports(const kvx_attend8_args *a) {
-  const int64_t most = (int64_t)(a->q_heads / a->cache.heads) * most_new(a);
-  return most <= 64 && a->max_len <= 2048 && (int64_t)a->num_requests * a->cache.heads <= INT32_MAX;
+  return rows_of(a) <= 64 && a->max_len <= 2048 && (int64_t)a->num_requests * a->cache.heads <= INT32_MAX;
 }
 
-kvx_status kvx_attend8_own_launch(const kvx_attend8_args *a, const kvx8::AttendParams &params, cudaStream_t s) {
-  SplitParams p = {};
-  p.a = params;
+// Splits of the prefixes' slots that let about two CTAs an SM work, each on at least four
+// tiles of its warps; 0 where the products are too many for 16 x 8 x 16 instructions.
+int kvx_attend8_parts(const kvx_attend8_args *before) {
+  const int64_t most = rows_of(before), rows = before->ntok * before->q_heads, d = before->cache.head_dim;
+  const double work = (double)rows * before->max_len * (double)d * (before->dtype == KVX_BF16 ? 1 : 2);
+  const int cols = columns_of(most, (int)d);
+  const int64_t items = (int64_t)before->num_requests * before->cache.heads * ((most + cols - 1) / cols);
+  if (work > kMostWork || items > 65535 || before->max_len == 0) return 0;
+  const int64_t fill = (2 * 152 + items - 1) / items, tiles = ((int64_t)before->max_len + 255) / 256;
+  int64_t parts = fill < tiles ? fill : tiles;
+  if (parts > kMostParts) parts = kMostParts;
+  return bytes_of(parts, rows, d) <= kPartRoom ? (int)parts : 0;
+}
+// What calls of at most these sizes leave in parts.
+size_t kvx_attend8_parts_bytes(const kvx_attend8_args *before) {
+  const size_t most = bytes_of(kMostParts, before->ntok * before->q_heads, before->cache.head_dim);
+  return most < kPartRoom ? most : kPartRoom;
+}
+
+kvx_status kvx_attend8_own_launch(const kvx_attend8_args *a, const kvx8::AttendParams &params, int parts, void *part_bytes, bool prefixes,
+                                  cudaStream_t s) {
+  OwnParams p = {};
+  p.s.a = params;
   const int size = a->dtype == KVX_BF16 ? 2 : 4, most = params.G * params.max_new;
-  p.vec_q = aligned_to(a->q, 16) && ((params.qt | params.qh) * size) % 16 == 0;
-  p.vec_out = aligned_to(a->out, 4 * size) && (params.ot | params.oh) % 4 == 0;
-  return size == 2 ? launch_dim<1>(p, most, s) : launch_dim<2>(p, most, s);
+  p.s.vec_q = aligned_to(a->q, 16) && ((params.qt | params.qh) * size) % 16 == 0;
+  p.s.vec_out = aligned_to(a->out, 4 * size) && (params.ot | params.oh) % 4 == 0;
+  p.parts.count = parts;
+  p.parts.rows = a->ntok * a->q_heads;
+  p.parts.sums = (float *)part_bytes;
+  p.parts.tops = (float2 *)((char *)part_bytes + up256((size_t)parts * p.parts.rows * params.d * sizeof(float)));
+  return size == 2 ? launch_dim<1>(p, most, prefixes, s) : launch_dim<2>(p, most, prefixes, s);
 }

@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(256, 3) join_kernel(const __grid_constant__ Tc
   w.h = x.h;
   w.group = x.group;
   w.beg = x.beg;
-  join_rows<G, 4>(p, w, x.c0, x.ctas, blockIdx.y * 8 + threadIdx.x / 32, gridDim.y * 8, x.rows);
+  join_rows<G, 1>(p, w, x.c0, x.ctas, blockIdx.y * 8 + threadIdx.x / 32, gridDim.y * 8, x.rows);
 }
 // The same with a block for a row, whose warps share the parts: few rows, many parts.
 template <class G>
@@ -2402,7 +2402,7 @@ kvx_status launch(K kernel, int threads, size_t smem, const TcParams &p, const C
   kernel<<<p.grid, threads, smem, s>>>(p, mk, mv);
   if (const kvx_status st = launched()) return st;
   if constexpr (G::ROWS <= 16) return launch_after(join_row_kernel<G>, dim3(p.grid - 1, p.slot_rows), 256, 0, s, p);
-  return launch_after(join_kernel<G>, dim3(p.grid - 1, (p.slot_rows + 31) / 32), 256, 0, s, p);
+  return launch_after(join_kernel<G>, dim3(p.grid - 1, (p.slot_rows + 7) / 8), 256, 0, s, p);
 }
 
 }  // namespace

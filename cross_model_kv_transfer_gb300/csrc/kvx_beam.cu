@@ -24,6 +24,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kvx_cache8.cuh"
 
 namespace {
@@ -71,24 +73,39 @@ __device__ __forceinline__ bool lives(const BeamParams &p, int row) {
 }
 
 // E logits a thread and chunk, V a load.  Position of element j * V + k: j * 256 V + V t + k.
+// As they lie in memory first, so that the next chunk's are on their way while one is
+// worked on; those behind the end are -inf.
 template <class T, int V, int E>
-__device__ __forceinline__ void load_chunk(const T *row, int at, int end, float (&x)[E]) {
+struct Raw {
+  static constexpr int LOADS = E / V;
+  typename std::conditional<V == 1, float, uint4>::type w[LOADS];
+  __device__ __forceinline__ void load(const T *row, int64_t at, int end) {
 #pragma unroll
-  for (int j = 0; j < E / V; ++j) {
-    const int v = at + (j * kThreads + threadIdx.x) * V;
-    if constexpr (V == 1) {
-      x[j] = v < end ? (float)row[v] : -INFINITY;
-    } else {
-      // rows are whole loads: a load is in or out; out are -inf
-      constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-      const uint4 w = v < end ? __ldcs(reinterpret_cast<const uint4 *>(row + v)) : make_uint4(none, none, none, none);
-      const uint32_t b[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        x[j * V + k] = __uint_as_float(sizeof(T) == 4 ? b[k % 4] : k % 2 ? b[k / 2 % 4] & 0xffff0000u : b[k / 2 % 4] << 16);
+    for (int j = 0; j < LOADS; ++j) {
+      const int64_t v = at + (j * kThreads + threadIdx.x) * V;
+      if constexpr (V == 1) {
+        w[j] = v < end ? (float)row[v] : -INFINITY;
+      } else {
+        // rows are whole loads: a load is in or out
+        constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+        w[j] = v < end ? __ldcs(reinterpret_cast<const uint4 *>(row + v)) : make_uint4(none, none, none, none);
+      }
     }
   }
-}
+  __device__ __forceinline__ void values(float (&x)[E]) const {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      if constexpr (V == 1) {
+        x[j] = w[j];
+      } else {
+        const uint32_t b[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          x[j * V + k] = __uint_as_float(sizeof(T) == 4 ? b[k % 4] : k % 2 ? b[k / 2 % 4] & 0xffff0000u : b[k / 2 % 4] << 16);
+      }
+    }
+  }
+};
 // The sum of a thread's chunk relative to exp(m).
 template <int E>
 __device__ __forceinline__ float sum_of(const float (&x)[E], float m) {
@@ -108,7 +125,7 @@ struct RowShared {
   double total;                 // of the CTA, relative to exp(unit)
   float sum[kWarps], max[kWarps];
   float unit;
-  int count, now;               // the list's; which of best is the last
+  int count[3], many, now;      // the list's, of a chunk that overflows; which of best is the last
 };
 // The first n of `count` keys, ranked, to `best` (0 behind the last); all threads call it.
 __device__ __forceinline__ void rank_list(const unsigned long long *list, int count, unsigned long long *best, int n) {
@@ -125,20 +142,21 @@ __device__ __forceinline__ void rank_list(const unsigned long long *list, int co
 // The chunk's list from ranked keys of the threads: where it overflows.  Apart from the
 // loop, from the logits read again, so that it costs that no registers.
 template <class T, int V, int E>
-__device__ __noinline__ void list_by_keys(RowShared &sh, int n, unsigned long long before, const T *row, int at, int end) {
+__device__ __noinline__ int list_by_keys(RowShared &sh, int n, unsigned long long before, const T *row, int at, int end) {
   const int tid = threadIdx.x;
+  Raw<T, V, E> raw;
+  raw.load(row, at, end);
   float x[E];
-  load_chunk<T, V, E>(row, at, end, x);
+  raw.values(x);
   const auto key = [&](int e) {
     return x[e] < INFINITY ? key_of(x[e] + 0.f, at + (e / V * kThreads + tid) * V + e % V) : 0ull;
   };
   unsigned long long mine = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) mine = max(mine, key(e));
-  __syncthreads();                  // the count that led here has been read by all
   sh.top[tid] = mine;
   if (tid == 0) {
-    sh.count = 0;
+    sh.many = 0;
     sh.bound = 1;                   // fewer than N threads have anything: all of it counts
   }
   __syncthreads();
@@ -151,9 +169,10 @@ __device__ __noinline__ void list_by_keys(RowShared &sh, int n, unsigned long lo
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const unsigned long long k = key(e);
-      if (k >= bound && k > before) sh.list[atomicAdd(&sh.count, 1)] = k;
+      if (k >= bound && k > before) sh.list[atomicAdd(&sh.many, 1)] = k;
     }
   __syncthreads();
+  return sh.many;
 }
 
 template <class T, int V, int E>
@@ -175,10 +194,18 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
   int now = 0;
   const int rounds = (p.N + kWarps - 1) / kWarps;
   if (tid < kMostBeams) sh.best[0][tid] = 0;
-  if (tid == 0) sh.count = 0;
-  for (int64_t at = begin; at < end; at += kThreads * E) {
+  if (tid == 0) sh.count[0] = 0;
+  // two to a register, the next chunk's logits are on their way while one is worked on; of
+  // fp32 ones other CTAs of the SM have theirs
+  constexpr bool kAhead = sizeof(T) == 2 && V > 1;
+  Raw<T, V, E> next;
+  if (kAhead) next.load(x_of, begin, end);
+  int turn = 0;
+  for (int64_t at = begin; at < end; at += kThreads * E, turn = turn == 2 ? 0 : turn + 1) {
     float x[E];
-    load_chunk<T, V, E>(x_of, (int)at, end, x);
+    if (!kAhead) next.load(x_of, at, end);
+    next.values(x);
+    if (kAhead) next.load(x_of, at + kThreads * E, end);
     float top = x[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
@@ -198,43 +225,48 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
     }
     sum = sum * ex2((unit - reference()) * kLog2e) + more;
     unit = fmaxf(unit, top);
-    // the bound
-    uint32_t left = top > -INFINITY ? ordered(top + 0.f) : 0u, least = 0;
-    for (int i = 0; i < rounds; ++i) {
-      least = __reduce_max_sync(~0u, left);
-      left = left == least ? 0u : left;
-    }
-    if (lane == 0) sh.warp_bound[warp] = least;
-    __syncthreads();
-    const unsigned long long before = sh.best[now][p.N - 1];
-    least = ~0u;
+    // the bound: what was found before, or of the first chunk what the warps agree on
+    unsigned long long before = 0;
+    float bound = -INFINITY;
+    if (at == begin) {
+      uint32_t left = top > -INFINITY ? ordered(top + 0.f) : 0u, least = 0;
+      for (int i = 0; i < rounds; ++i) {
+        least = __reduce_max_sync(~0u, left);
+        left = left == least ? 0u : left;
+      }
+      if (lane == 0) sh.warp_bound[warp] = least;
+      __syncthreads();
+      least = ~0u;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) least = min(least, sh.warp_bound[w]);
-    least = max(least, (uint32_t)(before >> 32));
-    const float bound = least ? logit_of((unsigned long long)least << 32) : -INFINITY;
+      for (int w = 0; w < kWarps; ++w) least = min(least, sh.warp_bound[w]);
+      if (least) bound = logit_of((unsigned long long)least << 32);
+    } else {
+      before = sh.best[now][p.N - 1];
+      if (before) bound = logit_of(before);
+    }
     const auto position = [&](int e) { return (int)at + (e / V * kThreads + tid) * V + e % V; };
-    const auto put = [&](unsigned long long key) {
-      const int to = atomicAdd(&sh.count, 1);
-      if (to < kList - kMostBeams) sh.list[to] = key;
-    };
     if (top >= bound) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (x[e] >= bound) {
           const unsigned long long key = key_of(x[e] + 0.f, position(e));   // -0 and 0 are equal
-          if (key > before) put(key);
+          if (key > before) {
+            const int to = atomicAdd(&sh.count[turn], 1);
+            if (to < kList - kMostBeams) sh.list[to] = key;
+          }
         }
     }
+    // three counts in turn: this chunk's, the next one's, and one that a thread may still read
+    if (tid == 0) sh.count[turn == 2 ? 0 : turn + 1] = 0;
     __syncthreads();
-    if (sh.count > kList - kMostBeams) list_by_keys<T, V, E>(sh, p.N, before, x_of, (int)at, end);
-    const int found = sh.count;
+    int found = sh.count[turn];
     if (found) {                      // of the whole CTA
+      if (found > kList - kMostBeams) found = list_by_keys<T, V, E>(sh, p.N, before, x_of, (int)at, end);
       const unsigned long long old = tid < p.N ? sh.best[now][tid] : 0;
       if (old) sh.list[found + tid] = old;      // they are at the front of best
       const int held = __syncthreads_count(old != 0);
       rank_list(sh.list, found + held, sh.best[now ^ 1], p.N);
       now ^= 1;
-      if (tid == 0) sh.count = 0;
       __syncthreads();
     }
   }
@@ -320,68 +352,55 @@ __device__ __forceinline__ unsigned long long ordered(double x) {
 __device__ __forceinline__ double score_of(unsigned long long k) {
   return __longlong_as_double((long long)(k ^ (k >> 63 ? 1ull << 63 : ~0ull)));
 }
-// a before b?
-__device__ __forceinline__ bool first(unsigned long long a, int at, unsigned long long b, int bt) {
-  return a > b || (a == b && at < bt);
-}
 constexpr int kEach = kMostBeams * kMostBeams / kThreads;     // candidates a thread
 struct PickShared {
-  unsigned long long top[kThreads], list[kMostBeams * kEach], bound;
-  int place[kThreads], list_place[kMostBeams * kEach], bound_place, count;
+  unsigned long long list[kMostBeams * kMostBeams];
+  int place[kMostBeams * kMostBeams], count;
+  uint32_t warp_bound[kWarps];
 };
 // Candidate i = k * N + j of a request: the j-th of beam k.  In that order equal scores
-// go to the lower beam and token.  Ranked as a chunk's logits are where they overflow.
+// go to the lower beam and token.  The list is bounded as a chunk's is, by the scores'
+// upper halves, and has room for all.
 __global__ void __launch_bounds__(kThreads) pick_kernel(const __grid_constant__ BeamParams p) {
   __shared__ PickShared sh;
   wait_for_kernel_before();
-  const int tid = threadIdx.x, b = blockIdx.x, all = p.K * p.N, threads = min(all, kThreads);
-  unsigned long long x[kEach], top = 0;
-  int place = INT32_MAX;
+  const int tid = threadIdx.x, b = blockIdx.x, all = p.K * p.N;
+  unsigned long long x[kEach];
+  uint32_t top = 0, bound = ~0u;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const int i = e * kThreads + tid;
+    // beams side by side, so that each warp has some of all
+    const int c = e * kThreads + tid, k = c % p.K, j = c / p.K, row = b * p.K + k;
     x[e] = 0;
-    if (i >= all) continue;
-    const int row = b * p.K + i / p.N;
+    if (c >= all) continue;
     const float score = p.scores[row];
     if (p.done && p.done[row]) {
-      if (i % p.N == 0 && fabsf(score) < INFINITY) x[e] = ordered((double)score);
+      if (j == 0 && fabsf(score) < INFINITY) x[e] = ordered((double)score);
     } else {
-      const unsigned long long key = __ldcg(p.keys + (int64_t)row * p.N + i % p.N);
+      const unsigned long long key = __ldcg(p.keys + (int64_t)row * p.N + j);
       if (key) x[e] = ordered((double)score + ((double)logit_of(key) - __ldcg(p.lse + row)));
     }
-    if (x[e] > top) {
-      top = x[e];
-      place = i;
-    }
+    top = max(top, (uint32_t)(x[e] >> 32));
   }
-  sh.top[tid] = top;
-  sh.place[tid] = place;
-  if (tid == 0) {
-    sh.count = 0;
-    sh.bound = 0;
-    sh.bound_place = INT32_MAX;
+  const int rounds = (p.N + kWarps - 1) / kWarps;
+  uint32_t least = 0;
+  for (int i = 0; i < rounds; ++i) {
+    least = __reduce_max_sync(~0u, top);
+    top = top == least ? 0u : top;
   }
-  __syncthreads();
-  if (top) {
-    int above = 0;
-#pragma unroll 4
-    for (int j = 0; j < threads; ++j) above += first(sh.top[j], sh.place[j], top, place);
-    if (above == p.N - 1) {
-      sh.bound = top;
-      sh.bound_place = place;
-    }
-  }
+  if (tid % 32 == 0) sh.warp_bound[tid / 32] = least;
+  if (tid == 0) sh.count = 0;
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int i = e * kThreads + tid;
-    if (x[e] && !first(sh.bound, sh.bound_place, x[e], i)) {
+  for (int w = 0; w < kWarps; ++w) bound = min(bound, sh.warp_bound[w]);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (x[e] && (uint32_t)(x[e] >> 32) >= bound) {
       const int at = atomicAdd(&sh.count, 1);
       sh.list[at] = x[e];
-      sh.list_place[at] = i;
+      const int c = e * kThreads + tid;
+      sh.place[at] = c % p.K * p.N + c / p.K;
     }
-  }
   __syncthreads();
   const int n = sh.count;
   const auto put = [&](int to, int token, int parent, float score) {
@@ -392,11 +411,11 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const __grid_constant__ 
     if (p.new_done) p.new_done[at] = token >= 0 && token == p.eos;
   };
   if (tid < p.N && tid >= n) put(tid, -1, -1, -INFINITY);
-  if (tid < n) {
-    const unsigned long long s = sh.list[tid];
-    const int i = sh.list_place[tid], row = b * p.K + i / p.N;
+  for (int k = tid; k < n; k += kThreads) {
+    const unsigned long long s = sh.list[k];
+    const int i = sh.place[k], row = b * p.K + i / p.N;
     int above = 0;
-    for (int j = 0; j < n; ++j) above += first(sh.list[j], sh.list_place[j], s, i);
+    for (int j = 0; j < n; ++j) above += sh.list[j] > s || (sh.list[j] == s && sh.place[j] < i);
     if (above < p.N)
       put(above, p.done && p.done[row] ? p.eos : token_of(__ldcg(p.keys + (int64_t)row * p.N + i % p.N)), row,
           (float)score_of(s));

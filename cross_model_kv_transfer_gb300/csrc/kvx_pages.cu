@@ -29,8 +29,17 @@ struct CacheView {
   int64_t page;              // bytes of a page's keys or values
   int heads;
 };
+constexpr int kMaxTables = 8;
+// Tables whose entries become the pages' new numbers.
+struct Tables {
+  int32_t *table[kMaxTables];
+  int64_t entries[kMaxTables];
+  const int32_t *moved;
+  int count;
+};
 struct CopyParams {
   CacheView cache[kMaxCaches];
+  Tables tables;
   const int32_t *pairs, *count;   // count NULL: all pairs
   uint32_t *status;
   int64_t num_blocks;
@@ -41,6 +50,18 @@ struct CopyParams {
 // their way before the first store.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
   wait_for_kernel_before();
+  for (int x = 0; x < p.tables.count; ++x) {
+    int32_t *table = p.tables.table[x];
+    for (int64_t i = blockIdx.x * (int64_t)kCopyThreads + threadIdx.x; i < p.tables.entries[x]; i += (int64_t)gridDim.x * kCopyThreads) {
+      const int page = table[i];
+      if (page >= 0 && page < p.num_blocks) {
+        const int to = __ldcg(p.tables.moved + page);
+        if (to != page) table[i] = to;
+      } else if (page != -1) {
+        raise(p.status, KVX_FLAG_BAD_BLOCK);
+      }
+    }
+  }
   int n = p.num_pairs;
   if (p.count) {
     const int c = __ldcg(p.count);
@@ -51,6 +72,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     n = c;
   }
   const int per = p.pieces * p.num_caches;
+  if (per == 0) return;
   const int64_t units = (int64_t)n * per;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t pair = u / per;
@@ -96,10 +118,14 @@ kvx_status check_caches(const kvx_cache8 *caches, int n, int64_t num_blocks, int
   }
   return KVX_OK;
 }
+// The pages of all caches, and `tables` in the first launch.
 kvx_status copy_pages(const kvx_cache8 *caches, int n, int64_t num_blocks, const int32_t *pairs, int64_t num_pairs,
-                      const int32_t *count, uint32_t *status, cudaStream_t s) {
-  if (num_pairs == 0) return KVX_OK;
-  for (int first = 0; first < n; first += kMaxCaches) {
+                      const int32_t *count, const Tables &tables, uint32_t *status, cudaStream_t s) {
+  int64_t entries = 0;
+  for (int i = 0; i < tables.count; ++i) entries = tables.entries[i] > entries ? tables.entries[i] : entries;
+  if (num_pairs == 0) n = 0;
+  int first = 0;
+  do {
     CopyParams p = {};
     p.num_caches = n - first < kMaxCaches ? n - first : kMaxCaches;
     int64_t most = 0;
@@ -109,16 +135,20 @@ kvx_status copy_pages(const kvx_cache8 *caches, int n, int64_t num_blocks, const
       p.cache[i] = {(uint8_t *)c.k_codes, (uint8_t *)c.v_codes, c.k_scale, c.v_scale, page, c.heads};
       most = page > most ? page : most;
     }
+    if (first == 0) p.tables = tables;
     p.pairs = pairs;
     p.count = count;
     p.status = status;
     p.num_blocks = num_blocks;
     p.num_pairs = (int)num_pairs;
     p.pieces = (int)((most + kPiece - 1) / kPiece);
-    const int64_t units = num_pairs * p.num_caches * p.pieces;
-    const int64_t grid = units < 152 * 8 ? units : 152 * 8;     // eight CTAs an SM
-    if (const kvx_status st = launch_after(copy_kernel, dim3((unsigned)grid), kCopyThreads, 0, s, p)) return st;
-  }
+    int64_t grid = num_pairs * p.num_caches * p.pieces;
+    if (first == 0 && (entries + kCopyThreads - 1) / kCopyThreads > grid) grid = (entries + kCopyThreads - 1) / kCopyThreads;
+    if (grid > 152 * 8) grid = 152 * 8;         // eight CTAs an SM
+    if (grid > 0)
+      if (const kvx_status st = launch_after(copy_kernel, dim3((unsigned)grid), kCopyThreads, 0, s, p)) return st;
+    first += kMaxCaches;
+  } while (first < n);
   return KVX_OK;
 }
 
@@ -191,9 +221,11 @@ __global__ void __launch_bounds__(256) free_kernel(int32_t *refs, int64_t num_bl
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBigCtas = 8;
-// A workspace: sums of the warps, how many pages move, and a list of pages or pairs.
-constexpr int kSums = kBigCtas * kWarps, kCountAt = 3 * kSums, kListAt = 1024;
+// A workspace: sums of the warps, pages that are wanted, pairs that are copied; from kListAt
+// on a list of num_blocks pages and one of as many pairs.
+constexpr int kSums = kBigCtas * kWarps, kWantedAt = 3 * kSums, kCountAt = kWantedAt + 1, kListAt = 1024;
 static_assert(kCountAt < kListAt, "workspace");
+__host__ __device__ inline int64_t pairs_at(int64_t num_blocks) { return kListAt + (num_blocks + 63) / 64 * 64; }
 
 // A barrier of all threads of the grid, which is one CTA or one cluster; what they wrote
 // to global memory before it is seen behind it.
@@ -362,10 +394,13 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const __grid_const
     if (lane == 0) needs_of[in] = needs;
     __syncthreads();
     const int sum = __reduce_add_sync(~0u, needs_of[lane]);
-    if (threadIdx.x == 0) p.work[kCountAt] = sum;
+    if (threadIdx.x == 0) {
+      p.work[kWantedAt] = sum;
+      p.work[kCountAt] = 0;
+    }
   }
   barrier<CTAS>();
-  const int wanted = __ldcg(p.work + kCountAt);
+  const int wanted = __ldcg(p.work + kWantedAt);
   const int2 free_sum = sums_of<CTAS>(free_of, warp);
   const bool enough = wanted <= free_sum.y;
   // the free pages that are taken, in order
@@ -399,8 +434,15 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const __grid_const
     at += __popc(mask);
     if (e.first && e.row >= 0) {
       const bool copied = page >= 0 && old >= 0 && !e.whole;
-      p.copies[2 * (int64_t)e.row] = copied ? old : -1;
-      p.copies[2 * (int64_t)e.row + 1] = copied ? page : -1;
+      if (copied) {          // in any order: pages are copied to once
+        int32_t *to = p.work + pairs_at(p.num_blocks) + 2 * (int64_t)atomicAdd(p.work + kCountAt, 1);
+        to[0] = old;
+        to[1] = page;
+      }
+      if (p.copies) {
+        p.copies[2 * (int64_t)e.row] = copied ? old : -1;
+        p.copies[2 * (int64_t)e.row + 1] = copied ? page : -1;
+      }
     }
   });
 }
@@ -457,29 +499,6 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
     *p.used = used;
   }
 }
-constexpr int kMaxTables = 8;
-struct RewriteParams {
-  int32_t *table[kMaxTables];
-  int64_t entries[kMaxTables];
-  const int32_t *moved;
-  int64_t num_blocks;
-  uint32_t *status;
-};
-__global__ void __launch_bounds__(256) rewrite_kernel(const __grid_constant__ RewriteParams p) {
-  wait_for_kernel_before();
-  int32_t *table = p.table[blockIdx.y];
-  const int64_t n = p.entries[blockIdx.y];
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-    const int page = table[i];
-    if (page >= 0 && page < p.num_blocks) {
-      const int to = __ldcg(p.moved + page);
-      if (to != page) table[i] = to;
-    } else if (page != -1) {
-      raise(p.status, KVX_FLAG_BAD_BLOCK);
-    }
-  }
-}
-
 // --- host ------------------------------------------------------------------------
 
 // One CTA for a small pool, a cluster of eight for more.
@@ -514,7 +533,7 @@ bool workspace_ok(const void *ws, size_t bytes, int64_t num_blocks) {
 
 extern "C" size_t kvx_pages_workspace_bytes(int64_t num_blocks) {
   if (num_blocks < 1 || num_blocks > kMostPages) return 0;
-  return (kListAt + ((size_t)num_blocks + 63) / 64 * 64) * 4;
+  return (size_t)(pairs_at(num_blocks) + 2 * num_blocks) * 4;
 }
 
 extern "C" kvx_status kvx_cache8_copy(const kvx_cache8_copy_args *a, void *stream) {
@@ -523,7 +542,7 @@ extern "C" kvx_status kvx_cache8_copy(const kvx_cache8_copy_args *a, void *strea
   if (a->num_caches == 0) return KVX_OK;
   const int64_t num_blocks = a->caches[0].num_blocks;
   if (const kvx_status st = check_caches(a->caches, a->num_caches, num_blocks, 0)) return st;
-  return copy_pages(a->caches, a->num_caches, num_blocks, a->pairs, a->num_pairs, a->count, a->status, (cudaStream_t)stream);
+  return copy_pages(a->caches, a->num_caches, num_blocks, a->pairs, a->num_pairs, a->count, Tables{}, a->status, (cudaStream_t)stream);
 }
 
 extern "C" kvx_status kvx_pages_fork(const kvx_pages_fork_args *a, void *stream) {
@@ -557,7 +576,7 @@ extern "C" kvx_status kvx_pages_reserve(const kvx_pages_reserve_args *a, void *s
   if (const kvx_status st = check_caches(a->caches, a->num_caches, a->num_blocks, a->block_size)) return st;
   if (a->num_rows == 0) return KVX_OK;
   if ((int64_t)a->num_rows * a->width > INT32_MAX) return KVX_ERR_UNSUPPORTED;   // needs are counted in 32 bits
-  if (!a->table || !a->lens || !a->copies || !workspace_ok(a->workspace, a->workspace_bytes, a->num_blocks))
+  if (!a->table || !a->lens || !workspace_ok(a->workspace, a->workspace_bytes, a->num_blocks))
     return KVX_ERR_INVALID_ARG;
   ReserveParams p = {a->refs, a->num_blocks, a->table,      a->copies,   (int32_t *)a->workspace, a->lens,
                      a->add,  a->status,     a->block_size, a->num_rows, a->width,                a->add_all};
@@ -570,7 +589,9 @@ extern "C" kvx_status kvx_pages_reserve(const kvx_pages_reserve_args *a, void *s
   p.rows = (int)(((int64_t)a->num_rows + kWarps * at_once - 1) / (kWarps * at_once)) * at_once;
   cudaStream_t s = (cudaStream_t)stream;
   if (const kvx_status st = launch_counting(reserve_kernel<1>, reserve_kernel<kBigCtas>, p, s)) return st;
-  return copy_pages(a->caches, a->num_caches, a->num_blocks, a->copies, a->num_rows, nullptr, a->status, s);
+  if (a->num_caches == 0) return KVX_OK;
+  const int64_t most = a->num_rows < a->num_blocks ? a->num_rows : a->num_blocks;
+  return copy_pages(a->caches, a->num_caches, a->num_blocks, p.work + pairs_at(a->num_blocks), most, p.work + kCountAt, Tables{}, a->status, s);
 }
 
 extern "C" kvx_status kvx_pages_compact(const kvx_pages_compact_args *a, void *stream) {
@@ -579,25 +600,17 @@ extern "C" kvx_status kvx_pages_compact(const kvx_pages_compact_args *a, void *s
     return KVX_ERR_INVALID_ARG;
   if (const kvx_status st = check_caches(a->caches, a->num_caches, a->num_blocks, a->block_size)) return st;
   if (!workspace_ok(a->workspace, a->workspace_bytes, a->num_blocks)) return KVX_ERR_INVALID_ARG;
-  RewriteParams t = {};
-  int64_t most = 0;
+  Tables t = {};
   for (int i = 0; i < a->num_tables; ++i) {
     if (a->entries[i] < 0 || (a->entries[i] > 0 && (!a->tables[i] || !aligned_to(a->tables[i], 4)))) return KVX_ERR_INVALID_ARG;
     t.table[i] = a->tables[i];
     t.entries[i] = a->entries[i];
-    most = a->entries[i] > most ? a->entries[i] : most;
   }
   t.moved = a->moved;
-  t.num_blocks = a->num_blocks;
-  t.status = a->status;
+  t.count = a->num_tables;
   int32_t *work = (int32_t *)a->workspace;
   const CompactParams p = {a->refs, a->num_blocks, a->used, a->moved, work};
   cudaStream_t s = (cudaStream_t)stream;
   if (const kvx_status st = launch_counting(compact_kernel<1>, compact_kernel<kBigCtas>, p, s)) return st;
-  if (most > 0) {
-    const int64_t ctas = (most + 255) / 256;
-    if (const kvx_status st = launch_after(rewrite_kernel, dim3((unsigned)(ctas < 152 * 8 ? ctas : 152 * 8), a->num_tables), 256, 0, s, t))
-      return st;
-  }
-  return copy_pages(a->caches, a->num_caches, a->num_blocks, work + kListAt, a->num_blocks / 2, work + kCountAt, a->status, s);
+  return copy_pages(a->caches, a->num_caches, a->num_blocks, work + kListAt, a->num_blocks / 2, work + kCountAt, t, a->status, s);
 }

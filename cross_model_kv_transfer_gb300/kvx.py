@@ -1444,9 +1444,9 @@ class Pages:
         each behind a page of the row's own, taken from the free ones where
         there is none or others hold it too; a page that holds slots of the
         row is then copied in all ``caches``.  ``new`` is one number, or
-        one for each row (int32 tensor, at most ``max_new``).  Returns
-        the copied pages [R][2], from and to (-1: none).  With too few free
-        pages nothing changes, and ``status`` tells (KVX_FLAG_NO_PAGES)."""
+        one for each row (int32 tensor, at most ``max_new``).  ``copies`` [R][2]
+        (int32) receives the copied pages, from and to (-1: none).  With too few
+        free pages nothing changes, and ``status`` tells (KVX_FLAG_NO_PAGES)."""
         dev = self.device
         _on_device(dev)
         R, width, ptr = self._rows(table, lens)
@@ -1458,9 +1458,7 @@ class Pages:
             if new.shape[0] != R:
                 raise ValueError("new must hold one entry for each row")
             most = width * self.block_size if max_new is None else max_new
-        if copies is None:
-            copies = _new(stream, (R, 2), _Fast.i32, dev)
-        elif tuple(copies.shape) != (R, 2):
+        if copies is not None and tuple(copies.shape) != (R, 2):
             raise ValueError("copies must be [R][2]")
         if workspace is None:
             workspace = _on_stream(self.workspace, stream)
@@ -1472,7 +1470,6 @@ class Pages:
         st = _Fast.reserve(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_pages_reserve")
-        return copies
 
     def compact(self, tables, caches=(), *, used=None, moved=None, workspace=None, status=None,
                 stream=None):

@@ -884,7 +884,8 @@ typedef struct {
   const int32_t *lens;      /* [R] slots that each row holds                  */
   const int32_t *add;       /* [R] slots to reserve for each row, or NULL     */
   int32_t add_all;          /* the same for all rows, >= 0 (with add: a bound on it) */
-  int32_t *copies;          /* [R][2] pages copied, from and to, else -1, -1  */
+  int32_t *copies;          /* [R][2] pages copied, from and to, else -1, -1; or
+                               NULL                                           */
   const kvx_cache8 *caches; /* HOST array [num_caches] of the layers' caches, with
                                num_blocks and block_size as here (their block
                                tables are not used); or NULL                  */
@@ -904,8 +905,8 @@ typedef struct {
  * If fewer are free than are needed nothing changes (KVX_FLAG_NO_PAGES, copies all
  * -1): free some and call again.  A row whose length or whose new slots do not fit
  * its width reserves nothing (KVX_FLAG_BAD_LENGTH); an entry outside
- * [-1, num_blocks) counts as -1 (KVX_FLAG_BAD_BLOCK).  Asynchronous; one to four
- * launches, and one for every 32 caches. */
+ * [-1, num_blocks) counts as -1 (KVX_FLAG_BAD_BLOCK).  One launch, and one for every
+ * 32 caches. */
 kvx_status kvx_pages_reserve(const kvx_pages_reserve_args *args, void *stream);
 
 typedef struct {
@@ -929,8 +930,8 @@ typedef struct {
  * their order, into the free ones below it, for all caches, and rewrite the tables
  * by `moved`.  All tables that hold pages of the pool must be among them, or be
  * rewritten by `moved` afterwards.  An entry outside [-1, num_blocks) stays
- * (KVX_FLAG_BAD_BLOCK); one of a free page becomes -1.  Two or three launches, and one
- * for every 32 caches. */
+ * (KVX_FLAG_BAD_BLOCK); one of a free page becomes -1.  Two launches, one more
+ * for every 32 caches beyond the first. */
 kvx_status kvx_pages_compact(const kvx_pages_compact_args *args, void *stream);
 
 /* Scratch of the two calls above; 0 for a num_blocks that they refuse. */

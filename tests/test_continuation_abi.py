@@ -113,7 +113,7 @@ def test_pages_refuse():
                       dict(width=2 ** 27)]),
             (kvx.PagesFreeArgs, kvx.kvx_pages_free, shape),
             (kvx.PagesReserveArgs, kvx.kvx_pages_reserve,
-             shape + [dict(block_size=0), dict(lens=None), dict(add_all=-1), dict(copies=None), dict(workspace=None),
+             shape + [dict(block_size=0), dict(lens=None), dict(add_all=-1), dict(workspace=None),
                       dict(workspace=P + 4), dict(workspace_bytes=100), dict(num_caches=-1), dict(num_caches=1),
                       dict(width=2 ** 27)]),
             (kvx.PagesCompactArgs, kvx.kvx_pages_compact,

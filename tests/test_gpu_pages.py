@@ -35,6 +35,12 @@ def same_contents(caches, model):
         assert torch.equal(got, torch.stack(want))
 
 
+def reserve(pages, t, l, *args, **kw):
+    copies = torch.full((t.shape[0], 2), 77, dtype=torch.int32, device="cuda")
+    pages.reserve(t, l, *args, copies=copies, **kw)
+    return copies
+
+
 def program(rng, blocks, bs, width, rows):
     """A random table and the references of it: rows share pages as forks leave them."""
     free = list(range(blocks))
@@ -82,9 +88,9 @@ def test_a_random_program(blocks, bs, width, rows, layers, heads, d):
         status.zero_()
         if turn % 2:
             add = [min(1, width * bs - max(lens))] * len(lens)
-            got = pages.reserve(t, l, add[0], caches=caches, workspace=ws, status=status)
+            got = reserve(pages, t, l, add[0], caches=caches, workspace=ws, status=status)
         else:
-            got = pages.reserve(t, l, dev(add), caches=caches, workspace=ws, status=status)
+            got = reserve(pages, t, l, dev(add), caches=caches, workspace=ws, status=status)
         want = model.reserve(table, lens, add)
         if want is None:
             assert int(status.item()) == kvx.KVX_FLAG_NO_PAGES
@@ -119,7 +125,7 @@ def test_prompts_are_reserved_from_nothing(blocks):
     add = [0, 1, 16, 17, 9000, 333, 0, 11200, 700 * 16]
     table = [[-1] * width for _ in add]
     t = dev(table)
-    got = pages.reserve(t, dev([0] * len(add)), dev(add), max_new=width * bs, status=status)
+    got = reserve(pages, t, dev([0] * len(add)), dev(add), max_new=width * bs, status=status)
     model.reserve(table, [0] * len(add), add)
     assert (got == -1).all() and t.tolist() == table and pages.refs.tolist() == model.refs
     assert int(status.item()) == 0
@@ -142,7 +148,7 @@ def test_too_few_pages_leave_shared_rows_as_they_were():
     t, l = dev([[0, -1], [0, -1], [0, -1], [1, -1]]), dev([2, 2, 2, 4])
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     before = t.clone()
-    copies = pages.reserve(t, l, status=status)     # two copies and a new page
+    copies = reserve(pages, t, l, status=status)     # two copies and a new page
     assert int(status.item()) == kvx.KVX_FLAG_NO_PAGES and (copies == -1).all()
     assert torch.equal(t, before) and pages.refs.tolist() == [3, 1, 0]
 
@@ -152,7 +158,7 @@ def test_a_page_held_outside_the_call_stays():
     pages = kvx.Pages(dev([3, 0, 0, 0]), 4)
     t = dev([[0], [0], [0]])
     caches = caches_of(1, 4, 2, 4, 16, 5)
-    copies = pages.reserve(t[:2], dev([3, 1]), caches=caches)
+    copies = reserve(pages, t[:2], dev([3, 1]), caches=caches)
     assert copies.tolist() == [[0, 1], [0, 2]] and t.tolist() == [[1], [2], [0]]
     assert pages.refs.tolist() == [1, 1, 1, 0]
     for x in parts(caches):
@@ -160,7 +166,7 @@ def test_a_page_held_outside_the_call_stays():
     # a shared page without slots of the row is replaced, not copied
     pages = kvx.Pages(dev([2, 0, 0]), 4)
     t = dev([[0], [0]])
-    assert pages.reserve(t, dev([0, 0])).tolist() == [[-1, -1], [-1, -1]]
+    assert reserve(pages, t, dev([0, 0])).tolist() == [[-1, -1], [-1, -1]]
     assert t.tolist() == [[1], [0]] and pages.refs.tolist() == [1, 1, 0]
 
 
@@ -188,7 +194,7 @@ def test_bad_rows_and_entries_are_flagged_and_skipped():
     assert flags() == kvx.KVX_FLAG_BAD_BLOCK and (t == -1).all() and pages.refs.tolist() == [0] * 4
     # reserve: rows whose slots do not fit, or that ask for more than the bound
     t = dev([[-1, -1]] * 4)
-    got = pages.reserve(t, dev([8, -1, 0, 2]), dev([1, 1, 3, 1]), max_new=2, status=status)
+    got = reserve(pages, t, dev([8, -1, 0, 2]), dev([1, 1, 3, 1]), max_new=2, status=status)
     assert flags() == kvx.KVX_FLAG_BAD_LENGTH and (got == -1).all()
     assert t.tolist() == [[-1, -1]] * 3 + [[0, -1]] and pages.refs.tolist() == [1, 0, 0, 0]
     t = dev([[70, -5]])
