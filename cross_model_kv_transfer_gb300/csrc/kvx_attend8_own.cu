@@ -1,6 +1,3 @@
-#define OWN_MT 2
-#define OWN_W 4
-#define OWN_COLS 8
 // kvx_attend8_own.cu -- kvx_attend8_shared where a request has few rows and few slots of
 // its own: samples and beams that have been decoded for a while.
 //
@@ -24,7 +21,10 @@
 namespace {
 
 constexpr int kMostParts = 32;      // splits of a prefix
-constexpr double kMostWork = 4e8;   // multiplications of the scores
+// Multiplications of the scores up to which the prefixes go in parts.  bf16: 2.6e8 take 27 to
+// 37 us, 27 to 47 otherwise, 5.2e8 37 to 43 and 41 to 44.  fp32, which counts twice: 5.4e8
+// take 33 us, 66 otherwise, 8.4e9 251 and 202.
+constexpr double kMostWork = 5e8, kMostWorkF32 = 2e9;
 
 // What the splits leave: [part][token][Hq][d] sums, [part][token][Hq] maxima and totals,
 // relative to exp2(maximum + kRoom).
@@ -471,32 +471,25 @@ __global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constan
   }
 }
 
-template <int DP, int NT, int PARTS>
+// Eight columns a CTA: more of them (two to four tiles) took the same time or longer in all
+// of 8 beams, 64 samples and 192 rows of three tokens, as four or eight warps and one or two
+// 16-slot tiles did; this takes the fewest registers.
+template <int DP, int PARTS>
 kvx_status launch_own(const OwnParams &p, int groups, bool part, cudaStream_t s) {
-  constexpr int W = DP <= 128 ? OWN_W : 4;
-  using C = SplitCfg<DP, NT, PARTS, (DP <= 128 && NT * PARTS <= 2 ? OWN_MT : 1), W, 2>;
-  static_assert(C::kStage % 16 == 0 && W * 8 * (DP + 4) * 4 <= C::kRing, "shared memory");
+  using C = SplitCfg<DP, 1, PARTS, DP <= 128 ? 2 : 1, 4, 2>;
+  static_assert(C::kStage % 16 == 0 && C::WARPS * 8 * (DP + 4) * 4 <= C::kRing, "shared memory");
   constexpr int smem = (int)own_smem<C>();
   const auto kernel = part ? own_kernel<C, true> : own_kernel<C, false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return KVX_ERR_CUDA;
-  return launch_after(kernel, dim3((unsigned)(p.s.a.req.R * p.s.a.H), (unsigned)groups, part ? (unsigned)p.parts.count : 1u), 32 * W, smem,
-                      s, p);
+  return launch_after(kernel, dim3((unsigned)(p.s.a.req.R * p.s.a.H), (unsigned)groups, part ? (unsigned)p.parts.count : 1u),
+                      32 * C::WARPS, smem, s, p);
 }
-// Columns of a CTA: registers hold 4096 sums a warp.
-int columns_of(int64_t most, int d) { return most <= 8 ? 8 : OWN_COLS; }
 template <int PARTS>
 kvx_status launch_dim(const OwnParams &p, int most, bool part, cudaStream_t s) {
-  const int d = p.s.a.d, cols = columns_of(most, d), groups = (most + cols - 1) / cols;
-  if (d > 128) return cols == 8 ? launch_own<256, 1, PARTS>(p, groups, part, s) : launch_own<256, 2, PARTS>(p, groups, part, s);
-  if (d > 64)
-    return cols == 8    ? launch_own<128, 1, PARTS>(p, groups, part, s)
-           : cols == 16 ? launch_own<128, 2, PARTS>(p, groups, part, s)
-           : cols == 24 ? launch_own<128, 3, PARTS>(p, groups, part, s)
-                        : launch_own<128, 4, PARTS>(p, groups, part, s);
-  return cols == 8    ? launch_own<64, 1, PARTS>(p, groups, part, s)
-         : cols == 16 ? launch_own<64, 2, PARTS>(p, groups, part, s)
-         : cols == 24 ? launch_own<64, 3, PARTS>(p, groups, part, s)
-                      : launch_own<64, 4, PARTS>(p, groups, part, s);
+  const int groups = (most + 7) / 8;
+  return p.s.a.d <= 64    ? launch_own<64, PARTS>(p, groups, part, s)
+         : p.s.a.d <= 128 ? launch_own<128, PARTS>(p, groups, part, s)
+                          : launch_own<256, PARTS>(p, groups, part, s);
 }
 int64_t rows_of(const kvx_attend8_args *a) { return (int64_t)(a->q_heads / a->cache.heads) * most_new(a); }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -518,9 +511,8 @@ bool kvx_attend8_own_supports(const kvx_attend8_args *a) {
 int kvx_attend8_parts(const kvx_attend8_args *before) {
   const int64_t most = rows_of(before), rows = before->ntok * before->q_heads, d = before->cache.head_dim;
   const double work = (double)rows * before->max_len * (double)d * (before->dtype == KVX_BF16 ? 1 : 2);
-  const int cols = columns_of(most, (int)d);
-  const int64_t items = (int64_t)before->num_requests * before->cache.heads * ((most + cols - 1) / cols);
-  if (work > kMostWork || items > 65535 || before->max_len == 0) return 0;
+  const int64_t groups = (most + 7) / 8, items = (int64_t)before->num_requests * before->cache.heads * groups;
+  if (work > (before->dtype == KVX_BF16 ? kMostWork : kMostWorkF32) || groups > 65535 || items > INT32_MAX || before->max_len == 0) return 0;
   const int64_t fill = (2 * 152 + items - 1) / items, tiles = ((int64_t)before->max_len + 255) / 256;
   int64_t parts = fill < tiles ? fill : tiles;
   if (parts > kMostParts) parts = kMostParts;

@@ -115,7 +115,8 @@ __device__ __forceinline__ float sum_of(const float (&x)[E], float m) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-constexpr int kList = kMostBeams * 32 + kMostBeams;
+// A chunk's elements, those gathered before it, and the best ones before those.
+constexpr int kChunk = kMostBeams * 32, kGather = 128, kList = kGather + kChunk + kMostBeams;
 struct RowShared {
   unsigned long long top[kThreads];
   unsigned long long list[kList];
@@ -134,6 +135,7 @@ __device__ __forceinline__ void rank_list(const unsigned long long *list, int co
   for (int i = threadIdx.x; i < count; i += kThreads) {
     const unsigned long long key = list[i];
     int above = 0;
+#pragma unroll 8
     for (int j = 0; j < count; ++j) above += list[j] > key;
     if (above < n) best[above] = key;
   }
@@ -142,7 +144,7 @@ __device__ __forceinline__ void rank_list(const unsigned long long *list, int co
 // The chunk's list from ranked keys of the threads: where it overflows.  Apart from the
 // loop, from the logits read again, so that it costs that no registers.
 template <class T, int V, int E>
-__device__ __noinline__ int list_by_keys(RowShared &sh, int n, unsigned long long before, const T *row, int at, int end) {
+__device__ __noinline__ int list_by_keys(RowShared &sh, int gathered, int n, unsigned long long before, const T *row, int at, int end) {
   const int tid = threadIdx.x;
   Raw<T, V, E> raw;
   raw.load(row, at, end);
@@ -169,7 +171,7 @@ __device__ __noinline__ int list_by_keys(RowShared &sh, int n, unsigned long lon
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const unsigned long long k = key(e);
-      if (k >= bound && k > before) sh.list[atomicAdd(&sh.many, 1)] = k;
+      if (k >= bound && k > before) sh.list[gathered + atomicAdd(&sh.many, 1)] = k;
     }
   __syncthreads();
   return sh.many;
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
   static_assert(E <= 32, "the list holds 32 elements of each thread above the bound");
   __shared__ RowShared sh;
   wait_for_kernel_before();
+  let_next_kernel_start();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, rank = blockIdx.x % p.ctas, row = blockIdx.x / p.ctas;
   if (!lives(p, row)) {               // the whole cluster
     if (rank == 0 && tid == 0 && !(p.scores[row] < INFINITY)) raise(p.status, KVX_FLAG_NOT_FINITE);
@@ -200,7 +203,22 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
   constexpr bool kAhead = sizeof(T) == 2 && V > 1;
   Raw<T, V, E> next;
   if (kAhead) next.load(x_of, begin, end);
-  int turn = 0;
+  // What is not below `bound`, and whose key is above `before`, is gathered from chunk to
+  // chunk and ranked when it has become many, or at the end.
+  float bound = -INFINITY;
+  unsigned long long before = 0;
+  int turn = 0, gathered = 0;
+  const auto rank_gathered = [&] {
+    const unsigned long long old = tid < p.N ? sh.best[now][tid] : 0;
+    if (old) sh.list[gathered + tid] = old;      // they are at the front of best
+    const int held = __syncthreads_count(old != 0);
+    rank_list(sh.list, gathered + held, sh.best[now ^ 1], p.N);
+    now ^= 1;
+    gathered = 0;
+    __syncthreads();
+    before = sh.best[now][p.N - 1];
+    if (before) bound = fmaxf(bound, logit_of(before));
+  };
   for (int64_t at = begin; at < end; at += kThreads * E, turn = turn == 2 ? 0 : turn + 1) {
     float x[E];
     if (!kAhead) next.load(x_of, at, end);
@@ -225,10 +243,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
     }
     sum = sum * ex2((unit - reference()) * kLog2e) + more;
     unit = fmaxf(unit, top);
-    // the bound: what was found before, or of the first chunk what the warps agree on
-    unsigned long long before = 0;
-    float bound = -INFINITY;
-    if (at == begin) {
+    if (at == begin) {                // what the warps agree on
       uint32_t left = top > -INFINITY ? ordered(top + 0.f) : 0u, least = 0;
       for (int i = 0; i < rounds; ++i) {
         least = __reduce_max_sync(~0u, left);
@@ -240,9 +255,6 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) least = min(least, sh.warp_bound[w]);
       if (least) bound = logit_of((unsigned long long)least << 32);
-    } else {
-      before = sh.best[now][p.N - 1];
-      if (before) bound = logit_of(before);
     }
     const auto position = [&](int e) { return (int)at + (e / V * kThreads + tid) * V + e % V; };
     if (top >= bound) {
@@ -252,24 +264,18 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
           const unsigned long long key = key_of(x[e] + 0.f, position(e));   // -0 and 0 are equal
           if (key > before) {
             const int to = atomicAdd(&sh.count[turn], 1);
-            if (to < kList - kMostBeams) sh.list[to] = key;
+            if (to < kChunk) sh.list[gathered + to] = key;
           }
         }
     }
     // three counts in turn: this chunk's, the next one's, and one that a thread may still read
     if (tid == 0) sh.count[turn == 2 ? 0 : turn + 1] = 0;
     __syncthreads();
-    int found = sh.count[turn];
-    if (found) {                      // of the whole CTA
-      if (found > kList - kMostBeams) found = list_by_keys<T, V, E>(sh, p.N, before, x_of, (int)at, end);
-      const unsigned long long old = tid < p.N ? sh.best[now][tid] : 0;
-      if (old) sh.list[found + tid] = old;      // they are at the front of best
-      const int held = __syncthreads_count(old != 0);
-      rank_list(sh.list, found + held, sh.best[now ^ 1], p.N);
-      now ^= 1;
-      __syncthreads();
-    }
+    const int found = sh.count[turn];
+    gathered += found <= kChunk ? found : list_by_keys<T, V, E>(sh, gathered, p.N, before, x_of, (int)at, end);
+    if (gathered > kGather) rank_gathered();
   }
+  if (gathered) rank_gathered();
   // the CTA's sum
   float top = unit;
 #pragma unroll
@@ -334,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
     unsigned long long *to = p.keys + (int64_t)row * p.N;
     const unsigned long long key = tid < n ? sh.list[tid] : 0;
     int above = 0, some = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) {
       above += sh.list[j] > key;
       some += sh.list[j] != 0;
@@ -415,7 +422,11 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const __grid_constant__ 
     const unsigned long long s = sh.list[k];
     const int i = sh.place[k], row = b * p.K + i / p.N;
     int above = 0;
-    for (int j = 0; j < n; ++j) above += sh.list[j] > s || (sh.list[j] == s && sh.place[j] < i);
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {     // no branches: n steps of a few instructions each
+      const unsigned long long other = sh.list[j];
+      above += (int)(other > s) | ((int)(other == s) & (int)(sh.place[j] < i));
+    }
     if (above < p.N)
       put(above, p.done && p.done[row] ? p.eos : token_of(__ldcg(p.keys + (int64_t)row * p.N + i % p.N)), row,
           (float)score_of(s));

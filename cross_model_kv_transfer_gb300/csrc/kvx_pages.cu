@@ -50,6 +50,7 @@ struct CopyParams {
 // their way before the first store.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
   wait_for_kernel_before();
+  let_next_kernel_start();
   for (int x = 0; x < p.tables.count; ++x) {
     int32_t *table = p.tables.table[x];
     for (int64_t i = blockIdx.x * (int64_t)kCopyThreads + threadIdx.x; i < p.tables.entries[x]; i += (int64_t)gridDim.x * kCopyThreads) {
@@ -175,6 +176,7 @@ __device__ __forceinline__ int held_of(const ForkParams &p, int r, bool tell) {
 // holds: a page that its length covers gains its children and loses the row itself.
 __global__ void __launch_bounds__(128) fork_kernel(const __grid_constant__ ForkParams p) {
   wait_for_kernel_before();
+  let_next_kernel_start();
   const int tid = threadIdx.x;
   if ((int)blockIdx.x < p.N) {
     const int n = blockIdx.x, r = p.parents[n];
@@ -209,6 +211,7 @@ __global__ void __launch_bounds__(128) fork_kernel(const __grid_constant__ ForkP
 
 __global__ void __launch_bounds__(256) free_kernel(int32_t *refs, int64_t num_blocks, int32_t *table, int64_t entries, uint32_t *status) {
   wait_for_kernel_before();
+  let_next_kernel_start();
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < entries; i += (int64_t)gridDim.x * blockDim.x) {
     const int page = table[i];
     if (page >= 0 && page < num_blocks) atomicSub(refs + page, 1);
@@ -328,6 +331,7 @@ template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const __grid_constant__ ReserveParams p) {
   __shared__ int needs_of[kWarps];
   wait_for_kernel_before();
+  let_next_kernel_start();
   const int lane = threadIdx.x % 32, in = threadIdx.x / 32, warp = blockIdx.x * kWarps + in;
   int32_t *free_of = p.work, *list = p.work + kListAt;
   const bool leads = blockIdx.x == 0;
@@ -455,6 +459,7 @@ struct CompactParams {
 template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_constant__ CompactParams p) {
   wait_for_kernel_before();
+  let_next_kernel_start();
   const int lane = threadIdx.x % 32, warp = blockIdx.x * kWarps + threadIdx.x / 32;
   int32_t *held_of = p.work, *holes_of = p.work + kSums, *movers_of = p.work + 2 * kSums, *pairs = p.work + kListAt;
   const Range pages = share_of<CTAS>(p.num_blocks, 32);
