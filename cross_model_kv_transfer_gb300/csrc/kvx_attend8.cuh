@@ -8,7 +8,27 @@
 
 #include "kvx_cache8.cuh"
 
+// Compiled twice: for kvx_attend8, and (KVX_ATTEND_SHARED) for the passes of
+// kvx_attend8_shared, so that what those need costs the others nothing.
+#ifndef KVX_ATTEND_SHARED
+#define KVX_ATTEND_SHARED 0
+#endif
+
 namespace kvx8 {
+
+// Requests that share prefixes, in the passes of kvx_attend8_shared.  Over the prefixes
+// (`all`): a query sees every slot, and request r of the pass is the queries of the requests
+// of[r] .. of[r + 1] - 1 of `inner`, or of all tokens (`whole`).  Over the requests' own
+// slots: `before` and `before_stats` are what the first pass left, [ntok][Hq][d] and
+// [ntok][Hq], to join with, and the `count` groups `of` are checked again, at most `most`
+// tokens each, so that a bad table stops both passes.
+struct Sharing {
+  const int32_t *of;
+  int inner, count, whole, all;
+  int64_t most;
+  const float *before;
+  const float2 *before_stats;
+};
 
 struct AttendParams {
   const uint8_t *k, *v;
@@ -23,17 +43,10 @@ struct AttendParams {
   float2 *stats;
   uint32_t *status;
   kvx8::Requests req;
-  // Requests that share a prefix.  The pass over the prefixes: `all`, a query sees every
-  // slot, and `req` is the groups.  The pass over the requests' own slots: `before` and
-  // `before_stats` are what the first left, [ntok][Hq][d] and [ntok][Hq], to join with,
-  // and `groups` is checked again, so that a bad table stops both passes.
-  kvx8::Groups groups;
-  const float *before;
-  const float2 *before_stats;
+  Sharing share;
   int64_t wstride;
   int num_blocks, H, Hq, G, d, bs, max_blocks, max_len, max_new;
   int bf16;                    // the type of out
-  int all;
   uint32_t bs_mul, bs_shift;   // j / bs = j * bs_mul >> bs_shift for j < 2^31
   float c;   // scale * log2(e): scores are kept in base 2
 };
@@ -43,6 +56,8 @@ struct AttendParams {
 namespace {
 
 using kvx8::AttendParams;
+
+constexpr bool kShared = KVX_ATTEND_SHARED;
 
 // A workspace begins with the split form's counters, which are zero between calls: where
 // they lie and how many there are depends on no call's sizes, and no form uses these
@@ -69,18 +84,47 @@ __device__ __forceinline__ int page_of(const AttendParams &p, int r, uint32_t bl
   const int page = block < (uint32_t)p.max_blocks ? __ldg(p.table + (int64_t)r * p.max_blocks + block) : -1;
   return page < p.num_blocks ? page : -1;
 }
-// The last slot that query i of a request sees is first_limit + i * a query's step.
-__device__ __forceinline__ int first_limit(const AttendParams &p, int len, int fresh) {
-  return p.all ? len - 1 : len - fresh;
+// A request's first token, and behind the last request the end.  An entry of the groups that
+// is no request gives -1, which no good table holds.
+__device__ __forceinline__ int64_t begin_of(const AttendParams &p, int r) {
+  if (kShared && p.share.all) {
+    if (p.share.whole) return r ? p.req.ntok : 0;
+    r = p.share.of[r];
+    if (r < 0 || r > p.share.inner) return -1;
+  }
+  return p.req.begin(r);
 }
-__device__ __forceinline__ int limit_step(const AttendParams &p) { return p.all ? 0 : 1; }
+// The last slot that query i of a request sees is first_limit + i * limit_step.
+__device__ __forceinline__ int first_limit(const AttendParams &p, int len, int fresh) {
+  return kShared && p.share.all ? len - 1 : len - fresh;
+}
+__device__ __forceinline__ int limit_step(const AttendParams &p) { return kShared && p.share.all ? 0 : 1; }
+// Groups of requests start at 0, never decrease, end at the last request and have at most
+// `most` tokens each: this thread's share of the check, in the pass over own slots.
+__device__ __forceinline__ bool groups_ok(const AttendParams &p, int first, int stride) {
+  bool good = true;
+  if (kShared && !p.share.all && p.share.of)
+    for (int i = first; i < p.share.count; i += stride) {
+      const int a = p.share.of[i], b = p.share.of[i + 1];
+      good = good && a >= 0 && b >= a && b <= p.req.R && (i > 0 || a == 0) && (i + 1 < p.share.count || b == p.req.R);
+      if (good) good = p.req.begin(b) - p.req.begin(a) <= p.share.most;
+    }
+  return good;
+}
 __device__ __forceinline__ bool requests_ok(const AttendParams &p) {
+  if (kShared) {
+    bool good = groups_ok(p, threadIdx.x, blockDim.x);
+    for (int r = threadIdx.x; r < p.req.R; r += blockDim.x) {
+      const int64_t from = begin_of(p, r), to = begin_of(p, r + 1);
+      good = good && to >= from && to - from <= p.max_new && (r > 0 || from == 0) && (r + 1 < p.req.R || to == p.req.ntok);
+    }
+    return __syncthreads_and(good);
+  }
   bool good = p.req.ok();
-  if (good && p.groups.of) good = __syncthreads_and(p.groups.ok(p.req, threadIdx.x, blockDim.x));
-  if (p.req.table()) {
+  if (p.req.cu) {
     bool few = true;
     for (int r = threadIdx.x; good && r < p.req.R; r += blockDim.x)
-      few = few && p.req.begin(r + 1) - p.req.begin(r) <= p.max_new;
+      few = few && p.req.cu[r + 1] - p.req.cu[r] <= p.max_new;
     good = __syncthreads_and(good && few);
   }
   return good;
@@ -97,7 +141,7 @@ struct Joined {
   float2 lse;
 };
 __device__ __forceinline__ Joined join_before(const AttendParams &p, int64_t g, int hq, float m, float shift, float l) {
-  const float2 b = __ldcg(p.before_stats + g * p.Hq + hq);
+  const float2 b = __ldcg(p.share.before_stats + g * p.Hq + hq);
   if (l == 0.f) return {0.f, b.y < INFINITY ? 1.f : 0.f, b};
   const float rest = shift + log2f(l);
   if (b.y == INFINITY) return {1.f, 0.f, make_float2(m, rest)};
@@ -107,7 +151,7 @@ __device__ __forceinline__ Joined join_before(const AttendParams &p, int64_t g, 
 }
 // The log-sum-exp of a row whose sum l is relative to exp2(m + shift).
 __device__ __forceinline__ void store_lse(const AttendParams &p, int64_t g, int hq, float m, float shift, float l) {
-  if (p.before) {
+  if (kShared && p.share.before) {
     const float2 both = join_before(p, g, hq, m, shift, l).lse;
     if (p.lse) p.lse[g * p.Hq + hq] = both.y == INFINITY ? -INFINITY : (both.x + both.y) * kLn2;
     return;
@@ -125,22 +169,20 @@ __device__ __forceinline__ void store_out(const AttendParams &p, int64_t g, int 
                                           float shift, float l) {
   const float inv = l != 0.f ? 1.f / l : 0.f;
   const int64_t to = g * p.ot + hq * p.oh + d;
-  o.x *= inv;
-  o.y *= inv;
-  if (p.before) {
+  float2 y = make_float2(o.x * inv, o.y * inv);
+  if (kShared && p.share.before) {
     const Joined j = join_before(p, g, hq, m, shift, l);
-    const float2 b = __ldcg(reinterpret_cast<const float2 *>(p.before + (g * p.Hq + hq) * p.d + d));
-    o.x = o.x * j.own + b.x * j.before;
-    o.y = o.y * j.own + b.y * j.before;
+    const float2 b = __ldcg(reinterpret_cast<const float2 *>(p.share.before + (g * p.Hq + hq) * p.d + d));
+    y = make_float2(y.x * j.own + b.x * j.before, y.y * j.own + b.y * j.before);
   }
   if (p.bf16) {
     __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + to;
-    out[0] = __float2bfloat16_rn(o.x);
-    out[1] = __float2bfloat16_rn(o.y);
+    out[0] = __float2bfloat16_rn(y.x);
+    out[1] = __float2bfloat16_rn(y.y);
   } else {
     float *out = reinterpret_cast<float *>(p.out) + to;
-    out[0] = o.x;
-    out[1] = o.y;
+    out[0] = y.x;
+    out[1] = y.y;
   }
   if (d == 0) store_lse(p, g, hq, m, shift, l);
 }
@@ -165,14 +207,17 @@ __device__ __forceinline__ float finite_or_0(float m) { return m > -INFINITY ? m
 }  // namespace
 
 // kvx_attend8_tc.cu: bf16 queries and head_dim up to 128 over blocks of whole 8-slot
-// groups.
+// groups; kvx_attend8_split.cu: all others.
 bool kvx_attend8_tc_supports(const kvx_attend8_args *a);
 // Of a workspace: the bytes that the call needs, and with those in which calls of at most
 // its sizes can keep scores.
 size_t kvx_attend8_tc_least_bytes(const kvx_attend8_args *a);
 size_t kvx_attend8_tc_workspace_bytes(const kvx_attend8_args *a);
-kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *a, const kvx8::AttendParams &p, char *workspace,
-                                 cudaStream_t s);
+size_t kvx_attend8_split_least_bytes(const kvx_attend8_args *a);
+size_t kvx_attend8_split_workspace_bytes(const kvx_attend8_args *a);
+// The launches, for kvx_attend8 and for the passes of kvx_attend8_shared.
+typedef kvx_status kvx_attend8_launch(const kvx_attend8_args *a, const kvx8::AttendParams &p, char *workspace, cudaStream_t s);
+kvx_attend8_launch kvx_attend8_tc_launch, kvx_attend8_tc_launch_shared, kvx_attend8_split_launch, kvx_attend8_split_launch_shared;
 
 // kvx_attend8_own.cu: the own slots of requests that share prefixes, few rows and not too
 // many slots; and their prefixes, where they are not much work, in a number of parts.

@@ -16,6 +16,7 @@
 // prefix, KV head, group of up to 32 columns and split of the slots leaves its maxima, totals and
 // sums, and the items join all splits' with their own.  Two launches then, and no
 // kernel that joins.
+#define KVX_ATTEND_SHARED 1
 #include "kvx_attend8_mma.cuh"
 
 namespace {
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constan
     page2 = look(warp + 2 * W);
   }
   const int len = len_of(a, r);
-  const int64_t beg = a.req.begin(r), end = a.req.begin(r + 1);
+  const int64_t beg = begin_of(a, r), end = begin_of(a, r + 1);
   const int all = (len + KW - 1) / KW;
   // the CTA's tiles
   const int begin = PART ? (int)((int64_t)all * blockIdx.z / parts.count) : 0;
@@ -242,10 +243,10 @@ __global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constan
   const auto table_ok = [&]() {
     bool good = true;
     for (int i = tid; i < a.req.R; i += 32 * W) {
-      const int64_t from = a.req.begin(i), to = a.req.begin(i + 1);
+      const int64_t from = begin_of(a, i), to = begin_of(a, i + 1);
       good = good && to >= from && to - from <= a.max_new && (i > 0 || from == 0) && (i + 1 < a.req.R || to == a.req.ntok);
     }
-    return good && (!a.groups.of || a.groups.ok(a.req, tid, 32 * W));
+    return good && groups_ok(a, tid, 32 * W);
   };
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && !__syncthreads_and(table_ok())) {
     if (tid == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constan
       for (int k = 0; k < kQuads; ++k) {
         const int i = tid + k * 32 * W, d = i % (DP / 4) * 4, col = col0 + 8 * n + i / (DP / 4);
         before_row[n][k] = col < cols && d < a.d ? __ldcg(reinterpret_cast<const float4 *>(
-                                                       a.before + ((beg + col / a.G) * a.Hq + h * a.G + col % a.G) * a.d + d))
+                                                       a.share.before + ((beg + col / a.G) * a.Hq + h * a.G + col % a.G) * a.d + d))
                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
       }
   }

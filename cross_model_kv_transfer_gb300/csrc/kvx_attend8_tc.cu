@@ -181,7 +181,7 @@ struct Narrow {
 template <class G>
 __device__ __forceinline__ int steps_of(const AttendParams &a, int len, int fresh, int group) {
   const int64_t end = ((int64_t)(group + 1) * G::ROWS + a.G - 1) / a.G;   // its tokens end here
-  const int64_t seen = a.all ? len : len - fresh + (end < fresh ? end : fresh);
+  const int64_t seen = kShared && a.share.all ? len : len - fresh + (end < fresh ? end : fresh);
   return seen <= 0 ? 1 : (int)((seen + G::SLOTS - 1) / G::SLOTS);
 }
 template <class G>
@@ -200,8 +200,8 @@ __device__ __forceinline__ void next_item(const AttendParams &a, TcWalk &w) {
       do {
         if (++w.r >= a.req.R) return;
         w.len = len_of(a, w.r);
-        w.beg = a.req.begin(w.r);
-        w.fresh = (int)(a.req.begin(w.r + 1) - w.beg);
+        w.beg = begin_of(a, w.r);
+        w.fresh = (int)(begin_of(a, w.r + 1) - w.beg);
         w.groups = groups_of<G>(a, w.fresh);
       } while (w.groups == 0);
     }
@@ -235,8 +235,8 @@ __device__ __forceinline__ Requests32 look(const AttendParams &a, int r0, bool t
   bool good = true;
   if (r < a.req.R) {
     q.len = len_of(a, r);
-    q.beg = a.req.begin(r);
-    const int64_t end = a.req.begin(r + 1);
+    q.beg = begin_of(a, r);
+    const int64_t end = begin_of(a, r + 1);
     q.fresh = (int)(end - q.beg);
     good = end >= q.beg && end - q.beg <= a.max_new && (r > 0 || q.beg == 0) && (r + 1 < a.req.R || end == a.req.ntok);
     if (!good) q.fresh = 0;
@@ -262,7 +262,7 @@ __device__ __forceinline__ Requests32 look(const AttendParams &a, int r0, bool t
 template <class G>
 __device__ void find_share(const AttendParams &a, int cta, int ctas, bool tell, Share &s) {
   const int lane = threadIdx.x % 32;
-  s.good = !a.groups.of || __all_sync(~0u, a.groups.ok(a.req, lane, 32));
+  s.good = !kShared || __all_sync(~0u, groups_ok(a, lane, 32));
   s.T = 0;
   s.N = 0;
   s.last = -1;
@@ -921,7 +921,9 @@ __global__ void __launch_bounds__(256, 3) join_kernel(const __grid_constant__ Tc
   w.h = x.h;
   w.group = x.group;
   w.beg = x.beg;
-  join_rows<G, 1>(p, w, x.c0, x.ctas, blockIdx.y * 8 + threadIdx.x / 32, gridDim.y * 8, x.rows);
+  // after a prompt four rows a warp at a time; of shared prefixes, whose few items are in many
+  // parts, one (64 samples of four prompts 13 us, so 8)
+  join_rows<G, kShared ? 1 : 4>(p, w, x.c0, x.ctas, blockIdx.y * 8 + threadIdx.x / 32, gridDim.y * 8, x.rows);
 }
 // The same with a block for a row, whose warps share the parts: few rows, many parts.
 template <class G>
@@ -1017,9 +1019,10 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
   const bool direct = WIDE && whole;
   if (warp_live) {
     const float inv = direct ? (l != 0.f ? back / l : 0.f) : back;
-    const bool full = direct && !a.bf16;      // the result in fp32
+    const bool full = kShared && direct && !a.bf16;      // the result in fp32
+    const bool join = kShared && direct && a.share.before;
     __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + tok * a.ot + hq * a.oh;
-    if (WIDE && (!direct || full || (p.vec_out && !a.before))) {
+    if (WIDE && (!direct || full || (p.vec_out && !join))) {
       // Through shared memory, so that rows go out whole: a lane's row is written
       // there 16 bytes at a time, and half a warp stores a row's 256.  It lies where
       // the warp's own query rows were, whose products are over.
@@ -1069,15 +1072,15 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
     } else {
       // rows of the thread's own; what came before them is joined here
       Joined j = {1.f, 0.f, {}};
-      if (live && direct && a.before) j = join_before(a, tok, hq, m, shift, l);
+      if (live && join) j = join_before(a, tok, hq, m, shift, l);
       const float own = inv * j.own;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         tc_ld32(o_col + 32 * c, o);
         tc_wait_ld32(o);
-        if (live && direct && a.before) {
-          const float *b = a.before + (tok * a.Hq + hq) * a.d + 32 * c;
+        if (live && join) {
+          const float *b = a.share.before + (tok * a.Hq + hq) * a.d + 32 * c;
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             if (32 * c + e < a.d) {
@@ -1097,7 +1100,7 @@ __device__ __noinline__ bool finish_item(const TcParams &p, TcShared *sh, const 
         } else if (live) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (32 * c + e < a.d) out[32 * c + e] = __float2bfloat16_rn(__uint_as_float(o[e]) * (a.before ? 1.f : inv));
+            if (32 * c + e < a.d) out[32 * c + e] = __float2bfloat16_rn(__uint_as_float(o[e]) * (join ? 1.f : inv));
         }
         __syncwarp();   // together to the next load
       }
@@ -1437,6 +1440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
+#if !KVX_ATTEND_SHARED
 // weights[r][h][j] += sum over the rows of exp2(score - lse): narrow calls leave
 // their scores, [rows][score_ld].
 __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_constant__ TcParams p) {
@@ -1445,8 +1449,8 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
   __shared__ float lse1[64];     // of near rows as one number
   const bool good = requests_ok(a);
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
-  const int64_t beg = a.req.begin(r);
-  const int rows = (int)(a.req.begin(r + 1) - beg) * a.G;
+  const int64_t beg = begin_of(a, r);
+  const int rows = (int)(begin_of(a, r + 1) - beg) * a.G;
   wait_for_kernel_before();
   if (!good) return;
   bool far = false;
@@ -1475,6 +1479,7 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
   }
   a.weights[((int64_t)r * a.H + h) * a.wstride + j] += sum;
 }
+#endif
 
 // --- few columns --------------------------------------------------------------------
 // At most 16 (query, head of the group) pairs: one token of a group of heads, or a
@@ -2046,6 +2051,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
 }
 
+#if !KVX_ATTEND_SHARED
 // --- accumulated weights where the scores were not kept ----------------------------
 // weights[r][h][j] += sum over the rows that see slot j of exp2(score - lse).
 // The scores are formed again, transposed (S^T = K Q^T, slots in the lanes), so
@@ -2133,8 +2139,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   const WaiterT<WtShared> W{sh, a.status};
-  const int64_t beg = a.req.begin(r);
-  const int fresh = good ? (int)(a.req.begin(r + 1) - beg) : 0, rows = fresh * a.G;
+  const int64_t beg = begin_of(a, r);
+  const int fresh = good ? (int)(begin_of(a, r + 1) - beg) : 0, rows = fresh * a.G;
   // rows that see the CTA's first slot: from the first query whose limit reaches it
   const int row0 = max(0, t0 * kTile - (len - fresh)) * a.G / (2 * kTile) * (2 * kTile);
   const int chunks = tiles > 0 && row0 < rows ? (rows - row0 + 2 * kTile - 1) / (2 * kTile) : 0;
@@ -2308,9 +2314,9 @@ __global__ void __launch_bounds__(256) weights_of_columns_kernel(const __grid_co
   const AttendParams &a = p.a;
   __shared__ float2 lse2[16];
   const int r = blockIdx.z, h = blockIdx.y, len = len_of(a, r);
-  const int64_t beg = a.req.begin(r), j0 = (int64_t)blockIdx.x * (256 * kSlotsOfThread) + threadIdx.x;
+  const int64_t beg = begin_of(a, r), j0 = (int64_t)blockIdx.x * (256 * kSlotsOfThread) + threadIdx.x;
   const bool good = requests_ok(a);
-  const int rows = good ? (int)(a.req.begin(r + 1) - beg) * a.G : 0;
+  const int rows = good ? (int)(begin_of(a, r + 1) - beg) * a.G : 0;
   float *to = a.weights + ((int64_t)r * a.H + h) * a.wstride + j0;
   float before[kSlotsOfThread], sum[kSlotsOfThread] = {};
 #pragma unroll
@@ -2342,6 +2348,7 @@ __global__ void __launch_bounds__(256) weights_of_columns_kernel(const __grid_co
   for (int k = 0; k < kSlotsOfThread; ++k)
     if (j0 + 256 * k < len) to[256 * k] = before[k] + sum[k];
 }
+#endif
 
 // --- host ------------------------------------------------------------------------
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -2402,11 +2409,13 @@ kvx_status launch(K kernel, int threads, size_t smem, const TcParams &p, const C
   kernel<<<p.grid, threads, smem, s>>>(p, mk, mv);
   if (const kvx_status st = launched()) return st;
   if constexpr (G::ROWS <= 16) return launch_after(join_row_kernel<G>, dim3(p.grid - 1, p.slot_rows), 256, 0, s, p);
-  return launch_after(join_kernel<G>, dim3(p.grid - 1, (p.slot_rows + 7) / 8), 256, 0, s, p);
+  const int at_once = kShared ? 8 : 32;
+  return launch_after(join_kernel<G>, dim3(p.grid - 1, (p.slot_rows + at_once - 1) / at_once), 256, 0, s, p);
 }
 
 }  // namespace
 
+#if !KVX_ATTEND_SHARED
 bool kvx_attend8_tc_supports(const kvx_attend8_args *a) {
   const kvx_cache8 &c = a->cache;
   return a->dtype == KVX_BF16 && c.head_dim <= kD && c.block_size % 8 == 0 &&
@@ -2415,8 +2424,13 @@ bool kvx_attend8_tc_supports(const kvx_attend8_args *a) {
 
 size_t kvx_attend8_tc_least_bytes(const kvx_attend8_args *a) { return tc_shape(a).scores; }
 size_t kvx_attend8_tc_workspace_bytes(const kvx_attend8_args *a) { return tc_shape(a).bytes; }
+#endif
 
+#if KVX_ATTEND_SHARED
+kvx_status kvx_attend8_tc_launch_shared(const kvx_attend8_args *args, const kvx8::AttendParams &a, char *ws, cudaStream_t s) {
+#else
 kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::AttendParams &a, char *ws, cudaStream_t s) {
+#endif
   const TcShape sh = tc_shape(args);
   CUtensorMap mk, mv;
   if (!encode(&mk, args->cache, a.k, sh.box) || !encode(&mv, args->cache, a.v, sh.box)) return KVX_ERR_CUDA;
@@ -2438,6 +2452,9 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
       : !sh.columns ? launch<Narrow>(attend_tc_kernel<false>, kThreads, smem_bytes<false>(), p, mk, mv, s)
       : sh.slot_rows == 8 ? launch<Columns<8>>(columns_kernel<8>, kColThreads, kColSmem, p, mk, mv, s)
                           : launch<Columns<16>>(columns_kernel<16>, kColThreads, kColSmem, p, mk, mv, s);
+#if KVX_ATTEND_SHARED
+  return st;
+#else
   if (st != KVX_OK || !a.weights || a.max_len == 0) return st;
   if (!sh.spool) {
     // as few slot tiles a CTA as lets all run at once, within what it has room for
@@ -2451,4 +2468,5 @@ kvx_status kvx_attend8_tc_launch(const kvx_attend8_args *args, const kvx8::Atten
   const auto grid = [&](int slots) { return dim3((a.max_len + slots - 1) / slots, a.H, a.req.R); };
   if (sh.columns) return launch_after(weights_of_columns_kernel, grid(256 * kSlotsOfThread), 256, 0, s, p);
   return launch_after(weights_of_rows_kernel, grid(256), 256, sh.slot_rows * sizeof(float2), s, p);
+#endif
 }

@@ -12,51 +12,19 @@
 
 namespace kvx8 {
 
-// Requests of a packed batch: cu[0 .. R] (or one token each without it).  As groups of
-// such requests, group r holds requests outer[r] .. outer[r + 1] - 1 of `inner`, or
-// `whole`: the only one holds all tokens.
+// Requests of a packed batch: cu[0 .. R] (or one token each without it).
 struct Requests {
   const int32_t *cu;
   int R;
   int64_t ntok;
-  const int32_t *outer;
-  int inner;
-  int whole;
-  __device__ bool table() const { return cu || outer || whole; }
-  // An entry of `outer` that is no request gives -1, which no good table holds.
-  __device__ int64_t begin(int r) const {
-    if (whole) return r ? ntok : 0;
-    if (outer) {
-      r = outer[r];
-      if (r < 0 || r > inner) return -1;
-    }
-    return cu ? (int64_t)cu[r] : r;
-  }
+  __device__ int64_t begin(int r) const { return cu ? (int64_t)cu[r] : r; }
   // Starts at 0, never decreases, ends at ntok; every thread of the CTA calls it.
   __device__ bool ok() const {
     bool good = true;
-    if (table()) {
-      for (int r = threadIdx.x; r < R; r += blockDim.x) good = good && begin(r + 1) >= begin(r);
-      if (threadIdx.x == 0) good = good && begin(0) == 0 && begin(R) == ntok;
+    if (cu) {
+      for (int r = threadIdx.x; r < R; r += blockDim.x) good = good && cu[r + 1] >= cu[r];
+      if (threadIdx.x == 0) good = good && cu[0] == 0 && (int64_t)cu[R] == ntok;
       good = __syncthreads_and(good);
-    }
-    return good;
-  }
-};
-
-// Groups of requests, of[0 .. count]: they start at 0, never decrease, end at the last
-// request and have at most `most` tokens each.  NULL: no groups.
-struct Groups {
-  const int32_t *of;
-  int count;
-  int64_t most;
-  // This thread's share of the check, of a good request table.
-  __device__ bool ok(const Requests &req, int first, int stride) const {
-    bool good = true;
-    for (int i = first; i < count; i += stride) {
-      const int a = of[i], b = of[i + 1];
-      good = good && a >= 0 && b >= a && b <= req.R && (i > 0 || a == 0) && (i + 1 < count || b == req.R);
-      if (good) good = req.begin(b) - req.begin(a) <= most;
     }
     return good;
   }
