@@ -15,8 +15,8 @@
 // The maximum that is subtracted follows the running one lazily: P holds up to
 // 2^8 times what it would with the true one before the sums are scaled down.
 //
-// Roles: warps 0-3 and 4-7 two softmax groups, warps 8-11 convert V, warp 12
-// loads (block lookups, scales, TMA), warps 13 and 14 issue the groups' MMAs.  WIDE: the groups
+// Roles: warps 0-3 and 4-7 two softmax groups, warps 8-11 convert V, warps 12 and 15
+// load keys and values (block lookups, scales, TMA), warps 13 and 14 issue the groups' MMAs.  WIDE: the groups
 // take the two 128-row halves of 256 rows, over the same slot tiles.  Narrow
 // (at most 64 rows): they take the even and the odd slot tiles of the same
 // rows, so that one tile's softmax overlaps the other's products.
@@ -59,7 +59,7 @@ constexpr int kTileBytes = kTile * kD;
 constexpr int kMaxKStages = 4, kVStages = 2, kWStages = 2;
 template <bool WIDE>
 constexpr int kStagesOf = WIDE ? 3 : 4;
-constexpr int kLoadWarp = 12, kMmaWarp = 13, kThreads = 16 * 32;
+constexpr int kLoadWarp = 12, kMmaWarp = 13, kValueWarp = 15, kThreads = 16 * 32;
 // registers a thread: 8 softmax warps, 4 that convert, 4 others; together the
 // launch's 512 x 128
 constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kOtherRegs = 64;
@@ -667,34 +667,42 @@ __device__ __noinline__ float query_factor(const AttendParams &a, bool vec, cons
 // time where a CTA does one or two items and runs this code cold, sixteen where it
 // does many (wide calls).  Returns the lane's factor on its row's
 // scores (its sign is in the parts).
+// The 16 bytes of a row that a lane of put_queries takes.
+__device__ __forceinline__ uint4 query_piece(bool vec, const __nv_bfloat16 *from) {
+  if (vec) return __ldg(reinterpret_cast<const uint4 *>(from));
+  const unsigned short *h = reinterpret_cast<const unsigned short *>(from);
+  uint32_t v[4] = {};
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t u = (uint32_t)h[e] << (16 * (e & 1));
+    v[0] |= e / 2 == 0 ? u : 0u;
+    v[1] |= e / 2 == 1 ? u : 0u;
+    v[2] |= e / 2 == 2 ? u : 0u;
+    v[3] |= e / 2 == 3 ? u : 0u;
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
 template <int N>
 __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
                                           unsigned char *tile, int first, int part, int count) {
   const int lane = threadIdx.x % 32, c = lane % 16;      // 8 dimensions
   float mine = 0.f;
+  const auto ask = [&](int pair) {
+    const int row = (2 * pair + lane / 16) & 31;
+    const uint64_t p = __shfl_sync(~0u, (uint64_t)src, row);
+    const bool there = __shfl_sync(~0u, (int)live, row) && 8 * c < a.d && 2 * pair < 32;
+    return there ? query_piece(vec, reinterpret_cast<const __nv_bfloat16 *>(p) + 8 * c) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 next[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) next[i] = ask(i);
 #pragma unroll 1
   for (int i0 = 0; 2 * i0 < count; i0 += N) {
     uint4 x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int row = 2 * (i0 + i) + lane / 16;
-      const uint64_t p = __shfl_sync(~0u, (uint64_t)src, row);
-      const bool there = __shfl_sync(~0u, (int)live, row) && 8 * c < a.d;
-      const uint4 *from = reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + 8 * c);
-      x[i] = there && vec ? __ldg(from) : make_uint4(0, 0, 0, 0);
-      if (!vec && there) {
-        const unsigned short *h = reinterpret_cast<const unsigned short *>(from);
-        uint32_t v[4] = {};
-#pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t u = (uint32_t)h[e] << (16 * (e & 1));
-          v[0] |= e / 2 == 0 ? u : 0u;
-          v[1] |= e / 2 == 1 ? u : 0u;
-          v[2] |= e / 2 == 2 ? u : 0u;
-          v[3] |= e / 2 == 3 ? u : 0u;
-        }
-        x[i] = make_uint4(v[0], v[1], v[2], v[3]);
-      }
+      x[i] = next[i];
+      next[i] = ask(i0 + N + i);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -709,7 +717,8 @@ __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
       const float unit = pow2_scale(top);   // top <= 448 unit
-      const float up = a.c != 0.f ? copysignf(1.f / unit, a.c) : 0.f;
+      // 1 / unit, a power of two
+      const float up = a.c != 0.f ? copysignf(__uint_as_float(0x7f000000u - __float_as_uint(unit)), a.c) : 0.f;
       const float other = __shfl_xor_sync(~0u, top, 16);
       if (lane / 2 == i0 + i) mine = lane % 2 == lane / 16 ? top : other;
       uint32_t p1[2], p2[2];
@@ -1217,7 +1226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
       float m = -INFINITY, shift = 0.f, l = 0.f, cs;
       if (WIDE || i == 0) {
-        cs = put_queries<WIDE ? 8 : 4>(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes, 32);
+        cs = put_queries<WIDE && !kShared ? 4 : 2>(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes, 32);
         fence_async_proxy();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[i]));
@@ -1318,73 +1327,107 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   cv_done:;
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kLoadWarp || warp == kValueWarp) {
     fewer_registers<kOtherRegs>();
     // ----------------------------------------------------------------------
-    // block lookups, scales and TMA: lane l looks up slots 4l .. 4l + 3
+    // Block lookups, scales and TMA, lane l for slots 4l .. 4l + 3: a warp for the keys and
+    // one for the values, so that neither's full stages hold up the other.  A tile's blocks
+    // are looked up two tiles ahead, their scales one: nothing waits for them.
     // ----------------------------------------------------------------------
-    uint32_t n = 0;
-    for (; w.base + G_::SETUP < last; next_item<G_>(a, w)) {
-      const int count = steps_here<G_>(w, last);
-      int j = w.step * G_::SLOTS + 4 * lane;
-      for (int k = 0; k < count * (WIDE ? 1 : 2); ++k, ++n, j += kTile) {
-        const int ks = n % kKStages, vs = n % kVStages;
-        int page = -1;
-        uint32_t off = 0;
-        if (j < w.len) {
-          const uint32_t block = block_of(a, j);
-          off = j - block * a.bs;
-          page = page_of(a, w.r, block);
-          if (page < 0) raise(a.status, KVX_FLAG_BAD_BLOCK);
-        }
-        const uint32_t sb = page < 0 ? 0u : (uint32_t)page * a.H + w.h;
-        const int row = (int)(sb * a.bs + off);
-        const float kscale = page >= 0 ? __ldg(a.ks + sb) : 0.f, vscale = page >= 0 ? __ldg(a.vs + sb) : 0.f;
-        const unsigned mask = __ballot_sync(~0u, page >= 0);
-        // the tile's largest value scale, rounded up to a power of two 2^e.  Not below
-        // 2^-96: such values vanish beside any other.  Not above 2^126: ex2 gives 0 for
-        // 2^-127, and codes whose values are finite leave f16 room for the rest.
-        const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(vscale));
-        const int e = min(max((int)(most >> 23) + ((most & 0x7fffff) != 0), 127 - 96), 127 + 126);
-        const int per = p.box / 4, boxes = kTile / p.box;     // lanes a box, boxes
-        const int from = __shfl_sync(~0u, row, lane < boxes ? lane * per : 0);
-        const bool there = lane < boxes && (mask >> (lane * per) & 1);
-        const uint32_t bytes = __popc(__ballot_sync(~0u, there)) * (uint32_t)p.box * kD;
-        if (!W.warp_wait(&sh->k_empty[ks], (n / kKStages & 1) ^ 1)) goto ld_done;
-        sh->ks[ks][lane] = kscale;
+    const bool keys = warp == kLoadWarp;
+    struct Tile {
+      int page, off;
+      bool asked;
+    };
+    int k = 0, end = 0, j = 0;      // tile of the item, tiles of the item in this CTA, the lane's first slot
+    bool more = w.base + G_::SETUP < last;
+    const auto enter = [&]() {
+      k = 0;
+      end = steps_here<G_>(w, last) * (WIDE ? 1 : 2);
+      j = w.step * G_::SLOTS + 4 * lane;
+    };
+    if (more) enter();
+    const auto next = [&](Tile &x, int &h) {
+      x.asked = more;
+      x.page = -1;
+      x.off = 0;
+      h = w.h;
+      if (!more) return;
+      if (j < w.len) {
+        const uint32_t block = block_of(a, j);
+        x.off = j - block * a.bs;
+        x.page = page_of(a, w.r, block);
+        if (x.page < 0 && keys) raise(a.status, KVX_FLAG_BAD_BLOCK);
+      }
+      j += kTile;
+      if (++k == end) {
+        next_item<G_>(a, w);
+        more = w.base + G_::SETUP < last;
+        if (more) enter();
+      }
+    };
+    const auto scales = [&](const Tile &x, int h, float &f, float &g) {
+      f = g = 0.f;
+      if (x.page < 0) return;
+      const uint32_t sb = (uint32_t)x.page * a.H + h;
+      if (keys) f = __ldg(a.ks + sb);
+      g = __ldg(a.vs + sb);
+    };
+    Tile t0, t1;
+    int h0, h1;
+    float f0 = 0.f, g0 = 0.f;
+    next(t0, h0);
+    scales(t0, h0, f0, g0);
+    next(t1, h1);
+    const int stages = keys ? kKStages : kVStages, per = p.box / 4, boxes = kTile / p.box;   // lanes a box, boxes
+    uint64_t *full = keys ? sh->k_full : sh->v_full, *empty = keys ? sh->k_empty : sh->v_empty;
+    unsigned char *buf = keys ? kbuf : vbuf;
+    const CUtensorMap *map = keys ? &map_k : &map_v;
+    uint32_t n = 0, phase = 0;
+    for (int st = 0; t0.asked; ++n) {
+      const int row = t0.page < 0 ? 0 : (int)(((uint32_t)t0.page * a.H + h0) * a.bs + t0.off);
+      const unsigned mask = __ballot_sync(~0u, t0.page >= 0);
+      const float kscale = f0, vscale = g0;
+      // what the next tiles need, on its way
+      t0 = t1;
+      h0 = h1;
+      scales(t0, h0, f0, g0);
+      next(t1, h1);
+      // the tile's largest value scale, rounded up to a power of two 2^e.  Not below
+      // 2^-96: such values vanish beside any other.  Not above 2^126: ex2 gives 0 for
+      // 2^-127, and codes whose values are finite leave f16 room for the rest.
+      const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(vscale));
+      const int e = min(max((int)(most >> 23) + ((most & 0x7fffff) != 0), 127 - 96), 127 + 126);
+      const int from = __shfl_sync(~0u, row, lane < boxes ? lane * per : 0);
+      const bool there = lane < boxes && (mask >> (lane * per) & 1);
+      const uint32_t bytes = __popc(__ballot_sync(~0u, there)) * (uint32_t)p.box * kD;
+      if (!W.warp_wait(&empty[st], phase ^ 1)) break;
+      if (keys) {
+        sh->ks[st][lane] = kscale;
         if (lane == 0) {
-          sh->k_mask[ks] = mask;
-          sh->k_ref[ks] = (float)(e - 127);
-          mbar_expect_tx(smem_addr(&sh->k_full[ks]), bytes);
+          sh->k_mask[st] = mask;
+          sh->k_ref[st] = (float)(e - 127);
         }
-        __syncwarp();
-        if (there)
-          tma_load_2d(smem_addr(kbuf + ks * kTileBytes + lane * p.box * kD), &map_k, 0, from,
-                      smem_addr(&sh->k_full[ks]));
-        if (lane != 0) mbar_arrive(smem_addr(&sh->k_full[ks]));
-        if (!W.warp_wait(&sh->v_empty[vs], (n / kVStages & 1) ^ 1)) goto ld_done;
-        sh->vs[vs][lane] = vscale;
+      } else {
+        sh->vs[st][lane] = vscale;
         if (lane == 0) {
-          sh->v_mask[vs] = mask;
-          sh->v_unit[vs] = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
-          mbar_expect_tx(smem_addr(&sh->v_full[vs]), bytes);
+          sh->v_mask[st] = mask;
+          sh->v_unit[st] = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
         }
-        __syncwarp();
-        if (there)
-          tma_load_2d(smem_addr(vbuf + vs * kTileBytes + lane * p.box * kD), &map_v, 0, from,
-                      smem_addr(&sh->v_full[vs]));
-        if (lane != 0) mbar_arrive(smem_addr(&sh->v_full[vs]));
+      }
+      if (lane == 0) mbar_expect_tx(smem_addr(&full[st]), bytes);
+      __syncwarp();
+      if (there) tma_load_2d(smem_addr(buf + st * kTileBytes + lane * p.box * kD), map, 0, from, smem_addr(&full[st]));
+      if (lane != 0) mbar_arrive(smem_addr(&full[st]));
+      if (++st == stages) {
+        st = 0;
+        phase ^= 1;
       }
     }
-  ld_done:
-    // drain: the tiles that were asked for have landed (n counts whole tiles; after
-    // an abort the last keys may be one ahead of the values)
+    // drain: the tiles that were asked for have landed
     __syncwarp();
-    if (lane == 0) {
-      for (uint32_t x = n > kKStages ? n - kKStages : 0; x < n; ++x) drain_wait(&sh->k_full[x % kKStages], x / kKStages & 1);
-      for (uint32_t x = n > kVStages ? n - kVStages : 0; x < n; ++x) drain_wait(&sh->v_full[x % kVStages], x / kVStages & 1);
-      if (sh->abort) drain_wait(&sh->k_full[n % kKStages], n / kKStages & 1);
-    }
+    if (lane == 0)
+      for (uint32_t x = n > (uint32_t)stages ? n - stages : 0; x < n; ++x) drain_wait(&full[x % stages], x / stages & 1);
   } else if (warp < kMmaWarp + 2) {
     fewer_registers<kOtherRegs>();
     // ----------------------------------------------------------------------
@@ -1429,8 +1472,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) drain_wait(&sh->drain[i], 0);
     }
     __syncwarp();
-  } else {
-    fewer_registers<kOtherRegs>();   // the split counts whole warpgroups
   }
 
   tc_fence_before();
@@ -1694,7 +1735,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
       const int rows = (int)min((int64_t)NC, (int64_t)w.fresh * a.G - row0);
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
                                  (int64_t)(w.h * a.G + (int)((row0 + lane) % a.G)) * a.qh;
-      const float f = put_queries<4>(a, p.vec_q, src, lane < rows, qbuf + (item & 1) * 2 * kColQBytes, 0, kColQBytes, 16);
+      const float f = put_queries<2>(a, p.vec_q, src, lane < rows, qbuf + (item & 1) * 2 * kColQBytes, 0, kColQBytes, 16);
       if (lane < 16) sh->cs[item & 1][lane] = f;
       fence_async_proxy();
       __syncwarp();
