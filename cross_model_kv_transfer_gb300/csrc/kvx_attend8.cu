@@ -95,7 +95,8 @@ struct Shared {
 kvx_status shared_of(const kvx_attend8_shared_args *a, Shared &s) {
   if (!a) return KVX_ERR_INVALID_ARG;
   if (const kvx_status st = check(&a->own)) return st;
-  if (a->own.weights || !a->prefix_table || !aligned_to(a->prefix_table, 4) || !a->prefix_lens || a->max_prefix_blocks < 1 ||
+  if (a->own.weights || !a->prefix_table || !aligned_to(a->prefix_table, 4) || !a->prefix_lens || !aligned_to(a->prefix_lens, 4) ||
+      !aligned_to(a->groups, 4) || a->max_prefix_blocks < 1 ||
       a->num_prefixes < 1 || (!a->groups && a->num_prefixes != 1) || a->max_group < 1)
     return KVX_ERR_INVALID_ARG;
   s.own = s.before = a->own;

@@ -477,6 +477,7 @@ extern "C" kvx_status kvx_beam_select(const kvx_beam_args *a, void *stream) {
   if (a->num_requests == 0) return KVX_OK;
   const int size = a->dtype == KVX_BF16 ? 2 : 4;
   if (!a->logits || !aligned_to(a->logits, size) || !a->scores || !a->tokens || !a->parents || !a->new_scores ||
+      !aligned_to(a->scores, 4) || !aligned_to(a->tokens, 4) || !aligned_to(a->parents, 4) || !aligned_to(a->new_scores, 4) ||
       a->new_scores == a->scores || (a->new_done && a->new_done == a->done) || !a->workspace ||
       !aligned_to(a->workspace, 256) || a->workspace_bytes < kvx_beam_workspace_bytes(a))
     return KVX_ERR_INVALID_ARG;

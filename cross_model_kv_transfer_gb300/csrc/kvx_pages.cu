@@ -527,6 +527,11 @@ kvx_status launch_counting(void (*one)(P), void (*many)(P), const P &p, cudaStre
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, many, p) == cudaSuccess ? KVX_OK : KVX_ERR_CUDA;
 }
+// 32-bit words: all given lie on their boundaries.
+template <class... P>
+bool words_ok(P... p) {
+  return (aligned_to(p, 4) && ...);
+}
 bool pool_ok(const int32_t *refs, int64_t num_blocks) {
   return refs && aligned_to(refs, 4) && num_blocks >= 1 && num_blocks <= kMostPages;
 }
@@ -542,7 +547,7 @@ extern "C" size_t kvx_pages_workspace_bytes(int64_t num_blocks) {
 }
 
 extern "C" kvx_status kvx_cache8_copy(const kvx_cache8_copy_args *a, void *stream) {
-  if (!a || a->num_pairs < 0 || (a->num_pairs > 0 && (!a->pairs || !aligned_to(a->pairs, 4)))) return KVX_ERR_INVALID_ARG;
+  if (!a || a->num_pairs < 0 || (a->num_pairs > 0 && !a->pairs) || !words_ok(a->pairs, a->count, a->status)) return KVX_ERR_INVALID_ARG;
   if (a->num_caches < 0 || (a->num_caches > 0 && !a->caches)) return KVX_ERR_INVALID_ARG;
   if (a->num_caches == 0) return KVX_OK;
   const int64_t num_blocks = a->caches[0].num_blocks;
@@ -553,7 +558,8 @@ extern "C" kvx_status kvx_cache8_copy(const kvx_cache8_copy_args *a, void *strea
 extern "C" kvx_status kvx_pages_fork(const kvx_pages_fork_args *a, void *stream) {
   if (!a || !pool_ok(a->refs, a->num_blocks) || a->block_size < 1 || a->block_size > 1024 || a->num_rows < 0 || a->width < 1 ||
       a->num_new < 0 || (a->num_rows > 0 && (!a->table || !a->lens)) ||
-      (a->num_new > 0 && (!a->parents || !a->new_table || !a->new_lens)) || (int64_t)a->width * a->block_size > kMostSlots)
+      (a->num_new > 0 && (!a->parents || !a->new_table || !a->new_lens)) || (int64_t)a->width * a->block_size > kMostSlots ||
+      !words_ok(a->table, a->lens, a->parents, a->new_table, a->new_lens, a->status))
     return KVX_ERR_INVALID_ARG;
   if (a->num_new > 0 && a->num_rows > 0 && (a->new_table == a->table || a->new_lens == a->lens)) return KVX_ERR_INVALID_ARG;
   const int64_t ctas = (int64_t)a->num_new + a->num_rows;
@@ -565,7 +571,7 @@ extern "C" kvx_status kvx_pages_fork(const kvx_pages_fork_args *a, void *stream)
 }
 
 extern "C" kvx_status kvx_pages_free(const kvx_pages_free_args *a, void *stream) {
-  if (!a || !pool_ok(a->refs, a->num_blocks) || a->num_rows < 0 || a->width < 1 || (a->num_rows > 0 && !a->table))
+  if (!a || !pool_ok(a->refs, a->num_blocks) || a->num_rows < 0 || a->width < 1 || (a->num_rows > 0 && !a->table) || !words_ok(a->table, a->status))
     return KVX_ERR_INVALID_ARG;
   const int64_t entries = (int64_t)a->num_rows * a->width;
   if (entries == 0) return KVX_OK;
@@ -576,7 +582,7 @@ extern "C" kvx_status kvx_pages_free(const kvx_pages_free_args *a, void *stream)
 
 extern "C" kvx_status kvx_pages_reserve(const kvx_pages_reserve_args *a, void *stream) {
   if (!a || !pool_ok(a->refs, a->num_blocks) || a->block_size < 1 || a->block_size > 1024 || a->num_rows < 0 || a->width < 1 ||
-      a->add_all < 0 || (int64_t)a->width * a->block_size > kMostSlots)
+      a->add_all < 0 || (int64_t)a->width * a->block_size > kMostSlots || !words_ok(a->table, a->lens, a->add, a->copies, a->status))
     return KVX_ERR_INVALID_ARG;
   if (const kvx_status st = check_caches(a->caches, a->num_caches, a->num_blocks, a->block_size)) return st;
   if (a->num_rows == 0) return KVX_OK;
@@ -601,7 +607,8 @@ extern "C" kvx_status kvx_pages_reserve(const kvx_pages_reserve_args *a, void *s
 
 extern "C" kvx_status kvx_pages_compact(const kvx_pages_compact_args *a, void *stream) {
   if (!a || !pool_ok(a->refs, a->num_blocks) || a->block_size < 1 || a->block_size > 1024 || a->num_tables < 0 ||
-      a->num_tables > kMaxTables || (a->num_tables > 0 && (!a->tables || !a->entries)) || !a->used || !a->moved)
+      a->num_tables > kMaxTables || (a->num_tables > 0 && (!a->tables || !a->entries)) || !a->used || !a->moved ||
+      !words_ok(a->used, a->moved, a->status))
     return KVX_ERR_INVALID_ARG;
   if (const kvx_status st = check_caches(a->caches, a->num_caches, a->num_blocks, a->block_size)) return st;
   if (!workspace_ok(a->workspace, a->workspace_bytes, a->num_blocks)) return KVX_ERR_INVALID_ARG;

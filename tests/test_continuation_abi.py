@@ -62,7 +62,7 @@ def test_shared_attention_refuses():
     call = lambda **over: kvx.kvx_attend8_shared(shared_args(**over), None)
     for over in BAD_CACHES:
         assert kvx.kvx_attend8_shared(shared_args(cache_desc(**over)), None) == bad
-    for over in (dict(prefix_table=None), dict(prefix_table=P + 2), dict(prefix_lens=None),
+    for over in (dict(prefix_table=None), dict(prefix_table=P + 2), dict(prefix_lens=None), dict(prefix_lens=P + 1), dict(groups=P + 2),
                  dict(groups=None), dict(max_prefix_blocks=0), dict(num_prefixes=0), dict(max_prefix=-1),
                  dict(max_group=0), dict(weights=P, weights_stride=64), dict(q=None), dict(out=P + 1),
                  dict(workspace=None), dict(workspace=P + 128), dict(q_heads=3), dict(max_new=0),
@@ -109,15 +109,17 @@ def test_pages_refuse():
     for cls, call, more in (
             (kvx.PagesForkArgs, kvx.kvx_pages_fork,
              shape + [dict(block_size=0), dict(block_size=1025), dict(lens=None), dict(parents=None), dict(num_new=-1),
-                      dict(new_table=None), dict(new_lens=None), dict(new_table=P), dict(new_lens=P),
+                      dict(new_table=None), dict(new_lens=None), dict(new_table=P), dict(new_lens=P), dict(table=P + 2),
+                      dict(lens=P + 1), dict(parents=P + 3), dict(new_table=P + 2), dict(new_lens=P + 2),
                       dict(width=2 ** 27)]),
             (kvx.PagesFreeArgs, kvx.kvx_pages_free, shape),
             (kvx.PagesReserveArgs, kvx.kvx_pages_reserve,
-             shape + [dict(block_size=0), dict(lens=None), dict(add_all=-1), dict(workspace=None),
+             shape + [dict(block_size=0), dict(lens=None), dict(add_all=-1), dict(add=P + 2), dict(copies=P + 2),
+                      dict(table=P + 1), dict(workspace=None),
                       dict(workspace=P + 4), dict(workspace_bytes=100), dict(num_caches=-1), dict(num_caches=1),
                       dict(width=2 ** 27)]),
             (kvx.PagesCompactArgs, kvx.kvx_pages_compact,
-             [dict(block_size=0), dict(used=None), dict(moved=None), dict(num_tables=-1), dict(num_tables=9),
+             [dict(block_size=0), dict(used=None), dict(moved=None), dict(used=P + 2), dict(moved=P + 1), dict(num_tables=-1), dict(num_tables=9),
               dict(num_tables=1), dict(workspace=None), dict(workspace_bytes=0), dict(num_caches=2)])):
         for over in pool + more:
             assert call(pages_args(cls, **over), None) == bad, (cls, over)
@@ -166,7 +168,7 @@ def beam_args(**over):
 def test_beam_selection_refuses():
     for over in (dict(logits=None), dict(logits=P + 2), dict(dtype=2), dict(num_requests=-1), dict(beams=0),
                  dict(beams=33), dict(out_beams=0), dict(out_beams=33), dict(vocab=0), dict(eos=-2), dict(eos=100),
-                 dict(scores=None), dict(tokens=None), dict(parents=None), dict(new_scores=None),
+                 dict(scores=None), dict(scores=P + 2), dict(tokens=P + 1), dict(tokens=None), dict(parents=None), dict(new_scores=None),
                  dict(new_scores=P), dict(done=P), dict(done=P, new_done=P, eos=1), dict(workspace=None),
                  dict(workspace=P + 8), dict(workspace_bytes=10), dict(vocab=2 ** 31 - 1), dict(num_requests=2 ** 30)):
         assert kvx.kvx_beam_select(beam_args(**over), None) == kvx.KVX_ERR_INVALID_ARG, over

@@ -111,6 +111,21 @@ def test_matches_fp64(H, G, d, bs, prefixes, members, lens, news, dtype):
     check(make(H, G, d, bs, prefixes, members, lens, news, dtype, 3))
 
 
+LONG = [
+    (1, 2, 64, 16, [300], [2], [2100, 5], [1, 1]),                         # more own slots than an item's CTA takes
+    (1, 13, 128, 16, [90], [2], [100, 30], [5, 4]),                        # 65 rows, one more than it takes
+    (1, 16, 64, 32, [5000], [2], [33, 2048], [4, 1]),                      # 64 rows
+    (1, 8, 128, 16, [9000], [64], [3] * 64, [1] * 64),                     # a prefix of much work
+    (1, 8, 128, 64, [70, 9000], [3, 125], [1 + r % 5 for r in range(128)], [1] * 128),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H,G,d,bs,prefixes,members,lens,news", LONG)
+def test_matches_fp64_beyond_each_form(H, G, d, bs, prefixes, members, lens, news, dtype):
+    check(make(H, G, d, bs, prefixes, members, lens, news, dtype, 31))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_without_tables(dtype):
     """One token for each request and one prefix for all: neither table is needed."""
