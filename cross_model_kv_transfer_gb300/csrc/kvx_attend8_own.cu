@@ -198,7 +198,7 @@ struct Sums {
 // PART: of a prefix's slots, CTAs (prefix and KV head, group of columns, split).  Else: of a
 // request's own, CTAs (request and KV head, group of columns).
 template <class C, bool PART>
-__global__ void __launch_bounds__(32 * C::WARPS) own_kernel(const __grid_constant__ OwnParams op) {
+__global__ void __launch_bounds__(32 * C::WARPS, C::DP <= 128 ? 3 : 1) own_kernel(const __grid_constant__ OwnParams op) {
   constexpr int DP = C::DP, NT = C::NT, KW = C::KW, CH = C::CH, W = C::WARPS, COLS = C::COLS;
   extern __shared__ __align__(128) unsigned char smem[];
   const SplitParams &p = op.s;

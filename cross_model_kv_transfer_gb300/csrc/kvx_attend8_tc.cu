@@ -661,12 +661,6 @@ __device__ __noinline__ float query_factor(const AttendParams &a, bool vec, cons
   }
   return row_factor(a, top, pow2_scale(top));
 }
-// Up to 32 query rows of a warp (`count` of them, rounded up to 8) as two e4m3
-// parts, `part` bytes apart, in the swizzled K-major tile, from row `first` of the
-// tile on; `src` is the lane's own row.  Half a warp loads a row, eight rows at a
-// time where a CTA does one or two items and runs this code cold, sixteen where it
-// does many (wide calls).  Returns the lane's factor on its row's
-// scores (its sign is in the parts).
 // The 16 bytes of a row that a lane of put_queries takes.
 __device__ __forceinline__ uint4 query_piece(bool vec, const __nv_bfloat16 *from) {
   if (vec) return __ldg(reinterpret_cast<const uint4 *>(from));
@@ -682,6 +676,13 @@ __device__ __forceinline__ uint4 query_piece(bool vec, const __nv_bfloat16 *from
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
+// Up to 32 query rows of a warp (`count` of them, rounded up to 8) as two e4m3
+// parts, `part` bytes apart, in the swizzled K-major tile, from row `first` of the
+// tile on; `src` is the lane's own row.  Half a warp loads a row, 2 N rows at a time, the
+// next ones on their way.  Where a CTA does one or two items it runs this code cold, and
+// four rows at a time are best (the 16 requests below with 128 rows a KV head 153 us, 163
+// with sixteen); where it does many, eight (a prompt of 8192 tokens 1074 us, 1099 with
+// four).  Returns the lane's factor on its row's scores (its sign is in the parts).
 template <int N>
 __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
                                           unsigned char *tile, int first, int part, int count) {
@@ -1541,7 +1542,7 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
 // One query of 64 heads over 131,071 slots of 8 heads takes 57 us, 4.7 TB/s (a copy
 // 6.7); 16 requests of 1024 to 16,384 slots 73 us, and with 16 columns, which read the
 // same bytes, 94: the chain of a tile's softmax counts beside them.  The narrow form
-// above takes 146 there, matrix instructions on registers (16 x 8 x 16) 88 with 8.
+// above takes 124 there, matrix instructions on registers (16 x 8 x 16) 88 with 8.
 // even numbers of stages: a stage serves one group, whose waits on it then know
 // that the phase before is over
 constexpr int kCkStages = 4, kCvStages = 6, kScales = 16, kColThreads = 12 * 32;
@@ -2405,9 +2406,9 @@ TcShape tc_shape(const kvx_attend8_args *a) {
   TcShape s;
   const int64_t G = a->q_heads / a->cache.heads, most = G * most_new(a);
   // 16 requests of 1024 to 16,384 slots, 8 KV heads, without and with weights.  16 rows:
-  // columns 94 and 119 us, narrow 146 and 189.  24 rows: narrow 147 and 202, wide 151 and
-  // 298; 64 rows: 167 and 274 against 159 and 308; 128 rows: 216 and 432 against 160 and
-  // 309.
+  // columns 93 and 118 us, narrow 124 and 175.  24 rows: narrow 130 and 189, wide 140 and
+  // 282; 64 rows: 156 and 268 against 152 and 297; 128 rows: 209 and 439 against 154 and
+  // 298.
   s.columns = most <= 16;
   s.wide = most > 64;
   s.slot_rows = s.wide ? Wide::ROWS : s.columns ? (most <= 8 ? 8 : 16) : (int)most;
