@@ -1378,6 +1378,7 @@ class Pages:
             raise ValueError("refs must be a contiguous 1-D int32 tensor")
         self.refs, self.block_size, self.device = refs, int(block_size), refs.device
         self.num_blocks = refs.shape[0]
+        self._index = refs.device.index
 
     @classmethod
     def empty(cls, num_blocks, block_size, device="cuda"):
@@ -1393,34 +1394,45 @@ class Pages:
             raise KvxError(KVX_ERR_INVALID_ARG, "kvx_pages_workspace_bytes")
         return torch.empty(need, dtype=torch.uint8, device=self.device)
 
-    def _rows(self, table, lens, name="table"):
-        ptr = _int_table(table, name, self.device, 2)
-        if lens is not None and lens.shape[0] != table.shape[0]:
-            raise ValueError(f"lens and {name} must hold the same rows")
-        return table.shape[0], table.shape[1], ptr
+    def _ready(self):
+        """The pool's device, which has to be the current one."""
+        if _Fast.torch is None or _Fast.device() != self._index:
+            _on_device(self.device)
+        return self.device
+
+    def _rows(self, table, lens):
+        """Rows, width and pointer of a table, and the pointer of the rows' lengths."""
+        ptr = _int_table(table, "table", self.device, 2)
+        R, width = table.shape
+        if lens.shape[0] != R:
+            raise ValueError("lens and table must hold the same rows")
+        return R, width, ptr, _int_table(lens, "lens", self.device)
 
     def fork(self, table, lens, parents, *, new_table=None, new_lens=None, status=None, stream=None):
         """New rows in place of those of ``table`` [R][width]: row n continues
         row parents[n] (-1: an empty row) and shares the pages that its length
         covers.  The old rows hold nothing afterwards.  Returns (new_table
         [N][width], new_lens [N])."""
-        dev = self.device
-        _on_device(dev)
-        R, width, ptr = self._rows(table, lens)
+        dev = self._ready()
+        R, width, ptr, len_ptr = self._rows(table, lens)
         parent = _int_table(parents, "parents", dev)
         N = parents.shape[0]
         if new_table is None:
             new_table = _new(stream, (N, width), _Fast.i32, dev)
-        elif tuple(new_table.shape) != (N, width):
-            raise ValueError("new_table must be [N][width]")
+            to = new_table.data_ptr()
+        else:
+            to = _int_table(new_table, "new_table", dev, 2)
+            if tuple(new_table.shape) != (N, width):
+                raise ValueError("new_table must be [N][width]")
         if new_lens is None:
             new_lens = _new(stream, (N,), _Fast.i32, dev)
-        elif tuple(new_lens.shape) != (N,):
-            raise ValueError("new_lens must be [N]")
+            to_lens = new_lens.data_ptr()
+        else:
+            to_lens = _int_table(new_lens, "new_lens", dev)
+            if new_lens.shape[0] != N:
+                raise ValueError("new_lens must be [N]")
         a = _pack_fork(self.refs.data_ptr(), self.num_blocks, self.block_size, R, width, ptr,
-                       _int_table(lens, "lens", dev), parent, N,
-                       _int_table(new_table, "new_table", dev, 2),
-                       _int_table(new_lens, "new_lens", dev), _status_ptr(status, dev))
+                       len_ptr, parent, N, to, to_lens, _status_ptr(status, dev))
         st = _Fast.fork(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_pages_fork")
@@ -1429,10 +1441,9 @@ class Pages:
     def free(self, table, *, status=None, stream=None):
         """The rows of ``table`` (some rows of one: a slice) release their pages;
         their entries become -1."""
-        dev = self.device
-        _on_device(dev)
-        R, width, ptr = self._rows(table, None)
-        a = PagesFreeArgs(self.refs.data_ptr(), self.num_blocks, R, width, ptr,
+        dev = self._ready()
+        ptr = _int_table(table, "table", dev, 2)
+        a = PagesFreeArgs(self.refs.data_ptr(), self.num_blocks, *table.shape, ptr,
                           _status_ptr(status, dev))
         st = kvx_pages_free(a, _raw_stream(stream, dev))
         if st != KVX_OK:
@@ -1447,9 +1458,8 @@ class Pages:
         one for each row (int32 tensor, at most ``max_new``).  ``copies`` [R][2]
         (int32) receives the copied pages, from and to (-1: none).  With too few
         free pages nothing changes, and ``status`` tells (KVX_FLAG_NO_PAGES)."""
-        dev = self.device
-        _on_device(dev)
-        R, width, ptr = self._rows(table, lens)
+        dev = self._ready()
+        R, width, ptr, len_ptr = self._rows(table, lens)
         add = 0
         if isinstance(new, int):
             most = new
@@ -1458,14 +1468,14 @@ class Pages:
             if new.shape[0] != R:
                 raise ValueError("new must hold one entry for each row")
             most = width * self.block_size if max_new is None else max_new
-        if copies is not None and tuple(copies.shape) != (R, 2):
+        copy_ptr = _int_table(copies, "copies", dev, 2)
+        if copy_ptr and tuple(copies.shape) != (R, 2):
             raise ValueError("copies must be [R][2]")
         if workspace is None:
             workspace = _on_stream(self.workspace, stream)
         keep, array = _cache_array(caches, self.num_blocks, dev)
         a = _pack_reserve(self.refs.data_ptr(), self.num_blocks, self.block_size, R, width, ptr,
-                          _int_table(lens, "lens", dev), add, most,
-                          _int_table(copies, "copies", dev, 2), array, len(caches),
+                          len_ptr, add, most, copy_ptr, array, len(caches),
                           *_workspace(workspace, dev), _status_ptr(status, dev))
         st = _Fast.reserve(a, _raw_stream(stream, dev))
         if st != KVX_OK:
@@ -1477,14 +1487,19 @@ class Pages:
         rewrite ``tables`` (up to eight int32 tensors, which hold all
         references).  Returns (used [1], moved [num_blocks]): how many pages are
         held, and each page's new number (-1: it is free)."""
-        dev = self.device
-        _on_device(dev)
+        dev = self._ready()
         if used is None:
             used = _new(stream, (1,), _Fast.i32, dev)
+            used_ptr = used.data_ptr()
+        else:
+            used_ptr = _int_table(used, "used", dev)
         if moved is None:
             moved = _new(stream, (self.num_blocks,), _Fast.i32, dev)
-        elif tuple(moved.shape) != (self.num_blocks,):
-            raise ValueError("moved must be [num_blocks]")
+            moved_ptr = moved.data_ptr()
+        else:
+            moved_ptr = _int_table(moved, "moved", dev)
+            if moved.shape[0] != self.num_blocks:
+                raise ValueError("moved must be [num_blocks]")
         if workspace is None:
             workspace = _on_stream(self.workspace, stream)
         keep, array = _cache_array(caches, self.num_blocks, dev)
@@ -1493,8 +1508,7 @@ class Pages:
             *[_int_table(t, "tables", dev, t.dim()) for t in tables], *[t.numel() for t in tables])
         at = ctypes.addressof(lists)
         a = _pack_compact(self.refs.data_ptr(), self.num_blocks, self.block_size, at, at + 8 * n, n,
-                          _int_table(used, "used", dev), _int_table(moved, "moved", dev), array,
-                          len(caches), *_workspace(workspace, dev), _status_ptr(status, dev))
+                          used_ptr, moved_ptr, array, len(caches), *_workspace(workspace, dev), _status_ptr(status, dev))
         st = _Fast.compact(a, _raw_stream(stream, dev))
         if st != KVX_OK:
             raise KvxError(st, "kvx_pages_compact")
