@@ -248,12 +248,20 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::DP <= 128 ? 3 : 1) own_kerne
     }
     return good && groups_ok(a, tid, 32 * W);
   };
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && !__syncthreads_and(table_ok())) {
+  // What follows this kernel on its stream waits for this kernel alone, which may start beside
+  // the one before it.  So the first CTA never leaves before that one has ended, whatever the
+  // tables hold: else no CTA might, and the next call would write where its parts still go.
+  const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+  if (first_cta && !__syncthreads_and(table_ok())) {
+    if (!PART) wait_for_kernel_before();
     if (tid == 0) raise(a.status, KVX_FLAG_BAD_SEQLENS);
     return;
   }
   if (h == 0 && col0 == 0 && blockIdx.z == 0 && tid == 0 && len != __ldg(a.lens + r)) raise(a.status, KVX_FLAG_BAD_LENGTH);
-  if (col0 >= cols) return;
+  if (col0 >= cols) {
+    if (!PART && first_cta) wait_for_kernel_before();
+    return;
+  }
 
   // A tile goes through three steps, so that nothing waits for one before it: its blocks are
   // looked up (lane l slot l), a turn later its codes and scales are asked for, and the
