@@ -100,9 +100,11 @@ __device__ __forceinline__ int first_limit(const AttendParams &p, int len, int f
 }
 __device__ __forceinline__ int limit_step(const AttendParams &p) { return kShared && p.share.all ? 0 : 1; }
 // Groups of requests start at 0, never decrease, end at the last request and have at most
-// `most` tokens each: this thread's share of the check, in the pass over own slots.
+// `most` tokens each (without a table all tokens are one group's): this thread's share of the
+// check, in the pass over own slots.
 __device__ __forceinline__ bool groups_ok(const AttendParams &p, int first, int stride) {
   bool good = true;
+  if (kShared && p.share.whole) good = p.req.ntok <= p.share.most;
   if (kShared && !p.share.all && p.share.of)
     for (int i = first; i < p.share.count; i += stride) {
       const int a = p.share.of[i], b = p.share.of[i + 1];
