@@ -421,11 +421,6 @@ kvx_status check(const kvx_evict8_args *a) {
   return KVX_OK;
 }
 
-bool overlap(const void *a, int64_t a_words, const void *b, int64_t b_words) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x < y + 4 * (uintptr_t)b_words && y < x + 4 * (uintptr_t)a_words;
-}
-
 }  // namespace
 
 extern "C" size_t kvx_evict8_workspace_bytes(const kvx_evict8_args *a) {

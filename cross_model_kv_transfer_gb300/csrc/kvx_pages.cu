@@ -510,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
 constexpr int64_t kSmallPool = 8192;
 // pages, and slots of a row, are counted in 32 bits, a little beyond the last one too
 constexpr int64_t kMostPages = INT32_MAX - 1024, kMostSlots = INT32_MAX - 1024;
+constexpr int64_t kMostEntries = (int64_t)1 << 60;   // of a table: their bytes are counted in 64 bits
 template <class P>
 kvx_status launch_counting(void (*one)(P), void (*many)(P), const P &p, cudaStream_t s) {
   if (p.num_blocks <= kSmallPool) return launch_after(one, dim3(1), kThreads, 0, s, p);
@@ -614,7 +615,11 @@ extern "C" kvx_status kvx_pages_compact(const kvx_pages_compact_args *a, void *s
   if (!workspace_ok(a->workspace, a->workspace_bytes, a->num_blocks)) return KVX_ERR_INVALID_ARG;
   Tables t = {};
   for (int i = 0; i < a->num_tables; ++i) {
-    if (a->entries[i] < 0 || (a->entries[i] > 0 && (!a->tables[i] || !aligned_to(a->tables[i], 4)))) return KVX_ERR_INVALID_ARG;
+    if (a->entries[i] < 0 || a->entries[i] > kMostEntries || (a->entries[i] > 0 && (!a->tables[i] || !aligned_to(a->tables[i], 4))))
+      return KVX_ERR_INVALID_ARG;
+    // an entry is rewritten once: its new number may be another page's old one
+    for (int j = 0; j < i; ++j)
+      if (overlap(a->tables[j], a->entries[j], a->tables[i], a->entries[i])) return KVX_ERR_INVALID_ARG;
     t.table[i] = a->tables[i];
     t.entries[i] = a->entries[i];
   }

@@ -1485,7 +1485,7 @@ class Pages:
                 stream=None):
         """Move the held pages to the lowest numbers, in all ``caches``, and
         rewrite ``tables`` (up to eight int32 tensors, which hold all
-        references).  Returns (used [1], moved [num_blocks]): how many pages are
+        references and do not overlap).  Returns (used [1], moved [num_blocks]): how many pages are
         held, and each page's new number (-1: it is free)."""
         dev = self._ready()
         if used is None:

@@ -913,8 +913,8 @@ typedef struct {
   int32_t *refs;            /* [num_blocks]                                   */
   int64_t num_blocks;
   int32_t block_size;
-  int32_t *const *tables;   /* HOST array of tables to rewrite (device pointers);
-                               or NULL                                        */
+  int32_t *const *tables;   /* HOST array of tables to rewrite (device pointers),
+                               no two of which overlap; or NULL               */
   const int64_t *entries;   /* HOST array: entries of each                    */
   int32_t num_tables;       /* 0..8                                           */
   int32_t *used;            /* [1] pages that are held                        */

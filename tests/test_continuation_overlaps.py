@@ -1,0 +1,26 @@
+"""Tables of one compaction that overlap are refused (no GPU needed: nothing is enqueued)."""
+import ctypes
+
+import pytest
+
+from cross_model_kv_transfer_gb300 import kvx
+from test_continuation_abi import pages_args
+from test_decode_abi import P
+
+
+@pytest.mark.parametrize("tables", [
+    [(P, 8), (P, 8)],                          # one table twice
+    [(P, 8), (P + 16, 2)],                     # a table and rows of it
+    [(P + 28, 1), (P, 8)],
+    [(P, 2), (P + 4096, 8), (P + 4, 1)],
+    [(P, 4), (P + 12, 4)],
+    [(P, 2 ** 62)],                            # entries that no memory holds
+    [(P + 4096, 8), (P, 2 ** 61 + 1)],
+])
+def test_tables_of_a_compaction_do_not_overlap(tables):
+    n = len(tables)
+    at = (ctypes.c_void_p * n)(*[t for t, _ in tables])
+    entries = (ctypes.c_int64 * n)(*[e for _, e in tables])
+    a = pages_args(kvx.PagesCompactArgs, used=P + 65536, moved=P + 69632, tables=ctypes.addressof(at),
+                   entries=ctypes.addressof(entries), num_tables=n)
+    assert kvx.kvx_pages_compact(a, None) == kvx.KVX_ERR_INVALID_ARG
