@@ -562,7 +562,11 @@ extern "C" kvx_status kvx_pages_fork(const kvx_pages_fork_args *a, void *stream)
       (a->num_new > 0 && (!a->parents || !a->new_table || !a->new_lens)) || (int64_t)a->width * a->block_size > kMostSlots ||
       !words_ok(a->table, a->lens, a->parents, a->new_table, a->new_lens, a->status))
     return KVX_ERR_INVALID_ARG;
-  if (a->num_new > 0 && a->num_rows > 0 && (a->new_table == a->table || a->new_lens == a->lens)) return KVX_ERR_INVALID_ARG;
+  // new rows are written while other CTAs still read the old ones
+  const int64_t old_words = (int64_t)a->num_rows * a->width, new_words = (int64_t)a->num_new * a->width;
+  if (overlap(a->table, old_words, a->new_table, new_words) || overlap(a->lens, a->num_rows, a->new_lens, a->num_new) ||
+      overlap(a->parents, a->num_new, a->new_table, new_words) || overlap(a->parents, a->num_new, a->new_lens, a->num_new))
+    return KVX_ERR_INVALID_ARG;
   const int64_t ctas = (int64_t)a->num_new + a->num_rows;
   if (ctas == 0) return KVX_OK;
   if (ctas > INT32_MAX) return KVX_ERR_UNSUPPORTED;

@@ -847,8 +847,8 @@ typedef struct {
   const int32_t *parents;   /* [N] row of `table` that each new row continues,
                                or -1: an empty row                            */
   int32_t num_new;          /* N, >= 0                                        */
-  int32_t *new_table;       /* [N][width]; overlaps no table                  */
-  int32_t *new_lens;        /* [N]; overlaps no lens                          */
+  int32_t *new_table;       /* [N][width]; overlaps neither table nor parents */
+  int32_t *new_lens;        /* [N]; overlaps neither lens nor parents         */
   uint32_t *status;
 } kvx_pages_fork_args;
 

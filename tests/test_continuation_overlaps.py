@@ -1,4 +1,5 @@
-"""Tables of one compaction that overlap are refused (no GPU needed: nothing is enqueued)."""
+"""Buffers that a call reads and writes do not overlap: tables of one compaction, a fork's old
+and new rows are refused (no GPU needed: nothing is enqueued)."""
 import ctypes
 
 import pytest
@@ -24,3 +25,14 @@ def test_tables_of_a_compaction_do_not_overlap(tables):
     a = pages_args(kvx.PagesCompactArgs, used=P + 65536, moved=P + 69632, tables=ctypes.addressof(at),
                    entries=ctypes.addressof(entries), num_tables=n)
     assert kvx.kvx_pages_compact(a, None) == kvx.KVX_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [
+    # 2 old rows of 4 at P, their lengths 4096 bytes behind; 2 new rows 8192 bytes behind them
+    dict(new_table=P + 16), dict(new_table=P + 28), dict(new_table=P - 28), dict(num_new=3, new_table=P - 36),
+    dict(new_lens=P + 4096 + 4), dict(new_lens=P + 4096 - 4), dict(parents=P + 8192), dict(parents=P + 8192 + 28),
+    dict(parents=P + 12288), dict(parents=P + 12288 + 4), dict(parents=P + 12288 - 4)])
+def test_new_rows_overlap_nothing_that_a_fork_reads(over):
+    a = pages_args(kvx.PagesForkArgs, **{**dict(lens=P + 4096, parents=P + 16384, new_table=P + 8192,
+                                                new_lens=P + 12288), **over})
+    assert kvx.kvx_pages_fork(a, None) == kvx.KVX_ERR_INVALID_ARG
