@@ -478,10 +478,14 @@ extern "C" kvx_status kvx_beam_select(const kvx_beam_args *a, void *stream) {
   const int size = a->dtype == KVX_BF16 ? 2 : 4;
   if (!a->logits || !aligned_to(a->logits, size) || !a->scores || !a->tokens || !a->parents || !a->new_scores ||
       !aligned_to(a->scores, 4) || !aligned_to(a->tokens, 4) || !aligned_to(a->parents, 4) || !aligned_to(a->new_scores, 4) ||
-      a->new_scores == a->scores || (a->new_done && a->new_done == a->done) || !a->workspace ||
+      !a->workspace ||
       !aligned_to(a->workspace, 256) || a->workspace_bytes < kvx_beam_workspace_bytes(a))
     return KVX_ERR_INVALID_ARG;
   const int rows = a->num_requests * a->beams;
+  // results are written while other CTAs still read the scores
+  const int64_t chosen = (int64_t)a->num_requests * a->out_beams;
+  if (overlap(a->scores, rows, a->new_scores, chosen) || (a->done && a->new_done && overlap(a->done, rows, a->new_done, chosen, 1)))
+    return KVX_ERR_INVALID_ARG;
   BeamParams p = {a->logits, a->row_stride, a->scores, a->done,   a->tokens,    a->parents, a->new_scores, a->new_done, a->status,
                   nullptr,   nullptr,       a->beams,  a->out_beams, a->vocab, a->eos, 1};
   p.keys = (unsigned long long *)a->workspace;

@@ -67,10 +67,10 @@ __device__ __forceinline__ void raise(uint32_t *status, uint32_t bits) {
 }
 
 inline bool aligned_to(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-// Do arrays of 32-bit words share any?
-inline bool overlap(const void *a, int64_t a_words, const void *b, int64_t b_words) {
+// Do arrays of 32-bit words (or elements of another size) share memory?
+inline bool overlap(const void *a, int64_t a_words, const void *b, int64_t b_words, int size = 4) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a_words > 0 && b_words > 0 && x < y + 4 * (uintptr_t)b_words && y < x + 4 * (uintptr_t)a_words;
+  return a_words > 0 && b_words > 0 && x < y + size * (uintptr_t)b_words && y < x + size * (uintptr_t)a_words;
 }
 
 // The kernel is launched while the one before on its stream still runs: what that

@@ -1,11 +1,11 @@
 """Buffers that a call reads and writes do not overlap: tables of one compaction, a fork's old
-and new rows are refused (no GPU needed: nothing is enqueued)."""
+and new rows, a selection's old and new scores are refused (no GPU needed: nothing is enqueued)."""
 import ctypes
 
 import pytest
 
 from cross_model_kv_transfer_gb300 import kvx
-from test_continuation_abi import pages_args
+from test_continuation_abi import beam_args, pages_args
 from test_decode_abi import P
 
 
@@ -36,3 +36,11 @@ def test_new_rows_overlap_nothing_that_a_fork_reads(over):
     a = pages_args(kvx.PagesForkArgs, **{**dict(lens=P + 4096, parents=P + 16384, new_table=P + 8192,
                                                 new_lens=P + 12288), **over})
     assert kvx.kvx_pages_fork(a, None) == kvx.KVX_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [
+    # scores and done of 2 x 3, new ones of 2 x 4
+    dict(new_scores=P + 20), dict(new_scores=P - 28), dict(new_done=P + 65536 + 5), dict(new_done=P + 65536 - 7)])
+def test_new_scores_overlap_no_old_ones(over):
+    a = beam_args(**{**dict(eos=1, done=P + 65536, new_done=P + 69632), **over})
+    assert kvx.kvx_beam_select(a, None) == kvx.KVX_ERR_INVALID_ARG
