@@ -15,8 +15,15 @@
 // the logit in an order-preserving form and behind it the falling position: no two are
 // equal, so nothing depends on the order in which a list was filled.
 //
-// Sums of exponentials are relative to a thread's running maximum, fp32 over a warp's
-// elements and fp64 above (about as many additions as there are warps: fp64 is slow here).
+// Sums of exponentials are relative to a thread's reference, which is raised to a chunk's
+// maximum where that is more than kBehind above it: so the old sum is scaled a few times at
+// most while it still counts, however often the maximum moves.  They are fp32 over a warp's
+// elements and fp64 above (about as many additions as there are warps: fp64 is slow here);
+// a thread's sum over its chunks carries the rest of each addition along.  Their error so
+// does not grow with the row: 2^-16 of the sum is a bound for 2^31 logits (two roundings of
+// each argument to fp32, seven exponentials of 2^-22, twenty roundings), 2^-22.7 to 2^-24 was
+// measured for normal logits.  With each maximum a reference and plain fp32 sums 2,000,001
+// logits of one CTA were off by up to 2^-16.9, now 2^-21 (256 rows of 151,936 take 52.9 us, 52.2 so).
 //
 // Bound by HBM where there are many rows, by the latency of a chunk's ranking (a few
 // barriers) where there are few.
@@ -31,7 +38,7 @@
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kCluster = 8, kMostBeams = 32;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kBehind = 8.f;
 
 struct BeamParams {
   const void *logits;
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
   // the CTA's share of the row, in whole loads
   const int64_t loads = (p.V + V - 1) / V;
   const int begin = (int)(loads * rank / p.ctas * V), end = (int)min((int64_t)p.V, loads * (rank + 1) / p.ctas * V);
-  float unit = -INFINITY, sum = 0.f;  // the thread's sum, relative to exp(unit)
+  float unit = -INFINITY, sum = 0.f, rest = 0.f;  // the thread's sum, relative to exp(unit)
   int now = 0;
   const int rounds = (p.N + kWarps - 1) / kWarps;
   if (tid < kMostBeams) sh.best[0][tid] = 0;
@@ -227,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
     float top = x[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
-    // relative to the maximum so far, or 0 before any
-    const auto reference = [&] { return fmaxf(unit, top) > -INFINITY ? fmaxf(unit, top) : 0.f; };
+    // 0 before any logit
+    const auto reference = [&] { return top > unit + kBehind ? top : unit > -INFINITY ? unit : 0.f; };
     float more = sum_of<E>(x, reference());
     if (!(top < INFINITY) || !(more < INFINITY)) {
       // a NaN or an infinity: they become -inf
@@ -241,8 +248,15 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
       }
       more = sum_of<E>(x, reference());
     }
-    sum = sum * ex2((unit - reference()) * kLog2e) + more;
-    unit = fmaxf(unit, top);
+    if (top > unit + kBehind) {
+      const float down = ex2((unit - top) * kLog2e);
+      sum *= down;
+      rest *= down;
+      unit = top;
+    }
+    const float both = __fadd_rn(sum, more), part = __fsub_rn(both, sum);
+    rest += __fsub_rn(sum, __fsub_rn(both, part)) + __fsub_rn(more, part);
+    sum = both;
     if (at == begin) {                // what the warps agree on
       uint32_t left = top > -INFINITY ? ordered(top + 0.f) : 0u, least = 0;
       for (int i = 0; i < rounds; ++i) {
@@ -280,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_kernel(const __grid_constant_
   float top = unit;
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  float part = unit > -INFINITY ? sum * ex2((unit - top) * kLog2e) : 0.f;
+  float part = unit > -INFINITY ? (sum + rest) * ex2((unit - top) * kLog2e) : 0.f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
   if (lane == 0) {

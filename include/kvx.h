@@ -987,8 +987,10 @@ size_t kvx_beam_workspace_bytes(const kvx_beam_args *args);
  * has tokens and parents of -1 and scores of -inf behind them.  A logit that is
  * NaN or +inf counts as -inf, a beam whose score is NaN or +inf as none
  * (KVX_FLAG_NOT_FINITE).  Each beam's logits are read once; scores are ranked as
- * fp64 sums of the fp32 (or bf16) logits, the scores and log-sum-exps that are
- * known to about 2^-22, and rounded to fp32 when they are written.  parents are what
+ * fp64 sums of the fp32 (or bf16) logits, the scores and log-sum-exps, and rounded to
+ * fp32 when they are written.  A log-sum-exp is off by at most 2^-16, whatever the logits
+ * and their number, and by about 2^-22 where they are spread as a model's are: candidates
+ * of different beams that are nearer than that may change places.  parents are what
  * kvx_pages_fork takes.  Two launches.  KVX_ERR_INVALID_ARG also for eos outside
  * [-1, V), and for done without eos. */
 kvx_status kvx_beam_select(const kvx_beam_args *args, void *stream);
