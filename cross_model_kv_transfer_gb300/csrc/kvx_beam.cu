@@ -380,7 +380,7 @@ struct PickShared {
   uint32_t warp_bound[kWarps];
 };
 // Candidate i = k * N + j of a request: the j-th of beam k.  In that order equal scores
-// go to the lower beam and token.  The list is bounded as a chunk's is, by the scores'
+// go to the lower beam, and in a beam to the larger logit, then the lower token.  The list is bounded as a chunk's is, by the scores'
 // upper halves, and has room for all.
 __global__ void __launch_bounds__(kThreads) pick_kernel(const __grid_constant__ BeamParams p) {
   __shared__ PickShared sh;

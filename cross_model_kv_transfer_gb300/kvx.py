@@ -1550,8 +1550,8 @@ def beam_select(logits, scores, *, beams=None, eos=None, done=None, tokens=None,
                 new_scores=None, new_done=None, workspace=None, status=None, stream=None):
     """Beam search's selection (``kvx_beam_select``): of the candidates of each
     request, scores[b][k] + log_softmax(logits[b * K + k])[v], the ``beams`` (K) of
-    the largest score, equal ones by k and v.  ``logits`` [B * K][V] (fp32 or bf16,
-    unit stride inside a row), ``scores`` [B][K] fp32 (-inf: no beam); beams that
+    the largest score: within a beam by logit, equal ones by v; equal scores of
+    different beams by k.  ``logits`` [B * K][V] (fp32 or bf16, unit stride inside a row), ``scores`` [B][K] fp32 (-inf: no beam); beams that
     are ``done`` [B][K] (bool) have one candidate, ``eos`` with the score they
     have.  Returns (tokens, parents, scores, done) [B][beams]: parents are rows of
     logits, as ``Pages.fork`` takes them (-1, with a score of -inf: no candidate);

@@ -981,7 +981,8 @@ size_t kvx_beam_workspace_bytes(const kvx_beam_args *args);
 
 /* Beam search's selection: of every request's candidates the N of the largest score,
  *   score(k, v) = scores[k] + logits[k][v] - log sum_u exp(logits[k][u]),
- * in falling order; equal ones by k, then v.  A beam that has ended has one candidate:
+ * in falling order: within a beam by falling logit, equal logits by v, also where the
+ * scores' sums in fp64 no longer differ; equal scores of different beams by k.  A beam that has ended has one candidate:
  * eos, with the score that it has.  new_done: the token is eos.  Logits of -inf
  * and beams whose score is -inf give no candidates; a request with fewer than N
  * has tokens and parents of -1 and scores of -inf behind them.  A logit that is
