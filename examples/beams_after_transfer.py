@@ -56,7 +56,8 @@ def run(prompts=(70, 200), layers=2, beams=4, steps=(10, 10), vocab=1000, group=
         watch=None):
     """Two stretches of beam search; the first prompt is dropped between them and the
     pool compacted.  ``watch(stage, **tensors)`` sees what the calls read and wrote.
-    Returns (token histories of the prompts that are left, scores, flags)."""
+    Returns (token histories of the prompts that are left, scores, flags); a row without a
+    beam has a history of -1 and a score of -inf."""
     wl = dataclasses.replace(WORKLOADS["llama31_8b_70b_paged"].with_tokens(prompts, [0] * len(prompts)),
                              tgt_layers=layers)
     watch = watch or (lambda stage, **tensors: None)
@@ -97,7 +98,7 @@ def run(prompts=(70, 200), layers=2, beams=4, steps=(10, 10), vocab=1000, group=
         groups = i32([beams * p for p in range(prefix.shape[0] + 1)])
         for _ in range(steps[stretch]):
             pages.reserve(table, lens, 1, caches=caches, workspace=scratch, status=status)
-            x = target.embed[tokens.long()]
+            x = target.embed[tokens.long().clamp(min=0)]     # rows without a beam go along
             position = (before.repeat_interleave(beams) + lens).int()
             after = lens + 1
             for l, cache in enumerate(caches):
@@ -120,7 +121,9 @@ def run(prompts=(70, 200), layers=2, beams=4, steps=(10, 10), vocab=1000, group=
             watch("fork", pages=pages, old=table, old_lens=after, parents=parents, table=new_table,
                   lens=new_lens, prefix=prefix)
             table, lens, scores, done = new_table, new_lens, new_scores, new_done
-            history = torch.cat([history[parents.long()], tokens[:, None]], 1)
+            # a prompt with fewer candidates than beams has rows without one: parents and tokens of -1
+            kept = torch.where(parents[:, None] < 0, parents[:, None], history[parents.long().clamp(min=0)])
+            history = torch.cat([kept, tokens[:, None]], 1)
         if stretch == 0 and P > 1:
             # the first prompt is answered: its pages go, the others move together
             pages.free(prefix[:1], status=status)
