@@ -1457,7 +1457,8 @@ class Pages:
         row is then copied in all ``caches``.  ``new`` is one number, or
         one for each row (int32 tensor, at most ``max_new``).  ``copies`` [R][2]
         (int32) receives the copied pages, from and to (-1: none).  With too few
-        free pages nothing changes, and ``status`` tells (KVX_FLAG_NO_PAGES)."""
+        free pages none is taken or copied, and ``status`` tells
+        (KVX_FLAG_NO_PAGES): then only entries that are no pages change, to -1."""
         dev = self._ready()
         R, width, ptr, len_ptr = self._rows(table, lens)
         add = 0

@@ -97,7 +97,7 @@ typedef enum {
                                         (stored as 0); kvx_beam_select: a
                                         logit or score that is NaN or +inf   */
 #define KVX_FLAG_NO_PAGES     1024u  /* kvx_pages_reserve: fewer pages are free
-                                        than the call needs: nothing changes */
+                                        than the call needs: none is taken   */
 
 typedef enum { KVX_F32 = 0, KVX_BF16 = 1 } kvx_dtype;
 typedef enum { KVX_CONTIGUOUS = 0, KVX_PAGED = 1 } kvx_layout;
@@ -902,11 +902,11 @@ typedef struct {
  * of it and takes a free one (the last of its holders keeps it), and where
  * such a page holds slots of the row it is copied for all caches, codes and
  * scales.  The i-th page taken is the i-th free one, by number, before the call.
- * If fewer are free than are needed nothing changes (KVX_FLAG_NO_PAGES, copies all
- * -1): free some and call again.  A row whose length or whose new slots do not fit
- * its width reserves nothing (KVX_FLAG_BAD_LENGTH); an entry outside
- * [-1, num_blocks) counts as -1 (KVX_FLAG_BAD_BLOCK).  One launch, and one for every
- * 32 caches. */
+ * If fewer are free than are needed no reference and no page changes (KVX_FLAG_NO_PAGES,
+ * copies all -1): free some and call again.  A row whose length or whose new slots do not
+ * fit its width reserves nothing (KVX_FLAG_BAD_LENGTH); an entry of the new slots outside
+ * [-1, num_blocks) counts as -1, and is -1 afterwards where it gets no page
+ * (KVX_FLAG_BAD_BLOCK).  One launch, and one for every 32 caches. */
 kvx_status kvx_pages_reserve(const kvx_pages_reserve_args *args, void *stream);
 
 typedef struct {
