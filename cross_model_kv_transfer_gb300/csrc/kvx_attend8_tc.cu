@@ -678,32 +678,35 @@ __device__ __forceinline__ uint4 query_piece(bool vec, const __nv_bfloat16 *from
 }
 // Up to 32 query rows of a warp (`count` of them, rounded up to 8) as two e4m3
 // parts, `part` bytes apart, in the swizzled K-major tile, from row `first` of the
-// tile on; `src` is the lane's own row.  Half a warp loads a row, 2 N rows at a time, the
-// next ones on their way.  Where a CTA does one or two items it runs this code cold, and
-// four rows at a time are best (the 16 requests below with 128 rows a KV head 153 us, 163
-// with sixteen); where it does many, eight (a prompt of 8192 tokens 1074 us, 1099 with
-// four).  Returns the lane's factor on its row's scores (its sign is in the parts).
-template <int N>
+// tile on; `src` is the lane's own row.  Half a warp loads a row, 2 N rows at a time, with
+// AHEAD the next ones on their way.  Where a CTA does one or two items it runs this code cold,
+// and little of it is best (the 16 requests below with 128 rows a KV head 152 us, 163
+// with sixteen rows at a time and others on their way); a prompt of 8192 tokens takes 1077 us
+// with eight at a time, 1082 with the next ones on their way, 1095 with four and those.  Few
+// columns, whose CTAs wait for nothing else, gain 1 % from reading ahead (16 of them 94 us, 95).
+// Returns the lane's factor on its row's scores (its sign is in the parts).
+template <int N, bool AHEAD>
 __device__ __noinline__ float put_queries(const AttendParams &a, bool vec, const __nv_bfloat16 *src, bool live,
                                           unsigned char *tile, int first, int part, int count) {
   const int lane = threadIdx.x % 32, c = lane % 16;      // 8 dimensions
   float mine = 0.f;
   const auto ask = [&](int pair) {
-    const int row = (2 * pair + lane / 16) & 31;
+    const int row = (2 * pair + lane / 16) & 31;    // ahead of the last one: a load of none
     const uint64_t p = __shfl_sync(~0u, (uint64_t)src, row);
     const bool there = __shfl_sync(~0u, (int)live, row) && 8 * c < a.d && 2 * pair < 32;
     return there ? query_piece(vec, reinterpret_cast<const __nv_bfloat16 *>(p) + 8 * c) : make_uint4(0, 0, 0, 0);
   };
   uint4 next[N];
+  if (AHEAD)
 #pragma unroll
-  for (int i = 0; i < N; ++i) next[i] = ask(i);
+    for (int i = 0; i < N; ++i) next[i] = ask(i);
 #pragma unroll 1
   for (int i0 = 0; 2 * i0 < count; i0 += N) {
     uint4 x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      x[i] = next[i];
-      next[i] = ask(i0 + N + i);
+      x[i] = AHEAD ? next[i] : ask(i0 + i);
+      if (AHEAD) next[i] = ask(i0 + N + i);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -1227,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (int64_t)(w.h * a.G + (int)(at % a.G)) * a.qh;
       float m = -INFINITY, shift = 0.f, l = 0.f, cs;
       if (WIDE || i == 0) {
-        cs = put_queries<WIDE && !kShared ? 4 : 2>(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes, 32);
+        cs = put_queries<WIDE && !kShared ? 4 : 2, false>(a, p.vec_q, src, live, qbuf + (WIDE ? i * 2 * kTileBytes : 0), warp % 4 * 32, kTileBytes, 32);
         fence_async_proxy();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh->q_full[i]));
@@ -1736,7 +1739,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
       const int rows = (int)min((int64_t)NC, (int64_t)w.fresh * a.G - row0);
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (w.beg + tok) * a.qt +
                                  (int64_t)(w.h * a.G + (int)((row0 + lane) % a.G)) * a.qh;
-      const float f = put_queries<2>(a, p.vec_q, src, lane < rows, qbuf + (item & 1) * 2 * kColQBytes, 0, kColQBytes, 16);
+      const float f = put_queries<2, true>(a, p.vec_q, src, lane < rows, qbuf + (item & 1) * 2 * kColQBytes, 0, kColQBytes, 16);
       if (lane < 16) sh->cs[item & 1][lane] = f;
       fence_async_proxy();
       __syncwarp();
@@ -2204,7 +2207,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int64_t tok = beg + row / a.G;
       const int hq = h * a.G + row % a.G;
       const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + tok * a.qt + (int64_t)hq * a.qh;
-      const float cs = put_queries<4>(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32, kTileBytes, 32);
+      const float cs = put_queries<4, false>(a, p.vec_q, src, live, qbuf + i * 2 * kTileBytes, warp % 4 * 32, kTileBytes, 32);
       float *pair_of = reinterpret_cast<float *>(&sh->rows[tid / 2]) + tid % 2;
       float *terms_of = reinterpret_cast<float *>(&sh->terms[tid / 2]) + tid % 2;
       if (c == 0) wait_for_kernel_before();   // the log-sum-exps
