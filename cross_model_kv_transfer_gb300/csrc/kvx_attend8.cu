@@ -153,8 +153,9 @@ extern "C" size_t kvx_attend8_shared_workspace_bytes(const kvx_attend8_shared_ar
 
 // Two passes: each prefix against the queries of all requests that share it, as one
 // request's, and the requests' own slots, whose results are joined with the first pass's
-// where they are written.  A prefix is read once for its group and not once a request, and
-// its products have a group's rows: what they cost is that of a prompt of as many tokens.
+// where they are written.  A prefix is read once for up to 256 rows of its group (8 where the
+// slots go in parts, 8 to 32 in the split form) and not once a request, and its products have as
+// many: what they cost is that of a prompt of as many tokens.
 extern "C" kvx_status kvx_attend8_shared(const kvx_attend8_shared_args *a, void *stream) {
   Shared s;
   if (const kvx_status st = shared_of(a, s)) return st;

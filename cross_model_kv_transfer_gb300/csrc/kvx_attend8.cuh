@@ -1,5 +1,6 @@
 // kvx_attend8.cuh -- what the attention kernels over the 8-bit cache share
-// (kvx_attend8.cu, kvx_attend8_tc.cu): their parameters, lookups and checks.
+// (kvx_attend8_split.cu, kvx_attend8_tc.cu, kvx_attend8_own.cu) and their calls
+// (kvx_attend8.cu): parameters, lookups and checks.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -1,5 +1,5 @@
 // kvx_attend8_mma.cuh -- what the attention kernels on 16 x 8 x 16 matrix instructions
-// share (kvx_attend8.cu, kvx_attend8_own.cu): the instructions, sizes, the queries'
+// share (kvx_attend8_split.cu, kvx_attend8_own.cu): the instructions, sizes, the queries'
 // fragments.
 #pragma once
 

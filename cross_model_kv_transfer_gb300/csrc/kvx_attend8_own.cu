@@ -10,12 +10,13 @@
 // warps takes one item whole, several CTAs share an SM and hide each other's loads, and the
 // result is joined with the prefix's where it is formed.  A warp takes tiles of 16 MT slots
 // in turn, two on their way; the products and roundings are those of the split form
-// (kvx_attend8.cu).
+// (kvx_attend8_split.cu).
 //
 // The prefixes themselves go the same way while their products are few: a CTA for each
-// prefix, KV head, group of up to 32 columns and split of the slots leaves its maxima, totals and
+// prefix, KV head, group of eight columns and split of the slots leaves its maxima, totals and
 // sums, and the items join all splits' with their own.  Two launches then, and no
-// kernel that joins.
+// kernel that joins.  So a prefix is read (from L2, mostly) once for every eight columns of its
+// group, which with eight heads to a KV head and one token is once for each request.
 #define KVX_ATTEND_SHARED 1
 #include "kvx_attend8_mma.cuh"
 
@@ -480,9 +481,12 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::DP <= 128 ? 3 : 1) own_kerne
   }
 }
 
-// Eight columns a CTA: more of them (two to four tiles) took the same time or longer in all
-// of 8 beams, 64 samples and 192 rows of three tokens, as four or eight warps and one or two
-// 16-slot tiles did; this takes the fewest registers.
+// Eight columns a CTA: with bf16 queries more of them (two to four tiles) took the same time or
+// longer in all of 8 beams, 64 samples and 192 rows of three tokens, as four or eight warps and one
+// or two 16-slot tiles did; this takes the fewest registers.  With fp32 queries, whose products
+// cost twice, long prefixes in parts of up to 32 columns took less: 8 requests over
+// 65,000 slots 152 us (254 with eight columns, 223 in the split form, which they take now), 4 x
+// 32 over 8000 316 us (428, 361).  That is not built.
 template <int DP, int PARTS>
 kvx_status launch_own(const OwnParams &p, int groups, bool part, cudaStream_t s) {
   using C = SplitCfg<DP, 1, PARTS, DP <= 128 ? 2 : 1, 4, 2>;

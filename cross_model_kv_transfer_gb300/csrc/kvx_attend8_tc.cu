@@ -21,14 +21,14 @@
 // (at most 64 rows): they take the even and the odd slot tiles of the same
 // rows, so that one tile's softmax overlaps the other's products.
 //
-// What it reaches.  Wide, one request of 8192 tokens, 64 heads: 1070 us, 1.03
+// What it reaches.  Wide, one request of 8192 tokens, 64 heads: 1077 us, 1.02
 // PFLOP/s of the two products counted once, 0.52 of what bf16 matrix products reach;
 // counters have the tensor pipe active 0.45 of the time and the schedulers issuing
 // 0.55 of it: bound by the two groups' chain of score product, softmax and value
 // product.  (Score products in half tiles of 64 columns run at 0.6 of their rate at
 // 128, but whole tiles leave a group nothing to do while they are formed: 1397 us
 // where half tiles took 1217.)  61 tokens of 32 heads against 8192 slots, two
-// requests: 45 us, 16 to join what 152 CTAs left, 26 for the weights; about a third
+// requests: 35 us, 12 to join what 152 CTAs left, 29 for the weights; about a third
 // of that fills and drains pipelines.
 //
 // Work: every CTA takes an equal share of all steps and item costs (below); what
@@ -160,11 +160,12 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
 // part (queries, a filling and draining pipeline, the result), so the CTAs' shares
 // are of costs: an item takes SETUP + steps places from `base` on, and its step s
 // is at place base + SETUP + s.  Measured, us, with SETUP as given: wide 5, 6, 7, 8, 9: a
-// prompt of 8192 tokens 1133, 1082, 1070, 1079, 1089, one of 2048 158, 157, 154, 159, 147,
-// 128 rows each of 16 requests of 1024 to 16,384 slots 168, 163, 161, 161, 163.  The same
-// requests narrow 2, 3, 4, 5, 6: 24 rows 152, 145, 147, 152, 155, 40 rows 168, 157, 152, 153,
-// 156, 64 rows 193, 180, 167, 161, 156; columns 1, 2, 3, 4: 8 rows 84, 74, 73, 72, 16 rows 136,
-// 108, 101, 95.
+// prompt of 8192 tokens 1153, 1102, 1077, 1088, 1096, one of 2048 147, 140, 145, 148, 138,
+// 128 rows each of 16 requests of 1024 to 16,384 slots 166, 155, 153, 152, 155.  The same
+// requests narrow 2, 3, 4, 5, 6: 24 rows 144, 137, 130, 127, 129, 40 rows 162, 153, 139, 135,
+// 131, 64 rows 189, 175, 157, 156, 138 (4 was taken when they were 147, 152, 167 and 5 and 6
+// not better for all; the loaders' own warps changed that, the shares are as they were); columns 1, 2, 3, 4: 8 rows 84, 71, 71, 70, 16 rows 136,
+// 108, 104, 96.
 struct Wide {
   static constexpr int ROWS = 2 * kTile, SLOTS = kTile;   // of an item, of a step
   static constexpr int PARTS = 1;                         // results that a CTA keeps for an item
@@ -680,7 +681,7 @@ __device__ __forceinline__ uint4 query_piece(bool vec, const __nv_bfloat16 *from
 // parts, `part` bytes apart, in the swizzled K-major tile, from row `first` of the
 // tile on; `src` is the lane's own row.  Half a warp loads a row, 2 N rows at a time, with
 // AHEAD the next ones on their way.  Where a CTA does one or two items it runs this code cold,
-// and little of it is best (the 16 requests below with 128 rows a KV head 152 us, 163
+// and little of it is best (the 16 requests below with 128 rows a KV head 152 us, 162
 // with sixteen rows at a time and others on their way); a prompt of 8192 tokens takes 1077 us
 // with eight at a time, 1082 with the next ones on their way, 1095 with four and those.  Few
 // columns, whose CTAs wait for nothing else, gain 1 % from reading ahead (16 of them 94 us, 95).
@@ -1543,9 +1544,9 @@ __global__ void __launch_bounds__(256) weights_of_rows_kernel(const __grid_const
 // item takes the largest score and the largest value scale apart.
 // Two groups of four warps take the even and the odd slot tiles.
 // One query of 64 heads over 131,071 slots of 8 heads takes 57 us, 4.7 TB/s (a copy
-// 6.7); 16 requests of 1024 to 16,384 slots 73 us, and with 16 columns, which read the
+// 6.7); 16 requests of 1024 to 16,384 slots 71 us, and with 16 columns, which read the
 // same bytes, 94: the chain of a tile's softmax counts beside them.  The narrow form
-// above takes 124 there, matrix instructions on registers (16 x 8 x 16) 88 with 8.
+// above takes 123 there, matrix instructions on registers (16 x 8 x 16) 88 with 8.
 // even numbers of stages: a stage serves one group, whose waits on it then know
 // that the phase before is over
 constexpr int kCkStages = 4, kCvStages = 6, kScales = 16, kColThreads = 12 * 32;
@@ -2409,9 +2410,9 @@ TcShape tc_shape(const kvx_attend8_args *a) {
   TcShape s;
   const int64_t G = a->q_heads / a->cache.heads, most = G * most_new(a);
   // 16 requests of 1024 to 16,384 slots, 8 KV heads, without and with weights.  16 rows:
-  // columns 93 and 118 us, narrow 124 and 175.  24 rows: narrow 130 and 189, wide 140 and
-  // 282; 64 rows: 156 and 268 against 152 and 297; 128 rows: 209 and 439 against 154 and
-  // 298.
+  // columns 93 and 118 us, narrow 123 and 173.  24 rows: narrow 128 and 188, wide 138 and
+  // 280; 64 rows: 155 and 265 against 150 and 294; 128 rows: 213 and 439 against 152 and
+  // 296.
   s.columns = most <= 16;
   s.wide = most > 64;
   s.slot_rows = s.wide ? Wide::ROWS : s.columns ? (most <= 8 ? 8 : 16) : (int)most;

@@ -1,5 +1,5 @@
 // kvx_cache8.cuh -- the 8-bit paged cache as the kernels see it (kvx_cache8.cu,
-// kvx_attend8.cu, kvx_evict8.cu): e4m3 conversions, power-of-two scales, block
+// kvx_attend8*.cu, kvx_pages.cu, kvx_evict8.cu): e4m3 conversions, power-of-two scales, block
 // lookup, request tables and the host's checks of a kvx_cache8.
 #pragma once
 

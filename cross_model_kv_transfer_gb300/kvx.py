@@ -1249,10 +1249,11 @@ class Cache8:
         groups[p] .. groups[p + 1] - 1 (``groups`` [P + 1]; without it all) have
         the slots of row p of ``prefix_table`` (``prefix_lens`` [P], at most
         ``max_prefix``) before those of ``block_table`` and ``lens``; a prefix has
-        at most ``max_group`` requests (more: nothing is written, and ``status``
-        tells).  The new queries are the last of a request's own slots.  A prefix
-        is read once for its whole group.  Returns (out, lse [tokens][q_heads])
-        over both.  Scratch is allocated here unless ``workspace`` (from
+        at most ``max_group`` requests (with more than max_group * max_new queries
+        nothing is written, and ``status`` tells).  The new queries are the last of
+        a request's own slots.  A prefix is read once for 8 to 256 rows of a
+        KV head and its group.  Returns (out, lse [tokens][q_heads]) over both.
+        Scratch is allocated here unless ``workspace`` (from
         ``attend_shared_workspace``) is given."""
         dev, dt = self.device, q.dtype
         _on_device(dev)
@@ -1412,7 +1413,7 @@ class Pages:
         """New rows in place of those of ``table`` [R][width]: row n continues
         row parents[n] (-1: an empty row) and shares the pages that its length
         covers.  The old rows hold nothing afterwards.  Returns (new_table
-        [N][width], new_lens [N])."""
+        [N][width], new_lens [N]), which overlap nothing that is read."""
         dev = self._ready()
         R, width, ptr, len_ptr = self._rows(table, lens)
         parent = _int_table(parents, "parents", dev)

@@ -819,11 +819,11 @@ size_t kvx_attend8_shared_workspace_bytes(const kvx_attend8_shared_args *args);
  *   out_i = sum_j p_ij v_j,  p_ij = exp(scale q_i.k_j - lse_i)
  * over both, as kvx_attend8 of one sequence that holds the prefix's slots and then
  * the request's.  The prefix's last block may be part full, and its blocks
- * need not be the requests'.  A prefix is read once for its group, not once for
- * each request, and multiplied with the rows of all of them at once; what that
- * gives is kept in fp32 until it is joined with the request's own slots.  A length
- * outside its bound counts as 0 (KVX_FLAG_BAD_LENGTH); slots of a block id outside the pool
- * are masked (KVX_FLAG_BAD_BLOCK); a malformed request or group table, or a group
+ * need not be the requests'.  A prefix is read once for 8 (little work) to 256 rows of
+ * a KV head and its group, whosever they are; what that gives is kept in fp32 until it is
+ * joined with the request's own slots.  A length outside its bound counts as 0
+ * (KVX_FLAG_BAD_LENGTH); slots of a block id outside the pool are masked
+ * (KVX_FLAG_BAD_BLOCK); a malformed request or group table, or a group
  * with more than max_group * max_new queries, writes neither out nor lse
  * (KVX_FLAG_BAD_SEQLENS).  Accuracy as of kvx_attend8.  Two to four launches.
  * KVX_ERR_INVALID_ARG also for weights, and without groups for P != 1. */
