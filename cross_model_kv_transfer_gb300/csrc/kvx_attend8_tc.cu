@@ -164,8 +164,8 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
 // 128 rows each of 16 requests of 1024 to 16,384 slots 166, 155, 153, 152, 155.  The same
 // requests narrow 2, 3, 4, 5, 6: 24 rows 144, 137, 130, 127, 129, 40 rows 162, 153, 139, 135,
 // 131, 64 rows 189, 175, 157, 156, 138 (4 was taken when they were 147, 152, 167 and 5 and 6
-// not better for all; the loaders' own warps changed that, the shares are as they were); columns 1, 2, 3, 4: 8 rows 84, 71, 71, 70, 16 rows 136,
-// 108, 104, 96.
+// not better for all; the loaders' own warps changed that, the shares are as they were);
+// columns 1, 2, 3, 4: 8 rows 84, 71, 71, 70, 16 rows 136, 108, 104, 96.
 struct Wide {
   static constexpr int ROWS = 2 * kTile, SLOTS = kTile;   // of an item, of a step
   static constexpr int PARTS = 1;                         // results that a CTA keeps for an item
